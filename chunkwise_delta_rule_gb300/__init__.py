@@ -18,3 +18,25 @@ from .ops import (  # noqa: F401
     kda_workspace_size,
     make_problem,
 )
+from .layer import (  # noqa: F401
+    ConvProblem,
+    NormProblem,
+    SsmGrads,
+    SsmProblem,
+    kda_conv_bwd,
+    kda_conv_fwd,
+    kda_conv_workspace_size,
+    kda_norm_bwd,
+    kda_norm_fwd,
+    kda_norm_workspace_size,
+    kda_ssm_bwd,
+    kda_ssm_fwd,
+    kda_ssm_saved_size,
+    kda_ssm_workspace_size,
+    make_conv_problem,
+    make_norm_problem,
+    make_ssm_problem,
+    rms_norm,
+    short_conv,
+    ssm_scan,
+)

@@ -48,6 +48,48 @@ class KdaProblem(ctypes.Structure):
     ]
 
 
+class ConvProblem(ctypes.Structure):
+    """Mirror of ``kda_conv_problem``."""
+
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("W", ctypes.c_int),
+        ("N", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
+        ("io", ctypes.c_int), ("silu", ctypes.c_int), ("ldx", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("h0", ctypes.c_void_p),
+    ]
+
+
+class SsmProblem(ctypes.Structure):
+    """Mirror of ``kda_ssm_problem``."""
+
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("S", ctypes.c_int), ("G", ctypes.c_int),
+        ("N", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
+        ("io", ctypes.c_int), ("dt_softplus", ctypes.c_int), ("save_policy", ctypes.c_int),
+        ("ldx", ctypes.c_int64), ("lddt", ctypes.c_int64), ("ldz", ctypes.c_int64), ("ldb", ctypes.c_int64),
+        ("ldc", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("dt", ctypes.c_void_p), ("z", ctypes.c_void_p),
+        ("b", ctypes.c_void_p), ("c", ctypes.c_void_p),
+        ("A_log", ctypes.c_void_p), ("d_skip", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("h0", ctypes.c_void_p),
+    ]
+
+
+class SsmGrads(ctypes.Structure):
+    """Mirror of ``kda_ssm_grads``."""
+
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "ddt", "dz", "db", "dc", "dA_log", "dd_skip", "ddt_bias", "dh0")]
+
+
+class NormProblem(ctypes.Structure):
+    """Mirror of ``kda_norm_problem``."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int), ("D", ctypes.c_int), ("io", ctypes.c_int), ("out", ctypes.c_int),
+        ("group", ctypes.c_int), ("eps", ctypes.c_float),
+        ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+    ]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status: int, where: str, msg: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {msg}")
@@ -83,6 +125,20 @@ def load() -> ctypes.CDLL:
     lib.kda_last_error.restype = ctypes.c_char_p
     lib.kda_recurrent_fwd.argtypes = [P, vp, vp, vp, vp]
     lib.kda_recurrent_fwd.restype = ctypes.c_int
+    CP, SP, NP = ctypes.POINTER(ConvProblem), ctypes.POINTER(SsmProblem), ctypes.POINTER(NormProblem)
+    for name, args, res in (
+            ("kda_conv_fwd", [CP, vp, vp, vp, vp], ctypes.c_int),
+            ("kda_conv_workspace_size", [CP], sz),
+            ("kda_conv_bwd", [CP, vp, vp, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+            ("kda_ssm_workspace_size", [SP, ctypes.c_int], sz),
+            ("kda_ssm_saved_size", [SP], sz),
+            ("kda_ssm_fwd", [SP, vp, vp, vp, vp, sz, vp, vp], ctypes.c_int),
+            ("kda_ssm_bwd", [SP, vp, vp, vp, ctypes.POINTER(SsmGrads), vp, sz, vp], ctypes.c_int),
+            ("kda_norm_fwd", [NP, vp, vp, vp, vp], ctypes.c_int),
+            ("kda_norm_workspace_size", [NP], sz),
+            ("kda_norm_bwd", [NP, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int)):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, res
     lib.kda_abi_version.argtypes = []
     lib.kda_abi_version.restype = ctypes.c_int
     _lib = lib

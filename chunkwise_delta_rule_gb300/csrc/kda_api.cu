@@ -562,6 +562,17 @@ int bwd_pieces(const kda_problem* p, const Dims& d) {
 
 namespace kda {
 void set_last_error(const char* msg) { g_err = msg; }
+int trace_open(const char* name, cudaStream_t st) {
+    if (!g_prof.on) return -1;
+    cudaEvent_t a = g_prof.ev(), b = g_prof.ev();
+    if (!a || !b) return -1;
+    cudaEventRecord(a, st);
+    g_prof.recs.push_back({name, a, b});
+    return (int)g_prof.recs.size() - 1;
+}
+void trace_close(int id, cudaStream_t st) {
+    if (id >= 0) cudaEventRecord(g_prof.recs[id].b, st);
+}
 }  // namespace kda
 
 extern "C" {

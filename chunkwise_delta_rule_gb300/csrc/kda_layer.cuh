@@ -1,0 +1,238 @@
+// Shared declarations of the layer operators around the delta rule: the short
+// causal convolution (kda_conv.cu), the selective state space scan (kda_ssm.cu,
+// kda_ssm_bwd.cu) and the root-mean-square norm (kda_norm.cu).
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// Tracing hooks of kda_api.cu (kda_profile_begin): a pair of events around one launch; -1 when tracing
+// is off.
+int trace_open(const char* name, cudaStream_t st);
+void trace_close(int id, cudaStream_t st);
+
+template <class F>
+cudaError_t traced_launch(const char* name, cudaStream_t st, F&& launch) {
+    const int id = trace_open(name, st);
+    launch();
+    trace_close(id, st);
+    return cudaGetLastError();
+}
+
+// The token axis: equal-length sequences are `rows` rows of `len` tokens, one sequence each; packed
+// sequences are one row of all tokens, cut by the N + 1 offsets in cu.
+struct TokenAxis {
+    const int32_t* cu;
+    int N;      // sequences
+    int rows, len;
+};
+
+// Offset cu[n], kept inside the token axis whatever the caller's array holds.
+__device__ __forceinline__ int axis_cu(const TokenAxis& ax, int n) { return min(max(ax.cu[n], 0), ax.len); }
+
+// Packed axis: the sequence that holds token t (the first n with cu[n + 1] > t; the last sequence when
+// inconsistent offsets leave t to none).
+__device__ __forceinline__ int axis_find(const TokenAxis& ax, int t) {
+    int lo = 0, hi = ax.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (axis_cu(ax, mid + 1) > t) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+struct Seq {
+    int n, first, end;    // sequence, its first token and its end on the row
+};
+
+// The sequence holding token t of the row; first <= t < end whatever the offsets hold.
+__device__ __forceinline__ Seq seq_at(const TokenAxis& ax, int row, int t) {
+    if (!ax.cu) return {row, 0, ax.len};
+    Seq s;
+    s.n = axis_find(ax, t);
+    s.first = min(axis_cu(ax, s.n), t);
+    s.end = axis_cu(ax, s.n + 1);
+    if (s.end <= t) s.end = ax.len;
+    return s;
+}
+
+// Packed axis: sets bit 0 of *err when cu does not start at 0, decreases, or does not end at the token
+// count. Called by one whole CTA.
+__device__ __forceinline__ void axis_check(const TokenAxis& ax, int32_t* err) {
+    if (!ax.cu || !err) return;
+    bool bad = false;
+    for (int n = threadIdx.x; n < ax.N; n += blockDim.x) bad |= ax.cu[n + 1] < ax.cu[n];
+    if (threadIdx.x == 0) bad |= ax.cu[0] != 0 || ax.cu[ax.N] != ax.len;
+    if (bad) atomicOr(err, 1);
+}
+
+// 2^x (2^-22 relative; the argument already carries one fp32 rounding) and 1 / x.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp(1.f + ex2(-LOG2E * x)); }
+
+// Packed pairs of fp32 (one instruction for two lanes of work).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return d;
+}
+
+// V consecutive elements of a row as fp32: 16-byte accesses when `vec` (V elements, aligned), else
+// element by element with the ones past `valid` read as zero (not stored).
+template <int V>
+__device__ __forceinline__ void load_row(const float* p, float (&x)[V], int valid, bool vec) {
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 v = reinterpret_cast<const float4*>(p)[i];
+            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = i < valid ? p[i] : 0.f;
+    }
+}
+template <int V>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&x)[V], int valid, bool vec) {
+    if (V >= 8 && vec) {
+#pragma unroll
+        for (int i = 0; i < V / 8; ++i) {
+            const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = i < valid ? __bfloat162float(p[i]) : 0.f;
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_row(float* p, const float (&x)[V], int valid, bool vec) {
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < valid) p[i] = x[i];
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&x)[V], int valid, bool vec) {
+    if (V >= 8 && vec) {
+#pragma unroll
+        for (int i = 0; i < V / 8; ++i) {
+            uint4 v;
+            __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
+            reinterpret_cast<uint4*>(p)[i] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < valid) p[i] = __float2bfloat16_rn(x[i]);
+    }
+}
+
+// ------------------------------------------------------------------ launchers
+struct ConvArgs {
+    TokenAxis ax;
+    int D, W, silu, tile, ntiles, groups;   // tokens per thread; tiles of all rows; channel groups
+    int tiles_row;                          // tiles per row
+    size_t ldx;
+    const void *x, *h0;
+    const float *weight, *bias;
+    void *y, *final_state;
+    int32_t* err;
+    // backward
+    const void *dy, *dfinal;
+    void *dx, *dinit;
+    float *dweight, *dbias, *part;          // part: [parts][W + 1][D] sums of blocks of tiles
+    int parts;
+};
+// Elements per thread of the vector path (16 bytes) or 1; tokens per thread and block counts.
+void conv_shape(ConvArgs& a, int bf16, bool vec, bool backward);
+cudaError_t launch_conv_fwd(ConvArgs a, int bf16, bool vec, cudaStream_t st);
+cudaError_t launch_conv_bwd(ConvArgs a, int bf16, bool vec, cudaStream_t st);
+
+struct NormArgs {
+    int rows, D, out, group, ngroups;   // out: 0 the I/O type, 1 e4m3 with scales
+    float eps;
+    const void *x, *residual;
+    const float* weight;
+    void *y, *h;
+    float* scale;
+    // backward
+    const void *dy, *dres;
+    void* dx;
+    float *dweight, *part;
+    int parts;
+};
+int norm_bwd_parts(int rows);
+constexpr int NORM_MAX_D = 16384;
+cudaError_t launch_norm_fwd(const NormArgs& a, int bf16, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormArgs& a, int bf16, cudaStream_t st);
+
+// Checkpoint interval of the scan's saved states, in tokens.
+constexpr int SSM_CKPT = 16;
+
+enum { SSM_VEC_X = 1, SSM_VEC_DT = 2, SSM_VEC_Z = 4, SSM_VEC_B = 8, SSM_VEC_C = 16, SSM_VEC_OUT = 32 };
+
+struct SsmArgs {
+    TokenAxis ax;
+    int D, S, G, softplus;     // channels, states per channel, groups of b, c
+    int vec;                   // tensors whose rows take 16-byte accesses (SSM_VEC_*)
+    int units_row, unit_len;   // time pieces per row and their tokens (a multiple of 32)
+    size_t ldx, lddt, ldz, ldb, ldc;
+    const void *x, *dt, *z, *b, *c;
+    const float *A_log, *d_skip, *dt_bias, *h0;
+    void* y;
+    float* ht;
+    int32_t* err;
+    float* ckpt;               // [rows][ceil(len / SSM_CKPT)][D][S]: state entering every 16th token
+    float *hloc, *sdt;         // pieces: [rows * units_row][D][S] local end states, [..][D] sums of delta
+    // backward
+    const void* dy;
+    const float* dht;
+    void *dx, *ddt, *dz, *db, *dc;
+    float *dA_log, *dd_skip, *ddt_bias, *dh0;
+    float *rloc;               // pieces: [rows * units_row][D][S] local adjoints leaving the piece's start
+    float *pA, *pv;            // [units][D][S]; [units][2][D] (skip, dt_bias)
+    float* pbc;                // [channel tiles][rows * len][2][S]
+};
+int ssm_channel_tiles(int D, int G);   // channel tiles of all groups (forward and backward)
+int ssm_units(int rows, int len, int D, int G, int S, bool backward);
+cudaError_t launch_ssm_fwd(const SsmArgs& a, int bf16, int mode, cudaStream_t st);   // 0 outputs, 1 + checkpoints, 2 checkpoints only
+cudaError_t launch_ssm_pieces(const SsmArgs& a, int bf16, cudaStream_t st);          // local end states of every piece
+cudaError_t launch_ssm_bwd_pieces(const SsmArgs& a, int bf16, cudaStream_t st);
+cudaError_t launch_ssm_bwd(const SsmArgs& a, int bf16, cudaStream_t st);
+cudaError_t launch_ssm_bwd_sums(const SsmArgs& a, int bf16, cudaStream_t st);
+
+}  // namespace kda

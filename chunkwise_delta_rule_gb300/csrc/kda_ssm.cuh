@@ -1,0 +1,92 @@
+// Device helpers shared by the scan's forward and backward.
+#pragma once
+
+#include "kda_layer.cuh"
+
+namespace kda {
+
+constexpr unsigned SSM_FULL = 0xffffffffu;
+constexpr int SSM_T = 128;    // threads per CTA: 32 channels x 4 lanes
+constexpr int SSM_CH = 32;    // channels per CTA
+
+// log(1 + e^v) without overflow.
+__device__ __forceinline__ float ssm_softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+
+// A CTA's place: time piece `unit` of row `row` (tokens [lo, hi)), 32 channels from c0 of group g.
+struct SsmPlace {
+    int unit, row, u, lo, hi, tile, g, c0, nch;
+};
+__device__ __forceinline__ SsmPlace ssm_place(const SsmArgs& a) {
+    SsmPlace p;
+    const int M = a.D / a.G, tpg = (M + SSM_CH - 1) / SSM_CH, tiles = tpg * a.G;
+    p.unit = blockIdx.x / tiles;
+    p.tile = blockIdx.x - p.unit * tiles;
+    p.g = p.tile / tpg;
+    const int tg = p.tile - p.g * tpg;
+    p.c0 = p.g * M + tg * SSM_CH;
+    p.nch = min(SSM_CH, M - tg * SSM_CH);
+    p.row = p.unit / a.units_row;
+    p.u = p.unit - p.row * a.units_row;
+    p.lo = p.u * a.unit_len;
+    p.hi = min(p.lo + a.unit_len, a.ax.len);
+    return p;
+}
+
+// A lane's EL states of channel d (states n0 .. n0 + EL - 1 of S), zero past S or for an absent channel.
+template <int EL>
+__device__ __forceinline__ void load_states(const float* p, int n0, int S, bool on, float (&x)[EL]) {
+    const bool vec = on && S == 4 * EL && EL >= 4 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+    if (vec) {
+#pragma unroll
+        for (int e = 0; e + 3 < EL; e += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + n0 + e);
+            x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < EL; ++e) x[e] = on && n0 + e < S ? p[n0 + e] : 0.f;
+    }
+}
+template <int EL>
+__device__ __forceinline__ void store_states(float* p, int n0, int S, bool on, const float (&x)[EL]) {
+    const bool vec = S == 4 * EL && EL >= 4 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+    if (!on) return;
+    if (vec) {
+#pragma unroll
+        for (int e = 0; e + 3 < EL; e += 4)
+            *reinterpret_cast<float4*>(p + n0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < EL; ++e)
+            if (n0 + e < S) p[n0 + e] = x[e];
+    }
+}
+
+// One halving step of a sum over lanes: each lane keeps half of its V values and adds the partner's copy of them.
+template <int V>
+__device__ __forceinline__ void halve(float* v, int lane, int mask) {
+    const bool up = lane & mask;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        const float send = up ? v[i] : v[i + V / 2];
+        const float keep = up ? v[i + V / 2] : v[i];
+        v[i] = keep + __shfl_xor_sync(SSM_FULL, send, mask);
+    }
+}
+
+// The EL states of a lane's row in a shared [..][4 * EL] tile.
+template <int EL>
+__device__ __forceinline__ void lds_states(const float* p, float (&x)[EL]) {
+    if (EL % 4 == 0) {
+#pragma unroll
+        for (int e = 0; e + 3 < EL; e += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + e);
+            x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
+        }
+    } else {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        x[0] = v.x; x[1] = v.y;
+    }
+}
+
+}  // namespace kda

@@ -253,6 +253,130 @@ kda_status kda_device_status(const kda_problem *p, const void *ws, size_t ws_byt
 kda_status kda_selftest_device_timeout(const kda_problem *p, void *ws, size_t ws_bytes, unsigned limit_us,
                                        kda_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Layer operators around the delta rule: the short causal convolution in front
+ * of a mixer's recurrence, the selective state space scan (the diagonal
+ * recurrence that hybrid stacks put beside it), and the norm of the residual
+ * stream in front of both. Conventions as above, with two differences: token
+ * tensors that are inputs may be slices of wider rows (a leading dimension in
+ * elements, 0 for contiguous rows), and cu_seqlens may hold empty sequences. An
+ * inconsistent cu_seqlens sets bit 0 of *err (NULL or a device int32 word) and
+ * leaves the results of that call unspecified; every access stays in bounds.
+ * ------------------------------------------------------------------------- */
+
+/* Short causal convolution, one filter per channel:
+ *     s_t = bias + sum_j weight[j] x_{t-W+1+j},   y_t = s_t, or s_t sigmoid(s_t) with silu.
+ * Tokens before a sequence's first are the rows of its state h0, its previous
+ * W - 1 inputs, oldest first (zeros without h0). */
+typedef struct {
+    int B, T, D, W;             /* batch, tokens per sequence (total when packed), channels, taps (2..4) */
+    int N;                      /* packed sequences (used only when cu_seqlens != NULL; then B == 1) */
+    const int32_t *cu_seqlens;  /* device, N+1 offsets, or NULL */
+    kda_dtype io;               /* type of x, h0, y, the final state and their gradients */
+    int silu;                   /* 1: SiLU behind the convolution */
+    int64_t ldx;                /* elements between tokens of x (0: D) */
+    const void *x;              /* [B*T, D] */
+    const float *weight;        /* [D, W] fp32 */
+    const float *bias;          /* [D] fp32 or NULL */
+    const void *h0;             /* [N, W-1, D] or NULL */
+} kda_conv_problem;
+
+/* Writes y [B*T, D] and, if not NULL, final_state [N, W-1, D] (the last W - 1
+ * inputs; rows of h0 where a sequence is shorter), which may be the same buffer
+ * as h0. One token per call (T = 1) is one step of decoding. */
+kda_status kda_conv_fwd(const kda_conv_problem *p, void *y, void *final_state, int32_t *err, kda_stream_t stream);
+
+/* Bytes of workspace kda_conv_bwd needs (256-byte aligned; 0 for an invalid problem). */
+size_t kda_conv_workspace_size(const kda_conv_problem *p);
+
+/* Backward of <dy, y> + <dfinal, final_state>: dy [B*T, D], dfinal [N, W-1, D]
+ * or NULL; writes dx [B*T, D], dweight [D, W] and dbias [D] fp32 (dbias may be
+ * NULL), dinit [N, W-1, D] (may be NULL). The parameters' sums are formed in a
+ * fixed order: repeated calls agree bitwise. */
+kda_status kda_conv_bwd(const kda_conv_problem *p, const void *dy, const void *dfinal, void *dx, float *dweight,
+                        float *dbias, void *dinit, void *ws, size_t ws_bytes, kda_stream_t stream);
+
+/* Selective state space scan: per channel d a diagonal recurrence over S states
+ * whose step depends on the token,
+ *     delta = softplus(dt + dt_bias) (or dt + dt_bias),  A = -exp(A_log),
+ *     h_t = exp(delta_t A) h_{t-1} + delta_t x_t b_t,
+ *     y_t = (sum_n c_t[n] h_t[n] + d_skip x_t) silu(z_t),
+ * b and c shared by the D / G channels of a group; the skip and the gate are
+ * left out where d_skip or z is NULL. */
+typedef struct {
+    int B, T, D, S, G;          /* batch, tokens, channels, states per channel (1..64), groups (divide D) */
+    int N;                      /* packed sequences (used only when cu_seqlens != NULL; then B == 1) */
+    const int32_t *cu_seqlens;  /* device, N+1 offsets, or NULL */
+    kda_dtype io;               /* type of x, dt, z, b, c, y and their gradients */
+    int dt_softplus;            /* 1: delta = softplus(dt + dt_bias); 0: dt + dt_bias */
+    int save_policy;            /* 0: the backward recomputes the states; 1: the forward keeps every
+                                   16th one in `saved` */
+    int64_t ldx, lddt, ldz, ldb, ldc;   /* elements between tokens (0: contiguous) */
+    const void *x, *dt;         /* [B*T, D] */
+    const void *z;              /* [B*T, D] or NULL */
+    const void *b, *c;          /* [B*T, G, S] */
+    const float *A_log;         /* [D, S] fp32 */
+    const float *d_skip;        /* [D] fp32 or NULL */
+    const float *dt_bias;       /* [D] fp32 or NULL */
+    const float *h0;            /* [N, D, S] fp32 or NULL */
+} kda_ssm_problem;
+
+/* Bytes of workspace of kda_ssm_fwd (for_backward = 0) or kda_ssm_bwd (1), and of
+ * the `saved` buffer of save_policy 1; 256-byte aligned, no initialisation. 0
+ * where none is needed or the problem is invalid. */
+size_t kda_ssm_workspace_size(const kda_ssm_problem *p, int for_backward);
+size_t kda_ssm_saved_size(const kda_ssm_problem *p);
+
+/* Writes y [B*T, D] and, if not NULL, the final states ht [N, D, S] fp32, which
+ * may be the same buffer as h0 (decoding in place). */
+kda_status kda_ssm_fwd(const kda_ssm_problem *p, void *y, float *ht, void *saved, void *ws, size_t ws_bytes,
+                       int32_t *err, kda_stream_t stream);
+
+/* Gradients of <dy, y> + <dht, ht>; each of dd_skip, ddt_bias, dz and dh0 may be
+ * NULL where its input is absent (dd_skip, ddt_bias and dh0 also otherwise). */
+typedef struct {
+    void *dx, *ddt, *dz;        /* [B*T, D] */
+    void *db, *dc;              /* [B*T, G, S] */
+    float *dA_log;              /* [D, S] */
+    float *dd_skip, *ddt_bias;  /* [D] */
+    float *dh0;                 /* [N, D, S] */
+} kda_ssm_grads;
+
+/* dy [B*T, D], dht [N, D, S] fp32 or NULL. Sums over tokens and channels are
+ * formed in a fixed order (no atomics): repeated calls agree bitwise. */
+kda_status kda_ssm_bwd(const kda_ssm_problem *p, const void *dy, const float *dht, const void *saved,
+                       const kda_ssm_grads *g, void *ws, size_t ws_bytes, kda_stream_t stream);
+
+/* Root-mean-square norm of rows, with the residual's addition in front:
+ *     h = x + residual (fp32),  y = h (mean h^2 + eps)^(-1/2) weight.
+ * out 0: y in the I/O type. out 1: y as e4m3 bytes with fp32 scales per row and
+ * group of `group` columns (32, 64, 128, or 0 for the whole row; the last group
+ * may be short): scale = max |y| / 448, y ~ scale * e4m3. */
+typedef struct {
+    int rows, D;                /* D up to 16384 */
+    kda_dtype io;               /* type of x, residual, h (and y with out 0) */
+    int out, group;
+    float eps;
+    const void *x;              /* [rows, D] */
+    const void *residual;       /* [rows, D] or NULL */
+    const float *weight;        /* [D] fp32 */
+} kda_norm_problem;
+
+/* Writes y [rows, D], with out 1 scale [rows, ceil(D / group)], and with a
+ * residual h [rows, D] (rounded once; it may be the residual's or x's buffer). */
+kda_status kda_norm_fwd(const kda_norm_problem *p, void *y, float *scale, void *h, kda_stream_t stream);
+
+/* Bytes of workspace kda_norm_bwd needs (256-byte aligned; 0 for an invalid problem). */
+size_t kda_norm_workspace_size(const kda_norm_problem *p);
+
+/* Backward at p->x = the stored h (p->residual must be NULL, out and group are
+ * ignored): dy [rows, D]; dres [rows, D] or NULL, the gradient that reaches h
+ * past the norm, added to dx. Writes dx [rows, D] (the gradient of h, hence of x
+ * and of the residual) and dweight [D] fp32 (fixed order, bitwise repeatable).
+ * The rounding to 8 bits passes its gradient through. */
+kda_status kda_norm_bwd(const kda_norm_problem *p, const void *dy, const void *dres, void *dx, float *dweight,
+                        void *ws, size_t ws_bytes, kda_stream_t stream);
+
 /* Message for the last non-OK status returned on the calling thread
  * (thread-local; "" if none). */
 const char *kda_last_error(void);

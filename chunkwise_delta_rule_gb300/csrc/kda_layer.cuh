@@ -3,6 +3,8 @@
 // kda_ssm_bwd.cu) and the root-mean-square norm (kda_norm.cu).
 #pragma once
 
+#include <atomic>
+
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -19,6 +21,21 @@ cudaError_t traced_launch(const char* name, cudaStream_t st, F&& launch) {
     trace_close(id, st);
     return cudaGetLastError();
 }
+
+// A kernel's dynamic shared memory limit, raised once per device.
+struct SmemLimit {
+    std::atomic<uint64_t> done{0};
+    cudaError_t set(const void* kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
 
 // The token axis: equal-length sequences are `rows` rows of `len` tokens, one sequence each; packed
 // sequences are one row of all tokens, cut by the N + 1 offsets in cu.
@@ -161,6 +178,31 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&x)[V],
     }
 }
 
+// Asynchronous copies of a thread's own data into shared memory: n elements of a row of 8 (zeros past n), in
+// 16-byte, 4-byte or, for odd 16-bit addresses, plain accesses. `how`: 0, 1 or 2.
+template <typename TI>
+__device__ __forceinline__ void copy8_async(TI* dst, const TI* src, int n, int how) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if (how == 0 && (n >= 8 || n <= 0)) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(TI) / 2; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + 16 * i), "l"(reinterpret_cast<const char*>(src) + (n > 0 ? 16 * i : 0)), "r"(n > 0 ? 16 : 0) : "memory");
+    } else if (how <= 1) {
+        constexpr int PER = 4 / sizeof(TI);
+#pragma unroll
+        for (int i = 0; i < 8 / PER; ++i) {
+            const int left = min(max(n - i * PER, 0), PER) * (int)sizeof(TI);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d + 4 * i), "l"(src + (left > 0 ? i * PER : 0)), "r"(left) : "memory");
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dst[i] = i < n ? src[i] : TI(0.f);
+    }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // ------------------------------------------------------------------ launchers
 struct ConvArgs {
     TokenAxis ax;
@@ -203,12 +245,14 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int bf16, cudaStream_t st);
 // Checkpoint interval of the scan's saved states, in tokens.
 constexpr int SSM_CKPT = 16;
 
-enum { SSM_VEC_X = 1, SSM_VEC_DT = 2, SSM_VEC_Z = 4, SSM_VEC_B = 8, SSM_VEC_C = 16, SSM_VEC_OUT = 32 };
+// How the scan reaches the rows of its tensors, two bits each: 0 in 16-byte accesses, 1 in 4-byte ones, 2 element by
+// element (see copy8_async).
+enum { SSM_X = 0, SSM_DT = 2, SSM_Z = 4, SSM_B = 6, SSM_C = 8, SSM_DY = 10, SSM_OUT = 12 };
 
 struct SsmArgs {
     TokenAxis ax;
     int D, S, G, softplus;     // channels, states per channel, groups of b, c
-    int vec;                   // tensors whose rows take 16-byte accesses (SSM_VEC_*)
+    int how;                   // access to each tensor's rows (SSM_X ...)
     int units_row, unit_len;   // time pieces per row and their tokens (a multiple of 32)
     size_t ldx, lddt, ldz, ldb, ldc;
     const void *x, *dt, *z, *b, *c;

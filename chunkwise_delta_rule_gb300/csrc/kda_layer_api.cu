@@ -144,15 +144,21 @@ void ssm_pieces(kda::SsmArgs& a, bool backward) {
     a.unit_len = len > 0 ? len : 32;
     a.units_row = a.ax.len > 0 ? (a.ax.len + a.unit_len - 1) / a.unit_len : 1;
 }
-void ssm_vec(kda::SsmArgs& a, int es, const void* out) {
-    const size_t v = 16 / es;
-    const bool ch = a.G == 1 || (a.D / a.G) % v == 0, sc = a.G == 1 || a.S % v == 0;
-    a.vec = (ch && a.ldx % v == 0 && aligned16(a.x) ? kda::SSM_VEC_X : 0) |
-            (ch && a.lddt % v == 0 && aligned16(a.dt) ? kda::SSM_VEC_DT : 0) |
-            (ch && a.ldz % v == 0 && aligned16(a.z) ? kda::SSM_VEC_Z : 0) |
-            (sc && a.ldb % v == 0 && aligned16(a.b) ? kda::SSM_VEC_B : 0) |
-            (sc && a.ldc % v == 0 && aligned16(a.c) ? kda::SSM_VEC_C : 0) |
-            (ch && a.D % v == 0 && aligned16(out) ? kda::SSM_VEC_OUT : 0);
+// Access to the rows of p, `ld` elements apart; whether the groups inside a row start on 16 (4) bytes.
+int ssm_how(const void* p, size_t ld, bool groups16, bool groups4, int es, int shift) {
+    const uintptr_t q = reinterpret_cast<uintptr_t>(p);
+    const int how = groups16 && q % 16 == 0 && ld * es % 16 == 0 ? 0 : groups4 && q % 4 == 0 && ld * es % 4 == 0 ? 1 : 2;
+    return how << shift;
+}
+void ssm_access(kda::SsmArgs& a, int es, const void* dy, const void* o0, const void* o1, const void* o2) {
+    // a group's channels and states start D / G and S elements after the previous group's
+    const bool c16 = a.G == 1 || (size_t)(a.D / a.G) * es % 16 == 0, c4 = a.G == 1 || (size_t)(a.D / a.G) * es % 4 == 0;
+    const bool s16 = a.G == 1 || (size_t)a.S * es % 16 == 0, s4 = a.G == 1 || (size_t)a.S * es % 4 == 0;
+    const bool out = c16 && (size_t)a.D * es % 16 == 0 && aligned16(o0) && aligned16(o1) && aligned16(o2);
+    a.how = ssm_how(a.x, a.ldx, c16, c4, es, kda::SSM_X) | ssm_how(a.dt, a.lddt, c16, c4, es, kda::SSM_DT) |
+            ssm_how(a.z, a.ldz, c16, c4, es, kda::SSM_Z) | ssm_how(a.b, a.ldb, s16, s4, es, kda::SSM_B) |
+            ssm_how(a.c, a.ldc, s16, s4, es, kda::SSM_C) | ssm_how(dy, a.D, c16, c4, es, kda::SSM_DY) |
+            (out ? 0 : 2) << kda::SSM_OUT;
 }
 size_t ssm_state_bytes(const kda::SsmArgs& a, size_t n) { return up(sizeof(float) * n * a.D * a.S); }
 size_t ssm_ckpt_bytes(const kda::SsmArgs& a) {
@@ -277,7 +283,7 @@ kda_status kda_ssm_fwd(const kda_ssm_problem* p, void* y, float* ht, void* saved
     if ((st = check_ws(ws, ws_bytes, L.pieces + L.alias, "workspace")) != KDA_OK) return st;
     if (p->save_policy && (st = check_ws(saved, ssm_ckpt_bytes(a), ssm_ckpt_bytes(a), "saved buffer")) != KDA_OK) return st;
     const int bf16 = p->io == KDA_BF16;
-    ssm_vec(a, esize(p->io), y);
+    ssm_access(a, esize(p->io), nullptr, y, nullptr, nullptr);
     a.y = y;
     a.err = err;
     a.ckpt = p->save_policy ? static_cast<float*>(saved) : nullptr;
@@ -325,7 +331,7 @@ kda_status kda_ssm_bwd(const kda_ssm_problem* p, const void* dy, const float* dh
     a.pA = cw.take<float>(L.pA);
     a.pv = cw.take<float>(L.pv);
     a.pbc = cw.take<float>(L.pbc);
-    ssm_vec(a, esize(p->io), nullptr);
+    ssm_access(a, esize(p->io), dy, g->dx, g->ddt, g->dz);
     if (!p->save_policy && a.ax.len > 0) {
         if (a.units_row > 1 && (st = cuda_result(kda::launch_ssm_pieces(a, bf16, cs), "scan (pieces)")) != KDA_OK) return st;
         if ((st = cuda_result(kda::launch_ssm_fwd(a, bf16, 2, cs), "scan (recompute)")) != KDA_OK) return st;

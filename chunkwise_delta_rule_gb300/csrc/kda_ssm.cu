@@ -2,9 +2,14 @@
 //     delta = softplus(dt + dt_bias),  a = exp(-delta exp(A_log)),  u = delta x
 //     h_t = a h_{t-1} + u B_t,   y_t = (sum_n C_t[n] h_t[n] + d_skip x_t) silu(z_t)
 // Four lanes share a channel and hold its states in registers; a CTA of 128 threads
-// walks 32 channels through a time piece, tile by tile: the tile's steps are formed
-// once per (token, channel) in shared memory, the recurrence runs over them, and
-// the outputs are gated and stored from shared memory.
+// walks 32 channels through a time piece in tiles of 32 tokens. A thread copies its
+// share of a tile (8 channels of one token, 8 states of one row) into shared memory
+// asynchronously, several tiles ahead; the tile's steps are formed once per (token,
+// channel) and spread through shared memory; the recurrence runs over them with the
+// lanes' partial outputs left in shared memory; the sums are gated and stored.
+// Per four states and token the recurrence takes 4 exponentials (16 cycles of a
+// scheduler's share at 32 per cycle and SM) and 8 paired multiply-adds (16 cycles):
+// both pipes are full, which bounds the kernel, not memory.
 // A long row is cut into time pieces when its channels alone do not fill the GPU:
 // a first pass forms each piece's end state from zero and its sum of delta (the
 // piece's decay is exp(A sum delta)); in the second pass each piece joins the
@@ -15,18 +20,43 @@ namespace kda {
 namespace {
 
 constexpr int TT = 32;   // tokens per tile
-constexpr int YP = 40;   // row stride of the shared outputs (conflict-free for 4 tokens x 8 channels)
 
 enum { OUT = 0, OUT_CKPT = 1, CKPT = 2, PIECE = 3 };
 
 template <typename TI, int EL, int MODE>
+struct FwdShape {
+    static constexpr int NP = 4 * EL;
+    static constexpr bool HAS_Y = MODE == OUT || MODE == OUT_CKPT, HAS_CK = MODE == OUT_CKPT || MODE == CKPT;
+    static constexpr int ROWS = HAS_Y ? 2 * TT : TT;                    // rows of b (and c) in a tile
+    static constexpr int NBC = (ROWS * (NP / 8) + SSM_T - 1) / SSM_T;   // their chunks of 8 per thread
+    static constexpr int NTOK = HAS_Y ? 3 : 2;                          // x, dt (and z)
+    static constexpr int STAGES = sizeof(TI) == 2 ? (NP <= 32 ? 4 : 3) : (NP <= 32 ? 3 : 2);
+    struct Smem {
+        TI raw[STAGES][NTOK + NBC][SSM_T][8];
+        float4 du[TT][SSM_CH / 2];          // (delta, u) of two channels; see du_at
+        float b[TT][NP];
+        float c[HAS_Y ? TT : 1][NP];
+        float y[HAS_Y ? TT : 1][SSM_CH][4]; // the four lanes' parts; see y_at
+    };
+};
+
+// Places of channel pairs and of channels in a token's row, permuted so that the eight threads of a quarter warp that
+// hold (two tokens) x (four groups of 8 channels) reach distinct banks.
+__device__ __forceinline__ int du_at(int tok, int pair) { return pair ^ ((pair >> 3) | (tok & 1) << 1); }
+__device__ __forceinline__ int y_at(int tok, int ch) { return ch ^ ((ch >> 3) | (tok & 1) << 2); }
+
+template <int V>
+__device__ __forceinline__ void raw_row(const float* p, float (&x)[V]) { load_row<V>(p, x, V, true); }
+template <int V>
+__device__ __forceinline__ void raw_row(const __nv_bfloat16* p, float (&x)[V]) { load_row<V>(p, x, V, true); }
+
+template <typename TI, int EL, int MODE>
 __global__ void __launch_bounds__(SSM_T) k_ssm_fwd(SsmArgs a) {
-    constexpr int NP = 4 * EL;
-    constexpr bool HAS_Y = MODE == OUT || MODE == OUT_CKPT, HAS_CK = MODE == OUT_CKPT || MODE == CKPT;
-    __shared__ float2 s_du[TT][SSM_CH];
-    __shared__ __align__(16) float s_b[TT][NP];
-    __shared__ __align__(16) float s_c[HAS_Y ? TT : 1][NP];
-    __shared__ float s_y[HAS_Y ? TT : 1][YP];
+    using Sh = FwdShape<TI, EL, MODE>;
+    constexpr int NP = Sh::NP, NBC = Sh::NBC, STAGES = Sh::STAGES, P = EL / 2;
+    constexpr bool HAS_Y = Sh::HAS_Y, HAS_CK = Sh::HAS_CK;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    typename Sh::Smem& sm = *reinterpret_cast<typename Sh::Smem*>(smem_raw);
     if (blockIdx.x == 0 && MODE != PIECE) axis_check(a.ax, a.err);
     const SsmPlace pl = ssm_place(a);
     const int tid = threadIdx.x, l = tid & 3, ch = tid >> 2, n0 = l * EL;
@@ -64,20 +94,52 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_fwd(SsmArgs a) {
         s = seq_at(a.ax, pl.row, pl.hi - 1);
         if (s.end <= pl.hi) return;
         t = max(pl.lo, s.first);
-        if (s.first >= pl.lo) init_state(s.n);
-        else {
-#pragma unroll
-            for (int e = 0; e < EL; ++e) h[e] = 0.f;
-        }
     } else {
         s = seq_at(a.ax, pl.row, t);
-        if (t == s.first) {
-            init_state(s.n);
-        } else {
-            // the state entering this piece: the earlier pieces of its sequence, joined in order
-            const int q = s.first / a.unit_len;
+    }
+    // this thread's part of a tile: one token, 8 channels; NBC chunks of 8 states of b's and c's rows
+    const int ptok = tid >> 2, pc = (tid & 3) * 8, pvalid = pl.nch - pc;
+    const TI* xp = static_cast<const TI*>(a.x) + tok0 * a.ldx + pl.c0 + pc;
+    const TI* dp = static_cast<const TI*>(a.dt) + tok0 * a.lddt + pl.c0 + pc;
+    const TI* zp = a.z ? static_cast<const TI*>(a.z) + tok0 * a.ldz + pl.c0 + pc : nullptr;
+    const TI* bp = static_cast<const TI*>(a.b) + tok0 * a.ldb + (size_t)pl.g * a.S;
+    const TI* cp = static_cast<const TI*>(a.c) + tok0 * a.ldc + (size_t)pl.g * a.S;
+    constexpr int NC = NP / 8;
+    const int first_tile = t;
+    auto fetch = [&](int k) {   // tile k of the piece into its stage
+        const int tb = first_tile + k * TT;
+        if (tb < pl.hi) {
+            TI(*raw)[SSM_T][8] = sm.raw[k % STAGES];
+            const size_t tt = min(tb + ptok, pl.hi - 1);
+            const int n = tb + ptok < pl.hi ? pvalid : 0;
+            copy8_async(raw[0][tid], xp + tt * a.ldx, n, a.how >> SSM_X & 3);
+            copy8_async(raw[1][tid], dp + tt * a.lddt, n, a.how >> SSM_DT & 3);
+            if (HAS_Y && zp) copy8_async(raw[2][tid], zp + tt * a.ldz, n, a.how >> SSM_Z & 3);
 #pragma unroll
-            for (int e = 0; e < EL; ++e) h[e] = 0.f;
+            for (int j = 0; j < NBC; ++j) {
+                const int i = tid + j * SSM_T;
+                if (i >= Sh::ROWS * NC) break;
+                const bool isc = i >= TT * NC;
+                const int r = isc ? i - TT * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
+                const size_t tr = min(tb + tok, pl.hi - 1);
+                const int m = tb + tok < pl.hi ? a.S - k8 : 0;
+                const TI* src = isc ? cp + tr * a.ldc : bp + tr * a.ldb;
+                copy8_async(raw[Sh::NTOK + j][tid], src + (m > 0 ? k8 : 0), m, a.how >> (isc ? SSM_C : SSM_B) & 3);
+            }
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < STAGES - 1; ++k) fetch(k);
+    // the state entering this piece
+    if (MODE == PIECE ? s.first >= pl.lo : t == s.first) {
+        init_state(s.n);
+    } else {
+#pragma unroll
+        for (int e = 0; e < EL; ++e) h[e] = 0.f;
+        if (MODE != PIECE) {
+            // the earlier pieces of its sequence, joined in order
+            const int q = s.first / a.unit_len;
             for (int r = q; r < pl.u; ++r) {
                 const size_t ru = (size_t)pl.row * a.units_row + r;
                 float hl[EL];
@@ -88,53 +150,72 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_fwd(SsmArgs a) {
             }
         }
     }
-    // this thread's part of a tile: one token, 8 channels
-    const int ptok = tid >> 2, pc = (tid & 3) * 8, pvalid = pl.nch - pc;
-    const TI* xp = static_cast<const TI*>(a.x) + tok0 * a.ldx + pl.c0 + pc;
-    const TI* dp = static_cast<const TI*>(a.dt) + tok0 * a.lddt + pl.c0 + pc;
-    const TI* zp = a.z ? static_cast<const TI*>(a.z) + tok0 * a.ldz + pl.c0 + pc : nullptr;
-    const TI* bp = static_cast<const TI*>(a.b) + tok0 * a.ldb + (size_t)pl.g * a.S;
-    const TI* cp = static_cast<const TI*>(a.c) + tok0 * a.ldc + (size_t)pl.g * a.S;
-    const bool wide = pvalid >= 8;
     float bias[8], skip[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         bias[i] = a.dt_bias && i < pvalid ? a.dt_bias[pl.c0 + pc + i] : 0.f;
-        skip[i] = a.d_skip && i < pvalid ? a.d_skip[pl.c0 + pc + i] : 0.f;
+        skip[i] = HAS_Y && a.d_skip && i < pvalid ? a.d_skip[pl.c0 + pc + i] : 0.f;
     }
-    for (int tb = t; tb < pl.hi; tb += TT) {
-        const int te = min(tb + TT, pl.hi);
-        float x[8], dt[8];
-        const bool in = tb + ptok < te && pvalid > 0;
-        if (in) {
-            load_row<8>(xp + (size_t)(tb + ptok) * a.ldx, x, pvalid, wide && (a.vec & SSM_VEC_X));
-            load_row<8>(dp + (size_t)(tb + ptok) * a.lddt, dt, pvalid, wide && (a.vec & SSM_VEC_DT));
+    // N tokens of the recurrence from tile row i: every operand read before the first store
+    auto tokens = [&](int i, auto n_) {
+        constexpr int N = decltype(n_)::value;
+        float2 du[N], b[N][P], c[N][P], acc[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            du[j] = reinterpret_cast<const float2*>(&sm.du[i + j][du_at(i + j, ch >> 1)])[ch & 1];
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                b[j][e] = reinterpret_cast<const float2*>(&sm.b[i + j][n0])[e];
+                if (HAS_Y) c[j][e] = reinterpret_cast<const float2*>(&sm.c[HAS_Y ? i + j : 0][n0])[e];
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float dl = 0.f;
-            if (in) {
-                dl = dt[i] + bias[i];
-                if (a.softplus) dl = ssm_softplus(dl);
-            } else {
-                x[i] = 0.f;
+        for (int j = 0; j < N; ++j) {
+            const float2 dl = make_float2(du[j].x, du[j].x), u = make_float2(du[j].y, du[j].y);
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                const float2 g = mul2(dl, make_float2(A2[2 * e], A2[2 * e + 1]));
+                const float2 hn = fma2(make_float2(ex2(g.x), ex2(g.y)), make_float2(h[2 * e], h[2 * e + 1]), mul2(u, b[j][e]));
+                h[2 * e] = hn.x;
+                h[2 * e + 1] = hn.y;
+                if (HAS_Y) acc[j] = e == 0 ? mul2(hn, c[j][e]) : fma2(hn, c[j][e], acc[j]);
             }
-            s_du[ptok][pc + i] = make_float2(dl, dl * x[i]);
+            if (MODE == PIECE) sd += du[j].x;
         }
-        constexpr int NC = NP / 8;   // chunks of 8 states per row
-        for (int i = tid; i < TT * NC * (HAS_Y ? 2 : 1); i += SSM_T) {
+        if (HAS_Y) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) sm.y[HAS_Y ? i + j : 0][y_at(i + j, ch)][l] = acc[j].x + acc[j].y;
+        }
+    };
+    for (int k = 0; first_tile + k * TT < pl.hi; ++k) {
+        const int tb = first_tile + k * TT, te = min(tb + TT, pl.hi);
+        fetch(k + STAGES - 1);
+        copies_wait<STAGES - 1>();
+        TI(*raw)[SSM_T][8] = sm.raw[k % STAGES];
+        float x[8];
+        {
+            float dt[8];
+            raw_row<8>(raw[0][tid], x);
+            raw_row<8>(raw[1][tid], dt);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                float2 dl = make_float2(dt[i] + bias[i], dt[i + 1] + bias[i + 1]);
+                if (a.softplus) dl = ssm_softplus2(dl);
+                const float2 u = mul2(dl, make_float2(x[i], x[i + 1]));
+                sm.du[ptok][du_at(ptok, (pc + i) >> 1)] = make_float4(dl.x, u.x, dl.y, u.y);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NBC; ++j) {
+            const int i = tid + j * SSM_T;
+            if (i >= Sh::ROWS * NC) break;
             const bool isc = i >= TT * NC;
-            const int j = isc ? i - TT * NC : i, tok = j / NC, k = (j - tok * NC) * 8;
+            const int r = isc ? i - TT * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
             float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
-            if (tb + tok < te) {
-                if (isc) load_row<8>(cp + (size_t)(tb + tok) * a.ldc + k, v, a.S - k, a.S - k >= 8 && (a.vec & SSM_VEC_C));
-                else load_row<8>(bp + (size_t)(tb + tok) * a.ldb + k, v, a.S - k, a.S - k >= 8 && (a.vec & SSM_VEC_B));
-            }
-            float* dst = isc ? &s_c[HAS_Y ? tok : 0][k] : &s_b[tok][k];
-            reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            raw_row<8>(raw[Sh::NTOK + j][tid], v);
+            float4* dst = reinterpret_cast<float4*>(isc ? &sm.c[HAS_Y ? tok : 0][k8] : &sm.b[tok][k8]);
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
         __syncthreads();
         t = tb;
@@ -150,42 +231,22 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_fwd(SsmArgs a) {
             }
             int run = MODE == PIECE ? te : min(te, s.end);
             if (HAS_CK) run = min(run, (t | (SSM_CKPT - 1)) + 1);
-            for (; t < run; t += 4) {
-                float acc[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[i] = 0.f;
-                    if (t + i >= run) continue;
-                    const float2 du = s_du[t + i - tb][ch];
-                    float b[EL], c[EL];
-                    lds_states<EL>(&s_b[t + i - tb][n0], b);
-                    if (HAS_Y) lds_states<EL>(&s_c[HAS_Y ? t + i - tb : 0][n0], c);
-#pragma unroll
-                    for (int e = 0; e < EL; ++e) {
-                        h[e] = fmaf(ex2(du.x * A2[e]), h[e], du.y * b[e]);
-                        if (HAS_Y) acc[i] = fmaf(h[e], c[e], acc[i]);
-                    }
-                    if (MODE == PIECE) sd += du.x;
-                }
-                if (HAS_Y) {
-                    // lane l of a channel's four keeps token l's sum
-                    halve<4>(acc, l, 2);
-                    halve<2>(acc, l, 1);
-                    if (t + l < run) s_y[HAS_Y ? t + l - tb : 0][ch] = acc[0];
-                }
-            }
-            t = run;
+#pragma unroll 2
+            for (; t + 4 <= run; t += 4) tokens(t - tb, Int<4>{});
+            for (; t < run; ++t) tokens(t - tb, Int<1>{});
         }
         __syncthreads();
-        if (HAS_Y && in) {
+        if (HAS_Y && tb + ptok < te && pvalid > 0) {
             float o[8], z[8];
-            if (zp) load_row<8>(zp + (size_t)(tb + ptok) * a.ldz, z, pvalid, wide && (a.vec & SSM_VEC_Z));
+            if (zp) raw_row<8>(raw[HAS_Y ? 2 : 0][tid], z);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                o[i] = fmaf(skip[i], x[i], s_y[HAS_Y ? ptok : 0][pc + i]);
+                const float4 v = *reinterpret_cast<const float4*>(sm.y[HAS_Y ? ptok : 0][y_at(ptok, pc + i)]);
+                o[i] = fmaf(skip[i], x[i], (v.x + v.y) + (v.z + v.w));
                 if (zp) o[i] *= z[i] * sigmoid_fast(z[i]);
             }
-            store_row<8>(static_cast<TI*>(a.y) + (tok0 + tb + ptok) * a.D + pl.c0 + pc, o, pvalid, wide && (a.vec & SSM_VEC_OUT));
+            store_row<8>(static_cast<TI*>(a.y) + (tok0 + tb + ptok) * a.D + pl.c0 + pc, o, pvalid,
+                         pvalid >= 8 && !(a.how >> SSM_OUT & 3));
         }
     }
     if (MODE == PIECE) {
@@ -196,22 +257,139 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_fwd(SsmArgs a) {
     }
 }
 
+// A few tokens of each sequence (decoding): the state is the traffic, 8 bytes per value against 8 per channel for the
+// token. The same four lanes per channel, NS sequences per thread so that their states are in flight together and A is
+// formed once; everything is read directly, and after the exchange over the four lanes lane i holds sequence i's output.
+template <typename TI, int EL, int NS>
+__global__ void __launch_bounds__(SSM_T) k_ssm_step(SsmArgs a) {
+    static_assert(NS == 1 || NS == 4, "sequences per thread");
+    const int M = a.D / a.G, tpg = (M + SSM_CH - 1) / SSM_CH, tiles = tpg * a.G;
+    const int sb = blockIdx.x / tiles, tile = blockIdx.x - sb * tiles, g = tile / tpg, tg = tile - g * tpg;
+    const int l = threadIdx.x & 3, ch = threadIdx.x >> 2, n0 = l * EL, d = g * M + tg * SSM_CH + ch;
+    const bool on = ch < M - tg * SSM_CH;
+    const size_t DS = (size_t)a.D * a.S;
+    const int B = a.ax.N, T = a.ax.len, s0 = sb * NS;
+    float A2[EL], h[NS][EL];
+    load_states<EL>(a.A_log + (size_t)d * a.S, n0, a.S, on, A2);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        if (a.h0 && s0 + i < B) {
+            load_states<EL>(a.h0 + (s0 + i) * DS + (size_t)d * a.S, n0, a.S, on, h[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < EL; ++e) h[i][e] = 0.f;
+        }
+    }
+    const float bias = a.dt_bias && on ? a.dt_bias[d] : 0.f, skip = a.d_skip && on ? a.d_skip[d] : 0.f;
+    for (int t = 0; t < T; ++t) {
+        float x[NS], dt[NS], b[NS][EL], c[NS][EL], acc[NS];
+        const int mine = s0 + (NS == 4 ? l : 0);   // the sequence whose output this lane stores
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const bool in = on && s0 + i < B;
+            const size_t tok = (size_t)(s0 + i) * T + t;
+            x[i] = in ? ld(static_cast<const TI*>(a.x) + tok * a.ldx + d) : 0.f;
+            dt[i] = in ? ld(static_cast<const TI*>(a.dt) + tok * a.lddt + d) : 0.f;
+            const TI* bp = static_cast<const TI*>(a.b) + tok * a.ldb + (size_t)g * a.S + n0;
+            const TI* cp = static_cast<const TI*>(a.c) + tok * a.ldc + (size_t)g * a.S + n0;
+#pragma unroll
+            for (int e = 0; e < EL; ++e) {
+                const bool one = s0 + i < B && n0 + e < a.S;
+                b[i][e] = one ? ld(bp + e) : 0.f;
+                c[i][e] = one ? ld(cp + e) : 0.f;
+            }
+        }
+        const bool store = on && mine < B && (NS == 4 || l == 0);
+        if (a.z && store) z = ld(static_cast<const TI*>(a.z) + ((size_t)mine * T + t) * a.ldz + d);
+        if (t == 0) {
+#pragma unroll
+            for (int e = 0; e < EL; ++e) A2[e] = on && n0 + e < a.S ? -expf(A2[e]) * LOG2E : 0.f;
+        }
+        float xm = 0.f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            float dl = dt[i] + bias;
+            if (a.softplus) dl = ssm_softplus(dl);
+            const float u = dl * x[i];
+            acc[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < EL; ++e) {
+                h[i][e] = fmaf(ex2(dl * A2[e]), h[i][e], u * b[i][e]);
+                acc[i] = fmaf(h[i][e], c[i][e], acc[i]);
+            }
+            if (i == 0 || l == i) xm = x[i];
+        }
+        if (NS == 4) {
+            halve<4>(acc, l, 2);
+            halve<2>(acc, l, 1);
+        } else {
+            acc[0] += __shfl_xor_sync(SSM_FULL, acc[0], 2);
+            acc[0] += __shfl_xor_sync(SSM_FULL, acc[0], 1);
+        }
+        if (store) {
+            float o = fmaf(skip, xm, acc[0]);
+            if (a.z) o *= z * sigmoid_fast(z);
+            st(static_cast<TI*>(a.y) + ((size_t)mine * T + t) * a.D + d, o);
+        }
+    }
+    if (a.ht) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (s0 + i < B) store_states<EL>(a.ht + (s0 + i) * DS + (size_t)d * a.S, n0, a.S, on, h[i]);
+    }
+}
+
 template <typename TI, int EL>
-void run_mode(const SsmArgs& a, int mode, unsigned grid, cudaStream_t st) {
+void run_step(const SsmArgs& a, cudaStream_t st) {
+    const unsigned tiles = ssm_channel_tiles(a.D, a.G);
+    // four sequences per thread once that still leaves every SM two CTAs
+    if ((long long)tiles * (a.ax.N / 4) >= 2 * sm_count()) k_ssm_step<TI, EL, 4><<<tiles * ((a.ax.N + 3) / 4), SSM_T, 0, st>>>(a);
+    else k_ssm_step<TI, EL, 1><<<tiles * a.ax.N, SSM_T, 0, st>>>(a);
+}
+
+template <typename TI, int EL, int MODE>
+cudaError_t run_one(const SsmArgs& a, cudaStream_t st) {
+    const unsigned grid = (unsigned)(a.ax.rows * a.units_row) * ssm_channel_tiles(a.D, a.G);
+    const int smem = (int)sizeof(typename FwdShape<TI, EL, MODE>::Smem);
+    static SmemLimit limit;
+    const cudaError_t e = limit.set(reinterpret_cast<const void*>(k_ssm_fwd<TI, EL, MODE>), smem);
+    if (e != cudaSuccess) return e;
+    k_ssm_fwd<TI, EL, MODE><<<grid, SSM_T, smem, st>>>(a);
+    return cudaSuccess;
+}
+template <typename TI, int EL>
+cudaError_t run_mode(const SsmArgs& a, int mode, cudaStream_t st) {
     switch (mode) {
-        case OUT: k_ssm_fwd<TI, EL, OUT><<<grid, SSM_T, 0, st>>>(a); break;
-        case OUT_CKPT: k_ssm_fwd<TI, EL, OUT_CKPT><<<grid, SSM_T, 0, st>>>(a); break;
-        case CKPT: k_ssm_fwd<TI, EL, CKPT><<<grid, SSM_T, 0, st>>>(a); break;
-        default: k_ssm_fwd<TI, EL, PIECE><<<grid, SSM_T, 0, st>>>(a); break;
+        case OUT: return run_one<TI, EL, OUT>(a, st);
+        case OUT_CKPT: return run_one<TI, EL, OUT_CKPT>(a, st);
+        case CKPT: return run_one<TI, EL, CKPT>(a, st);
+        default: return run_one<TI, EL, PIECE>(a, st);
     }
 }
 template <typename TI>
-void run_states(const SsmArgs& a, int mode, cudaStream_t st) {
-    const unsigned grid = (unsigned)(a.ax.rows * a.units_row) * ssm_channel_tiles(a.D, a.G);
-    if (a.S <= 8) run_mode<TI, 2>(a, mode, grid, st);
-    else if (a.S <= 16) run_mode<TI, 4>(a, mode, grid, st);
-    else if (a.S <= 32) run_mode<TI, 8>(a, mode, grid, st);
-    else run_mode<TI, 16>(a, mode, grid, st);
+cudaError_t run_states(const SsmArgs& a, int mode, cudaStream_t st) {
+    if (a.S <= 8) return run_mode<TI, 2>(a, mode, st);
+    if (a.S <= 16) return run_mode<TI, 4>(a, mode, st);
+    if (a.S <= 32) return run_mode<TI, 8>(a, mode, st);
+    return run_mode<TI, 16>(a, mode, st);
+}
+template <typename TI>
+void run_step_states(const SsmArgs& a, cudaStream_t st) {
+    if (a.S <= 8) run_step<TI, 2>(a, st);
+    else if (a.S <= 16) run_step<TI, 4>(a, st);
+    else if (a.S <= 32) run_step<TI, 8>(a, st);
+    else run_step<TI, 16>(a, st);
+}
+// Tokens per sequence up to which everything is read directly: past it the tiles' prefetch pays.
+constexpr int STEP_TOKENS = 4;
+
+cudaError_t launch(const char* name, const SsmArgs& a, int bf16, int mode, cudaStream_t st) {
+    cudaError_t r = cudaSuccess;
+    const cudaError_t e = traced_launch(name, st, [&] {
+        r = bf16 ? run_states<__nv_bfloat16>(a, mode, st) : run_states<float>(a, mode, st);
+    });
+    return r != cudaSuccess ? r : e;
 }
 
 }  // namespace
@@ -228,15 +406,15 @@ int ssm_units(int rows, int len, int D, int G, int S, bool backward) {
 }
 
 cudaError_t launch_ssm_fwd(const SsmArgs& a, int bf16, int mode, cudaStream_t st) {
-    return traced_launch(mode == CKPT ? "k_ssm_ckpt" : "k_ssm_fwd", st, [&] {
-        bf16 ? run_states<__nv_bfloat16>(a, mode, st) : run_states<float>(a, mode, st);
-    });
+    if (mode == OUT && !a.ax.cu && a.ax.len > 0 && a.ax.len <= STEP_TOKENS)
+        return traced_launch("k_ssm_step", st, [&] {
+            bf16 ? run_step_states<__nv_bfloat16>(a, st) : run_step_states<float>(a, st);
+        });
+    return launch(mode == CKPT ? "k_ssm_ckpt" : "k_ssm_fwd", a, bf16, mode, st);
 }
 
 cudaError_t launch_ssm_pieces(const SsmArgs& a, int bf16, cudaStream_t st) {
-    return traced_launch("k_ssm_pieces", st, [&] {
-        bf16 ? run_states<__nv_bfloat16>(a, PIECE, st) : run_states<float>(a, PIECE, st);
-    });
+    return launch("k_ssm_pieces", a, bf16, PIECE, st);
 }
 
 }  // namespace kda

@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_bwd(SsmArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = 0.f;
             if (tb + tok < te) {
-                if (isc) load_row<8>(cp + (size_t)(tb + tok) * a.ldc + k, v, a.S - k, a.S - k >= 8 && (a.vec & SSM_VEC_C));
-                else load_row<8>(bp + (size_t)(tb + tok) * a.ldb + k, v, a.S - k, a.S - k >= 8 && (a.vec & SSM_VEC_B));
+                if (isc) load_row<8>(cp + (size_t)(tb + tok) * a.ldc + k, v, a.S - k, a.S - k >= 8 && !(a.how >> SSM_C & 3));
+                else load_row<8>(bp + (size_t)(tb + tok) * a.ldb + k, v, a.S - k, a.S - k >= 8 && !(a.how >> SSM_B & 3));
             }
             float* dst = isc ? &sm.c[tok][k] : &sm.b[tok][k];
             reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_bwd_pieces(SsmArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = 0.f;
             if (tb + tok < te)
-                load_row<8>(cp + (size_t)(tb + tok) * a.ldc + k, v, a.S - k, a.S - k >= 8 && (a.vec & SSM_VEC_C));
+                load_row<8>(cp + (size_t)(tb + tok) * a.ldc + k, v, a.S - k, a.S - k >= 8 && !(a.how >> SSM_C & 3));
             reinterpret_cast<float4*>(&s_c[tok][k])[0] = make_float4(v[0], v[1], v[2], v[3]);
             reinterpret_cast<float4*>(&s_c[tok][k])[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
@@ -416,7 +416,8 @@ __global__ void k_ssm_sums(SsmArgs a, unsigned nbc) {
 template <typename TI, int EL>
 cudaError_t run_bwd(const SsmArgs& a, unsigned grid, cudaStream_t st) {
     const size_t smem = sizeof(typename BwdShape<EL>::Smem);
-    cudaError_t e = cudaFuncSetAttribute(k_ssm_bwd<TI, EL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemLimit limit;
+    const cudaError_t e = limit.set(reinterpret_cast<const void*>(k_ssm_bwd<TI, EL>), (int)smem);
     if (e != cudaSuccess) return e;
     k_ssm_bwd<TI, EL><<<grid, SSM_T, smem, st>>>(a);
     return cudaSuccess;

@@ -1,12 +1,12 @@
 // Selective state space scan (diagonal, input-dependent step), forward:
 //     delta = softplus(dt + dt_bias),  a = exp(-delta exp(A_log)),  u = delta x
 //     h_t = a h_{t-1} + u B_t,   y_t = (sum_n C_t[n] h_t[n] + d_skip x_t) silu(z_t)
-// Four lanes share a channel and hold its states in registers; a CTA of 128 threads
-// walks 32 channels through a time piece in tiles of 32 tokens. A thread copies its
-// share of a tile (8 channels of one token, 8 states of one row) into shared memory
-// asynchronously, several tiles ahead; the tile's steps are formed once per (token,
-// channel) and spread through shared memory; the recurrence runs over them with the
-// lanes' partial outputs left in shared memory; the sums are gated and stored.
+// Four lanes share a channel and hold its states in registers; a CTA walks 32 channels
+// through a time piece in tiles of 32 tokens. Four warps run the recurrence, four
+// others work around it, so that the recurrence never waits for them: while tile k
+// runs they copy tiles ahead into shared memory (asynchronously, each thread its own 8
+// channels of one token and 8 states of one row), form tile k + 1's steps once per
+// (token, channel), and sum, gate and store tile k - 1's outputs. One barrier per tile.
 // Per four states and token the recurrence takes 4 exponentials (16 cycles of a
 // scheduler's share at 32 per cycle and SM) and 8 paired multiply-adds (16 cycles):
 // both pipes are full, which bounds the kernel, not memory.
@@ -23,6 +23,8 @@ constexpr int TT = 32;   // tokens per tile
 
 enum { OUT = 0, OUT_CKPT = 1, CKPT = 2, PIECE = 3 };
 
+constexpr int FT = 2 * SSM_T;   // threads: 128 for the recurrence, 128 around it
+
 template <typename TI, int EL, int MODE>
 struct FwdShape {
     static constexpr int NP = 4 * EL;
@@ -30,13 +32,14 @@ struct FwdShape {
     static constexpr int ROWS = HAS_Y ? 2 * TT : TT;                    // rows of b (and c) in a tile
     static constexpr int NBC = (ROWS * (NP / 8) + SSM_T - 1) / SSM_T;   // their chunks of 8 per thread
     static constexpr int NTOK = HAS_Y ? 3 : 2;                          // x, dt (and z)
-    static constexpr int STAGES = sizeof(TI) == 2 ? (NP <= 32 ? 4 : 3) : (NP <= 32 ? 3 : 2);
+    // tiles in flight: the previous (its x and z), the current, the next, and those copied ahead
+    static constexpr int STAGES = sizeof(TI) == 2 ? (NP <= 32 ? 6 : 5) : (NP <= 16 ? 5 : 4);
     struct Smem {
         TI raw[STAGES][NTOK + NBC][SSM_T][8];
-        float4 du[TT][SSM_CH / 2];          // (delta, u) of two channels; see du_at
-        float b[TT][NP];
-        float c[HAS_Y ? TT : 1][NP];
-        float y[HAS_Y ? TT : 1][SSM_CH][4]; // the four lanes' parts; see y_at
+        float4 du[2][TT][SSM_CH / 2];          // (delta, u) of two channels; see du_at
+        float b[2][TT][NP];
+        float c[2][HAS_Y ? TT : 1][NP];
+        float y[2][HAS_Y ? TT : 1][SSM_CH][4]; // the four lanes' parts; see y_at
     };
 };
 
@@ -45,13 +48,8 @@ struct FwdShape {
 __device__ __forceinline__ int du_at(int tok, int pair) { return pair ^ ((pair >> 3) | (tok & 1) << 1); }
 __device__ __forceinline__ int y_at(int tok, int ch) { return ch ^ ((ch >> 3) | (tok & 1) << 2); }
 
-template <int V>
-__device__ __forceinline__ void raw_row(const float* p, float (&x)[V]) { load_row<V>(p, x, V, true); }
-template <int V>
-__device__ __forceinline__ void raw_row(const __nv_bfloat16* p, float (&x)[V]) { load_row<V>(p, x, V, true); }
-
 template <typename TI, int EL, int MODE>
-__global__ void __launch_bounds__(SSM_T) k_ssm_fwd(SsmArgs a) {
+__global__ void __launch_bounds__(FT, 2) k_ssm_fwd(SsmArgs a) {
     using Sh = FwdShape<TI, EL, MODE>;
     constexpr int NP = Sh::NP, NBC = Sh::NBC, STAGES = Sh::STAGES, P = EL / 2;
     constexpr bool HAS_Y = Sh::HAS_Y, HAS_CK = Sh::HAS_CK;
@@ -59,11 +57,118 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_fwd(SsmArgs a) {
     typename Sh::Smem& sm = *reinterpret_cast<typename Sh::Smem*>(smem_raw);
     if (blockIdx.x == 0 && MODE != PIECE) axis_check(a.ax, a.err);
     const SsmPlace pl = ssm_place(a);
-    const int tid = threadIdx.x, l = tid & 3, ch = tid >> 2, n0 = l * EL;
-    const int d = pl.c0 + ch;
-    const bool on = ch < pl.nch;
     const size_t tok0 = (size_t)pl.row * a.ax.len;
     const size_t DS = (size_t)a.D * a.S;
+    int t = pl.lo;
+    Seq s{0, 0, 0};
+    if (pl.lo < pl.hi || !a.ax.cu) {
+        if (MODE == PIECE) {
+            // the part of the piece that reaches past its end
+            s = seq_at(a.ax, pl.row, pl.hi - 1);
+            if (s.end <= pl.hi) return;
+            t = max(pl.lo, s.first);
+        } else {
+            s = seq_at(a.ax, pl.row, t);
+        }
+    }
+    const int first_tile = t, ntiles = (pl.hi - t + TT - 1) / TT;
+    const int tid = threadIdx.x & (SSM_T - 1);
+
+    if (threadIdx.x >= SSM_T) {
+        // ---------------------------------------------------------------- around the recurrence
+        // this thread's part of a tile: one token, 8 channels; NBC chunks of 8 states of b's and c's rows
+        const int ptok = tid >> 2, pc = (tid & 3) * 8, pvalid = pl.nch - pc;
+        const TI* xp = static_cast<const TI*>(a.x) + tok0 * a.ldx + pl.c0 + pc;
+        const TI* dp = static_cast<const TI*>(a.dt) + tok0 * a.lddt + pl.c0 + pc;
+        const TI* zp = a.z ? static_cast<const TI*>(a.z) + tok0 * a.ldz + pl.c0 + pc : nullptr;
+        const TI* bp = static_cast<const TI*>(a.b) + tok0 * a.ldb + (size_t)pl.g * a.S;
+        const TI* cp = static_cast<const TI*>(a.c) + tok0 * a.ldc + (size_t)pl.g * a.S;
+        constexpr int NC = NP / 8;
+        auto fetch = [&](int k) {   // tile k of the piece into its stage
+            const int tb = first_tile + k * TT;
+            if (k < ntiles) {
+                TI(*raw)[SSM_T][8] = sm.raw[k % STAGES];
+                const size_t tt = min(tb + ptok, pl.hi - 1);
+                const int n = tb + ptok < pl.hi ? pvalid : 0;
+                copy8_async(raw[0][tid], xp + tt * a.ldx, n, a.how >> SSM_X & 3);
+                copy8_async(raw[1][tid], dp + tt * a.lddt, n, a.how >> SSM_DT & 3);
+                if (HAS_Y && zp) copy8_async(raw[2][tid], zp + tt * a.ldz, n, a.how >> SSM_Z & 3);
+#pragma unroll
+                for (int j = 0; j < NBC; ++j) {
+                    const int i = tid + j * SSM_T;
+                    if (i >= Sh::ROWS * NC) break;
+                    const bool isc = i >= TT * NC;
+                    const int r = isc ? i - TT * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
+                    const size_t tr = min(tb + tok, pl.hi - 1);
+                    const int m = tb + tok < pl.hi ? a.S - k8 : 0;
+                    const TI* src = isc ? cp + tr * a.ldc : bp + tr * a.ldb;
+                    copy8_async(raw[Sh::NTOK + j][tid], src + (m > 0 ? k8 : 0), m, a.how >> (isc ? SSM_C : SSM_B) & 3);
+                }
+            }
+            copies_commit();
+        };
+        for (int k = 0; k < STAGES - 2; ++k) fetch(k);
+        float bias[8], skip[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            bias[i] = a.dt_bias && i < pvalid ? a.dt_bias[pl.c0 + pc + i] : 0.f;
+            skip[i] = HAS_Y && a.d_skip && i < pvalid ? a.d_skip[pl.c0 + pc + i] : 0.f;
+        }
+        // step k: tile k + 1's steps, tile k - 1's outputs (k = -1: the first tile's steps alone)
+        for (int k = -1; k <= ntiles; ++k) {
+            if (k + 1 < ntiles) {
+                const int w = (k + 1) & 1;
+                copies_wait<STAGES - 3>();
+                TI(*raw)[SSM_T][8] = sm.raw[(k + 1) % STAGES];
+                float x[8], dt[8];
+                load_row<8>(raw[0][tid], x, 8, true);
+                load_row<8>(raw[1][tid], dt, 8, true);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    float2 dl = make_float2(dt[i] + bias[i], dt[i + 1] + bias[i + 1]);
+                    if (a.softplus) dl = ssm_softplus2(dl);
+                    const float2 u = mul2(dl, make_float2(x[i], x[i + 1]));
+                    sm.du[w][ptok][du_at(ptok, (pc + i) >> 1)] = make_float4(dl.x, u.x, dl.y, u.y);
+                }
+#pragma unroll
+                for (int j = 0; j < NBC; ++j) {
+                    const int i = tid + j * SSM_T;
+                    if (i >= Sh::ROWS * NC) break;
+                    const bool isc = i >= TT * NC;
+                    const int r = isc ? i - TT * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
+                    float v[8];
+                    load_row<8>(raw[Sh::NTOK + j][tid], v, 8, true);
+                    float4* dst = reinterpret_cast<float4*>(isc ? &sm.c[w][HAS_Y ? tok : 0][k8] : &sm.b[w][tok][k8]);
+                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                }
+            }
+            if (HAS_Y && k > 0) {
+                const int tok = first_tile + (k - 1) * TT + ptok, w = (k - 1) & 1;
+                if (tok < pl.hi && pvalid > 0) {
+                    TI(*raw)[SSM_T][8] = sm.raw[(k - 1) % STAGES];
+                    float o[8], x[8], z[8];
+                    load_row<8>(raw[0][tid], x, 8, true);
+                    if (zp) load_row<8>(raw[HAS_Y ? 2 : 0][tid], z, 8, true);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 v = *reinterpret_cast<const float4*>(sm.y[w][HAS_Y ? ptok : 0][y_at(ptok, pc + i)]);
+                        o[i] = fmaf(skip[i], x[i], (v.x + v.y) + (v.z + v.w));
+                        if (zp) o[i] *= z[i] * sigmoid_fast(z[i]);
+                    }
+                    store_row<8>(static_cast<TI*>(a.y) + (tok0 + tok) * a.D + pl.c0 + pc, o, pvalid,
+                                 pvalid >= 8 && !(a.how >> SSM_OUT & 3));
+                }
+            }
+            fetch(k + STAGES - 1);   // into the stage of tile k - 1, which was read last
+            if (k < ntiles) __syncthreads();
+        }
+        return;
+    }
+
+    // -------------------------------------------------------------------- the recurrence
+    const int l = tid & 3, ch = tid >> 2, n0 = l * EL, d = pl.c0 + ch;
+    const bool on = ch < pl.nch;
     float A2[EL], h[EL], sd = 0.f;
     load_states<EL>(a.A_log + (size_t)d * a.S, n0, a.S, on, A2);
 #pragma unroll
@@ -85,52 +190,7 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_fwd(SsmArgs a) {
             init_state(n);
             store_states<EL>(ht + n * DS, n0, a.S, on, h);
         }
-        if (pl.lo >= pl.hi) return;
     }
-    int t = pl.lo;
-    Seq s;
-    if (MODE == PIECE) {
-        // the part of the piece that reaches past its end
-        s = seq_at(a.ax, pl.row, pl.hi - 1);
-        if (s.end <= pl.hi) return;
-        t = max(pl.lo, s.first);
-    } else {
-        s = seq_at(a.ax, pl.row, t);
-    }
-    // this thread's part of a tile: one token, 8 channels; NBC chunks of 8 states of b's and c's rows
-    const int ptok = tid >> 2, pc = (tid & 3) * 8, pvalid = pl.nch - pc;
-    const TI* xp = static_cast<const TI*>(a.x) + tok0 * a.ldx + pl.c0 + pc;
-    const TI* dp = static_cast<const TI*>(a.dt) + tok0 * a.lddt + pl.c0 + pc;
-    const TI* zp = a.z ? static_cast<const TI*>(a.z) + tok0 * a.ldz + pl.c0 + pc : nullptr;
-    const TI* bp = static_cast<const TI*>(a.b) + tok0 * a.ldb + (size_t)pl.g * a.S;
-    const TI* cp = static_cast<const TI*>(a.c) + tok0 * a.ldc + (size_t)pl.g * a.S;
-    constexpr int NC = NP / 8;
-    const int first_tile = t;
-    auto fetch = [&](int k) {   // tile k of the piece into its stage
-        const int tb = first_tile + k * TT;
-        if (tb < pl.hi) {
-            TI(*raw)[SSM_T][8] = sm.raw[k % STAGES];
-            const size_t tt = min(tb + ptok, pl.hi - 1);
-            const int n = tb + ptok < pl.hi ? pvalid : 0;
-            copy8_async(raw[0][tid], xp + tt * a.ldx, n, a.how >> SSM_X & 3);
-            copy8_async(raw[1][tid], dp + tt * a.lddt, n, a.how >> SSM_DT & 3);
-            if (HAS_Y && zp) copy8_async(raw[2][tid], zp + tt * a.ldz, n, a.how >> SSM_Z & 3);
-#pragma unroll
-            for (int j = 0; j < NBC; ++j) {
-                const int i = tid + j * SSM_T;
-                if (i >= Sh::ROWS * NC) break;
-                const bool isc = i >= TT * NC;
-                const int r = isc ? i - TT * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
-                const size_t tr = min(tb + tok, pl.hi - 1);
-                const int m = tb + tok < pl.hi ? a.S - k8 : 0;
-                const TI* src = isc ? cp + tr * a.ldc : bp + tr * a.ldb;
-                copy8_async(raw[Sh::NTOK + j][tid], src + (m > 0 ? k8 : 0), m, a.how >> (isc ? SSM_C : SSM_B) & 3);
-            }
-        }
-        copies_commit();
-    };
-#pragma unroll
-    for (int k = 0; k < STAGES - 1; ++k) fetch(k);
     // the state entering this piece
     if (MODE == PIECE ? s.first >= pl.lo : t == s.first) {
         init_state(s.n);
@@ -150,110 +210,115 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_fwd(SsmArgs a) {
             }
         }
     }
-    float bias[8], skip[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = a.dt_bias && i < pvalid ? a.dt_bias[pl.c0 + pc + i] : 0.f;
-        skip[i] = HAS_Y && a.d_skip && i < pvalid ? a.d_skip[pl.c0 + pc + i] : 0.f;
-    }
-    // N tokens of the recurrence from tile row i: every operand read before the first store
-    auto tokens = [&](int i, auto n_) {
-        constexpr int N = decltype(n_)::value;
-        float2 du[N], b[N][P], c[N][P], acc[N];
+    constexpr int N = EL <= 4 ? 4 : 16 / EL;   // tokens whose operands are in registers together
+    struct Operands {
+        float2 du[N], b[N][P], c[HAS_Y ? N : 1][P];
+    };
+    auto load = [&](int w, int i, int n, Operands& o) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            du[j] = reinterpret_cast<const float2*>(&sm.du[i + j][du_at(i + j, ch >> 1)])[ch & 1];
+            if (j >= n) break;
+            o.du[j] = reinterpret_cast<const float2*>(&sm.du[w][i + j][du_at(i + j, ch >> 1)])[ch & 1];
+            float v[EL];
+            lds_states<EL>(&sm.b[w][i + j][n0], v);
 #pragma unroll
-            for (int e = 0; e < P; ++e) {
-                b[j][e] = reinterpret_cast<const float2*>(&sm.b[i + j][n0])[e];
-                if (HAS_Y) c[j][e] = reinterpret_cast<const float2*>(&sm.c[HAS_Y ? i + j : 0][n0])[e];
+            for (int e = 0; e < P; ++e) o.b[j][e] = make_float2(v[2 * e], v[2 * e + 1]);
+            if (HAS_Y) {
+                lds_states<EL>(&sm.c[w][HAS_Y ? i + j : 0][n0], v);
+#pragma unroll
+                for (int e = 0; e < P; ++e) o.c[HAS_Y ? j : 0][e] = make_float2(v[2 * e], v[2 * e + 1]);
             }
         }
+    };
+    auto run_tokens = [&](int w, int i, int n, const Operands& o) {
+        float2 acc[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const float2 dl = make_float2(du[j].x, du[j].x), u = make_float2(du[j].y, du[j].y);
+            if (j >= n) break;
+            const float2 dl = make_float2(o.du[j].x, o.du[j].x), u = make_float2(o.du[j].y, o.du[j].y);
 #pragma unroll
             for (int e = 0; e < P; ++e) {
                 const float2 g = mul2(dl, make_float2(A2[2 * e], A2[2 * e + 1]));
-                const float2 hn = fma2(make_float2(ex2(g.x), ex2(g.y)), make_float2(h[2 * e], h[2 * e + 1]), mul2(u, b[j][e]));
+                const float2 hn = fma2(make_float2(ex2(g.x), ex2(g.y)), make_float2(h[2 * e], h[2 * e + 1]), mul2(u, o.b[j][e]));
                 h[2 * e] = hn.x;
                 h[2 * e + 1] = hn.y;
-                if (HAS_Y) acc[j] = e == 0 ? mul2(hn, c[j][e]) : fma2(hn, c[j][e], acc[j]);
+                if (HAS_Y) acc[j] = e == 0 ? mul2(hn, o.c[HAS_Y ? j : 0][e]) : fma2(hn, o.c[HAS_Y ? j : 0][e], acc[j]);
             }
-            if (MODE == PIECE) sd += du[j].x;
+            if (MODE == PIECE) sd += o.du[j].x;
         }
         if (HAS_Y) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) sm.y[HAS_Y ? i + j : 0][y_at(i + j, ch)][l] = acc[j].x + acc[j].y;
+            for (int j = 0; j < N; ++j)
+                if (j < n) sm.y[w][HAS_Y ? i + j : 0][y_at(i + j, ch)][l] = acc[j].x + acc[j].y;
         }
     };
-    for (int k = 0; first_tile + k * TT < pl.hi; ++k) {
-        const int tb = first_tile + k * TT, te = min(tb + TT, pl.hi);
-        fetch(k + STAGES - 1);
-        copies_wait<STAGES - 1>();
-        TI(*raw)[SSM_T][8] = sm.raw[k % STAGES];
-        float x[8];
-        {
-            float dt[8];
-            raw_row<8>(raw[0][tid], x);
-            raw_row<8>(raw[1][tid], dt);
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                float2 dl = make_float2(dt[i] + bias[i], dt[i + 1] + bias[i + 1]);
-                if (a.softplus) dl = ssm_softplus2(dl);
-                const float2 u = mul2(dl, make_float2(x[i], x[i + 1]));
-                sm.du[ptok][du_at(ptok, (pc + i) >> 1)] = make_float4(dl.x, u.x, dl.y, u.y);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < NBC; ++j) {
-            const int i = tid + j * SSM_T;
-            if (i >= Sh::ROWS * NC) break;
-            const bool isc = i >= TT * NC;
-            const int r = isc ? i - TT * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
-            float v[8];
-            raw_row<8>(raw[Sh::NTOK + j][tid], v);
-            float4* dst = reinterpret_cast<float4*>(isc ? &sm.c[HAS_Y ? tok : 0][k8] : &sm.b[tok][k8]);
-            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
-        __syncthreads();
+    auto checkpoint = [&](int tok) {
+        const size_t slot = (size_t)pl.row * ((a.ax.len + SSM_CKPT - 1) / SSM_CKPT) + tok / SSM_CKPT;
+        store_states<EL>(a.ckpt + slot * DS + (size_t)d * a.S, n0, a.S, on, h);
+    };
+    __syncthreads();   // the first tile's steps
+    for (int k = 0; k < ntiles; ++k) {
+        const int tb = first_tile + k * TT, te = min(tb + TT, pl.hi), w = k & 1;
         t = tb;
-        while (t < te) {
-            if (MODE != PIECE && t == s.end) {
-                if (ht) store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
-                s = seq_at(a.ax, pl.row, t);
-                init_state(s.n);
+        if (MODE != PIECE && t == s.end) {
+            if (ht) store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
+            s = seq_at(a.ax, pl.row, t);
+            init_state(s.n);
+        }
+        if (te - tb == TT && (MODE == PIECE || s.end >= te)) {
+            // a whole tile of one sequence: the next tokens' operands are read while these run
+            Operands o[2];
+            load(w, 0, N, o[0]);
+#pragma unroll
+            for (int i = 0; i < TT; i += N) {
+                if (HAS_CK && i % SSM_CKPT == 0) checkpoint(tb + i);
+                if (i + N < TT) load(w, i + N, N, o[(i / N + 1) & 1]);
+                run_tokens(w, i, N, o[(i / N) & 1]);
             }
-            if (HAS_CK && t % SSM_CKPT == 0) {
-                const size_t slot = (size_t)pl.row * ((a.ax.len + SSM_CKPT - 1) / SSM_CKPT) + t / SSM_CKPT;
-                store_states<EL>(a.ckpt + slot * DS + (size_t)d * a.S, n0, a.S, on, h);
+        } else {
+            while (t < te) {
+                if (MODE != PIECE && t == s.end) {
+                    if (ht) store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
+                    s = seq_at(a.ax, pl.row, t);
+                    init_state(s.n);
+                }
+                if (HAS_CK && t % SSM_CKPT == 0) checkpoint(t);
+                int run = MODE == PIECE ? te : min(te, s.end);
+                if (HAS_CK) run = min(run, (t | (SSM_CKPT - 1)) + 1);
+                Operands o;
+                if (t + N <= run) {
+                    load(w, t - tb, N, o);
+                    run_tokens(w, t - tb, N, o);
+                    t += N;
+                } else {
+                    load(w, t - tb, 1, o);
+                    run_tokens(w, t - tb, 1, o);
+                    ++t;
+                }
             }
-            int run = MODE == PIECE ? te : min(te, s.end);
-            if (HAS_CK) run = min(run, (t | (SSM_CKPT - 1)) + 1);
-#pragma unroll 2
-            for (; t + 4 <= run; t += 4) tokens(t - tb, Int<4>{});
-            for (; t < run; ++t) tokens(t - tb, Int<1>{});
         }
         __syncthreads();
-        if (HAS_Y && tb + ptok < te && pvalid > 0) {
-            float o[8], z[8];
-            if (zp) raw_row<8>(raw[HAS_Y ? 2 : 0][tid], z);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 v = *reinterpret_cast<const float4*>(sm.y[HAS_Y ? ptok : 0][y_at(ptok, pc + i)]);
-                o[i] = fmaf(skip[i], x[i], (v.x + v.y) + (v.z + v.w));
-                if (zp) o[i] *= z[i] * sigmoid_fast(z[i]);
-            }
-            store_row<8>(static_cast<TI*>(a.y) + (tok0 + tb + ptok) * a.D + pl.c0 + pc, o, pvalid,
-                         pvalid >= 8 && !(a.how >> SSM_OUT & 3));
-        }
     }
+    if (pl.lo >= pl.hi && a.ax.cu) return;
     if (MODE == PIECE) {
         store_states<EL>(a.hloc + pl.unit * DS + (size_t)d * a.S, n0, a.S, on, h);
         if (on && l == 0) a.sdt[(size_t)pl.unit * a.D + d] = sd;
     } else if (ht && pl.hi == s.end) {
         store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
+    }
+}
+
+// A lane's EL states of a row of b or c: one access of EL elements where the row is aligned to it.
+template <int EL, typename TI>
+__device__ __forceinline__ void load_lane(const TI* p, int n, bool aligned, float (&x)[EL]) {
+    if (aligned && n >= EL && EL >= 4) {
+        struct alignas(sizeof(TI) * EL > 16 ? 16 : sizeof(TI) * EL) Pack { TI v[EL]; };
+        const Pack k = *reinterpret_cast<const Pack*>(p);
+#pragma unroll
+        for (int e = 0; e < EL; ++e) x[e] = ld(&k.v[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < EL; ++e) x[e] = e < n ? ld(p + e) : 0.f;
     }
 }
 
@@ -291,14 +356,9 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_step(SsmArgs a) {
             const size_t tok = (size_t)(s0 + i) * T + t;
             x[i] = in ? ld(static_cast<const TI*>(a.x) + tok * a.ldx + d) : 0.f;
             dt[i] = in ? ld(static_cast<const TI*>(a.dt) + tok * a.lddt + d) : 0.f;
-            const TI* bp = static_cast<const TI*>(a.b) + tok * a.ldb + (size_t)g * a.S + n0;
-            const TI* cp = static_cast<const TI*>(a.c) + tok * a.ldc + (size_t)g * a.S + n0;
-#pragma unroll
-            for (int e = 0; e < EL; ++e) {
-                const bool one = s0 + i < B && n0 + e < a.S;
-                b[i][e] = one ? ld(bp + e) : 0.f;
-                c[i][e] = one ? ld(cp + e) : 0.f;
-            }
+            const int n = s0 + i < B ? a.S - n0 : 0;
+            load_lane<EL>(static_cast<const TI*>(a.b) + tok * a.ldb + (size_t)g * a.S + n0, n, !(a.how >> SSM_B & 3), b[i]);
+            load_lane<EL>(static_cast<const TI*>(a.c) + tok * a.ldc + (size_t)g * a.S + n0, n, !(a.how >> SSM_C & 3), c[i]);
         }
         const bool store = on && mine < B && (NS == 4 || l == 0);
         if (a.z && store) z = ld(static_cast<const TI*>(a.z) + ((size_t)mine * T + t) * a.ldz + d);
@@ -355,7 +415,7 @@ cudaError_t run_one(const SsmArgs& a, cudaStream_t st) {
     static SmemLimit limit;
     const cudaError_t e = limit.set(reinterpret_cast<const void*>(k_ssm_fwd<TI, EL, MODE>), smem);
     if (e != cudaSuccess) return e;
-    k_ssm_fwd<TI, EL, MODE><<<grid, SSM_T, smem, st>>>(a);
+    k_ssm_fwd<TI, EL, MODE><<<grid, FT, smem, st>>>(a);
     return cudaSuccess;
 }
 template <typename TI, int EL>

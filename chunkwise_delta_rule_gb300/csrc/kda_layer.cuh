@@ -180,14 +180,11 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&x)[V],
 
 // Asynchronous copies of a thread's own data into shared memory: n elements of a row of 8 (zeros past n), in
 // 16-byte, 4-byte or, for odd 16-bit addresses, plain accesses. `how`: 0, 1 or 2.
+// (The slow forms stay out of line: in line at every call they pushed the callers' loops out of the instruction cache.)
 template <typename TI>
-__device__ __forceinline__ void copy8_async(TI* dst, const TI* src, int n, int how) {
+__device__ __noinline__ void copy8_slow(TI* dst, const TI* src, int n, int how) {
     const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-    if (how == 0 && (n >= 8 || n <= 0)) {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(TI) / 2; ++i)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + 16 * i), "l"(reinterpret_cast<const char*>(src) + (n > 0 ? 16 * i : 0)), "r"(n > 0 ? 16 : 0) : "memory");
-    } else if (how <= 1) {
+    if (how <= 1) {
         constexpr int PER = 4 / sizeof(TI);
 #pragma unroll
         for (int i = 0; i < 8 / PER; ++i) {
@@ -197,6 +194,17 @@ __device__ __forceinline__ void copy8_async(TI* dst, const TI* src, int n, int h
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) dst[i] = i < n ? src[i] : TI(0.f);
+    }
+}
+template <typename TI>
+__device__ __forceinline__ void copy8_async(TI* dst, const TI* src, int n, int how) {
+    if (how == 0 && (n >= 8 || n <= 0)) {
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(TI) / 2; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + 16 * i), "l"(reinterpret_cast<const char*>(src) + (n > 0 ? 16 * i : 0)), "r"(n > 0 ? 16 : 0) : "memory");
+    } else {
+        copy8_slow(dst, src, n, how);
     }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -271,7 +279,7 @@ struct SsmArgs {
     float *pA, *pv;            // [units][D][S]; [units][2][D] (skip, dt_bias)
     float* pbc;                // [channel tiles][rows * len][2][S]
 };
-int ssm_channel_tiles(int D, int G);   // channel tiles of all groups (forward and backward)
+int ssm_channel_tiles(int D, int G);   // channel tiles of all groups
 int ssm_units(int rows, int len, int D, int G, int S, bool backward);
 cudaError_t launch_ssm_fwd(const SsmArgs& a, int bf16, int mode, cudaStream_t st);   // 0 outputs, 1 + checkpoints, 2 checkpoints only
 cudaError_t launch_ssm_pieces(const SsmArgs& a, int bf16, cudaStream_t st);          // local end states of every piece

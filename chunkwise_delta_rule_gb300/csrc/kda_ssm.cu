@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(FT, 2) k_ssm_fwd(SsmArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     typename Sh::Smem& sm = *reinterpret_cast<typename Sh::Smem*>(smem_raw);
     if (blockIdx.x == 0 && MODE != PIECE) axis_check(a.ax, a.err);
-    const SsmPlace pl = ssm_place(a);
+    const SsmPlace pl = ssm_place<SSM_CH>(a);
     const size_t tok0 = (size_t)pl.row * a.ax.len;
     const size_t DS = (size_t)a.D * a.S;
     int t = pl.lo;
@@ -184,8 +184,7 @@ __global__ void __launch_bounds__(FT, 2) k_ssm_fwd(SsmArgs a) {
         }
     };
     if (ht && a.ax.cu) {   // sequences without tokens
-        const int units = gridDim.x / (((a.D / a.G + SSM_CH - 1) / SSM_CH) * a.G);
-        for (int n = pl.unit; n < a.ax.N; n += units) {
+        for (int n = pl.unit; n < a.ax.N; n += pl.units) {
             if (axis_cu(a.ax, n + 1) > axis_cu(a.ax, n)) continue;
             init_state(n);
             store_states<EL>(ht + n * DS, n0, a.S, on, h);
@@ -453,8 +452,6 @@ cudaError_t launch(const char* name, const SsmArgs& a, int bf16, int mode, cudaS
 }
 
 }  // namespace
-
-int ssm_channel_tiles(int D, int G) { return (D / G + SSM_CH - 1) / SSM_CH * G; }
 
 int ssm_units(int rows, int len, int D, int G, int S, bool backward) {
     // pieces only while the channels and rows alone leave SMs idle; a piece is at least 128 tokens

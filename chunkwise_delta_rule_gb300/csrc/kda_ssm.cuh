@@ -12,41 +12,40 @@ struct Int {
 };
 
 constexpr unsigned SSM_FULL = 0xffffffffu;
-constexpr int SSM_T = 128;    // threads per CTA: 32 channels x 4 lanes
+constexpr int SSM_T = 128;    // threads of the recurrence per CTA: 32 channels x 4 lanes
 constexpr int SSM_CH = 32;    // channels per CTA
 
-// log(1 + e^v) without overflow: max(v, 0) + log(1 + e) with e = e^-|v| in (0, 1]. The logarithm is the series of
-// the inverse hyperbolic tangent, log(1 + e) = 2 (s + s^3/3 + s^5/5 + ...), s = e / (2 + e) <= 1/3: relative to its
-// value (a step of 1e-3 is as exact as one of 1), and past s^13 it adds less than 2e-8.
+// log(1 + e^v) without overflow: max(v, 0) + log(1 + e) with e = e^-|v| in (0, 1]. With s = e / (2 + e) <= 1/3 the
+// logarithm is 2 atanh(s), whose quotient by s is a smooth function of q = s^2 in [0, 1/9]: the polynomial interpolates
+// it at the five Chebyshev points of that interval (8e-9 relative with fp32 coefficients), so that a step of 1e-3
+// is as exact relative to itself as one of 1.
 __device__ __forceinline__ float2 ssm_softplus2(float2 v) {
     const float2 e = make_float2(ex2(-LOG2E * fabsf(v.x)), ex2(-LOG2E * fabsf(v.y)));
-    const float2 s = mul2(e, make_float2(rcp(2.f + e.x), rcp(2.f + e.y)));
-    const float2 q = mul2(s, s);
-    float2 p = make_float2(1.f / 13.f, 1.f / 13.f);
-    p = fma2(p, q, make_float2(1.f / 11.f, 1.f / 11.f));
-    p = fma2(p, q, make_float2(1.f / 9.f, 1.f / 9.f));
-    p = fma2(p, q, make_float2(1.f / 7.f, 1.f / 7.f));
-    p = fma2(p, q, make_float2(1.f / 5.f, 1.f / 5.f));
-    p = fma2(p, q, make_float2(1.f / 3.f, 1.f / 3.f));
+    const float2 s = mul2(e, make_float2(rcp(2.f + e.x), rcp(2.f + e.y))), q = mul2(s, s);
+    float2 p = make_float2(0.140788892f, 0.140788892f);
+    p = fma2(p, q, make_float2(0.139825789f, 0.139825789f));
+    p = fma2(p, q, make_float2(0.200122976f, 0.200122976f));
+    p = fma2(p, q, make_float2(0.333331608f, 0.333331608f));
     p = fma2(p, q, make_float2(1.f, 1.f));
-    p = mul2(p, s);
-    return fma2(p, make_float2(2.f, 2.f), make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+    return fma2(mul2(p, s), make_float2(2.f, 2.f), make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
 __device__ __forceinline__ float ssm_softplus(float v) { return ssm_softplus2(make_float2(v, v)).x; }
 
-// A CTA's place: time piece `unit` of row `row` (tokens [lo, hi)), 32 channels from c0 of group g.
+// A CTA's place: time piece `unit` of `units` (tokens [lo, hi) of row `row`), nch <= CH channels from c0 of group g.
 struct SsmPlace {
-    int unit, row, u, lo, hi, tile, g, c0, nch;
+    int unit, units, row, u, lo, hi, tile, g, c0, nch;
 };
+template <int CH>
 __device__ __forceinline__ SsmPlace ssm_place(const SsmArgs& a) {
     SsmPlace p;
-    const int M = a.D / a.G, tpg = (M + SSM_CH - 1) / SSM_CH, tiles = tpg * a.G;
+    const int M = a.D / a.G, tpg = (M + CH - 1) / CH, tiles = tpg * a.G;
     p.unit = blockIdx.x / tiles;
+    p.units = gridDim.x / tiles;
     p.tile = blockIdx.x - p.unit * tiles;
     p.g = p.tile / tpg;
     const int tg = p.tile - p.g * tpg;
-    p.c0 = p.g * M + tg * SSM_CH;
-    p.nch = min(SSM_CH, M - tg * SSM_CH);
+    p.c0 = p.g * M + tg * CH;
+    p.nch = min(CH, M - tg * CH);
     p.row = p.unit / a.units_row;
     p.u = p.unit - p.row * a.units_row;
     p.lo = p.u * a.unit_len;

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_bwd(SsmArgs a) {
     constexpr int NP = Sh::NP, L = Sh::L, NSUB = Sh::NSUB, VB = Sh::VB, KEEP = Sh::KEEP;
     extern __shared__ __align__(16) unsigned char raw[];
     typename Sh::Smem& sm = *reinterpret_cast<typename Sh::Smem*>(raw);
-    const SsmPlace pl = ssm_place(a);
+    const SsmPlace pl = ssm_place<SSM_CH>(a);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = tid & 3, ch = tid >> 2, n0 = l * EL;
     const int d = pl.c0 + ch;
     const bool on = ch < pl.nch;
@@ -62,8 +62,7 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_bwd(SsmArgs a) {
         }
     };
     if (a.dh0 && (a.ax.cu || a.ax.len == 0)) {   // sequences without tokens: their adjoint passes through
-        const int units = gridDim.x / (((a.D / a.G + SSM_CH - 1) / SSM_CH) * a.G);
-        for (int n = pl.unit; n < a.ax.N; n += units) {
+        for (int n = pl.unit; n < a.ax.N; n += pl.units) {
             if (a.ax.cu && axis_cu(a.ax, n + 1) > axis_cu(a.ax, n)) continue;
             float v[EL];
             state_of(a.dht, n, v);
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_bwd_pieces(SsmArgs a) {
     constexpr int NP = 4 * EL;
     __shared__ float2 s_in[TB][SSM_CH];
     __shared__ __align__(16) float s_c[TB][NP];
-    const SsmPlace pl = ssm_place(a);
+    const SsmPlace pl = ssm_place<SSM_CH>(a);
     if (pl.lo >= pl.hi) return;
     const Seq s = seq_at(a.ax, pl.row, pl.lo);
     if (s.first >= pl.lo) return;
@@ -439,6 +438,8 @@ cudaError_t run_states(const SsmArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+int ssm_channel_tiles(int D, int G) { return (D / G + SSM_CH - 1) / SSM_CH * G; }
 
 cudaError_t launch_ssm_bwd_pieces(const SsmArgs& a, int bf16, cudaStream_t st) {
     return traced_launch("k_ssm_bwd_pieces", st, [&] {

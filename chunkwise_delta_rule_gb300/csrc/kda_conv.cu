@@ -5,8 +5,11 @@
 // inputs of what came before (oldest first; zero without one). The backward
 // recomputes s, forms d_t = dy_t act'(s_t), and gathers
 //     dx_t = sum_j w[j] d_{t+W-1-j},  dw[j] = sum_t d_t x_{t-W+1+j},  dbias = sum_t d_t
-// A thread owns 16 bytes of neighbouring channels and walks a tile of tokens with
-// the window in registers, so each input is read once plus W - 1 rows per tile.
+// A thread owns four neighbouring channels and walks a tile
+// of tokens with the window in registers, so each input is read once plus W - 1 rows
+// per tile; the next tokens' rows are in flight while the present ones are formed. The
+// filters pass through shared memory: read directly, each lane's 32 values lie 128
+// bytes from its neighbour's and cost more than the tile's inputs.
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -14,15 +17,43 @@ namespace {
 
 constexpr int CT = 128;   // threads of the forward
 constexpr int CB = 256;   // threads of the backward
-constexpr int CU = 4;     // tokens whose loads are in flight together
+constexpr int VC = 4;     // channels per thread
+constexpr int CU = 8;     // tokens whose loads are in flight together, forward
 
+// The block's filters to shared memory, tap by tap: sw[j * ncol + c] = weight[first + c][j], row W the bias.
+template <int W, int NT>
+__device__ __forceinline__ void stage_weights(const ConvArgs& a, float* sw, int first, int ncol) {
+    for (int i = threadIdx.x; i < ncol * W; i += NT) {
+        const int c = i / W, j = i - c * W;
+        sw[j * ncol + c] = first + c < a.D ? a.weight[(size_t)first * W + i] : 0.f;
+    }
+    for (int c = threadIdx.x; c < ncol; c += NT) sw[W * ncol + c] = a.bias && first + c < a.D ? a.bias[first + c] : 0.f;
+    __syncthreads();
+}
+// A thread's filters, taps of neighbouring channels paired.
 template <int W, int V>
-__device__ __forceinline__ void load_weights(const ConvArgs& a, int c0, float (&w)[V][W], float (&bias)[V]) {
+__device__ __forceinline__ void read_weights(const float* sw, int ncol, int c, float (&w)[W][V], float (&bias)[V]) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int j = 0; j <= W; ++j) {
+        float v[V];
+        unpack<V>(load_raw<float, V>(sw + j * ncol + c), v);
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[v][j] = a.weight[(size_t)(c0 + v) * W + j];
-        bias[v] = a.bias ? a.bias[c0 + v] : 0.f;
+        for (int i = 0; i < V; ++i) (j < W ? w[j < W ? j : 0][i] : bias[i]) = v[i];
+    }
+}
+
+// acc + w x over V channels, in pairs.
+template <int V>
+__device__ __forceinline__ void fma_v(const float (&w)[V], const float (&x)[V], float (&acc)[V]) {
+    if (V == 1) {
+        acc[0] = fmaf(w[0], x[0], acc[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i + 1 < V; i += 2) {
+            const float2 r = fma2(make_float2(w[i], w[i + 1]), make_float2(x[i], x[i + 1]), make_float2(acc[i], acc[i + 1]));
+            acc[i] = r.x;
+            acc[i + 1] = r.y;
+        }
     }
 }
 
@@ -34,10 +65,10 @@ __device__ __forceinline__ void load_window(const ConvArgs& a, const Seq& s, con
     for (int j = 0; j < W - 1; ++j) {
         const int p = t - (W - 1) + j;
         if (p >= s.first) {
-            load_row<V>(x + (size_t)p * a.ldx, win[j], V, V > 1);
+            unpack<V>(load_raw<TI, V>(x + (size_t)p * a.ldx), win[j]);
         } else if (a.h0) {
-            load_row<V>(static_cast<const TI*>(a.h0) + ((size_t)s.n * (W - 1) + (p - s.first) + (W - 1)) * a.D + c0,
-                        win[j], V, V > 1);
+            unpack<V>(load_raw<TI, V>(static_cast<const TI*>(a.h0) + ((size_t)s.n * (W - 1) + (p - s.first) + (W - 1)) * a.D + c0),
+                      win[j]);
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v) win[j][v] = 0.f;
@@ -57,30 +88,57 @@ __device__ __forceinline__ void copy_empty(const ConvArgs& a, int tile_id, int r
             float v[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = 0.f;
-            if (src) load_row<V>(static_cast<const TI*>(src) + o, v, V, V > 1);
-            store_row<V>(static_cast<TI*>(dst) + o, v, V, V > 1);
+            if (src) unpack<V>(load_raw<TI, V>(static_cast<const TI*>(src) + o), v);
+            store_values<V>(static_cast<TI*>(dst) + o, v);
         }
     }
 }
 
+// Output of one token; the window moves on.
+template <int W, int V, bool SILU>
+__device__ __forceinline__ void conv_token(const float (&w)[W][V], const float (&bias)[V], float (&win)[W - 1][V],
+                                           const float (&x)[V], float (&o)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = bias[v];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) fma_v<V>(w[j], win[j], o);
+    fma_v<V>(w[W - 1], x, o);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (SILU) o[v] *= sigmoid_fast(o[v]);
+#pragma unroll
+        for (int j = 0; j < W - 2; ++j) win[j][v] = win[j + 1][v];
+        win[W - 2][v] = x[v];
+    }
+}
+
+// Block of gx channel groups by gy tiles.
 template <typename TI, int W, int V, bool SILU>
 __global__ void __launch_bounds__(CT) k_conv_fwd(ConvArgs a) {
+    extern __shared__ float sw[];
     if (blockIdx.x == 0) axis_check(a.ax, a.err);
-    const size_t item = (size_t)blockIdx.x * CT + threadIdx.x;
-    const int tile_id = (int)(item / a.groups);
-    if (tile_id >= a.ntiles) return;
-    const int c0 = (int)(item - (size_t)tile_id * a.groups) * V;
+    const int lx = threadIdx.x & (a.gx - 1), ly = threadIdx.x / a.gx, gy = CT / a.gx;
+    const int nbx = (a.groups + a.gx - 1) / a.gx;
+    const int by = blockIdx.x / nbx, bx = blockIdx.x - by * nbx;
+    stage_weights<W, CT>(a, sw, bx * a.gx * V, a.gx * V);
+    const int cg = bx * a.gx + lx, tile_id = by * gy + ly, c0 = cg * V;
+    if (cg >= a.groups || tile_id >= a.ntiles) return;
     const int row = tile_id / a.tiles_row;
     int t = (tile_id - row * a.tiles_row) * a.tile;
     const int t1 = min(t + a.tile, a.ax.len);
     const size_t tok0 = (size_t)row * a.ax.len;
     const TI* x = static_cast<const TI*>(a.x) + tok0 * a.ldx + c0;
     TI* y = static_cast<TI*>(a.y) + tok0 * a.D + c0;
-    float w[V][W], bias[V], win[W - 1][V];
-    load_weights<W, V>(a, c0, w, bias);
+    float w[W][V], bias[V], win[W - 1][V];
+    read_weights<W, V>(sw, a.gx * V, lx * V, w, bias);
     copy_empty<TI, W, V>(a, tile_id, row, c0, a.h0, a.final_state);
     while (t < t1) {
         const Seq s = seq_at(a.ax, row, t);
+        const int run = min(t1, s.end);
+        Raw<TI, V> next[CU];
+#pragma unroll
+        for (int u = 0; u < CU; ++u)
+            if (t + u < run) next[u] = load_raw<TI, V>(x + (size_t)(t + u) * a.ldx);
         load_window<TI, W, V>(a, s, x, t, c0, win);
         if (t == s.first && a.final_state) {
             // the final state, by the thread that has the initial one in its window: the two may be one buffer
@@ -90,7 +148,7 @@ __global__ void __launch_bounds__(CT) k_conv_fwd(ConvArgs a) {
                 const int p = len - (W - 1) + r;
                 float f[V];
                 if (p >= 0) {
-                    load_row<V>(x + (size_t)(s.first + p) * a.ldx, f, V, V > 1);
+                    unpack<V>(load_raw<TI, V>(x + (size_t)(s.first + p) * a.ldx), f);
                 } else {
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k)
@@ -99,34 +157,98 @@ __global__ void __launch_bounds__(CT) k_conv_fwd(ConvArgs a) {
                             for (int v = 0; v < V; ++v) f[v] = win[k][v];
                         }
                 }
-                store_row<V>(static_cast<TI*>(a.final_state) + ((size_t)s.n * (W - 1) + r) * a.D + c0, f, V, V > 1);
+                store_values<V>(static_cast<TI*>(a.final_state) + ((size_t)s.n * (W - 1) + r) * a.D + c0, f);
             }
         }
-        const int run = min(t1, s.end);
-        for (; t < run; t += CU) {
-            float xt[CU][V];
+        const TI* xp = x + (size_t)t * a.ldx;
+        TI* yp = y + (size_t)t * a.D;
+        for (; t + CU <= run; t += CU) {
+            Raw<TI, V> cur[CU];
+#pragma unroll
+            for (int u = 0; u < CU; ++u) cur[u] = next[u];
+            xp += CU * a.ldx;
 #pragma unroll
             for (int u = 0; u < CU; ++u)
-                if (t + u < run) load_row<V>(x + (size_t)(t + u) * a.ldx, xt[u], V, V > 1);
+                if (t + CU + u < run) next[u] = load_raw<TI, V>(xp + u * a.ldx);
 #pragma unroll
             for (int u = 0; u < CU; ++u) {
-                if (t + u >= run) break;
-                float o[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float acc = bias[v];
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) acc = fmaf(w[v][j], win[j][v], acc);
-                    acc = fmaf(w[v][W - 1], xt[u][v], acc);
-                    o[v] = SILU ? acc * sigmoid_fast(acc) : acc;
-#pragma unroll
-                    for (int j = 0; j < W - 2; ++j) win[j][v] = win[j + 1][v];
-                    win[W - 2][v] = xt[u][v];
-                }
-                store_row<V>(y + (size_t)(t + u) * a.D, o, V, V > 1);
+                float xt[V], o[V];
+                unpack<V>(cur[u], xt);
+                conv_token<W, V, SILU>(w, bias, win, xt, o);
+                store_values<V>(yp + (size_t)u * a.D, o);
             }
+            yp += (size_t)CU * a.D;
+        }
+#pragma unroll
+        for (int u = 0; u < CU - 1; ++u) {
+            if (t + u >= run) break;
+            float xt[V], o[V];
+            unpack<V>(next[u], xt);
+            conv_token<W, V, SILU>(w, bias, win, xt, o);
+            store_values<V>(yp + (size_t)u * a.D, o);
         }
         t = run;
+    }
+}
+
+// One token per sequence (decoding): a thread takes its channels of RB sequences, every row in flight together and the
+// filters read once for all of them.
+template <typename TI, int W, int V, bool SILU, int RB>
+__global__ void __launch_bounds__(CT) k_conv_step(ConvArgs a) {
+    const size_t item = (size_t)blockIdx.x * CT + threadIdx.x;
+    const int n0 = (int)(item / a.groups) * RB;
+    if (n0 >= a.ax.N) return;
+    const int c0 = (int)(item % a.groups) * V;
+    Raw<TI, V> x[RB], win[RB][W - 1];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+        if (n0 + r >= a.ax.N) break;
+        x[r] = load_raw<TI, V>(static_cast<const TI*>(a.x) + (size_t)(n0 + r) * a.ldx + c0);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            if (a.h0) {
+                win[r][j] = load_raw<TI, V>(static_cast<const TI*>(a.h0) + ((size_t)(n0 + r) * (W - 1) + j) * a.D + c0);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) win[r][j].v[v] = TI(0.f);
+            }
+        }
+    }
+    float w[W][V], bias[V];
+    {
+        Raw<float, V> q[W];   // V channels of W taps: W accesses of V values
+        const bool wide = (reinterpret_cast<uintptr_t>(a.weight) & 15) == 0;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            if (wide) {
+                q[k] = load_raw<float, V>(a.weight + (size_t)c0 * W + k * V);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) q[k].v[v] = a.weight[(size_t)c0 * W + k * V + v];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][v] = q[(v * W + j) / V].v[(v * W + j) % V];
+            bias[v] = a.bias ? a.bias[c0 + v] : 0.f;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+        if (n0 + r >= a.ax.N) break;
+        float xt[V], h[W - 1][V], o[V];
+        unpack<V>(x[r], xt);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) unpack<V>(win[r][j], h[j]);
+        conv_token<W, V, SILU>(w, bias, h, xt, o);
+        store_values<V>(static_cast<TI*>(a.y) + (size_t)(n0 + r) * a.D + c0, o);
+        if (a.final_state) {
+            TI* f = static_cast<TI*>(a.final_state) + (size_t)(n0 + r) * (W - 1) * a.D + c0;
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+                *reinterpret_cast<Raw<TI, V>*>(f + (size_t)j * a.D) = j < W - 2 ? win[r][j < W - 2 ? j + 1 : 0] : x[r];
+        }
     }
 }
 
@@ -151,30 +273,32 @@ __global__ void __launch_bounds__(CT) k_conv_state(ConvArgs a) {
         const int p = end - (W - 1) + r;
 #pragma unroll
         for (int v = 0; v < V; ++v) f[r][v] = 0.f;
-        if (p >= first) load_row<V>(x + (size_t)p * a.ldx, f[r], V, V > 1);
-        else if (a.h0) load_row<V>(static_cast<const TI*>(a.h0) + o + (size_t)(end - first + r) * a.D, f[r], V, V > 1);
+        if (p >= first) unpack<V>(load_raw<TI, V>(x + (size_t)p * a.ldx), f[r]);
+        else if (a.h0) unpack<V>(load_raw<TI, V>(static_cast<const TI*>(a.h0) + o + (size_t)(end - first + r) * a.D), f[r]);
     }
 #pragma unroll
-    for (int r = 0; r < W - 1; ++r) store_row<V>(static_cast<TI*>(a.final_state) + o + (size_t)r * a.D, f[r], V, V > 1);
+    for (int r = 0; r < W - 1; ++r) store_values<V>(static_cast<TI*>(a.final_state) + o + (size_t)r * a.D, f[r]);
 }
 
 // Block of gx channel groups by gy tiles; the tiles' parameter sums are added in tile order.
 template <typename TI, int W, int V, bool SILU>
-__global__ void __launch_bounds__(CB) k_conv_bwd(ConvArgs a, int gx) {
-    extern __shared__ float red[];   // [gy][gx * V]
-    const int gy = CB / gx;
-    const int lx = threadIdx.x % gx, ly = threadIdx.x / gx;
+__global__ void __launch_bounds__(CB, 2) k_conv_bwd(ConvArgs a) {
+    constexpr int BU = W == 4 ? 3 : 2;   // tokens whose loads are in flight together
+    extern __shared__ float smem[];      // the filters, then [gy][gx * V] sums
+    const int gx = a.gx, gy = CB / gx;
+    const int lx = threadIdx.x & (gx - 1), ly = threadIdx.x / gx;
     const int nbx = (a.groups + gx - 1) / gx;
     const int part = blockIdx.x / nbx, bx = blockIdx.x - part * nbx;
     const int cg = bx * gx + lx, c0 = cg * V;
     const int tile_id = part * gy + ly;
     const bool on = cg < a.groups && tile_id < a.ntiles;
-    float dw[V][W], db[V];
+    stage_weights<W, CB>(a, smem, bx * gx * V, gx * V);
+    float dw[W][V], db[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         db[v] = 0.f;
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[v][j] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j][v] = 0.f;
     }
     if (on) {
         const int row = tile_id / a.tiles_row;
@@ -185,67 +309,115 @@ __global__ void __launch_bounds__(CB) k_conv_bwd(ConvArgs a, int gx) {
         const TI* dy = static_cast<const TI*>(a.dy) + tok0 * a.D + c0;
         TI* dx = static_cast<TI*>(a.dx) + tok0 * a.D + c0;
         const TI* df = static_cast<const TI*>(a.dfinal);
-        float w[V][W], bias[V];
-        load_weights<W, V>(a, c0, w, bias);
+        float w[W][V], bias[V];
+        read_weights<W, V>(smem, gx * V, lx * V, w, bias);
         copy_empty<TI, W, V>(a, tile_id, row, c0, a.dfinal, a.dinit);
         while (t < t1) {
             const Seq s = seq_at(a.ax, row, t);
-            const int run = min(t1, s.end), len = s.end - s.first;
+            const int run = min(t1, s.end), len = s.end - s.first, lim = min(run + W - 1, s.end);
             const bool start = t == s.first;
+            Raw<TI, V> nx[BU], nd[BU];
+#pragma unroll
+            for (int u = 0; u < BU; ++u)
+                if (t + u < lim) {
+                    nx[u] = load_raw<TI, V>(x + (size_t)(t + u) * a.ldx);
+                    nd[u] = load_raw<TI, V>(dy + (size_t)(t + u) * a.D);
+                }
             float win[W - 1][V], dwin[W - 1][V];   // x before the token (oldest first); d before it (newest first)
             load_window<TI, W, V>(a, s, x, t, c0, win);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
                 for (int v = 0; v < V; ++v) dwin[j][v] = 0.f;
-            // W - 1 tokens past the run: their d reaches back into it (zero past the sequence)
-            for (int tb = t; tb < run + W - 1; tb += CU) {
-                float xt[CU][V], dt[CU][V];
+            // the gradient of a token's s, and its part of the filters' sums
+            auto gradient = [&](const float(&xt)[V], float(&d)[V]) {
+                if (!SILU) return;
+                float pre[V];
 #pragma unroll
-                for (int u = 0; u < CU; ++u) {
-                    const int tt = tb + u;
-                    if (tt < min(run + W - 1, s.end)) {
-                        load_row<V>(x + (size_t)tt * a.ldx, xt[u], V, V > 1);
-                        load_row<V>(dy + (size_t)tt * a.D, dt[u], V, V > 1);
+                for (int v = 0; v < V; ++v) pre[v] = bias[v];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) fma_v<V>(w[j], win[j], pre);
+                fma_v<V>(w[W - 1], xt, pre);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float sg = sigmoid_fast(pre[v]);
+                    d[v] *= sg * fmaf(pre[v], 1.f - sg, 1.f);
+                }
+            };
+            auto add_sums = [&](const float(&xt)[V], const float(&d)[V]) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) db[v] += d[v];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) fma_v<V>(d, win[j], dw[j]);
+                fma_v<V>(d, xt, dw[W - 1]);
+            };
+            auto next_x = [&](const float(&xt)[V]) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+#pragma unroll
+                    for (int j = 0; j < W - 2; ++j) win[j][v] = win[j + 1][v];
+                    win[W - 2][v] = xt[v];
+                }
+            };
+            // dx of the token W - 1 back, complete with this one's d
+            auto gather = [&](const float(&d)[V], float(&e)[V]) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) e[v] = w[0][v] * d[v];
+#pragma unroll
+                for (int j = 1; j < W; ++j) fma_v<V>(w[j], dwin[j - 1], e);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+#pragma unroll
+                    for (int j = W - 2; j > 0; --j) dwin[j][v] = dwin[j - 1][v];
+                    dwin[0][v] = d[v];
+                }
+            };
+            // W - 1 tokens past the run: their d reaches back into it (zero past the sequence)
+            for (int tb = t; tb < run + W - 1; tb += BU) {
+                Raw<TI, V> cx[BU], cd[BU];
+                const TI* xn = x + (size_t)(tb + BU) * a.ldx;
+                const TI* dn = dy + (size_t)(tb + BU) * a.D;
+#pragma unroll
+                for (int u = 0; u < BU; ++u) {
+                    cx[u] = nx[u];
+                    cd[u] = nd[u];
+                    if (tb + BU + u < lim) {
+                        nx[u] = load_raw<TI, V>(xn + u * a.ldx);
+                        nd[u] = load_raw<TI, V>(dn + (size_t)u * a.D);
                     }
                 }
+                if (tb >= t + W - 1 && tb + BU <= run && tb + BU <= s.end - (df ? 1 : 0)) {
+                    // inside the run: no case to tell apart
+                    TI* dst = dx + (size_t)(tb - (W - 1)) * a.D;
 #pragma unroll
-                for (int u = 0; u < CU; ++u) {
+                    for (int u = 0; u < BU; ++u) {
+                        float xt[V], d[V], e[V];
+                        unpack<V>(cx[u], xt);
+                        unpack<V>(cd[u], d);
+                        gradient(xt, d);
+                        add_sums(xt, d);
+                        next_x(xt);
+                        gather(d, e);
+                        store_values<V>(dst + (size_t)u * a.D, e);
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int u = 0; u < BU; ++u) {
                     const int tt = tb + u;
                     if (tt >= run + W - 1) break;
-                    float e[V];
-                    const bool own = tt < run, real = tt < s.end;
+                    float d[V], e[V];
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        float d = 0.f;
-                        if (real) {
-                            d = dt[u][v];
-                            if (SILU) {
-                                float pre = bias[v];
-#pragma unroll
-                                for (int j = 0; j < W - 1; ++j) pre = fmaf(w[v][j], win[j][v], pre);
-                                pre = fmaf(w[v][W - 1], xt[u][v], pre);
-                                const float sg = sigmoid_fast(pre);
-                                d *= sg * fmaf(pre, 1.f - sg, 1.f);
-                            }
-                            if (own) {
-                                db[v] += d;
-#pragma unroll
-                                for (int j = 0; j < W - 1; ++j) dw[v][j] = fmaf(d, win[j][v], dw[v][j]);
-                                dw[v][W - 1] = fmaf(d, xt[u][v], dw[v][W - 1]);
-                            }
-#pragma unroll
-                            for (int j = 0; j < W - 2; ++j) win[j][v] = win[j + 1][v];
-                            win[W - 2][v] = xt[u][v];
-                        }
-                        float acc = w[v][0] * d;
-#pragma unroll
-                        for (int j = 1; j < W; ++j) acc = fmaf(w[v][j], dwin[j - 1][v], acc);
-                        e[v] = acc;
-#pragma unroll
-                        for (int j = W - 2; j > 0; --j) dwin[j][v] = dwin[j - 1][v];
-                        dwin[0][v] = d;
+                    for (int v = 0; v < V; ++v) d[v] = 0.f;
+                    if (tt < lim) {
+                        float xt[V];
+                        unpack<V>(cx[u], xt);
+                        unpack<V>(cd[u], d);
+                        gradient(xt, d);
+                        if (tt < run) add_sums(xt, d);
+                        next_x(xt);
                     }
+                    gather(d, e);
                     const int q = tt - (W - 1);   // the token whose gradient is complete
                     int r = -1;                   // the final state's row that reads it
                     TI* dst = nullptr;
@@ -260,11 +432,11 @@ __global__ void __launch_bounds__(CB) k_conv_bwd(ConvArgs a, int gx) {
                     if (dst) {
                         if (df && r >= 0) {
                             float f[V];
-                            load_row<V>(df + ((size_t)s.n * (W - 1) + r) * a.D + c0, f, V, V > 1);
+                            unpack<V>(load_raw<TI, V>(df + ((size_t)s.n * (W - 1) + r) * a.D + c0), f);
 #pragma unroll
                             for (int v = 0; v < V; ++v) e[v] += f[v];
                         }
-                        store_row<V>(dst, e, V, V > 1);
+                        store_values<V>(dst, e);
                     }
                 }
             }
@@ -273,11 +445,12 @@ __global__ void __launch_bounds__(CB) k_conv_bwd(ConvArgs a, int gx) {
     }
     // the block's sums, tap by tap
     const int ncol = gx * V;
+    float* red = smem + (W + 1) * ncol;
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
         __syncthreads();
 #pragma unroll
-        for (int v = 0; v < V; ++v) red[ly * ncol + lx * V + v] = j < W ? dw[v][j < W ? j : 0] : db[v];
+        for (int v = 0; v < V; ++v) red[ly * ncol + lx * V + v] = j < W ? dw[j < W ? j : 0][v] : db[v];
         __syncthreads();
         for (int c = threadIdx.x; c < ncol; c += CB) {
             if (bx * ncol + c >= a.D) continue;
@@ -288,29 +461,36 @@ __global__ void __launch_bounds__(CB) k_conv_bwd(ConvArgs a, int gx) {
     }
 }
 
-// dweight and dbias: the blocks' sums in block order.
-__global__ void k_conv_sum(ConvArgs a) {
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+// dweight and dbias from the blocks' sums.
+__global__ void __launch_bounds__(256) k_conv_sum(ConvArgs a) {
+    float sum;
+    const int i = sum_parts(a.part, a.parts, (size_t)(a.W + 1) * a.D, sum);
+    if (i < 0) return;
     const int j = i / a.D, d = i - j * a.D;
-    if (j > a.W) return;
-    float sum = 0.f;
-    for (int p = 0; p < a.parts; ++p) sum += a.part[((size_t)p * (a.W + 1) + j) * a.D + d];
     if (j < a.W) a.dweight[(size_t)d * a.W + j] = sum;
     else if (a.dbias) a.dbias[d] = sum;
 }
 
-int bwd_gx(int groups) {
-    int gx = 1;
-    while (gx < 32 && gx < groups) gx *= 2;
-    return gx;
-}
-
 template <typename TI, int W, int V>
 void run_fwd(const ConvArgs& a, cudaStream_t st) {
-    const size_t items = (size_t)a.ntiles * a.groups;
+    const int gy = CT / a.gx;
+    const unsigned grid = (unsigned)((a.ntiles + gy - 1) / gy) * ((a.groups + a.gx - 1) / a.gx);
+    const size_t smem = sizeof(float) * (W + 1) * a.gx * V;
+    if (a.silu) k_conv_fwd<TI, W, V, true><<<grid, CT, smem, st>>>(a);
+    else k_conv_fwd<TI, W, V, false><<<grid, CT, smem, st>>>(a);
+}
+template <typename TI, int W, int V, int RB>
+void run_step_rows(const ConvArgs& a, cudaStream_t st) {
+    const size_t items = (size_t)((a.ax.N + RB - 1) / RB) * a.groups;
     const unsigned grid = (unsigned)((items + CT - 1) / CT);
-    if (a.silu) k_conv_fwd<TI, W, V, true><<<grid, CT, 0, st>>>(a);
-    else k_conv_fwd<TI, W, V, false><<<grid, CT, 0, st>>>(a);
+    if (a.silu) k_conv_step<TI, W, V, true, RB><<<grid, CT, 0, st>>>(a);
+    else k_conv_step<TI, W, V, false, RB><<<grid, CT, 0, st>>>(a);
+}
+template <typename TI, int W, int V>
+void run_step(const ConvArgs& a, cudaStream_t st) {
+    // four sequences per thread once that leaves every SM a CTA
+    if ((size_t)(a.ax.N / 4) * a.groups >= (size_t)sm_count() * CT) run_step_rows<TI, W, V, 4>(a, st);
+    else run_step_rows<TI, W, V, 1>(a, st);
 }
 template <typename TI, int W, int V>
 void run_state(const ConvArgs& a, cudaStream_t st) {
@@ -319,17 +499,18 @@ void run_state(const ConvArgs& a, cudaStream_t st) {
 }
 template <typename TI, int W, int V>
 void run_bwd(const ConvArgs& a, cudaStream_t st) {
-    const int gx = bwd_gx(a.groups);
-    const unsigned grid = (unsigned)a.parts * ((a.groups + gx - 1) / gx);
-    const size_t smem = sizeof(float) * CB * V;
-    if (a.silu) k_conv_bwd<TI, W, V, true><<<grid, CB, smem, st>>>(a, gx);
-    else k_conv_bwd<TI, W, V, false><<<grid, CB, smem, st>>>(a, gx);
+    const unsigned grid = (unsigned)a.parts * ((a.groups + a.gx - 1) / a.gx);
+    const size_t smem = sizeof(float) * ((W + 1) * a.gx * V + CB * V);
+    if (a.silu) k_conv_bwd<TI, W, V, true><<<grid, CB, smem, st>>>(a);
+    else k_conv_bwd<TI, W, V, false><<<grid, CB, smem, st>>>(a);
 }
-enum { FWD, STATE, BWD };
+
+enum { FWD, STEP, STATE, BWD };
 template <int OP, typename TI, int W, int V>
 void run_op(const ConvArgs& a, cudaStream_t st) {
-    if (OP == FWD) run_fwd<TI, W, V>(a, st);
-    else if (OP == STATE) run_state<TI, W, V>(a, st);
+    if constexpr (OP == FWD) run_fwd<TI, W, V>(a, st);
+    else if constexpr (OP == STEP) run_step<TI, W, V>(a, st);
+    else if constexpr (OP == STATE) run_state<TI, W, V>(a, st);
     else run_bwd<TI, W, V>(a, st);
 }
 template <int OP, typename TI, int V>
@@ -342,28 +523,42 @@ void run_w(const ConvArgs& a, cudaStream_t st) {
 }
 template <int OP>
 void run_conv(const ConvArgs& a, int bf16, bool vec, cudaStream_t st) {
-    if (bf16) vec ? run_w<OP, __nv_bfloat16, 8>(a, st) : run_w<OP, __nv_bfloat16, 1>(a, st);
-    else vec ? run_w<OP, float, 4>(a, st) : run_w<OP, float, 1>(a, st);
+    if (bf16) vec ? run_w<OP, __nv_bfloat16, VC>(a, st) : run_w<OP, __nv_bfloat16, 1>(a, st);
+    else vec ? run_w<OP, float, VC>(a, st) : run_w<OP, float, 1>(a, st);
 }
 
 }  // namespace
 
-void conv_shape(ConvArgs& a, int bf16, bool vec, bool backward) {
-    const int V = vec ? (bf16 ? 8 : 4) : 1;
+void conv_shape(ConvArgs& a, bool vec, bool backward) {
+    const int V = vec ? VC : 1;
     a.groups = a.D / V;
-    // tokens per thread: long tiles re-read fewer window rows, short ones fill the GPU
-    const long long want = 152LL * 1024;
-    int tile = backward ? 64 : 32;
-    while (tile > 1 && (long long)a.groups * a.ax.rows * ((a.ax.len + tile - 1) / tile) < want) tile /= 2;
-    if (backward && tile < 8) tile = 8;
+    a.gx = 1;
+    const int most = backward ? 32 : CT;
+    while (a.gx < most && a.gx < a.groups) a.gx *= 2;
+    // Tokens per thread: long tiles re-read fewer window rows and filters, short ones fill the GPU.
+    int tile;
+    if (backward) {
+        // whole waves of CTAs (two per SM) of at most 256 tokens per thread, and no fewer than 8
+        const long long nbx = (a.groups + a.gx - 1) / a.gx, gy = CB / a.gx, tokens = (long long)a.ax.rows * a.ax.len;
+        long long parts = 0;
+        do parts += 2LL * sm_count() / nbx > 0 ? 2LL * sm_count() / nbx : 1;
+        while (tokens > parts * gy * 256);
+        const long long per_row = parts * gy / a.ax.rows > 0 ? parts * gy / a.ax.rows : 1;
+        tile = (int)((a.ax.len + per_row - 1) / per_row);
+        if (tile < 8) tile = 8;
+    } else {
+        tile = 64;
+        while (tile > 1 && (long long)a.groups * a.ax.rows * ((a.ax.len + tile - 1) / tile) < sm_count() * 1024LL) tile /= 2;
+    }
     a.tile = tile;
     a.tiles_row = a.ax.len > 0 ? (a.ax.len + tile - 1) / tile : 1;
     a.ntiles = a.ax.rows * a.tiles_row;
-    const int gy = CB / bwd_gx(a.groups);
+    const int gy = CB / a.gx;
     a.parts = (a.ntiles + gy - 1) / gy;
 }
 
 cudaError_t launch_conv_fwd(ConvArgs a, int bf16, bool vec, cudaStream_t st) {
+    if (!a.ax.cu && a.ax.len == 1) return traced_launch("k_conv_step", st, [&] { run_conv<STEP>(a, bf16, vec, st); });
     // a state updated in place: the thread that starts a sequence writes its final state, which is safe unless a
     // second tile reads initial rows too (tiles shorter than the window, or packed offsets anywhere in a tile)
     void* in_place = nullptr;
@@ -380,8 +575,8 @@ cudaError_t launch_conv_fwd(ConvArgs a, int bf16, bool vec, cudaStream_t st) {
 cudaError_t launch_conv_bwd(ConvArgs a, int bf16, bool vec, cudaStream_t st) {
     cudaError_t e = traced_launch("k_conv_bwd", st, [&] { run_conv<BWD>(a, bf16, vec, st); });
     if (e != cudaSuccess) return e;
-    const int n = (a.W + 1) * a.D;
-    return traced_launch("k_conv_sum", st, [&] { k_conv_sum<<<(n + 127) / 128, 128, 0, st>>>(a); });
+    const unsigned n = (unsigned)((a.W + 1) * a.D);
+    return traced_launch("k_conv_sum", st, [&] { k_conv_sum<<<(n + 31) / 32, 256, 0, st>>>(a); });
 }
 
 }  // namespace kda

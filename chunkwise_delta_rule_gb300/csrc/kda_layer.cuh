@@ -211,11 +211,78 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// V elements of a row as they lie in memory (one access of up to 16 bytes when V > 1), and their values as pairs.
+template <typename TI, int V>
+struct alignas(sizeof(TI) * V > 16 ? 16 : sizeof(TI) * V) Raw {
+    TI v[V];
+};
+template <int V>
+__device__ __forceinline__ void unpack(const Raw<float, V>& r, float (&x)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = r.v[i];
+}
+template <int V>
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, V>& r, float (&x)[V]) {
+    if (V == 1) {
+        x[0] = __bfloat162float(r.v[0]);
+    } else {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+template <typename TI, int V>
+__device__ __forceinline__ Raw<TI, V> load_raw(const TI* p) { return *reinterpret_cast<const Raw<TI, V>*>(p); }
+template <int V>
+__device__ __forceinline__ void store_values(float* p, const float (&x)[V]) {
+    Raw<float, V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = x[i];
+    *reinterpret_cast<Raw<float, V>*>(p) = r;
+}
+template <int V>
+__device__ __forceinline__ void store_values(__nv_bfloat16* p, const float (&x)[V]) {
+    Raw<__nv_bfloat16, V> r;
+    if (V == 1) {
+        r.v[0] = __float2bfloat16_rn(x[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[V > 1 ? 2 * i + 1 : 0]);
+            reinterpret_cast<__nv_bfloat162*>(&r)[i] = h;
+        }
+    }
+    *reinterpret_cast<Raw<__nv_bfloat16, V>*>(p) = r;
+}
+
+// Sums over `parts` rows of `n` columns in a fixed order: a CTA of 32 columns x 8 groups of rows (a group's rows in
+// order, then the groups in order). Returns the total to the threads of group 0 (column -1 elsewhere).
+__device__ __forceinline__ int sum_parts(const float* part, int parts, size_t n, float& total) {
+    __shared__ float red[8][32];
+    const int lx = threadIdx.x & 31, ly = threadIdx.x >> 5;
+    const size_t c = (size_t)blockIdx.x * 32 + lx;
+    float s = 0.f;
+    if (c < n) {
+#pragma unroll 8
+        for (int p = ly; p < parts; p += 8) s += part[p * n + c];
+    }
+    red[ly][lx] = s;
+    __syncthreads();
+    total = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) total += red[k][lx];
+    return ly == 0 && c < n ? (int)c : -1;
+}
+
 // ------------------------------------------------------------------ launchers
 struct ConvArgs {
     TokenAxis ax;
-    int D, W, silu, tile, ntiles, groups;   // tokens per thread; tiles of all rows; channel groups
+    int D, W, silu, tile, ntiles, groups;   // tokens per thread; tiles of all rows; channel groups of V channels
     int tiles_row;                          // tiles per row
+    int gx;                                 // channel groups side by side in a CTA (a power of two)
     size_t ldx;
     const void *x, *h0;
     const float *weight, *bias;
@@ -227,8 +294,8 @@ struct ConvArgs {
     float *dweight, *dbias, *part;          // part: [parts][W + 1][D] sums of blocks of tiles
     int parts;
 };
-// Elements per thread of the vector path (16 bytes) or 1; tokens per thread and block counts.
-void conv_shape(ConvArgs& a, int bf16, bool vec, bool backward);
+// Channels per thread (4 on the vector path, else 1), tokens per thread and block counts.
+void conv_shape(ConvArgs& a, bool vec, bool backward);
 cudaError_t launch_conv_fwd(ConvArgs a, int bf16, bool vec, cudaStream_t st);
 cudaError_t launch_conv_bwd(ConvArgs a, int bf16, bool vec, cudaStream_t st);
 

@@ -72,18 +72,17 @@ kda_status conv_pointers(const kda::ConvArgs& a) {
     if (a.ax.len > 0 && !a.x) return fail(KDA_ERR_INVALID_ARG, "x must be non-NULL");
     return KDA_OK;
 }
-// Whether rows take 16-byte accesses.
-bool conv_vec(const kda::ConvArgs& a, int es) {
-    const size_t v = 16 / es;
-    return a.D % v == 0 && a.ldx % v == 0 && aligned16(a.x) && aligned16(a.h0) && aligned16(a.y) &&
+// Whether rows take accesses of four channels.
+bool conv_vec(const kda::ConvArgs& a) {
+    return a.D % 4 == 0 && a.ldx % 4 == 0 && aligned16(a.x) && aligned16(a.h0) && aligned16(a.y) &&
            aligned16(a.final_state) && aligned16(a.dy) && aligned16(a.dfinal) && aligned16(a.dx) && aligned16(a.dinit);
 }
 // The partial sums' bytes, whichever path the pointers' alignment will select.
-size_t conv_part_bytes(kda::ConvArgs a, int bf16) {
+size_t conv_part_bytes(kda::ConvArgs a) {
     size_t most = 0;
     for (int vec = 0; vec < 2; ++vec) {
-        if (vec && a.D % (bf16 ? 8 : 4)) continue;
-        kda::conv_shape(a, bf16, vec, true);
+        if (vec && a.D % 4) continue;
+        kda::conv_shape(a, vec, true);
         const size_t b = sizeof(float) * (size_t)a.parts * (a.W + 1) * a.D;
         most = b > most ? b : most;
     }
@@ -228,14 +227,14 @@ kda_status kda_conv_fwd(const kda_conv_problem* p, void* y, void* final_state, i
     a.final_state = final_state;
     a.err = err;
     const int bf16 = p->io == KDA_BF16;
-    const bool vec = conv_vec(a, esize(p->io));
-    kda::conv_shape(a, bf16, vec, false);
+    const bool vec = conv_vec(a);
+    kda::conv_shape(a, vec, false);
     return cuda_result(kda::launch_conv_fwd(a, bf16, vec, reinterpret_cast<cudaStream_t>(stream)), "short convolution");
 }
 
 size_t kda_conv_workspace_size(const kda_conv_problem* p) {
     kda::ConvArgs a;
-    return conv_args(p, a) == KDA_OK ? conv_part_bytes(a, p->io == KDA_BF16) : 0;
+    return conv_args(p, a) == KDA_OK ? conv_part_bytes(a) : 0;
 }
 
 kda_status kda_conv_bwd(const kda_conv_problem* p, const void* dy, const void* dfinal, void* dx, float* dweight,
@@ -245,7 +244,7 @@ kda_status kda_conv_bwd(const kda_conv_problem* p, const void* dy, const void* d
     if (st != KDA_OK || (st = conv_pointers(a)) != KDA_OK) return st;
     if (!dweight || (a.ax.len > 0 && (!dy || !dx))) return fail(KDA_ERR_INVALID_ARG, "dy, dx and dweight must be non-NULL");
     const int bf16 = p->io == KDA_BF16;
-    if ((st = check_ws(ws, ws_bytes, conv_part_bytes(a, bf16), "workspace")) != KDA_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, conv_part_bytes(a), "workspace")) != KDA_OK) return st;
     a.dy = dy;
     a.dfinal = dfinal;
     a.dx = dx;
@@ -253,8 +252,8 @@ kda_status kda_conv_bwd(const kda_conv_problem* p, const void* dy, const void* d
     a.dbias = dbias;
     a.dinit = dinit;
     a.part = static_cast<float*>(ws);
-    const bool vec = conv_vec(a, esize(p->io));
-    kda::conv_shape(a, bf16, vec, true);
+    const bool vec = conv_vec(a);
+    kda::conv_shape(a, vec, true);
     return cuda_result(kda::launch_conv_bwd(a, bf16, vec, reinterpret_cast<cudaStream_t>(stream)),
                        "short convolution backward");
 }

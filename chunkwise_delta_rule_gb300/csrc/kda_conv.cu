@@ -7,9 +7,10 @@
 //     dx_t = sum_j w[j] d_{t+W-1-j},  dw[j] = sum_t d_t x_{t-W+1+j},  dbias = sum_t d_t
 // A thread owns four neighbouring channels and walks a tile
 // of tokens with the window in registers, so each input is read once plus W - 1 rows
-// per tile; the next tokens' rows are in flight while the present ones are formed. The
-// filters pass through shared memory: read directly, each lane's 32 values lie 128
-// bytes from its neighbour's and cost more than the tile's inputs.
+// per tile. Each thread copies its own rows ahead into shared memory asynchronously (a
+// dozen tokens; held in registers they cost the warps that hide the latency). The
+// filters pass through shared memory too: read directly, each lane's values lie apart
+// from its neighbour's and cost more than the tile's inputs.
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -18,7 +19,12 @@ namespace {
 constexpr int CT = 128;   // threads of the forward
 constexpr int CB = 256;   // threads of the backward
 constexpr int VC = 4;     // channels per thread
-constexpr int CU = 8;     // tokens whose loads are in flight together, forward
+constexpr int CU = 4;     // tokens of a group of copies, forward
+constexpr int CD = 4;     // groups of copies in flight or in use
+
+// ... and backward: as many as the window holds, so that a group's first tokens are the next one's window.
+template <int W>
+constexpr int BWD_U = W == 4 ? 3 : 2;
 
 // The block's filters to shared memory, tap by tap: sw[j * ncol + c] = weight[first + c][j], row W the bias.
 template <int W, int NT>
@@ -94,6 +100,39 @@ __device__ __forceinline__ void copy_empty(const ConvArgs& a, int tile_id, int r
     }
 }
 
+// A thread's rows on their way: groups of U tokens, CD of them in a ring in shared memory (for single 16-bit elements,
+// which have no asynchronous copy, one group ahead in registers).
+template <typename TI, int V, int U, int NT>
+struct Ring {
+    static constexpr bool ASYNC = sizeof(TI) * V >= 4;
+    static constexpr int BYTES = ASYNC ? CD * U * NT * (int)sizeof(TI) * V : 0;
+    using R = Raw<TI, V>;
+    R* mine;
+    const TI* src;      // token 0 of the run
+    size_t ld;
+    int n;              // tokens of the run
+    R next[ASYNC ? 1 : U];
+    __device__ __forceinline__ void start(void* smem, const TI* p, size_t stride, int tokens) {
+        mine = static_cast<R*>(smem) + threadIdx.x;
+        src = p;
+        ld = stride;
+        n = tokens;
+    }
+    __device__ __forceinline__ void fetch(int g) {
+        const TI* p = src + (size_t)(g * U) * ld;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (g * U + u >= n) break;
+            if constexpr (ASYNC) copy_async(mine + ((g % CD) * U + u) * NT, p + u * ld);
+            else next[u] = load_raw<TI, V>(p + u * ld);
+        }
+    }
+    __device__ __forceinline__ R get(int g, int u) const {
+        if constexpr (ASYNC) return mine[((g % CD) * U + u) * NT];
+        else return next[u];
+    }
+};
+
 // Output of one token; the window moves on.
 template <int W, int V, bool SILU>
 __device__ __forceinline__ void conv_token(const float (&w)[W][V], const float (&bias)[V], float (&win)[W - 1][V],
@@ -115,7 +154,7 @@ __device__ __forceinline__ void conv_token(const float (&w)[W][V], const float (
 // Block of gx channel groups by gy tiles.
 template <typename TI, int W, int V, bool SILU>
 __global__ void __launch_bounds__(CT) k_conv_fwd(ConvArgs a) {
-    extern __shared__ float sw[];
+    extern __shared__ __align__(16) float sw[];   // the filters, the ring
     if (blockIdx.x == 0) axis_check(a.ax, a.err);
     const int lx = threadIdx.x & (a.gx - 1), ly = threadIdx.x / a.gx, gy = CT / a.gx;
     const int nbx = (a.groups + a.gx - 1) / a.gx;
@@ -135,10 +174,14 @@ __global__ void __launch_bounds__(CT) k_conv_fwd(ConvArgs a) {
     while (t < t1) {
         const Seq s = seq_at(a.ax, row, t);
         const int run = min(t1, s.end);
-        Raw<TI, V> next[CU];
+        Ring<TI, V, CU, CT> ring;
+        ring.start(sw + (W + 1) * a.gx * V, x + (size_t)t * a.ldx, a.ldx, run - t);
+        constexpr int AHEAD = ring.ASYNC ? CD - 1 : 1;
 #pragma unroll
-        for (int u = 0; u < CU; ++u)
-            if (t + u < run) next[u] = load_raw<TI, V>(x + (size_t)(t + u) * a.ldx);
+        for (int g = 0; g < AHEAD; ++g) {
+            ring.fetch(g);
+            copies_commit();
+        }
         load_window<TI, W, V>(a, s, x, t, c0, win);
         if (t == s.first && a.final_state) {
             // the final state, by the thread that has the initial one in its window: the two may be one buffer
@@ -160,32 +203,36 @@ __global__ void __launch_bounds__(CT) k_conv_fwd(ConvArgs a) {
                 store_values<V>(static_cast<TI*>(a.final_state) + ((size_t)s.n * (W - 1) + r) * a.D + c0, f);
             }
         }
-        const TI* xp = x + (size_t)t * a.ldx;
         TI* yp = y + (size_t)t * a.D;
-        for (; t + CU <= run; t += CU) {
+        for (int g = 0; t < run; ++g, t += CU) {
             Raw<TI, V> cur[CU];
+            if (ring.ASYNC) {
+                ring.fetch(g + AHEAD);
+                copies_commit();
+                copies_wait<CD - 1>();
+            }
 #pragma unroll
-            for (int u = 0; u < CU; ++u) cur[u] = next[u];
-            xp += CU * a.ldx;
+            for (int u = 0; u < CU; ++u) cur[u] = ring.get(g, u);
+            if (!ring.ASYNC) ring.fetch(g + AHEAD);
+            if (t + CU <= run) {
 #pragma unroll
-            for (int u = 0; u < CU; ++u)
-                if (t + CU + u < run) next[u] = load_raw<TI, V>(xp + u * a.ldx);
+                for (int u = 0; u < CU; ++u) {
+                    float xt[V], o[V];
+                    unpack<V>(cur[u], xt);
+                    conv_token<W, V, SILU>(w, bias, win, xt, o);
+                    store_values<V>(yp + (size_t)u * a.D, o);
+                }
+            } else {
 #pragma unroll
-            for (int u = 0; u < CU; ++u) {
-                float xt[V], o[V];
-                unpack<V>(cur[u], xt);
-                conv_token<W, V, SILU>(w, bias, win, xt, o);
-                store_values<V>(yp + (size_t)u * a.D, o);
+                for (int u = 0; u < CU - 1; ++u) {
+                    if (t + u >= run) break;
+                    float xt[V], o[V];
+                    unpack<V>(cur[u], xt);
+                    conv_token<W, V, SILU>(w, bias, win, xt, o);
+                    store_values<V>(yp + (size_t)u * a.D, o);
+                }
             }
             yp += (size_t)CU * a.D;
-        }
-#pragma unroll
-        for (int u = 0; u < CU - 1; ++u) {
-            if (t + u >= run) break;
-            float xt[V], o[V];
-            unpack<V>(next[u], xt);
-            conv_token<W, V, SILU>(w, bias, win, xt, o);
-            store_values<V>(yp + (size_t)u * a.D, o);
         }
         t = run;
     }
@@ -283,8 +330,9 @@ __global__ void __launch_bounds__(CT) k_conv_state(ConvArgs a) {
 // Block of gx channel groups by gy tiles; the tiles' parameter sums are added in tile order.
 template <typename TI, int W, int V, bool SILU>
 __global__ void __launch_bounds__(CB, 2) k_conv_bwd(ConvArgs a) {
-    constexpr int BU = W == 4 ? 3 : 2;   // tokens whose loads are in flight together
-    extern __shared__ float smem[];      // the filters, then [gy][gx * V] sums
+    constexpr int BU = BWD_U<W>;
+    extern __shared__ __align__(16) float smem[];   // the filters, [gy][gx * V] sums, the rings of x and dy
+    char* const ring = reinterpret_cast<char*>(smem + (W + 1) * a.gx * V + CB * V);
     const int gx = a.gx, gy = CB / gx;
     const int lx = threadIdx.x & (gx - 1), ly = threadIdx.x / gx;
     const int nbx = (a.groups + gx - 1) / gx;
@@ -316,13 +364,16 @@ __global__ void __launch_bounds__(CB, 2) k_conv_bwd(ConvArgs a) {
             const Seq s = seq_at(a.ax, row, t);
             const int run = min(t1, s.end), len = s.end - s.first, lim = min(run + W - 1, s.end);
             const bool start = t == s.first;
-            Raw<TI, V> nx[BU], nd[BU];
+            Ring<TI, V, BU, CB> rx, rd;
+            rx.start(ring, x + (size_t)t * a.ldx, a.ldx, lim - t);
+            rd.start(ring + rx.BYTES, dy + (size_t)t * a.D, a.D, lim - t);
+            constexpr int AHEAD = rx.ASYNC ? CD - 1 : 1;
 #pragma unroll
-            for (int u = 0; u < BU; ++u)
-                if (t + u < lim) {
-                    nx[u] = load_raw<TI, V>(x + (size_t)(t + u) * a.ldx);
-                    nd[u] = load_raw<TI, V>(dy + (size_t)(t + u) * a.D);
-                }
+            for (int g = 0; g < AHEAD; ++g) {
+                rx.fetch(g);
+                rd.fetch(g);
+                copies_commit();
+            }
             float win[W - 1][V], dwin[W - 1][V];   // x before the token (oldest first); d before it (newest first)
             load_window<TI, W, V>(a, s, x, t, c0, win);
 #pragma unroll
@@ -373,18 +424,22 @@ __global__ void __launch_bounds__(CB, 2) k_conv_bwd(ConvArgs a) {
                 }
             };
             // W - 1 tokens past the run: their d reaches back into it (zero past the sequence)
-            for (int tb = t; tb < run + W - 1; tb += BU) {
+            for (int tb = t, g = 0; tb < run + W - 1; tb += BU, ++g) {
                 Raw<TI, V> cx[BU], cd[BU];
-                const TI* xn = x + (size_t)(tb + BU) * a.ldx;
-                const TI* dn = dy + (size_t)(tb + BU) * a.D;
+                if (rx.ASYNC) {
+                    rx.fetch(g + AHEAD);
+                    rd.fetch(g + AHEAD);
+                    copies_commit();
+                    copies_wait<CD - 1>();
+                }
 #pragma unroll
                 for (int u = 0; u < BU; ++u) {
-                    cx[u] = nx[u];
-                    cd[u] = nd[u];
-                    if (tb + BU + u < lim) {
-                        nx[u] = load_raw<TI, V>(xn + u * a.ldx);
-                        nd[u] = load_raw<TI, V>(dn + (size_t)u * a.D);
-                    }
+                    cx[u] = rx.get(g, u);
+                    cd[u] = rd.get(g, u);
+                }
+                if (!rx.ASYNC) {
+                    rx.fetch(g + AHEAD);
+                    rd.fetch(g + AHEAD);
                 }
                 if (tb >= t + W - 1 && tb + BU <= run && tb + BU <= s.end - (df ? 1 : 0)) {
                     // inside the run: no case to tell apart
@@ -475,7 +530,7 @@ template <typename TI, int W, int V>
 void run_fwd(const ConvArgs& a, cudaStream_t st) {
     const int gy = CT / a.gx;
     const unsigned grid = (unsigned)((a.ntiles + gy - 1) / gy) * ((a.groups + a.gx - 1) / a.gx);
-    const size_t smem = sizeof(float) * (W + 1) * a.gx * V;
+    const size_t smem = sizeof(float) * (W + 1) * a.gx * V + Ring<TI, V, CU, CT>::BYTES;
     if (a.silu) k_conv_fwd<TI, W, V, true><<<grid, CT, smem, st>>>(a);
     else k_conv_fwd<TI, W, V, false><<<grid, CT, smem, st>>>(a);
 }
@@ -497,34 +552,49 @@ void run_state(const ConvArgs& a, cudaStream_t st) {
     const size_t items = (size_t)a.ax.N * a.groups;
     k_conv_state<TI, W, V><<<(unsigned)((items + CT - 1) / CT), CT, 0, st>>>(a);
 }
+constexpr int SMEM_MOST = 112 * 1024;   // two CTAs per SM
 template <typename TI, int W, int V>
-void run_bwd(const ConvArgs& a, cudaStream_t st) {
+cudaError_t run_bwd(const ConvArgs& a, cudaStream_t st) {
     const unsigned grid = (unsigned)a.parts * ((a.groups + a.gx - 1) / a.gx);
-    const size_t smem = sizeof(float) * ((W + 1) * a.gx * V + CB * V);
-    if (a.silu) k_conv_bwd<TI, W, V, true><<<grid, CB, smem, st>>>(a);
-    else k_conv_bwd<TI, W, V, false><<<grid, CB, smem, st>>>(a);
+    const size_t smem = sizeof(float) * ((W + 1) * a.gx * V + CB * V) + 2 * Ring<TI, V, BWD_U<W>, CB>::BYTES;
+    static SmemLimit limit[2];
+    if (a.silu) {
+        const cudaError_t e = limit[1].set(reinterpret_cast<const void*>(k_conv_bwd<TI, W, V, true>), SMEM_MOST);
+        if (e != cudaSuccess) return e;
+        k_conv_bwd<TI, W, V, true><<<grid, CB, smem, st>>>(a);
+    } else {
+        const cudaError_t e = limit[0].set(reinterpret_cast<const void*>(k_conv_bwd<TI, W, V, false>), SMEM_MOST);
+        if (e != cudaSuccess) return e;
+        k_conv_bwd<TI, W, V, false><<<grid, CB, smem, st>>>(a);
+    }
+    return cudaSuccess;
 }
 
 enum { FWD, STEP, STATE, BWD };
 template <int OP, typename TI, int W, int V>
-void run_op(const ConvArgs& a, cudaStream_t st) {
+cudaError_t run_op(const ConvArgs& a, cudaStream_t st) {
     if constexpr (OP == FWD) run_fwd<TI, W, V>(a, st);
     else if constexpr (OP == STEP) run_step<TI, W, V>(a, st);
     else if constexpr (OP == STATE) run_state<TI, W, V>(a, st);
-    else run_bwd<TI, W, V>(a, st);
+    else return run_bwd<TI, W, V>(a, st);
+    return cudaSuccess;
 }
 template <int OP, typename TI, int V>
-void run_w(const ConvArgs& a, cudaStream_t st) {
+cudaError_t run_w(const ConvArgs& a, cudaStream_t st) {
     switch (a.W) {
-        case 2: run_op<OP, TI, 2, V>(a, st); break;
-        case 3: run_op<OP, TI, 3, V>(a, st); break;
-        default: run_op<OP, TI, 4, V>(a, st); break;
+        case 2: return run_op<OP, TI, 2, V>(a, st);
+        case 3: return run_op<OP, TI, 3, V>(a, st);
+        default: return run_op<OP, TI, 4, V>(a, st);
     }
 }
 template <int OP>
-void run_conv(const ConvArgs& a, int bf16, bool vec, cudaStream_t st) {
-    if (bf16) vec ? run_w<OP, __nv_bfloat16, VC>(a, st) : run_w<OP, __nv_bfloat16, 1>(a, st);
-    else vec ? run_w<OP, float, VC>(a, st) : run_w<OP, float, 1>(a, st);
+cudaError_t run_conv(const char* name, const ConvArgs& a, int bf16, bool vec, cudaStream_t st) {
+    cudaError_t r = cudaSuccess;
+    const cudaError_t e = traced_launch(name, st, [&] {
+        if (bf16) r = vec ? run_w<OP, __nv_bfloat16, VC>(a, st) : run_w<OP, __nv_bfloat16, 1>(a, st);
+        else r = vec ? run_w<OP, float, VC>(a, st) : run_w<OP, float, 1>(a, st);
+    });
+    return r != cudaSuccess ? r : e;
 }
 
 }  // namespace
@@ -558,7 +628,7 @@ void conv_shape(ConvArgs& a, bool vec, bool backward) {
 }
 
 cudaError_t launch_conv_fwd(ConvArgs a, int bf16, bool vec, cudaStream_t st) {
-    if (!a.ax.cu && a.ax.len == 1) return traced_launch("k_conv_step", st, [&] { run_conv<STEP>(a, bf16, vec, st); });
+    if (!a.ax.cu && a.ax.len == 1) return run_conv<STEP>("k_conv_step", a, bf16, vec, st);
     // a state updated in place: the thread that starts a sequence writes its final state, which is safe unless a
     // second tile reads initial rows too (tiles shorter than the window, or packed offsets anywhere in a tile)
     void* in_place = nullptr;
@@ -566,14 +636,14 @@ cudaError_t launch_conv_fwd(ConvArgs a, int bf16, bool vec, cudaStream_t st) {
         in_place = a.final_state;
         a.final_state = nullptr;
     }
-    cudaError_t e = traced_launch("k_conv_fwd", st, [&] { run_conv<FWD>(a, bf16, vec, st); });
+    cudaError_t e = run_conv<FWD>("k_conv_fwd", a, bf16, vec, st);
     if (e != cudaSuccess || !in_place) return e;
     a.final_state = in_place;
-    return traced_launch("k_conv_state", st, [&] { run_conv<STATE>(a, bf16, vec, st); });
+    return run_conv<STATE>("k_conv_state", a, bf16, vec, st);
 }
 
 cudaError_t launch_conv_bwd(ConvArgs a, int bf16, bool vec, cudaStream_t st) {
-    cudaError_t e = traced_launch("k_conv_bwd", st, [&] { run_conv<BWD>(a, bf16, vec, st); });
+    cudaError_t e = run_conv<BWD>("k_conv_bwd", a, bf16, vec, st);
     if (e != cudaSuccess) return e;
     const unsigned n = (unsigned)((a.W + 1) * a.D);
     return traced_launch("k_conv_sum", st, [&] { k_conv_sum<<<(n + 31) / 32, 256, 0, st>>>(a); });

@@ -207,6 +207,13 @@ __device__ __forceinline__ void copy8_async(TI* dst, const TI* src, int n, int h
         copy8_slow(dst, src, n, how);
     }
 }
+// One aligned access of 4, 8 or 16 bytes, asynchronously.
+template <typename R>
+__device__ __forceinline__ void copy_async(R* dst, const void* src) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if (sizeof(R) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(sizeof(R) == 16 ? 8 : sizeof(R)) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }

@@ -319,7 +319,7 @@ struct NormArgs {
     float *dweight, *part;
     int parts;
 };
-int norm_bwd_parts(int rows);
+int norm_bwd_parts(int rows, int D);
 constexpr int NORM_MAX_D = 16384;
 cudaError_t launch_norm_fwd(const NormArgs& a, int bf16, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormArgs& a, int bf16, cudaStream_t st);

@@ -367,7 +367,7 @@ kda_status kda_norm_fwd(const kda_norm_problem* p, void* y, float* scale, void* 
 
 size_t kda_norm_workspace_size(const kda_norm_problem* p) {
     kda::NormArgs a;
-    return norm_args(p, a) == KDA_OK ? up(sizeof(float) * (size_t)kda::norm_bwd_parts(a.rows) * a.D) : 0;
+    return norm_args(p, a) == KDA_OK ? up(sizeof(float) * (size_t)kda::norm_bwd_parts(a.rows, a.D) * a.D) : 0;
 }
 
 kda_status kda_norm_bwd(const kda_norm_problem* p, const void* dy, const void* dres, void* dx, float* dweight,
@@ -378,7 +378,7 @@ kda_status kda_norm_bwd(const kda_norm_problem* p, const void* dy, const void* d
     if (a.residual) return fail(KDA_ERR_INVALID_ARG, "the backward takes the stored sum as x and no residual");
     if (!a.weight || !dweight || (a.rows > 0 && (!a.x || !dy || !dx)))
         return fail(KDA_ERR_INVALID_ARG, "x, weight, dy, dx and dweight must be non-NULL");
-    a.parts = kda::norm_bwd_parts(a.rows);
+    a.parts = kda::norm_bwd_parts(a.rows, a.D);
     if ((st = check_ws(ws, ws_bytes, sizeof(float) * (size_t)a.parts * a.D, "workspace")) != KDA_OK) return st;
     a.dy = dy;
     a.dres = dres;

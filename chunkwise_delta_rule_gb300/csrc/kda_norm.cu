@@ -32,19 +32,25 @@ __device__ __forceinline__ float amax(float a, float b) {
 // halves by `turn`, so that one barrier per call is enough.
 template <int NT, int K, bool MAX>
 __device__ __forceinline__ void cta_reduce(float (&x)[K], float (*buf)[K][NT / 32], int turn) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const float y = __shfl_xor_sync(FULL, x[k], o);
-            x[k] = MAX ? amax(x[k], y) : x[k] + y;
-        }
-    if (NT == 32) return;
-    float(*b)[NT / 32] = buf[turn & 1];
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) b[k][threadIdx.x >> 5] = x[k];
+    static_assert(K == 1 || (K == 2 && !MAX), "one value, or two sums");
+    const int lane = threadIdx.x & 31;
+    float v0 = x[0];
+    if (K == 2) {   // each half of the warp goes on with one of the sums
+        const float send = lane & 16 ? x[0] : x[K - 1];
+        v0 = (lane & 16 ? x[K - 1] : x[0]) + __shfl_xor_sync(FULL, send, 16);
     }
+#pragma unroll
+    for (int o = K == 2 ? 8 : 16; o > 0; o >>= 1) {
+        const float y = __shfl_xor_sync(FULL, v0, o);
+        v0 = MAX ? amax(v0, y) : v0 + y;
+    }
+    if (NT == 32) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) x[k] = K == 2 ? __shfl_sync(FULL, v0, 16 * k) : v0;
+        return;
+    }
+    float(*b)[NT / 32] = buf[turn & 1];
+    if ((lane & (K == 2 ? 15 : 31)) == 0) b[lane >> 4][threadIdx.x >> 5] = v0;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -204,50 +210,86 @@ __global__ void __launch_bounds__(NT) k_norm_fwd(NormArgs a, int vec) {
     }
 }
 
+// Rows on their way of the backward: a thread's chunks of h, dy and dres, `STAGES` rows in a ring in shared memory
+// copied asynchronously (chunks of 8), or one row ahead in registers (single columns).
+template <typename TI, int NT, int NC, int CH>
+struct Rows {
+    static constexpr bool ASYNC = CH > 1;
+    static constexpr int ROW = 3 * NC * NT * CH * (int)sizeof(TI);
+    static constexpr int STAGES = ROW <= 72 * 1024 ? 3 : ROW <= 100 * 1024 ? 2 : 1;   // 216 KB at most
+    static constexpr int BYTES = ASYNC ? STAGES * ROW : 0;
+    using C = Chunk<TI, CH>;
+    C next[ASYNC ? 1 : 3][ASYNC ? 1 : NC];
+    __device__ __forceinline__ static C* place(void* smem, int stage, int which, int k) {
+        return static_cast<C*>(smem) + ((stage * 3 + which) * NC + k) * NT + threadIdx.x;
+    }
+    __device__ __forceinline__ void fetch(const NormArgs& a, void* smem, int rw, int stage) {
+        if (rw < a.rows) {
+            const TI* src[3] = {static_cast<const TI*>(a.x), static_cast<const TI*>(a.dy), static_cast<const TI*>(a.dres)};
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                if (!src[q]) continue;
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    const int c = col_of<NT, CH>(k);
+                    if (c >= a.D) continue;
+                    const TI* p = src[q] + (size_t)rw * a.D + c;
+                    if constexpr (ASYNC) {
+#pragma unroll
+                        for (int i = 0; i < (int)sizeof(C) / 16; ++i)
+                            copy_async(reinterpret_cast<uint4*>(place(smem, stage, q, k)) + i, reinterpret_cast<const uint4*>(p) + i);
+                    } else {
+                        next[q][k].load(p, a.D - c, false);
+                    }
+                }
+            }
+        }
+        copies_commit();
+    }
+    __device__ __forceinline__ void get(void* smem, int stage, int which, int k, float (&x)[CH]) const {
+        if constexpr (ASYNC) unpack<CH>(place(smem, stage, which, k)->r, x);
+        else unpack<CH>(next[which][k].r, x);
+    }
+};
+
 // CTA p takes rows p, p + parts, ...; each thread keeps its columns' dw sums.
 template <typename TI, int NT, int NC, int CH>
-__global__ void __launch_bounds__(NT) k_norm_bwd(NormArgs a, int vec) {
+__global__ void __launch_bounds__(NT, NT == 256 && CH > 1 && sizeof(TI) == 2 ? 3 : 1) k_norm_bwd(NormArgs a) {
+    using R = Rows<TI, NT, NC, CH>;
+    constexpr int AHEAD = R::ASYNC ? R::STAGES - 1 : 1;
+    extern __shared__ __align__(16) unsigned char ring[];
     __shared__ __align__(16) float buf[2][2][NT / 32];
     const float inv_d = 1.f / (float)a.D;
-    Chunk<TI, CH> nh[NC], nd[NC], ng[NC];
-    auto fetch = [&](int rw) {
-        const size_t o = (size_t)rw * a.D;
+    R rows;
 #pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            const int c = col_of<NT, CH>(k);
-            if (c >= a.D) continue;
-            nh[k].load(static_cast<const TI*>(a.x) + o + c, a.D - c, vec);
-            nd[k].load(static_cast<const TI*>(a.dy) + o + c, a.D - c, vec);
-            if (a.dres) ng[k].load(static_cast<const TI*>(a.dres) + o + c, a.D - c, vec);
-        }
-    };
-    if (blockIdx.x < a.rows) fetch(blockIdx.x);
+    for (int i = 0; i < AHEAD; ++i) rows.fetch(a, ring, blockIdx.x + i * a.parts, i);
     float w[NC][CH], dw[NC][CH];
-    load_weight<NT, NC, CH>(a, vec, w);
+    load_weight<NT, NC, CH>(a, CH > 1, w);
 #pragma unroll
     for (int k = 0; k < NC; ++k)
 #pragma unroll
         for (int i = 0; i < CH; ++i) dw[k][i] = 0.f;
+    int stage = 0;
     for (int rw = blockIdx.x, turn = 0; rw < a.rows; rw += a.parts, ++turn) {
-        const size_t o = (size_t)rw * a.D;
-        Chunk<TI, CH> ch[NC], cd[NC], cg[NC];
+        if (R::ASYNC) {   // the row after those in flight goes where the previous row lay
+            rows.fetch(a, ring, rw + AHEAD * a.parts, stage == 0 ? R::STAGES - 1 : stage - 1);
+            copies_wait<R::STAGES - 1>();
+        }
+        float h[NC][CH], d[NC][CH], g[R::ASYNC ? 1 : NC][CH];
         float sums[2] = {0.f, 0.f};   // h h, h w dy
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
             if (col_of<NT, CH>(k) >= a.D) continue;
-            ch[k] = nh[k];
-            cd[k] = nd[k];
-            cg[k] = ng[k];
-            float h[CH], d[CH];
-            unpack<CH>(ch[k].r, h);
-            unpack<CH>(cd[k].r, d);
+            rows.get(ring, stage, 0, k, h[k]);
+            rows.get(ring, stage, 1, k, d[k]);
+            if (!R::ASYNC) rows.get(ring, stage, 2, k, g[R::ASYNC ? 0 : k]);
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                sums[0] = fmaf(h[i], h[i], sums[0]);
-                sums[1] = fmaf(h[i] * w[k][i], d[i], sums[1]);
+                sums[0] = fmaf(h[k][i], h[k][i], sums[0]);
+                sums[1] = fmaf(h[k][i] * w[k][i], d[k][i], sums[1]);
             }
         }
-        if (rw + a.parts < a.rows) fetch(rw + a.parts);
+        if (!R::ASYNC) rows.fetch(a, ring, rw + a.parts, 0);
         cta_reduce<NT, 2, false>(sums, buf, turn);
         // correctly rounded: for rows of a few columns the two parts of dx all but cancel
         const float r = 1.f / sqrtf(fmaf(sums[0], inv_d, a.eps));
@@ -256,24 +298,30 @@ __global__ void __launch_bounds__(NT) k_norm_bwd(NormArgs a, int vec) {
         for (int k = 0; k < NC; ++k) {
             const int c = col_of<NT, CH>(k);
             if (c >= a.D) continue;
-            float h[CH], d[CH], g[CH];
-            unpack<CH>(ch[k].r, h);
-            unpack<CH>(cd[k].r, d);
+            float o[CH];
 #pragma unroll
-            for (int i = 0; i < CH; ++i) g[i] = 0.f;
-            if (a.dres) unpack<CH>(cg[k].r, g);
+            for (int i = 0; i < CH; ++i) o[i] = 0.f;
+            if (a.dres) {
+                if constexpr (R::ASYNC) {
+                    rows.get(ring, stage, 2, k, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) o[i] = g[k][i];
+                }
+            }
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                dw[k][i] = fmaf(d[i], h[i] * r, dw[k][i]);
-                g[i] = fmaf(r, fmaf(w[k][i], d[i], -h[i] * m), g[i]);
+                dw[k][i] = fmaf(d[k][i], h[k][i] * r, dw[k][i]);
+                o[i] = fmaf(r, fmaf(w[k][i], d[k][i], -h[k][i] * m), o[i]);
             }
-            store_row<CH>(static_cast<TI*>(a.dx) + o + c, g, a.D - c, CH > 1 && vec);
+            store_row<CH>(static_cast<TI*>(a.dx) + (size_t)rw * a.D + c, o, a.D - c, CH > 1);
         }
+        stage = stage + 1 == R::STAGES ? 0 : stage + 1;
     }
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
         const int c = col_of<NT, CH>(k);
-        if (c < a.D) store_row<CH>(a.part + (size_t)blockIdx.x * a.D + c, dw[k], a.D - c, CH > 1 && vec);
+        if (c < a.D) store_row<CH>(a.part + (size_t)blockIdx.x * a.D + c, dw[k], a.D - c, CH > 1);
     }
 }
 
@@ -285,9 +333,13 @@ __global__ void __launch_bounds__(256) k_norm_sum(NormArgs a) {
 }
 
 template <typename TI, int NT, int NC, int CH, bool BWD>
-void run_one(NormArgs a, int vec, cudaStream_t st) {
+cudaError_t run_one(NormArgs a, int vec, cudaStream_t st) {
     if constexpr (BWD) {
-        k_norm_bwd<TI, NT, NC, CH><<<a.parts, NT, 0, st>>>(a, vec);
+        constexpr int smem = Rows<TI, NT, NC, CH>::BYTES;
+        static SmemLimit limit;
+        const cudaError_t e = limit.set(reinterpret_cast<const void*>(k_norm_bwd<TI, NT, NC, CH>), smem);
+        if (e != cudaSuccess) return e;
+        k_norm_bwd<TI, NT, NC, CH><<<a.parts, NT, smem, st>>>(a);
     } else {
         // as many CTAs as are resident together, about 1024 threads per SM
         const int most = sm_count() * (NT >= 1024 ? 1 : 1024 / NT < 16 ? 1024 / NT : 16);
@@ -295,42 +347,51 @@ void run_one(NormArgs a, int vec, cudaStream_t st) {
         if (a.out) k_norm_fwd<TI, NT, NC, CH, true><<<a.parts, NT, 0, st>>>(a, vec);
         else k_norm_fwd<TI, NT, NC, CH, false><<<a.parts, NT, 0, st>>>(a, vec);
     }
+    return cudaSuccess;
 }
 
 // Threads and elements per thread by the row's width.
 template <typename TI, int CH, bool BWD>
-void run_width(const NormArgs& a, int vec, cudaStream_t st) {
-    if (a.D <= 256) run_one<TI, 32, 8 / CH, CH, BWD>(a, vec, st);
-    else if (a.D <= 1024) run_one<TI, 128, 8 / CH, CH, BWD>(a, vec, st);
-    else if (a.D <= 2048) run_one<TI, 256, 8 / CH, CH, BWD>(a, vec, st);
-    else if (a.D <= 4096) run_one<TI, 256, 16 / CH, CH, BWD>(a, vec, st);
-    else if (a.D <= 8192) run_one<TI, 512, 16 / CH, CH, BWD>(a, vec, st);
-    else run_one<TI, 1024, 16 / CH, CH, BWD>(a, vec, st);
+cudaError_t run_width(const NormArgs& a, int vec, cudaStream_t st) {
+    if (a.D <= 256) return run_one<TI, 32, 8 / CH, CH, BWD>(a, vec, st);
+    if (a.D <= 1024) return run_one<TI, 128, 8 / CH, CH, BWD>(a, vec, st);
+    if (a.D <= 2048) return run_one<TI, 256, 8 / CH, CH, BWD>(a, vec, st);
+    if (a.D <= 4096) return run_one<TI, 256, 16 / CH, CH, BWD>(a, vec, st);
+    if (a.D <= 8192) return run_one<TI, 512, 16 / CH, CH, BWD>(a, vec, st);
+    return run_one<TI, 1024, 16 / CH, CH, BWD>(a, vec, st);
+}
+template <bool BWD>
+cudaError_t run_norm(const char* name, const NormArgs& a, int bf16, bool chunks, int vec, cudaStream_t st) {
+    cudaError_t r = cudaSuccess;
+    const cudaError_t e = traced_launch(name, st, [&] {
+        if (chunks) r = bf16 ? run_width<__nv_bfloat16, 8, BWD>(a, vec, st) : run_width<float, 8, BWD>(a, vec, st);
+        else r = bf16 ? run_width<__nv_bfloat16, 1, BWD>(a, 0, st) : run_width<float, 1, BWD>(a, 0, st);
+    });
+    return r != cudaSuccess ? r : e;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
 
-int norm_bwd_parts(int rows) { return rows < 2 * sm_count() ? (rows > 0 ? rows : 1) : 2 * sm_count(); }
+int norm_bwd_parts(int rows, int D) {
+    // the CTAs resident together: about 768 threads per SM
+    const int nt = D <= 256 ? 32 : D <= 1024 ? 128 : D <= 4096 ? 256 : D <= 8192 ? 512 : 1024;
+    const int most = sm_count() * (nt >= 512 ? 1 : nt == 32 ? 8 : 768 / nt);
+    return rows < most ? (rows > 0 ? rows : 1) : most;
+}
 
 cudaError_t launch_norm_fwd(const NormArgs& a, int bf16, cudaStream_t st) {
     const int vec = a.D % 8 == 0 && aligned16(a.x) && aligned16(a.residual) && aligned16(a.weight) && aligned16(a.y) &&
                     aligned16(a.h);
-    return traced_launch("k_norm_fwd", st, [&] {
-        // an 8-bit output packs 8 columns per thread and forms its groups' maxima over them
-        if (vec || a.out) bf16 ? run_width<__nv_bfloat16, 8, false>(a, vec, st) : run_width<float, 8, false>(a, vec, st);
-        else bf16 ? run_width<__nv_bfloat16, 1, false>(a, 0, st) : run_width<float, 1, false>(a, 0, st);
-    });
+    // an 8-bit output packs 8 columns per thread and forms its groups' maxima over them
+    return run_norm<false>("k_norm_fwd", a, bf16, vec || a.out, vec, st);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, int bf16, cudaStream_t st) {
     const int vec = a.D % 8 == 0 && aligned16(a.x) && aligned16(a.dy) && aligned16(a.weight) && aligned16(a.dres) &&
                     aligned16(a.dx);
-    cudaError_t e = traced_launch("k_norm_bwd", st, [&] {
-        if (vec) bf16 ? run_width<__nv_bfloat16, 8, true>(a, vec, st) : run_width<float, 8, true>(a, vec, st);
-        else bf16 ? run_width<__nv_bfloat16, 1, true>(a, 0, st) : run_width<float, 1, true>(a, 0, st);
-    });
+    const cudaError_t e = run_norm<true>("k_norm_bwd", a, bf16, vec, vec, st);
     if (e != cudaSuccess) return e;
     return traced_launch("k_norm_sum", st, [&] { k_norm_sum<<<(a.D + 31) / 32, 256, 0, st>>>(a); });
 }

@@ -178,35 +178,42 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&x)[V],
     }
 }
 
-// Asynchronous copies of a thread's own data into shared memory: n elements of a row of 8 (zeros past n), in
-// 16-byte, 4-byte or, for odd 16-bit addresses, plain accesses. `how`: 0, 1 or 2.
+// Asynchronous copies of a thread's own data into shared memory: n elements of a row of V (zeros past n), in one or two
+// whole accesses (`how` 0), 4-byte ones (1) or, for odd 16-bit addresses, plain ones (2).
 // (The slow forms stay out of line: in line at every call they pushed the callers' loops out of the instruction cache.)
-template <typename TI>
-__device__ __noinline__ void copy8_slow(TI* dst, const TI* src, int n, int how) {
+template <typename TI, int V>
+__device__ __noinline__ void copy_row_slow(TI* dst, const TI* src, int n, int how) {
     const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
     if (how <= 1) {
         constexpr int PER = 4 / sizeof(TI);
 #pragma unroll
-        for (int i = 0; i < 8 / PER; ++i) {
+        for (int i = 0; i < V / PER; ++i) {
             const int left = min(max(n - i * PER, 0), PER) * (int)sizeof(TI);
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d + 4 * i), "l"(src + (left > 0 ? i * PER : 0)), "r"(left) : "memory");
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = i < n ? src[i] : TI(0.f);
+        for (int i = 0; i < V; ++i) dst[i] = i < n ? src[i] : TI(0.f);
+    }
+}
+template <typename TI, int V>
+__device__ __forceinline__ void copy_row_async(TI* dst, const TI* src, int n, int how) {
+    constexpr int BYTES = V * (int)sizeof(TI), ONE = BYTES < 16 ? BYTES : 16;
+    if (how == 0 && (n >= V || n <= 0)) {
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+        const char* p = reinterpret_cast<const char*>(src);
+        const int full = n > 0 ? ONE : 0;
+#pragma unroll
+        for (int i = 0; i < BYTES / ONE; ++i) {
+            if (ONE == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + 16 * i), "l"(p + (n > 0 ? 16 * i : 0)), "r"(full) : "memory");
+            else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(p), "n"(ONE < 16 ? ONE : 8), "r"(full) : "memory");
+        }
+    } else {
+        copy_row_slow<TI, V>(dst, src, n, how);
     }
 }
 template <typename TI>
-__device__ __forceinline__ void copy8_async(TI* dst, const TI* src, int n, int how) {
-    if (how == 0 && (n >= 8 || n <= 0)) {
-        const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(TI) / 2; ++i)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + 16 * i), "l"(reinterpret_cast<const char*>(src) + (n > 0 ? 16 * i : 0)), "r"(n > 0 ? 16 : 0) : "memory");
-    } else {
-        copy8_slow(dst, src, n, how);
-    }
-}
+__device__ __forceinline__ void copy8_async(TI* dst, const TI* src, int n, int how) { copy_row_async<TI, 8>(dst, src, n, how); }
 // One aligned access of 4, 8 or 16 bytes, asynchronously.
 template <typename R>
 __device__ __forceinline__ void copy_async(R* dst, const void* src) {
@@ -328,7 +335,7 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int bf16, cudaStream_t st);
 constexpr int SSM_CKPT = 16;
 
 // How the scan reaches the rows of its tensors, two bits each: 0 in 16-byte accesses, 1 in 4-byte ones, 2 element by
-// element (see copy8_async).
+// element (see copy_row_async).
 enum { SSM_X = 0, SSM_DT = 2, SSM_Z = 4, SSM_B = 6, SSM_C = 8, SSM_DY = 10, SSM_OUT = 12 };
 
 struct SsmArgs {
@@ -353,7 +360,7 @@ struct SsmArgs {
     float *pA, *pv;            // [units][D][S]; [units][2][D] (skip, dt_bias)
     float* pbc;                // [channel tiles][rows * len][2][S]
 };
-int ssm_channel_tiles(int D, int G);   // channel tiles of all groups
+int ssm_bwd_tiles(int D, int G, int S);   // the backward's channel tiles of all groups
 int ssm_units(int rows, int len, int D, int G, int S, bool backward);
 cudaError_t launch_ssm_fwd(const SsmArgs& a, int bf16, int mode, cudaStream_t st);   // 0 outputs, 1 + checkpoints, 2 checkpoints only
 cudaError_t launch_ssm_pieces(const SsmArgs& a, int bf16, cudaStream_t st);          // local end states of every piece

@@ -176,7 +176,7 @@ SsmLayout ssm_layout(const kda::SsmArgs& a, bool backward, int save) {
     if (a.units_row > 1) L.rloc = ssm_state_bytes(a, units);
     L.pA = ssm_state_bytes(a, units);
     L.pv = up(sizeof(float) * units * 2 * a.D);
-    L.pbc = up(sizeof(float) * kda::ssm_channel_tiles(a.D, a.G) * tokens * 2 * a.S);
+    L.pbc = up(sizeof(float) * kda::ssm_bwd_tiles(a.D, a.G, a.S) * tokens * 2 * a.S);
     return L;
 }
 

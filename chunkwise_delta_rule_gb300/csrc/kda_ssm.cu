@@ -399,9 +399,11 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_step(SsmArgs a) {
     }
 }
 
+int fwd_tiles(int D, int G) { return (D / G + SSM_CH - 1) / SSM_CH * G; }
+
 template <typename TI, int EL>
 void run_step(const SsmArgs& a, cudaStream_t st) {
-    const unsigned tiles = ssm_channel_tiles(a.D, a.G);
+    const unsigned tiles = fwd_tiles(a.D, a.G);
     // four sequences per thread once that still leaves every SM two CTAs
     if ((long long)tiles * (a.ax.N / 4) >= 2 * sm_count()) k_ssm_step<TI, EL, 4><<<tiles * ((a.ax.N + 3) / 4), SSM_T, 0, st>>>(a);
     else k_ssm_step<TI, EL, 1><<<tiles * a.ax.N, SSM_T, 0, st>>>(a);
@@ -409,7 +411,7 @@ void run_step(const SsmArgs& a, cudaStream_t st) {
 
 template <typename TI, int EL, int MODE>
 cudaError_t run_one(const SsmArgs& a, cudaStream_t st) {
-    const unsigned grid = (unsigned)(a.ax.rows * a.units_row) * ssm_channel_tiles(a.D, a.G);
+    const unsigned grid = (unsigned)(a.ax.rows * a.units_row) * fwd_tiles(a.D, a.G);
     const int smem = (int)sizeof(typename FwdShape<TI, EL, MODE>::Smem);
     static SmemLimit limit;
     const cudaError_t e = limit.set(reinterpret_cast<const void*>(k_ssm_fwd<TI, EL, MODE>), smem);
@@ -455,8 +457,9 @@ cudaError_t launch(const char* name, const SsmArgs& a, int bf16, int mode, cudaS
 
 int ssm_units(int rows, int len, int D, int G, int S, bool backward) {
     // pieces only while the channels and rows alone leave SMs idle; a piece is at least 128 tokens
-    const long long ctas = (long long)rows * ssm_channel_tiles(D, G), want = 4LL * sm_count();
-    long long units = ctas >= sm_count() ? 1 : want / ctas;
+    const long long ctas = (long long)rows * (backward ? ssm_bwd_tiles(D, G, S) : fwd_tiles(D, G));
+    const long long full = backward ? 2 * sm_count() / 3 : sm_count(), want = (backward ? 2LL : 4LL) * sm_count();
+    long long units = ctas >= full ? 1 : want / ctas;
     const long long most = (len + 127) / 128;
     if (units > most) units = most;
     return units < 1 ? 1 : (int)units;

@@ -4,48 +4,221 @@
 //     dC_t = sum_d d0 h,  dB_t = sum_d u g,  s1 = sum_n g B,  s2 = sum_n A a g h_{t-1}
 //     dx = delta s1 + d_skip d0,  ddelta = x s1 + s2,  dA = sum_t delta a g h_{t-1}
 //     dz = dy y0 silu'(z) with y0 = sum_n C h + d_skip x,  dh0 = a_1 g_1
-// A CTA walks 32 channels backwards through a time piece in tiles of 16 tokens: the
-// states inside a tile are recomputed from the checkpoint the forward left at its
-// first token (L tokens at a time in registers), then the adjoint runs over them.
-// dB and dC are summed over the warp's channels by halving exchanges, over the CTA
-// in shared memory and over the CTAs' rows in a second kernel, in a fixed order;
-// the parameters' gradients go the same way, so nothing depends on timing.
+// A CTA walks its channels backwards through a time piece in tiles of 16 tokens. Eight
+// warps (four for more than 16 states) run the recurrences, four lanes per channel:
+// the states inside a tile are recomputed from the checkpoint the forward left at its
+// first token and held in registers (L tokens at a time), then the adjoint runs over
+// them. Four others work around them, one tile apart, as in the forward: they copy
+// tiles ahead, form the steps and gated gradients, and turn s1, s2 and sum C h into dx,
+// ddelta and dz. dB and dC are summed over a warp's channels by
+// halving exchanges, over the CTA's warps in shared memory and over the CTAs' rows in
+// a second kernel, in a fixed order; the parameters' gradients go the same way, so
+// nothing depends on timing.
 #include "kda_ssm.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int TB = SSM_CKPT;   // tokens per tile
-constexpr int YP = 40;
+constexpr int HT = 128;        // threads around the recurrences
 
-template <int EL>
+template <typename TI, int EL>
 struct BwdShape {
-    static constexpr int NP = 4 * EL;
-    static constexpr int L = EL <= 4 ? 16 : 64 / EL;      // tokens whose states are held at once
+    static constexpr int NP = 4 * EL, P = EL / 2;
+    static constexpr int RT = EL <= 4 ? 256 : 128;        // threads of the recurrences
+    static constexpr int CH = RT / 4, RW = RT / 32;       // their channels, their warps
+    static constexpr int CP = CH / 8;                     // channels of a token per thread around them
+    // tokens whose states are held at once: more would save recomputed steps, but the unrolled loop over them (about 100
+    // instructions each) has to stay in the instruction cache
+    static constexpr int L = EL <= 4 ? 8 : 64 / EL;
     static constexpr int NSUB = TB / L;
     static constexpr int VB = 2 * EL;                     // dB and dC values of a lane
     static constexpr int KEEP = VB >= 8 ? VB / 8 : 1;     // ... it holds after the sum over 8 channels
+    static constexpr int NBC = (TB * 2 * (NP / 8) + HT - 1) / HT;   // chunks of 8 states of b and c per thread
+    static constexpr int STAGES = 5;                      // tiles: the one after, the present, the one before, two on their way
     struct Smem {
-        float4 in[TB][SSM_CH];            // delta, u, d0, x
-        float s1[TB][YP], s2[TB][YP], yc[TB][YP];
-        float b[TB][NP], c[TB][NP];
-        float red[4][TB][2 * NP];
-        float sub[NSUB > 1 ? NSUB - 1 : 1][EL][SSM_T];
+        TI tok[STAGES][4][HT][CP];            // x, dt, dy, z
+        TI bc[STAGES][NBC][HT][8];
+        float4 in[2][TB][CH];                 // delta, u, d0
+        float4 out[2][TB][CH];                // s1, s2 (in log2 units), sum C h
+        float b[2][TB][NP], c[2][TB][NP];
+        float red[2][RW][TB][2 * NP];
+        float sub[NSUB > 1 ? NSUB - 1 : 1][EL][RT];
     };
 };
 
+// Place of a channel in a token's row, permuted so that the eight threads of a quarter warp, of eight (or four)
+// neighbouring channels each, reach distinct banks.
+__device__ __forceinline__ int in_at(int ch) { return ch ^ ((ch >> 3) & 7); }
+
+__device__ __forceinline__ void named_barrier(int id, int count) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+template <typename TI, int V>
+__device__ __forceinline__ void store_part(TI* p, const float (&x)[V], int valid, bool whole) {
+    if (whole) {
+        store_values<V>(p, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < valid) st(p + i, x[i]);
+    }
+}
+
 template <typename TI, int EL>
-__global__ void __launch_bounds__(SSM_T) k_ssm_bwd(SsmArgs a) {
-    using Sh = BwdShape<EL>;
-    constexpr int NP = Sh::NP, L = Sh::L, NSUB = Sh::NSUB, VB = Sh::VB, KEEP = Sh::KEEP;
-    extern __shared__ __align__(16) unsigned char raw[];
-    typename Sh::Smem& sm = *reinterpret_cast<typename Sh::Smem*>(raw);
-    const SsmPlace pl = ssm_place<SSM_CH>(a);
+__global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArgs a) {
+    using Sh = BwdShape<TI, EL>;
+    constexpr int NP = Sh::NP, P = Sh::P, RT = Sh::RT, CH = Sh::CH, RW = Sh::RW, CP = Sh::CP, L = Sh::L, NSUB = Sh::NSUB,
+                  VB = Sh::VB, KEEP = Sh::KEEP, NBC = Sh::NBC, STAGES = Sh::STAGES;
+    extern __shared__ __align__(16) unsigned char raw_smem[];
+    typename Sh::Smem& sm = *reinterpret_cast<typename Sh::Smem*>(raw_smem);
+    const SsmPlace pl = ssm_place<CH>(a);
+    const size_t tok0 = (size_t)pl.row * a.ax.len;
+    const size_t DS = (size_t)a.D * a.S;
+    // tile k = 0 is the piece's last one
+    const int ntiles = (pl.hi - pl.lo + TB - 1) / TB;
+    auto tile_begin = [&](int k) { return pl.lo + (ntiles - 1 - k) * TB; };
+
+    if (threadIdx.x >= RT) {
+        // ---------------------------------------------------------------- around the recurrences
+        const int tid = threadIdx.x - RT;
+        const int ptok = tid >> 3, pc = (tid & 7) * CP, pvalid = pl.nch - pc;   // one token, CP channels
+        const TI* src[4] = {static_cast<const TI*>(a.x) + tok0 * a.ldx + pl.c0 + pc,
+                            static_cast<const TI*>(a.dt) + tok0 * a.lddt + pl.c0 + pc,
+                            static_cast<const TI*>(a.dy) + tok0 * a.D + pl.c0 + pc,
+                            a.z ? static_cast<const TI*>(a.z) + tok0 * a.ldz + pl.c0 + pc : nullptr};
+        const size_t ld[4] = {a.ldx, a.lddt, (size_t)a.D, a.ldz};
+        constexpr int SHIFT[4] = {SSM_X, SSM_DT, SSM_DY, SSM_Z};
+        const TI* bp = static_cast<const TI*>(a.b) + tok0 * a.ldb + (size_t)pl.g * a.S;
+        const TI* cp = static_cast<const TI*>(a.c) + tok0 * a.ldc + (size_t)pl.g * a.S;
+        constexpr int NC = NP / 8;
+        auto fetch = [&](int k) {
+            if (k < ntiles) {
+                const int tb = tile_begin(k), st = k % STAGES;
+                const size_t tt = min(tb + ptok, pl.hi - 1);
+                const int n = tb + ptok < pl.hi ? pvalid : 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q < 3 || src[3]) copy_row_async<TI, CP>(sm.tok[st][q][tid], src[q] + tt * ld[q], n, a.how >> SHIFT[q] & 3);
+#pragma unroll
+                for (int j = 0; j < NBC; ++j) {
+                    const int i = tid + j * HT;
+                    if (i >= 2 * TB * NC) break;
+                    const bool isc = i >= TB * NC;
+                    const int r = isc ? i - TB * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
+                    const size_t tr = min(tb + tok, pl.hi - 1);
+                    const int m = tb + tok < pl.hi ? a.S - k8 : 0;
+                    const TI* p = isc ? cp + tr * a.ldc : bp + tr * a.ldb;
+                    copy8_async(sm.bc[st][j][tid], p + (m > 0 ? k8 : 0), m, a.how >> (isc ? SSM_C : SSM_B) & 3);
+                }
+            }
+            copies_commit();
+        };
+        for (int k = 0; k < STAGES - 2; ++k) fetch(k);
+        float bias[CP], skip[CP], dskip[CP], dbias[CP];
+#pragma unroll
+        for (int i = 0; i < CP; ++i) {
+            bias[i] = a.dt_bias && i < pvalid ? a.dt_bias[pl.c0 + pc + i] : 0.f;
+            skip[i] = a.d_skip && i < pvalid ? a.d_skip[pl.c0 + pc + i] : 0.f;
+            dskip[i] = dbias[i] = 0.f;
+        }
+        // step k: tile k - 1's outputs, tile k + 1's inputs (in the place of tile k - 1's)
+        for (int k = -1; k <= ntiles; ++k) {
+            if (k > 0) {
+                const int w = (k - 1) & 1, st = (k - 1) % STAGES, tb = tile_begin(k - 1), nt = min(TB, pl.hi - tb);
+                if (ptok < nt && pvalid > 0) {
+                    float x[CP], dt[CP], dy[CP], z[CP], ox[CP], od[CP], oz[CP];
+                    load_row<CP>(sm.tok[st][0][tid], x, CP, true);
+                    load_row<CP>(sm.tok[st][1][tid], dt, CP, true);
+                    load_row<CP>(sm.tok[st][2][tid], dy, CP, true);
+                    if (src[3]) load_row<CP>(sm.tok[st][3][tid], z, CP, true);
+#pragma unroll
+                    for (int i = 0; i < CP; ++i) {
+                        const float4 in = sm.in[w][ptok][in_at(pc + i)];
+                        const float4 v = sm.out[w][ptok][in_at(pc + i)];
+                        const float y0 = fmaf(skip[i], x[i], v.z);
+                        ox[i] = fmaf(in.x, v.x, skip[i] * in.z);
+                        od[i] = fmaf(x[i], v.x, v.y * (1.f / LOG2E));
+                        if (a.softplus) od[i] *= sigmoid_fast(dt[i] + bias[i]);
+                        if (src[3]) {
+                            const float sg = sigmoid_fast(z[i]);
+                            oz[i] = dy[i] * y0 * sg * fmaf(z[i], 1.f - sg, 1.f);
+                        }
+                        if (i < pvalid) {
+                            dskip[i] = fmaf(in.z, x[i], dskip[i]);
+                            dbias[i] += od[i];
+                        }
+                    }
+                    const size_t o = (tok0 + tb + ptok) * a.D + pl.c0 + pc;
+                    const bool whole = pvalid >= CP && !(a.how >> SSM_OUT & 3);
+                    store_part<TI, CP>(static_cast<TI*>(a.dx) + o, ox, pvalid, whole);
+                    store_part<TI, CP>(static_cast<TI*>(a.ddt) + o, od, pvalid, whole);
+                    if (src[3]) store_part<TI, CP>(static_cast<TI*>(a.dz) + o, oz, pvalid, whole);
+                }
+                for (int i = tid; i < nt * 2 * NP; i += HT) {
+                    const int tok = i / (2 * NP), f = i - tok * (2 * NP), which = f / NP, n = f - which * NP;
+                    float v = 0.f;
+#pragma unroll
+                    for (int r = 0; r < RW; ++r) v += sm.red[w][r][tok][f];
+                    if (n < a.S) a.pbc[((pl.tile * (size_t)a.ax.rows * a.ax.len + tok0 + tb + tok) * 2 + which) * a.S + n] = v;
+                }
+            }
+            if (k + 1 < ntiles) {
+                const int w = (k + 1) & 1, st = (k + 1) % STAGES;
+                copies_wait<STAGES - 3>();
+                float x[CP], dt[CP], dy[CP], z[CP];
+                load_row<CP>(sm.tok[st][0][tid], x, CP, true);
+                load_row<CP>(sm.tok[st][1][tid], dt, CP, true);
+                load_row<CP>(sm.tok[st][2][tid], dy, CP, true);
+                if (src[3]) load_row<CP>(sm.tok[st][3][tid], z, CP, true);
+#pragma unroll
+                for (int i = 0; i < CP; i += 2) {
+                    float2 dl = make_float2(dt[i] + bias[i], dt[i + 1] + bias[i + 1]);
+                    if (a.softplus) dl = ssm_softplus2(dl);
+                    const float2 u = mul2(dl, make_float2(x[i], x[i + 1]));
+                    float2 d0 = make_float2(dy[i], dy[i + 1]);
+                    if (src[3]) d0 = make_float2(d0.x * z[i] * sigmoid_fast(z[i]), d0.y * z[i + 1] * sigmoid_fast(z[i + 1]));
+                    sm.in[w][ptok][in_at(pc + i)] = make_float4(dl.x, u.x, d0.x, 0.f);
+                    sm.in[w][ptok][in_at(pc + i + 1)] = make_float4(dl.y, u.y, d0.y, 0.f);
+                }
+#pragma unroll
+                for (int j = 0; j < NBC; ++j) {
+                    const int i = tid + j * HT;
+                    if (i >= 2 * TB * NC) break;
+                    const bool isc = i >= TB * NC;
+                    const int r = isc ? i - TB * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
+                    float v[8];
+                    load_row<8>(sm.bc[st][j][tid], v, 8, true);
+                    float4* dst = reinterpret_cast<float4*>(isc ? &sm.c[w][tok][k8] : &sm.b[w][tok][k8]);
+                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                }
+            }
+            fetch(k + STAGES - 1);   // into the stage of tile k - 1, which was read last
+            if (k < ntiles) __syncthreads();
+        }
+        // this piece's sums for d_skip and dt_bias
+        float* red = &sm.red[0][0][0][0];   // [16 tokens][CH]
+        for (int which = 0; which < 2; ++which) {
+            named_barrier(1, HT);
+#pragma unroll
+            for (int i = 0; i < CP; ++i) red[ptok * CH + pc + i] = which ? dbias[i] : dskip[i];
+            named_barrier(1, HT);
+            if (tid < pl.nch) {
+                float v = 0.f;
+#pragma unroll
+                for (int i = 0; i < TB; ++i) v += red[i * CH + tid];
+                a.pv[((size_t)pl.unit * 2 + which) * a.D + pl.c0 + tid] = v;
+            }
+        }
+        return;
+    }
+
+    // -------------------------------------------------------------------- the recurrences
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = tid & 3, ch = tid >> 2, n0 = l * EL;
     const int d = pl.c0 + ch;
     const bool on = ch < pl.nch;
-    const size_t tok0 = (size_t)pl.row * a.ax.len;
-    const size_t DS = (size_t)a.D * a.S;
     float A2[EL], r[EL], dA[EL];
     load_states<EL>(a.A_log + (size_t)d * a.S, n0, a.S, on, A2);
 #pragma unroll
@@ -69,23 +242,8 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_bwd(SsmArgs a) {
             store_states<EL>(a.dh0 + n * DS + (size_t)d * a.S, n0, a.S, on, v);
         }
     }
-    // this thread's part of a tile: one token, 4 channels
-    const int ptok = tid >> 3, pc = (tid & 7) * 4, pvalid = pl.nch - pc;
-    const TI* xp = static_cast<const TI*>(a.x) + tok0 * a.ldx + pl.c0 + pc;
-    const TI* dp = static_cast<const TI*>(a.dt) + tok0 * a.lddt + pl.c0 + pc;
-    const TI* zp = a.z ? static_cast<const TI*>(a.z) + tok0 * a.ldz + pl.c0 + pc : nullptr;
-    const TI* yp = static_cast<const TI*>(a.dy) + tok0 * a.D + pl.c0 + pc;
-    const TI* bp = static_cast<const TI*>(a.b) + tok0 * a.ldb + (size_t)pl.g * a.S;
-    const TI* cp = static_cast<const TI*>(a.c) + tok0 * a.ldc + (size_t)pl.g * a.S;
-    float bias[4], skip[4], dskip[4], dbias[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        bias[i] = a.dt_bias && i < pvalid ? a.dt_bias[pl.c0 + pc + i] : 0.f;
-        skip[i] = a.d_skip && i < pvalid ? a.d_skip[pl.c0 + pc + i] : 0.f;
-        dskip[i] = dbias[i] = 0.f;
-    }
     Seq s{0, 0, 0};
-    if (pl.hi > pl.lo) {
+    if (ntiles > 0) {
         s = seq_at(a.ax, pl.row, pl.hi - 1);
         if (s.end > pl.hi) {
             // the adjoint entering this piece from the later pieces of its sequence, joined in order
@@ -100,44 +258,20 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_bwd(SsmArgs a) {
             }
         }
     }
-    const int last = pl.hi > pl.lo ? (pl.hi - 1) / TB * TB : pl.lo - TB;
-    for (int tb = last; tb >= pl.lo; tb -= TB) {
-        const int te = min(tb + TB, pl.hi), nt = te - tb;
-        const int t = tb + ptok;
-        const bool in = t < te && pvalid > 0;
-        // steps and gated gradients of the tile
-        float x[4], raw_dt[4], z[4], dy[4];
+    const size_t slot0 = (size_t)pl.row * ((a.ax.len + TB - 1) / TB);
+    float hnext[EL];   // the next tile's checkpoint, on its way
+    if (ntiles > 0) load_states<EL>(a.ckpt + (slot0 + tile_begin(0) / TB) * DS + (size_t)d * a.S, n0, a.S, on, hnext);
+    const int my_in = in_at(ch);
+    // the first of the values a lane holds after the sum over channels: dB of state n0 + f for f < EL, then dC
+    int my_red = (lane & 4 ? VB / 2 : 0) + (lane & 8 ? VB / 4 : 0) + (VB >= 8 && lane & 16 ? VB / 8 : 0);
+    my_red = my_red < EL ? n0 + my_red : NP + n0 + my_red - EL;
+    __syncthreads();   // the first tile's inputs
+    for (int k = 0; k < ntiles; ++k) {
+        const int tb = tile_begin(k), te = min(tb + TB, pl.hi), nt = te - tb, w = k & 1;
+        float hstart[EL];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = raw_dt[i] = z[i] = dy[i] = 0.f;
-        if (in) {
-            load_row<4>(xp + (size_t)t * a.ldx, x, pvalid, false);
-            load_row<4>(dp + (size_t)t * a.lddt, raw_dt, pvalid, false);
-            load_row<4>(yp + (size_t)t * a.D, dy, pvalid, false);
-            if (zp) load_row<4>(zp + (size_t)t * a.ldz, z, pvalid, false);
-        }
-        float d0[4], dl[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            raw_dt[i] += bias[i];
-            dl[i] = !in || i >= pvalid ? 0.f : a.softplus ? ssm_softplus(raw_dt[i]) : raw_dt[i];
-            d0[i] = zp ? dy[i] * z[i] * sigmoid_fast(z[i]) : dy[i];
-            sm.in[ptok][pc + i] = make_float4(dl[i], dl[i] * x[i], d0[i], x[i]);
-        }
-        constexpr int NC = NP / 8;
-        for (int i = tid; i < 2 * TB * NC; i += SSM_T) {
-            const bool isc = i >= TB * NC;
-            const int j = isc ? i - TB * NC : i, tok = j / NC, k = (j - tok * NC) * 8;
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
-            if (tb + tok < te) {
-                if (isc) load_row<8>(cp + (size_t)(tb + tok) * a.ldc + k, v, a.S - k, a.S - k >= 8 && !(a.how >> SSM_C & 3));
-                else load_row<8>(bp + (size_t)(tb + tok) * a.ldb + k, v, a.S - k, a.S - k >= 8 && !(a.how >> SSM_B & 3));
-            }
-            float* dst = isc ? &sm.c[tok][k] : &sm.b[tok][k];
-            reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
+        for (int e = 0; e < EL; ++e) hstart[e] = hnext[e];
+        if (k + 1 < ntiles) load_states<EL>(a.ckpt + (slot0 + tile_begin(k + 1) / TB) * DS + (size_t)d * a.S, n0, a.S, on, hnext);
         // first and last tokens of sequences inside the tile
         uint32_t starts = 0, ends = 0;
         for (int p = te - 1;;) {
@@ -148,162 +282,132 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_bwd(SsmArgs a) {
             if (s.first == tb) break;
             p = s.first - 1;
         }
-        __syncthreads();
-        float hstart[EL];
-        {
-            const size_t slot = (size_t)pl.row * ((a.ax.len + TB - 1) / TB) + tb / TB;
-            load_states<EL>(a.ckpt + slot * DS + (size_t)d * a.S, n0, a.S, on, hstart);
-        }
-        // one token of the recurrence
+        // one token of the forward recurrence
         auto step = [&](int i, float(&h)[EL]) {
-            if (i > 0 && (starts >> i & 1)) state_of(a.h0, seq_at(a.ax, pl.row, tb + i).n, h);
-            const float4 v = sm.in[i][ch];
+            const float2 v = *reinterpret_cast<const float2*>(&sm.in[w][i][my_in]);
             float b[EL];
-            lds_states<EL>(&sm.b[i][n0], b);
+            lds_states<EL>(&sm.b[w][i][n0], b);
+            const float2 dl = make_float2(v.x, v.x), u = make_float2(v.y, v.y);
 #pragma unroll
-            for (int e = 0; e < EL; ++e) h[e] = fmaf(ex2(v.x * A2[e]), h[e], v.y * b[e]);
+            for (int e = 0; e < P; ++e) {
+                const float2 g = mul2(dl, make_float2(A2[2 * e], A2[2 * e + 1]));
+                const float2 hn = fma2(make_float2(ex2(g.x), ex2(g.y)), make_float2(h[2 * e], h[2 * e + 1]),
+                                       mul2(u, make_float2(b[2 * e], b[2 * e + 1])));
+                h[2 * e] = hn.x;
+                h[2 * e + 1] = hn.y;
+            }
         };
-        if (NSUB > 1) {
-            // states at the sub-blocks' starts
-            float h[EL];
+        // one token of the adjoint, from its state h and the one before it
+        auto reverse = [&](int it, const float(&h)[EL], const float(&hp)[EL]) {
+            const float4 v = sm.in[w][it][my_in];
+            float b[EL], c[EL], bc[VB];
+            lds_states<EL>(&sm.b[w][it][n0], b);
+            lds_states<EL>(&sm.c[w][it][n0], c);
+            const float2 dl = make_float2(v.x, v.x), u = make_float2(v.y, v.y), d0 = make_float2(v.z, v.z);
+            float2 p1, p2, py;
 #pragma unroll
-            for (int e = 0; e < EL; ++e) h[e] = hstart[e];
-            for (int i = 0; i < min(nt, TB - L); ++i) {
-                step(i, h);
-                if ((i + 1) % L == 0)
-#pragma unroll
-                    for (int e = 0; e < EL; ++e) sm.sub[(i + 1) / L - 1][e][tid] = h[e];
+            for (int e = 0; e < P; ++e) {
+                const float2 cc = make_float2(c[2 * e], c[2 * e + 1]), hh = make_float2(h[2 * e], h[2 * e + 1]);
+                const float2 AA = make_float2(A2[2 * e], A2[2 * e + 1]), bb = make_float2(b[2 * e], b[2 * e + 1]);
+                const float2 g = fma2(cc, d0, make_float2(r[2 * e], r[2 * e + 1]));
+                const float2 x = mul2(dl, AA);
+                const float2 dc = mul2(d0, hh), dbv = mul2(u, g);
+                const float2 rn = mul2(make_float2(ex2(x.x), ex2(x.y)), g);
+                const float2 wv = mul2(rn, make_float2(hp[2 * e], hp[2 * e + 1]));
+                py = e == 0 ? mul2(hh, cc) : fma2(hh, cc, py);
+                p1 = e == 0 ? mul2(g, bb) : fma2(g, bb, p1);
+                p2 = e == 0 ? mul2(wv, AA) : fma2(wv, AA, p2);
+                const float2 da = fma2(wv, dl, make_float2(dA[2 * e], dA[2 * e + 1]));
+                dA[2 * e] = da.x;
+                dA[2 * e + 1] = da.y;
+                r[2 * e] = rn.x;
+                r[2 * e + 1] = rn.y;
+                bc[2 * e] = dbv.x;
+                bc[2 * e + 1] = dbv.y;
+                bc[EL + 2 * e] = dc.x;
+                bc[EL + 2 * e + 1] = dc.y;
             }
-        }
-        for (int k = NSUB - 1; k >= 0; --k) {
-            const int i0 = k * L;
-            if (i0 >= nt) continue;
-            float hs[L][EL], h[EL], hk[EL];
+            // over the channel's four lanes: lane 0 keeps s1, lane 1 s2, lane 2 sum C h
+            float pv[4] = {p1.x + p1.y, p2.x + p2.y, py.x + py.y, 0.f};
+            halve<4>(pv, l, 2);
+            halve<2>(pv, l, 1);
+            reinterpret_cast<float*>(&sm.out[w][it][my_in])[l] = pv[0];
+            // over the warp's 8 channels: lane bits 2, 3, 4
+            halve<VB>(bc, lane, 4);
+            halve<VB / 2>(bc, lane, 8);
+            if constexpr (VB >= 8) halve<VB / 4>(bc, lane, 16);
+            else bc[0] += __shfl_xor_sync(SSM_FULL, bc[0], 16);
 #pragma unroll
-            for (int e = 0; e < EL; ++e) {
-                hk[e] = k == 0 ? hstart[e] : sm.sub[k > 0 ? k - 1 : 0][e][tid];
-                h[e] = hk[e];
+            for (int f = 0; f < KEEP; ++f) sm.red[w][warp][it][my_red + f] = bc[f];
+        };
+        auto leave = [&](int it) {   // the first token of a sequence: its state's adjoint goes out, the previous one's comes in
+            if (a.dh0) {
+                const int n = seq_at(a.ax, pl.row, tb + it).n;
+                store_states<EL>(a.dh0 + n * DS + (size_t)d * a.S, n0, a.S, on, r);
             }
 #pragma unroll
-            for (int i = 0; i < L; ++i) {
-                if (i0 + i < nt) step(i0 + i, h);
+            for (int e = 0; e < EL; ++e) r[e] = 0.f;
+        };
+        if (nt == TB && !(starts & ~1u) && !(ends & ~(1u << (TB - 1)))) {
+            // a whole tile of one sequence
+            if (ends) state_of(a.dht, seq_at(a.ax, pl.row, te - 1).n, r);
+            if (NSUB > 1) {
+                // states at the sub-blocks' starts
+                float h[EL];
 #pragma unroll
-                for (int e = 0; e < EL; ++e) hs[i][e] = h[e];
-            }
+                for (int e = 0; e < EL; ++e) h[e] = hstart[e];
+#pragma unroll 1
+                for (int sb = 1; sb < NSUB; ++sb) {
 #pragma unroll
-            for (int q = L / 4 - 1; q >= 0; --q) {
-                float p1[4], p2[4], py[4];
+                    for (int i = 0; i < L; ++i) step((sb - 1) * L + i, h);
 #pragma unroll
-                for (int j = 3; j >= 0; --j) {
-                    const int i = 4 * q + j, it = i0 + i;
-                    p1[j] = p2[j] = py[j] = 0.f;
-                    if (it >= nt) continue;
-                    if (ends >> it & 1) state_of(a.dht, seq_at(a.ax, pl.row, tb + it).n, r);
-                    float hp[EL];
-#pragma unroll
-                    for (int e = 0; e < EL; ++e) hp[e] = i > 0 ? hs[i > 0 ? i - 1 : 0][e] : hk[e];
-                    const bool start = starts >> it & 1;
-                    if (start && it > 0) state_of(a.h0, seq_at(a.ax, pl.row, tb + it).n, hp);
-                    const float4 v = sm.in[it][ch];
-                    float b[EL], c[EL], bc[VB];
-                    lds_states<EL>(&sm.b[it][n0], b);
-                    lds_states<EL>(&sm.c[it][n0], c);
-#pragma unroll
-                    for (int e = 0; e < EL; ++e) {
-                        const float g = fmaf(c[e], v.z, r[e]);
-                        py[j] = fmaf(hs[i][e], c[e], py[j]);
-                        bc[EL + e] = v.z * hs[i][e];
-                        bc[e] = v.y * g;
-                        p1[j] = fmaf(g, b[e], p1[j]);
-                        r[e] = ex2(v.x * A2[e]) * g;
-                        const float w = r[e] * hp[e];
-                        p2[j] = fmaf(w, A2[e], p2[j]);
-                        dA[e] = fmaf(w, v.x, dA[e]);
-                    }
-                    if (start) {
-                        if (a.dh0) {
-                            const int n = seq_at(a.ax, pl.row, tb + it).n;
-                            store_states<EL>(a.dh0 + n * DS + (size_t)d * a.S, n0, a.S, on, r);
-                        }
-#pragma unroll
-                        for (int e = 0; e < EL; ++e) r[e] = 0.f;
-                    }
-                    // over the warp's 8 channels: lane bits 2, 3, 4
-                    int first = 0;
-                    halve<VB>(bc, lane, 4);
-                    first += lane & 4 ? VB / 2 : 0;
-                    halve<VB / 2>(bc, lane, 8);
-                    first += lane & 8 ? VB / 4 : 0;
-                    if (VB >= 8) {
-                        halve<(VB >= 8 ? VB / 4 : 2)>(bc, lane, 16);
-                        first += lane & 16 ? VB / 8 : 0;
-                    } else {
-                        bc[0] += __shfl_xor_sync(SSM_FULL, bc[0], 16);
-                    }
-                    // value f of a lane: dB of its state f, or dC of state f - EL
-#pragma unroll
-                    for (int f = 0; f < KEEP; ++f) {
-                        const int w = first + f;
-                        sm.red[warp][it][w < EL ? n0 + w : NP + n0 + w - EL] = bc[f];
-                    }
-                }
-                halve<4>(p1, l, 2); halve<2>(p1, l, 1);
-                halve<4>(p2, l, 2); halve<2>(p2, l, 1);
-                halve<4>(py, l, 2); halve<2>(py, l, 1);
-                const int it = i0 + 4 * q + l;
-                if (it < nt) {
-                    sm.s1[it][ch] = p1[0];
-                    sm.s2[it][ch] = p2[0];
-                    sm.yc[it][ch] = py[0];
+                    for (int e = 0; e < EL; ++e) sm.sub[NSUB > 1 ? sb - 1 : 0][e][tid] = h[e];
                 }
             }
-        }
-        __syncthreads();
-        if (in) {
-            float ox[4], od[4], oz[4];
+#pragma unroll 1
+            for (int sb = NSUB - 1; sb >= 0; --sb) {
+                float hs[L][EL], h[EL], hk[EL];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float s1 = sm.s1[ptok][pc + i];
-                ox[i] = fmaf(dl[i], s1, skip[i] * d0[i]);
-                float g = fmaf(x[i], s1, sm.s2[ptok][pc + i] * (1.f / LOG2E));
-                if (a.softplus) g *= 1.f / (1.f + expf(-raw_dt[i]));
-                od[i] = g;
-                const float y0 = fmaf(skip[i], x[i], sm.yc[ptok][pc + i]), sg = sigmoid_fast(z[i]);
-                oz[i] = dy[i] * y0 * sg * fmaf(z[i], 1.f - sg, 1.f);
-                if (i < pvalid) {
-                    dskip[i] = fmaf(d0[i], x[i], dskip[i]);
-                    dbias[i] += g;
+                for (int e = 0; e < EL; ++e) {
+                    hk[e] = NSUB == 1 || sb == 0 ? hstart[e] : sm.sub[NSUB > 1 && sb > 0 ? sb - 1 : 0][e][tid];
+                    h[e] = hk[e];
                 }
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    step(sb * L + i, h);
+#pragma unroll
+                    for (int e = 0; e < EL; ++e) hs[i][e] = h[e];
+                }
+#pragma unroll
+                for (int i = L - 1; i >= 0; --i) reverse(sb * L + i, hs[i], i > 0 ? hs[i > 0 ? i - 1 : 0] : hk);
             }
-            const size_t o = (tok0 + t) * a.D + pl.c0 + pc;
-            store_row<4>(static_cast<TI*>(a.dx) + o, ox, pvalid, false);
-            store_row<4>(static_cast<TI*>(a.ddt) + o, od, pvalid, false);
-            if (zp) store_row<4>(static_cast<TI*>(a.dz) + o, oz, pvalid, false);
-        }
-        for (int i = tid; i < nt * 2 * NP; i += SSM_T) {
-            const int tok = i / (2 * NP), f = i - tok * (2 * NP), which = f / NP, n = f - which * NP;
-            if (n >= a.S) continue;
-            const float v = (sm.red[0][tok][f] + sm.red[1][tok][f]) + (sm.red[2][tok][f] + sm.red[3][tok][f]);
-            const size_t tokens = (size_t)a.ax.rows * a.ax.len;
-            a.pbc[((pl.tile * tokens + tok0 + tb + tok) * 2 + which) * a.S + n] = v;
+            if (starts) leave(0);
+        } else {
+            // sequences begin or end inside, or tokens are missing: each token's state from the tile's (or its
+            // sequence's) first one, without holding any
+#pragma unroll 1
+            for (int it = nt - 1; it >= 0; --it) {
+                if (ends >> it & 1) state_of(a.dht, seq_at(a.ax, pl.row, tb + it).n, r);
+                const int from = 31 - __clz((starts & (2u << it) - 1) | 1u);   // the last start at or before it
+                float h[EL], hp[EL];
+                if (from > 0) {
+                    state_of(a.h0, seq_at(a.ax, pl.row, tb + from).n, h);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < EL; ++e) h[e] = hstart[e];
+                }
+#pragma unroll 1
+                for (int i = from; i < it; ++i) step(i, h);
+#pragma unroll
+                for (int e = 0; e < EL; ++e) hp[e] = h[e];
+                step(it, h);
+                reverse(it, h, hp);
+                if (starts >> it & 1) leave(it);
+            }
         }
         __syncthreads();
     }
-    // parameters: this piece's sums
     store_states<EL>(a.pA + pl.unit * DS + (size_t)d * a.S, n0, a.S, on, dA);
-    float* red = &sm.red[0][0][0];   // [16 tokens][32 channels]
-    for (int which = 0; which < 2; ++which) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red[ptok * SSM_CH + pc + i] = which ? dbias[i] : dskip[i];
-        __syncthreads();
-        if (tid < pl.nch) {
-            float v = 0.f;
-#pragma unroll
-            for (int i = 0; i < TB; ++i) v += red[i * SSM_CH + tid];
-            a.pv[((size_t)pl.unit * 2 + which) * a.D + pl.c0 + tid] = v;
-        }
-    }
 }
 
 // Local adjoint leaving a time piece's first token: from dht where the piece's sequence ends inside it, else from zero.
@@ -379,6 +483,8 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_bwd_pieces(SsmArgs a) {
     if (on && l == 0) a.sdt[(size_t)pl.unit * a.D + d] = sd;
 }
 
+__host__ __device__ constexpr int bwd_channels(int S) { return S <= 16 ? 64 : 32; }   // channels per CTA
+
 // db and dc: the channel tiles' sums in tile order (the first `nbc` CTAs); then the parameters' sums over the pieces.
 template <typename TI>
 __global__ void k_ssm_sums(SsmArgs a, unsigned nbc) {
@@ -389,8 +495,9 @@ __global__ void k_ssm_sums(SsmArgs a, unsigned nbc) {
         if (i >= tokens * 2 * GS) return;
         const size_t tok = i / (2 * GS);
         const int f = (int)(i - tok * 2 * GS), which = f / GS, gs = f - which * GS, g = gs / a.S, n = gs - g * a.S;
-        const int tpg = (a.D / a.G + SSM_CH - 1) / SSM_CH;
+        const int CH = bwd_channels(a.S), tpg = (a.D / a.G + CH - 1) / CH;
         float v = 0.f;
+#pragma unroll 8
         for (int k = 0; k < tpg; ++k) v += a.pbc[(((size_t)(g * tpg + k) * tokens + tok) * 2 + which) * a.S + n];
         st(static_cast<TI*>(which ? a.dc : a.db) + tok * GS + gs, v);
         return;
@@ -400,6 +507,7 @@ __global__ void k_ssm_sums(SsmArgs a, unsigned nbc) {
     const int units = a.ax.rows * a.units_row;
     if (i < DS) {
         float v = 0.f;
+#pragma unroll 8
         for (int u = 0; u < units; ++u) v += a.pA[u * DS + i];
         a.dA_log[i] = -expf(a.A_log[i]) * v;
     } else if (i < DS + 2 * (size_t)a.D) {
@@ -413,47 +521,46 @@ __global__ void k_ssm_sums(SsmArgs a, unsigned nbc) {
 }
 
 template <typename TI, int EL>
-cudaError_t run_bwd(const SsmArgs& a, unsigned grid, cudaStream_t st) {
-    const size_t smem = sizeof(typename BwdShape<EL>::Smem);
+cudaError_t run_bwd(const SsmArgs& a, cudaStream_t st) {
+    using Sh = BwdShape<TI, EL>;
+    const unsigned grid = (unsigned)(a.ax.rows * a.units_row) * ((a.D / a.G + Sh::CH - 1) / Sh::CH) * a.G;
     static SmemLimit limit;
-    const cudaError_t e = limit.set(reinterpret_cast<const void*>(k_ssm_bwd<TI, EL>), (int)smem);
+    const cudaError_t e = limit.set(reinterpret_cast<const void*>(k_ssm_bwd<TI, EL>), (int)sizeof(typename Sh::Smem));
     if (e != cudaSuccess) return e;
-    k_ssm_bwd<TI, EL><<<grid, SSM_T, smem, st>>>(a);
+    k_ssm_bwd<TI, EL><<<grid, Sh::RT + HT, sizeof(typename Sh::Smem), st>>>(a);
     return cudaSuccess;
 }
-template <typename TI, bool PIECES>
+template <typename TI, int EL>
+cudaError_t run_pieces(const SsmArgs& a, cudaStream_t st) {
+    const unsigned grid = (unsigned)(a.ax.rows * a.units_row) * ((a.D / a.G + SSM_CH - 1) / SSM_CH) * a.G;
+    k_ssm_bwd_pieces<TI, EL><<<grid, SSM_T, 0, st>>>(a);
+    return cudaSuccess;
+}
+template <bool PIECES, typename TI>
 cudaError_t run_states(const SsmArgs& a, cudaStream_t st) {
-    const unsigned grid = (unsigned)(a.ax.rows * a.units_row) * ssm_channel_tiles(a.D, a.G);
-    if (PIECES) {
-        if (a.S <= 8) k_ssm_bwd_pieces<TI, 2><<<grid, SSM_T, 0, st>>>(a);
-        else if (a.S <= 16) k_ssm_bwd_pieces<TI, 4><<<grid, SSM_T, 0, st>>>(a);
-        else if (a.S <= 32) k_ssm_bwd_pieces<TI, 8><<<grid, SSM_T, 0, st>>>(a);
-        else k_ssm_bwd_pieces<TI, 16><<<grid, SSM_T, 0, st>>>(a);
-        return cudaSuccess;
-    }
-    if (a.S <= 8) return run_bwd<TI, 2>(a, grid, st);
-    if (a.S <= 16) return run_bwd<TI, 4>(a, grid, st);
-    if (a.S <= 32) return run_bwd<TI, 8>(a, grid, st);
-    return run_bwd<TI, 16>(a, grid, st);
+    if (a.S <= 8) return PIECES ? run_pieces<TI, 2>(a, st) : run_bwd<TI, 2>(a, st);
+    if (a.S <= 16) return PIECES ? run_pieces<TI, 4>(a, st) : run_bwd<TI, 4>(a, st);
+    if (a.S <= 32) return PIECES ? run_pieces<TI, 8>(a, st) : run_bwd<TI, 8>(a, st);
+    return PIECES ? run_pieces<TI, 16>(a, st) : run_bwd<TI, 16>(a, st);
+}
+template <bool PIECES>
+cudaError_t launch(const char* name, const SsmArgs& a, int bf16, cudaStream_t st) {
+    cudaError_t r = cudaSuccess;
+    const cudaError_t e = traced_launch(name, st, [&] {
+        r = bf16 ? run_states<PIECES, __nv_bfloat16>(a, st) : run_states<PIECES, float>(a, st);
+    });
+    return r != cudaSuccess ? r : e;
 }
 
 }  // namespace
 
-int ssm_channel_tiles(int D, int G) { return (D / G + SSM_CH - 1) / SSM_CH * G; }
+int ssm_bwd_tiles(int D, int G, int S) { return (D / G + bwd_channels(S) - 1) / bwd_channels(S) * G; }
 
 cudaError_t launch_ssm_bwd_pieces(const SsmArgs& a, int bf16, cudaStream_t st) {
-    return traced_launch("k_ssm_bwd_pieces", st, [&] {
-        bf16 ? run_states<__nv_bfloat16, true>(a, st) : run_states<float, true>(a, st);
-    });
+    return launch<true>("k_ssm_bwd_pieces", a, bf16, st);
 }
 
-cudaError_t launch_ssm_bwd(const SsmArgs& a, int bf16, cudaStream_t st) {
-    cudaError_t r = cudaSuccess;
-    const cudaError_t e = traced_launch("k_ssm_bwd", st, [&] {
-        r = bf16 ? run_states<__nv_bfloat16, false>(a, st) : run_states<float, false>(a, st);
-    });
-    return r != cudaSuccess ? r : e;
-}
+cudaError_t launch_ssm_bwd(const SsmArgs& a, int bf16, cudaStream_t st) { return launch<false>("k_ssm_bwd", a, bf16, st); }
 
 cudaError_t launch_ssm_bwd_sums(const SsmArgs& a, int bf16, cudaStream_t st) {
     const size_t bc = (size_t)a.ax.rows * a.ax.len * 2 * a.G * a.S, params = (size_t)a.D * (a.S + 2);

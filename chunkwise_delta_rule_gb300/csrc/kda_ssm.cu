@@ -1,62 +1,141 @@
 // Selective state space scan (diagonal, input-dependent step), forward:
 //     delta = softplus(dt + dt_bias),  a = exp(-delta exp(A_log)),  u = delta x
 //     h_t = a h_{t-1} + u B_t,   y_t = (sum_n C_t[n] h_t[n] + d_skip x_t) silu(z_t)
-// Four lanes share a channel and hold its states in registers; a CTA walks 32 channels
-// through a time piece in tiles of 32 tokens. Four warps run the recurrence, four
-// others work around it, so that the recurrence never waits for them: while tile k
-// runs they copy tiles ahead into shared memory (asynchronously, each thread its own 8
-// channels of one token and 8 states of one row), form tile k + 1's steps once per
-// (token, channel), and sum, gate and store tile k - 1's outputs. One barrier per tile.
+// Four lanes share a channel and hold its states in registers; a CTA walks 64 channels
+// through a time piece in tiles of up to 32 tokens. Eight warps run the recurrence,
+// eight others work around it, so that the recurrence never waits for them: while tile
+// k runs they copy tiles ahead into shared memory (asynchronously, each thread its own
+// share), form tile k + 1's steps once per (token, channel), and sum, gate and store
+// tile k - 1's outputs. One barrier per tile.
+// Every lane needs its states' values of the rows b_t and c_t, the same for all
+// channels. Read from shared memory they bound the kernel: a load fills 128 bytes of
+// registers per cycle however few addresses it has, and the two rows are three quarters
+// of what the recurrence reads. So the tensor core spreads them: with A[m][k] = 1 where
+// k = m mod 4 and B[k][(token, e)] = the row's state 4 k' + e of lane group k, the product
+// holds in tensor memory, in each lane's own row, that lane's values of every token of
+// the tile, from where a warp reads 32 columns in one instruction. The product is exact:
+// a bf16 value has one non-zero term, an fp32 one is split into three bf16 parts that
+// add up to its 24 bits.
 // Per four states and token the recurrence takes 4 exponentials (16 cycles of a
-// scheduler's share at 32 per cycle and SM) and 8 paired multiply-adds (16 cycles):
-// both pipes are full, which bounds the kernel, not memory.
+// scheduler's share at 32 per cycle and SM) and 8 paired multiply-adds (16 cycles).
 // A long row is cut into time pieces when its channels alone do not fill the GPU:
 // a first pass forms each piece's end state from zero and its sum of delta (the
 // piece's decay is exp(A sum delta)); in the second pass each piece joins the
 // states of the pieces before it and runs its outputs.
 #include "kda_ssm.cuh"
+#include "tc.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int TT = 32;   // tokens per tile
-
 enum { OUT = 0, OUT_CKPT = 1, CKPT = 2, PIECE = 3 };
 
-constexpr int FT = 2 * SSM_T;   // threads: 128 for the recurrence, 128 around it
+constexpr int RT = 256;         // threads of the recurrence: 64 channels x 4 lanes
+constexpr int CH = RT / 4;
+constexpr int HT = 256;         // threads around it
 
 template <typename TI, int EL, int MODE>
 struct FwdShape {
-    static constexpr int NP = 4 * EL;
     static constexpr bool HAS_Y = MODE == OUT || MODE == OUT_CKPT, HAS_CK = MODE == OUT_CKPT || MODE == CKPT;
-    static constexpr int ROWS = HAS_Y ? 2 * TT : TT;                    // rows of b (and c) in a tile
-    static constexpr int NBC = (ROWS * (NP / 8) + SSM_T - 1) / SSM_T;   // their chunks of 8 per thread
-    static constexpr int NTOK = HAS_Y ? 3 : 2;                          // x, dt (and z)
-    // tiles in flight: the previous (its x and z), the current, the next, and those copied ahead
-    static constexpr int STAGES = sizeof(TI) == 2 ? (NP <= 32 ? 6 : 5) : (NP <= 16 ? 5 : 4);
+    static constexpr int NROW = HAS_Y ? 2 : 1;           // rows of a token: b (and c)
+    // tokens per tile: at most 256 columns of spread rows, two tiles of them in the SM's 512; fp32 tiles are half as long
+    // for their shared memory
+    static constexpr int MOST = sizeof(TI) == 2 ? 32 : 16, TT = 128 / EL < MOST ? 128 / EL : MOST;
+    static constexpr int COLS = TT * NROW * EL;          // columns of a tile
+    static constexpr int ALLOC = 2 * COLS < 32 ? 32 : 2 * COLS;
+    static constexpr int CP = TT * CH / HT;              // channels of a token per thread around the recurrence
+    static constexpr int PIECES = TT * NROW * 4;         // (token, row, lane group) of EL states
+    static constexpr int NTOK = HAS_Y ? 3 : 2;           // x, dt (and z)
+    // tiles copied: the previous (its x and z), the current, the next two, and with 16-bit elements one ahead
+    static constexpr int STAGES = sizeof(TI) == 2 ? 5 : 4;
+    static constexpr int ATOM = 16 * 128;                // 16 k-rows of 64 columns
+    static constexpr int OPB = (COLS + 63) / 64 * ATOM;  // bytes of a B operand
     struct Smem {
-        TI raw[STAGES][NTOK + NBC][SSM_T][8];
-        float4 du[2][TT][SSM_CH / 2];          // (delta, u) of two channels; see du_at
-        float b[2][TT][NP];
-        float c[2][HAS_Y ? TT : 1][NP];
-        float y[2][HAS_Y ? TT : 1][SSM_CH][4]; // the four lanes' parts; see y_at
+        unsigned char a[2 * ATOM];                       // 128 rows of ones
+        unsigned char b[3][OPB];
+        TI tok[STAGES][NTOK][HT][CP];
+        TI bc[STAGES][PIECES][EL];
+        float4 du[2][TT][CH / 2];                        // (delta, u) of two channels; see du_at
+        float y[2][HAS_Y ? TT : 1][CH][4];               // the four lanes' parts; see y_at
+        uint64_t bar[2];
+        uint32_t tmem;
     };
+    static_assert(CP % 2 == 0 && PIECES <= HT && sizeof(Smem) + 1024 <= 227 * 1024, "tile shape");
 };
 
-// Places of channel pairs and of channels in a token's row, permuted so that the eight threads of a quarter warp that
-// hold (two tokens) x (four groups of 8 channels) reach distinct banks.
-__device__ __forceinline__ int du_at(int tok, int pair) { return pair ^ ((pair >> 3) | (tok & 1) << 1); }
-__device__ __forceinline__ int y_at(int tok, int ch) { return ch ^ ((ch >> 3) | (tok & 1) << 2); }
+// Places of channel pairs and of channels in a token's row, permuted so that the eight threads of a quarter warp, which
+// hold a few neighbouring channels each, reach distinct banks.
+__device__ __forceinline__ int du_at(int pair) { return pair ^ ((pair >> 3) & 3); }
+__device__ __forceinline__ int y_at(int ch) { return ch ^ ((ch >> 3) & 7); }
+
+// Byte of column n of k-row k in an operand whose columns are contiguous (128-byte swizzle).
+__device__ __forceinline__ int op_at(int k, int n) {
+    const int byte = (n & 63) * 2;
+    return (n >> 6) * (16 * 128) + k * 128 + ((((byte >> 4) ^ (k & 7)) << 4) | (byte & 15));
+}
+
+// N columns of a warp's 32 lanes from tensor memory; the values are there after spread_wait on the same registers.
+template <int N>
+__device__ __forceinline__ void spread_load(uint32_t addr, uint32_t (&r)[N]) {
+    static_assert(N == 16 || N == 32, "columns per load");
+    if constexpr (N == 32) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16 % N]),
+              "=r"(r[17 % N]), "=r"(r[18 % N]), "=r"(r[19 % N]), "=r"(r[20 % N]), "=r"(r[21 % N]), "=r"(r[22 % N]),
+              "=r"(r[23 % N]), "=r"(r[24 % N]), "=r"(r[25 % N]), "=r"(r[26 % N]), "=r"(r[27 % N]), "=r"(r[28 % N]),
+              "=r"(r[29 % N]), "=r"(r[30 % N]), "=r"(r[31 % N])
+            : "r"(addr));
+    } else {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(addr));
+    }
+}
+template <int N>
+__device__ __forceinline__ void spread_wait(uint32_t (&r)[N]) {
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));   // no use of them may move before the wait
+}
+
+// A piece of EL states into k-rows l (bf16) or l, 4 + l, 8 + l (the three bf16 parts of fp32) from column n.
+template <int EL>
+__device__ __forceinline__ void put_piece(unsigned char* op, int l, int n, const __nv_bfloat16* v) {
+    constexpr int W = EL < 8 ? EL : 8;   // elements of one access
+    struct alignas(2 * W) Pack { uint32_t w[W / 2]; };
+#pragma unroll
+    for (int e = 0; e < EL; e += W) *reinterpret_cast<Pack*>(op + op_at(l, n + e)) = *reinterpret_cast<const Pack*>(v + e);
+}
+template <int EL>
+__device__ __forceinline__ void put_piece(unsigned char* op, int l, int n, const float* v) {
+#pragma unroll
+    for (int e = 0; e < EL; e += 2) {
+        float x0 = v[e], x1 = v[e + 1];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            // the upper 16 bits, exact, and what is left of the value (an infinity is whole in its first part)
+            const uint32_t h0 = __float_as_uint(x0) & 0xffff0000u, h1 = __float_as_uint(x1) & 0xffff0000u;
+            *reinterpret_cast<uint32_t*>(op + op_at(4 * j + l, n + e)) = h0 >> 16 | h1;
+            x0 = isinf(x0) ? 0.f : x0 - __uint_as_float(h0);
+            x1 = isinf(x1) ? 0.f : x1 - __uint_as_float(h1);
+        }
+    }
+}
 
 template <typename TI, int EL, int MODE>
-__global__ void __launch_bounds__(FT, 2) k_ssm_fwd(SsmArgs a) {
+__global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
     using Sh = FwdShape<TI, EL, MODE>;
-    constexpr int NP = Sh::NP, NBC = Sh::NBC, STAGES = Sh::STAGES, P = EL / 2;
+    constexpr int NROW = Sh::NROW, STAGES = Sh::STAGES, P = EL / 2, TT = Sh::TT, CP = Sh::CP, COLS = Sh::COLS;
     constexpr bool HAS_Y = Sh::HAS_Y, HAS_CK = Sh::HAS_CK;
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    typename Sh::Smem& sm = *reinterpret_cast<typename Sh::Smem*>(smem_raw);
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    typename Sh::Smem& sm = *reinterpret_cast<typename Sh::Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     if (blockIdx.x == 0 && MODE != PIECE) axis_check(a.ax, a.err);
-    const SsmPlace pl = ssm_place<SSM_CH>(a);
+    const SsmPlace pl = ssm_place<CH>(a);
     const size_t tok0 = (size_t)pl.row * a.ax.len;
     const size_t DS = (size_t)a.D * a.S;
     int t = pl.lo;
@@ -72,239 +151,287 @@ __global__ void __launch_bounds__(FT, 2) k_ssm_fwd(SsmArgs a) {
         }
     }
     const int first_tile = t, ntiles = (pl.hi - t + TT - 1) / TT;
-    const int tid = threadIdx.x & (SSM_T - 1);
+    // tensor memory, the operands' constant parts
+    if (threadIdx.x < 32) {
+        tc::tmem_alloc(&sm.tmem, Sh::ALLOC);
+        tc::tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        tc::mbar_init(&sm.bar[0], 1);
+        tc::mbar_init(&sm.bar[1], 1);
+        tc::fence_mbar_init();
+    }
+    for (int i = threadIdx.x; i < 16 * 128; i += RT + HT) {
+        const int k = i >> 7, m = i & 127;
+        *reinterpret_cast<__nv_bfloat16*>(sm.a + op_at(k, m)) = __float2bfloat16_rn(k < 12 && (m & 3) == (k & 3) ? 1.f : 0.f);
+    }
+    for (int i = threadIdx.x; i < 3 * Sh::OPB / 16; i += RT + HT) reinterpret_cast<uint4*>(&sm.b[0][0])[i] = make_uint4(0, 0, 0, 0);
+    tc::fence_async_smem();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sm.tmem;
 
-    if (threadIdx.x >= SSM_T) {
+    if (threadIdx.x >= RT) {
         // ---------------------------------------------------------------- around the recurrence
-        // this thread's part of a tile: one token, 8 channels; NBC chunks of 8 states of b's and c's rows
-        const int ptok = tid >> 2, pc = (tid & 3) * 8, pvalid = pl.nch - pc;
-        const TI* xp = static_cast<const TI*>(a.x) + tok0 * a.ldx + pl.c0 + pc;
-        const TI* dp = static_cast<const TI*>(a.dt) + tok0 * a.lddt + pl.c0 + pc;
-        const TI* zp = a.z ? static_cast<const TI*>(a.z) + tok0 * a.ldz + pl.c0 + pc : nullptr;
-        const TI* bp = static_cast<const TI*>(a.b) + tok0 * a.ldb + (size_t)pl.g * a.S;
-        const TI* cp = static_cast<const TI*>(a.c) + tok0 * a.ldc + (size_t)pl.g * a.S;
-        constexpr int NC = NP / 8;
+        // this thread's part of a tile: CP channels of one token; up to one piece of b's and c's rows
+        const int tid = threadIdx.x - RT;
+        constexpr int PER = CH / CP;   // threads per token
+        const int ptok = tid / PER, pc = (tid % PER) * CP, pvalid = pl.nch - pc;
+        const TI* src[3] = {static_cast<const TI*>(a.x) + tok0 * a.ldx + pl.c0 + pc,
+                            static_cast<const TI*>(a.dt) + tok0 * a.lddt + pl.c0 + pc,
+                            HAS_Y && a.z ? static_cast<const TI*>(a.z) + tok0 * a.ldz + pl.c0 + pc : nullptr};
+        const bool gate = src[2] != nullptr;
+        const size_t ld[3] = {a.ldx, a.lddt, a.ldz};
+        constexpr int SHIFT[3] = {SSM_X, SSM_DT, SSM_Z};
+        const int btok = tid / (4 * NROW), brow = (tid / 4) % NROW, bl = tid & 3;   // piece tid
+        const bool has_piece = tid < Sh::PIECES;
+        const TI* bsrc = brow ? static_cast<const TI*>(a.c) + tok0 * a.ldc + (size_t)pl.g * a.S
+                              : static_cast<const TI*>(a.b) + tok0 * a.ldb + (size_t)pl.g * a.S;
+        const size_t bld = brow ? a.ldc : a.ldb;
+        const int bhow = a.how >> (brow ? SSM_C : SSM_B) & 3, bvalid = a.S - bl * EL;
         auto fetch = [&](int k) {   // tile k of the piece into its stage
-            const int tb = first_tile + k * TT;
             if (k < ntiles) {
-                TI(*raw)[SSM_T][8] = sm.raw[k % STAGES];
+                const int tb = first_tile + k * TT, st = k % STAGES;
                 const size_t tt = min(tb + ptok, pl.hi - 1);
                 const int n = tb + ptok < pl.hi ? pvalid : 0;
-                copy8_async(raw[0][tid], xp + tt * a.ldx, n, a.how >> SSM_X & 3);
-                copy8_async(raw[1][tid], dp + tt * a.lddt, n, a.how >> SSM_DT & 3);
-                if (HAS_Y && zp) copy8_async(raw[2][tid], zp + tt * a.ldz, n, a.how >> SSM_Z & 3);
 #pragma unroll
-                for (int j = 0; j < NBC; ++j) {
-                    const int i = tid + j * SSM_T;
-                    if (i >= Sh::ROWS * NC) break;
-                    const bool isc = i >= TT * NC;
-                    const int r = isc ? i - TT * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
-                    const size_t tr = min(tb + tok, pl.hi - 1);
-                    const int m = tb + tok < pl.hi ? a.S - k8 : 0;
-                    const TI* src = isc ? cp + tr * a.ldc : bp + tr * a.ldb;
-                    copy8_async(raw[Sh::NTOK + j][tid], src + (m > 0 ? k8 : 0), m, a.how >> (isc ? SSM_C : SSM_B) & 3);
+                for (int q = 0; q < Sh::NTOK; ++q)
+                    if (q < 2 || gate) copy_row_async<TI, CP>(sm.tok[st][q][tid], src[q] + tt * ld[q], n, a.how >> SHIFT[q] & 3);
+                if (has_piece) {
+                    const size_t tr = min(tb + btok, pl.hi - 1);
+                    const int m = tb + btok < pl.hi ? bvalid : 0;
+                    copy_row_async<TI, EL>(sm.bc[st][tid], bsrc + tr * bld + (m > 0 ? bl * EL : 0), m, bhow);
                 }
             }
             copies_commit();
         };
-        for (int k = 0; k < STAGES - 2; ++k) fetch(k);
-        float bias[8], skip[8];
+        for (int k = 0; k < STAGES - 3; ++k) fetch(k);
+        float bias[CP], skip[CP];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < CP; ++i) {
             bias[i] = a.dt_bias && i < pvalid ? a.dt_bias[pl.c0 + pc + i] : 0.f;
             skip[i] = HAS_Y && a.d_skip && i < pvalid ? a.d_skip[pl.c0 + pc + i] : 0.f;
         }
-        // step k: tile k + 1's steps, tile k - 1's outputs (k = -1: the first tile's steps alone)
-        for (int k = -1; k <= ntiles; ++k) {
-            if (k + 1 < ntiles) {
-                const int w = (k + 1) & 1;
-                copies_wait<STAGES - 3>();
-                TI(*raw)[SSM_T][8] = sm.raw[(k + 1) % STAGES];
-                float x[8], dt[8];
-                load_row<8>(raw[0][tid], x, 8, true);
-                load_row<8>(raw[1][tid], dt, 8, true);
+        constexpr uint32_t idesc = tc::idesc_bf16_abmn(128, COLS);
+        const uint64_t adesc = tc::sdesc_mn(tc::smem_u32(sm.a), Sh::ATOM, 0);
+        // step k: tile k + 2's rows into their operand, tile k + 1's rows spread and its steps formed, tile k - 1's
+        // outputs stored
+        for (int k = -2; k <= ntiles; ++k) {
+            if (k + 1 >= 0 && k + 1 < ntiles && threadIdx.x < RT + 32) {
+                tc::fence_after_sync();
+                tc::mma_bf16_w(tmem + ((k + 1) & 1) * COLS, adesc, tc::sdesc_mn(tc::smem_u32(sm.b[(k + 1) % 3]), Sh::ATOM, 0), idesc, 0);
+                tc::mma_commit_w(&sm.bar[(k + 1) & 1]);
+            }
+            copies_wait<STAGES - 4>();
+            if (k + 2 < ntiles && has_piece) {
+                put_piece<EL>(sm.b[(k + 2) % 3], bl, (btok * NROW + brow) * EL, sm.bc[(k + 2) % STAGES][tid]);
+                tc::fence_async_smem();
+            }
+            if (k + 1 >= 0 && k + 1 < ntiles) {
+                const int w = (k + 1) & 1, st = (k + 1) % STAGES;
+                float x[CP], dt[CP];
+                load_part<CP>(sm.tok[st][0][tid], x);
+                load_part<CP>(sm.tok[st][1][tid], dt);
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
+                for (int i = 0; i < CP; i += 2) {
                     float2 dl = make_float2(dt[i] + bias[i], dt[i + 1] + bias[i + 1]);
                     if (a.softplus) dl = ssm_softplus2(dl);
                     const float2 u = mul2(dl, make_float2(x[i], x[i + 1]));
-                    sm.du[w][ptok][du_at(ptok, (pc + i) >> 1)] = make_float4(dl.x, u.x, dl.y, u.y);
-                }
-#pragma unroll
-                for (int j = 0; j < NBC; ++j) {
-                    const int i = tid + j * SSM_T;
-                    if (i >= Sh::ROWS * NC) break;
-                    const bool isc = i >= TT * NC;
-                    const int r = isc ? i - TT * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
-                    float v[8];
-                    load_row<8>(raw[Sh::NTOK + j][tid], v, 8, true);
-                    float4* dst = reinterpret_cast<float4*>(isc ? &sm.c[w][HAS_Y ? tok : 0][k8] : &sm.b[w][tok][k8]);
-                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    sm.du[w][ptok][du_at((pc + i) >> 1)] = make_float4(dl.x, u.x, dl.y, u.y);
                 }
             }
             if (HAS_Y && k > 0) {
-                const int tok = first_tile + (k - 1) * TT + ptok, w = (k - 1) & 1;
+                const int tok = first_tile + (k - 1) * TT + ptok, w = (k - 1) & 1, st = (k - 1) % STAGES;
                 if (tok < pl.hi && pvalid > 0) {
-                    TI(*raw)[SSM_T][8] = sm.raw[(k - 1) % STAGES];
-                    float o[8], x[8], z[8];
-                    load_row<8>(raw[0][tid], x, 8, true);
-                    if (zp) load_row<8>(raw[HAS_Y ? 2 : 0][tid], z, 8, true);
+                    float o[CP], x[CP], z[CP];
+                    load_part<CP>(sm.tok[st][0][tid], x);
+                    if (gate) load_part<CP>(sm.tok[st][HAS_Y ? 2 : 0][tid], z);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 v = *reinterpret_cast<const float4*>(sm.y[w][HAS_Y ? ptok : 0][y_at(ptok, pc + i)]);
+                    for (int i = 0; i < CP; ++i) {
+                        const float4 v = *reinterpret_cast<const float4*>(sm.y[w][HAS_Y ? ptok : 0][y_at(pc + i)]);
                         o[i] = fmaf(skip[i], x[i], (v.x + v.y) + (v.z + v.w));
-                        if (zp) o[i] *= z[i] * sigmoid_fast(z[i]);
+                        if (gate) o[i] *= z[i] * sigmoid_fast(z[i]);
                     }
-                    store_row<8>(static_cast<TI*>(a.y) + (tok0 + tok) * a.D + pl.c0 + pc, o, pvalid,
-                                 pvalid >= 8 && !(a.how >> SSM_OUT & 3));
+                    store_part<TI, CP>(static_cast<TI*>(a.y) + (tok0 + tok) * a.D + pl.c0 + pc, o, pvalid,
+                                       pvalid >= CP && !(a.how >> SSM_OUT & 3));
                 }
             }
             fetch(k + STAGES - 1);   // into the stage of tile k - 1, which was read last
-            if (k < ntiles) __syncthreads();
+            if (k < ntiles) {
+                tc::fence_before_sync();
+                __syncthreads();
+            }
         }
-        return;
-    }
-
-    // -------------------------------------------------------------------- the recurrence
-    const int l = tid & 3, ch = tid >> 2, n0 = l * EL, d = pl.c0 + ch;
-    const bool on = ch < pl.nch;
-    float A2[EL], h[EL], sd = 0.f;
-    load_states<EL>(a.A_log + (size_t)d * a.S, n0, a.S, on, A2);
+    } else {
+        // ---------------------------------------------------------------- the recurrence
+        const int tid = threadIdx.x, l = tid & 3, ch = tid >> 2, n0 = l * EL, d = pl.c0 + ch;
+        const bool on = ch < pl.nch;
+        const uint32_t lanes = tmem + ((uint32_t)((tid >> 5) & 3) << 21);   // this warp's quarter of the tensor memory's lanes
+        float A2[EL], h[EL], sd = 0.f;
+        load_states<EL>(a.A_log + (size_t)d * a.S, n0, a.S, on, A2);
 #pragma unroll
-    for (int e = 0; e < EL; ++e) A2[e] = on && n0 + e < a.S ? -expf(A2[e]) * LOG2E : 0.f;
-    const float* h0 = a.h0 ? a.h0 + (size_t)d * a.S : nullptr;
-    float* ht = a.ht && MODE != PIECE ? a.ht + (size_t)d * a.S : nullptr;
-    auto init_state = [&](int n) {
-        if (h0) {
-            load_states<EL>(h0 + n * DS, n0, a.S, on, h);
+        for (int e = 0; e < EL; ++e) A2[e] = on && n0 + e < a.S ? -expf(A2[e]) * LOG2E : 0.f;
+        const float* h0 = a.h0 ? a.h0 + (size_t)d * a.S : nullptr;
+        float* ht = a.ht && MODE != PIECE ? a.ht + (size_t)d * a.S : nullptr;
+        auto init_state = [&](int n) {
+            if (h0) {
+                load_states<EL>(h0 + n * DS, n0, a.S, on, h);
+            } else {
+#pragma unroll
+                for (int e = 0; e < EL; ++e) h[e] = 0.f;
+            }
+        };
+        if (ht && a.ax.cu) {   // sequences without tokens
+            for (int n = pl.unit; n < a.ax.N; n += pl.units) {
+                if (axis_cu(a.ax, n + 1) > axis_cu(a.ax, n)) continue;
+                init_state(n);
+                store_states<EL>(ht + n * DS, n0, a.S, on, h);
+            }
+        }
+        // the state entering this piece
+        if (MODE == PIECE ? s.first >= pl.lo : t == s.first) {
+            init_state(s.n);
         } else {
 #pragma unroll
             for (int e = 0; e < EL; ++e) h[e] = 0.f;
-        }
-    };
-    if (ht && a.ax.cu) {   // sequences without tokens
-        for (int n = pl.unit; n < a.ax.N; n += pl.units) {
-            if (axis_cu(a.ax, n + 1) > axis_cu(a.ax, n)) continue;
-            init_state(n);
-            store_states<EL>(ht + n * DS, n0, a.S, on, h);
-        }
-    }
-    // the state entering this piece
-    if (MODE == PIECE ? s.first >= pl.lo : t == s.first) {
-        init_state(s.n);
-    } else {
+            if (MODE != PIECE) {
+                // the earlier pieces of its sequence, joined in order
+                const int q = s.first / a.unit_len;
+                for (int r = q; r < pl.u; ++r) {
+                    const size_t ru = (size_t)pl.row * a.units_row + r;
+                    float hl[EL];
+                    load_states<EL>(a.hloc + ru * DS + (size_t)d * a.S, n0, a.S, on, hl);
+                    const float sum = on ? a.sdt[ru * a.D + d] : 0.f;
 #pragma unroll
-        for (int e = 0; e < EL; ++e) h[e] = 0.f;
-        if (MODE != PIECE) {
-            // the earlier pieces of its sequence, joined in order
-            const int q = s.first / a.unit_len;
-            for (int r = q; r < pl.u; ++r) {
-                const size_t ru = (size_t)pl.row * a.units_row + r;
-                float hl[EL];
-                load_states<EL>(a.hloc + ru * DS + (size_t)d * a.S, n0, a.S, on, hl);
-                const float sum = on ? a.sdt[ru * a.D + d] : 0.f;
-#pragma unroll
-                for (int e = 0; e < EL; ++e) h[e] = r == q ? hl[e] : fmaf(ex2(A2[e] * sum), h[e], hl[e]);
+                    for (int e = 0; e < EL; ++e) h[e] = r == q ? hl[e] : fmaf(ex2(A2[e] * sum), h[e], hl[e]);
+                }
             }
         }
-    }
-    constexpr int N = EL <= 4 ? 4 : 16 / EL;   // tokens whose operands are in registers together
-    struct Operands {
-        float2 du[N], b[N][P], c[HAS_Y ? N : 1][P];
-    };
-    auto load = [&](int w, int i, int n, Operands& o) {
+        constexpr int N = 16 / EL;              // tokens of a batch of operands
+        constexpr int NCOL = N * NROW * EL;     // their columns
+        const int my_du = du_at(ch >> 1), my_y = y_at(ch);
+        auto load_du = [&](int w, int i, float2(&du)[N]) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            if (j >= n) break;
-            o.du[j] = reinterpret_cast<const float2*>(&sm.du[w][i + j][du_at(i + j, ch >> 1)])[ch & 1];
-            float v[EL];
-            lds_states<EL>(&sm.b[w][i + j][n0], v);
+            for (int j = 0; j < N; ++j) du[j] = reinterpret_cast<const float2*>(&sm.du[w][min(i + j, TT - 1)][my_du])[ch & 1];
+        };
+        // the first n tokens of a batch from tile row i
+        auto run_tokens = [&](int w, int i, int n, const float2(&du)[N], const uint32_t(&bc)[NCOL]) {
+            float2 acc[N];
 #pragma unroll
-            for (int e = 0; e < P; ++e) o.b[j][e] = make_float2(v[2 * e], v[2 * e + 1]);
+            for (int j = 0; j < N; ++j) {
+                if (j >= n) break;
+                const float2 dl = make_float2(du[j].x, du[j].x), u = make_float2(du[j].y, du[j].y);
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const int col = j * NROW * EL + 2 * e;
+                    const float2 b = make_float2(__uint_as_float(bc[col]), __uint_as_float(bc[col + 1]));
+                    const float2 g = mul2(dl, make_float2(A2[2 * e], A2[2 * e + 1]));
+                    const float2 hn = fma2(make_float2(ex2(g.x), ex2(g.y)), make_float2(h[2 * e], h[2 * e + 1]), mul2(u, b));
+                    h[2 * e] = hn.x;
+                    h[2 * e + 1] = hn.y;
+                    if (HAS_Y) {
+                        const int cc = HAS_Y ? col + EL : 0;
+                        const float2 c = make_float2(__uint_as_float(bc[cc]), __uint_as_float(bc[cc + 1]));
+                        acc[j] = e == 0 ? mul2(hn, c) : fma2(hn, c, acc[j]);
+                    }
+                }
+                if (MODE == PIECE) sd += du[j].x;
+            }
             if (HAS_Y) {
-                lds_states<EL>(&sm.c[w][HAS_Y ? i + j : 0][n0], v);
 #pragma unroll
-                for (int e = 0; e < P; ++e) o.c[HAS_Y ? j : 0][e] = make_float2(v[2 * e], v[2 * e + 1]);
+                for (int j = 0; j < N; ++j)
+                    if (j < n) sm.y[w][HAS_Y ? i + j : 0][my_y][l] = acc[j].x + acc[j].y;
             }
-        }
-    };
-    auto run_tokens = [&](int w, int i, int n, const Operands& o) {
-        float2 acc[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            if (j >= n) break;
-            const float2 dl = make_float2(o.du[j].x, o.du[j].x), u = make_float2(o.du[j].y, o.du[j].y);
-#pragma unroll
-            for (int e = 0; e < P; ++e) {
-                const float2 g = mul2(dl, make_float2(A2[2 * e], A2[2 * e + 1]));
-                const float2 hn = fma2(make_float2(ex2(g.x), ex2(g.y)), make_float2(h[2 * e], h[2 * e + 1]), mul2(u, o.b[j][e]));
-                h[2 * e] = hn.x;
-                h[2 * e + 1] = hn.y;
-                if (HAS_Y) acc[j] = e == 0 ? mul2(hn, o.c[HAS_Y ? j : 0][e]) : fma2(hn, o.c[HAS_Y ? j : 0][e], acc[j]);
+        };
+        auto checkpoint = [&](int tok) {
+            const size_t slot = (size_t)pl.row * ((a.ax.len + SSM_CKPT - 1) / SSM_CKPT) + tok / SSM_CKPT;
+            store_states<EL>(a.ckpt + slot * DS + (size_t)d * a.S, n0, a.S, on, h);
+        };
+        bool lost = false;   // a wait for the tensor core gave up: the results are not valid, and no further wait is tried
+        tc::fence_before_sync();
+        __syncthreads();     // the first tile's rows in their operand
+        __syncthreads();     // the first tile's steps
+        for (int k = 0; k < ntiles; ++k) {
+            const int tb = first_tile + k * TT, te = min(tb + TT, pl.hi), w = k & 1;
+            if (!lost && !tc::mbar_wait(&sm.bar[w], (k >> 1) & 1)) {
+                lost = true;
+                if (a.err) atomicOr(a.err, 2);
             }
-            if (MODE == PIECE) sd += o.du[j].x;
-        }
-        if (HAS_Y) {
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (j < n) sm.y[w][HAS_Y ? i + j : 0][y_at(i + j, ch)][l] = acc[j].x + acc[j].y;
-        }
-    };
-    auto checkpoint = [&](int tok) {
-        const size_t slot = (size_t)pl.row * ((a.ax.len + SSM_CKPT - 1) / SSM_CKPT) + tok / SSM_CKPT;
-        store_states<EL>(a.ckpt + slot * DS + (size_t)d * a.S, n0, a.S, on, h);
-    };
-    __syncthreads();   // the first tile's steps
-    for (int k = 0; k < ntiles; ++k) {
-        const int tb = first_tile + k * TT, te = min(tb + TT, pl.hi), w = k & 1;
-        t = tb;
-        if (MODE != PIECE && t == s.end) {
-            if (ht) store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
-            s = seq_at(a.ax, pl.row, t);
-            init_state(s.n);
-        }
-        if (te - tb == TT && (MODE == PIECE || s.end >= te)) {
-            // a whole tile of one sequence: the next tokens' operands are read while these run
-            Operands o[2];
-            load(w, 0, N, o[0]);
-#pragma unroll
-            for (int i = 0; i < TT; i += N) {
-                if (HAS_CK && i % SSM_CKPT == 0) checkpoint(tb + i);
-                if (i + N < TT) load(w, i + N, N, o[(i / N + 1) & 1]);
-                run_tokens(w, i, N, o[(i / N) & 1]);
+            tc::fence_after_sync();
+            const uint32_t cols = lanes + w * COLS;
+            t = tb;
+            if (MODE != PIECE && t == s.end) {
+                if (ht) store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
+                s = seq_at(a.ax, pl.row, t);
+                init_state(s.n);
             }
-        } else {
-            while (t < te) {
-                if (MODE != PIECE && t == s.end) {
-                    if (ht) store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
-                    s = seq_at(a.ax, pl.row, t);
-                    init_state(s.n);
+            if (te - tb == TT && (MODE == PIECE || s.end >= te)) {
+                // a whole tile of one sequence: the next tokens' operands are read while these run
+                uint32_t bc[2][NCOL];
+                float2 du[2][N];
+                spread_load<NCOL>(cols, bc[0]);
+                load_du(w, 0, du[0]);
+#pragma unroll
+                for (int i = 0; i < TT; i += N) {
+                    const int cur = (i / N) & 1;
+                    if (HAS_CK && i % SSM_CKPT == 0 && (TT >= SSM_CKPT || (tb + i) % SSM_CKPT == 0)) checkpoint(tb + i);
+                    spread_wait<NCOL>(bc[cur]);
+                    if (i + N < TT) {
+                        spread_load<NCOL>(cols + (i + N) * NROW * EL, bc[cur ^ 1]);
+                        load_du(w, i + N, du[cur ^ 1]);
+                    }
+                    run_tokens(w, i, N, du[cur], bc[cur]);
                 }
-                if (HAS_CK && t % SSM_CKPT == 0) checkpoint(t);
-                int run = MODE == PIECE ? te : min(te, s.end);
-                if (HAS_CK) run = min(run, (t | (SSM_CKPT - 1)) + 1);
-                Operands o;
-                if (t + N <= run) {
-                    load(w, t - tb, N, o);
-                    run_tokens(w, t - tb, N, o);
-                    t += N;
-                } else {
-                    load(w, t - tb, 1, o);
-                    run_tokens(w, t - tb, 1, o);
-                    ++t;
+            } else {
+                while (t < te) {
+                    if (MODE != PIECE && t == s.end) {
+                        if (ht) store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
+                        s = seq_at(a.ax, pl.row, t);
+                        init_state(s.n);
+                    }
+                    if (HAS_CK && t % SSM_CKPT == 0) checkpoint(t);
+                    int run = MODE == PIECE ? te : min(te, s.end);
+                    if (HAS_CK) run = min(run, (t | (SSM_CKPT - 1)) + 1);
+                    uint32_t bc[NCOL];
+                    float2 du[N];
+                    // a batch that starts near the tile's end would read past its columns: it starts earlier there
+                    const int at = min(t - tb, TT - N);
+                    spread_load<NCOL>(cols + at * NROW * EL, bc);
+                    load_du(w, at, du);
+                    spread_wait<NCOL>(bc);
+                    const int skip = t - tb - at;
+                    if (skip == 0 && t + N <= run) {
+                        run_tokens(w, at, N, du, bc);
+                        t += N;
+                    } else {
+                        // one token: the batch's entry `skip` brought to its front
+#pragma unroll
+                        for (int j = 1; j < N; ++j)
+                            if (j == skip) {
+                                du[0] = du[j];
+#pragma unroll
+                                for (int e = 0; e < NROW * EL; ++e) bc[e] = bc[j * NROW * EL + e];
+                            }
+                        run_tokens(w, t - tb, 1, du, bc);
+                        ++t;
+                    }
                 }
             }
+            tc::fence_before_sync();
+            __syncthreads();
         }
-        __syncthreads();
+        if (pl.lo < pl.hi || !a.ax.cu) {
+            if (MODE == PIECE) {
+                store_states<EL>(a.hloc + pl.unit * DS + (size_t)d * a.S, n0, a.S, on, h);
+                if (on && l == 0) a.sdt[(size_t)pl.unit * a.D + d] = sd;
+            } else if (ht && pl.hi == s.end) {
+                store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
+            }
+        }
     }
-    if (pl.lo >= pl.hi && a.ax.cu) return;
-    if (MODE == PIECE) {
-        store_states<EL>(a.hloc + pl.unit * DS + (size_t)d * a.S, n0, a.S, on, h);
-        if (on && l == 0) a.sdt[(size_t)pl.unit * a.D + d] = sd;
-    } else if (ht && pl.hi == s.end) {
-        store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
-    }
+    __syncthreads();
+    if (threadIdx.x < 32) tc::tmem_dealloc(tmem, Sh::ALLOC);
 }
 
 // A lane's EL states of a row of b or c: one access of EL elements where the row is aligned to it.
@@ -399,11 +526,11 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_step(SsmArgs a) {
     }
 }
 
-int fwd_tiles(int D, int G) { return (D / G + SSM_CH - 1) / SSM_CH * G; }
+int fwd_tiles(int D, int G) { return (D / G + CH - 1) / CH * G; }
 
 template <typename TI, int EL>
 void run_step(const SsmArgs& a, cudaStream_t st) {
-    const unsigned tiles = fwd_tiles(a.D, a.G);
+    const unsigned tiles = (a.D / a.G + SSM_CH - 1) / SSM_CH * a.G;
     // four sequences per thread once that still leaves every SM two CTAs
     if ((long long)tiles * (a.ax.N / 4) >= 2 * sm_count()) k_ssm_step<TI, EL, 4><<<tiles * ((a.ax.N + 3) / 4), SSM_T, 0, st>>>(a);
     else k_ssm_step<TI, EL, 1><<<tiles * a.ax.N, SSM_T, 0, st>>>(a);
@@ -412,11 +539,11 @@ void run_step(const SsmArgs& a, cudaStream_t st) {
 template <typename TI, int EL, int MODE>
 cudaError_t run_one(const SsmArgs& a, cudaStream_t st) {
     const unsigned grid = (unsigned)(a.ax.rows * a.units_row) * fwd_tiles(a.D, a.G);
-    const int smem = (int)sizeof(typename FwdShape<TI, EL, MODE>::Smem);
+    const int smem = (int)sizeof(typename FwdShape<TI, EL, MODE>::Smem) + 1024;
     static SmemLimit limit;
     const cudaError_t e = limit.set(reinterpret_cast<const void*>(k_ssm_fwd<TI, EL, MODE>), smem);
     if (e != cudaSuccess) return e;
-    k_ssm_fwd<TI, EL, MODE><<<grid, FT, smem, st>>>(a);
+    k_ssm_fwd<TI, EL, MODE><<<grid, RT + HT, smem, st>>>(a);
     return cudaSuccess;
 }
 template <typename TI, int EL>
@@ -458,8 +585,7 @@ cudaError_t launch(const char* name, const SsmArgs& a, int bf16, int mode, cudaS
 int ssm_units(int rows, int len, int D, int G, int S, bool backward) {
     // pieces only while the channels and rows alone leave SMs idle; a piece is at least 128 tokens
     const long long ctas = (long long)rows * (backward ? ssm_bwd_tiles(D, G, S) : fwd_tiles(D, G));
-    const long long full = backward ? 2 * sm_count() / 3 : sm_count(), want = (backward ? 2LL : 4LL) * sm_count();
-    long long units = ctas >= full ? 1 : want / ctas;
+    long long units = ctas >= 2 * sm_count() / 3 ? 1 : 2LL * sm_count() / ctas;
     const long long most = (len + 127) / 128;
     if (units > most) units = most;
     return units < 1 ? 1 : (int)units;

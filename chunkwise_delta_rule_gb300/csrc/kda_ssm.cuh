@@ -110,4 +110,21 @@ __device__ __forceinline__ void lds_states(const float* p, float (&x)[EL]) {
     }
 }
 
+// A thread's V channels of a token: from its place in shared memory, and to a row of an output.
+template <int V, typename TI>
+__device__ __forceinline__ void load_part(const TI* p, float (&x)[V]) {
+    if constexpr (V * sizeof(TI) >= 16) load_row<V>(p, x, V, true);
+    else unpack<V>(load_raw<TI, V>(p), x);
+}
+template <typename TI, int V>
+__device__ __forceinline__ void store_part(TI* p, const float (&x)[V], int valid, bool whole) {
+    if (whole) {
+        store_values<V>(p, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < valid) st(p + i, x[i]);
+    }
+}
+
 }  // namespace kda

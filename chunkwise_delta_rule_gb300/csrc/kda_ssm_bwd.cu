@@ -55,17 +55,6 @@ __device__ __forceinline__ void named_barrier(int id, int count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-template <typename TI, int V>
-__device__ __forceinline__ void store_part(TI* p, const float (&x)[V], int valid, bool whole) {
-    if (whole) {
-        store_values<V>(p, x);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < valid) st(p + i, x[i]);
-    }
-}
-
 template <typename TI, int EL>
 __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArgs a) {
     using Sh = BwdShape<TI, EL>;

@@ -46,27 +46,27 @@ struct FwdShape {
     static constexpr int CP = TT * CH / HT;              // channels of a token per thread around the recurrence
     static constexpr int PIECES = TT * NROW * 4;         // (token, row, lane group) of EL states
     static constexpr int NTOK = HAS_Y ? 3 : 2;           // x, dt (and z)
-    // tiles copied: the previous (its x and z), the current, the next two, and with 16-bit elements one ahead
+    // tiles copied: the previous (its x and z), the current, the next two, and one ahead where there is room
     static constexpr int STAGES = sizeof(TI) == 2 ? 5 : 4;
     static constexpr int ATOM = 16 * 128;                // 16 k-rows of 64 columns
     static constexpr int OPB = (COLS + 63) / 64 * ATOM;  // bytes of a B operand
     struct Smem {
         unsigned char a[2 * ATOM];                       // 128 rows of ones
-        unsigned char b[3][OPB];
+        unsigned char b[2][OPB];
         TI tok[STAGES][NTOK][HT][CP];
         TI bc[STAGES][PIECES][EL];
-        float4 du[2][TT][CH / 2];                        // (delta, u) of two channels; see du_at
-        float y[2][HAS_Y ? TT : 1][CH][4];               // the four lanes' parts; see y_at
+        float2 du[2][TT][CH];                            // delta, u
+        float y[2][HAS_Y ? TT : 1][CH][4];               // the four lanes' parts; see ch_at
         uint64_t bar[2];
         uint32_t tmem;
     };
     static_assert(CP % 2 == 0 && PIECES <= HT && sizeof(Smem) + 1024 <= 227 * 1024, "tile shape");
 };
 
-// Places of channel pairs and of channels in a token's row, permuted so that the eight threads of a quarter warp, which
-// hold a few neighbouring channels each, reach distinct banks.
-__device__ __forceinline__ int du_at(int pair) { return pair ^ ((pair >> 3) & 3); }
-__device__ __forceinline__ int y_at(int ch) { return ch ^ ((ch >> 3) & 7); }
+// Place of a channel in a token's row, permuted so that the eight threads of a quarter warp, which hold a few
+// neighbouring channels each, reach distinct banks.
+__device__ __forceinline__ int ch_at(int ch) { return ch ^ ((ch >> 3) & 7); }
+__device__ __forceinline__ int du_at(int ch) { return ch ^ ((ch >> 3) & 6); }   // pairs stay together
 
 // Byte of column n of k-row k in an operand whose columns are contiguous (128-byte swizzle).
 __device__ __forceinline__ int op_at(int k, int n) {
@@ -74,7 +74,7 @@ __device__ __forceinline__ int op_at(int k, int n) {
     return (n >> 6) * (16 * 128) + k * 128 + ((((byte >> 4) ^ (k & 7)) << 4) | (byte & 15));
 }
 
-// N columns of a warp's 32 lanes from tensor memory; the values are there after spread_wait on the same registers.
+// N columns of a warp's 32 lanes from tensor memory; the values are there after tmem_wait_ld.
 template <int N>
 __device__ __forceinline__ void spread_load(uint32_t addr, uint32_t (&r)[N]) {
     static_assert(N == 16 || N == 32, "columns per load");
@@ -96,13 +96,6 @@ __device__ __forceinline__ void spread_load(uint32_t addr, uint32_t (&r)[N]) {
             : "r"(addr));
     }
 }
-template <int N>
-__device__ __forceinline__ void spread_wait(uint32_t (&r)[N]) {
-    tc::tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));   // no use of them may move before the wait
-}
-
 // A piece of EL states into k-rows l (bf16) or l, 4 + l, 8 + l (the three bf16 parts of fp32) from column n.
 template <int EL>
 __device__ __forceinline__ void put_piece(unsigned char* op, int l, int n, const __nv_bfloat16* v) {
@@ -165,7 +158,7 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
         const int k = i >> 7, m = i & 127;
         *reinterpret_cast<__nv_bfloat16*>(sm.a + op_at(k, m)) = __float2bfloat16_rn(k < 12 && (m & 3) == (k & 3) ? 1.f : 0.f);
     }
-    for (int i = threadIdx.x; i < 3 * Sh::OPB / 16; i += RT + HT) reinterpret_cast<uint4*>(&sm.b[0][0])[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < 2 * Sh::OPB / 16; i += RT + HT) reinterpret_cast<uint4*>(&sm.b[0][0])[i] = make_uint4(0, 0, 0, 0);
     tc::fence_async_smem();
     tc::fence_before_sync();
     __syncthreads();
@@ -190,19 +183,23 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
                               : static_cast<const TI*>(a.b) + tok0 * a.ldb + (size_t)pl.g * a.S;
         const size_t bld = brow ? a.ldc : a.ldb;
         const int bhow = a.how >> (brow ? SSM_C : SSM_B) & 3, bvalid = a.S - bl * EL;
-        auto fetch = [&](int k) {   // tile k of the piece into its stage
-            if (k < ntiles) {
-                const int tb = first_tile + k * TT, st = k % STAGES;
-                const size_t tt = min(tb + ptok, pl.hi - 1);
-                const int n = tb + ptok < pl.hi ? pvalid : 0;
+        // tile k of the piece into its stage; tiles are fetched in order, the pointers move along
 #pragma unroll
-                for (int q = 0; q < Sh::NTOK; ++q)
-                    if (q < 2 || gate) copy_row_async<TI, CP>(sm.tok[st][q][tid], src[q] + tt * ld[q], n, a.how >> SHIFT[q] & 3);
-                if (has_piece) {
-                    const size_t tr = min(tb + btok, pl.hi - 1);
-                    const int m = tb + btok < pl.hi ? bvalid : 0;
-                    copy_row_async<TI, EL>(sm.bc[st][tid], bsrc + tr * bld + (m > 0 ? bl * EL : 0), m, bhow);
+        for (int q = 0; q < Sh::NTOK; ++q) src[q] += (size_t)(first_tile + ptok) * ld[q];
+        bsrc += (size_t)(first_tile + btok) * bld + bl * EL;
+        const size_t step[3] = {TT * a.ldx, TT * a.lddt, TT * a.ldz}, bstep = TT * bld;
+        int left = pl.hi - first_tile;   // tokens from the next tile to fetch on
+        auto fetch = [&](int k) {
+            if (left > 0) {
+                const int st = k % STAGES, n = ptok < left ? pvalid : 0, m = btok < left ? bvalid : 0;
+#pragma unroll
+                for (int q = 0; q < Sh::NTOK; ++q) {
+                    if (q < 2 || gate) copy_row_async<TI, CP>(sm.tok[st][q][tid], src[q], n, a.how >> SHIFT[q] & 3);
+                    src[q] += step[q];
                 }
+                if (has_piece) copy_row_async<TI, EL>(sm.bc[st][tid], bsrc, m, bhow);
+                bsrc += bstep;
+                left -= TT;
             }
             copies_commit();
         };
@@ -215,19 +212,33 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
         }
         constexpr uint32_t idesc = tc::idesc_bf16_abmn(128, COLS);
         const uint64_t adesc = tc::sdesc_mn(tc::smem_u32(sm.a), Sh::ATOM, 0);
-        // step k: tile k + 2's rows into their operand, tile k + 1's rows spread and its steps formed, tile k - 1's
-        // outputs stored
+        // step k: tile k + 1's rows spread, tile k - 1's outputs stored, tile k + 1's steps formed, tile k + 2's rows into the
+        // operand that tile k's left
+        bool lost = false;
         for (int k = -2; k <= ntiles; ++k) {
             if (k + 1 >= 0 && k + 1 < ntiles && threadIdx.x < RT + 32) {
                 tc::fence_after_sync();
-                tc::mma_bf16_w(tmem + ((k + 1) & 1) * COLS, adesc, tc::sdesc_mn(tc::smem_u32(sm.b[(k + 1) % 3]), Sh::ATOM, 0), idesc, 0);
+                tc::mma_bf16_w(tmem + ((k + 1) & 1) * COLS, adesc, tc::sdesc_mn(tc::smem_u32(sm.b[(k + 1) & 1]), Sh::ATOM, 0), idesc, 0);
                 tc::mma_commit_w(&sm.bar[(k + 1) & 1]);
             }
-            copies_wait<STAGES - 4>();
-            if (k + 2 < ntiles && has_piece) {
-                put_piece<EL>(sm.b[(k + 2) % 3], bl, (btok * NROW + brow) * EL, sm.bc[(k + 2) % STAGES][tid]);
-                tc::fence_async_smem();
+            if (HAS_Y && k > 0) {
+                const int tok = first_tile + (k - 1) * TT + ptok, w = (k - 1) & 1, st = (k - 1) % STAGES;
+                if (tok < pl.hi && pvalid > 0) {
+                    float o[CP], x[CP], z[CP];
+                    load_part<CP>(sm.tok[st][0][tid], x);
+                    if (gate) load_part<CP>(sm.tok[st][HAS_Y ? 2 : 0][tid], z);
+#pragma unroll
+                    for (int i = 0; i < CP; ++i) {
+                        const float4 v = *reinterpret_cast<const float4*>(sm.y[w][HAS_Y ? ptok : 0][ch_at(pc + i)]);
+                        o[i] = fmaf(skip[i], x[i], (v.x + v.y) + (v.z + v.w));
+                        if (gate) o[i] *= z[i] * sigmoid_fast(z[i]);
+                    }
+                    store_part<TI, CP>(static_cast<TI*>(a.y) + (tok0 + tok) * a.D + pl.c0 + pc, o, pvalid,
+                                       pvalid >= CP && !(a.how >> SSM_OUT & 3));
+                }
             }
+            fetch(k + STAGES - 1);   // into the stage of tile k - 1, which was read last
+            copies_wait<STAGES - 3>();
             if (k + 1 >= 0 && k + 1 < ntiles) {
                 const int w = (k + 1) & 1, st = (k + 1) % STAGES;
                 float x[CP], dt[CP];
@@ -238,26 +249,15 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
                     float2 dl = make_float2(dt[i] + bias[i], dt[i + 1] + bias[i + 1]);
                     if (a.softplus) dl = ssm_softplus2(dl);
                     const float2 u = mul2(dl, make_float2(x[i], x[i + 1]));
-                    sm.du[w][ptok][du_at((pc + i) >> 1)] = make_float4(dl.x, u.x, dl.y, u.y);
+                    *reinterpret_cast<float4*>(&sm.du[w][ptok][du_at(pc + i)]) = make_float4(dl.x, u.x, dl.y, u.y);
                 }
             }
-            if (HAS_Y && k > 0) {
-                const int tok = first_tile + (k - 1) * TT + ptok, w = (k - 1) & 1, st = (k - 1) % STAGES;
-                if (tok < pl.hi && pvalid > 0) {
-                    float o[CP], x[CP], z[CP];
-                    load_part<CP>(sm.tok[st][0][tid], x);
-                    if (gate) load_part<CP>(sm.tok[st][HAS_Y ? 2 : 0][tid], z);
-#pragma unroll
-                    for (int i = 0; i < CP; ++i) {
-                        const float4 v = *reinterpret_cast<const float4*>(sm.y[w][HAS_Y ? ptok : 0][y_at(pc + i)]);
-                        o[i] = fmaf(skip[i], x[i], (v.x + v.y) + (v.z + v.w));
-                        if (gate) o[i] *= z[i] * sigmoid_fast(z[i]);
-                    }
-                    store_part<TI, CP>(static_cast<TI*>(a.y) + (tok0 + tok) * a.D + pl.c0 + pc, o, pvalid,
-                                       pvalid >= CP && !(a.how >> SSM_OUT & 3));
-                }
+            if (k + 2 < ntiles && has_piece) {
+                // tile k's product was issued a step ago (its results are being read): it has read its operand
+                if (k >= 0 && !lost) lost = !tc::mbar_wait(&sm.bar[k & 1], (k >> 1) & 1);
+                put_piece<EL>(sm.b[k & 1], bl, (btok * NROW + brow) * EL, sm.bc[(k + 2) % STAGES][tid]);
+                tc::fence_async_smem();
             }
-            fetch(k + STAGES - 1);   // into the stage of tile k - 1, which was read last
             if (k < ntiles) {
                 tc::fence_before_sync();
                 __syncthreads();
@@ -310,10 +310,10 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
         }
         constexpr int N = 16 / EL;              // tokens of a batch of operands
         constexpr int NCOL = N * NROW * EL;     // their columns
-        const int my_du = du_at(ch >> 1), my_y = y_at(ch);
+        const int my_ch = ch_at(ch), my_du = du_at(ch);
         auto load_du = [&](int w, int i, float2(&du)[N]) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) du[j] = reinterpret_cast<const float2*>(&sm.du[w][min(i + j, TT - 1)][my_du])[ch & 1];
+            for (int j = 0; j < N; ++j) du[j] = sm.du[w][i + j][my_du];
         };
         // the first n tokens of a batch from tile row i
         auto run_tokens = [&](int w, int i, int n, const float2(&du)[N], const uint32_t(&bc)[NCOL]) {
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
             if (HAS_Y) {
 #pragma unroll
                 for (int j = 0; j < N; ++j)
-                    if (j < n) sm.y[w][HAS_Y ? i + j : 0][my_y][l] = acc[j].x + acc[j].y;
+                    if (j < n) sm.y[w][HAS_Y ? i + j : 0][my_ch][l] = acc[j].x + acc[j].y;
             }
         };
         auto checkpoint = [&](int tok) {
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
                 for (int i = 0; i < TT; i += N) {
                     const int cur = (i / N) & 1;
                     if (HAS_CK && i % SSM_CKPT == 0 && (TT >= SSM_CKPT || (tb + i) % SSM_CKPT == 0)) checkpoint(tb + i);
-                    spread_wait<NCOL>(bc[cur]);
+                    tc::tmem_wait_ld();
                     if (i + N < TT) {
                         spread_load<NCOL>(cols + (i + N) * NROW * EL, bc[cur ^ 1]);
                         load_du(w, i + N, du[cur ^ 1]);
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
                     const int at = min(t - tb, TT - N);
                     spread_load<NCOL>(cols + at * NROW * EL, bc);
                     load_du(w, at, du);
-                    spread_wait<NCOL>(bc);
+                    tc::tmem_wait_ld();
                     const int skip = t - tb - at;
                     if (skip == 0 && t + N <= run) {
                         run_tokens(w, at, N, du, bc);

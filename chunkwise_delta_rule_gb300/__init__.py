@@ -19,10 +19,7 @@ from .ops import (  # noqa: F401
     make_problem,
 )
 from .layer import (  # noqa: F401
-    ConvProblem,
-    NormProblem,
     SsmGrads,
-    SsmProblem,
     kda_conv_bwd,
     kda_conv_fwd,
     kda_conv_workspace_size,

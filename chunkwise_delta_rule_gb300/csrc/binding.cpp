@@ -1,0 +1,269 @@
+// Python binding of the layer operators (include/kda.h): argument checks, output
+// allocation and the call, in one step each. A decoding step takes a few
+// microseconds on the device; the same marshalling written in Python takes 10 to
+// 20 microseconds of host time per call and bounds it.
+#include <c10/cuda/CUDAStream.h>
+#include <torch/extension.h>
+
+#include <optional>
+
+#include "../../include/kda.h"
+
+namespace py = pybind11;
+using at::Tensor;
+using OptT = std::optional<Tensor>;
+
+namespace {
+
+void need(bool ok, const char* msg) {
+    if (!ok) throw py::value_error(msg);
+}
+[[noreturn]] void refuse(const char* name, const char* what, at::IntArrayRef shape, at::ScalarType type) {
+    std::ostringstream s;
+    s << name << " must be a " << what << "CUDA tensor " << shape << ", " << type;
+    throw py::value_error(s.str());
+}
+
+// An io type's kda_dtype.
+kda_dtype io_of(const Tensor& t, const char* msg) {
+    const at::ScalarType s = t.scalar_type();
+    need(s == at::kBFloat16 || s == at::kFloat, msg);
+    return s == at::kBFloat16 ? KDA_BF16 : KDA_FP32;
+}
+
+void* dense(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type) {
+    if (t.scalar_type() != type || t.sizes() != shape || !t.is_cuda() || !t.is_contiguous()) refuse(name, "contiguous ", shape, type);
+    return t.data_ptr();
+}
+void* dense(const OptT& t, const char* name, at::IntArrayRef shape, at::ScalarType type) {
+    return t ? dense(*t, name, shape, type) : nullptr;
+}
+float* f32(const OptT& t, const char* name, at::IntArrayRef shape) { return static_cast<float*>(dense(t, name, shape, at::kFloat)); }
+
+// Checks a [B, T, ...] input and returns the elements between its tokens (0: contiguous).
+int64_t rows(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type) {
+    if (t.scalar_type() != type || t.sizes() != shape || !t.is_cuda()) refuse(name, "", shape, type);
+    if (t.is_contiguous()) return 0;
+    int64_t width = 1;
+    for (int64_t i = (int64_t)shape.size() - 1; i >= 2; --i) {
+        if (shape[i] != 1 && t.stride(i) != width) throw py::value_error(std::string(name) + "'s rows must be dense");
+        width *= shape[i];
+    }
+    const int64_t B = shape[0], T = shape[1];
+    const int64_t ld = T > 1 ? t.stride(1) : B > 1 ? t.stride(0) : width;
+    if (ld < width || (B > 1 && T > 1 && t.stride(0) != T * ld)) throw py::value_error(std::string(name) + "'s tokens must be evenly spaced");
+    return ld;
+}
+
+// Sequences; packed ones' count and offsets.
+int64_t axis(const OptT& cu, int64_t B, int& N, const int32_t*& p) {
+    N = 0;
+    p = nullptr;
+    if (!cu) return B;
+    need(cu->scalar_type() == at::kInt && cu->is_cuda() && cu->dim() == 1 && cu->is_contiguous() && cu->numel() >= 2,
+         "cu_seqlens must be an int32 CUDA vector");
+    need(B == 1, "packed sequences need B == 1");
+    N = (int)cu->numel() - 1;
+    p = cu->data_ptr<int32_t>();
+    return N;
+}
+int32_t* error_word(const OptT& err) {
+    if (!err) return nullptr;
+    need(err->scalar_type() == at::kInt && err->is_cuda() && err->numel() >= 1, "err must be an int32 CUDA tensor");
+    return err->data_ptr<int32_t>();
+}
+kda_stream_t stream_of(const py::object& stream, const Tensor& x) {
+    if (stream.is_none()) return reinterpret_cast<kda_stream_t>(c10::cuda::getCurrentCUDAStream(x.get_device()).stream());
+    return reinterpret_cast<kda_stream_t>(stream.attr("cuda_stream").cast<uintptr_t>());
+}
+void check(kda_status st, const char* where) {
+    if (st != KDA_OK) py::module_::import("chunkwise_delta_rule_gb300._lib").attr("check")((int)st, where);
+}
+Tensor like(const Tensor& t) { return at::empty(t.sizes(), t.options()); }
+OptT like(const OptT& t) { return t ? OptT(like(*t)) : OptT(); }
+void* ptr(const OptT& t) { return t ? t->data_ptr() : nullptr; }
+size_t bytes(const OptT& t) { return t ? t->nbytes() : 0; }
+// The given buffer if it is large enough, else a new one (nothing for no bytes).
+OptT buffer(size_t n, const Tensor& x, const OptT& given) {
+    if (n == 0 || (given && given->nbytes() >= n)) return given;
+    return at::empty({(int64_t)n}, x.options().dtype(at::kByte));
+}
+
+// ------------------------------------------------------------------ convolution
+struct Conv {
+    kda_conv_problem c{};
+    Tensor x, weight;
+    OptT bias, h0, cu;
+    std::vector<int64_t> state;
+    Conv(Tensor x_, Tensor w, OptT b, bool silu, OptT h, OptT cu_) : x(x_), weight(w), bias(b), h0(h), cu(cu_) {
+        need(x.dim() == 3, "x must be [B, T, D], bf16 or fp32");
+        c.io = io_of(x, "x must be [B, T, D], bf16 or fp32");
+        need(weight.dim() == 2, "weight must be [D, W]");
+        const int64_t B = x.size(0), T = x.size(1), D = x.size(2), W = weight.size(1);
+        c.B = (int)B; c.T = (int)T; c.D = (int)D; c.W = (int)W;
+        c.ldx = rows(x, "x", x.sizes(), x.scalar_type());
+        const int64_t n = axis(cu, B, c.N, c.cu_seqlens);
+        state = {n, W - 1, D};
+        c.silu = silu;
+        c.x = x.data_ptr();
+        c.weight = static_cast<float*>(dense(weight, "weight", {D, W}, at::kFloat));
+        c.bias = f32(bias, "bias", {D});
+        c.h0 = dense(h0, "initial_state", state, x.scalar_type());
+    }
+};
+py::tuple conv_fwd(const Conv& p, bool out_final, OptT final_state, OptT err, py::object stream) {
+    Tensor y = like(p.x);
+    if (!final_state && out_final) final_state = at::empty(p.state, p.x.options());
+    void* f = dense(final_state, "final_state", p.state, p.x.scalar_type());
+    check(kda_conv_fwd(&p.c, y.data_ptr(), f, error_word(err), stream_of(stream, p.x)), "kda_conv_fwd");
+    return py::make_tuple(y, final_state);
+}
+py::tuple conv_bwd(const Conv& p, Tensor dy, OptT dfinal, OptT ws, py::object stream, std::optional<bool> need_dinit) {
+    void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type());
+    void* pdf = dense(dfinal, "dfinal", p.state, p.x.scalar_type());
+    Tensor dx = like(p.x), dw = like(p.weight);
+    OptT db = like(p.bias), dinit;
+    if (need_dinit ? *need_dinit : p.h0.has_value()) dinit = at::empty(p.state, p.x.options());
+    ws = buffer(kda_conv_workspace_size(&p.c), p.x, ws);
+    check(kda_conv_bwd(&p.c, pdy, pdf, dx.data_ptr(), dw.data_ptr<float>(), static_cast<float*>(ptr(db)), ptr(dinit), ptr(ws),
+                       bytes(ws), stream_of(stream, p.x)), "kda_conv_bwd");
+    return py::make_tuple(dx, dw, db, dinit);
+}
+
+// ------------------------------------------------------------------ scan
+struct Ssm {
+    kda_ssm_problem c{};
+    Tensor x, dt, A_log, b, cm;
+    OptT d_skip, z, dt_bias, h0, cu;
+    std::vector<int64_t> state;
+    Ssm(Tensor x_, Tensor dt_, Tensor A, Tensor b_, Tensor c_, OptT skip, OptT z_, OptT bias, bool softplus, OptT h, OptT cu_, int save)
+        : x(x_), dt(dt_), A_log(A), b(b_), cm(c_), d_skip(skip), z(z_), dt_bias(bias), h0(h), cu(cu_) {
+        need(x.dim() == 3, "x must be [B, T, D], bf16 or fp32");
+        c.io = io_of(x, "x must be [B, T, D], bf16 or fp32");
+        need(b.dim() == 4, "b must be [B, T, G, S]");
+        const int64_t B = x.size(0), T = x.size(1), D = x.size(2), G = b.size(2), S = b.size(3);
+        const at::ScalarType type = x.scalar_type();
+        const std::array<int64_t, 4> bc{B, T, G, S};
+        c.B = (int)B; c.T = (int)T; c.D = (int)D; c.S = (int)S; c.G = (int)G;
+        const int64_t n = axis(cu, B, c.N, c.cu_seqlens);
+        state = {n, D, S};
+        c.dt_softplus = softplus;
+        c.save_policy = save;
+        c.ldx = rows(x, "x", x.sizes(), type);
+        c.lddt = rows(dt, "dt", x.sizes(), type);
+        if (z) c.ldz = rows(*z, "z", x.sizes(), type);
+        c.ldb = rows(b, "b", bc, type);
+        c.ldc = rows(cm, "c", bc, type);
+        c.x = x.data_ptr();
+        c.dt = dt.data_ptr();
+        c.z = ptr(z);
+        c.b = b.data_ptr();
+        c.c = cm.data_ptr();
+        c.A_log = static_cast<float*>(dense(A_log, "A_log", {D, S}, at::kFloat));
+        c.d_skip = f32(d_skip, "d_skip", {D});
+        c.dt_bias = f32(dt_bias, "dt_bias", {D});
+        c.h0 = f32(h0, "initial_state", state);
+    }
+};
+py::tuple ssm_fwd(const Ssm& p, bool out_final, OptT ht, OptT saved, OptT ws, OptT err, py::object stream) {
+    Tensor y = like(p.x);
+    if (!ht && out_final) ht = at::empty(p.state, p.x.options().dtype(at::kFloat));
+    float* h = f32(ht, "ht", p.state);
+    ws = buffer(kda_ssm_workspace_size(&p.c, 0), p.x, ws);
+    OptT sv = p.c.save_policy ? buffer(kda_ssm_saved_size(&p.c), p.x, saved) : OptT();
+    check(kda_ssm_fwd(&p.c, y.data_ptr(), h, ptr(sv), ptr(ws), bytes(ws), error_word(err), stream_of(stream, p.x)), "kda_ssm_fwd");
+    return py::make_tuple(y, ht, sv);
+}
+py::tuple ssm_bwd(const Ssm& p, Tensor dy, OptT dht, OptT saved, OptT ws, py::object stream, std::optional<bool> need_dh0) {
+    void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type());
+    float* pdh = f32(dht, "dht", p.state);
+    if (p.c.save_policy) need(bytes(saved) >= kda_ssm_saved_size(&p.c), "save_policy 1 needs the forward's saved buffer");
+    else saved = OptT();
+    Tensor dx = like(p.x), ddt = like(p.dt), dA = like(p.A_log), db = like(p.b), dc = like(p.cm);
+    OptT dskip = like(p.d_skip), dz = like(p.z), dbias = like(p.dt_bias), dh0;
+    if (need_dh0 ? *need_dh0 : p.h0.has_value()) dh0 = at::empty(p.state, p.x.options().dtype(at::kFloat));
+    kda_ssm_grads g{};
+    g.dx = dx.data_ptr();
+    g.ddt = ddt.data_ptr();
+    g.dz = ptr(dz);
+    g.db = db.data_ptr();
+    g.dc = dc.data_ptr();
+    g.dA_log = dA.data_ptr<float>();
+    g.dd_skip = static_cast<float*>(ptr(dskip));
+    g.ddt_bias = static_cast<float*>(ptr(dbias));
+    g.dh0 = static_cast<float*>(ptr(dh0));
+    ws = buffer(kda_ssm_workspace_size(&p.c, 1), p.x, ws);
+    check(kda_ssm_bwd(&p.c, pdy, pdh, ptr(saved), &g, ptr(ws), bytes(ws), stream_of(stream, p.x)), "kda_ssm_bwd");
+    return py::make_tuple(dx, ddt, dA, db, dc, dskip, dz, dbias, dh0);
+}
+
+// ------------------------------------------------------------------ norm
+struct Norm {
+    kda_norm_problem c{};
+    Tensor x, weight;
+    OptT residual;
+    std::vector<int64_t> scales;   // shape of the scales of an 8-bit output
+    Norm(Tensor x_, Tensor w, OptT r, double eps, const std::string& out, int64_t group) : x(x_), weight(w), residual(r) {
+        need(x.dim() >= 1, "x must be bf16 or fp32 rows");
+        c.io = io_of(x, "x must be bf16 or fp32 rows");
+        need(out == "io" || out == "e4m3", "out must be \"io\" or \"e4m3\"");
+        const int64_t D = x.size(-1);
+        c.rows = D ? (int)(x.numel() / D) : 0;
+        c.D = (int)D;
+        c.out = out == "e4m3";
+        c.group = (int)group;
+        c.eps = (float)eps;
+        c.x = dense(x, "x", x.sizes(), x.scalar_type());
+        c.residual = dense(residual, "residual", x.sizes(), x.scalar_type());
+        c.weight = static_cast<float*>(dense(weight, "weight", {D}, at::kFloat));
+        if (c.out) {
+            scales.assign(x.sizes().begin(), x.sizes().end());
+            scales.back() = group > 0 ? (D + group - 1) / group : 1;
+        }
+    }
+};
+py::tuple norm_fwd(const Norm& p, OptT h, py::object stream) {
+    Tensor y = p.c.out ? at::empty(p.x.sizes(), p.x.options().dtype(at::kFloat8_e4m3fn)) : like(p.x);
+    OptT scale;
+    if (p.c.out) scale = at::empty(p.scales, p.x.options().dtype(at::kFloat));
+    if (!p.residual) h = p.x;
+    else if (!h) h = like(p.x);
+    else dense(h, "h", p.x.sizes(), p.x.scalar_type());
+    check(kda_norm_fwd(&p.c, y.data_ptr(), static_cast<float*>(ptr(scale)), h->data_ptr(), stream_of(stream, p.x)), "kda_norm_fwd");
+    return py::make_tuple(y, scale, h);
+}
+py::tuple norm_bwd(const Norm& p, Tensor dy, OptT dres, OptT ws, py::object stream) {
+    void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type());
+    void* pdr = dense(dres, "dres", p.x.sizes(), p.x.scalar_type());
+    Tensor dx = like(p.x), dw = like(p.weight);
+    ws = buffer(kda_norm_workspace_size(&p.c), p.x, ws);
+    check(kda_norm_bwd(&p.c, pdy, pdr, dx.data_ptr(), dw.data_ptr<float>(), ptr(ws), bytes(ws), stream_of(stream, p.x)), "kda_norm_bwd");
+    return py::make_tuple(dx, dw);
+}
+
+}  // namespace
+
+PYBIND11_MODULE(_binding, m) {
+    m.doc() = "Argument checks and calls of the layer operators; see layer.py for their documentation.";
+    py::class_<Conv>(m, "ConvProblem", "A validated convolution call plus the tensors it points to.")
+        .def(py::init<Tensor, Tensor, OptT, bool, OptT, OptT>())
+        .def_readonly("x", &Conv::x)
+        .def_readonly("state_shape", &Conv::state);
+    py::class_<Ssm>(m, "SsmProblem", "A validated scan call plus the tensors it points to.")
+        .def(py::init<Tensor, Tensor, Tensor, Tensor, Tensor, OptT, OptT, OptT, bool, OptT, OptT, int>())
+        .def_readonly("x", &Ssm::x)
+        .def_readonly("state_shape", &Ssm::state);
+    py::class_<Norm>(m, "NormProblem", "A validated norm call plus the tensors it points to.")
+        .def(py::init<Tensor, Tensor, OptT, double, const std::string&, int64_t>())
+        .def_readonly("x", &Norm::x);
+    m.def("conv_fwd", &conv_fwd);
+    m.def("conv_bwd", &conv_bwd);
+    m.def("conv_workspace_size", [](const Conv& p) { return kda_conv_workspace_size(&p.c); });
+    m.def("ssm_fwd", &ssm_fwd);
+    m.def("ssm_bwd", &ssm_bwd);
+    m.def("ssm_workspace_size", [](const Ssm& p, bool backward) { return kda_ssm_workspace_size(&p.c, backward); });
+    m.def("ssm_saved_size", [](const Ssm& p) { return kda_ssm_saved_size(&p.c); });
+    m.def("norm_fwd", &norm_fwd);
+    m.def("norm_bwd", &norm_bwd);
+    m.def("norm_workspace_size", [](const Norm& p) { return kda_norm_workspace_size(&p.c); });
+}

@@ -434,77 +434,98 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
     if (threadIdx.x < 32) tc::tmem_dealloc(tmem, Sh::ALLOC);
 }
 
-// A lane's EL states of a row of b or c: one access of EL elements where the row is aligned to it.
-template <int EL, typename TI>
-__device__ __forceinline__ void load_lane(const TI* p, int n, bool aligned, float (&x)[EL]) {
-    if (aligned && n >= EL && EL >= 4) {
-        struct alignas(sizeof(TI) * EL > 16 ? 16 : sizeof(TI) * EL) Pack { TI v[EL]; };
-        const Pack k = *reinterpret_cast<const Pack*>(p);
-#pragma unroll
-        for (int e = 0; e < EL; ++e) x[e] = ld(&k.v[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < EL; ++e) x[e] = e < n ? ld(p + e) : 0.f;
-    }
-}
-
 // A few tokens of each sequence (decoding): the state is the traffic, 8 bytes per value against 8 per channel for the
 // token. The same four lanes per channel, NS sequences per thread so that their states are in flight together and A is
-// formed once; everything is read directly, and after the exchange over the four lanes lane i holds sequence i's output.
-template <typename TI, int EL, int NS>
-__global__ void __launch_bounds__(SSM_T) k_ssm_step(SsmArgs a) {
+// formed once; everything is read directly. Of four sequences lane i forms sequence i's step for the channel's lanes, and
+// after the exchange over them holds its output. WHOLE: the states fill the lanes and every row is aligned.
+template <typename TI, int EL, int NS, bool WHOLE>
+__global__ void __launch_bounds__(SSM_T, EL <= 4 ? (WHOLE ? 8 : 5) : 1) k_ssm_step(SsmArgs a) {
     static_assert(NS == 1 || NS == 4, "sequences per thread");
-    const int M = a.D / a.G, tpg = (M + SSM_CH - 1) / SSM_CH, tiles = tpg * a.G;
+    constexpr int SC = SSM_T / 4;   // channels per CTA
+    const int M = a.D / a.G, tpg = (M + SC - 1) / SC, tiles = tpg * a.G;
     const int sb = blockIdx.x / tiles, tile = blockIdx.x - sb * tiles, g = tile / tpg, tg = tile - g * tpg;
-    const int l = threadIdx.x & 3, ch = threadIdx.x >> 2, n0 = l * EL, d = g * M + tg * SSM_CH + ch;
-    const bool on = ch < M - tg * SSM_CH;
+    const int l = threadIdx.x & 3, ch = threadIdx.x >> 2, n0 = l * EL, d = g * M + tg * SC + ch;
+    const bool on = ch < M - tg * SC;
     const size_t DS = (size_t)a.D * a.S;
-    const int B = a.ax.N, T = a.ax.len, s0 = sb * NS;
+    const int B = a.ax.N, T = a.ax.len, s0 = sb * NS, valid = on ? a.S - n0 : 0;
+    auto states = [&](const float* p, float(&v)[EL]) {
+        if (WHOLE && EL >= 4) {
+#pragma unroll
+            for (int e = 0; e + 3 < EL; e += 4) {
+                const float4 q = on ? *reinterpret_cast<const float4*>(p + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[e] = q.x; v[e + 1] = q.y; v[e + 2] = q.z; v[e + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < EL; ++e) v[e] = e < valid ? p[e] : 0.f;
+        }
+    };
+    auto row = [&](const TI* p, bool in, float(&v)[EL]) {
+        if (WHOLE) {
+            Raw<TI, EL> r;
+            if (in) {
+                constexpr int N = sizeof(r) > 16 ? sizeof(r) / 16 : 1;
+                if (sizeof(r) > 16) {
+#pragma unroll
+                    for (int q = 0; q < N; ++q) reinterpret_cast<uint4*>(&r)[q] = reinterpret_cast<const uint4*>(p)[q];
+                } else {
+                    r = load_raw<TI, EL>(p);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < EL; ++e) r.v[e] = TI(0.f);
+            }
+            unpack<EL>(r, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < EL; ++e) v[e] = in && n0 + e < a.S ? ld(p + e) : 0.f;
+        }
+    };
     float A2[EL], h[NS][EL];
-    load_states<EL>(a.A_log + (size_t)d * a.S, n0, a.S, on, A2);
+    const size_t base = (size_t)d * a.S + n0;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
         if (a.h0 && s0 + i < B) {
-            load_states<EL>(a.h0 + (s0 + i) * DS + (size_t)d * a.S, n0, a.S, on, h[i]);
+            states(a.h0 + (s0 + i) * DS + base, h[i]);
         } else {
 #pragma unroll
             for (int e = 0; e < EL; ++e) h[i][e] = 0.f;
         }
     }
+    states(a.A_log + base, A2);
     const float bias = a.dt_bias && on ? a.dt_bias[d] : 0.f, skip = a.d_skip && on ? a.d_skip[d] : 0.f;
+    const int mine = s0 + (NS == 4 ? l : 0);   // the sequence whose step this lane forms and whose output it stores
+    const bool own = on && mine < B;
+    const TI* bp = static_cast<const TI*>(a.b) + (size_t)g * a.S + n0;
+    const TI* cp = static_cast<const TI*>(a.c) + (size_t)g * a.S + n0;
     for (int t = 0; t < T; ++t) {
-        float x[NS], dt[NS], b[NS][EL], c[NS][EL], acc[NS];
-        const int mine = s0 + (NS == 4 ? l : 0);   // the sequence whose output this lane stores
-        float z = 0.f;
+        const size_t tok = (size_t)mine * T + t;
+        const float x = own ? ld(static_cast<const TI*>(a.x) + tok * a.ldx + d) : 0.f;
+        const float dt = own ? ld(static_cast<const TI*>(a.dt) + tok * a.lddt + d) : 0.f;
+        const float z = own && a.z ? ld(static_cast<const TI*>(a.z) + tok * a.ldz + d) : 0.f;
+        float b[NS][EL], c[NS][EL], acc[NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            const bool in = on && s0 + i < B;
-            const size_t tok = (size_t)(s0 + i) * T + t;
-            x[i] = in ? ld(static_cast<const TI*>(a.x) + tok * a.ldx + d) : 0.f;
-            dt[i] = in ? ld(static_cast<const TI*>(a.dt) + tok * a.lddt + d) : 0.f;
-            const int n = s0 + i < B ? a.S - n0 : 0;
-            load_lane<EL>(static_cast<const TI*>(a.b) + tok * a.ldb + (size_t)g * a.S + n0, n, !(a.how >> SSM_B & 3), b[i]);
-            load_lane<EL>(static_cast<const TI*>(a.c) + tok * a.ldc + (size_t)g * a.S + n0, n, !(a.how >> SSM_C & 3), c[i]);
+            const size_t ti = (size_t)(s0 + i) * T + t;
+            row(bp + ti * a.ldb, s0 + i < B, b[i]);
+            row(cp + ti * a.ldc, s0 + i < B, c[i]);
         }
-        const bool store = on && mine < B && (NS == 4 || l == 0);
-        if (a.z && store) z = ld(static_cast<const TI*>(a.z) + ((size_t)mine * T + t) * a.ldz + d);
         if (t == 0) {
 #pragma unroll
-            for (int e = 0; e < EL; ++e) A2[e] = on && n0 + e < a.S ? -expf(A2[e]) * LOG2E : 0.f;
+            for (int e = 0; e < EL; ++e) A2[e] = e < valid ? -LOG2E * ex2(LOG2E * A2[e]) : 0.f;
         }
-        float xm = 0.f;
+        float dl = dt + bias;
+        if (a.softplus) dl = ssm_softplus(dl);
+        const float u = dl * x;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            float dl = dt[i] + bias;
-            if (a.softplus) dl = ssm_softplus(dl);
-            const float u = dl * x[i];
+            const float di = NS == 4 ? __shfl_sync(SSM_FULL, dl, i, 4) : dl, ui = NS == 4 ? __shfl_sync(SSM_FULL, u, i, 4) : u;
             acc[i] = 0.f;
 #pragma unroll
             for (int e = 0; e < EL; ++e) {
-                h[i][e] = fmaf(ex2(dl * A2[e]), h[i][e], u * b[i][e]);
+                h[i][e] = fmaf(ex2(di * A2[e]), h[i][e], ui * b[i][e]);
                 acc[i] = fmaf(h[i][e], c[i][e], acc[i]);
             }
-            if (i == 0 || l == i) xm = x[i];
         }
         if (NS == 4) {
             halve<4>(acc, l, 2);
@@ -513,27 +534,45 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_step(SsmArgs a) {
             acc[0] += __shfl_xor_sync(SSM_FULL, acc[0], 2);
             acc[0] += __shfl_xor_sync(SSM_FULL, acc[0], 1);
         }
-        if (store) {
-            float o = fmaf(skip, xm, acc[0]);
+        if (own && (NS == 4 || l == 0)) {
+            float o = fmaf(skip, x, acc[0]);
             if (a.z) o *= z * sigmoid_fast(z);
-            st(static_cast<TI*>(a.y) + ((size_t)mine * T + t) * a.D + d, o);
+            st(static_cast<TI*>(a.y) + tok * a.D + d, o);
         }
     }
     if (a.ht) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
-            if (s0 + i < B) store_states<EL>(a.ht + (s0 + i) * DS + (size_t)d * a.S, n0, a.S, on, h[i]);
+        for (int i = 0; i < NS; ++i) {
+            if (s0 + i >= B || !on) continue;
+            float* p = a.ht + (s0 + i) * DS + base;
+            if (WHOLE && EL >= 4) {
+#pragma unroll
+                for (int e = 0; e + 3 < EL; e += 4) *reinterpret_cast<float4*>(p + e) = make_float4(h[i][e], h[i][e + 1], h[i][e + 2], h[i][e + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < EL; ++e)
+                    if (e < valid) p[e] = h[i][e];
+            }
+        }
     }
 }
 
 int fwd_tiles(int D, int G) { return (D / G + CH - 1) / CH * G; }
 
-template <typename TI, int EL>
-void run_step(const SsmArgs& a, cudaStream_t st) {
+template <typename TI, int EL, bool WHOLE>
+void run_step_form(const SsmArgs& a, cudaStream_t st) {
     const unsigned tiles = (a.D / a.G + SSM_CH - 1) / SSM_CH * a.G;
     // four sequences per thread once that still leaves every SM two CTAs
-    if ((long long)tiles * (a.ax.N / 4) >= 2 * sm_count()) k_ssm_step<TI, EL, 4><<<tiles * ((a.ax.N + 3) / 4), SSM_T, 0, st>>>(a);
-    else k_ssm_step<TI, EL, 1><<<tiles * a.ax.N, SSM_T, 0, st>>>(a);
+    if ((long long)tiles * (a.ax.N / 4) >= 2 * sm_count())
+        k_ssm_step<TI, EL, 4, WHOLE><<<tiles * ((a.ax.N + 3) / 4), SSM_T, 0, st>>>(a);
+    else
+        k_ssm_step<TI, EL, 1, WHOLE><<<tiles * a.ax.N, SSM_T, 0, st>>>(a);
+}
+template <typename TI, int EL>
+void run_step(const SsmArgs& a, cudaStream_t st) {
+    auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    const bool whole = a.S == 4 * EL && al(a.h0) && al(a.ht) && al(a.A_log) && !(a.how >> SSM_B & 3) && !(a.how >> SSM_C & 3);
+    whole ? run_step_form<TI, EL, true>(a, st) : run_step_form<TI, EL, false>(a, st);
 }
 
 template <typename TI, int EL, int MODE>

@@ -2,11 +2,13 @@
 //     delta = softplus(dt + dt_bias),  a = exp(-delta exp(A_log)),  u = delta x
 //     h_t = a h_{t-1} + u B_t,   y_t = (sum_n C_t[n] h_t[n] + d_skip x_t) silu(z_t)
 // Four lanes share a channel and hold its states in registers; a CTA walks 64 channels
-// through a time piece in tiles of up to 32 tokens. Eight warps run the recurrence,
-// eight others work around it, so that the recurrence never waits for them: while tile
-// k runs they copy tiles ahead into shared memory (asynchronously, each thread its own
-// share), form tile k + 1's steps once per (token, channel), and sum, gate and store
-// tile k - 1's outputs. One barrier per tile.
+// through a time piece in tiles of up to 32 tokens. Eight warps run the recurrence; four
+// in front of it copy tiles ahead into shared memory (asynchronously, each thread its own
+// share) and form a tile's steps once per (token, channel); four behind it sum, gate and
+// store the outputs. Two tiles of buffers and an mbarrier per hand-over let the three
+// run apart, and each warp of the recurrence on its own (with one barrier for all per
+// tile, the latencies of the three added up: 461 against XXX us for two sequences of
+// 8192 tokens and 4096 channels).
 // Every lane needs its states' values of the rows b_t and c_t, the same for all
 // channels. Read from shared memory they bound the kernel: a load fills 128 bytes of
 // registers per cycle however few addresses it has, and the two rows are three quarters
@@ -32,35 +34,37 @@ enum { OUT = 0, OUT_CKPT = 1, CKPT = 2, PIECE = 3 };
 
 constexpr int RT = 256;         // threads of the recurrence: 64 channels x 4 lanes
 constexpr int CH = RT / 4;
-constexpr int HT = 256;         // threads around it
+constexpr int PT = 128;         // threads in front of it, and as many behind it
 
 template <typename TI, int EL, int MODE>
 struct FwdShape {
     static constexpr bool HAS_Y = MODE == OUT || MODE == OUT_CKPT, HAS_CK = MODE == OUT_CKPT || MODE == CKPT;
+    static constexpr int THREADS = RT + (HAS_Y ? 2 : 1) * PT;
     static constexpr int NROW = HAS_Y ? 2 : 1;           // rows of a token: b (and c)
     // tokens per tile: at most 256 columns of spread rows, two tiles of them in the SM's 512; fp32 tiles are half as long
     // for their shared memory
     static constexpr int MOST = sizeof(TI) == 2 ? 32 : 16, TT = 128 / EL < MOST ? 128 / EL : MOST;
     static constexpr int COLS = TT * NROW * EL;          // columns of a tile
     static constexpr int ALLOC = 2 * COLS < 32 ? 32 : 2 * COLS;
-    static constexpr int CP = TT * CH / HT;              // channels of a token per thread around the recurrence
+    static constexpr int CP = TT * CH / PT < 8 ? TT * CH / PT : 8;   // channels of a token together in a thread around the recurrence
+    static constexpr int IT = TT * CH / PT / CP;         // its tokens
     static constexpr int PIECES = TT * NROW * 4;         // (token, row, lane group) of EL states
-    static constexpr int NTOK = HAS_Y ? 3 : 2;           // x, dt (and z)
-    // tiles copied: the previous (its x and z), the current, the next two, and one ahead where there is room
-    static constexpr int STAGES = sizeof(TI) == 2 ? 5 : 4;
+    static constexpr int PP = (PIECES + PT - 1) / PT;    // per thread
+    static constexpr int STAGES = 4;                     // tiles in copies
     static constexpr int ATOM = 16 * 128;                // 16 k-rows of 64 columns
     static constexpr int OPB = (COLS + 63) / 64 * ATOM;  // bytes of a B operand
     struct Smem {
         unsigned char a[2 * ATOM];                       // 128 rows of ones
         unsigned char b[2][OPB];
-        TI tok[STAGES][NTOK][HT][CP];
-        TI bc[STAGES][PIECES][EL];
+        TI front[STAGES][2][IT][PT][CP];                 // x, dt
+        TI back[HAS_Y ? STAGES : 1][2][IT][PT][CP];      // x, z
+        TI bc[STAGES][PP][PT][EL];
         float2 du[2][TT][CH];                            // delta, u
         float y[2][HAS_Y ? TT : 1][CH][4];               // the four lanes' parts; see ch_at
-        uint64_t bar[2];
+        uint64_t full[2], mma[2], done[2], yfree[2];     // hand-overs of a tile's buffers
         uint32_t tmem;
     };
-    static_assert(CP % 2 == 0 && PIECES <= HT && sizeof(Smem) + 1024 <= 227 * 1024, "tile shape");
+    static_assert(CP % 2 == 0 && sizeof(Smem) + 1024 <= 227 * 1024, "tile shape");
 };
 
 // Place of a channel in a token's row, permuted so that the eight threads of a quarter warp, which hold a few
@@ -120,10 +124,50 @@ __device__ __forceinline__ void put_piece(unsigned char* op, int l, int n, const
     }
 }
 
+// Copies of a thread's share of a tile: CP channels of IT tokens of two tensors, in a ring of STAGES tiles.
+template <typename TI, typename Sh>
+struct Share {
+    static constexpr int CP = Sh::CP, IT = Sh::IT, PER = CH / CP;   // threads per token
+    const TI* src[2][IT];
+    size_t step[2];
+    int how[2], tok[IT], pc, valid, left;   // left: tokens from the next tile to fetch on
+    __device__ __forceinline__ void start(int tid, const SsmPlace& pl, int first, const void* s0, size_t ld0, int how0,
+                                          const void* s1, size_t ld1, int how1, size_t row0) {
+        pc = (tid % PER) * CP;
+        valid = pl.nch - pc;
+        left = pl.hi - first;
+        how[0] = how0;
+        how[1] = how1;
+        step[0] = Sh::TT * ld0;
+        step[1] = Sh::TT * ld1;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            tok[i] = (tid + i * PT) / PER;
+            src[0][i] = static_cast<const TI*>(s0) + (row0 + first + tok[i]) * ld0 + pl.c0 + pc;
+            src[1][i] = s1 ? static_cast<const TI*>(s1) + (row0 + first + tok[i]) * ld1 + pl.c0 + pc : nullptr;
+        }
+    }
+    __device__ __forceinline__ void fetch(TI (*stage)[IT][PT][CP], int tid) {
+        if (left > 0) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int n = tok[i] < left ? valid : 0;
+                copy_row_async<TI, CP>(stage[0][i][tid], src[0][i], n, how[0]);
+                src[0][i] += step[0];
+                if (src[1][i]) {
+                    copy_row_async<TI, CP>(stage[1][i][tid], src[1][i], n, how[1]);
+                    src[1][i] += step[1];
+                }
+            }
+            left -= Sh::TT;
+        }
+    }
+};
+
 template <typename TI, int EL, int MODE>
-__global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
+__global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(SsmArgs a) {
     using Sh = FwdShape<TI, EL, MODE>;
-    constexpr int NROW = Sh::NROW, STAGES = Sh::STAGES, P = EL / 2, TT = Sh::TT, CP = Sh::CP, COLS = Sh::COLS;
+    constexpr int NROW = Sh::NROW, STAGES = Sh::STAGES, P = EL / 2, TT = Sh::TT, CP = Sh::CP, IT = Sh::IT, COLS = Sh::COLS, PP = Sh::PP;
     constexpr bool HAS_Y = Sh::HAS_Y, HAS_CK = Sh::HAS_CK;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     typename Sh::Smem& sm = *reinterpret_cast<typename Sh::Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -144,124 +188,143 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
         }
     }
     const int first_tile = t, ntiles = (pl.hi - t + TT - 1) / TT;
-    // tensor memory, the operands' constant parts
+    // tensor memory, hand-overs, the operands' constant parts
     if (threadIdx.x < 32) {
         tc::tmem_alloc(&sm.tmem, Sh::ALLOC);
         tc::tmem_relinquish();
     }
     if (threadIdx.x == 0) {
-        tc::mbar_init(&sm.bar[0], 1);
-        tc::mbar_init(&sm.bar[1], 1);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            tc::mbar_init(&sm.full[w], PT / 32);
+            tc::mbar_init(&sm.mma[w], 1);
+            tc::mbar_init(&sm.done[w], RT / 32);
+            tc::mbar_init(&sm.yfree[w], PT / 32);
+        }
         tc::fence_mbar_init();
     }
-    for (int i = threadIdx.x; i < 16 * 128; i += RT + HT) {
+    for (int i = threadIdx.x; i < 16 * 128; i += Sh::THREADS) {
         const int k = i >> 7, m = i & 127;
         *reinterpret_cast<__nv_bfloat16*>(sm.a + op_at(k, m)) = __float2bfloat16_rn(k < 12 && (m & 3) == (k & 3) ? 1.f : 0.f);
     }
-    for (int i = threadIdx.x; i < 2 * Sh::OPB / 16; i += RT + HT) reinterpret_cast<uint4*>(&sm.b[0][0])[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < 2 * Sh::OPB / 16; i += Sh::THREADS) reinterpret_cast<uint4*>(&sm.b[0][0])[i] = make_uint4(0, 0, 0, 0);
     tc::fence_async_smem();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem;
+    // A wait that gives up (a lost hand-over) is recorded and no further one is tried: the results are not valid then.
+    bool lost = false;
+    auto await = [&](uint64_t* bar, int phase) {
+        if (!lost && !tc::mbar_wait(bar, phase & 1)) {
+            lost = true;
+            if (a.err) atomicOr(a.err, 2);
+        }
+    };
+    auto hand_over = [&](uint64_t* bar) {   // this warp's part
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+    };
 
-    if (threadIdx.x >= RT) {
-        // ---------------------------------------------------------------- around the recurrence
-        // this thread's part of a tile: CP channels of one token; up to one piece of b's and c's rows
-        const int tid = threadIdx.x - RT;
-        constexpr int PER = CH / CP;   // threads per token
-        const int ptok = tid / PER, pc = (tid % PER) * CP, pvalid = pl.nch - pc;
-        const TI* src[3] = {static_cast<const TI*>(a.x) + tok0 * a.ldx + pl.c0 + pc,
-                            static_cast<const TI*>(a.dt) + tok0 * a.lddt + pl.c0 + pc,
-                            HAS_Y && a.z ? static_cast<const TI*>(a.z) + tok0 * a.ldz + pl.c0 + pc : nullptr};
-        const bool gate = src[2] != nullptr;
-        const size_t ld[3] = {a.ldx, a.lddt, a.ldz};
-        constexpr int SHIFT[3] = {SSM_X, SSM_DT, SSM_Z};
-        const int btok = tid / (4 * NROW), brow = (tid / 4) % NROW, bl = tid & 3;   // piece tid
-        const bool has_piece = tid < Sh::PIECES;
-        const TI* bsrc = brow ? static_cast<const TI*>(a.c) + tok0 * a.ldc + (size_t)pl.g * a.S
-                              : static_cast<const TI*>(a.b) + tok0 * a.ldb + (size_t)pl.g * a.S;
-        const size_t bld = brow ? a.ldc : a.ldb;
-        const int bhow = a.how >> (brow ? SSM_C : SSM_B) & 3, bvalid = a.S - bl * EL;
-        // tile k of the piece into its stage; tiles are fetched in order, the pointers move along
+    if (threadIdx.x >= RT + PT) {
+        // ---------------------------------------------------------------- behind the recurrence
+        const int tid = threadIdx.x - RT - PT;
+        Share<TI, Sh> sh;
+        sh.start(tid, pl, first_tile, a.x, a.ldx, a.how >> SSM_X & 3, a.z, a.ldz, a.how >> SSM_Z & 3, tok0);
+        const bool gate = a.z != nullptr, whole = sh.valid >= CP && !(a.how >> SSM_OUT & 3);
+        float skip[CP];
 #pragma unroll
-        for (int q = 0; q < Sh::NTOK; ++q) src[q] += (size_t)(first_tile + ptok) * ld[q];
-        bsrc += (size_t)(first_tile + btok) * bld + bl * EL;
-        const size_t step[3] = {TT * a.ldx, TT * a.lddt, TT * a.ldz}, bstep = TT * bld;
-        int left = pl.hi - first_tile;   // tokens from the next tile to fetch on
-        auto fetch = [&](int k) {
-            if (left > 0) {
-                const int st = k % STAGES, n = ptok < left ? pvalid : 0, m = btok < left ? bvalid : 0;
+        for (int i = 0; i < CP; ++i) skip[i] = a.d_skip && i < sh.valid ? a.d_skip[pl.c0 + sh.pc + i] : 0.f;
+        for (int k = 0; k < STAGES - 1; ++k) {
+            sh.fetch(sm.back[HAS_Y ? k : 0], tid);
+            copies_commit();
+        }
+        for (int k = 0; k < ntiles; ++k) {
+            const int w = k & 1, st = HAS_Y ? k % STAGES : 0;
+            sh.fetch(sm.back[HAS_Y ? (k + STAGES - 1) % STAGES : 0], tid);
+            copies_commit();
+            copies_wait<STAGES - 1>();
+            await(&sm.done[w], k >> 1);
 #pragma unroll
-                for (int q = 0; q < Sh::NTOK; ++q) {
-                    if (q < 2 || gate) copy_row_async<TI, CP>(sm.tok[st][q][tid], src[q], n, a.how >> SHIFT[q] & 3);
-                    src[q] += step[q];
+            for (int it = 0; it < IT; ++it) {
+                const int row = sh.tok[it], tok = first_tile + k * TT + row;
+                if (tok >= pl.hi || sh.valid <= 0) continue;
+                float o[CP], x[CP], z[CP];
+                load_part<CP>(sm.back[st][0][it][tid], x);
+                if (gate) load_part<CP>(sm.back[st][1][it][tid], z);
+#pragma unroll
+                for (int i = 0; i < CP; ++i) {
+                    const float4 v = *reinterpret_cast<const float4*>(sm.y[w][HAS_Y ? row : 0][ch_at(sh.pc + i)]);
+                    o[i] = fmaf(skip[i], x[i], (v.x + v.y) + (v.z + v.w));
                 }
-                if (has_piece) copy_row_async<TI, EL>(sm.bc[st][tid], bsrc, m, bhow);
-                bsrc += bstep;
-                left -= TT;
+                if (gate) {
+#pragma unroll
+                    for (int i = 0; i < CP; ++i) o[i] *= z[i] * sigmoid_fast(z[i]);
+                }
+                store_part<TI, CP>(static_cast<TI*>(a.y) + (tok0 + tok) * a.D + pl.c0 + sh.pc, o, sh.valid, whole);
+            }
+            hand_over(&sm.yfree[w]);
+        }
+    } else if (threadIdx.x >= RT) {
+        // ---------------------------------------------------------------- in front of the recurrence
+        const int tid = threadIdx.x - RT;
+        Share<TI, Sh> sh;
+        sh.start(tid, pl, first_tile, a.x, a.ldx, a.how >> SSM_X & 3, a.dt, a.lddt, a.how >> SSM_DT & 3, tok0);
+        float bias[CP];
+#pragma unroll
+        for (int i = 0; i < CP; ++i) bias[i] = a.dt_bias && i < sh.valid ? a.dt_bias[pl.c0 + sh.pc + i] : 0.f;
+        // pieces of b's and c's rows: a quarter's thread has the same lane group and row in each
+        const int bl = tid & 3, brow = (tid / 4) % NROW, bvalid = a.S - bl * EL, bhow = a.how >> (brow ? SSM_C : SSM_B) & 3;
+        const size_t bld = brow ? a.ldc : a.ldb;
+        const TI* bsrc = static_cast<const TI*>(brow ? a.c : a.b) + (tok0 + first_tile) * bld + (size_t)pl.g * a.S + bl * EL;
+        int bleft = pl.hi - first_tile;
+        auto fetch = [&](int k) {
+            const int st = k % STAGES;
+            sh.fetch(sm.front[st], tid);
+            if (bleft > 0) {
+#pragma unroll
+                for (int p = 0; p < PP; ++p) {
+                    const int btok = (tid + p * PT) / (4 * NROW);
+                    if (tid + p * PT < Sh::PIECES) copy_row_async<TI, EL>(sm.bc[st][p][tid], bsrc + btok * bld, btok < bleft ? bvalid : 0, bhow);
+                }
+                bsrc += TT * bld;
+                bleft -= TT;
             }
             copies_commit();
         };
-        for (int k = 0; k < STAGES - 3; ++k) fetch(k);
-        float bias[CP], skip[CP];
-#pragma unroll
-        for (int i = 0; i < CP; ++i) {
-            bias[i] = a.dt_bias && i < pvalid ? a.dt_bias[pl.c0 + pc + i] : 0.f;
-            skip[i] = HAS_Y && a.d_skip && i < pvalid ? a.d_skip[pl.c0 + pc + i] : 0.f;
-        }
+        for (int k = 0; k < STAGES - 1; ++k) fetch(k);
         constexpr uint32_t idesc = tc::idesc_bf16_abmn(128, COLS);
         const uint64_t adesc = tc::sdesc_mn(tc::smem_u32(sm.a), Sh::ATOM, 0);
-        // step k: tile k + 1's rows spread, tile k - 1's outputs stored, tile k + 1's steps formed, tile k + 2's rows into the
-        // operand that tile k's left
-        bool lost = false;
-        for (int k = -2; k <= ntiles; ++k) {
-            if (k + 1 >= 0 && k + 1 < ntiles && threadIdx.x < RT + 32) {
-                tc::fence_after_sync();
-                tc::mma_bf16_w(tmem + ((k + 1) & 1) * COLS, adesc, tc::sdesc_mn(tc::smem_u32(sm.b[(k + 1) & 1]), Sh::ATOM, 0), idesc, 0);
-                tc::mma_commit_w(&sm.bar[(k + 1) & 1]);
-            }
-            if (HAS_Y && k > 0) {
-                const int tok = first_tile + (k - 1) * TT + ptok, w = (k - 1) & 1, st = (k - 1) % STAGES;
-                if (tok < pl.hi && pvalid > 0) {
-                    float o[CP], x[CP], z[CP];
-                    load_part<CP>(sm.tok[st][0][tid], x);
-                    if (gate) load_part<CP>(sm.tok[st][HAS_Y ? 2 : 0][tid], z);
+        for (int k = 0; k < ntiles; ++k) {
+            const int w = k & 1, st = k % STAGES;
+            fetch(k + STAGES - 1);
+            copies_wait<STAGES - 1>();
+            if (k >= 2) await(&sm.done[w], (k >> 1) - 1);   // the buffers of tile k - 2
 #pragma unroll
-                    for (int i = 0; i < CP; ++i) {
-                        const float4 v = *reinterpret_cast<const float4*>(sm.y[w][HAS_Y ? ptok : 0][ch_at(pc + i)]);
-                        o[i] = fmaf(skip[i], x[i], (v.x + v.y) + (v.z + v.w));
-                        if (gate) o[i] *= z[i] * sigmoid_fast(z[i]);
-                    }
-                    store_part<TI, CP>(static_cast<TI*>(a.y) + (tok0 + tok) * a.D + pl.c0 + pc, o, pvalid,
-                                       pvalid >= CP && !(a.how >> SSM_OUT & 3));
-                }
+            for (int p = 0; p < PP; ++p)
+                if (tid + p * PT < Sh::PIECES)
+                    put_piece<EL>(sm.b[w], bl, ((tid + p * PT) / (4 * NROW) * NROW + brow) * EL, sm.bc[st][p][tid]);
+            tc::fence_async_smem();
+            tc::named_sync(1, PT);
+            if (threadIdx.x < RT + 32) {
+                tc::fence_after_sync();
+                tc::mma_bf16_w(tmem + w * COLS, adesc, tc::sdesc_mn(tc::smem_u32(sm.b[w]), Sh::ATOM, 0), idesc, 0);
+                tc::mma_commit_w(&sm.mma[w]);
             }
-            fetch(k + STAGES - 1);   // into the stage of tile k - 1, which was read last
-            copies_wait<STAGES - 3>();
-            if (k + 1 >= 0 && k + 1 < ntiles) {
-                const int w = (k + 1) & 1, st = (k + 1) % STAGES;
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
                 float x[CP], dt[CP];
-                load_part<CP>(sm.tok[st][0][tid], x);
-                load_part<CP>(sm.tok[st][1][tid], dt);
+                load_part<CP>(sm.front[st][0][it][tid], x);
+                load_part<CP>(sm.front[st][1][it][tid], dt);
 #pragma unroll
                 for (int i = 0; i < CP; i += 2) {
                     float2 dl = make_float2(dt[i] + bias[i], dt[i + 1] + bias[i + 1]);
                     if (a.softplus) dl = ssm_softplus2(dl);
                     const float2 u = mul2(dl, make_float2(x[i], x[i + 1]));
-                    *reinterpret_cast<float4*>(&sm.du[w][ptok][du_at(pc + i)]) = make_float4(dl.x, u.x, dl.y, u.y);
+                    *reinterpret_cast<float4*>(&sm.du[w][sh.tok[it]][du_at(sh.pc + i)]) = make_float4(dl.x, u.x, dl.y, u.y);
                 }
             }
-            if (k + 2 < ntiles && has_piece) {
-                // tile k's product was issued a step ago (its results are being read): it has read its operand
-                if (k >= 0 && !lost) lost = !tc::mbar_wait(&sm.bar[k & 1], (k >> 1) & 1);
-                put_piece<EL>(sm.b[k & 1], bl, (btok * NROW + brow) * EL, sm.bc[(k + 2) % STAGES][tid]);
-                tc::fence_async_smem();
-            }
-            if (k < ntiles) {
-                tc::fence_before_sync();
-                __syncthreads();
-            }
+            hand_over(&sm.full[w]);
         }
     } else {
         // ---------------------------------------------------------------- the recurrence
@@ -348,16 +411,12 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
             const size_t slot = (size_t)pl.row * ((a.ax.len + SSM_CKPT - 1) / SSM_CKPT) + tok / SSM_CKPT;
             store_states<EL>(a.ckpt + slot * DS + (size_t)d * a.S, n0, a.S, on, h);
         };
-        bool lost = false;   // a wait for the tensor core gave up: the results are not valid, and no further wait is tried
-        tc::fence_before_sync();
-        __syncthreads();     // the first tile's rows in their operand
-        __syncthreads();     // the first tile's steps
         for (int k = 0; k < ntiles; ++k) {
             const int tb = first_tile + k * TT, te = min(tb + TT, pl.hi), w = k & 1;
-            if (!lost && !tc::mbar_wait(&sm.bar[w], (k >> 1) & 1)) {
-                lost = true;
-                if (a.err) atomicOr(a.err, 2);
-            }
+            await(&sm.mma[w], k >> 1);
+            await(&sm.full[w], k >> 1);
+            if (HAS_Y && k >= 2) await(&sm.yfree[w], (k >> 1) - 1);
+            __syncwarp();
             tc::fence_after_sync();
             const uint32_t cols = lanes + w * COLS;
             t = tb;
@@ -419,7 +478,7 @@ __global__ void __launch_bounds__(RT + HT, 1) k_ssm_fwd(SsmArgs a) {
                 }
             }
             tc::fence_before_sync();
-            __syncthreads();
+            hand_over(&sm.done[w]);
         }
         if (pl.lo < pl.hi || !a.ax.cu) {
             if (MODE == PIECE) {
@@ -582,7 +641,7 @@ cudaError_t run_one(const SsmArgs& a, cudaStream_t st) {
     static SmemLimit limit;
     const cudaError_t e = limit.set(reinterpret_cast<const void*>(k_ssm_fwd<TI, EL, MODE>), smem);
     if (e != cudaSuccess) return e;
-    k_ssm_fwd<TI, EL, MODE><<<grid, RT + HT, smem, st>>>(a);
+    k_ssm_fwd<TI, EL, MODE><<<grid, FwdShape<TI, EL, MODE>::THREADS, smem, st>>>(a);
     return cudaSuccess;
 }
 template <typename TI, int EL>

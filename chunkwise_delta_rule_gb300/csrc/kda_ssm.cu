@@ -7,7 +7,7 @@
 // share) and form a tile's steps once per (token, channel); four behind it sum, gate and
 // store the outputs. Two tiles of buffers and an mbarrier per hand-over let the three
 // run apart, and each warp of the recurrence on its own (with one barrier for all per
-// tile, the latencies of the three added up: 461 against XXX us for two sequences of
+// tile, the latencies of the three added up: 461 against 444 us for two sequences of
 // 8192 tokens and 4096 channels).
 // Every lane needs its states' values of the rows b_t and c_t, the same for all
 // channels. Read from shared memory they bound the kernel: a load fills 128 bytes of

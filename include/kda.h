@@ -328,7 +328,11 @@ size_t kda_ssm_workspace_size(const kda_ssm_problem *p, int for_backward);
 size_t kda_ssm_saved_size(const kda_ssm_problem *p);
 
 /* Writes y [B*T, D] and, if not NULL, the final states ht [N, D, S] fp32, which
- * may be the same buffer as h0 (decoding in place). */
+ * may be the same buffer as h0 (decoding in place). A NaN or an infinity in b_t
+ * or c_t may reach states of its token other than its own as NaN (the rows are
+ * spread by a matrix product); tokens before it are not touched. Bit 1 of *err is set
+ * where a bounded wait inside the kernel gave up; the results are then
+ * unspecified. */
 kda_status kda_ssm_fwd(const kda_ssm_problem *p, void *y, float *ht, void *saved, void *ws, size_t ws_bytes,
                        int32_t *err, kda_stream_t stream);
 

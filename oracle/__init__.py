@@ -13,6 +13,8 @@ it, and it shares no code with the CUDA library.
 * ``prologue`` -- numpy FP64 gate activation (softplus and lower-bound forms,
   with A_log and dt_bias) and q/k L2 normalisation, forward and backward;
   ``cases.run_oracle_prologue_arrays`` composes them with the recurrence.
+* ``layer`` -- numpy FP64 short convolution, selective state space scan and
+  norm, forward and hand-derived backward.
 
 Parity pins: every function here is pinned by ``tests/test_oracle_*.py``
 against finite differences, closed forms, invariants and the pages' printed

@@ -75,6 +75,23 @@ __device__ __forceinline__ Seq seq_at(const TokenAxis& ax, int row, int t) {
     return s;
 }
 
+// The sequences behind and before s on its row (which has tokens there): the neighbour's one offset where it has tokens,
+// instead of a search of the offsets.
+__device__ __forceinline__ Seq seq_next(const TokenAxis& ax, int row, const Seq& s) {
+    if (ax.cu && s.n + 1 < ax.N) {
+        const int end = axis_cu(ax, s.n + 2);
+        if (end > s.end) return {s.n + 1, s.end, end};
+    }
+    return seq_at(ax, row, s.end);
+}
+__device__ __forceinline__ Seq seq_prev(const TokenAxis& ax, int row, const Seq& s) {
+    if (ax.cu && s.n > 0) {
+        const int first = axis_cu(ax, s.n - 1);
+        if (first < s.first) return {s.n - 1, first, s.first};
+    }
+    return seq_at(ax, row, s.first - 1);
+}
+
 // Packed axis: sets bit 0 of *err when cu does not start at 0, decreases, or does not end at the token
 // count. Called by one whole CTA.
 __device__ __forceinline__ void axis_check(const TokenAxis& ax, int32_t* err) {

@@ -358,18 +358,8 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
         } else {
 #pragma unroll
             for (int e = 0; e < EL; ++e) h[e] = 0.f;
-            if (MODE != PIECE) {
-                // the earlier pieces of its sequence, joined in order
-                const int q = s.first / a.unit_len;
-                for (int r = q; r < pl.u; ++r) {
-                    const size_t ru = (size_t)pl.row * a.units_row + r;
-                    float hl[EL];
-                    load_states<EL>(a.hloc + ru * DS + (size_t)d * a.S, n0, a.S, on, hl);
-                    const float sum = on ? a.sdt[ru * a.D + d] : 0.f;
-#pragma unroll
-                    for (int e = 0; e < EL; ++e) h[e] = r == q ? hl[e] : fmaf(ex2(A2[e] * sum), h[e], hl[e]);
-                }
-            }
+            // the earlier pieces of its sequence
+            if (MODE != PIECE) join_pieces<EL>(a, a.hloc, pl.row, s.first / a.unit_len, pl.u, 1, d, n0, on, A2, h);
         }
         constexpr int N = 16 / EL;              // tokens of a batch of operands
         constexpr int NCOL = N * NROW * EL;     // their columns
@@ -422,7 +412,7 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
             t = tb;
             if (MODE != PIECE && t == s.end) {
                 if (ht) store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
-                s = seq_at(a.ax, pl.row, t);
+                s = seq_next(a.ax, pl.row, s);
                 init_state(s.n);
             }
             if (te - tb == TT && (MODE == PIECE || s.end >= te)) {
@@ -446,7 +436,7 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
                 while (t < te) {
                     if (MODE != PIECE && t == s.end) {
                         if (ht) store_states<EL>(ht + s.n * DS, n0, a.S, on, h);
-                        s = seq_at(a.ax, pl.row, t);
+                        s = seq_next(a.ax, pl.row, s);
                         init_state(s.n);
                     }
                     if (HAS_CK && t % SSM_CKPT == 0) checkpoint(t);
@@ -680,13 +670,28 @@ cudaError_t launch(const char* name, const SsmArgs& a, int bf16, int mode, cudaS
 
 }  // namespace
 
+// Time pieces of a row. One CTA walks `len` tokens, and CTAs beyond the SMs wait for a further wave; with pieces each
+// token is walked about twice (the pass for the pieces' states costs three quarters of the main one) and a CTA joins the
+// pieces before its own. In units of a token's step: a CTA's fixed cost is about 64, a joined piece's about 2. The shortest
+// pieces are 32 tokens. (Two rows of 1688 tokens and 32 channels, forward and backward: 98 us in pieces of 128 tokens joined
+// one by one, 69 us so chosen and joined eight at a time.)
 int ssm_units(int rows, int len, int D, int G, int S, bool backward) {
-    // pieces only while the channels and rows alone leave SMs idle; a piece is at least 128 tokens
-    const long long ctas = (long long)rows * (backward ? ssm_bwd_tiles(D, G, S) : fwd_tiles(D, G));
-    long long units = ctas >= 2 * sm_count() / 3 ? 1 : 2LL * sm_count() / ctas;
-    const long long most = (len + 127) / 128;
-    if (units > most) units = most;
-    return units < 1 ? 1 : (int)units;
+    const long long ctas = (long long)rows * (backward ? ssm_bwd_tiles(D, G, S) : fwd_tiles(D, G)), sms = sm_count();
+    auto waves = [&](long long units) { return (ctas * units + sms - 1) / sms; };
+    if (len <= 32 || ctas <= 0 || ctas > sms) return 1;
+    long long best = 1, least = 4 * waves(1) * (len + 64);
+    for (int wave = 1; wave <= 2; ++wave)
+        for (int piece = 32; piece <= 128; piece *= 2) {
+            const long long fit = wave * sms / ctas, most = (len + piece - 1) / piece, tried = fit < most ? fit : most;
+            if (tried < 2) continue;
+            const long long tokens = ((len + tried - 1) / tried + 31) / 32 * 32, units = (len + tokens - 1) / tokens;
+            const long long cost = 7 * waves(units) * (tokens + 64) + 8 * units;
+            if (cost < least) {
+                least = cost;
+                best = units;
+            }
+        }
+    return (int)best;
 }
 
 cudaError_t launch_ssm_fwd(const SsmArgs& a, int bf16, int mode, cudaStream_t st) {

@@ -127,4 +127,28 @@ __device__ __forceinline__ void store_part(TI* p, const float (&x)[V], int valid
     }
 }
 
+// The state (or adjoint) h behind the time pieces from, from + dir, .. before `to` of a row: each piece's local one plus
+// the decay exp(A sum delta) times what enters it. Several pieces' values are on their way together: one after another,
+// each costs the memory's latency (0.3 us a piece).
+template <int EL>
+__device__ __forceinline__ void join_pieces(const SsmArgs& a, const float* local, int row, int from, int to, int dir, int d,
+                                            int n0, bool on, const float (&A2)[EL], float (&h)[EL]) {
+    constexpr int J = EL <= 4 ? 8 : 32 / EL;
+    const int count = (to - from) * dir;
+    for (int r = 0; r < count; r += J) {
+        float hl[J][EL], sum[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const bool in = on && r + j < count;
+            const size_t u = (size_t)row * a.units_row + from + (in ? r + j : 0) * dir;
+            load_states<EL>(local + (u * a.D + d) * a.S, n0, a.S, in, hl[j]);
+            sum[j] = in ? a.sdt[u * a.D + d] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < EL; ++e) h[e] = fmaf(ex2(A2[e] * sum[j]), h[e], hl[j][e]);
+    }
+}
+
 }  // namespace kda

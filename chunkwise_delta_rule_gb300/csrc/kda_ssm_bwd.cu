@@ -237,14 +237,7 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
         if (s.end > pl.hi) {
             // the adjoint entering this piece from the later pieces of its sequence, joined in order
             const int q = min((s.end - 1) / a.unit_len, a.units_row - 1);
-            for (int v = q; v > pl.u; --v) {
-                const size_t ru = (size_t)pl.row * a.units_row + v;
-                float rl[EL];
-                load_states<EL>(a.rloc + ru * DS + (size_t)d * a.S, n0, a.S, on, rl);
-                const float sum = on ? a.sdt[ru * a.D + d] : 0.f;
-#pragma unroll
-                for (int e = 0; e < EL; ++e) r[e] = v == q ? rl[e] : fmaf(ex2(A2[e] * sum), r[e], rl[e]);
-            }
+            join_pieces<EL>(a, a.rloc, pl.row, q, pl.u, -1, d, n0, on, A2, r);
         }
     }
     const size_t slot0 = (size_t)pl.row * ((a.ax.len + TB - 1) / TB);
@@ -263,8 +256,10 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
         if (k + 1 < ntiles) load_states<EL>(a.ckpt + (slot0 + tile_begin(k + 1) / TB) * DS + (size_t)d * a.S, n0, a.S, on, hnext);
         // first and last tokens of sequences inside the tile
         uint32_t starts = 0, ends = 0;
+        Seq last{0, 0, 0};   // the tile's last sequence; s becomes its first
         for (int p = te - 1;;) {
-            if (p < s.first || p >= s.end) s = seq_at(a.ax, pl.row, p);
+            if (p < s.first) s = seq_prev(a.ax, pl.row, s);
+            if (p == te - 1) last = s;
             if (s.end <= te && s.end > tb) ends |= 1u << (s.end - 1 - tb);
             if (s.first < tb) break;
             starts |= 1u << (s.first - tb);
@@ -329,17 +324,14 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
 #pragma unroll
             for (int f = 0; f < KEEP; ++f) sm.red[w][warp][it][my_red + f] = bc[f];
         };
-        auto leave = [&](int it) {   // the first token of a sequence: its state's adjoint goes out, the previous one's comes in
-            if (a.dh0) {
-                const int n = seq_at(a.ax, pl.row, tb + it).n;
-                store_states<EL>(a.dh0 + n * DS + (size_t)d * a.S, n0, a.S, on, r);
-            }
+        auto leave = [&](int n) {   // at the first token of sequence n its state's adjoint goes out
+            if (a.dh0) store_states<EL>(a.dh0 + n * DS + (size_t)d * a.S, n0, a.S, on, r);
 #pragma unroll
             for (int e = 0; e < EL; ++e) r[e] = 0.f;
         };
         if (nt == TB && !(starts & ~1u) && !(ends & ~(1u << (TB - 1)))) {
             // a whole tile of one sequence
-            if (ends) state_of(a.dht, seq_at(a.ax, pl.row, te - 1).n, r);
+            if (ends) state_of(a.dht, last.n, r);
             if (NSUB > 1) {
                 // states at the sub-blocks' starts
                 float h[EL];
@@ -370,28 +362,36 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
 #pragma unroll
                 for (int i = L - 1; i >= 0; --i) reverse(sb * L + i, hs[i], i > 0 ? hs[i > 0 ? i - 1 : 0] : hk);
             }
-            if (starts) leave(0);
+            if (starts) leave(s.n);
         } else {
-            // sequences begin or end inside, or tokens are missing: each token's state from the tile's (or its
-            // sequence's) first one, without holding any
+            // sequences begin or end inside, or tokens are missing: the state before each token in the thread's own memory
+            // (such tiles are rare, and unrolled this would not fit the instruction cache beside the other path)
+            float before[TB][EL], h[EL];
+            Seq q = s;
+#pragma unroll
+            for (int e = 0; e < EL; ++e) h[e] = hstart[e];
+#pragma unroll 1
+            for (int it = 0; it < nt; ++it) {
+                if (it > 0 && (starts >> it & 1)) {
+                    q = seq_next(a.ax, pl.row, q);
+                    state_of(a.h0, q.n, h);
+                }
+#pragma unroll
+                for (int e = 0; e < EL; ++e) before[it][e] = h[e];
+                step(it, h);
+            }
 #pragma unroll 1
             for (int it = nt - 1; it >= 0; --it) {
-                if (ends >> it & 1) state_of(a.dht, seq_at(a.ax, pl.row, tb + it).n, r);
-                const int from = 31 - __clz((starts & (2u << it) - 1) | 1u);   // the last start at or before it
-                float h[EL], hp[EL];
-                if (from > 0) {
-                    state_of(a.h0, seq_at(a.ax, pl.row, tb + from).n, h);
-                } else {
+                if (ends >> it & 1) state_of(a.dht, last.n, r);
+                float hp[EL];
 #pragma unroll
-                    for (int e = 0; e < EL; ++e) h[e] = hstart[e];
-                }
-#pragma unroll 1
-                for (int i = from; i < it; ++i) step(i, h);
-#pragma unroll
-                for (int e = 0; e < EL; ++e) hp[e] = h[e];
+                for (int e = 0; e < EL; ++e) h[e] = hp[e] = before[it][e];
                 step(it, h);
                 reverse(it, h, hp);
-                if (starts >> it & 1) leave(it);
+                if (starts >> it & 1) {
+                    leave(last.n);
+                    if (it > 0) last = seq_prev(a.ax, pl.row, last);
+                }
             }
         }
         __syncthreads();
@@ -429,42 +429,64 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_bwd_pieces(SsmArgs a) {
     const TI* zp = a.z ? static_cast<const TI*>(a.z) + tok0 * a.ldz + pl.c0 + pc : nullptr;
     const TI* yp = static_cast<const TI*>(a.dy) + tok0 * a.D + pl.c0 + pc;
     const TI* cp = static_cast<const TI*>(a.c) + tok0 * a.ldc + (size_t)pl.g * a.S;
-    for (int tb = (hi - 1) / TB * TB; tb >= pl.lo; tb -= TB) {
+    float bias[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bias[i] = a.dt_bias && i < pvalid ? a.dt_bias[pl.c0 + pc + i] : 0.f;
+    constexpr int NC = NP / 8, NPT = (TB * NC + SSM_T - 1) / SSM_T;
+    float dt[4], z[4], dy[4], cv[NPT][8];
+    auto fetch = [&](int tb) {   // a tile's rows, as far as they are there
         const int te = min(tb + TB, hi), t = tb + ptok;
-        const bool in = t < te && pvalid > 0;
-        float dt[4], z[4], dy[4];
+        const int n = t < te && tb >= pl.lo ? pvalid : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) dt[i] = z[i] = dy[i] = 0.f;
-        if (in) {
-            load_row<4>(dp + (size_t)t * a.lddt, dt, pvalid, false);
-            load_row<4>(yp + (size_t)t * a.D, dy, pvalid, false);
-            if (zp) load_row<4>(zp + (size_t)t * a.ldz, z, pvalid, false);
+        if (n > 0) {
+            load_row<4>(dp + (size_t)t * a.lddt, dt, n, false);
+            load_row<4>(yp + (size_t)t * a.D, dy, n, false);
+            if (zp) load_row<4>(zp + (size_t)t * a.ldz, z, n, false);
         }
 #pragma unroll
+        for (int j = 0; j < NPT; ++j) {
+            const int i = tid + j * SSM_T, tok = i / NC, k = (i - tok * NC) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) cv[j][e] = 0.f;
+            if (i < TB * NC && tb + tok < te && tb >= pl.lo)
+                load_row<8>(cp + (size_t)(tb + tok) * a.ldc + k, cv[j], a.S - k, a.S - k >= 8 && !(a.how >> SSM_C & 3));
+        }
+    };
+    const int top = (hi - 1) / TB * TB;
+    fetch(top);
+    for (int tb = top; tb >= pl.lo; tb -= TB) {
+        const int te = min(tb + TB, hi);
+        const bool in = tb + ptok < te;
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float v = dt[i] + (a.dt_bias && i < pvalid ? a.dt_bias[pl.c0 + pc + i] : 0.f);
+            const float v = dt[i] + bias[i];
             const float dl = !in || i >= pvalid ? 0.f : a.softplus ? ssm_softplus(v) : v;
             s_in[ptok][pc + i] = make_float2(dl, zp ? dy[i] * z[i] * sigmoid_fast(z[i]) : dy[i]);
         }
-        constexpr int NC = NP / 8;
-        for (int i = tid; i < TB * NC; i += SSM_T) {
-            const int tok = i / NC, k = (i - tok * NC) * 8;
-            float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
-            if (tb + tok < te)
-                load_row<8>(cp + (size_t)(tb + tok) * a.ldc + k, v, a.S - k, a.S - k >= 8 && !(a.how >> SSM_C & 3));
-            reinterpret_cast<float4*>(&s_c[tok][k])[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(&s_c[tok][k])[1] = make_float4(v[4], v[5], v[6], v[7]);
+        for (int j = 0; j < NPT; ++j) {
+            const int i = tid + j * SSM_T, tok = i / NC, k = (i - tok * NC) * 8;
+            if (i >= TB * NC) break;
+            reinterpret_cast<float4*>(&s_c[tok][k])[0] = make_float4(cv[j][0], cv[j][1], cv[j][2], cv[j][3]);
+            reinterpret_cast<float4*>(&s_c[tok][k])[1] = make_float4(cv[j][4], cv[j][5], cv[j][6], cv[j][7]);
         }
         __syncthreads();
-        for (int i = te - tb - 1; i >= 0; --i) {
+        fetch(tb - TB);
+        auto token = [&](int i) {
             const float2 v = s_in[i][ch];
             float c[EL];
             lds_states<EL>(&s_c[i][n0], c);
 #pragma unroll
             for (int e = 0; e < EL; ++e) r[e] = ex2(v.x * A2[e]) * fmaf(c[e], v.y, r[e]);
             sd += v.x;
+        };
+        if (te - tb == TB) {
+#pragma unroll 8
+            for (int i = TB - 1; i >= 0; --i) token(i);
+        } else {
+#pragma unroll 1
+            for (int i = te - tb - 1; i >= 0; --i) token(i);
         }
         __syncthreads();
     }

@@ -229,6 +229,17 @@ __device__ __forceinline__ void copy_row_async(TI* dst, const TI* src, int n, in
         copy_row_slow<TI, V>(dst, src, n, how);
     }
 }
+// The same of a row that is there and aligned.
+template <typename TI, int V>
+__device__ __forceinline__ void copy_whole_async(TI* dst, const TI* src) {
+    constexpr int BYTES = V * (int)sizeof(TI), ONE = BYTES < 16 ? BYTES : 16;
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+#pragma unroll
+    for (int i = 0; i < BYTES; i += ONE) {
+        if (ONE == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i), "l"(reinterpret_cast<const char*>(src) + i) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d + i), "l"(reinterpret_cast<const char*>(src) + i), "n"(ONE < 16 ? ONE : 8) : "memory");
+    }
+}
 template <typename TI>
 __device__ __forceinline__ void copy8_async(TI* dst, const TI* src, int n, int how) { copy_row_async<TI, 8>(dst, src, n, how); }
 // One aligned access of 4, 8 or 16 bytes, asynchronously.

@@ -131,6 +131,7 @@ struct Share {
     const TI* src[2][IT];
     size_t step[2];
     int how[2], tok[IT], pc, valid, left;   // left: tokens from the next tile to fetch on
+    bool whole;                             // all CP channels are there, in rows that are aligned
     __device__ __forceinline__ void start(int tid, const SsmPlace& pl, int first, const void* s0, size_t ld0, int how0,
                                           const void* s1, size_t ld1, int how1, size_t row0) {
         pc = (tid % PER) * CP;
@@ -138,6 +139,7 @@ struct Share {
         left = pl.hi - first;
         how[0] = how0;
         how[1] = how1;
+        whole = valid >= CP && how0 == 0 && (how1 == 0 || !s1);
         step[0] = Sh::TT * ld0;
         step[1] = Sh::TT * ld1;
 #pragma unroll
@@ -148,7 +150,18 @@ struct Share {
         }
     }
     __device__ __forceinline__ void fetch(TI (*stage)[IT][PT][CP], int tid) {
-        if (left > 0) {
+        if (whole && left >= Sh::TT) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                copy_whole_async<TI, CP>(stage[0][i][tid], src[0][i]);
+                src[0][i] += step[0];
+                if (src[1][i]) {
+                    copy_whole_async<TI, CP>(stage[1][i][tid], src[1][i]);
+                    src[1][i] += step[1];
+                }
+            }
+            left -= Sh::TT;
+        } else if (left > 0) {
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int n = tok[i] < left ? valid : 0;
@@ -278,10 +291,20 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
         const size_t bld = brow ? a.ldc : a.ldb;
         const TI* bsrc = static_cast<const TI*>(brow ? a.c : a.b) + (tok0 + first_tile) * bld + (size_t)pl.g * a.S + bl * EL;
         int bleft = pl.hi - first_tile;
+        const bool bwhole = bvalid >= EL && bhow == 0 && EL * sizeof(TI) >= 4;
+        size_t boff[PP];
+#pragma unroll
+        for (int p = 0; p < PP; ++p) boff[p] = (tid + p * PT) / (4 * NROW) * bld;
         auto fetch = [&](int k) {
             const int st = k % STAGES;
             sh.fetch(sm.front[st], tid);
-            if (bleft > 0) {
+            if (bwhole && bleft >= TT) {
+#pragma unroll
+                for (int p = 0; p < PP; ++p)
+                    if (tid + p * PT < Sh::PIECES) copy_whole_async<TI, EL>(sm.bc[st][p][tid], bsrc + boff[p]);
+                bsrc += TT * bld;
+                bleft -= TT;
+            } else if (bleft > 0) {
 #pragma unroll
                 for (int p = 0; p < PP; ++p) {
                     const int btok = (tid + p * PT) / (4 * NROW);

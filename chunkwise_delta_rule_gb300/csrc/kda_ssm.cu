@@ -46,8 +46,7 @@ struct FwdShape {
     static constexpr int MOST = sizeof(TI) == 2 ? 32 : 16, TT = 128 / EL < MOST ? 128 / EL : MOST;
     static constexpr int COLS = TT * NROW * EL;          // columns of a tile
     static constexpr int ALLOC = 2 * COLS < 32 ? 32 : 2 * COLS;
-    static constexpr int CP = TT * CH / PT < 8 ? TT * CH / PT : 8;   // channels of a token together in a thread around the recurrence
-    static constexpr int IT = TT * CH / PT / CP;         // its tokens
+    static constexpr int IT = 2, CP = TT * CH / PT / IT; // a thread's share around the recurrence: CP channels of two successive tokens
     static constexpr int PIECES = TT * NROW * 4;         // (token, row, lane group) of EL states
     static constexpr int PP = (PIECES + PT - 1) / PT;    // per thread
     static constexpr int STAGES = 4;                     // tiles in copies
@@ -59,18 +58,18 @@ struct FwdShape {
         TI front[STAGES][2][IT][PT][CP];                 // x, dt
         TI back[HAS_Y ? STAGES : 1][2][IT][PT][CP];      // x, z
         TI bc[STAGES][PP][PT][EL];
-        float2 du[2][TT][CH];                            // delta, u
-        float y[2][HAS_Y ? TT : 1][CH][4];               // the four lanes' parts; see ch_at
+        float4 du[2][TT / 2][CH];                        // delta, u of two tokens; see du_at
+        float4 y[2][HAS_Y ? TT / 2 : 1][2 * CH];         // two lanes' parts of two tokens; see y_at
         uint64_t full[2], mma[2], done[2], yfree[2];     // hand-overs of a tile's buffers
         uint32_t tmem;
     };
     static_assert(CP % 2 == 0 && sizeof(Smem) + 1024 <= 227 * 1024, "tile shape");
 };
 
-// Place of a channel in a token's row, permuted so that the eight threads of a quarter warp, which hold a few
-// neighbouring channels each, reach distinct banks.
-__device__ __forceinline__ int ch_at(int ch) { return ch ^ ((ch >> 3) & 7); }
-__device__ __forceinline__ int du_at(int ch) { return ch ^ ((ch >> 3) & 6); }   // pairs stay together
+// Places of a channel in the rows of two tokens' steps, and of its lanes 2 half and 2 half + 1 in those of their outputs,
+// permuted so that the eight threads of a quarter warp, which hold a few neighbouring channels each, reach distinct banks.
+__device__ __forceinline__ int du_at(int ch) { return ch ^ ((ch >> 3) & 7); }
+__device__ __forceinline__ int y_at(int ch, int half) { return (2 * ch + half) ^ ((ch >> 3) & 7); }
 
 // Byte of column n of k-row k in an operand whose columns are contiguous (128-byte swizzle).
 __device__ __forceinline__ int op_at(int k, int n) {
@@ -144,7 +143,7 @@ struct Share {
         step[1] = Sh::TT * ld1;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            tok[i] = (tid + i * PT) / PER;
+            tok[i] = tid / PER * IT + i;
             src[0][i] = static_cast<const TI*>(s0) + (row0 + first + tok[i]) * ld0 + pl.c0 + pc;
             src[1][i] = s1 ? static_cast<const TI*>(s1) + (row0 + first + tok[i]) * ld1 + pl.c0 + pc : nullptr;
         }
@@ -258,23 +257,28 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
             copies_commit();
             copies_wait<STAGES - 1>();
             await(&sm.done[w], k >> 1);
-#pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int row = sh.tok[it], tok = first_tile + k * TT + row;
-                if (tok >= pl.hi || sh.valid <= 0) continue;
-                float o[CP], x[CP], z[CP];
-                load_part<CP>(sm.back[st][0][it][tid], x);
-                if (gate) load_part<CP>(sm.back[st][1][it][tid], z);
+            const int row = sh.tok[0], tok = first_tile + k * TT + row;
+            if (tok < pl.hi && sh.valid > 0) {
+                float2 sum[CP];   // over the lanes, of the two tokens
 #pragma unroll
                 for (int i = 0; i < CP; ++i) {
-                    const float4 v = *reinterpret_cast<const float4*>(sm.y[w][HAS_Y ? row : 0][ch_at(sh.pc + i)]);
-                    o[i] = fmaf(skip[i], x[i], (v.x + v.y) + (v.z + v.w));
+                    const float4 p = sm.y[w][HAS_Y ? row / 2 : 0][y_at(sh.pc + i, 0)], q = sm.y[w][HAS_Y ? row / 2 : 0][y_at(sh.pc + i, 1)];
+                    sum[i] = add2(add2(make_float2(p.x, p.y), make_float2(p.z, p.w)), add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
                 }
-                if (gate) {
 #pragma unroll
-                    for (int i = 0; i < CP; ++i) o[i] *= z[i] * sigmoid_fast(z[i]);
+                for (int it = 0; it < IT; ++it) {
+                    if (tok + it >= pl.hi) break;
+                    float o[CP], x[CP], z[CP];
+                    load_part<CP>(sm.back[st][0][it][tid], x);
+                    if (gate) load_part<CP>(sm.back[st][1][it][tid], z);
+#pragma unroll
+                    for (int i = 0; i < CP; ++i) o[i] = fmaf(skip[i], x[i], it ? sum[i].y : sum[i].x);
+                    if (gate) {
+#pragma unroll
+                        for (int i = 0; i < CP; ++i) o[i] *= z[i] * sigmoid_fast(z[i]);
+                    }
+                    store_part<TI, CP>(static_cast<TI*>(a.y) + (tok0 + tok + it) * a.D + pl.c0 + sh.pc, o, sh.valid, whole);
                 }
-                store_part<TI, CP>(static_cast<TI*>(a.y) + (tok0 + tok) * a.D + pl.c0 + sh.pc, o, sh.valid, whole);
             }
             hand_over(&sm.yfree[w]);
         }
@@ -334,18 +338,24 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
                 tc::mma_bf16_w(tmem + w * COLS, adesc, tc::sdesc_mn(tc::smem_u32(sm.b[w]), Sh::ATOM, 0), idesc, 0);
                 tc::mma_commit_w(&sm.mma[w]);
             }
+            float2 dl[IT][CP / 2], u[IT][CP / 2];
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
                 float x[CP], dt[CP];
                 load_part<CP>(sm.front[st][0][it][tid], x);
                 load_part<CP>(sm.front[st][1][it][tid], dt);
 #pragma unroll
-                for (int i = 0; i < CP; i += 2) {
-                    float2 dl = make_float2(dt[i] + bias[i], dt[i + 1] + bias[i + 1]);
-                    if (a.softplus) dl = ssm_softplus2(dl);
-                    const float2 u = mul2(dl, make_float2(x[i], x[i + 1]));
-                    *reinterpret_cast<float4*>(&sm.du[w][sh.tok[it]][du_at(sh.pc + i)]) = make_float4(dl.x, u.x, dl.y, u.y);
+                for (int i = 0; i < CP / 2; ++i) {
+                    dl[it][i] = make_float2(dt[2 * i] + bias[2 * i], dt[2 * i + 1] + bias[2 * i + 1]);
+                    if (a.softplus) dl[it][i] = ssm_softplus2(dl[it][i]);
+                    u[it][i] = mul2(dl[it][i], make_float2(x[2 * i], x[2 * i + 1]));
                 }
+            }
+            float4* du = sm.du[w][sh.tok[0] / 2];
+#pragma unroll
+            for (int i = 0; i < CP / 2; ++i) {
+                du[du_at(sh.pc + 2 * i)] = make_float4(dl[0][i].x, u[0][i].x, dl[1][i].x, u[1][i].x);
+                du[du_at(sh.pc + 2 * i + 1)] = make_float4(dl[0][i].y, u[0][i].y, dl[1][i].y, u[1][i].y);
             }
             hand_over(&sm.full[w]);
         }
@@ -386,13 +396,23 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
         }
         constexpr int N = 16 / EL;              // tokens of a batch of operands
         constexpr int NCOL = N * NROW * EL;     // their columns
-        const int my_ch = ch_at(ch), my_du = du_at(ch);
-        auto load_du = [&](int w, int i, float2(&du)[N]) {
+        const int my_du = du_at(ch), my_y = y_at(ch, l >> 1);
+        // PAIR: from an even tile row
+        auto load_du = [&](bool pair, int w, int i, float2(&du)[N]) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) du[j] = sm.du[w][i + j][my_du];
+            for (int j = 0; j < N; ++j) {
+                if (pair) {
+                    if (j & 1) continue;
+                    const float4 v = sm.du[w][(i + j) / 2][my_du];
+                    du[j] = make_float2(v.x, v.y);
+                    du[j + 1 < N ? j + 1 : j] = make_float2(v.z, v.w);
+                } else {
+                    du[j] = reinterpret_cast<const float2*>(&sm.du[w][(i + j) / 2][my_du])[(i + j) & 1];
+                }
+            }
         };
         // the first n tokens of a batch from tile row i
-        auto run_tokens = [&](int w, int i, int n, const float2(&du)[N], const uint32_t(&bc)[NCOL]) {
+        auto run_tokens = [&](bool pair, int w, int i, int n, const float2(&du)[N], const uint32_t(&bc)[NCOL]) {
             float2 acc[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) {
@@ -416,8 +436,16 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
             }
             if (HAS_Y) {
 #pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (j < n) sm.y[w][HAS_Y ? i + j : 0][my_ch][l] = acc[j].x + acc[j].y;
+                for (int j = 0; j < N; ++j) {
+                    if (j >= n) break;
+                    float* to = reinterpret_cast<float*>(&sm.y[w][HAS_Y ? (i + j) / 2 : 0][my_y]) + 2 * (l & 1);
+                    if (pair) {
+                        const int o = j + 1 < N ? j + 1 : j;
+                        if (!(j & 1)) *reinterpret_cast<float2*>(to) = make_float2(acc[j].x + acc[j].y, acc[o].x + acc[o].y);
+                    } else {
+                        to[(i + j) & 1] = acc[j].x + acc[j].y;
+                    }
+                }
             }
         };
         auto checkpoint = [&](int tok) {
@@ -443,7 +471,8 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
                 uint32_t bc[2][NCOL];
                 float2 du[2][N];
                 spread_load<NCOL>(cols, bc[0]);
-                load_du(w, 0, du[0]);
+                constexpr bool pair = N % 2 == 0;
+                load_du(pair, w, 0, du[0]);
 #pragma unroll
                 for (int i = 0; i < TT; i += N) {
                     const int cur = (i / N) & 1;
@@ -451,9 +480,9 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
                     tc::tmem_wait_ld();
                     if (i + N < TT) {
                         spread_load<NCOL>(cols + (i + N) * NROW * EL, bc[cur ^ 1]);
-                        load_du(w, i + N, du[cur ^ 1]);
+                        load_du(pair, w, i + N, du[cur ^ 1]);
                     }
-                    run_tokens(w, i, N, du[cur], bc[cur]);
+                    run_tokens(pair, w, i, N, du[cur], bc[cur]);
                 }
             } else {
                 while (t < te) {
@@ -470,11 +499,11 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
                     // a batch that starts near the tile's end would read past its columns: it starts earlier there
                     const int at = min(t - tb, TT - N);
                     spread_load<NCOL>(cols + at * NROW * EL, bc);
-                    load_du(w, at, du);
+                    load_du(false, w, at, du);
                     tc::tmem_wait_ld();
                     const int skip = t - tb - at;
                     if (skip == 0 && t + N <= run) {
-                        run_tokens(w, at, N, du, bc);
+                        run_tokens(false, w, at, N, du, bc);
                         t += N;
                     } else {
                         // one token: the batch's entry `skip` brought to its front
@@ -485,7 +514,7 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
 #pragma unroll
                                 for (int e = 0; e < NROW * EL; ++e) bc[e] = bc[j * NROW * EL + e];
                             }
-                        run_tokens(w, t - tb, 1, du, bc);
+                        run_tokens(false, w, t - tb, 1, du, bc);
                         ++t;
                     }
                 }

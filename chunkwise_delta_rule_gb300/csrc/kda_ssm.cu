@@ -60,7 +60,7 @@ struct FwdShape {
         TI bc[STAGES][PP][PT][EL];
         float4 du[2][TT / 2][CH];                        // delta, u of two tokens; see du_at
         float4 y[2][HAS_Y ? TT / 2 : 1][2 * CH];         // two lanes' parts of two tokens; see y_at
-        uint64_t full[2], mma[2], done[2], yfree[2];     // hand-overs of a tile's buffers
+        uint64_t full[2], done[2], yfree[2];             // hand-overs of a tile's buffers
         uint32_t tmem;
     };
     static_assert(CP % 2 == 0 && sizeof(Smem) + 1024 <= 227 * 1024, "tile shape");
@@ -208,8 +208,7 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            tc::mbar_init(&sm.full[w], PT / 32);
-            tc::mbar_init(&sm.mma[w], 1);
+            tc::mbar_init(&sm.full[w], PT / 32 + 1);   // the warps' steps and the spread rows
             tc::mbar_init(&sm.done[w], RT / 32);
             tc::mbar_init(&sm.yfree[w], PT / 32);
         }
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
             if (threadIdx.x < RT + 32) {
                 tc::fence_after_sync();
                 tc::mma_bf16_w(tmem + w * COLS, adesc, tc::sdesc_mn(tc::smem_u32(sm.b[w]), Sh::ATOM, 0), idesc, 0);
-                tc::mma_commit_w(&sm.mma[w]);
+                tc::mma_commit_w(&sm.full[w]);
             }
             float2 dl[IT][CP / 2], u[IT][CP / 2];
 #pragma unroll
@@ -454,7 +453,6 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
         };
         for (int k = 0; k < ntiles; ++k) {
             const int tb = first_tile + k * TT, te = min(tb + TT, pl.hi), w = k & 1;
-            await(&sm.mma[w], k >> 1);
             await(&sm.full[w], k >> 1);
             if (HAS_Y && k >= 2) await(&sm.yfree[w], (k >> 1) - 1);
             __syncwarp();

@@ -22,12 +22,12 @@ constexpr int SSM_CH = 32;    // channels per CTA
 __device__ __forceinline__ float2 ssm_softplus2(float2 v) {
     const float2 e = make_float2(ex2(-LOG2E * fabsf(v.x)), ex2(-LOG2E * fabsf(v.y)));
     const float2 s = mul2(e, make_float2(rcp(2.f + e.x), rcp(2.f + e.y))), q = mul2(s, s);
-    float2 p = make_float2(0.140788892f, 0.140788892f);
-    p = fma2(p, q, make_float2(0.139825789f, 0.139825789f));
-    p = fma2(p, q, make_float2(0.200122976f, 0.200122976f));
-    p = fma2(p, q, make_float2(0.333331608f, 0.333331608f));
-    p = fma2(p, q, make_float2(1.f, 1.f));
-    return fma2(mul2(p, s), make_float2(2.f, 2.f), make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+    float2 p = make_float2(0.281577796f, 0.281577796f);
+    p = fma2(p, q, make_float2(0.279651582f, 0.279651582f));
+    p = fma2(p, q, make_float2(0.400245965f, 0.400245965f));
+    p = fma2(p, q, make_float2(0.666663229f, 0.666663229f));
+    p = fma2(p, q, make_float2(2.f, 2.f));
+    return fma2(p, s, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
 __device__ __forceinline__ float ssm_softplus(float v) { return ssm_softplus2(make_float2(v, v)).x; }
 

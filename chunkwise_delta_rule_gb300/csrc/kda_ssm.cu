@@ -58,8 +58,8 @@ struct FwdShape {
         TI front[STAGES][2][IT][PT][CP];                 // x, dt
         TI back[HAS_Y ? STAGES : 1][2][IT][PT][CP];      // x, z
         TI bc[STAGES][PP][PT][EL];
-        float4 du[2][TT / 2][CH];                        // delta, u of two tokens; see du_at
-        float4 y[2][HAS_Y ? TT / 2 : 1][2 * CH];         // two lanes' parts of two tokens; see y_at
+        float4 du[2][TT / 2][CH + CH / 8];               // delta, u of two tokens; see du_at
+        float4 y[2][HAS_Y ? TT / 2 : 1][2 * CH + CH / 8]; // two lanes' parts of two tokens; see y_at
         uint64_t full[2], done[2], yfree[2];             // hand-overs of a tile's buffers
         uint32_t tmem;
     };
@@ -67,9 +67,10 @@ struct FwdShape {
 };
 
 // Places of a channel in the rows of two tokens' steps, and of its lanes 2 half and 2 half + 1 in those of their outputs,
-// permuted so that the eight threads of a quarter warp, which hold a few neighbouring channels each, reach distinct banks.
-__device__ __forceinline__ int du_at(int ch) { return ch ^ ((ch >> 3) & 7); }
-__device__ __forceinline__ int y_at(int ch, int half) { return (2 * ch + half) ^ ((ch >> 3) & 7); }
+// spaced so that the eight threads of a quarter warp, which hold a few neighbouring channels each, reach distinct banks
+// (and so that a thread's places are a constant apart: permuted ones took an instruction each).
+__device__ __forceinline__ int du_at(int ch) { return ch + (ch >> 3); }
+__device__ __forceinline__ int y_at(int ch, int half) { return 2 * ch + half + (ch >> 3); }
 
 // Byte of column n of k-row k in an operand whose columns are contiguous (128-byte swizzle).
 __device__ __forceinline__ int op_at(int k, int n) {

@@ -39,17 +39,17 @@ struct BwdShape {
     struct Smem {
         TI tok[STAGES][4][HT][CP];            // x, dt, dy, z
         TI bc[STAGES][NBC][HT][8];
-        float4 in[2][TB][CH];                 // delta, u, d0
-        float4 out[2][TB][CH];                // s1, s2 (in log2 units), sum C h
+        float4 in[2][TB][CH + CH / 8];               // delta, u, d0
+        float4 out[2][TB][CH + CH / 8];              // s1, s2 (in log2 units), sum C h
         float b[2][TB][NP], c[2][TB][NP];
         float red[2][RW][TB][2 * NP];
         float sub[NSUB > 1 ? NSUB - 1 : 1][EL][RT];
     };
 };
 
-// Place of a channel in a token's row, permuted so that the eight threads of a quarter warp, of eight (or four)
+// Place of a channel in a token's row, spaced so that the eight threads of a quarter warp, of eight (or four)
 // neighbouring channels each, reach distinct banks.
-__device__ __forceinline__ int in_at(int ch) { return ch ^ ((ch >> 3) & 7); }
+__device__ __forceinline__ int in_at(int ch) { return ch + (ch >> 3); }
 
 __device__ __forceinline__ void named_barrier(int id, int count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");

@@ -32,8 +32,9 @@ struct BwdShape {
     // instructions each) has to stay in the instruction cache
     static constexpr int L = EL <= 4 ? 8 : 64 / EL;
     static constexpr int NSUB = TB / L;
-    static constexpr int VB = 2 * EL;                     // dB and dC values of a lane
-    static constexpr int KEEP = VB >= 8 ? VB / 8 : 1;     // ... it holds after the sum over 8 channels
+    static constexpr int KEEP = EL >= 4 ? EL / 4 : 1;     // dB and dC values a lane holds after the sum over 8 channels
+    // copies of the rows b and c, each in an order of its own inside four states (see the sums over channels)
+    static constexpr int NVER = EL == 4 ? 4 : EL == 16 ? 1 : 2;
     static constexpr int NBC = (TB * 2 * (NP / 8) + HT - 1) / HT;   // chunks of 8 states of b and c per thread
     static constexpr int STAGES = 5;                      // tiles: the one after, the present, the one before, two on their way
     struct Smem {
@@ -41,7 +42,7 @@ struct BwdShape {
         TI bc[STAGES][NBC][HT][8];
         float4 in[2][TB][CH + CH / 8];               // delta, u, d0
         float4 out[2][TB][CH + CH / 8];              // s1, s2 (in log2 units), sum C h
-        float b[2][TB][NP], c[2][TB][NP];
+        float b[2][NVER][TB * NP + 16], c[2][NVER][TB * NP + 16];   // the copies start in other banks
         float red[2][RW][TB][2 * NP];
         float sub[NSUB > 1 ? NSUB - 1 : 1][EL][RT];
     };
@@ -59,7 +60,7 @@ template <typename TI, int EL>
 __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArgs a) {
     using Sh = BwdShape<TI, EL>;
     constexpr int NP = Sh::NP, P = Sh::P, RT = Sh::RT, CH = Sh::CH, RW = Sh::RW, CP = Sh::CP, L = Sh::L, NSUB = Sh::NSUB,
-                  VB = Sh::VB, KEEP = Sh::KEEP, NBC = Sh::NBC, STAGES = Sh::STAGES;
+                  KEEP = Sh::KEEP, NVER = Sh::NVER, NBC = Sh::NBC, STAGES = Sh::STAGES;
     extern __shared__ __align__(16) unsigned char raw_smem[];
     typename Sh::Smem& sm = *reinterpret_cast<typename Sh::Smem*>(raw_smem);
     const SsmPlace pl = ssm_place<CH>(a);
@@ -179,9 +180,13 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
                     const int r = isc ? i - TB * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
                     float v[8];
                     load_row<8>(sm.bc[st][j][tid], v, 8, true);
-                    float4* dst = reinterpret_cast<float4*>(isc ? &sm.c[w][tok][k8] : &sm.b[w][tok][k8]);
-                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+                    for (int ver = 0; ver < NVER; ++ver) {
+                        const int x = EL == 8 ? 2 * ver : ver;
+                        float4* dst = reinterpret_cast<float4*>((isc ? sm.c[w][ver] : sm.b[w][ver]) + tok * NP + k8);
+                        dst[0] = make_float4(v[x], v[1 ^ x], v[2 ^ x], v[3 ^ x]);
+                        dst[1] = make_float4(v[4 + x], v[4 + (1 ^ x)], v[4 + (2 ^ x)], v[4 + (3 ^ x)]);
+                    }
                 }
             }
             fetch(k + STAGES - 1);   // into the stage of tile k - 1, which was read last
@@ -215,20 +220,63 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
         A2[e] = on && n0 + e < a.S ? -expf(A2[e]) * LOG2E : 0.f;
         r[e] = dA[e] = 0.f;
     }
+    // The sums over a warp's channels halve a lane's values at each exchange. So that nothing has to be chosen between,
+    // a lane's states are held in the order n0 + (e ^ order), where lanes that exchange differ in the part of `order`
+    // they exchange by: each sends the upper half of its registers and adds what arrives to its lower half.
+    constexpr int O1 = EL / 2, O2 = EL >= 4 ? EL / 4 : 0;
+    const int order = (lane & 8 ? O1 : 0) | (lane & 16 ? O2 : 0);
+    const int my_ver = EL == 8 ? (order & 3) >> 1 : order & 3, my_n0 = n0 + (order & ~3);
+    auto reorder = [&](float(&v)[EL]) {   // to that order or back
+#pragma unroll
+        for (int e = 0; e < EL; ++e)
+            if (!(e & O1)) {
+                const float x = v[e], y = v[e ^ O1];
+                v[e] = lane & 8 ? y : x;
+                v[e ^ O1] = lane & 8 ? x : y;
+            }
+#pragma unroll
+        for (int e = 0; e < EL; ++e)
+            if (O2 && !(e & O2)) {
+                const float x = v[e], y = v[e ^ O2];
+                v[e] = lane & 16 ? y : x;
+                v[e ^ O2] = lane & 16 ? x : y;
+            }
+    };
+    auto lds_row = [&](const float* row, float(&v)[EL]) {
+        if (EL == 2) {
+            const float2 q = *reinterpret_cast<const float2*>(row + n0);
+            v[0] = q.x;
+            v[EL > 1 ? 1 : 0] = q.y;
+        } else {
+#pragma unroll
+            for (int e = 0; e + 3 < EL; e += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(row + (EL > 4 ? n0 + (e ^ (order & ~3)) : my_n0));
+                v[e] = q.x; v[e + 1] = q.y; v[e + 2] = q.z; v[e + 3] = q.w;
+            }
+        }
+    };
     auto state_of = [&](const float* base, int n, float(&v)[EL]) {
         if (base) {
             load_states<EL>(base + n * DS + (size_t)d * a.S, n0, a.S, on, v);
+            reorder(v);
         } else {
 #pragma unroll
             for (int e = 0; e < EL; ++e) v[e] = 0.f;
         }
+    };
+    auto put_states = [&](float* base, int n, const float(&v)[EL]) {
+        float x[EL];
+#pragma unroll
+        for (int e = 0; e < EL; ++e) x[e] = v[e];
+        reorder(x);
+        store_states<EL>(base + n * DS + (size_t)d * a.S, n0, a.S, on, x);
     };
     if (a.dh0 && (a.ax.cu || a.ax.len == 0)) {   // sequences without tokens: their adjoint passes through
         for (int n = pl.unit; n < a.ax.N; n += pl.units) {
             if (a.ax.cu && axis_cu(a.ax, n + 1) > axis_cu(a.ax, n)) continue;
             float v[EL];
             state_of(a.dht, n, v);
-            store_states<EL>(a.dh0 + n * DS + (size_t)d * a.S, n0, a.S, on, v);
+            put_states(a.dh0, n, v);
         }
     }
     Seq s{0, 0, 0};
@@ -240,19 +288,21 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
             join_pieces<EL>(a, a.rloc, pl.row, q, pl.u, -1, d, n0, on, A2, r);
         }
     }
+    reorder(A2);
+    reorder(r);
     const size_t slot0 = (size_t)pl.row * ((a.ax.len + TB - 1) / TB);
     float hnext[EL];   // the next tile's checkpoint, on its way
     if (ntiles > 0) load_states<EL>(a.ckpt + (slot0 + tile_begin(0) / TB) * DS + (size_t)d * a.S, n0, a.S, on, hnext);
     const int my_in = in_at(ch);
-    // the first of the values a lane holds after the sum over channels: dB of state n0 + f for f < EL, then dC
-    int my_red = (lane & 4 ? VB / 2 : 0) + (lane & 8 ? VB / 4 : 0) + (VB >= 8 && lane & 16 ? VB / 8 : 0);
-    my_red = my_red < EL ? n0 + my_red : NP + n0 + my_red - EL;
+    // the first of the values a lane holds after the sums over channels: dB of a state, or its dC in lanes with bit 2
+    const int my_red = (lane & 4 ? NP : 0) + n0 + order;
     __syncthreads();   // the first tile's inputs
     for (int k = 0; k < ntiles; ++k) {
         const int tb = tile_begin(k), te = min(tb + TB, pl.hi), nt = te - tb, w = k & 1;
         float hstart[EL];
 #pragma unroll
         for (int e = 0; e < EL; ++e) hstart[e] = hnext[e];
+        reorder(hstart);
         if (k + 1 < ntiles) load_states<EL>(a.ckpt + (slot0 + tile_begin(k + 1) / TB) * DS + (size_t)d * a.S, n0, a.S, on, hnext);
         // first and last tokens of sequences inside the tile
         uint32_t starts = 0, ends = 0;
@@ -270,7 +320,7 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
         auto step = [&](int i, float(&h)[EL]) {
             const float2 v = *reinterpret_cast<const float2*>(&sm.in[w][i][my_in]);
             float b[EL];
-            lds_states<EL>(&sm.b[w][i][n0], b);
+            lds_row(sm.b[w][my_ver] + i * NP, b);
             const float2 dl = make_float2(v.x, v.x), u = make_float2(v.y, v.y);
 #pragma unroll
             for (int e = 0; e < P; ++e) {
@@ -284,9 +334,9 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
         // one token of the adjoint, from its state h and the one before it
         auto reverse = [&](int it, const float(&h)[EL], const float(&hp)[EL]) {
             const float4 v = sm.in[w][it][my_in];
-            float b[EL], c[EL], bc[VB];
-            lds_states<EL>(&sm.b[w][it][n0], b);
-            lds_states<EL>(&sm.c[w][it][n0], c);
+            float b[EL], c[EL], db[EL], dc[EL];
+            lds_row(sm.b[w][my_ver] + it * NP, b);
+            lds_row(sm.c[w][my_ver] + it * NP, c);
             const float2 dl = make_float2(v.x, v.x), u = make_float2(v.y, v.y), d0 = make_float2(v.z, v.z);
             float2 p1, p2, py;
 #pragma unroll
@@ -295,7 +345,7 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
                 const float2 AA = make_float2(A2[2 * e], A2[2 * e + 1]), bb = make_float2(b[2 * e], b[2 * e + 1]);
                 const float2 g = fma2(cc, d0, make_float2(r[2 * e], r[2 * e + 1]));
                 const float2 x = mul2(dl, AA);
-                const float2 dc = mul2(d0, hh), dbv = mul2(u, g);
+                const float2 dcv = mul2(d0, hh), dbv = mul2(u, g);
                 const float2 rn = mul2(make_float2(ex2(x.x), ex2(x.y)), g);
                 const float2 wv = mul2(rn, make_float2(hp[2 * e], hp[2 * e + 1]));
                 py = e == 0 ? mul2(hh, cc) : fma2(hh, cc, py);
@@ -306,26 +356,36 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
                 dA[2 * e + 1] = da.y;
                 r[2 * e] = rn.x;
                 r[2 * e + 1] = rn.y;
-                bc[2 * e] = dbv.x;
-                bc[2 * e + 1] = dbv.y;
-                bc[EL + 2 * e] = dc.x;
-                bc[EL + 2 * e + 1] = dc.y;
+                db[2 * e] = dbv.x;
+                db[2 * e + 1] = dbv.y;
+                dc[2 * e] = dcv.x;
+                dc[2 * e + 1] = dcv.y;
             }
             // over the channel's four lanes: lane 0 keeps s1, lane 1 s2, lane 2 sum C h
             float pv[4] = {p1.x + p1.y, p2.x + p2.y, py.x + py.y, 0.f};
             halve<4>(pv, l, 2);
             halve<2>(pv, l, 1);
             reinterpret_cast<float*>(&sm.out[w][it][my_in])[l] = pv[0];
-            // over the warp's 8 channels: lane bits 2, 3, 4
-            halve<VB>(bc, lane, 4);
-            halve<VB / 2>(bc, lane, 8);
-            if constexpr (VB >= 8) halve<VB / 4>(bc, lane, 16);
-            else bc[0] += __shfl_xor_sync(SSM_FULL, bc[0], 16);
+            // over the warp's 8 channels: lane bits 3 and 4 by the states' order, bit 2 with dB against dC
 #pragma unroll
-            for (int f = 0; f < KEEP; ++f) sm.red[w][warp][it][my_red + f] = bc[f];
+            for (int e = 0; e < O1; ++e) {
+                db[e] += __shfl_xor_sync(SSM_FULL, db[e + O1], 8);
+                dc[e] += __shfl_xor_sync(SSM_FULL, dc[e + O1], 8);
+            }
+#pragma unroll
+            for (int e = 0; e < O2; ++e) {
+                db[e] += __shfl_xor_sync(SSM_FULL, db[e + O2], 16);
+                dc[e] += __shfl_xor_sync(SSM_FULL, dc[e + O2], 16);
+            }
+#pragma unroll
+            for (int f = 0; f < KEEP; ++f) {
+                float v = (lane & 4 ? dc[f] : db[f]) + __shfl_xor_sync(SSM_FULL, lane & 4 ? db[f] : dc[f], 4);
+                if (!O2) v += __shfl_xor_sync(SSM_FULL, v, 16);
+                sm.red[w][warp][it][my_red + f] = v;
+            }
         };
         auto leave = [&](int n) {   // at the first token of sequence n its state's adjoint goes out
-            if (a.dh0) store_states<EL>(a.dh0 + n * DS + (size_t)d * a.S, n0, a.S, on, r);
+            if (a.dh0) put_states(a.dh0, n, r);
 #pragma unroll
             for (int e = 0; e < EL; ++e) r[e] = 0.f;
         };
@@ -396,7 +456,7 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
         }
         __syncthreads();
     }
-    store_states<EL>(a.pA + pl.unit * DS + (size_t)d * a.S, n0, a.S, on, dA);
+    put_states(a.pA, pl.unit, dA);
 }
 
 // Local adjoint leaving a time piece's first token: from dht where the piece's sequence ends inside it, else from zero.

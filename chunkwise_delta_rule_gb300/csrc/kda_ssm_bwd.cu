@@ -74,38 +74,62 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
         // ---------------------------------------------------------------- around the recurrences
         const int tid = threadIdx.x - RT;
         const int ptok = tid >> 3, pc = (tid & 7) * CP, pvalid = pl.nch - pc;   // one token, CP channels
-        const TI* src[4] = {static_cast<const TI*>(a.x) + tok0 * a.ldx + pl.c0 + pc,
-                            static_cast<const TI*>(a.dt) + tok0 * a.lddt + pl.c0 + pc,
-                            static_cast<const TI*>(a.dy) + tok0 * a.D + pl.c0 + pc,
-                            a.z ? static_cast<const TI*>(a.z) + tok0 * a.ldz + pl.c0 + pc : nullptr};
         const size_t ld[4] = {a.ldx, a.lddt, (size_t)a.D, a.ldz};
         constexpr int SHIFT[4] = {SSM_X, SSM_DT, SSM_DY, SSM_Z};
-        const TI* bp = static_cast<const TI*>(a.b) + tok0 * a.ldb + (size_t)pl.g * a.S;
-        const TI* cp = static_cast<const TI*>(a.c) + tok0 * a.ldc + (size_t)pl.g * a.S;
+        const bool gate = a.z != nullptr;
         constexpr int NC = NP / 8;
+        // the rows of the next tile to fetch (tiles run backwards); whole ones of a whole tile need no checks
+        const int first = tile_begin(0);
+        const TI *tok_src[4], *bc_src[NBC];
+        bool whole_rows = pvalid >= CP;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const void* base = q == 0 ? a.x : q == 1 ? a.dt : q == 2 ? a.dy : a.z;
+            tok_src[q] = static_cast<const TI*>(base) + (tok0 + first + ptok) * ld[q] + pl.c0 + pc;
+            whole_rows = whole_rows && ((q == 3 && !gate) || !(a.how >> SHIFT[q] & 3));
+        }
+#pragma unroll
+        for (int j = 0; j < NBC; ++j) {
+            const int i = tid + j * HT, isc = i >= TB * NC, r = isc ? i - TB * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
+            bc_src[j] = static_cast<const TI*>(isc ? a.c : a.b) + (tok0 + first + tok) * (isc ? a.ldc : a.ldb) + (size_t)pl.g * a.S + k8;
+            whole_rows = whole_rows && (i >= 2 * TB * NC || (k8 + 8 <= a.S && !(a.how >> (isc ? SSM_C : SSM_B) & 3)));
+        }
         auto fetch = [&](int k) {
-            if (k < ntiles) {
-                const int tb = tile_begin(k), st = k % STAGES;
-                const size_t tt = min(tb + ptok, pl.hi - 1);
+            const int tb = tile_begin(k), st = k % STAGES;
+            if (k < ntiles && whole_rows && tb + TB <= pl.hi) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q < 3 || gate) copy_whole_async<TI, CP>(sm.tok[st][q][tid], tok_src[q]);
+#pragma unroll
+                for (int j = 0; j < NBC; ++j)
+                    if (tid + j * HT < 2 * TB * NC) copy_whole_async<TI, 8>(sm.bc[st][j][tid], bc_src[j]);
+            } else if (k < ntiles) {
                 const int n = tb + ptok < pl.hi ? pvalid : 0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (q < 3 || src[3]) copy_row_async<TI, CP>(sm.tok[st][q][tid], src[q] + tt * ld[q], n, a.how >> SHIFT[q] & 3);
+                    if (q < 3 || gate)
+                        copy_row_async<TI, CP>(sm.tok[st][q][tid], n > 0 ? tok_src[q] : static_cast<const TI*>(a.x), n, a.how >> SHIFT[q] & 3);
 #pragma unroll
                 for (int j = 0; j < NBC; ++j) {
                     const int i = tid + j * HT;
                     if (i >= 2 * TB * NC) break;
                     const bool isc = i >= TB * NC;
                     const int r = isc ? i - TB * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
-                    const size_t tr = min(tb + tok, pl.hi - 1);
                     const int m = tb + tok < pl.hi ? a.S - k8 : 0;
-                    const TI* p = isc ? cp + tr * a.ldc : bp + tr * a.ldb;
-                    copy8_async(sm.bc[st][j][tid], p + (m > 0 ? k8 : 0), m, a.how >> (isc ? SSM_C : SSM_B) & 3);
+                    copy8_async(sm.bc[st][j][tid], m > 0 ? bc_src[j] : static_cast<const TI*>(a.b), m, a.how >> (isc ? SSM_C : SSM_B) & 3);
                 }
             }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tok_src[q] -= TB * ld[q];
+#pragma unroll
+            for (int j = 0; j < NBC; ++j) bc_src[j] -= TB * (tid + j * HT >= TB * NC ? a.ldc : a.ldb);
             copies_commit();
         };
         for (int k = 0; k < STAGES - 2; ++k) fetch(k);
+        // of dB and dC each thread sums one state's (or row's) place over the warps, for every ROWS-th token
+        constexpr int ROWS = HT / (2 * NP);
+        const int sum_f = tid % (2 * NP), sum_tok = tid / (2 * NP), sum_n = sum_f % NP;
+        float* sums = a.pbc + ((pl.tile * (size_t)a.ax.rows * a.ax.len + tok0 + first + sum_tok) * 2 + sum_f / NP) * a.S + sum_n;
         float bias[CP], skip[CP], dskip[CP], dbias[CP];
 #pragma unroll
         for (int i = 0; i < CP; ++i) {
@@ -122,7 +146,7 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
                     load_row<CP>(sm.tok[st][0][tid], x, CP, true);
                     load_row<CP>(sm.tok[st][1][tid], dt, CP, true);
                     load_row<CP>(sm.tok[st][2][tid], dy, CP, true);
-                    if (src[3]) load_row<CP>(sm.tok[st][3][tid], z, CP, true);
+                    if (gate) load_row<CP>(sm.tok[st][3][tid], z, CP, true);
 #pragma unroll
                     for (int i = 0; i < CP; ++i) {
                         const float4 in = sm.in[w][ptok][in_at(pc + i)];
@@ -131,7 +155,7 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
                         ox[i] = fmaf(in.x, v.x, skip[i] * in.z);
                         od[i] = fmaf(x[i], v.x, v.y * (1.f / LOG2E));
                         if (a.softplus) od[i] *= sigmoid_fast(dt[i] + bias[i]);
-                        if (src[3]) {
+                        if (gate) {
                             const float sg = sigmoid_fast(z[i]);
                             oz[i] = dy[i] * y0 * sg * fmaf(z[i], 1.f - sg, 1.f);
                         }
@@ -144,15 +168,16 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
                     const bool whole = pvalid >= CP && !(a.how >> SSM_OUT & 3);
                     store_part<TI, CP>(static_cast<TI*>(a.dx) + o, ox, pvalid, whole);
                     store_part<TI, CP>(static_cast<TI*>(a.ddt) + o, od, pvalid, whole);
-                    if (src[3]) store_part<TI, CP>(static_cast<TI*>(a.dz) + o, oz, pvalid, whole);
+                    if (gate) store_part<TI, CP>(static_cast<TI*>(a.dz) + o, oz, pvalid, whole);
                 }
-                for (int i = tid; i < nt * 2 * NP; i += HT) {
-                    const int tok = i / (2 * NP), f = i - tok * (2 * NP), which = f / NP, n = f - which * NP;
+#pragma unroll
+                for (int j = 0; j < TB; j += ROWS) {
                     float v = 0.f;
 #pragma unroll
-                    for (int r = 0; r < RW; ++r) v += sm.red[w][r][tok][f];
-                    if (n < a.S) a.pbc[((pl.tile * (size_t)a.ax.rows * a.ax.len + tok0 + tb + tok) * 2 + which) * a.S + n] = v;
+                    for (int r = 0; r < RW; ++r) v += sm.red[w][r][j + sum_tok][sum_f];
+                    if (j + sum_tok < nt && sum_n < a.S) sums[(size_t)j * 2 * a.S] = v;
                 }
+                sums -= (size_t)TB * 2 * a.S;
             }
             if (k + 1 < ntiles) {
                 const int w = (k + 1) & 1, st = (k + 1) % STAGES;
@@ -161,14 +186,14 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
                 load_row<CP>(sm.tok[st][0][tid], x, CP, true);
                 load_row<CP>(sm.tok[st][1][tid], dt, CP, true);
                 load_row<CP>(sm.tok[st][2][tid], dy, CP, true);
-                if (src[3]) load_row<CP>(sm.tok[st][3][tid], z, CP, true);
+                if (gate) load_row<CP>(sm.tok[st][3][tid], z, CP, true);
 #pragma unroll
                 for (int i = 0; i < CP; i += 2) {
                     float2 dl = make_float2(dt[i] + bias[i], dt[i + 1] + bias[i + 1]);
                     if (a.softplus) dl = ssm_softplus2(dl);
                     const float2 u = mul2(dl, make_float2(x[i], x[i + 1]));
                     float2 d0 = make_float2(dy[i], dy[i + 1]);
-                    if (src[3]) d0 = make_float2(d0.x * z[i] * sigmoid_fast(z[i]), d0.y * z[i + 1] * sigmoid_fast(z[i + 1]));
+                    if (gate) d0 = make_float2(d0.x * z[i] * sigmoid_fast(z[i]), d0.y * z[i + 1] * sigmoid_fast(z[i + 1]));
                     sm.in[w][ptok][in_at(pc + i)] = make_float4(dl.x, u.x, d0.x, 0.f);
                     sm.in[w][ptok][in_at(pc + i + 1)] = make_float4(dl.y, u.y, d0.y, 0.f);
                 }

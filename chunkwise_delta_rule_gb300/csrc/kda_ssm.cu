@@ -20,6 +20,15 @@
 // add up to its 24 bits.
 // Per four states and token the recurrence takes 4 exponentials (16 cycles of a
 // scheduler's share at 32 per cycle and SM) and 8 paired multiply-adds (16 cycles).
+// Measured, two rows of 8192 tokens, 4096 channels of 16 states, bf16: 408 us, 1.3 TB/s
+// of the tensors' bytes (20% of the copy rate). The bound is instruction dispatch: on
+// the 128 SMs that two rows of 64 channel tiles fill, a scheduler spends 106 cycles on
+// four tokens of a warp's recurrence however many warps it has (a paired multiply-add
+// holds it for two), 1700 of the 3100 cycles of a tile of 32 tokens; the steps, the
+// gate and the copies are most of the rest. So what helps is fewer instructions: two
+// tokens per shared access, rows spaced instead of permuted, copies without checks took
+// it from 444 to 408. Two channels per lane (509), 8-token batches of operands (470, with
+// registers moved between the warp groups) and exponentials one batch ahead (473) do not.
 // A long row is cut into time pieces when its channels alone do not fill the GPU:
 // a first pass forms each piece's end state from zero and its sum of delta (the
 // piece's decay is exp(A sum delta)); in the second pass each piece joins the
@@ -662,7 +671,8 @@ int fwd_tiles(int D, int G) { return (D / G + CH - 1) / CH * G; }
 template <typename TI, int EL, bool WHOLE>
 void run_step_form(const SsmArgs& a, cudaStream_t st) {
     const unsigned tiles = (a.D / a.G + SSM_CH - 1) / SSM_CH * a.G;
-    // four sequences per thread once that still leaves every SM two CTAs
+    // four sequences per thread once that still leaves every SM two CTAs (4096 channels of 16 states: 64 sequences 7.6 us
+    // against 12.6 with one per thread, 4 sequences 2.6 with one against 2.9)
     if ((long long)tiles * (a.ax.N / 4) >= 2 * sm_count())
         k_ssm_step<TI, EL, 4, WHOLE><<<tiles * ((a.ax.N + 3) / 4), SSM_T, 0, st>>>(a);
     else
@@ -708,8 +718,14 @@ void run_step_states(const SsmArgs& a, cudaStream_t st) {
     else if (a.S <= 32) run_step<TI, 8>(a, st);
     else run_step<TI, 16>(a, st);
 }
-// Tokens per sequence up to which everything is read directly: past it the tiles' prefetch pays.
-constexpr int STEP_TOKENS = 4;
+// Tokens per sequence up to which k_ssm_step takes them: it pays no start of tiles (5 us a wave of CTAs), the forward
+// nothing for a token's latency. Measured, 4096 channels of 16 states: one sequence of 6 tokens 5.2 against 6.0 us, of 8
+// 6.4 against 5.9; 8 sequences of 24 20.9 against 25.7, of 32 27 against 22; 64 of 24 104 against 165. 64 sequences, 1024
+// channels of 64 states: 8 tokens 30 against 39, 16 tokens 52 against 47.
+int step_tokens(const SsmArgs& a) {
+    if ((long long)a.ax.rows * fwd_tiles(a.D, a.G) < 3 * sm_count()) return 6;
+    return a.S <= 16 ? 24 : 12;
+}
 
 cudaError_t launch(const char* name, const SsmArgs& a, int bf16, int mode, cudaStream_t st) {
     cudaError_t r = cudaSuccess;
@@ -746,7 +762,7 @@ int ssm_units(int rows, int len, int D, int G, int S, bool backward) {
 }
 
 cudaError_t launch_ssm_fwd(const SsmArgs& a, int bf16, int mode, cudaStream_t st) {
-    if (mode == OUT && !a.ax.cu && a.ax.len > 0 && a.ax.len <= STEP_TOKENS)
+    if (mode == OUT && !a.ax.cu && a.ax.len > 0 && a.ax.len <= step_tokens(a))
         return traced_launch("k_ssm_step", st, [&] {
             bf16 ? run_step_states<__nv_bfloat16>(a, st) : run_step_states<float>(a, st);
         });

@@ -317,6 +317,19 @@ def test_scan_of_large_steps():
     check_close("ht", np64(ht), ref["ht"], 1e-4)
 
 
+@pytest.mark.parametrize("B,T,D,S", [(2, 6, 72, 16), (2, 7, 72, 16), (58, 24, 512, 16), (58, 25, 512, 16), (58, 12, 512, 20),
+                                     (58, 13, 512, 20)])
+def test_scan_of_few_tokens(B, T, D, S):
+    """On both sides of the lengths up to which tokens are taken one by one; the states in place."""
+    import chunkwise_delta_rule_gb300 as kda
+    k, c, cu, ref = scan_case(dict(io="bf16", B=B, T=T, D=D, S=S, state=True), 28)
+    h = c["h0"].clone()
+    c["h0"] = h
+    y, ht, _ = kda.kda_ssm_fwd(scan_problem(k, c, cu), ht=h)
+    check_close("y", np64(y).reshape(ref["y"].shape), ref["y"], tol(y, True))
+    check_close("ht", np64(ht), ref["ht"], tol(ht, True))
+
+
 @pytest.mark.parametrize("which", ["conv", "scan"])
 def test_inconsistent_offsets_set_the_error_word(which):
     """Decreasing offsets and offsets outside the axis: flagged, and every access stays in bounds (they are clamped)."""

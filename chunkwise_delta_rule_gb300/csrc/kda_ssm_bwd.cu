@@ -89,10 +89,10 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
         const int first = tile_begin(0);
         const TI *tok_src[4], *bc_src[NBC];
         bool whole_rows = pvalid >= CP;
+        auto input = [&](int q) { return q == 0 ? a.x : q == 1 ? a.dt : q == 2 ? a.dy : a.z; };
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const void* base = q == 0 ? a.x : q == 1 ? a.dt : q == 2 ? a.dy : a.z;
-            tok_src[q] = static_cast<const TI*>(base) + (tok0 + first + ptok) * ld[q] + pl.c0 + pc;
+            tok_src[q] = static_cast<const TI*>(input(q)) + (tok0 + first + ptok) * ld[q] + pl.c0 + pc;
             whole_rows = whole_rows && ((q == 3 && !gate) || !(a.how >> SHIFT[q] & 3));
         }
 #pragma unroll
@@ -111,11 +111,13 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
                 for (int j = 0; j < NBC; ++j)
                     if (tid + j * HT < 2 * TB * NC) copy_whole_async<TI, 8>(sm.bc[st][j][tid], bc_src[j]);
             } else if (k < ntiles) {
+                // a row that is not there is a copy of no bytes from its own tensor's start: the access that `how` names has
+                // to be aligned all the same, and another tensor's start need not be
                 const int n = tb + ptok < pl.hi ? pvalid : 0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     if (q < 3 || gate)
-                        copy_row_async<TI, CP>(sm.tok[st][q][tid], n > 0 ? tok_src[q] : static_cast<const TI*>(a.x), n, a.how >> SHIFT[q] & 3);
+                        copy_row_async<TI, CP>(sm.tok[st][q][tid], n > 0 ? tok_src[q] : static_cast<const TI*>(input(q)), n, a.how >> SHIFT[q] & 3);
 #pragma unroll
                 for (int j = 0; j < NBC; ++j) {
                     const int i = tid + j * HT;
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
                     const bool isc = i >= TB * NC;
                     const int r = isc ? i - TB * NC : i, tok = r / NC, k8 = (r - tok * NC) * 8;
                     const int m = tb + tok < pl.hi ? a.S - k8 : 0;
-                    copy8_async(sm.bc[st][j][tid], m > 0 ? bc_src[j] : static_cast<const TI*>(a.b), m, a.how >> (isc ? SSM_C : SSM_B) & 3);
+                    copy8_async(sm.bc[st][j][tid], m > 0 ? bc_src[j] : static_cast<const TI*>(isc ? a.c : a.b), m, a.how >> (isc ? SSM_C : SSM_B) & 3);
                 }
             }
 #pragma unroll

@@ -2,6 +2,7 @@
 // allocation and the call, in one step each. A decoding step takes a few
 // microseconds on the device; the same marshalling written in Python takes 10 to
 // 20 microseconds of host time per call and bounds it.
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
 
@@ -72,10 +73,39 @@ int32_t* error_word(const OptT& err) {
     need(err->scalar_type() == at::kInt && err->is_cuda() && err->numel() >= 1, "err must be an int32 CUDA tensor");
     return err->data_ptr<int32_t>();
 }
-kda_stream_t stream_of(const py::object& stream, const Tensor& x) {
-    if (stream.is_none()) return reinterpret_cast<kda_stream_t>(c10::cuda::getCurrentCUDAStream(x.get_device()).stream());
-    return reinterpret_cast<kda_stream_t>(stream.attr("cuda_stream").cast<uintptr_t>());
-}
+// The stream of a call: the current one, or one the caller names. A named one is current while the call allocates, so
+// that a block's earlier users, and the later ones of a workspace dropped at the call's end, are ordered with its kernels.
+// What the two sides hand each other is recorded, so that its memory waits for both when it is freed.
+class OnStream {
+    c10::cuda::CUDAStream caller_, mine_;
+    c10::cuda::OptionalCUDAStreamGuard guard_;
+    bool other_ = false;
+    void record(const Tensor& t, const c10::cuda::CUDAStream& s) {
+        if (other_ && t.numel()) t.record_stream(s.unwrap());
+    }
+
+public:
+    OnStream(const py::object& stream, const Tensor& x) : caller_(c10::cuda::getCurrentCUDAStream(x.get_device())), mine_(caller_) {
+        if (stream.is_none()) return;
+        const auto handle = reinterpret_cast<cudaStream_t>(stream.attr("cuda_stream").cast<uintptr_t>());
+        if (handle == caller_.stream()) return;
+        other_ = true;
+        mine_ = c10::cuda::getStreamFromExternal(handle, x.get_device());
+        guard_.reset_stream(mine_);
+    }
+    operator kda_stream_t() const { return reinterpret_cast<kda_stream_t>(mine_.stream()); }
+    // Tensors of the caller's that the kernels use, and tensors made here that the caller gets.
+    template <class... T>
+    void takes(const T&... t) { (each(t, mine_), ...); }
+    template <class... T>
+    void gives(const T&... t) { (each(t, caller_), ...); }
+
+private:
+    void each(const Tensor& t, const c10::cuda::CUDAStream& s) { record(t, s); }
+    void each(const OptT& t, const c10::cuda::CUDAStream& s) {
+        if (t) record(*t, s);
+    }
+};
 void check(kda_status st, const char* where) {
     if (st != KDA_OK) py::module_::import("chunkwise_delta_rule_gb300._lib").attr("check")((int)st, where);
 }
@@ -112,13 +142,18 @@ struct Conv {
     }
 };
 py::tuple conv_fwd(const Conv& p, bool out_final, OptT final_state, OptT err, py::object stream) {
+    OnStream on(stream, p.x);
+    on.takes(p.x, p.weight, p.bias, p.h0, p.cu, final_state, err);
     Tensor y = like(p.x);
     if (!final_state && out_final) final_state = at::empty(p.state, p.x.options());
     void* f = dense(final_state, "final_state", p.state, p.x.scalar_type());
-    check(kda_conv_fwd(&p.c, y.data_ptr(), f, error_word(err), stream_of(stream, p.x)), "kda_conv_fwd");
+    check(kda_conv_fwd(&p.c, y.data_ptr(), f, error_word(err), on), "kda_conv_fwd");
+    on.gives(y, final_state);
     return py::make_tuple(y, final_state);
 }
 py::tuple conv_bwd(const Conv& p, Tensor dy, OptT dfinal, OptT ws, py::object stream, std::optional<bool> need_dinit) {
+    OnStream on(stream, p.x);
+    on.takes(p.x, p.weight, p.bias, p.h0, p.cu, dy, dfinal, ws);
     void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type());
     void* pdf = dense(dfinal, "dfinal", p.state, p.x.scalar_type());
     Tensor dx = like(p.x), dw = like(p.weight);
@@ -126,7 +161,8 @@ py::tuple conv_bwd(const Conv& p, Tensor dy, OptT dfinal, OptT ws, py::object st
     if (need_dinit ? *need_dinit : p.h0.has_value()) dinit = at::empty(p.state, p.x.options());
     ws = buffer(kda_conv_workspace_size(&p.c), p.x, ws);
     check(kda_conv_bwd(&p.c, pdy, pdf, dx.data_ptr(), dw.data_ptr<float>(), static_cast<float*>(ptr(db)), ptr(dinit), ptr(ws),
-                       bytes(ws), stream_of(stream, p.x)), "kda_conv_bwd");
+                       bytes(ws), on), "kda_conv_bwd");
+    on.gives(dx, dw, db, dinit);
     return py::make_tuple(dx, dw, db, dinit);
 }
 
@@ -166,15 +202,20 @@ struct Ssm {
     }
 };
 py::tuple ssm_fwd(const Ssm& p, bool out_final, OptT ht, OptT saved, OptT ws, OptT err, py::object stream) {
+    OnStream on(stream, p.x);
+    on.takes(p.x, p.dt, p.A_log, p.b, p.cm, p.d_skip, p.z, p.dt_bias, p.h0, p.cu, ht, saved, ws, err);
     Tensor y = like(p.x);
     if (!ht && out_final) ht = at::empty(p.state, p.x.options().dtype(at::kFloat));
     float* h = f32(ht, "ht", p.state);
     ws = buffer(kda_ssm_workspace_size(&p.c, 0), p.x, ws);
     OptT sv = p.c.save_policy ? buffer(kda_ssm_saved_size(&p.c), p.x, saved) : OptT();
-    check(kda_ssm_fwd(&p.c, y.data_ptr(), h, ptr(sv), ptr(ws), bytes(ws), error_word(err), stream_of(stream, p.x)), "kda_ssm_fwd");
+    check(kda_ssm_fwd(&p.c, y.data_ptr(), h, ptr(sv), ptr(ws), bytes(ws), error_word(err), on), "kda_ssm_fwd");
+    on.gives(y, ht, sv);
     return py::make_tuple(y, ht, sv);
 }
 py::tuple ssm_bwd(const Ssm& p, Tensor dy, OptT dht, OptT saved, OptT ws, py::object stream, std::optional<bool> need_dh0) {
+    OnStream on(stream, p.x);
+    on.takes(p.x, p.dt, p.A_log, p.b, p.cm, p.d_skip, p.z, p.dt_bias, p.h0, p.cu, dy, dht, saved, ws);
     void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type());
     float* pdh = f32(dht, "dht", p.state);
     if (p.c.save_policy) need(bytes(saved) >= kda_ssm_saved_size(&p.c), "save_policy 1 needs the forward's saved buffer");
@@ -193,7 +234,8 @@ py::tuple ssm_bwd(const Ssm& p, Tensor dy, OptT dht, OptT saved, OptT ws, py::ob
     g.ddt_bias = static_cast<float*>(ptr(dbias));
     g.dh0 = static_cast<float*>(ptr(dh0));
     ws = buffer(kda_ssm_workspace_size(&p.c, 1), p.x, ws);
-    check(kda_ssm_bwd(&p.c, pdy, pdh, ptr(saved), &g, ptr(ws), bytes(ws), stream_of(stream, p.x)), "kda_ssm_bwd");
+    check(kda_ssm_bwd(&p.c, pdy, pdh, ptr(saved), &g, ptr(ws), bytes(ws), on), "kda_ssm_bwd");
+    on.gives(dx, ddt, dA, db, dc, dskip, dz, dbias, dh0);
     return py::make_tuple(dx, ddt, dA, db, dc, dskip, dz, dbias, dh0);
 }
 
@@ -223,21 +265,27 @@ struct Norm {
     }
 };
 py::tuple norm_fwd(const Norm& p, OptT h, py::object stream) {
+    OnStream on(stream, p.x);
+    on.takes(p.x, p.weight, p.residual, h);
     Tensor y = p.c.out ? at::empty(p.x.sizes(), p.x.options().dtype(at::kFloat8_e4m3fn)) : like(p.x);
     OptT scale;
     if (p.c.out) scale = at::empty(p.scales, p.x.options().dtype(at::kFloat));
     if (!p.residual) h = p.x;
     else if (!h) h = like(p.x);
     else dense(h, "h", p.x.sizes(), p.x.scalar_type());
-    check(kda_norm_fwd(&p.c, y.data_ptr(), static_cast<float*>(ptr(scale)), h->data_ptr(), stream_of(stream, p.x)), "kda_norm_fwd");
+    check(kda_norm_fwd(&p.c, y.data_ptr(), static_cast<float*>(ptr(scale)), h->data_ptr(), on), "kda_norm_fwd");
+    on.gives(y, scale, h);
     return py::make_tuple(y, scale, h);
 }
 py::tuple norm_bwd(const Norm& p, Tensor dy, OptT dres, OptT ws, py::object stream) {
+    OnStream on(stream, p.x);
+    on.takes(p.x, p.weight, dy, dres, ws);
     void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type());
     void* pdr = dense(dres, "dres", p.x.sizes(), p.x.scalar_type());
     Tensor dx = like(p.x), dw = like(p.weight);
     ws = buffer(kda_norm_workspace_size(&p.c), p.x, ws);
-    check(kda_norm_bwd(&p.c, pdy, pdr, dx.data_ptr(), dw.data_ptr<float>(), ptr(ws), bytes(ws), stream_of(stream, p.x)), "kda_norm_bwd");
+    check(kda_norm_bwd(&p.c, pdy, pdr, dx.data_ptr(), dw.data_ptr<float>(), ptr(ws), bytes(ws), on), "kda_norm_bwd");
+    on.gives(dx, dw);
     return py::make_tuple(dx, dw);
 }
 

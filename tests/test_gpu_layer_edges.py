@@ -28,3 +28,68 @@ def test_scan_with_one_tensor_off_its_alignment(io, S, name):
                    ddt_bias=g.ddt_bias, dh0=g.dh0)
         for n, v in got.items():
             check_close(n, np64(v).reshape(ref[n].shape), ref[n], tol(v, True))
+
+
+# ------------------------------------------------------------------ streams
+
+def busy():
+    """About 20 ms of the current stream."""
+    torch.cuda._sleep(40_000_000)
+
+
+def stream_calls(kda):
+    """name -> a call on a given stream (None: the current one) that makes its own outputs and workspace."""
+    from tests.test_gpu_layer import conv_case, norm_case
+    k, s, _, _ = scan_case(dict(io="fp32", B=1, T=2100, D=8, S=16, state=True), 72)      # in time pieces
+    _, c, _, _ = conv_case(dict(io="fp32", B=2, T=600, D=48, W=4, state=True), 73)
+    x, r, w, dy = norm_case("fp32", 300, 1000, 74)
+    p0, p1 = scan_problem(k, s, None, 0), scan_problem(k, s, None, 1)
+    pc = kda.make_conv_problem(c["x"], c["w"], c["bias"], initial_state=c["h0"])
+    pn, pq = kda.make_norm_problem(x, w), kda.make_norm_problem(x, w, residual=r, out="e4m3", group=128)
+    saved = kda.kda_ssm_fwd(p1)[2]
+    return {"ssm_fwd": lambda st: kda.kda_ssm_fwd(p1, stream=st), "ssm_bwd": lambda st: kda.kda_ssm_bwd(p0, s["dy"], s["dht"], stream=st),
+            "ssm_bwd_saved": lambda st: kda.kda_ssm_bwd(p1, s["dy"], s["dht"], saved=saved, stream=st),
+            "conv_fwd": lambda st: kda.kda_conv_fwd(pc, stream=st),
+            "conv_bwd": lambda st: kda.kda_conv_bwd(pc, c["dy"], c["df"], stream=st),
+            "norm_fwd": lambda st: kda.kda_norm_fwd(pq, stream=st), "norm_bwd": lambda st: kda.kda_norm_bwd(pn, dy, stream=st)}
+
+
+def tensors(out):
+    return [t.float() for t in out if t is not None]
+
+
+@pytest.mark.parametrize("name", ["ssm_fwd", "ssm_bwd", "ssm_bwd_saved", "conv_fwd", "conv_bwd", "norm_fwd", "norm_bwd"])
+def test_a_given_stream_owns_what_the_call_allocates(name):
+    """A call on a busy side stream: its workspace and outputs lie neither in blocks that earlier work of the current
+    stream still writes, nor in blocks that its later tensors get; outputs dropped by the current stream are not given
+    to the side stream's next call while they are still read."""
+    import chunkwise_delta_rule_gb300 as kda
+    call = stream_calls(kda)[name]
+    want = [t.clone() for t in tensors(call(None))]
+    torch.cuda.synchronize()
+    sizes = [1 << b for b in range(9, 23)] + [256 * i for i in range(1, 400, 7)]
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    # blocks that the current stream has freed but not finished with
+    busy()
+    late = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255) for n in sizes]
+    del late
+    got = call(side)                         # side does not wait for them
+    side.synchronize()
+    first = [t.clone() for t in tensors(got)]
+    # later tensors of the current stream, while the side stream is still to run
+    with torch.cuda.stream(side):
+        busy()
+    got2 = call(side)
+    later = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255) for n in sizes]
+    main.wait_stream(side)
+    second = [t.clone() for t in tensors(got2)]
+    # outputs dropped while the current stream is still to read them
+    busy()
+    third = [t.clone() for t in tensors(got2)]
+    del got2
+    with torch.cuda.stream(side):
+        again = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255) for n in sizes]
+    torch.cuda.synchronize()
+    del later, again
+    for got in (first, second, third):
+        assert all(torch.equal(torch.nan_to_num(a), torch.nan_to_num(b)) for a, b in zip(got, want))

@@ -24,6 +24,10 @@ void need(bool ok, const char* msg) {
     s << name << " must be a " << what << "CUDA tensor " << shape << ", " << type;
     throw py::value_error(s.str());
 }
+// Every tensor of a call lies on one device, x's.
+void same_device(const Tensor& t, const char* name, const Tensor& x) {
+    if (t.device() != x.device()) throw py::value_error(std::string(name) + " must be on x's device");
+}
 
 // An io type's kda_dtype.
 kda_dtype io_of(const Tensor& t, const char* msg) {
@@ -32,18 +36,22 @@ kda_dtype io_of(const Tensor& t, const char* msg) {
     return s == at::kBFloat16 ? KDA_BF16 : KDA_FP32;
 }
 
-void* dense(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type) {
+void* dense(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type, const Tensor& x) {
     if (t.scalar_type() != type || t.sizes() != shape || !t.is_cuda() || !t.is_contiguous()) refuse(name, "contiguous ", shape, type);
+    same_device(t, name, x);
     return t.data_ptr();
 }
-void* dense(const OptT& t, const char* name, at::IntArrayRef shape, at::ScalarType type) {
-    return t ? dense(*t, name, shape, type) : nullptr;
+void* dense(const OptT& t, const char* name, at::IntArrayRef shape, at::ScalarType type, const Tensor& x) {
+    return t ? dense(*t, name, shape, type, x) : nullptr;
 }
-float* f32(const OptT& t, const char* name, at::IntArrayRef shape) { return static_cast<float*>(dense(t, name, shape, at::kFloat)); }
+float* f32(const OptT& t, const char* name, at::IntArrayRef shape, const Tensor& x) {
+    return static_cast<float*>(dense(t, name, shape, at::kFloat, x));
+}
 
 // Checks a [B, T, ...] input and returns the elements between its tokens (0: contiguous).
-int64_t rows(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type) {
+int64_t rows(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type, const Tensor& x) {
     if (t.scalar_type() != type || t.sizes() != shape || !t.is_cuda()) refuse(name, "", shape, type);
+    same_device(t, name, x);
     if (t.is_contiguous()) return 0;
     int64_t width = 1;
     for (int64_t i = (int64_t)shape.size() - 1; i >= 2; --i) {
@@ -57,36 +65,44 @@ int64_t rows(const Tensor& t, const char* name, at::IntArrayRef shape, at::Scala
 }
 
 // Sequences; packed ones' count and offsets.
-int64_t axis(const OptT& cu, int64_t B, int& N, const int32_t*& p) {
+int64_t axis(const OptT& cu, int64_t B, int& N, const int32_t*& p, const Tensor& x) {
     N = 0;
     p = nullptr;
     if (!cu) return B;
     need(cu->scalar_type() == at::kInt && cu->is_cuda() && cu->dim() == 1 && cu->is_contiguous() && cu->numel() >= 2,
          "cu_seqlens must be an int32 CUDA vector");
+    same_device(*cu, "cu_seqlens", x);
     need(B == 1, "packed sequences need B == 1");
     N = (int)cu->numel() - 1;
     p = cu->data_ptr<int32_t>();
     return N;
 }
-int32_t* error_word(const OptT& err) {
+int32_t* error_word(const OptT& err, const Tensor& x) {
     if (!err) return nullptr;
     need(err->scalar_type() == at::kInt && err->is_cuda() && err->numel() >= 1, "err must be an int32 CUDA tensor");
+    same_device(*err, "err", x);
     return err->data_ptr<int32_t>();
 }
-// The stream of a call: the current one, or one the caller names. A named one is current while the call allocates, so
-// that a block's earlier users, and the later ones of a workspace dropped at the call's end, are ordered with its kernels.
-// What the two sides hand each other is recorded, so that its memory waits for both when it is freed.
+// The device of a call, x's, and its stream: the current one, or one the caller names. A named one is current while the
+// call allocates, so that a block's earlier users, and the later ones of a workspace dropped at the call's end, are
+// ordered with its kernels. What the two sides hand each other is recorded, so that its memory waits for both when it
+// is freed.
 class OnStream {
+    c10::cuda::OptionalCUDAGuard device_;   // unset where x's device is the current one already
     c10::cuda::CUDAStream caller_, mine_;
     c10::cuda::OptionalCUDAStreamGuard guard_;
     bool other_ = false;
     void record(const Tensor& t, const c10::cuda::CUDAStream& s) {
-        if (other_ && t.numel()) t.record_stream(s.unwrap());
+        if (other_ && t.is_cuda() && t.numel()) t.record_stream(s.unwrap());
     }
 
 public:
-    OnStream(const py::object& stream, const Tensor& x) : caller_(c10::cuda::getCurrentCUDAStream(x.get_device())), mine_(caller_) {
+    OnStream(const py::object& stream, const Tensor& x)
+        : caller_(c10::cuda::getCurrentCUDAStream(x.get_device())), mine_(caller_) {
+        if (c10::cuda::current_device() != x.get_device()) device_.set_device(x.device());
         if (stream.is_none()) return;
+        if (py::hasattr(stream, "device_index"))
+            need(stream.attr("device_index").cast<int>() == x.get_device(), "stream must be on x's device");
         const auto handle = reinterpret_cast<cudaStream_t>(stream.attr("cuda_stream").cast<uintptr_t>());
         if (handle == caller_.stream()) return;
         other_ = true;
@@ -114,7 +130,11 @@ OptT like(const OptT& t) { return t ? OptT(like(*t)) : OptT(); }
 void* ptr(const OptT& t) { return t ? t->data_ptr() : nullptr; }
 size_t bytes(const OptT& t) { return t ? t->nbytes() : 0; }
 // The given buffer if it is large enough, else a new one (nothing for no bytes).
-OptT buffer(size_t n, const Tensor& x, const OptT& given) {
+OptT buffer(size_t n, const char* name, const Tensor& x, const OptT& given) {
+    if (given) {
+        if (!given->is_cuda() || !given->is_contiguous()) throw py::value_error(std::string(name) + " must be a contiguous CUDA tensor");
+        same_device(*given, name, x);
+    }
     if (n == 0 || (given && given->nbytes() >= n)) return given;
     return at::empty({(int64_t)n}, x.options().dtype(at::kByte));
 }
@@ -131,14 +151,14 @@ struct Conv {
         need(weight.dim() == 2, "weight must be [D, W]");
         const int64_t B = x.size(0), T = x.size(1), D = x.size(2), W = weight.size(1);
         c.B = (int)B; c.T = (int)T; c.D = (int)D; c.W = (int)W;
-        c.ldx = rows(x, "x", x.sizes(), x.scalar_type());
-        const int64_t n = axis(cu, B, c.N, c.cu_seqlens);
+        c.ldx = rows(x, "x", x.sizes(), x.scalar_type(), x);
+        const int64_t n = axis(cu, B, c.N, c.cu_seqlens, x);
         state = {n, W - 1, D};
         c.silu = silu;
         c.x = x.data_ptr();
-        c.weight = static_cast<float*>(dense(weight, "weight", {D, W}, at::kFloat));
-        c.bias = f32(bias, "bias", {D});
-        c.h0 = dense(h0, "initial_state", state, x.scalar_type());
+        c.weight = static_cast<float*>(dense(weight, "weight", {D, W}, at::kFloat, x));
+        c.bias = f32(bias, "bias", {D}, x);
+        c.h0 = dense(h0, "initial_state", state, x.scalar_type(), x);
     }
 };
 py::tuple conv_fwd(const Conv& p, bool out_final, OptT final_state, OptT err, py::object stream) {
@@ -146,20 +166,20 @@ py::tuple conv_fwd(const Conv& p, bool out_final, OptT final_state, OptT err, py
     on.takes(p.x, p.weight, p.bias, p.h0, p.cu, final_state, err);
     Tensor y = like(p.x);
     if (!final_state && out_final) final_state = at::empty(p.state, p.x.options());
-    void* f = dense(final_state, "final_state", p.state, p.x.scalar_type());
-    check(kda_conv_fwd(&p.c, y.data_ptr(), f, error_word(err), on), "kda_conv_fwd");
+    void* f = dense(final_state, "final_state", p.state, p.x.scalar_type(), p.x);
+    check(kda_conv_fwd(&p.c, y.data_ptr(), f, error_word(err, p.x), on), "kda_conv_fwd");
     on.gives(y, final_state);
     return py::make_tuple(y, final_state);
 }
 py::tuple conv_bwd(const Conv& p, Tensor dy, OptT dfinal, OptT ws, py::object stream, std::optional<bool> need_dinit) {
     OnStream on(stream, p.x);
     on.takes(p.x, p.weight, p.bias, p.h0, p.cu, dy, dfinal, ws);
-    void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type());
-    void* pdf = dense(dfinal, "dfinal", p.state, p.x.scalar_type());
+    void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type(), p.x);
+    void* pdf = dense(dfinal, "dfinal", p.state, p.x.scalar_type(), p.x);
     Tensor dx = like(p.x), dw = like(p.weight);
     OptT db = like(p.bias), dinit;
     if (need_dinit ? *need_dinit : p.h0.has_value()) dinit = at::empty(p.state, p.x.options());
-    ws = buffer(kda_conv_workspace_size(&p.c), p.x, ws);
+    ws = buffer(kda_conv_workspace_size(&p.c), "workspace", p.x, ws);
     check(kda_conv_bwd(&p.c, pdy, pdf, dx.data_ptr(), dw.data_ptr<float>(), static_cast<float*>(ptr(db)), ptr(dinit), ptr(ws),
                        bytes(ws), on), "kda_conv_bwd");
     on.gives(dx, dw, db, dinit);
@@ -181,24 +201,24 @@ struct Ssm {
         const at::ScalarType type = x.scalar_type();
         const std::array<int64_t, 4> bc{B, T, G, S};
         c.B = (int)B; c.T = (int)T; c.D = (int)D; c.S = (int)S; c.G = (int)G;
-        const int64_t n = axis(cu, B, c.N, c.cu_seqlens);
+        const int64_t n = axis(cu, B, c.N, c.cu_seqlens, x);
         state = {n, D, S};
         c.dt_softplus = softplus;
         c.save_policy = save;
-        c.ldx = rows(x, "x", x.sizes(), type);
-        c.lddt = rows(dt, "dt", x.sizes(), type);
-        if (z) c.ldz = rows(*z, "z", x.sizes(), type);
-        c.ldb = rows(b, "b", bc, type);
-        c.ldc = rows(cm, "c", bc, type);
+        c.ldx = rows(x, "x", x.sizes(), type, x);
+        c.lddt = rows(dt, "dt", x.sizes(), type, x);
+        if (z) c.ldz = rows(*z, "z", x.sizes(), type, x);
+        c.ldb = rows(b, "b", bc, type, x);
+        c.ldc = rows(cm, "c", bc, type, x);
         c.x = x.data_ptr();
         c.dt = dt.data_ptr();
         c.z = ptr(z);
         c.b = b.data_ptr();
         c.c = cm.data_ptr();
-        c.A_log = static_cast<float*>(dense(A_log, "A_log", {D, S}, at::kFloat));
-        c.d_skip = f32(d_skip, "d_skip", {D});
-        c.dt_bias = f32(dt_bias, "dt_bias", {D});
-        c.h0 = f32(h0, "initial_state", state);
+        c.A_log = static_cast<float*>(dense(A_log, "A_log", {D, S}, at::kFloat, x));
+        c.d_skip = f32(d_skip, "d_skip", {D}, x);
+        c.dt_bias = f32(dt_bias, "dt_bias", {D}, x);
+        c.h0 = f32(h0, "initial_state", state, x);
     }
 };
 py::tuple ssm_fwd(const Ssm& p, bool out_final, OptT ht, OptT saved, OptT ws, OptT err, py::object stream) {
@@ -206,20 +226,24 @@ py::tuple ssm_fwd(const Ssm& p, bool out_final, OptT ht, OptT saved, OptT ws, Op
     on.takes(p.x, p.dt, p.A_log, p.b, p.cm, p.d_skip, p.z, p.dt_bias, p.h0, p.cu, ht, saved, ws, err);
     Tensor y = like(p.x);
     if (!ht && out_final) ht = at::empty(p.state, p.x.options().dtype(at::kFloat));
-    float* h = f32(ht, "ht", p.state);
-    ws = buffer(kda_ssm_workspace_size(&p.c, 0), p.x, ws);
-    OptT sv = p.c.save_policy ? buffer(kda_ssm_saved_size(&p.c), p.x, saved) : OptT();
-    check(kda_ssm_fwd(&p.c, y.data_ptr(), h, ptr(sv), ptr(ws), bytes(ws), error_word(err), on), "kda_ssm_fwd");
+    float* h = f32(ht, "ht", p.state, p.x);
+    ws = buffer(kda_ssm_workspace_size(&p.c, 0), "workspace", p.x, ws);
+    OptT sv = p.c.save_policy ? buffer(kda_ssm_saved_size(&p.c), "saved", p.x, saved) : OptT();
+    check(kda_ssm_fwd(&p.c, y.data_ptr(), h, ptr(sv), ptr(ws), bytes(ws), error_word(err, p.x), on), "kda_ssm_fwd");
     on.gives(y, ht, sv);
     return py::make_tuple(y, ht, sv);
 }
 py::tuple ssm_bwd(const Ssm& p, Tensor dy, OptT dht, OptT saved, OptT ws, py::object stream, std::optional<bool> need_dh0) {
     OnStream on(stream, p.x);
     on.takes(p.x, p.dt, p.A_log, p.b, p.cm, p.d_skip, p.z, p.dt_bias, p.h0, p.cu, dy, dht, saved, ws);
-    void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type());
-    float* pdh = f32(dht, "dht", p.state);
-    if (p.c.save_policy) need(bytes(saved) >= kda_ssm_saved_size(&p.c), "save_policy 1 needs the forward's saved buffer");
-    else saved = OptT();
+    void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type(), p.x);
+    float* pdh = f32(dht, "dht", p.state, p.x);
+    if (p.c.save_policy) {
+        need(bytes(saved) >= kda_ssm_saved_size(&p.c), "save_policy 1 needs the forward's saved buffer");
+        saved = buffer(0, "saved", p.x, saved);
+    } else {
+        saved = OptT();
+    }
     Tensor dx = like(p.x), ddt = like(p.dt), dA = like(p.A_log), db = like(p.b), dc = like(p.cm);
     OptT dskip = like(p.d_skip), dz = like(p.z), dbias = like(p.dt_bias), dh0;
     if (need_dh0 ? *need_dh0 : p.h0.has_value()) dh0 = at::empty(p.state, p.x.options().dtype(at::kFloat));
@@ -233,7 +257,7 @@ py::tuple ssm_bwd(const Ssm& p, Tensor dy, OptT dht, OptT saved, OptT ws, py::ob
     g.dd_skip = static_cast<float*>(ptr(dskip));
     g.ddt_bias = static_cast<float*>(ptr(dbias));
     g.dh0 = static_cast<float*>(ptr(dh0));
-    ws = buffer(kda_ssm_workspace_size(&p.c, 1), p.x, ws);
+    ws = buffer(kda_ssm_workspace_size(&p.c, 1), "workspace", p.x, ws);
     check(kda_ssm_bwd(&p.c, pdy, pdh, ptr(saved), &g, ptr(ws), bytes(ws), on), "kda_ssm_bwd");
     on.gives(dx, ddt, dA, db, dc, dskip, dz, dbias, dh0);
     return py::make_tuple(dx, ddt, dA, db, dc, dskip, dz, dbias, dh0);
@@ -255,9 +279,9 @@ struct Norm {
         c.out = out == "e4m3";
         c.group = (int)group;
         c.eps = (float)eps;
-        c.x = dense(x, "x", x.sizes(), x.scalar_type());
-        c.residual = dense(residual, "residual", x.sizes(), x.scalar_type());
-        c.weight = static_cast<float*>(dense(weight, "weight", {D}, at::kFloat));
+        c.x = dense(x, "x", x.sizes(), x.scalar_type(), x);
+        c.residual = dense(residual, "residual", x.sizes(), x.scalar_type(), x);
+        c.weight = static_cast<float*>(dense(weight, "weight", {D}, at::kFloat, x));
         if (c.out) {
             scales.assign(x.sizes().begin(), x.sizes().end());
             scales.back() = group > 0 ? (D + group - 1) / group : 1;
@@ -272,7 +296,7 @@ py::tuple norm_fwd(const Norm& p, OptT h, py::object stream) {
     if (p.c.out) scale = at::empty(p.scales, p.x.options().dtype(at::kFloat));
     if (!p.residual) h = p.x;
     else if (!h) h = like(p.x);
-    else dense(h, "h", p.x.sizes(), p.x.scalar_type());
+    else dense(h, "h", p.x.sizes(), p.x.scalar_type(), p.x);
     check(kda_norm_fwd(&p.c, y.data_ptr(), static_cast<float*>(ptr(scale)), h->data_ptr(), on), "kda_norm_fwd");
     on.gives(y, scale, h);
     return py::make_tuple(y, scale, h);
@@ -280,10 +304,10 @@ py::tuple norm_fwd(const Norm& p, OptT h, py::object stream) {
 py::tuple norm_bwd(const Norm& p, Tensor dy, OptT dres, OptT ws, py::object stream) {
     OnStream on(stream, p.x);
     on.takes(p.x, p.weight, dy, dres, ws);
-    void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type());
-    void* pdr = dense(dres, "dres", p.x.sizes(), p.x.scalar_type());
+    void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type(), p.x);
+    void* pdr = dense(dres, "dres", p.x.sizes(), p.x.scalar_type(), p.x);
     Tensor dx = like(p.x), dw = like(p.weight);
-    ws = buffer(kda_norm_workspace_size(&p.c), p.x, ws);
+    ws = buffer(kda_norm_workspace_size(&p.c), "workspace", p.x, ws);
     check(kda_norm_bwd(&p.c, pdy, pdr, dx.data_ptr(), dw.data_ptr<float>(), ptr(ws), bytes(ws), on), "kda_norm_bwd");
     on.gives(dx, dw);
     return py::make_tuple(dx, dw);
@@ -306,12 +330,21 @@ PYBIND11_MODULE(_binding, m) {
         .def_readonly("x", &Norm::x);
     m.def("conv_fwd", &conv_fwd);
     m.def("conv_bwd", &conv_bwd);
-    m.def("conv_workspace_size", [](const Conv& p) { return kda_conv_workspace_size(&p.c); });
+    m.def("conv_workspace_size", [](const Conv& p) {
+        const c10::cuda::CUDAGuard device(p.x.device());   // sizes go by the device's SMs
+        return kda_conv_workspace_size(&p.c);
+    });
     m.def("ssm_fwd", &ssm_fwd);
     m.def("ssm_bwd", &ssm_bwd);
-    m.def("ssm_workspace_size", [](const Ssm& p, bool backward) { return kda_ssm_workspace_size(&p.c, backward); });
+    m.def("ssm_workspace_size", [](const Ssm& p, bool backward) {
+        const c10::cuda::CUDAGuard device(p.x.device());
+        return kda_ssm_workspace_size(&p.c, backward);
+    });
     m.def("ssm_saved_size", [](const Ssm& p) { return kda_ssm_saved_size(&p.c); });
     m.def("norm_fwd", &norm_fwd);
     m.def("norm_bwd", &norm_bwd);
-    m.def("norm_workspace_size", [](const Norm& p) { return kda_norm_workspace_size(&p.c); });
+    m.def("norm_workspace_size", [](const Norm& p) {
+        const c10::cuda::CUDAGuard device(p.x.device());
+        return kda_norm_workspace_size(&p.c);
+    });
 }

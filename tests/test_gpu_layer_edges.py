@@ -93,3 +93,45 @@ def test_a_given_stream_owns_what_the_call_allocates(name):
     del later, again
     for got in (first, second, third):
         assert all(torch.equal(torch.nan_to_num(a), torch.nan_to_num(b)) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_tensors_of_another_device_are_refused():
+    """Every tensor of a call, buffers included, lies on x's device."""
+    import chunkwise_delta_rule_gb300 as kda
+    from tests.test_gpu_layer import conv_case, norm_case
+    k, s, _, _ = scan_case(dict(io="fp32", B=1, T=2100, D=8, S=16, state=True), 75)
+    p, ps = scan_problem(k, s, None), scan_problem(k, s, None, 1)
+    n = max(kda.kda_ssm_workspace_size(p, b) for b in (False, True))
+    host = torch.empty(n, dtype=torch.uint8)
+    spread = torch.empty(256, dtype=torch.uint8, device="cuda").expand(-(-n // 256), 256)   # n bytes in 256 places
+    for ws in (host, spread):
+        with pytest.raises(ValueError, match="workspace must be a contiguous CUDA tensor"):
+            kda.kda_ssm_fwd(p, workspace=ws)
+        with pytest.raises(ValueError, match="workspace must be a contiguous CUDA tensor"):
+            kda.kda_ssm_bwd(p, s["dy"], s["dht"], workspace=ws)
+        with pytest.raises(ValueError, match="saved must be a contiguous CUDA tensor"):
+            kda.kda_ssm_fwd(ps, saved=ws)
+    saved = torch.empty(kda.kda_ssm_saved_size(ps), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="saved must be a contiguous CUDA tensor"):
+        kda.kda_ssm_bwd(ps, s["dy"], s["dht"], saved=saved)
+    with pytest.raises(ValueError, match="err must be an int32 CUDA tensor"):
+        kda.kda_ssm_fwd(p, err=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="dy must be a contiguous CUDA tensor"):
+        kda.kda_ssm_bwd(p, s["dy"].cpu(), stream=torch.cuda.Stream())
+    with pytest.raises(ValueError, match="d_skip must be a contiguous CUDA tensor"):
+        scan_problem(k, dict(s, d_skip=s["d_skip"].cpu()), None)
+    _, c, _, _ = conv_case(dict(io="bf16", B=2, T=70, D=64, W=4, state=True), 76)
+    pc = kda.make_conv_problem(c["x"], c["w"], c["bias"], initial_state=c["h0"])
+    ws = torch.empty(kda.kda_conv_workspace_size(pc), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace must be a contiguous CUDA tensor"):
+        kda.kda_conv_bwd(pc, c["dy"], workspace=ws)
+    with pytest.raises(ValueError, match="final_state must be a contiguous CUDA tensor"):
+        kda.kda_conv_fwd(pc, final_state=c["h0"].cpu())
+    x, r, w, dy = norm_case("fp32", 4, 64, 77)
+    pn = kda.make_norm_problem(x, w)
+    with pytest.raises(ValueError, match="workspace must be a contiguous CUDA tensor"):
+        kda.kda_norm_bwd(pn, dy, workspace=torch.empty(kda.kda_norm_workspace_size(pn), dtype=torch.uint8))
+    with pytest.raises(ValueError, match="residual must be a contiguous CUDA tensor"):
+        kda.make_norm_problem(x, w, residual=r.cpu())

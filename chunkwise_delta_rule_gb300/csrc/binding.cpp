@@ -6,6 +6,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
 
+#include <climits>
 #include <optional>
 
 #include "../../include/kda.h"
@@ -18,6 +19,11 @@ namespace {
 
 void need(bool ok, const char* msg) {
     if (!ok) throw py::value_error(msg);
+}
+// A size as the C interface holds it.
+int size(int64_t v, const char* name) {
+    if (v < INT_MIN || v > INT_MAX) throw py::value_error(std::string(name) + " is beyond 32 bits");
+    return (int)v;
 }
 [[noreturn]] void refuse(const char* name, const char* what, at::IntArrayRef shape, at::ScalarType type) {
     std::ostringstream s;
@@ -73,7 +79,7 @@ int64_t axis(const OptT& cu, int64_t B, int& N, const int32_t*& p, const Tensor&
          "cu_seqlens must be an int32 CUDA vector");
     same_device(*cu, "cu_seqlens", x);
     need(B == 1, "packed sequences need B == 1");
-    N = (int)cu->numel() - 1;
+    N = size(cu->numel() - 1, "the number of sequences");
     p = cu->data_ptr<int32_t>();
     return N;
 }
@@ -150,7 +156,7 @@ struct Conv {
         c.io = io_of(x, "x must be [B, T, D], bf16 or fp32");
         need(weight.dim() == 2, "weight must be [D, W]");
         const int64_t B = x.size(0), T = x.size(1), D = x.size(2), W = weight.size(1);
-        c.B = (int)B; c.T = (int)T; c.D = (int)D; c.W = (int)W;
+        c.B = size(B, "B"); c.T = size(T, "T"); c.D = size(D, "D"); c.W = size(W, "W");
         c.ldx = rows(x, "x", x.sizes(), x.scalar_type(), x);
         const int64_t n = axis(cu, B, c.N, c.cu_seqlens, x);
         state = {n, W - 1, D};
@@ -200,7 +206,7 @@ struct Ssm {
         const int64_t B = x.size(0), T = x.size(1), D = x.size(2), G = b.size(2), S = b.size(3);
         const at::ScalarType type = x.scalar_type();
         const std::array<int64_t, 4> bc{B, T, G, S};
-        c.B = (int)B; c.T = (int)T; c.D = (int)D; c.S = (int)S; c.G = (int)G;
+        c.B = size(B, "B"); c.T = size(T, "T"); c.D = size(D, "D"); c.S = size(S, "S"); c.G = size(G, "G");
         const int64_t n = axis(cu, B, c.N, c.cu_seqlens, x);
         state = {n, D, S};
         c.dt_softplus = softplus;
@@ -274,10 +280,10 @@ struct Norm {
         c.io = io_of(x, "x must be bf16 or fp32 rows");
         need(out == "io" || out == "e4m3", "out must be \"io\" or \"e4m3\"");
         const int64_t D = x.size(-1);
-        c.rows = D ? (int)(x.numel() / D) : 0;
-        c.D = (int)D;
+        c.rows = D ? size(x.numel() / D, "the number of rows") : 0;
+        c.D = size(D, "D");
         c.out = out == "e4m3";
-        c.group = (int)group;
+        c.group = size(group, "group");
         c.eps = (float)eps;
         c.x = dense(x, "x", x.sizes(), x.scalar_type(), x);
         c.residual = dense(residual, "residual", x.sizes(), x.scalar_type(), x);

@@ -196,6 +196,8 @@ kda_status norm_args(const kda_norm_problem* p, kda::NormArgs& a) {
     if (!p) return fail(KDA_ERR_INVALID_ARG, "problem is NULL");
     a = kda::NormArgs{};
     if (p->rows < 0 || p->D < 1) return fail(KDA_ERR_INVALID_ARG, "rows must be >= 0 and D >= 1");
+    // the kernels' row counters step over the last row by a grid's rows
+    if (p->rows > (1 << 30)) return fail(KDA_ERR_UNSUPPORTED, "more than 2^30 rows");
     if (p->D > kda::NORM_MAX_D) return fail(KDA_ERR_UNSUPPORTED, "rows wider than 16384");
     if (p->io != KDA_BF16 && p->io != KDA_FP32) return fail(KDA_ERR_INVALID_ARG, "unknown io dtype");
     if (p->out != 0 && p->out != 1) return fail(KDA_ERR_INVALID_ARG, "out must be 0 or 1");

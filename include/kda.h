@@ -357,7 +357,7 @@ kda_status kda_ssm_bwd(const kda_ssm_problem *p, const void *dy, const float *dh
  * group of `group` columns (32, 64, 128, or 0 for the whole row; the last group
  * may be short): scale = max |y| / 448, y ~ scale * e4m3. */
 typedef struct {
-    int rows, D;                /* D up to 16384 */
+    int rows, D;                /* rows up to 2^30, D up to 16384 */
     kda_dtype io;               /* type of x, residual, h (and y with out 0) */
     int out, group;
     float eps;

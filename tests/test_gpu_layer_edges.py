@@ -135,3 +135,21 @@ def test_tensors_of_another_device_are_refused():
         kda.kda_norm_bwd(pn, dy, workspace=torch.empty(kda.kda_norm_workspace_size(pn), dtype=torch.uint8))
     with pytest.raises(ValueError, match="residual must be a contiguous CUDA tensor"):
         kda.make_norm_problem(x, w, residual=r.cpu())
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """They do not fit the C interface; cut to 32 bits they would be other, smaller calls."""
+    import chunkwise_delta_rule_gb300 as kda
+    n = (1 << 32) + 1
+    x = torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(1, 4, device="cuda")
+    with pytest.raises(ValueError, match="B is beyond 32 bits"):
+        kda.make_conv_problem(x.view(n, 1, 1), w)
+    with pytest.raises(ValueError, match="T is beyond 32 bits"):
+        kda.make_conv_problem(x.view(1, n, 1), w)
+    with pytest.raises(ValueError, match="T is beyond 32 bits"):
+        kda.make_ssm_problem(x.view(1, n, 1), x.view(1, n, 1), w[:, :1].contiguous(), x.view(1, n, 1, 1), x.view(1, n, 1, 1))
+    with pytest.raises(ValueError, match="the number of rows is beyond 32 bits"):
+        kda.make_norm_problem(x.view(n, 1), w[0, :1].contiguous())
+    with pytest.raises(ValueError, match="group is beyond 32 bits"):
+        kda.make_norm_problem(x[:64].view(1, 64), torch.ones(64, device="cuda"), out="e4m3", group=(1 << 32) + 32)

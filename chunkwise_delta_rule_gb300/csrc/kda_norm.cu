@@ -191,11 +191,17 @@ __global__ void __launch_bounds__(NT) k_norm_fwd(NormArgs a, int vec) {
             const int c = col_of<NT, CH>(k);
             if (c >= a.D) continue;
             if (a.group ? (c & (a.group - 1)) == 0 : c == 0) sc[a.group ? c >> (31 - __clz(a.group)) : 0] = m[k] * (1.f / E4M3_MAX);
-            if (m[k] < 1e-30f) {   // 448 / m may overflow: such a group is brought up by 2^64 first
-                m[k] *= 0x1p64f;
+            if (!(m[k] >= 1e-30f && m[k] <= 1e30f)) {
+                // 448 / m may overflow, or m be above 2^126, where the fast division gives 0: such a group is brought to
+                // the middle of the range first
+                const float by = m[k] < 1.f ? 0x1p64f : 0x1p-64f;
+                m[k] *= by;
 #pragma unroll
-                for (int i = 0; i < CH; ++i) h[k][i] *= 0x1p64f;
+                for (int i = 0; i < CH; ++i) h[k][i] *= by;
             }
+            // The fast division's two units do not show: of 2e8 values (bf16, 4096 columns) 125 are not the nearest 8-bit
+            // ones, 112 with a correctly rounded one, 135 in elementary fp32 operations; its registers would leave three
+            // CTAs of four on an SM (82 against 122 us).
             const float inv = m[k] > 0.f ? __fdividef(E4M3_MAX, m[k]) : m[k];   // 0 and NaN as they are
             uint32_t out[2] = {0, 0};
 #pragma unroll

@@ -2,9 +2,11 @@
 ones: rows of unlike alignment, streams, buffers and refusals. Oracle and
 tolerances as in test_gpu_layer."""
 
+import numpy as np
 import pytest
 import torch
 
+from oracle import layer
 from tests.helpers import check_close, np64
 from tests.test_gpu_layer import scan_case, scan_problem, tol, wide_rows
 
@@ -153,3 +155,40 @@ def test_sizes_beyond_32_bits_are_refused():
         kda.make_norm_problem(x.view(n, 1), w[0, :1].contiguous())
     with pytest.raises(ValueError, match="group is beyond 32 bits"):
         kda.make_norm_problem(x[:64].view(1, 64), torch.ones(64, device="cuda"), out="e4m3", group=(1 << 32) + 32)
+
+
+# ------------------------------------------------------------------ norm, 8-bit output
+
+def test_norm_8bit_of_the_largest_weights():
+    """Groups whose largest value is near the end of fp32's range keep their values, as groups near its start do:
+    value ~ scale * e4m3 to half a step."""
+    import chunkwise_delta_rule_gb300 as kda
+    x = torch.linspace(-1.7, 1.7, 512, device="cuda").repeat(3, 1)
+    w = torch.ones(512, device="cuda")
+    w[:128], w[128:256], w[256:384] = 1.9e38, 8.6e37, 8.4e37     # on both sides of 2^126
+    for group in (128, 0):
+        q, scale, _ = kda.kda_norm_fwd(kda.make_norm_problem(x, w, out="e4m3", group=group))
+        ref = layer.norm(np64(x), np64(w), None, 1e-6)["y"]
+        s = np64(scale.repeat_interleave(group or 512, 1))
+        assert torch.isfinite(q.float()).all() and (q.float().abs().amax(1) == 448).all()
+        assert np.all(np.abs(np64(q.float()) * s - ref) <= np.maximum(np.abs(ref) / 16, s / 1024) * (1 + 1e-4) + s * 448 * 1e-6)
+
+
+def test_norm_8bit_values_are_the_nearest_ones():
+    """An 8-bit value differs from the nearest one only where the exact quotient lies within the fp32 arithmetic's
+    error of the middle between two: eight roundings of 2^-24 (sum, weight, product of the value and of its group's
+    largest one, quotient, last product; the root is the same in both), 4.8e-7 of the value."""
+    import chunkwise_delta_rule_gb300 as kda
+    from tests.test_gpu_layer import norm_case
+    x, r, w, _ = norm_case("fp32", 2000, 554, 78)
+    for group in (0, 32):
+        q, scale, _ = kda.kda_norm_fwd(kda.make_norm_problem(x, w, residual=r, out="e4m3", group=group))
+        y = layer.norm(np64(x), np64(w), np64(r), 1e-6)["y"]
+        gr = group or 554
+        pad = np.zeros((2000, -(-554 // gr) * gr))
+        pad[:, :554] = np.abs(y)
+        amax = pad.reshape(2000, -1, gr).max(axis=2)
+        v = y / np.repeat(amax, gr, axis=1)[:, :554] * 448.0
+        step = np.exp2(np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -6))) - 3)
+        off = np.abs(np64(q.float()) - v) - step / 2       # beyond half a step
+        assert np.max(off / np.maximum(np.abs(v), 2.0 ** -6)) <= 4.8e-7

@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
                 for (int e = 0; e < P; ++e) {
                     const int col = j * NROW * EL + 2 * e;
                     const float2 b = make_float2(__uint_as_float(bc[col]), __uint_as_float(bc[col + 1]));
-                    const float2 g = mul2(dl, make_float2(A2[2 * e], A2[2 * e + 1]));
+                    const float2 g = ssm_exponent2(dl, make_float2(A2[2 * e], A2[2 * e + 1]));
                     const float2 hn = fma2(make_float2(ex2(g.x), ex2(g.y)), make_float2(h[2 * e], h[2 * e + 1]), mul2(u, b));
                     h[2 * e] = hn.x;
                     h[2 * e + 1] = hn.y;
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(SSM_T, EL <= 4 ? (WHOLE ? 8 : 5) : 1) k_ssm_st
         }
         if (t == 0) {
 #pragma unroll
-            for (int e = 0; e < EL; ++e) A2[e] = e < valid ? -LOG2E * ex2(LOG2E * A2[e]) : 0.f;
+            for (int e = 0; e < EL; ++e) A2[e] = e < valid ? -expf(A2[e]) * LOG2E : 0.f;
         }
         float dl = dt + bias;
         if (a.softplus) dl = ssm_softplus(dl);
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(SSM_T, EL <= 4 ? (WHOLE ? 8 : 5) : 1) k_ssm_st
             acc[i] = 0.f;
 #pragma unroll
             for (int e = 0; e < EL; ++e) {
-                h[i][e] = fmaf(ex2(di * A2[e]), h[i][e], ui * b[i][e]);
+                h[i][e] = fmaf(ssm_decay(di, A2[e]), h[i][e], ui * b[i][e]);
                 acc[i] = fmaf(h[i][e], c[i][e], acc[i]);
             }
         }

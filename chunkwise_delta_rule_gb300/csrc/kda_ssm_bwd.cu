@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
             const float2 dl = make_float2(v.x, v.x), u = make_float2(v.y, v.y);
 #pragma unroll
             for (int e = 0; e < P; ++e) {
-                const float2 g = mul2(dl, make_float2(A2[2 * e], A2[2 * e + 1]));
+                const float2 g = ssm_exponent2(dl, make_float2(A2[2 * e], A2[2 * e + 1]));
                 const float2 hn = fma2(make_float2(ex2(g.x), ex2(g.y)), make_float2(h[2 * e], h[2 * e + 1]),
                                        mul2(u, make_float2(b[2 * e], b[2 * e + 1])));
                 h[2 * e] = hn.x;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
                 const float2 cc = make_float2(c[2 * e], c[2 * e + 1]), hh = make_float2(h[2 * e], h[2 * e + 1]);
                 const float2 AA = make_float2(A2[2 * e], A2[2 * e + 1]), bb = make_float2(b[2 * e], b[2 * e + 1]);
                 const float2 g = fma2(cc, d0, make_float2(r[2 * e], r[2 * e + 1]));
-                const float2 x = mul2(dl, AA);
+                const float2 x = ssm_exponent2(dl, AA);
                 const float2 dcv = mul2(d0, hh), dbv = mul2(u, g);
                 const float2 rn = mul2(make_float2(ex2(x.x), ex2(x.y)), g);
                 const float2 wv = mul2(rn, make_float2(hp[2 * e], hp[2 * e + 1]));
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(SSM_T) k_ssm_bwd_pieces(SsmArgs a) {
             float c[EL];
             lds_states<EL>(&s_c[i][n0], c);
 #pragma unroll
-            for (int e = 0; e < EL; ++e) r[e] = ex2(v.x * A2[e]) * fmaf(c[e], v.y, r[e]);
+            for (int e = 0; e < EL; ++e) r[e] = ssm_decay(v.x, A2[e]) * fmaf(c[e], v.y, r[e]);
             sd += v.x;
         };
         if (te - tb == TB) {

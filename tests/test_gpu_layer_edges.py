@@ -8,7 +8,7 @@ import torch
 
 from oracle import layer
 from tests.helpers import check_close, np64
-from tests.test_gpu_layer import scan_case, scan_problem, tol, wide_rows
+from tests.test_gpu_layer import gen_of, scan_case, scan_problem, tol, wide_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -192,3 +192,41 @@ def test_norm_8bit_values_are_the_nearest_ones():
         step = np.exp2(np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -6))) - 3)
         off = np.abs(np64(q.float()) - v) - step / 2       # beyond half a step
         assert np.max(off / np.maximum(np.abs(v), 2.0 ** -6)) <= 4.8e-7
+
+
+# ------------------------------------------------------------------ scan, decays
+
+@pytest.mark.parametrize("g", [0.35, 0.09, 0.02, 0.006, 0.0015])
+def test_decays_do_not_drift(g):
+    """A state that only decays is the product of its tokens' decays: an error with a mean grows with the tokens. The
+    hardware's 2^x, with the constant that the exponent carries, is off by 1.2e-8 or less on the average at every
+    size of exponent; what is random (2.5e-8 a token) and what differs by state (1e-7 of the exponents) averages out
+    over 1024 states to 1e-9 a token. So at most 1.5e-8 a token, forward, backward and token by token."""
+    import chunkwise_delta_rule_gb300 as kda
+    gen = gen_of(81)
+    D, S = 64, 16
+    for T in (20, int(min(600, 100 / g))):
+        A_log = torch.rand(D, S, generator=gen) * 0.5 - 0.25
+        dt = ((torch.rand(1, T, D, generator=gen) + 0.5) * (g * np.log(2))).float()
+        one = torch.ones(1, D, S, device="cuda")
+        zero, bc = torch.zeros(1, T, D, device="cuda"), torch.zeros(1, T, 1, S, device="cuda")
+        p = kda.make_ssm_problem(zero, dt.cuda(), A_log.cuda(), bc, bc, dt_softplus=False, initial_state=one)
+        want = np.exp(-np.exp(np64(A_log)) * np64(dt).sum(axis=1).reshape(D, 1))
+        _, ht, _ = kda.kda_ssm_fwd(p)
+        dh0 = kda.kda_ssm_bwd(p, zero, one).dh0
+        for t in (ht, dh0):
+            drift = np.mean(np64(t)[0] / want - 1) / T
+            assert abs(drift) <= 1.5e-8, (T, drift)
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("S", [16, 20])
+def test_decoding_and_prefill_give_the_same_states(io, S):
+    """The token-by-token kernel and the tiled one form rates, steps and states by the same operations: bitwise."""
+    import chunkwise_delta_rule_gb300 as kda
+    k, c, _, _ = scan_case(dict(io=io, B=1, T=6, D=72, S=S, state=True), 82)
+    c["A_log"] = c["A_log"] * 3 - 4
+    cu = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    tokens = kda.kda_ssm_fwd(scan_problem(k, c, None))[1]     # so few tokens are taken one by one
+    tiles = kda.kda_ssm_fwd(scan_problem(k, c, cu))[1]        # packed sequences are not
+    assert torch.equal(tokens, tiles)

@@ -230,3 +230,36 @@ def test_decoding_and_prefill_give_the_same_states(io, S):
     tokens = kda.kda_ssm_fwd(scan_problem(k, c, None))[1]     # so few tokens are taken one by one
     tiles = kda.kda_ssm_fwd(scan_problem(k, c, cu))[1]        # packed sequences are not
     assert torch.equal(tokens, tiles)
+
+
+def test_gradient_of_the_rates_sums_long_rows():
+    """dA_log of long rows whose terms have one sign, in one piece (160 CTAs). Summed one token after another each of 4096
+    addends would be rounded at the whole sum's size, about 0.58 x 64 x 1.7e-8 = 6.3e-7 of it; by tiles of 16 the sums' part
+    is (4 + 16) x 0.58 x 1.7e-8 = 2e-7. The terms' own errors with a mean (a decay in three places, 3e-8 each at these
+    exponents) add 1e-7, and the roundings of A, the product and the last one 1e-7: 4e-7."""
+    import chunkwise_delta_rule_gb300 as kda
+    B, T, D, S = 4, 4096, 2560, 4
+    gen = torch.Generator(device="cuda").manual_seed(83)
+
+    def rand(*shape):
+        return torch.rand(*shape, generator=gen, device="cuda") + 0.5
+
+    x, dt, dy, b, c = rand(B, T, D), rand(B, T, D), rand(B, T, D), rand(B, T, 1, S), rand(B, T, 1, S)
+    A_log = rand(D, S) - 1.0
+    p = kda.make_ssm_problem(x, dt, A_log, b, c, dt_softplus=False, save_policy=1)
+    got = kda.kda_ssm_bwd(p, dy, saved=kda.kda_ssm_fwd(p)[2]).dA_log
+    A = -torch.exp(A_log.double())
+    before = torch.empty(T, B, D, S, dtype=torch.float64, device="cuda")
+    h = torch.zeros(B, D, S, dtype=torch.float64, device="cuda")
+    for t in range(T):
+        before[t] = h
+        d = dt[:, t, :, None].double()
+        h = torch.exp(d * A) * h + d * x[:, t, :, None].double() * b[:, t].double()
+    g, dA = torch.zeros_like(h), torch.zeros_like(h)
+    for t in reversed(range(T)):
+        d = dt[:, t, :, None].double()
+        g = (g + c[:, t].double() * dy[:, t, :, None].double()) * torch.exp(d * A)
+        dA += g * before[t] * d
+    want = A * dA.sum(0)
+    err = float((got.double() - want).norm() / want.norm())
+    assert err <= 4e-7, err

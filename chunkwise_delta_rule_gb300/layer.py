@@ -15,6 +15,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -170,6 +171,7 @@ class ShortConvFunction(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dfinal):
         x, weight, bias, h0, cu = ctx.saved_tensors
         p = make_conv_problem(x, weight, bias, silu=ctx.silu, initial_state=h0, cu_seqlens=cu)
@@ -197,6 +199,7 @@ class SsmScanFunction(torch.autograd.Function):
         return y, ht
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dht):
         x, dt, A_log, b, c, d_skip, z, dt_bias, h0, cu, saved = ctx.saved_tensors
         p = make_ssm_problem(x, dt, A_log, b, c, d_skip=d_skip, z=z, dt_bias=dt_bias, dt_softplus=ctx.meta[0],
@@ -226,6 +229,7 @@ class RmsNormFunction(torch.autograd.Function):
         return y, h if residual is not None else x.view_as(x)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh):
         h, weight = ctx.saved_tensors
         eps, has_residual = ctx.meta

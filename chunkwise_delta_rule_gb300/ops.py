@@ -13,6 +13,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -266,6 +267,7 @@ class ChunkKDAFunction(torch.autograd.Function):
         return o, ht
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, dht):
         q, k, v, g, beta, h0, cu, sv, A_log, dt_bias = ctx.saved_tensors
         kw, has_g, has_h0, has_cu, has_A, has_dt = ctx.meta

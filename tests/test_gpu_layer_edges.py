@@ -263,3 +263,26 @@ def test_gradient_of_the_rates_sums_long_rows():
     want = A * dA.sum(0)
     err = float((got.double() - want).norm() / want.norm())
     assert err <= 4e-7, err
+
+
+# ------------------------------------------------------------------ autograd
+
+def test_second_derivatives_are_refused():
+    """The backwards are kernels without one of their own: a second derivative through them is an error, not a term
+    that is missing."""
+    import chunkwise_delta_rule_gb300 as kda
+    from tests.test_gpu_layer import conv_case, norm_case
+    _, c, _, _ = conv_case(dict(io="fp32", B=2, T=20, D=24, W=4), 84)
+    _, s, _, _ = scan_case(dict(io="fp32", B=2, T=20, D=24, S=16), 85)
+    x, r, w, _ = norm_case("fp32", 6, 200, 86)
+    q, k, v = (torch.randn(1, 20, 2, 64, device="cuda") for _ in range(3))
+    g, beta = -torch.rand(1, 20, 2, 64, device="cuda"), torch.rand(1, 20, 2, device="cuda")
+    calls = [(c["x"], lambda t: kda.short_conv(t, c["w"], c["bias"])[0]),
+             (s["x"], lambda t: kda.ssm_scan(t, s["dt"], s["A_log"], s["b"], s["c"], z=s["z"], dt_bias=s["dt_bias"])[0]),
+             (x, lambda t: kda.rms_norm(t, w, residual=r)[0]), (v, lambda t: kda.chunk_kda(q, k, t, g, beta)[0])]
+    for leaf, f in calls:
+        leaf = leaf.clone().requires_grad_(True)
+        y = f(leaf)
+        grad, = torch.autograd.grad((y * y).sum(), leaf, create_graph=True)   # a first one as ever
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (grad * grad).sum().backward()

@@ -134,6 +134,7 @@ def load() -> ctypes.CDLL:
             ("kda_ssm_saved_size", [SP], sz),
             ("kda_ssm_fwd", [SP, vp, vp, vp, vp, sz, vp, vp], ctypes.c_int),
             ("kda_ssm_bwd", [SP, vp, vp, vp, ctypes.POINTER(SsmGrads), vp, sz, vp], ctypes.c_int),
+            ("kda_ssm_bwd_err", [SP, vp, vp, vp, ctypes.POINTER(SsmGrads), vp, sz, vp, vp], ctypes.c_int),
             ("kda_norm_fwd", [NP, vp, vp, vp, vp], ctypes.c_int),
             ("kda_norm_workspace_size", [NP], sz),
             ("kda_norm_bwd", [NP, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int)):

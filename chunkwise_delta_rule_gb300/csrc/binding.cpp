@@ -239,9 +239,9 @@ py::tuple ssm_fwd(const Ssm& p, bool out_final, OptT ht, OptT saved, OptT ws, Op
     on.gives(y, ht, sv);
     return py::make_tuple(y, ht, sv);
 }
-py::tuple ssm_bwd(const Ssm& p, Tensor dy, OptT dht, OptT saved, OptT ws, py::object stream, std::optional<bool> need_dh0) {
+py::tuple ssm_bwd(const Ssm& p, Tensor dy, OptT dht, OptT saved, OptT ws, py::object stream, std::optional<bool> need_dh0, OptT err) {
     OnStream on(stream, p.x);
-    on.takes(p.x, p.dt, p.A_log, p.b, p.cm, p.d_skip, p.z, p.dt_bias, p.h0, p.cu, dy, dht, saved, ws);
+    on.takes(p.x, p.dt, p.A_log, p.b, p.cm, p.d_skip, p.z, p.dt_bias, p.h0, p.cu, dy, dht, saved, ws, err);
     void* pdy = dense(dy, "dy", p.x.sizes(), p.x.scalar_type(), p.x);
     float* pdh = f32(dht, "dht", p.state, p.x);
     if (p.c.save_policy) {
@@ -264,7 +264,7 @@ py::tuple ssm_bwd(const Ssm& p, Tensor dy, OptT dht, OptT saved, OptT ws, py::ob
     g.ddt_bias = static_cast<float*>(ptr(dbias));
     g.dh0 = static_cast<float*>(ptr(dh0));
     ws = buffer(kda_ssm_workspace_size(&p.c, 1), "workspace", p.x, ws);
-    check(kda_ssm_bwd(&p.c, pdy, pdh, ptr(saved), &g, ptr(ws), bytes(ws), on), "kda_ssm_bwd");
+    check(kda_ssm_bwd_err(&p.c, pdy, pdh, ptr(saved), &g, ptr(ws), bytes(ws), error_word(err, p.x), on), "kda_ssm_bwd");
     on.gives(dx, ddt, dA, db, dc, dskip, dz, dbias, dh0);
     return py::make_tuple(dx, ddt, dA, db, dc, dskip, dz, dbias, dh0);
 }

@@ -309,6 +309,11 @@ kda_status kda_ssm_fwd(const kda_ssm_problem* p, void* y, float* ht, void* saved
 
 kda_status kda_ssm_bwd(const kda_ssm_problem* p, const void* dy, const float* dht, const void* saved,
                        const kda_ssm_grads* g, void* ws, size_t ws_bytes, kda_stream_t stream) {
+    return kda_ssm_bwd_err(p, dy, dht, saved, g, ws, ws_bytes, nullptr, stream);
+}
+
+kda_status kda_ssm_bwd_err(const kda_ssm_problem* p, const void* dy, const float* dht, const void* saved,
+                           const kda_ssm_grads* g, void* ws, size_t ws_bytes, int32_t* err, kda_stream_t stream) {
     kda::SsmArgs a;
     kda_status st = ssm_args(p, a);
     if (st != KDA_OK || (st = ssm_pointers(a)) != KDA_OK) return st;
@@ -333,6 +338,7 @@ kda_status kda_ssm_bwd(const kda_ssm_problem* p, const void* dy, const float* dh
     a.pv = cw.take<float>(L.pv);
     a.pbc = cw.take<float>(L.pbc);
     ssm_access(a, esize(p->io), dy, g->dx, g->ddt, g->dz);
+    a.err = err;
     if (!p->save_policy && a.ax.len > 0) {
         if (a.units_row > 1 && (st = cuda_result(kda::launch_ssm_pieces(a, bf16, cs), "scan (pieces)")) != KDA_OK) return st;
         if ((st = cuda_result(kda::launch_ssm_fwd(a, bf16, 2, cs), "scan (recompute)")) != KDA_OK) return st;

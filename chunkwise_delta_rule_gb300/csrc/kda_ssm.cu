@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem;
-    // A wait that gives up (a lost hand-over) is recorded and no further one is tried: the results are not valid then.
+    // A wait that gives up (a lost hand-over) is recorded where the caller gave an error word, and no further one is tried:
+    // the results are not valid then.
     bool lost = false;
     auto await = [&](uint64_t* bar, int phase) {
         if (!lost && !tc::mbar_wait(bar, phase & 1)) {

@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(BwdShape<TI, EL>::RT + HT, 1) k_ssm_bwd(SsmArg
                   KEEP = Sh::KEEP, NVER = Sh::NVER, NBC = Sh::NBC, STAGES = Sh::STAGES;
     extern __shared__ __align__(16) unsigned char raw_smem[];
     typename Sh::Smem& sm = *reinterpret_cast<typename Sh::Smem*>(raw_smem);
+    if (blockIdx.x == 0) axis_check(a.ax, a.err);
     const SsmPlace pl = ssm_place<CH>(a);
     const size_t tok0 = (size_t)pl.row * a.ax.len;
     const size_t DS = (size_t)a.D * a.S;

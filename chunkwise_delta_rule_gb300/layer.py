@@ -113,10 +113,10 @@ def kda_ssm_fwd(p: "_binding.SsmProblem", *, output_final_state: bool = True, ht
 
 def kda_ssm_bwd(p: "_binding.SsmProblem", dy: torch.Tensor, dht: Optional[torch.Tensor] = None, *,
                 saved: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None,
-                need_dh0: Optional[bool] = None) -> SsmGrads:
+                need_dh0: Optional[bool] = None, err: Optional[torch.Tensor] = None) -> SsmGrads:
     """Backward of <dy, y> + <dht, final states>. With save_policy 1, ``saved`` is
-    what the forward returned for the same inputs."""
-    return SsmGrads(*_binding.ssm_bwd(p, dy, dht, saved, workspace, stream, need_dh0))
+    what the forward returned for the same inputs; ``err`` as in the forward."""
+    return SsmGrads(*_binding.ssm_bwd(p, dy, dht, saved, workspace, stream, need_dh0, err))
 
 
 # ------------------------------------------------------------------ norm
@@ -162,9 +162,9 @@ class ShortConvFunction(torch.autograd.Function):
     """Autograd wrapper: forward and backward both run the CUDA library."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, initial_state, cu_seqlens, silu):
+    def forward(ctx, x, weight, bias, initial_state, cu_seqlens, silu, err):
         p = make_conv_problem(x, weight, bias, silu=silu, initial_state=initial_state, cu_seqlens=cu_seqlens)
-        y, final = kda_conv_fwd(p)
+        y, final = kda_conv_fwd(p, err=err)
         ctx.set_materialize_grads(False)   # an output nobody used has no gradient to read
         ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
         ctx.silu = silu
@@ -176,26 +176,28 @@ class ShortConvFunction(torch.autograd.Function):
         x, weight, bias, h0, cu = ctx.saved_tensors
         p = make_conv_problem(x, weight, bias, silu=ctx.silu, initial_state=h0, cu_seqlens=cu)
         dx, dw, db, dinit = kda_conv_bwd(p, _grad(dy, x.shape, x), _grad(dfinal))
-        return dx, dw, db, dinit, None, None
+        return dx, dw, db, dinit, None, None, None
 
 
 def short_conv(x, weight, bias=None, *, silu: bool = True, initial_state: Optional[torch.Tensor] = None,
-               cu_seqlens: Optional[torch.Tensor] = None):
-    """Differentiable short causal convolution. Returns (y, final_state)."""
-    return ShortConvFunction.apply(x, weight, bias, initial_state, cu_seqlens, silu)
+               cu_seqlens: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None):
+    """Differentiable short causal convolution. Returns (y, final_state). ``err``
+    as in ``kda_conv_fwd``."""
+    return ShortConvFunction.apply(x, weight, bias, initial_state, cu_seqlens, silu, err)
 
 
 class SsmScanFunction(torch.autograd.Function):
     """Autograd wrapper: forward and backward both run the CUDA library."""
 
     @staticmethod
-    def forward(ctx, x, dt, A_log, b, c, d_skip, z, dt_bias, initial_state, cu_seqlens, dt_softplus, save_policy):
+    def forward(ctx, x, dt, A_log, b, c, d_skip, z, dt_bias, initial_state, cu_seqlens, dt_softplus, save_policy,
+                err):
         p = make_ssm_problem(x, dt, A_log, b, c, d_skip=d_skip, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus,
                              initial_state=initial_state, cu_seqlens=cu_seqlens, save_policy=save_policy)
-        y, ht, saved = kda_ssm_fwd(p)
+        y, ht, saved = kda_ssm_fwd(p, err=err)
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(x, dt, A_log, b, c, d_skip, z, dt_bias, initial_state, cu_seqlens, saved)
-        ctx.meta = (dt_softplus, save_policy)
+        ctx.meta = (dt_softplus, save_policy, err)
         return y, ht
 
     @staticmethod
@@ -204,17 +206,18 @@ class SsmScanFunction(torch.autograd.Function):
         x, dt, A_log, b, c, d_skip, z, dt_bias, h0, cu, saved = ctx.saved_tensors
         p = make_ssm_problem(x, dt, A_log, b, c, d_skip=d_skip, z=z, dt_bias=dt_bias, dt_softplus=ctx.meta[0],
                              initial_state=h0, cu_seqlens=cu, save_policy=ctx.meta[1])
-        g = kda_ssm_bwd(p, _grad(dy, x.shape, x), _grad(dht), saved=saved)
-        return g.dx, g.ddt, g.dA_log, g.db, g.dc, g.dd_skip, g.dz, g.ddt_bias, g.dh0, None, None, None
+        g = kda_ssm_bwd(p, _grad(dy, x.shape, x), _grad(dht), saved=saved, err=ctx.meta[2])
+        return (g.dx, g.ddt, g.dA_log, g.db, g.dc, g.dd_skip, g.dz, g.ddt_bias, g.dh0) + (None,) * 4
 
 
 def ssm_scan(x, dt, A_log, b, c, *, d_skip: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
              dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = True,
              initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
-             save_policy: int = 1):
-    """Differentiable selective state space scan. Returns (y, final_state)."""
+             save_policy: int = 1, err: Optional[torch.Tensor] = None):
+    """Differentiable selective state space scan. Returns (y, final_state). ``err``
+    as in ``kda_ssm_fwd``; its backward sets it too."""
     return SsmScanFunction.apply(x, dt, A_log, b, c, d_skip, z, dt_bias, initial_state, cu_seqlens, dt_softplus,
-                                 save_policy)
+                                 save_policy, err)
 
 
 class RmsNormFunction(torch.autograd.Function):

@@ -350,6 +350,10 @@ typedef struct {
  * formed in a fixed order (no atomics): repeated calls agree bitwise. */
 kda_status kda_ssm_bwd(const kda_ssm_problem *p, const void *dy, const float *dht, const void *saved,
                        const kda_ssm_grads *g, void *ws, size_t ws_bytes, kda_stream_t stream);
+/* The same with an error word (NULL or a device int32 word), set as by kda_ssm_fwd: bit 0 for inconsistent
+ * cu_seqlens, bit 1 where a wait of the recomputed forward (save_policy 0) gave up. */
+kda_status kda_ssm_bwd_err(const kda_ssm_problem *p, const void *dy, const float *dht, const void *saved,
+                           const kda_ssm_grads *g, void *ws, size_t ws_bytes, int32_t *err, kda_stream_t stream);
 
 /* Root-mean-square norm of rows, with the residual's addition in front:
  *     h = x + residual (fp32),  y = h (mean h^2 + eps)^(-1/2) weight.

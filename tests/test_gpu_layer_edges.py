@@ -286,3 +286,31 @@ def test_second_derivatives_are_refused():
         grad, = torch.autograd.grad((y * y).sum(), leaf, create_graph=True)   # a first one as ever
         with pytest.raises(RuntimeError, match="once_differentiable"):
             (grad * grad).sum().backward()
+
+
+@pytest.mark.parametrize("save", [0, 1])
+def test_the_backward_and_autograd_report_on_the_error_word(save):
+    """The recomputed forward of the backward, the backward itself and the autograd functions set the caller's word (its
+    bit for offsets that do not fit: the same word takes the bit of a wait that gave up)."""
+    import chunkwise_delta_rule_gb300 as kda
+    from tests.test_gpu_layer import conv_case
+    bad = torch.tensor([0, 9, 4, 12], dtype=torch.int32, device="cuda")
+    k, s, good, _ = scan_case(dict(io="bf16", B=1, D=16, S=16, state=True, lengths=[4, 4, 4]), 87)
+    _, c, _, _ = conv_case(dict(io="bf16", B=1, D=16, W=4, state=True, lengths=[4, 4, 4]), 87)
+    for cu, want in ((good, 0), (bad, 1)):
+        p = scan_problem(k, s, cu, save)
+        saved = kda.kda_ssm_fwd(p)[2]
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kda.kda_ssm_bwd(p, s["dy"], s["dht"], saved=saved, err=err)
+        assert int(err) == want
+        err.zero_()
+        x = s["x"].clone().requires_grad_(True)
+        y, _ = kda.ssm_scan(x, s["dt"], s["A_log"], s["b"], s["c"], z=s["z"], dt_bias=s["dt_bias"], cu_seqlens=cu,
+                            save_policy=save, err=err)
+        assert int(err) == want
+        err.zero_()
+        y.sum().backward()
+        assert int(err) == want
+        err.zero_()
+        kda.short_conv(c["x"], c["w"], c["bias"], cu_seqlens=cu, err=err)
+        assert int(err) == want

@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 from chunkwise_delta_rule_gb300 import _lib
-from tests.test_layer_abi import VP, X, norm
+from tests.test_layer_abi import VP, X, norm, ssm
 
 
 @pytest.mark.parametrize("rows", [(1 << 30) + 1, (1 << 31) - 1])
@@ -18,3 +18,13 @@ def test_norm_rows_beyond_the_kernels_counters_are_refused(rows):
     assert lib.kda_norm_bwd(ctypes.byref(p), VP(X), None, VP(X), VP(X), VP(X), 1 << 40, None) == 2
     assert lib.kda_norm_workspace_size(ctypes.byref(p)) == 0
     assert lib.kda_norm_workspace_size(ctypes.byref(norm(rows=1 << 30, D=1))) > 0
+
+
+def test_the_scans_backward_with_an_error_word_refuses_what_it_refuses_without():
+    lib = _lib.load()
+    g = _lib.SsmGrads(**{n: X for n, _ in _lib.SsmGrads._fields_})
+    for kw, status in ((dict(S=0), 1), (dict(S=65), 2), (dict(A_log=None), 1), (dict(G=3), 1)):
+        p = ssm(**kw)
+        assert lib.kda_ssm_bwd_err(ctypes.byref(p), VP(X), None, None, ctypes.byref(g), VP(X), 1 << 40, VP(X), None) == status
+    p = ssm()
+    assert lib.kda_ssm_bwd_err(ctypes.byref(p), VP(X), None, None, ctypes.byref(g), None, 0, VP(X), None) == 3

@@ -153,6 +153,32 @@ def kda_last_error() -> str:
     return _lib.last_error()
 
 
+def _dense(t: Optional[torch.Tensor], name: str, p: Problem):
+    _need(t is None or (t.device == p.q.device and t.is_contiguous()), f"{name} must be a contiguous tensor on q's device")
+
+
+def _other(stream) -> bool:
+    return stream is not None and stream.cuda_stream != torch.cuda.current_stream().cuda_stream
+
+
+def _on(stream, p: Problem, given, call):
+    """Runs `call` with `stream` current, so that what it allocates is ordered with
+    its kernels; what the two sides hand each other is recorded, so that its memory
+    waits for both when it is freed."""
+    caller = torch.cuda.current_stream()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    for t in list(vars(p).values()) + list(given):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        out = call()
+    for t in out:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(caller)
+    return out
+
+
 def _buffer(nbytes: int, device, given: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     if nbytes == 0:
         return given
@@ -174,7 +200,12 @@ def kda_device_status(p: Problem, workspace: torch.Tensor, stream=None):
 def kda_chunk_fwd(p: Problem, *, output_final_state: bool = True, workspace=None, saved=None,
                   stream=None):
     """Forward pass. Returns (o, ht or None, saved or None)."""
+    if _other(stream):
+        return _on(stream, p, (workspace, saved), lambda: kda_chunk_fwd(
+            p, output_final_state=output_final_state, workspace=workspace, saved=saved))
     lib = _lib.load()
+    _dense(workspace, "workspace", p)
+    _dense(saved, "saved", p)
     dev = p.q.device
     o = torch.empty_like(p.v)
     ht = torch.empty(p.state_shape, dtype=torch.float32, device=dev) if output_final_state else None
@@ -194,7 +225,10 @@ def kda_recurrent_fwd(p: Problem, *, output_final_state: bool = True, ht: Option
     """Token-by-token forward (decoding, short prompts). Returns (o, ht or None).
     ``ht`` may be given (fp32 [N, H, K, V], for example the initial state itself
     for an in-place update); ``err`` is an optional int32 device word."""
+    if _other(stream):
+        return _on(stream, p, (ht, err), lambda: kda_recurrent_fwd(p, output_final_state=output_final_state, ht=ht, err=err))
     _need(p.c.save_policy == 0, "the recurrent forward has no saved buffer: use save_policy 0")
+    _dense(ht, "ht", p)
     dev = p.q.device
     o = torch.empty_like(p.v)
     if ht is None and output_final_state:
@@ -215,8 +249,15 @@ def kda_chunk_bwd(p: Problem, do: torch.Tensor, dht: Optional[torch.Tensor] = No
     then, when the problem activates its gate (A_log given), dA_log and
     ddt_bias (None without dt_bias), then, with erase/write (GatedDeltaNet-2;
     dbeta is None), derase and dwrite."""
+    if _other(stream):
+        return _on(stream, p, (do, dht, saved, workspace), lambda: kda_chunk_bwd(
+            p, do, dht, saved=saved, workspace=workspace, need_dh0=need_dh0))
     lib = _lib.load()
     dev = p.q.device
+    for name, t in (("do", do), ("dht", dht), ("saved", saved), ("workspace", workspace)):
+        _dense(t, name, p)
+    _need(not p.c.save_policy or (saved is not None and saved.numel() * saved.element_size() >= kda_saved_size(p)),
+          "save_policy needs the forward's saved buffer")
     _need(do.shape == p.v.shape and do.dtype == p.v.dtype and do.is_contiguous(), "do must match v")
     if dht is not None:
         _need(dht.dtype == torch.float32 and dht.is_contiguous() and tuple(dht.shape) == p.state_shape,

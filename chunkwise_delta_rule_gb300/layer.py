@@ -27,7 +27,11 @@ class _Unloaded:
     def __getattr__(self, name):
         global _binding
         _lib.load()
-        from . import _binding as module
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError("_binding.so is not built for this torch (run `python -m chunkwise_delta_rule_gb300.build`); "
+                              "the layer operators have no other entry from Python") from e
         _binding = module
         return getattr(module, name)
 

@@ -354,8 +354,13 @@ cudaError_t run_one(NormArgs a, int vec, cudaStream_t st) {
         // as many CTAs as are resident together, about 1024 threads per SM
         const int most = sm_count() * (NT >= 1024 ? 1 : 1024 / NT < 16 ? 1024 / NT : 16);
         a.parts = a.rows < most ? a.rows : most;
-        if (a.out) k_norm_fwd<TI, NT, NC, CH, true><<<a.parts, NT, 0, st>>>(a, vec);
-        else k_norm_fwd<TI, NT, NC, CH, false><<<a.parts, NT, 0, st>>>(a, vec);
+        if constexpr (CH > 1) {   // an 8-bit output takes chunks at every width
+            if (a.out) {
+                k_norm_fwd<TI, NT, NC, CH, true><<<a.parts, NT, 0, st>>>(a, vec);
+                return cudaSuccess;
+            }
+        }
+        k_norm_fwd<TI, NT, NC, CH, false><<<a.parts, NT, 0, st>>>(a, vec);
     }
     return cudaSuccess;
 }

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from chunkwise_delta_rule_gb300 import _lib
 from oracle import layer
 from tests.helpers import check_close, np64
 from tests.test_gpu_layer import gen_of, scan_case, scan_problem, tol, wide_rows
@@ -139,6 +140,85 @@ def test_tensors_of_another_device_are_refused():
         kda.make_norm_problem(x, w, residual=r.cpu())
 
 
+def test_refusals_of_otherwise_valid_calls():
+    """One property off at a time."""
+    import chunkwise_delta_rule_gb300 as kda
+    from tests.test_gpu_layer import conv_case, norm_case
+    _, c, _, _ = conv_case(dict(io="bf16", B=2, T=10, D=16, W=4, state=True), 79)
+    k, s, _, _ = scan_case(dict(io="bf16", B=2, T=10, D=16, S=16, state=True), 79)
+    x, r, w, dy = norm_case("fp32", 4, 64, 79)
+    long = torch.zeros(2, 10, 32, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+
+    def conv(**kw):
+        a = dict(x=c["x"], weight=c["w"], bias=c["bias"], initial_state=c["h0"])
+        return kda.make_conv_problem(**dict(a, **kw))
+
+    def scan(save=0, **kw):
+        return scan_problem(k, dict(s, **kw), None, save)
+
+    conv(), scan()
+    with pytest.raises(ValueError, match="x must be a CUDA tensor|x must be"):
+        conv(x=c["x"].half())
+    with pytest.raises(ValueError, match="weight must be a contiguous"):
+        conv(weight=c["w"].bfloat16())
+    with pytest.raises(ValueError, match="weight must be a contiguous"):
+        conv(weight=c["w"][:8])
+    with pytest.raises(ValueError, match="bias must be a contiguous"):
+        conv(bias=c["bias"][:8])
+    with pytest.raises(ValueError, match="initial_state must be a contiguous"):
+        conv(initial_state=c["h0"][:, :2])
+    with pytest.raises(ValueError, match="initial_state must be a contiguous"):
+        conv(initial_state=c["h0"].float())
+    with pytest.raises(ValueError, match="x's rows must be dense"):
+        conv(x=long[..., ::2])
+    with pytest.raises(ValueError, match="x's tokens must be evenly spaced"):
+        conv(x=torch.zeros(2, 12, 16, dtype=torch.bfloat16, device="cuda")[:, :10])
+    with pytest.raises(ValueError, match="x's tokens must be evenly spaced"):
+        conv(x=c["x"][:, :1].expand(2, 10, 16))
+    with pytest.raises(ValueError, match="dt must be a CUDA tensor"):
+        scan(dt=s["dt"].float())
+    with pytest.raises(ValueError, match="b must be a CUDA tensor|c must be a CUDA tensor"):
+        scan(c=s["c"][..., :8])
+    with pytest.raises(ValueError, match="z's rows must be dense"):
+        scan(z=long[..., ::2])
+    with pytest.raises(ValueError, match="A_log must be a contiguous"):
+        scan(A_log=s["A_log"].double())
+    one = {n: s[n][:1] for n in ("x", "dt", "b", "c", "z")}
+    one["h0"] = s["h0"][:1]
+    scan_problem(k, dict(s, **one), cu)
+    with pytest.raises(ValueError, match="cu_seqlens must be an int32"):
+        scan_problem(k, dict(s, **one), cu.long())
+    with pytest.raises(ValueError, match="cu_seqlens must be an int32"):
+        scan_problem(k, dict(s, **one), cu[:1])
+    with pytest.raises(ValueError, match="packed sequences need B == 1"):
+        scan_problem(k, s, cu)
+    p = scan(1)
+    with pytest.raises(ValueError, match="save_policy 1 needs the forward's saved buffer"):
+        kda.kda_ssm_bwd(p, s["dy"])
+    saved = kda.kda_ssm_fwd(p)[2]
+    with pytest.raises(ValueError, match="save_policy 1 needs the forward's saved buffer"):
+        kda.kda_ssm_bwd(p, s["dy"], saved=saved[:-1])
+    with pytest.raises(ValueError, match="dy must be a contiguous"):
+        kda.kda_ssm_bwd(scan(), s["dy"].float())
+    with pytest.raises(ValueError, match="dht must be a contiguous"):
+        kda.kda_ssm_bwd(scan(), s["dy"], s["dht"][:1])
+    with pytest.raises(ValueError, match="ht must be a contiguous"):
+        kda.kda_ssm_fwd(scan(), ht=s["h0"].transpose(1, 2))
+    with pytest.raises(ValueError, match="x must be a contiguous"):
+        kda.make_norm_problem(x[:, ::2], w[:32].contiguous())
+    with pytest.raises(ValueError, match="weight must be a contiguous"):
+        kda.make_norm_problem(x, w[:32])
+    with pytest.raises(ValueError, match="residual must be a contiguous"):
+        kda.make_norm_problem(x, w, residual=r.bfloat16())
+    with pytest.raises(ValueError, match="h must be a contiguous"):
+        kda.kda_norm_fwd(kda.make_norm_problem(x, w, residual=r), h=r[:2])
+    with pytest.raises(_lib.KdaError, match="group must be"):
+        kda.kda_norm_fwd(kda.make_norm_problem(x, w, out="e4m3", group=48))
+    with pytest.raises(ValueError, match="dres must be a contiguous"):
+        kda.kda_norm_bwd(kda.make_norm_problem(x, w), dy, r.bfloat16())
+
+
 def test_sizes_beyond_32_bits_are_refused():
     """They do not fit the C interface; cut to 32 bits they would be other, smaller calls."""
     import chunkwise_delta_rule_gb300 as kda
@@ -263,6 +343,39 @@ def test_gradient_of_the_rates_sums_long_rows():
     want = A * dA.sum(0)
     err = float((got.double() - want).norm() / want.norm())
     assert err <= 4e-7, err
+
+
+PIECES = [
+    dict(io="bf16", B=1, T=1500, D=40, S=16, state=True, pad=3),
+    dict(io="bf16", B=3, T=900, D=24, S=8, G=2),
+    dict(io="fp32", B=2, T=700, D=34, S=6, G=2, state=True, pad=1, skip=False),
+    dict(io="bf16", B=1, D=36, S=32, state=True, lengths=[0, 500, 1, 700, 33]),
+    dict(io="fp32", B=1, T=600, D=10, S=64, G=2, state=True, gate=False, softplus=False, bias=False),
+    dict(io="bf16", B=4, T=333, D=72, S=20, state=True),
+    dict(io="fp32", B=1, D=33, S=41, state=True, lengths=[31, 1, 1, 800, 64]),
+    dict(io="bf16", B=1, D=24, S=16, state=True, lengths=[1] * 300 + [400] + [1] * 20),
+]
+
+
+@pytest.mark.parametrize("kw", PIECES, ids=lambda kw: "-".join(f"{n}{v}" for n, v in kw.items() if n != "lengths"))
+def test_scan_in_time_pieces(kw):
+    """Few channels and long rows of every kind that is cut into time pieces: types, states per lane, groups, unaligned
+    rows, several rows, packed ones, without gate, skip, bias or softplus; the states in place."""
+    import chunkwise_delta_rule_gb300 as kda
+    k, c, cu, ref = scan_case(kw, 88)
+    for save in (0, 1):
+        p = scan_problem(k, c, cu, save)
+        assert kda.kda_ssm_workspace_size(p, False) > 0      # in pieces
+        y, ht, saved = kda.kda_ssm_fwd(p)
+        g = kda.kda_ssm_bwd(p, c["dy"], c["dht"], saved=saved, need_dh0=True)
+        for name, t in dict(y=y, ht=ht, dx=g.dx, ddt=g.ddt, dA_log=g.dA_log, db=g.db, dc=g.dc, dd_skip=g.dd_skip,
+                            dz=g.dz, ddt_bias=g.ddt_bias, dh0=g.dh0).items():
+            if t is not None:
+                check_close(name, np64(t).reshape(ref[name].shape), ref[name], tol(t, True))
+    if c["h0"] is not None:
+        c["state"] = c["h0"].clone()
+        y2, _, _ = kda.kda_ssm_fwd(scan_problem(k, c, cu, h0="state"), ht=c["state"])
+        assert torch.equal(y2, y) and torch.equal(c["state"], ht)
 
 
 # ------------------------------------------------------------------ autograd

@@ -4,7 +4,9 @@ CUDA)."""
 import ctypes
 
 import pytest
+import torch
 
+import chunkwise_delta_rule_gb300 as kda
 from chunkwise_delta_rule_gb300 import _lib
 from tests.test_layer_abi import VP, X, norm, ssm
 
@@ -28,3 +30,28 @@ def test_the_scans_backward_with_an_error_word_refuses_what_it_refuses_without()
         assert lib.kda_ssm_bwd_err(ctypes.byref(p), VP(X), None, None, ctypes.byref(g), VP(X), 1 << 40, VP(X), None) == status
     p = ssm()
     assert lib.kda_ssm_bwd_err(ctypes.byref(p), VP(X), None, None, ctypes.byref(g), None, 0, VP(X), None) == 3
+
+
+def test_the_binding_names_what_it_refuses():
+    """Types and ranks are told apart from tensors that are not on a GPU."""
+    x, w = torch.zeros(2, 10, 16), torch.zeros(16, 4)
+    with pytest.raises(ValueError, match="x must be a CUDA tensor"):
+        kda.make_conv_problem(x, w)
+    with pytest.raises(ValueError, match="x must be a CUDA tensor"):
+        kda.make_ssm_problem(x, x, torch.zeros(16, 16), torch.zeros(2, 10, 1, 16), torch.zeros(2, 10, 1, 16))
+    with pytest.raises(ValueError, match="x must be a contiguous CUDA tensor"):
+        kda.make_norm_problem(x, torch.zeros(16))
+    for bad in (x.half(), x.double(), x[0]):
+        with pytest.raises(ValueError, match=r"x must be \[B, T, D\], bf16 or fp32"):
+            kda.make_conv_problem(bad, w)
+        with pytest.raises(ValueError, match=r"x must be \[B, T, D\], bf16 or fp32"):
+            kda.make_ssm_problem(bad, bad, torch.zeros(16, 16), torch.zeros(2, 10, 1, 16), torch.zeros(2, 10, 1, 16))
+    for bad in (x.half(), x.double(), torch.zeros(())):
+        with pytest.raises(ValueError, match="x must be bf16 or fp32 rows"):
+            kda.make_norm_problem(bad, torch.zeros(16))
+    with pytest.raises(ValueError, match=r"weight must be \[D, W\]"):
+        kda.make_conv_problem(x, w[0])
+    with pytest.raises(ValueError, match=r"b must be \[B, T, G, S\]"):
+        kda.make_ssm_problem(x, x, torch.zeros(16, 16), torch.zeros(2, 10, 16), torch.zeros(2, 10, 16))
+    with pytest.raises(ValueError, match="out must be"):
+        kda.make_norm_problem(x, torch.zeros(16), out="fp8")

@@ -34,7 +34,7 @@ __device__ __forceinline__ float ssm_softplus(float v) { return ssm_softplus2(ma
 // Decays 2^(delta A) of exponents in log2 units. The hardware's 2^x lies below the value on the average: 1.7e-8 to 3.2e-8
 // of it for exponents of -2^-8 .. -1, 5e-9 to 9e-9 for smaller ones (measured against 64 bits), and a state multiplies
 // the decays of all the tokens that it remembers. A constant in the exponent, added by the product's own instruction,
-// leaves at most 1.2e-8 (training four rows of 2048 tokens, 2048 channels: dA_log 1.5e-6 from 64 bits without it, 1.0e-6 with it).
+// leaves at most 1.2e-8 and is itself lost in 1: a token of step 0 leaves the state as it is (training four rows of 2048 tokens, 2048 channels: dA_log 1.5e-6 from 64 bits without it, 1.0e-6 with it).
 constexpr float SSM_EX2_MEAN = 2.5e-8f;
 __device__ __forceinline__ float2 ssm_exponent2(float2 dl, float2 A2) { return fma2(dl, A2, make_float2(SSM_EX2_MEAN, SSM_EX2_MEAN)); }
 __device__ __forceinline__ float ssm_decay(float dl, float A2) { return ex2(fmaf(dl, A2, SSM_EX2_MEAN)); }

@@ -299,6 +299,20 @@ def test_decays_do_not_drift(g):
             assert abs(drift) <= 1.5e-8, (T, drift)
 
 
+@pytest.mark.parametrize("softplus", [True, False])
+def test_tokens_of_step_zero_leave_the_state_as_it_is(softplus):
+    """Padding inside a row: the decay of a zero step is 1 and nothing is added, to the last bit, over thousands of
+    tokens; the adjoint passes through too."""
+    import chunkwise_delta_rule_gb300 as kda
+    k, c, _, _ = scan_case(dict(io="fp32", B=2, T=3, D=40, S=16, state=True, bias=False, softplus=softplus), 89)
+    for T in (6, 2000):
+        x, b, cm, z = (torch.randn(2, T, *c[n].shape[2:], device="cuda") for n in ("x", "b", "c", "z"))
+        dt = torch.full((2, T, 40), float("-inf") if softplus else 0.0, device="cuda")
+        p = kda.make_ssm_problem(x, dt, c["A_log"], b, cm, z=z, dt_softplus=softplus, initial_state=c["h0"])
+        assert torch.equal(kda.kda_ssm_fwd(p)[1], c["h0"])
+        assert torch.equal(kda.kda_ssm_bwd(p, torch.zeros_like(x), c["dht"]).dh0, c["dht"])
+
+
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
 @pytest.mark.parametrize("S", [16, 20])
 def test_decoding_and_prefill_give_the_same_states(io, S):

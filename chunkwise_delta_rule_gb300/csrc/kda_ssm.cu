@@ -369,6 +369,11 @@ __global__ void __launch_bounds__(FwdShape<TI, EL, MODE>::THREADS, 1) k_ssm_fwd(
             }
             hand_over(&sm.full[w]);
         }
+        // The products are complete before the tensor memory goes back. The recurrence waits for them as well, but no longer
+        // after a wait that gave up.
+        if (threadIdx.x < RT + 32)
+            for (int k = max(ntiles - 2, 0); k < ntiles; ++k)
+                if (!tc::mbar_wait(&sm.full[k & 1], (k >> 1) & 1) && a.err) atomicOr(a.err, 2);
     } else {
         // ---------------------------------------------------------------- the recurrence
         const int tid = threadIdx.x, l = tid & 3, ch = tid >> 2, n0 = l * EL, d = pl.c0 + ch;

@@ -12,10 +12,11 @@
 // filters pass through shared memory too: read directly, each lane's values lie apart
 // from its neighbour's and cost more than the tile's inputs.
 // Bound by HBM where the tensors are large, bf16, 4096 channels, four taps: forward of
-// 32768 packed tokens 92 us, 5.8 TB/s (86% of the copy rate); backward of two rows of
-// 8192 98 us, 4.1 TB/s (61%: its parameters' sums and recomputed outputs make it issue
-// 0.57 instructions per cycle and scheduler at 22% of the warps); a token of each of 64
-// sequences 3.3 us on the device, where the launch is what it waits for.
+// 32768 packed tokens 93 us, 5.8 TB/s (85% of the copy rate); backward of two rows of
+// 8192 98 us, 4.1 TB/s (61%: neither the memory nor the issue slots, 0.57 instructions
+// per cycle and scheduler, are full; its rings and its sums' registers leave two CTAs on
+// an SM, 22% of the warps). A token of each of 64 sequences of 12288 channels takes 3.3
+// us on the device, where the launch is what it waits for.
 #include "kda_layer.cuh"
 
 namespace kda {

@@ -11,8 +11,8 @@
 // A CTA holds a row in registers, so each tensor is read once; it walks rows with the
 // weight (and its gradient's sums) kept in registers and the next row's loads in
 // flight while the present row is summed and written.
-// Bound by HBM, 16384 rows of 4096, bf16: forward with residual and e4m3 output 80 us,
-// 5.9 TB/s (87% of the copy rate; 1024 threads per SM at 64 registers: at 72 registers
+// Bound by HBM, 16384 rows of 4096, bf16: forward with residual and e4m3 output 82 us,
+// 5.7 TB/s (85% of the copy rate; 1024 threads per SM at 64 registers: at 72 registers
 // three CTAs per SM instead of four, 118 us); backward 101 us, 5.3 TB/s (78%). Sums and
 // the row are fp32 throughout.
 #include <cuda_fp8.h>
@@ -367,8 +367,8 @@ cudaError_t run_one(NormArgs a, int vec, cudaStream_t st) {
 
 // Threads and elements per thread by the row's width, so that about 1024 threads of an SM share its rows. Measured forward,
 // 16384 rows, bf16, e4m3 output, taken against the other side: D = 256 with 32 threads 6.2 us against 11.6 with 128; 2048
-// with 256 x 8 42.3 against 56.9 with 128 x 16; 4096 with 256 x 16 80.5 against 82.4 with 512 x 8; 8192 with 1024 x 8 172
-// against 228 with 512 x 16.
+// with 256 x 8 42.3 against 56.9 with 128 x 16; 4096 with 256 x 16 80.5 against 82.4 with 512 x 8; 8192 with 1024 x 8 175
+// against 234 with 512 x 16, 5120 150 against 212, 6144 158 against 217, 7168 166 against 226.
 template <typename TI, int CH, bool BWD>
 cudaError_t run_width(const NormArgs& a, int vec, cudaStream_t st) {
     if (a.D <= 256) return run_one<TI, 32, 8 / CH, CH, BWD>(a, vec, st);

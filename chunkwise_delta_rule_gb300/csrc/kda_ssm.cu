@@ -20,7 +20,7 @@
 // add up to its 24 bits.
 // Per four states and token the recurrence takes 4 exponentials (16 cycles of a
 // scheduler's share at 32 per cycle and SM) and 8 paired multiply-adds (16 cycles).
-// Measured, two rows of 8192 tokens, 4096 channels of 16 states, bf16: 408 us, 1.3 TB/s
+// Measured, two rows of 8192 tokens, 4096 channels of 16 states, bf16: 406 us, 1.3 TB/s
 // of the tensors' bytes (20% of the copy rate). The bound is instruction dispatch: on
 // the 128 SMs that two rows of 64 channel tiles fill, a scheduler spends 106 cycles on
 // four tokens of a warp's recurrence however many warps it has (a paired multiply-add
@@ -727,7 +727,8 @@ void run_step_states(const SsmArgs& a, cudaStream_t st) {
 // Tokens per sequence up to which k_ssm_step takes them: it pays no start of tiles (5 us a wave of CTAs), the forward
 // nothing for a token's latency. Measured, 4096 channels of 16 states: one sequence of 6 tokens 5.2 against 6.0 us, of 8
 // 6.4 against 5.9; 8 sequences of 24 20.9 against 25.7, of 32 27 against 22; 64 of 24 104 against 165. 64 sequences, 1024
-// channels of 64 states: 8 tokens 30 against 39, 16 tokens 52 against 47.
+// channels of 64 states: 8 tokens 30 against 39, 16 tokens 52 against 47. The rule is coarse between the two: 3 sequences of
+// 8 tokens (192 CTAs of the forward) 9.3 against 12.6, of 24 18.6 against 14.6; 5 of 8 9.1 against 17.1, of 24 18.7 against 20.7.
 int step_tokens(const SsmArgs& a) {
     if ((long long)a.ax.rows * fwd_tiles(a.D, a.G) < 3 * sm_count()) return 6;
     return a.S <= 16 ? 24 : 12;

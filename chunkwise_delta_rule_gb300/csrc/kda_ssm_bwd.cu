@@ -14,7 +14,7 @@
 // halving exchanges, over the CTA's warps in shared memory and over the CTAs' rows in
 // a second kernel, in a fixed order; the parameters' gradients go the same way, so
 // nothing depends on timing.
-// Measured, four rows of 2048 tokens, 2048 channels of 16 states, bf16: 421 us (and 17
+// Measured, four rows of 2048 tokens, 2048 channels of 16 states, bf16: 418 us (and 16
 // for the second kernel), beside a floor of 55 us for the bytes and about 100 for the
 // multiply-adds. As in the forward the bound is instruction dispatch (0.63 instructions
 // per cycle on the busiest scheduler, a fifth of them paired ones that hold it twice):

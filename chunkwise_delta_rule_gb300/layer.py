@@ -5,7 +5,10 @@ scan and the root-mean-square norm.
 As in ``ops``: PyTorch provides device memory and the current stream, every step
 runs in libkda.so's CUDA kernels. Token tensors are [B, T, ...]; inputs may be
 slices of wider rows (the last axis dense, tokens evenly spaced), outputs are
-contiguous. Parameters and scan states are fp32. The argument checks and the
+contiguous. All tensors of a call lie on one device. A call with ``stream`` allocates
+and runs on it; that its inputs are ready there, and its outputs where they are
+used, is the caller's to order, as everywhere in PyTorch. Parameters and scan states
+are fp32. The argument checks and the
 calls are compiled (``csrc/binding.cpp``): a decoding step is short, and in
 Python they would take longer than it.
 """

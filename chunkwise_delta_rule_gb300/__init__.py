@@ -19,19 +19,32 @@ from .ops import (  # noqa: F401
     make_problem,
 )
 from .layer import (  # noqa: F401
+    LinGrads,
+    Quant8,
     SsmGrads,
     kda_conv_bwd,
     kda_conv_fwd,
     kda_conv_workspace_size,
+    kda_lin_bwd,
+    kda_lin_fwd,
+    kda_lin_workspace_size,
+    kda_mm8,
+    kda_mm8_workspace_size,
     kda_norm_bwd,
     kda_norm_fwd,
     kda_norm_workspace_size,
+    kda_quant8,
     kda_ssm_bwd,
     kda_ssm_fwd,
     kda_ssm_saved_size,
     kda_ssm_workspace_size,
+    linear8,
+    linear_attention,
     make_conv_problem,
+    make_lin_problem,
+    make_mm8_problem,
     make_norm_problem,
+    make_quant8_problem,
     make_ssm_problem,
     rms_norm,
     short_conv,

@@ -90,6 +90,38 @@ class NormProblem(ctypes.Structure):
     ]
 
 
+class LinProblem(ctypes.Structure):
+    """Mirror of ``kda_lin_problem``."""
+
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("K", ctypes.c_int), ("V", ctypes.c_int),
+        ("N", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
+        ("io", ctypes.c_int), ("HV", ctypes.c_int), ("scale", ctypes.c_float),
+        ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("decay", ctypes.c_void_p), ("h0", ctypes.c_void_p),
+    ]
+
+
+class Quant8Problem(ctypes.Structure):
+    """Mirror of ``kda_quant8_problem``."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int), ("D", ctypes.c_int), ("io", ctypes.c_int), ("blocks", ctypes.c_int),
+        ("ldx", ctypes.c_int64), ("ldq", ctypes.c_int64), ("ldqt", ctypes.c_int64), ("x", ctypes.c_void_p),
+    ]
+
+
+class Mm8Problem(ctypes.Structure):
+    """Mirror of ``kda_mm8_problem``."""
+
+    _fields_ = [
+        ("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int), ("out", ctypes.c_int), ("b_rows", ctypes.c_int),
+        ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
+        ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale_a", ctypes.c_void_p), ("scale_b", ctypes.c_void_p),
+    ]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status: int, where: str, msg: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {msg}")
@@ -126,6 +158,7 @@ def load() -> ctypes.CDLL:
     lib.kda_recurrent_fwd.argtypes = [P, vp, vp, vp, vp]
     lib.kda_recurrent_fwd.restype = ctypes.c_int
     CP, SP, NP = ctypes.POINTER(ConvProblem), ctypes.POINTER(SsmProblem), ctypes.POINTER(NormProblem)
+    LP, QP, MP = ctypes.POINTER(LinProblem), ctypes.POINTER(Quant8Problem), ctypes.POINTER(Mm8Problem)
     for name, args, res in (
             ("kda_conv_fwd", [CP, vp, vp, vp, vp], ctypes.c_int),
             ("kda_conv_workspace_size", [CP], sz),
@@ -137,7 +170,13 @@ def load() -> ctypes.CDLL:
             ("kda_ssm_bwd_err", [SP, vp, vp, vp, ctypes.POINTER(SsmGrads), vp, sz, vp, vp], ctypes.c_int),
             ("kda_norm_fwd", [NP, vp, vp, vp, vp], ctypes.c_int),
             ("kda_norm_workspace_size", [NP], sz),
-            ("kda_norm_bwd", [NP, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int)):
+            ("kda_norm_bwd", [NP, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+            ("kda_lin_workspace_size", [LP, ctypes.c_int], sz),
+            ("kda_lin_fwd", [LP, vp, vp, vp, sz, vp, vp], ctypes.c_int),
+            ("kda_lin_bwd", [LP, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp], ctypes.c_int),
+            ("kda_quant8", [QP, vp, vp, vp, vp, vp], ctypes.c_int),
+            ("kda_mm8_workspace_size", [MP], sz),
+            ("kda_mm8", [MP, vp, vp, sz, vp, vp], ctypes.c_int)):
         f = getattr(lib, name)
         f.argtypes, f.restype = args, res
     lib.kda_abi_version.argtypes = []

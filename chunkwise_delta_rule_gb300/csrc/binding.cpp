@@ -319,6 +319,182 @@ py::tuple norm_bwd(const Norm& p, Tensor dy, OptT dres, OptT ws, py::object stre
     return py::make_tuple(dx, dw);
 }
 
+// ------------------------------------------------------------------ linear attention
+struct Lin {
+    kda_lin_problem c{};
+    Tensor q, k, v;
+    OptT decay, h0, cu;
+    std::vector<int64_t> state;
+    Lin(Tensor q_, Tensor k_, Tensor v_, OptT d, std::optional<double> scale, OptT h, OptT cu_)
+        : q(q_), k(k_), v(v_), decay(d), h0(h), cu(cu_) {
+        need(q.dim() == 4, "q must be [B, T, H, K], bf16 or fp32");
+        c.io = io_of(q, "q must be [B, T, H, K], bf16 or fp32");
+        need(v.dim() == 4, "v must be [B, T, HV, V]");
+        const int64_t B = q.size(0), T = q.size(1), H = q.size(2), K = q.size(3), HV = v.size(2), V = v.size(3);
+        c.B = size(B, "B"); c.T = size(T, "T"); c.H = size(H, "H"); c.K = size(K, "K"); c.HV = size(HV, "HV"); c.V = size(V, "V");
+        need(HV >= 1, "v must have a head");
+        c.ldq = rows(q, "q", q.sizes(), q.scalar_type(), q);
+        c.ldk = rows(k, "k", q.sizes(), q.scalar_type(), q);
+        c.ldv = rows(v, "v", {B, T, HV, V}, q.scalar_type(), q);
+        const int64_t n = axis(cu, B, c.N, c.cu_seqlens, q);
+        state = {n, HV, K, V};
+        if (scale) need(*scale > 0 && *scale <= 3e38, "scale must be positive and finite");
+        c.scale = scale ? (float)*scale : 0.f;
+        need(!scale || c.scale > 0.f, "scale must be positive and finite");
+        c.q = q.data_ptr();
+        c.k = k.data_ptr();
+        c.v = v.data_ptr();
+        c.decay = f32(decay, "decay", {HV}, q);
+        c.h0 = f32(h0, "initial_state", state, q);
+    }
+};
+py::tuple lin_fwd(const Lin& p, bool out_final, OptT ht, OptT ws, OptT err, py::object stream) {
+    OnStream on(stream, p.q);
+    on.takes(p.q, p.k, p.v, p.decay, p.h0, p.cu, ht, ws, err);
+    Tensor o = at::empty(p.v.sizes(), p.v.options());
+    if (!ht && out_final) ht = at::empty(p.state, p.q.options().dtype(at::kFloat));
+    float* h = f32(ht, "ht", p.state, p.q);
+    ws = buffer(kda_lin_workspace_size(&p.c, 0), "workspace", p.q, ws);
+    check(kda_lin_fwd(&p.c, o.data_ptr(), h, ptr(ws), bytes(ws), error_word(err, p.q), on), "kda_lin_fwd");
+    on.gives(o, ht);
+    return py::make_tuple(o, ht);
+}
+py::tuple lin_bwd(const Lin& p, Tensor dout, OptT dht, OptT ws, py::object stream, std::optional<bool> need_dh0, OptT err) {
+    OnStream on(stream, p.q);
+    on.takes(p.q, p.k, p.v, p.decay, p.h0, p.cu, dout, dht, ws, err);
+    void* pdo = dense(dout, "do", p.v.sizes(), p.q.scalar_type(), p.q);
+    float* pdh = f32(dht, "dht", p.state, p.q);
+    Tensor dq = at::empty(p.q.sizes(), p.q.options()), dk = at::empty(p.q.sizes(), p.q.options()),
+           dv = at::empty(p.v.sizes(), p.q.options());
+    OptT dh0;
+    if (need_dh0 ? *need_dh0 : p.h0.has_value()) dh0 = at::empty(p.state, p.q.options().dtype(at::kFloat));
+    ws = buffer(kda_lin_workspace_size(&p.c, 1), "workspace", p.q, ws);
+    check(kda_lin_bwd(&p.c, pdo, pdh, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), static_cast<float*>(ptr(dh0)), ptr(ws),
+                      bytes(ws), error_word(err, p.q), on), "kda_lin_bwd");
+    on.gives(dq, dk, dv, dh0);
+    return py::make_tuple(dq, dk, dv, dh0);
+}
+
+// ------------------------------------------------------------------ 8 bits
+// The rows of a [..., D] tensor whose last axis is dense and whose rows are evenly spaced: their number and the elements
+// between them (0: contiguous).
+int64_t flat_rows(const Tensor& t, const char* name, int64_t& ld) {
+    const int64_t D = t.size(-1);
+    if (D < 1) throw py::value_error(std::string(name) + " must have columns");
+    ld = 0;
+    const int64_t n = t.numel() / D;
+    if (t.is_contiguous() || n == 0) return n;
+    int64_t step = D, span = 0;
+    bool first = true;
+    for (int64_t i = t.dim() - 2; i >= 0; --i) {
+        if (t.size(i) == 1) continue;
+        if (first) step = t.stride(i);
+        else if (t.stride(i) != span) throw py::value_error(std::string(name) + "'s rows must be evenly spaced");
+        first = false;
+        span = t.stride(i) * t.size(i);
+    }
+    if ((D > 1 && t.stride(-1) != 1) || step < D) throw py::value_error(std::string(name) + "'s rows must be dense");
+    ld = step;
+    return n;
+}
+int64_t groups_of(int64_t n) { return (n + 127) / 128; }
+// Rows of e4m3 that start every 16 bytes, so that a product reads them in whole accesses.
+Tensor rows8(at::IntArrayRef lead, int64_t D, const Tensor& x) {
+    std::vector<int64_t> shape(lead.begin(), lead.end()), strides(lead.size() + 1, 1);
+    shape.push_back(D);
+    const int64_t ld = (D + 15) / 16 * 16;
+    int64_t n = ld;
+    for (int64_t i = (int64_t)lead.size() - 1; i >= 0; --i) {
+        strides[i] = n;
+        n *= shape[i];
+    }
+    return at::empty_strided(shape, strides, x.options().dtype(at::kFloat8_e4m3fn));
+}
+
+struct Quant8 {
+    kda_quant8_problem c{};
+    Tensor x;
+    bool rows, transposed;
+    std::vector<int64_t> lead;
+    Quant8(Tensor x_, bool blocks, bool rows_, bool transposed_) : x(x_), rows(rows_), transposed(transposed_) {
+        need(x.dim() >= 1, "x must be bf16 or fp32 rows");
+        c.io = io_of(x, "x must be bf16 or fp32 rows");
+        if (!x.is_cuda()) refuse("x", "", x.sizes(), x.scalar_type());
+        need(rows || transposed, "one of rows and transposed must be asked for");
+        int64_t ld = 0;
+        const int64_t n = flat_rows(x, "x", ld);
+        c.rows = size(n, "the number of rows");
+        c.D = size(x.size(-1), "D");
+        c.blocks = blocks;
+        c.ldx = ld;
+        c.x = x.data_ptr();
+        lead.assign(x.sizes().begin(), x.sizes().end() - 1);
+    }
+};
+py::tuple quant8(const Quant8& p, py::object stream) {
+    OnStream on(stream, p.x);
+    on.takes(p.x);
+    const int64_t R = p.c.rows, D = p.c.D;
+    const auto f32o = p.x.options().dtype(at::kFloat);
+    kda_quant8_problem c = p.c;
+    OptT q, scale, qt, scale_t;
+    if (p.rows) {
+        q = rows8(p.lead, D, p.x);
+        std::vector<int64_t> s = p.lead;
+        if (c.blocks) s = {groups_of(R)};
+        s.push_back(groups_of(D));
+        scale = at::empty(s, f32o);
+        c.ldq = (D + 15) / 16 * 16;
+    }
+    if (p.transposed) {
+        qt = rows8({D}, R, p.x);
+        scale_t = at::empty({c.blocks ? groups_of(D) : D, groups_of(R)}, f32o);
+        c.ldqt = (R + 15) / 16 * 16;
+    }
+    check(kda_quant8(&c, ptr(q), static_cast<float*>(ptr(scale)), ptr(qt), static_cast<float*>(ptr(scale_t)), on), "kda_quant8");
+    on.gives(q, scale, qt, scale_t);
+    return py::make_tuple(q, scale, qt, scale_t);
+}
+
+struct Mm8 {
+    kda_mm8_problem c{};
+    Tensor a, sa, b, sb;
+    std::vector<int64_t> out;
+    Mm8(Tensor a_, Tensor sa_, Tensor b_, Tensor sb_, const std::string& type) : a(a_), sa(sa_), b(b_), sb(sb_) {
+        need(a.dim() >= 1 && a.scalar_type() == at::kFloat8_e4m3fn, "a must be e4m3 rows");
+        need(b.dim() == 2 && b.scalar_type() == at::kFloat8_e4m3fn, "b must be e4m3 [N, K]");
+        need(type == "bf16" || type == "fp32", "out must be \"bf16\" or \"fp32\"");
+        if (!a.is_cuda()) refuse("a", "", a.sizes(), a.scalar_type());
+        if (!b.is_cuda() || b.size(1) != a.size(-1)) refuse("b", "", {b.size(0), a.size(-1)}, b.scalar_type());
+        same_device(b, "b", a);
+        int64_t lda = 0, ldb = 0;
+        const int64_t M = flat_rows(a, "a", lda), K = a.size(-1), N = flat_rows(b, "b", ldb), G = groups_of(K);
+        c.M = size(M, "M"); c.N = size(N, "N"); c.K = size(K, "K");
+        c.lda = lda; c.ldb = ldb;
+        c.out = type == "bf16" ? KDA_BF16 : KDA_FP32;
+        out.assign(a.sizes().begin(), a.sizes().end());
+        std::vector<int64_t> s = out;
+        s.back() = G;
+        out.back() = N;
+        c.b_rows = sb.dim() == 2 && sb.size(0) == N && N > 1;
+        c.scale_a = static_cast<float*>(dense(sa, "scale_a", s, at::kFloat, a));
+        c.scale_b = static_cast<float*>(dense(sb, "scale_b", {c.b_rows ? N : groups_of(N), G}, at::kFloat, a));
+        c.a = a.data_ptr();
+        c.b = b.data_ptr();
+    }
+};
+Tensor mm8(const Mm8& p, OptT y, OptT ws, OptT err, py::object stream) {
+    OnStream on(stream, p.a);
+    on.takes(p.a, p.sa, p.b, p.sb, y, ws, err);
+    const at::ScalarType type = p.c.out == KDA_BF16 ? at::kBFloat16 : at::kFloat;
+    if (!y) y = at::empty(p.out, p.a.options().dtype(type));
+    void* py = dense(y, "y", p.out, type, p.a);
+    ws = buffer(kda_mm8_workspace_size(&p.c), "workspace", p.a, ws);
+    check(kda_mm8(&p.c, py, ptr(ws), bytes(ws), error_word(err, p.a), on), "kda_mm8");
+    on.gives(y);
+    return *y;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_binding, m) {
@@ -352,5 +528,28 @@ PYBIND11_MODULE(_binding, m) {
     m.def("norm_workspace_size", [](const Norm& p) {
         const c10::cuda::CUDAGuard device(p.x.device());
         return kda_norm_workspace_size(&p.c);
+    });
+    py::class_<Lin>(m, "LinProblem", "A validated linear attention call plus the tensors it points to.")
+        .def(py::init<Tensor, Tensor, Tensor, OptT, std::optional<double>, OptT, OptT>())
+        .def_readonly("q", &Lin::q)
+        .def_readonly("state_shape", &Lin::state);
+    py::class_<Quant8>(m, "Quant8Problem", "A validated rounding to 8 bits plus the tensor it points to.")
+        .def(py::init<Tensor, bool, bool, bool>())
+        .def_readonly("x", &Quant8::x);
+    py::class_<Mm8>(m, "Mm8Problem", "A validated 8-bit product plus the tensors it points to.")
+        .def(py::init<Tensor, Tensor, Tensor, Tensor, const std::string&>())
+        .def_readonly("a", &Mm8::a)
+        .def_readonly("shape", &Mm8::out);
+    m.def("lin_fwd", &lin_fwd);
+    m.def("lin_bwd", &lin_bwd);
+    m.def("lin_workspace_size", [](const Lin& p, bool backward) {
+        const c10::cuda::CUDAGuard device(p.q.device());
+        return kda_lin_workspace_size(&p.c, backward);
+    });
+    m.def("quant8", &quant8);
+    m.def("mm8", &mm8);
+    m.def("mm8_workspace_size", [](const Mm8& p) {
+        const c10::cuda::CUDAGuard device(p.a.device());
+        return kda_mm8_workspace_size(&p.c);
     });
 }

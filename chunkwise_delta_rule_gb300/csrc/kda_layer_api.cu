@@ -1,52 +1,11 @@
 // C entry points of the layer operators (short convolution, selective state space
 // scan, root-mean-square norm): argument validation, workspace layout, launch
 // order. Contracts in include/kda.h.
-#include <string>
-
-#include "../../include/kda.h"
-#include "kda_layer.cuh"
-
-namespace kda {
-void set_last_error(const char* msg);
-}
+#include "kda_api.cuh"
 
 namespace {
 
-constexpr size_t ALIGN = 256;
-size_t up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
-
-kda_status fail(kda_status st, const char* msg) {
-    kda::set_last_error(msg);
-    return st;
-}
-kda_status cuda_result(cudaError_t e, const char* where) {
-    if (e == cudaSuccess) return KDA_OK;
-    kda::set_last_error((std::string(where) + ": " + cudaGetErrorString(e)).c_str());
-    return KDA_ERR_CUDA;
-}
-kda_status check_ws(const void* ws, size_t bytes, size_t need, const char* what) {
-    if (need == 0) return KDA_OK;
-    if (ws && reinterpret_cast<uintptr_t>(ws) % ALIGN == 0 && bytes >= need) return KDA_OK;
-    kda::set_last_error((std::string(what) + " missing, not 256-byte aligned or below " + std::to_string(need) + " bytes").c_str());
-    return KDA_ERR_WORKSPACE;
-}
-
-int esize(kda_dtype io) { return io == KDA_BF16 ? 2 : 4; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// The token axis of B sequences of T tokens, or of N packed ones.
-kda_status make_axis(int B, int T, int N, const int32_t* cu, int D, kda_dtype io, kda::TokenAxis& ax) {
-    if (B < 1 || T < 0 || D < 1) return fail(KDA_ERR_INVALID_ARG, "B and D must be >= 1 and T >= 0");
-    if (io != KDA_BF16 && io != KDA_FP32) return fail(KDA_ERR_INVALID_ARG, "unknown io dtype");
-    if ((long long)B * T > (1LL << 30)) return fail(KDA_ERR_UNSUPPORTED, "too many tokens");
-    if (D > (1 << 20)) return fail(KDA_ERR_UNSUPPORTED, "more than 2^20 channels");
-    if (cu) {
-        if (B != 1) return fail(KDA_ERR_INVALID_ARG, "packed sequences need B == 1");
-        if (N < 1) return fail(KDA_ERR_INVALID_ARG, "packed sequences need N >= 1");
-    }
-    ax = {cu, cu ? N : B, B, T};
-    return KDA_OK;
-}
+using namespace kda::api;
 
 // ------------------------------------------------------------------ convolution
 kda_status conv_args(const kda_conv_problem* p, kda::ConvArgs& a) {
@@ -179,17 +138,6 @@ SsmLayout ssm_layout(const kda::SsmArgs& a, bool backward, int save) {
     L.pbc = up(sizeof(float) * kda::ssm_bwd_tiles(a.D, a.G, a.S) * tokens * 2 * a.S);
     return L;
 }
-
-struct Carver {
-    char* p;
-    size_t used = 0;
-    template <class T>
-    T* take(size_t bytes) {
-        T* r = reinterpret_cast<T*>(p + used);
-        used += bytes;
-        return bytes ? r : nullptr;
-    }
-};
 
 // ------------------------------------------------------------------ norm
 kda_status norm_args(const kda_norm_problem* p, kda::NormArgs& a) {

@@ -1,0 +1,69 @@
+// Linear attention with a decay for each head: what its kernels share. One recurrence serves the forward and the
+// three gradients (include/kda.h has the operator):
+//     forwards in time    S <- a S + w k v^T,  o = s q S       (o: (q, k, v);  dq: (do, v, k), the state transposed)
+//     backwards in time   R <- R + w k v^T,  o = s q R,  R <- a R    (dv: (k, q, do);  dk: (v, do, q), transposed)
+// with a = exp(decay of the head). A LinCall is one of them; its q, k, v are the roles, not the caller's tensors.
+// "Mirrored" tokens: a call that runs backwards counts its tokens, and its windows, from the row's end.
+#pragma once
+
+#include "kda_layer.cuh"
+
+namespace kda {
+
+struct LinCall {
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv;     // elements between tokens
+    int gq, gk, gv;            // value heads to a head of each
+    int K, V;                  // widths of q, k and of v, o
+    void* o;                   // [tokens][HV][V]
+    int o_f32;                 // fp32 instead of the I/O type (partial sums of shared heads)
+    const float* s0;           // [N][HV] states or NULL
+    float* s1;                 // final states or NULL (natural order only)
+    int transposed;            // s0 is [V][K]
+    int back;
+    float s, w;                // the formulas' s and w
+    float* local;              // [windows][HV][K][V]: end states of the windows' own tokens
+};
+
+struct LinArgs {
+    TokenAxis ax;
+    int HV;
+    const float* decay;        // [HV] or NULL
+    int units_row, unit_len;   // windows per row and their tokens
+    int32_t* err;
+    int calls;
+    LinCall c[3];
+};
+
+// The sequence that holds mirrored token t of the row, in mirrored tokens.
+__device__ __forceinline__ Seq lin_seq(const TokenAxis& ax, int row, int t, int back) {
+    if (!back) return seq_at(ax, row, t);
+    const Seq s = seq_at(ax, row, ax.len - 1 - t);
+    return {s.n, ax.len - s.end, ax.len - s.first};
+}
+
+// a^m = exp(g m): the product's rounding goes on as its low part, so that the power is within expf's two units.
+__device__ __forceinline__ float lin_power(float g, int m) {
+    if (m == 0) return 1.f;
+    const float x = g * (float)m, low = fmaf(g, (float)m, -x);
+    const float e = expf(x);
+    return e > 0.f && e < 3e38f ? fmaf(e, low, e) : e;
+}
+// The same as a sum of two fp32 values, to 2^-48: a state meets this factor once per step, and its error would grow
+// with the tokens that the state remembers.
+__device__ __forceinline__ float2 lin_power2(float g, int m) {
+    if (m == 0) return make_float2(1.f, 0.f);
+    const double e = exp((double)g * m);
+    const float hi = (float)e;
+    return make_float2(hi, isfinite(hi) ? (float)(e - hi) : 0.f);
+}
+
+constexpr int LIN_MAX_W = 256;    // widest key or value
+
+// Time windows of the kernels on CUDA cores, and whether a call may run on the tensor cores.
+int lin_units(int rows, int len, int ctas);
+cudaError_t launch_lin(const LinArgs& a, int bf16, cudaStream_t st);
+// out[t][h][:] = sum over the group's value heads of part[t][h * group + i][:], in order.
+cudaError_t launch_lin_heads(const float* part, void* out, int64_t rows, int group, int width, int bf16, cudaStream_t st);
+
+}  // namespace kda

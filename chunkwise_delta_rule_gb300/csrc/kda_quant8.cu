@@ -1,0 +1,199 @@
+// Rounding to e4m3 with a scale for each group of 128 (include/kda.h): per group m = max |x|, scale = m / 448,
+// q = e4m3(x 448 / m), to nearest even.
+// A CTA takes a tile of 128 x 128 values and reads it once into registers: a thread has 8 neighbouring columns of 8
+// neighbouring rows, so that a row's maximum is an exchange of 16 lanes, a column's one of a thread's own rows, a
+// lane and eight warps, a row of q leaves in 8-byte pieces, and a column's 8 values are one 8-byte piece of qt. Those
+// pieces turn in shared memory, piece p of column c at place p ^ (c / 8), which spreads both sides over all banks.
+// Bound by HBM.
+#include "kda_fp8.cuh"
+
+namespace kda {
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr int NT = 256, TILE = FP8_GROUP, PER = 8;
+
+// The larger of a and |b|; a NaN stays.
+__device__ __forceinline__ float amax(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
+}
+// What a group's values are multiplied by, in two factors: 448 / m may overflow, or m be above the range in which its
+// quotient is normal; such a group is brought to the middle of the range first.
+struct Factor {
+    float by, inv;
+};
+__device__ __forceinline__ Factor factor(float m) {
+    const float by = m >= 1e-30f && m <= 1e30f ? 1.f : m < 1.f ? 0x1p64f : 0x1p-64f;
+    const float v = m * by;
+    return {by, v > 0.f ? FP8_MAX / v : v};   // 0 and NaN as they are
+}
+__device__ __forceinline__ uint32_t pack4(const float (&v)[4]) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+}
+
+// ROWS: q is wanted, COLS: qt.
+template <typename TI, bool BLOCKS, bool ROWS, bool COLS>
+__global__ void __launch_bounds__(NT, 2) k_quant8(Quant8Args a, int vecx, int vecq, int vect) {
+    __shared__ __align__(16) uint2 turn[COLS ? TILE : 1][COLS ? TILE / PER : 1];
+    __shared__ float cmax[COLS && !BLOCKS ? NT / 32 : 1][COLS && !BLOCKS ? TILE : 1];
+    __shared__ float bmax[NT / 32];
+    const int lx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r0 = blockIdx.y * TILE + ty * PER, c0 = blockIdx.x * TILE + lx * PER;   // this thread's values
+    const int gd = (a.D + TILE - 1) / TILE, gr = (a.rows + TILE - 1) / TILE;
+    const int cols = min(max(a.D - c0, 0), PER);
+    Raw<TI, PER> raw[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const TI* p = static_cast<const TI*>(a.x) + (int64_t)(r0 + i) * a.ldx + c0;
+        if (r0 + i < a.rows && cols == PER && vecx) {
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(raw[0]) / 16; ++j)
+                reinterpret_cast<uint4*>(&raw[i])[j] = reinterpret_cast<const uint4*>(p)[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) raw[i].v[j] = r0 + i < a.rows && j < cols ? p[j] : TI(0.f);
+        }
+    }
+    float rm[PER], cm[PER];   // maxima of the rows and of the columns
+#pragma unroll
+    for (int j = 0; j < PER; ++j) cm[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        float v[PER];
+        unpack<PER>(raw[i], v);
+        rm[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            if (BLOCKS || ROWS) rm[i] = amax(rm[i], v[j]);
+            if (COLS && !BLOCKS) cm[j] = amax(cm[j], v[j]);
+        }
+    }
+    if (BLOCKS) {
+        float m = rm[0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) m = amax(m, rm[i]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = amax(m, __shfl_xor_sync(FULL, m, o));
+        if (lane == 0) bmax[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) m = amax(m, bmax[w]);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) rm[i] = cm[i] = m;
+        if (threadIdx.x == 0) {
+            if (ROWS) a.scale[(size_t)blockIdx.y * gd + blockIdx.x] = m / FP8_MAX;
+            if (COLS) a.scale_t[(size_t)blockIdx.x * gr + blockIdx.y] = m / FP8_MAX;
+        }
+    } else {
+        if (ROWS) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+#pragma unroll
+                for (int o = 8; o; o >>= 1) rm[i] = amax(rm[i], __shfl_xor_sync(FULL, rm[i], o));
+                if (lx == 0 && r0 + i < a.rows) a.scale[(size_t)(r0 + i) * gd + blockIdx.x] = rm[i] / FP8_MAX;
+            }
+        }
+        if (COLS) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                cm[j] = amax(cm[j], __shfl_xor_sync(FULL, cm[j], 16));
+                if (lane < 16) cmax[warp][lx * PER + j] = cm[j];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                cm[j] = cmax[0][lx * PER + j];
+#pragma unroll
+                for (int w = 1; w < NT / 32; ++w) cm[j] = amax(cm[j], cmax[w][lx * PER + j]);
+                if (ty == 0 && j < cols) a.scale_t[(size_t)(c0 + j) * gr + blockIdx.y] = cm[j] / FP8_MAX;
+            }
+        }
+    }
+    if (ROWS) {
+        Factor f = factor(rm[0]);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (!BLOCKS && i) f = factor(rm[i]);
+            float v[PER];
+            unpack<PER>(raw[i], v);
+            uint32_t w[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) x[z] = v[4 * j + z] * f.by * f.inv;
+                w[j] = pack4(x);
+            }
+            if (r0 + i >= a.rows) continue;
+            uint8_t* q = a.q + (int64_t)(r0 + i) * a.ldq + c0;
+            if (cols == PER && vecq) {
+                *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (j < cols) q[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+            }
+        }
+    }
+    if (COLS) {
+        Factor f = factor(cm[0]);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            if (!BLOCKS && j) f = factor(cm[j]);
+            uint32_t w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    float v[PER];
+                    unpack<PER>(raw[4 * i + z], v);
+                    x[z] = v[j] * f.by * f.inv;
+                }
+                w[i] = pack4(x);
+            }
+            turn[lx * PER + j][ty ^ lx] = make_uint2(w[0], w[1]);
+        }
+        __syncthreads();
+        const int p = threadIdx.x & 15;   // piece: rows 8 p .. 8 p + 7 of the tile
+        const int rt = blockIdx.y * TILE + p * PER, n = min(max(a.rows - rt, 0), PER);
+#pragma unroll
+        for (int k = 0; k < TILE / 16; ++k) {
+            const int c = k * 16 + (threadIdx.x >> 4), col = blockIdx.x * TILE + c;
+            if (col >= a.D) break;
+            const uint2 w = turn[c][p ^ (c >> 3)];
+            uint8_t* q = a.qt + (int64_t)col * a.ldqt + rt;
+            if (n == PER && vect) {
+                *reinterpret_cast<uint2*>(q) = w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (i < n) q[i] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+            }
+        }
+    }
+}
+
+template <typename TI, bool BLOCKS>
+void run(const Quant8Args& a, cudaStream_t st) {
+    const auto on = [](const void* p, int64_t ld, int n) { return (reinterpret_cast<uintptr_t>(p) % n == 0 && ld % n == 0) ? 1 : 0; };
+    const int vecx = on(a.x, a.ldx * (int64_t)sizeof(TI), 16), vecq = on(a.q, a.ldq, 8), vect = on(a.qt, a.ldqt, 8);
+    const dim3 grid((a.D + TILE - 1) / TILE, (unsigned)(((int64_t)a.rows + TILE - 1) / TILE));
+    if (a.q && a.qt) k_quant8<TI, BLOCKS, true, true><<<grid, NT, 0, st>>>(a, vecx, vecq, vect);
+    else if (a.q) k_quant8<TI, BLOCKS, true, false><<<grid, NT, 0, st>>>(a, vecx, vecq, vect);
+    else k_quant8<TI, BLOCKS, false, true><<<grid, NT, 0, st>>>(a, vecx, vecq, vect);
+}
+
+}  // namespace
+
+cudaError_t launch_quant8(const Quant8Args& a, int bf16, cudaStream_t st) {
+    return traced_launch("k_quant8", st, [&] {
+        if (bf16) a.blocks ? run<__nv_bfloat16, true>(a, st) : run<__nv_bfloat16, false>(a, st);
+        else a.blocks ? run<float, true>(a, st) : run<float, false>(a, st);
+    });
+}
+
+}  // namespace kda

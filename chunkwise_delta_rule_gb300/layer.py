@@ -1,6 +1,7 @@
 """PyTorch-facing binding of the layer operators around the delta rule (same
 names as include/kda.h): the short causal convolution, the selective state space
-scan and the root-mean-square norm.
+scan, linear attention with a decay for each head, the root-mean-square norm, and
+products in 8 bits.
 
 As in ``ops``: PyTorch provides device memory and the current stream, every step
 runs in libkda.so's CUDA kernels. Token tensors are [B, T, ...]; inputs may be
@@ -156,6 +157,95 @@ def kda_norm_bwd(p: "_binding.NormProblem", dy: torch.Tensor, dres: Optional[tor
     return _binding.norm_bwd(p, dy, dres, workspace, stream)
 
 
+# ------------------------------------------------------------------ linear attention
+
+class LinGrads(NamedTuple):
+    """Gradients of a linear attention call; dh0 is None where it was not asked for."""
+
+    dq: torch.Tensor
+    dk: torch.Tensor
+    dv: torch.Tensor
+    dh0: Optional[torch.Tensor]
+
+
+def make_lin_problem(q, k, v, decay: Optional[torch.Tensor] = None, *, scale: Optional[float] = None,
+                     initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None) -> "_binding.LinProblem":
+    """Describe one call of linear attention: q and k [B, T, H, K], v [B, T, HV, V]
+    in one type (bf16 or fp32; HV a multiple of H, value head j reading key head
+    j // (HV // H); widths up to 256), ``decay`` [HV] fp32, the natural logarithm
+    of each head's factor per token, or None for no decay, ``scale`` of the
+    queries (K ** -0.5 by default), ``initial_state`` [N, HV, K, V] fp32 or None."""
+    return _binding.LinProblem(q, k, v, decay, scale, initial_state, cu_seqlens)
+
+
+def kda_lin_workspace_size(p: "_binding.LinProblem", for_backward: bool) -> int:
+    return _binding.lin_workspace_size(p, for_backward)
+
+
+def kda_lin_fwd(p: "_binding.LinProblem", *, output_final_state: bool = True, ht: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None):
+    """Returns (o [B, T, HV, V], final states [N, HV, K, V] fp32 or None). ``ht`` may
+    be given, for example the initial state itself to update it in place; ``err``
+    is an optional int32 device word (bit 0: inconsistent cu_seqlens, bit 1: a
+    bounded wait inside the kernel gave up)."""
+    return _binding.lin_fwd(p, output_final_state, ht, workspace, err, stream)
+
+
+def kda_lin_bwd(p: "_binding.LinProblem", do: torch.Tensor, dht: Optional[torch.Tensor] = None, *,
+                workspace: Optional[torch.Tensor] = None, stream=None, need_dh0: Optional[bool] = None,
+                err: Optional[torch.Tensor] = None) -> LinGrads:
+    """Backward of <do, o> + <dht, final states> (the decay has no gradient); dh0
+    comes with an initial state, or as ``need_dh0`` says; ``err`` as in the
+    forward."""
+    return LinGrads(*_binding.lin_bwd(p, do, dht, workspace, stream, need_dh0, err))
+
+
+# ------------------------------------------------------------------ 8 bits
+
+class Quant8(NamedTuple):
+    """8-bit values and scales; None where they were not asked for."""
+
+    q: Optional[torch.Tensor]
+    scale: Optional[torch.Tensor]
+    qt: Optional[torch.Tensor]
+    scale_t: Optional[torch.Tensor]
+
+
+def make_quant8_problem(x, *, blocks: bool = False, rows: bool = True, transposed: bool = False) -> "_binding.Quant8Problem":
+    """Describe one rounding of x [..., D] (bf16 or fp32) to e4m3: with ``rows`` in
+    its own order, q [..., D] with a scale for each row and 128 columns (with
+    ``blocks`` for each 128 rows and 128 columns); with ``transposed`` (also) as
+    qt [D, R] over the R rows of all leading axes, with a scale for each 128 of
+    them (with ``blocks`` the same values and scales)."""
+    return _binding.Quant8Problem(x, blocks, rows, transposed)
+
+
+def kda_quant8(p: "_binding.Quant8Problem", *, stream=None) -> Quant8:
+    """Returns (q, scale, qt, scale_t). Rows of q and qt start every 16 bytes: they
+    are views of wider rows where their width is no multiple of 16."""
+    return Quant8(*_binding.quant8(p, stream))
+
+
+def make_mm8_problem(a, scale_a, b, scale_b, *, out: str = "bf16") -> "_binding.Mm8Problem":
+    """Describe the product a b^T of e4m3 values with scales: a [..., K] and scale_a
+    [..., ceil(K / 128)] as ``kda_norm_fwd`` (out "e4m3", group 128) or
+    ``kda_quant8`` give them, b [N, K] with scale_b [ceil(N / 128), ceil(K / 128)]
+    (blocks) or [N, ceil(K / 128)] (rows), all scales fp32; ``out`` "bf16" or
+    "fp32"."""
+    return _binding.Mm8Problem(a, scale_a, b, scale_b, out)
+
+
+def kda_mm8_workspace_size(p: "_binding.Mm8Problem") -> int:
+    return _binding.mm8_workspace_size(p)
+
+
+def kda_mm8(p: "_binding.Mm8Problem", *, y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+            err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Returns y [..., N]; ``err`` is an optional int32 device word (bit 1: a bounded
+    wait inside the kernel gave up)."""
+    return _binding.mm8(p, y, workspace, err, stream)
+
+
 # ------------------------------------------------------------------ autograd
 
 def _grad(t: Optional[torch.Tensor], shape=None, like: Optional[torch.Tensor] = None):
@@ -251,3 +341,73 @@ def rms_norm(x, weight, *, residual: Optional[torch.Tensor] = None, eps: float =
     """Differentiable root-mean-square norm of x + residual. Returns (y, the sum):
     the sum is the residual stream that goes on."""
     return RmsNormFunction.apply(x, weight, residual, eps)
+
+
+class LinearAttentionFunction(torch.autograd.Function):
+    """Autograd wrapper: forward and backward both run the CUDA library."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, decay, scale, initial_state, cu_seqlens, err):
+        p = make_lin_problem(q, k, v, decay, scale=scale, initial_state=initial_state, cu_seqlens=cu_seqlens)
+        o, ht = kda_lin_fwd(p, err=err)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(q, k, v, decay, initial_state, cu_seqlens)
+        ctx.meta = (scale, err)
+        return o, ht
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do, dht):
+        q, k, v, decay, h0, cu = ctx.saved_tensors
+        if ctx.needs_input_grad[3]:
+            raise RuntimeError("the decay has no gradient: it is a constant of the layer")
+        p = make_lin_problem(q, k, v, decay, scale=ctx.meta[0], initial_state=h0, cu_seqlens=cu)
+        g = kda_lin_bwd(p, _grad(do, v.shape, v), _grad(dht), err=ctx.meta[1])
+        return g.dq, g.dk, g.dv, None, None, g.dh0, None, None
+
+
+def linear_attention(q, k, v, decay: Optional[torch.Tensor] = None, *, scale: Optional[float] = None,
+                     initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                     err: Optional[torch.Tensor] = None):
+    """Differentiable linear attention with a decay for each head (a constant).
+    Returns (o, final_state). ``err`` as in ``kda_lin_fwd``; its backward sets it
+    too."""
+    return LinearAttentionFunction.apply(q, k, v, decay, scale, initial_state, cu_seqlens, err)
+
+
+class Linear8Function(torch.autograd.Function):
+    """Autograd wrapper: the three products run in 8 bits."""
+
+    @staticmethod
+    def forward(ctx, x, weight, err):
+        out = "bf16" if x.dtype == torch.bfloat16 else "fp32"
+        a = kda_quant8(make_quant8_problem(x, transposed=ctx.needs_input_grad[1]))
+        w = kda_quant8(make_quant8_problem(weight, blocks=True, transposed=ctx.needs_input_grad[0]))
+        y = kda_mm8(make_mm8_problem(a.q, a.scale, w.q, w.scale, out=out), err=err)
+        ctx.save_for_backward(a.qt, a.scale_t, w.qt, w.scale_t)
+        ctx.meta = (out, weight.dtype, err)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        xt, xt_scale, wt, wt_scale = ctx.saved_tensors
+        out, wtype, err = ctx.meta
+        need_x, need_w = ctx.needs_input_grad[:2]
+        d = kda_quant8(make_quant8_problem(dy.contiguous(), rows=need_x, transposed=need_w))
+        dx = kda_mm8(make_mm8_problem(d.q, d.scale, wt, wt_scale, out=out), err=err) if need_x else None
+        dw = None
+        if need_w:
+            wout = "bf16" if wtype == torch.bfloat16 else "fp32"
+            dw = kda_mm8(make_mm8_problem(d.qt, d.scale_t, xt, xt_scale, out=wout), err=err)
+        return dx, dw, None
+
+
+def linear8(x, weight, *, err: Optional[torch.Tensor] = None):
+    """Differentiable product x weight^T in 8 bits: x [..., K] and weight [N, K]
+    (bf16 or fp32) are rounded to e4m3, x by rows and groups of 128 columns, weight
+    by blocks of 128 x 128; the backward rounds the output's gradient by rows for
+    x's gradient and by groups of 128 tokens, as x, for the weight's. The roundings
+    pass their gradients through. y and dx come in x's type, the weight's gradient
+    in its own. ``err`` as in ``kda_mm8``."""
+    return Linear8Function.apply(x, weight, err)

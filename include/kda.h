@@ -385,6 +385,89 @@ size_t kda_norm_workspace_size(const kda_norm_problem *p);
 kda_status kda_norm_bwd(const kda_norm_problem *p, const void *dy, const void *dres, void *dx, float *dweight,
                         void *ws, size_t ws_bytes, kda_stream_t stream);
 
+/* Linear attention with a decay for each head, per sequence and value head j
+ * with a = exp(decay[j]) (a = 1 without decay):
+ *     S_t = a S_{t-1} + k_t v_t^T,   o_t = S_t^T (scale q_t)
+ * HV = G * H value heads (0: H) share H heads of queries and keys, value head j
+ * reading head j / G; S_0 = h0 or zero. Any real decay is taken (-infinity: a
+ * state that holds its own token alone); a positive one grows the state. */
+typedef struct {
+    int B, T, H, K, V;          /* batch, tokens per sequence (total when packed), heads, key and value width (1..256) */
+    int N;                      /* packed sequences (used only when cu_seqlens != NULL; then B == 1) */
+    const int32_t *cu_seqlens;  /* device, N+1 offsets, or NULL */
+    kda_dtype io;               /* type of q, k, v, o and their gradients */
+    int HV;                     /* value heads (0: H) */
+    float scale;                /* <= 0 selects K^-1/2 */
+    int64_t ldq, ldk, ldv;      /* elements between tokens (0: contiguous) */
+    const void *q, *k;          /* [B*T, H, K] */
+    const void *v;              /* [B*T, HV, V] */
+    const float *decay;         /* [HV] fp32 natural-log decay per token, or NULL */
+    const float *h0;            /* [N, HV, K, V] fp32 or NULL */
+} kda_lin_problem;
+
+/* Bytes of workspace of kda_lin_fwd (for_backward = 0) or kda_lin_bwd (1);
+ * 256-byte aligned, no initialisation. 0 where none is needed or the problem is
+ * invalid. */
+size_t kda_lin_workspace_size(const kda_lin_problem *p, int for_backward);
+
+/* Writes o [B*T, HV, V] and, if not NULL, the final states ht [N, HV, K, V]
+ * fp32, which may be the same buffer as h0 (decoding in place). bf16 rows that
+ * are whole 16-byte accesses (K and V multiples of 8, K <= 128, leading
+ * dimensions too) run on the tensor cores unless the sequences are short; there
+ * the states are fp32 sums of exact products and one copy of them in bf16 is
+ * what a chunk's queries meet. Bit 1 of *err is set where a bounded wait inside
+ * the kernel gave up; the results are then unspecified. */
+kda_status kda_lin_fwd(const kda_lin_problem *p, void *o, float *ht, void *ws, size_t ws_bytes, int32_t *err,
+                       kda_stream_t stream);
+
+/* Gradients of <dout, o> + <dht, ht>: dout [B*T, HV, V], dht [N, HV, K, V] fp32
+ * or NULL; writes dq, dk [B*T, H, K], dv [B*T, HV, V] and, if not NULL, dh0
+ * [N, HV, K, V] fp32 (a buffer of its own). The decay has no gradient. The sums
+ * over a key head's value heads are formed in order: repeated calls agree
+ * bitwise. */
+kda_status kda_lin_bwd(const kda_lin_problem *p, const void *dout, const float *dht, void *dq, void *dk, void *dv,
+                       float *dh0, void *ws, size_t ws_bytes, int32_t *err, kda_stream_t stream);
+
+/* Rounding to e4m3 with a scale for each group of 128 columns (or block of 128 x
+ * 128): scale = max |x| / 448 over the group, x ~ scale * e4m3, as kda_norm_fwd
+ * writes its 8-bit rows; a group of zeros has scale 0, and one that holds a NaN
+ * or an infinity has a NaN or infinite scale. */
+typedef struct {
+    int rows, D;                /* rows up to 2^22, D up to 2^20 */
+    kda_dtype io;               /* type of x */
+    int blocks;                 /* 0: a scale per row and 128 columns; 1: per 128 rows and 128 columns */
+    int64_t ldx;                /* elements between rows of x (0: D) */
+    int64_t ldq, ldqt;          /* bytes between rows of q (0: D) and of qt (0: rows) */
+    const void *x;              /* [rows, D] */
+} kda_quant8_problem;
+
+/* Writes, where not NULL, q [rows, D] with scale [rows or ceil(rows / 128),
+ * ceil(D / 128)], and the transposed copy qt [D, rows] with scale_t: rounded in
+ * groups of 128 rows of x ([D, ceil(rows / 128)]), or with blocks the same
+ * values and scales transposed. q comes with scale, qt with scale_t. */
+kda_status kda_quant8(const kda_quant8_problem *p, void *q, float *scale, void *qt, float *scale_t, kda_stream_t stream);
+
+/* Matrix product of e4m3 values with a scale for each 128 columns,
+ *     y[m, n] = sum_g scale_a[m, g] scale_b[n, g] sum_{c in group g} a[m, c] b[n, c],
+ * group sums and their scaled sum in fp32, one rounding to y's type. */
+typedef struct {
+    int M, N, K;                /* up to 2^22, 2^20, 2^20 */
+    int out;                    /* kda_dtype of y */
+    int b_rows;                 /* 0: scale_b per 128 rows of b; 1: per row */
+    int64_t lda, ldb;           /* bytes between rows (0: K) */
+    const void *a, *b;          /* [M, K], [N, K] e4m3 */
+    const float *scale_a;       /* [M, ceil(K / 128)] fp32 */
+    const float *scale_b;       /* [ceil(N / 128) or N, ceil(K / 128)] fp32 */
+} kda_mm8_problem;
+
+/* Bytes of workspace kda_mm8 needs (256-byte aligned; 0 where none is needed or
+ * the problem is invalid). */
+size_t kda_mm8_workspace_size(const kda_mm8_problem *p);
+
+/* Writes y [M, N]. Bit 1 of *err (NULL or a device int32 word) is set where a
+ * bounded wait inside the kernel gave up; the results are then unspecified. */
+kda_status kda_mm8(const kda_mm8_problem *p, void *y, void *ws, size_t ws_bytes, int32_t *err, kda_stream_t stream);
+
 /* Message for the last non-OK status returned on the calling thread
  * (thread-local; "" if none). */
 const char *kda_last_error(void);

@@ -1,5 +1,6 @@
 """FP64 oracle of the layer operators: short causal convolution, selective state
-space scan, root-mean-square norm; forward and hand-derived backward.
+space scan, linear attention, root-mean-square norm (forward and hand-derived
+backward), and the rounding to 8 bits with its product.
 
 TEST INFRASTRUCTURE ONLY (see the package docstring). Plain loops over the
 sequences and tokens, vectorised over channels; packed token axis [tokens, ...]
@@ -9,6 +10,7 @@ finite differences and closed forms.
     conv:  s_t = bias + sum_j w[:, j] x_{t-W+1+j},  y = s or s sigmoid(s)
     scan:  delta = softplus(dt + dt_bias),  a = exp(-delta exp(A_log))
            h_t = a h_{t-1} + delta x_t b_t,  y = (c_t . h_t + d_skip x_t) silu(z_t)
+    lin:   S_t = a S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t
     norm:  h = x + residual,  y = h (mean h^2 + eps)^(-1/2) w
 """
 
@@ -127,3 +129,68 @@ def norm(x, w, residual, eps, dy=None, dres=None):
         out["dx"] = r * (v - u * np.mean(u * v, axis=1, keepdims=True)) + (0.0 if dres is None else dres)
         out["dweight"] = np.sum(dy * u, axis=0)
     return out
+
+
+def lin(q, k, v, decay, scale, h0, starts, do=None, dht=None):
+    """q, k [tokens, H, K]; v [tokens, HV, V]; decay [HV] or None; h0 [N, HV, K, V] or
+    None. Returns a dict with o, ht and, given do, dq, dk, dv and dh0."""
+    T, HV, V = v.shape
+    H, K = q.shape[1:]
+    N, G = len(starts) - 1, HV // H
+    a = np.ones(HV) if decay is None else np.exp(decay)
+    h0 = np.zeros((N, HV, K, V)) if h0 is None else h0
+    out = dict(o=np.zeros_like(v), ht=np.zeros_like(h0))
+    if do is not None:
+        out.update(dq=np.zeros_like(q), dk=np.zeros_like(k), dv=np.zeros_like(v), dh0=np.zeros_like(h0))
+    for n in range(N):
+        lo, hi = starts[n], starts[n + 1]
+        for j in range(HV):
+            h, S, hs = j // G, h0[n, j].copy(), []
+            for t in range(lo, hi):
+                S = (a[j] * S if a[j] else 0.0) + np.outer(k[t, h], v[t, j])
+                hs.append(S)
+                out["o"][t, j] = scale * (q[t, h] @ S)
+            out["ht"][n, j] = S
+            if do is None:
+                continue
+            R = np.zeros((K, V)) if dht is None else dht[n, j].copy()
+            for t in range(hi - 1, lo - 1, -1):
+                R = R + scale * np.outer(q[t, h], do[t, j])
+                out["dq"][t, h] += scale * (hs[t - lo] @ do[t, j])
+                out["dk"][t, h] += R @ v[t, j]
+                out["dv"][t, j] = k[t, h] @ R
+                R = a[j] * R if a[j] else np.zeros_like(R)
+            out["dh0"][n, j] = R
+    return out
+
+
+def e4m3_values():
+    """Every finite value of the format, sorted: 4 bits of exponent (bias 7), 3 of fraction."""
+    e, m = np.divmod(np.arange(0x7f), 8)
+    pos = np.where(e == 0, m * 2.0 ** -9, (1 + m / 8) * 2.0 ** (e - 7.0))
+    return np.concatenate([-pos[:0:-1], pos])
+
+
+def quant8(x, rows):
+    """x [R, D]: the nearest e4m3 value of each x / scale (ties not decided) and the scales of groups of `rows` rows
+    and 128 columns."""
+    R, D = x.shape
+    gr, gd = -(-R // rows), -(-D // 128)
+    scale = np.zeros((gr, gd))
+    for i in range(gr):
+        for j in range(gd):
+            scale[i, j] = np.max(np.abs(x[i * rows:(i + 1) * rows, j * 128:(j + 1) * 128])) / 448
+    each = np.repeat(np.repeat(scale, rows, 0)[:R], 128, 1)[:, :D]
+    y = np.divide(x, each, out=np.zeros_like(x), where=each > 0)
+    grid = e4m3_values()
+    at = np.clip(np.searchsorted(grid, y), 1, len(grid) - 1)
+    q = np.where(y - grid[at - 1] <= grid[at] - y, grid[at - 1], grid[at])
+    return q, scale, y
+
+
+def mm8(a, sa, b, sb):
+    """a [M, K], sa [M, G]; b [N, K], sb [N or ceil(N / 128), G]: the product of the scaled values."""
+    K, N = a.shape[1], b.shape[0]
+    if sb.shape[0] != N:
+        sb = np.repeat(sb, 128, 0)[:N]
+    return (a * np.repeat(sa, 128, 1)[:, :K]) @ (b * np.repeat(sb, 128, 1)[:, :K]).T

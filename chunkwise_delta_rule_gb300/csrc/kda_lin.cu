@@ -276,10 +276,10 @@ __global__ void __launch_bounds__(256) k_lin_heads(const float* part, TI* out, i
 
 }  // namespace
 
-// Windows per row: as many as keep `ctas` per window below two CTAs on each of 152 SMs, of 64 tokens at least.
+// Windows per row: as many as keep `ctas` per window below two CTAs on each SM, of 64 tokens at least.
 int lin_units(int rows, int len, int ctas) {
     const long long all = (long long)rows * ctas;
-    int n = (int)(304 / (all > 0 ? all : 1));
+    int n = (int)(2LL * sm_count() / (all > 0 ? all : 1));
     if (n > len / 64) n = len / 64;
     return n > 1 ? n : 1;
 }

@@ -60,9 +60,15 @@ __device__ __forceinline__ float2 lin_power2(float g, int m) {
 
 constexpr int LIN_MAX_W = 256;    // widest key or value
 
-// Time windows of the kernels on CUDA cores, and whether a call may run on the tensor cores.
+// Time windows of the kernel on CUDA cores.
 int lin_units(int rows, int len, int ctas);
 cudaError_t launch_lin(const LinArgs& a, int bf16, cudaStream_t st);
+// The tensor cores' kernel: from this many tokens per sequence on; the tokens of its time windows where a window is
+// `ctas` CTAs; whether a bf16 call's widths and rows fit it.
+constexpr int LIN_TC_TOKENS = 32;
+int lin_tc_window(int rows, int len, int ctas);
+bool lin_tc_call(const LinCall& c);
+cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st);
 // out[t][h][:] = sum over the group's value heads of part[t][h * group + i][:], in order.
 cudaError_t launch_lin_heads(const float* part, void* out, int64_t rows, int group, int width, int bf16, cudaStream_t st);
 

@@ -41,11 +41,21 @@ kda_status lin_args(const kda_lin_problem* p, Lin& l) {
 }
 
 size_t state_bytes(const Lin& l, size_t n) { return up(sizeof(float) * n * l.a.HV * l.K * l.V); }
-void set_windows(Lin& l, bool backward) {
-    const int slices = (l.V + 127) / 128;
-    const int units = kda::lin_units(l.a.ax.rows, l.a.ax.len, l.a.HV * slices * (backward ? 3 : 1));
-    int len = (l.a.ax.len + units - 1) / units;
-    len = (len + 63) / 64 * 64;
+// Whether sizes alone let a call run on the tensor cores (its rows' alignment has to, too).
+bool tc_sizes(const Lin& l, bool backward) {
+    if (!l.bf16 || l.K % 8 || l.V % 8 || l.K > 128 || (backward && l.V > 128)) return false;
+    return (int64_t)l.a.ax.rows * l.a.ax.len >= (int64_t)kda::LIN_TC_TOKENS * l.a.ax.N;
+}
+void set_windows(Lin& l, bool backward, bool tc) {
+    const int heads = l.a.HV * (backward ? 3 : 1);
+    int len;
+    if (tc) {
+        const int blocks = (l.V + 63) / 64, kblocks = (l.K + 63) / 64;
+        len = kda::lin_tc_window(l.a.ax.rows, l.a.ax.len, backward ? l.a.HV * (blocks + 2 * kblocks) : l.a.HV * blocks);
+    } else {
+        const int units = kda::lin_units(l.a.ax.rows, l.a.ax.len, heads * ((l.V + 127) / 128));
+        len = ((l.a.ax.len + units - 1) / units + 63) / 64 * 64;
+    }
     l.a.unit_len = len > 0 ? len : 64;
     l.a.units_row = l.a.ax.len > 0 ? (l.a.ax.len + l.a.unit_len - 1) / l.a.unit_len : 1;
 }
@@ -62,6 +72,17 @@ Layout layout(const Lin& l, bool backward) {
     if (backward && l.a.HV != l.H) y.dq = y.dk = up(sizeof(float) * (size_t)l.a.ax.rows * l.a.ax.len * l.a.HV * l.K);
     return y;
 }
+// The larger of the two paths' workspaces: which one runs goes by the pointers' alignment, too.
+size_t most_bytes(Lin l, bool backward) {
+    size_t most = 0;
+    for (int tc = 0; tc < 2; ++tc) {
+        if (tc && !tc_sizes(l, backward)) continue;
+        set_windows(l, backward, tc);
+        const size_t b = layout(l, backward).all(backward);
+        most = b > most ? b : most;
+    }
+    return most;
+}
 
 }  // namespace
 
@@ -70,8 +91,7 @@ extern "C" {
 size_t kda_lin_workspace_size(const kda_lin_problem* p, int for_backward) {
     Lin l;
     if (lin_args(p, l) != KDA_OK) return 0;
-    set_windows(l, for_backward != 0);
-    return layout(l, for_backward != 0).all(for_backward != 0);
+    return most_bytes(l, for_backward != 0);
 }
 
 kda_status kda_lin_fwd(const kda_lin_problem* p, void* o, float* ht, void* ws, size_t ws_bytes, int32_t* err,
@@ -80,9 +100,7 @@ kda_status kda_lin_fwd(const kda_lin_problem* p, void* o, float* ht, void* ws, s
     kda_status st = lin_args(p, l);
     if (st != KDA_OK) return st;
     if (l.a.ax.len > 0 && (!p->q || !p->k || !p->v || !o)) return fail(KDA_ERR_INVALID_ARG, "q, k, v and o must be non-NULL");
-    set_windows(l, false);
-    const Layout y = layout(l, false);
-    if ((st = check_ws(ws, ws_bytes, y.all(false), "workspace")) != KDA_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, most_bytes(l, false), "workspace")) != KDA_OK) return st;
     Carver cw{static_cast<char*>(ws)};
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const int G = l.a.HV / l.H;
@@ -90,10 +108,13 @@ kda_status kda_lin_fwd(const kda_lin_problem* p, void* o, float* ht, void* ws, s
     l.a.calls = 1;
     kda::LinCall& c = l.a.c[0];
     c = {p->q, p->k, p->v, l.ldq, l.ldk, l.ldv, G, G, 1, l.K, l.V, o, 0, p->h0, ht, 0, 0, l.scale, 1.f, nullptr};
+    const bool tc = tc_sizes(l, false) && kda::lin_tc_call(c);
+    set_windows(l, false, tc);
+    const Layout y = layout(l, false);
     c.local = cw.take<float>(y.local);
     // the last window of a sequence would overwrite the state that its other windows read
     if (y.alias && ht && ht == p->h0) c.s1 = cw.take<float>(y.alias);
-    if ((st = cuda_result(kda::launch_lin(l.a, l.bf16, cs), "linear attention")) != KDA_OK) return st;
+    if ((st = cuda_result(tc ? kda::launch_lin_tc(l.a, cs) : kda::launch_lin(l.a, l.bf16, cs), "linear attention")) != KDA_OK) return st;
     if (c.s1 != ht)
         return cuda_result(cudaMemcpyAsync(ht, c.s1, sizeof(float) * (size_t)l.a.ax.N * l.a.HV * l.K * l.V,
                                            cudaMemcpyDeviceToDevice, cs), "copy of the final states");
@@ -108,22 +129,25 @@ kda_status kda_lin_bwd(const kda_lin_problem* p, const void* dout, const float* 
     if (l.a.ax.len > 0 && (!p->q || !p->k || !p->v || !dout || !dq || !dk || !dv))
         return fail(KDA_ERR_INVALID_ARG, "q, k, v, dout, dq, dk and dv must be non-NULL");
     if (dh0 && (dh0 == dht || dh0 == p->h0)) return fail(KDA_ERR_INVALID_ARG, "dh0 must have a buffer of its own");
-    set_windows(l, true);
-    const Layout y = layout(l, true);
-    if ((st = check_ws(ws, ws_bytes, y.all(true), "workspace")) != KDA_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, most_bytes(l, true), "workspace")) != KDA_OK) return st;
     Carver cw{static_cast<char*>(ws)};
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const int G = l.a.HV / l.H, K = l.K, V = l.V;
     const int64_t ldo = (int64_t)l.a.HV * V;
-    float* pq = cw.take<float>(y.dq);
-    float* pk = cw.take<float>(y.dk);
+    const size_t part = layout(l, true).dq;   // the same on both paths
+    float* pq = cw.take<float>(part);
+    float* pk = cw.take<float>(part);
     l.a.err = err;
     l.a.calls = 3;
     l.a.c[0] = {dout, p->v, p->k, ldo, l.ldv, l.ldk, 1, 1, G, V, K, pq ? pq : dq, pq != nullptr, p->h0, nullptr, 1, 0, l.scale, 1.f, nullptr};
     l.a.c[1] = {p->v, dout, p->q, l.ldv, ldo, l.ldq, 1, 1, G, V, K, pk ? pk : dk, pk != nullptr, dht, nullptr, 1, 1, 1.f, l.scale, nullptr};
     l.a.c[2] = {p->k, p->q, dout, l.ldk, l.ldq, ldo, G, G, 1, K, V, dv, 0, dht, dh0, 0, 1, 1.f, l.scale, nullptr};
+    bool tc = tc_sizes(l, true);
+    for (const kda::LinCall& c : l.a.c) tc = tc && kda::lin_tc_call(c);
+    set_windows(l, true, tc);
+    const Layout y = layout(l, true);
     for (kda::LinCall& c : l.a.c) c.local = cw.take<float>(y.local);
-    if ((st = cuda_result(kda::launch_lin(l.a, l.bf16, cs), "linear attention backward")) != KDA_OK) return st;
+    if ((st = cuda_result(tc ? kda::launch_lin_tc(l.a, cs) : kda::launch_lin(l.a, l.bf16, cs), "linear attention backward")) != KDA_OK) return st;
     if (!pq) return KDA_OK;
     const int64_t rows = (int64_t)l.a.ax.rows * l.a.ax.len * l.H;
     if ((st = cuda_result(kda::launch_lin_heads(pq, dq, rows, G, K, l.bf16, cs), "linear attention backward (heads)")) != KDA_OK) return st;

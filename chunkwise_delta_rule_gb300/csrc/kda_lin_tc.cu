@@ -1,0 +1,551 @@
+// Linear attention with a decay for each head on the tensor cores: bf16, K <= 128, in chunks of C = 128 tokens.
+// With a the head's decay, S the state entering a chunk of n tokens and the call's s and w (kda_lin.cuh), forwards
+//     P_ij = s w a^(i-j) (q_i k_j) for j <= i,   o_i = s a^(i+1) q_i S + sum_j P_ij v_j
+//     S <- a^n S + K^T V',   V'_j = w a^(n-1-j) v_j
+// and backwards in time (rows are tokens in memory order, the last one comes first)
+//     P_ij = s w a^(j-i) (q_i k_j) for j >= i,   o_i = s a^(n-1-i) q_i S + sum_j P_ij v_j,   V'_j = w a^(j+1) v_j.
+// A CTA walks a head's 64 value columns through a time window; the serial chain from chunk to chunk is one multiply-add
+// per state element in registers, everything else runs ahead of it. Roles: one warp loads (TMA, two chunks deep), one
+// issues the four products Q K^T, Q S, K^T V' and P V, and three groups of four warps turn scores into P (TMEM to TMEM),
+// keep the state, and form V' and then write the previous chunk's outputs.
+// Roundings: V' is three bf16 parts, 24 bits, so that the fp32 state is a sum of exact products (each chunk's is summed
+// by the tensor core from zero and added once); P and the copy of S that the queries meet are bf16; the output is
+// rounded once.
+// Powers of a: |i - j| = (i - block end) + (block end - j) for columns left of the row's block of 32, so that a score
+// costs two products and no exponential; on the diagonal block a row's 32 powers stay in registers.
+// Rows of the tiles behind a sequence's end belong to its neighbour: K, V and V' are zeroed there, so that whatever they
+// hold adds nothing; P is chosen, not multiplied, where masked.
+#include "kda_lin.cuh"
+#include "tc.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int C = 128, VB = 64;                 // tokens of a chunk, value columns of a CTA
+constexpr int NTHR = 14 * 32, LOADER = 12, ISSUER = 13;   // warps of the last two roles
+constexpr int ATOM = C * 128;                   // bytes of 128 rows of 64 bf16
+constexpr int OFF_K = 2 * ATOM, OFF_V = 4 * ATOM, STAGE = 5 * ATOM;
+constexpr int OFF_VP = 2 * STAGE, OFF_S = OFF_VP + 3 * ATOM, OFF_END = OFF_S + ATOM;
+constexpr int T_SC = 0, T_P = 128, T_O1 = 192, T_O2 = 256, T_KV = 320;   // TMEM columns
+
+struct Shared {
+    float pw[C + 1];            // a^m
+    float2 an;                  // a^C in two parts
+    uint64_t full[2], empty[2], sc_full, sc_free, p_full, pv_done, v_full, kv_done, s_full, o_free, drain;
+    uint32_t tmem;
+    int dead;
+};
+constexpr int SMEM = OFF_END + (int)sizeof(Shared) + 1024;
+static_assert(SMEM <= 232448, "shared memory above the per-block limit");
+
+struct LinTc {
+    CUtensorMap map[4];
+    LinArgs a;
+    int mq[3], mk[3], mv[3];    // each call's maps
+};
+
+// A whole warp waits for a phase; false once a wait of the CTA gave up (about 1 s).
+__device__ __forceinline__ bool wait(Shared& sm, uint64_t* bar, uint32_t parity) {
+    bool ok = tc::mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = tc::global_ns();
+        for (uint32_t i = 1; !(ok = tc::mbar_try_wait(bar, parity)); ++i)
+            if ((i & 63u) == 0 && (*reinterpret_cast<volatile int*>(&sm.dead) || tc::global_ns() - t0 > 1000000000ull)) break;
+        if (!ok) *reinterpret_cast<volatile int*>(&sm.dead) = 1;
+    }
+    return __all_sync(0xffffffffu, ok);   // a warp goes one way
+}
+// One arrival per warp, after all its lanes.
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
+// The chunks of a window, the same for every role.
+struct Chunks {
+    const LinArgs& a;
+    int row, t, t1, back;
+    Seq s;
+    __device__ Chunks(const LinArgs& a_, int row_, int t0, int t1_, int back_, bool local) : a(a_), row(row_), t(t0), t1(t1_), back(back_) {
+        if (t >= t1) return;
+        if (local) {   // only the sequence that goes on behind the window
+            s = lin_seq(a.ax, row, t1 - 1, back);
+            t = s.end <= t1 ? t1 : max(t0, s.first);
+        } else {
+            s = lin_seq(a.ax, row, t, back);
+        }
+    }
+    __device__ __forceinline__ bool more() const { return t < t1; }
+    __device__ __forceinline__ int n() const { return min(C, min(s.end, t1) - t); }
+    // the packed token of the tile's first row
+    __device__ __forceinline__ int64_t token(int n) const { return (int64_t)row * a.ax.len + (back ? a.ax.len - t - n : t); }
+    __device__ __forceinline__ void next(int n) {
+        t += n;
+        if (t < t1 && t == s.end) s = lin_seq(a.ax, row, t, back);
+    }
+};
+
+// LOCAL: the end states of the windows' own tokens only.
+template <bool LOCAL>
+__global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinTc g) {
+    extern __shared__ unsigned char raw[];
+    const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
+    unsigned char* mem = raw + (base - tc::smem_u32(raw));
+    Shared& sm = *reinterpret_cast<Shared*>(mem + OFF_END);
+    const LinArgs& a = g.a;
+    const LinCall& c = a.c[blockIdx.y];
+    const int blocks = (c.V + VB - 1) / VB;
+    int at = blockIdx.x;
+    const int v0 = at % blocks * VB;
+    at /= blocks;
+    const int h = at % a.HV, unit = at / a.HV;
+    if (unit >= a.ax.rows * a.units_row) return;
+    const int row = unit / a.units_row, u = unit - row * a.units_row;
+    const int t0 = u * a.unit_len, t1 = min(a.ax.len, t0 + a.unit_len);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, role = warp >> 2, q32 = (warp & 3) * 32;
+    const int KA = c.K > 64 ? 2 : 1;
+    const float decay = a.decay ? a.decay[h] : 0.f;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sm.full[i], 1);
+            tc::mbar_init(&sm.empty[i], 1);
+        }
+        tc::mbar_init(&sm.sc_full, 1);
+        tc::mbar_init(&sm.pv_done, 1);
+        tc::mbar_init(&sm.kv_done, 1);
+        tc::mbar_init(&sm.drain, 1);
+        tc::mbar_init(&sm.sc_free, 4);
+        tc::mbar_init(&sm.p_full, 4);
+        tc::mbar_init(&sm.v_full, 4);
+        tc::mbar_init(&sm.s_full, 4);
+        tc::mbar_init(&sm.o_free, 4);
+        sm.dead = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == ISSUER) {
+        tc::tmem_alloc(&sm.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    for (int m = threadIdx.x; m <= C; m += NTHR) sm.pw[m] = lin_power(decay, m);
+    if (threadIdx.x == LOADER * 32) sm.an = lin_power2(decay, C);
+    if (KA == 1)   // the second half of the key rows: nothing, in every chunk
+        for (int i = threadIdx.x; i < 2 * ATOM / 16; i += NTHR)
+            *reinterpret_cast<uint4*>(mem + (i >= ATOM / 16) * STAGE + OFF_K + ATOM + i % (ATOM / 16) * 16) = make_uint4(0, 0, 0, 0);
+    tc::fence_async_smem();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tb = sm.tmem;
+
+    if (role == 0 && !LOCAL) {
+        // ---------------------------------------------------------------- scores to P; this thread's row i
+        const int i = q32 + lane, w = warp;
+        const float sw = c.s * c.w;
+        float diag[32], rowf[4];
+#pragma unroll
+        for (int m = 0; m < 32; ++m) diag[m] = sw * sm.pw[abs(lane - m)];
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            rowf[b] = sw * (c.back ? (b > w ? sm.pw[32 * b - i] : 0.f) : (b < w ? sm.pw[i - 32 * b - 31] : 0.f));
+        const uint32_t tp = tc::taddr(tb, q32, T_P), ts = tc::taddr(tb, q32, T_SC);
+        {
+            uint32_t z[16];
+#pragma unroll
+            for (int m = 0; m < 16; ++m) z[m] = 0;
+            for (int b = 0; b < 4; ++b) tc::tmem_st16u(tp + 16 * b, z);
+            tc::tmem_wait_st();
+        }
+        uint32_t ph = 0;
+        for (Chunks k(a, row, t0, t1, c.back, false); k.more(); ph ^= 1) {
+            const int n = k.n();
+            if (!wait(sm, &sm.sc_full, ph)) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (c.back ? b < w : b > w) continue;
+                float x[2][16];
+                tc::tmem_ld16(ts + 32 * b, x[0]);
+                tc::tmem_ld16(ts + 32 * b + 16, x[1]);
+                tc::tmem_wait_ld();
+                uint32_t p[16];
+#pragma unroll
+                for (int m = 0; m < 32; m += 2) {
+                    float y[2];
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const float v = x[(m + z) >> 4][(m + z) & 15];
+                        if (b == w) {
+                            y[z] = (c.back ? m + z >= lane : m + z <= lane) ? v * diag[m + z] : 0.f;
+                        } else {
+                            y[z] = v * (rowf[b] * sm.pw[c.back ? m + z : 31 - m - z]);
+                        }
+                        if (c.back && n < C && 32 * b + m + z >= n) y[z] = 0.f;
+                    }
+                    p[m >> 1] = tc::pack_bf16(y[0], y[1]);
+                }
+                tc::tmem_st16u(tp + 16 * b, p);
+            }
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                tc::mbar_arrive(&sm.sc_free);
+                tc::mbar_arrive(&sm.p_full);
+            }
+            k.next(n);
+        }
+    } else if (role == 1) {
+        // ---------------------------------------------------------------- the state; this thread's key row
+        const int kk = q32 + lane;
+        const size_t KV = (size_t)c.K * c.V;
+        const bool mine = kk < c.K;
+        float S[VB];
+        auto start_state = [&](int n) {
+            const float* p = c.s0 ? c.s0 + ((size_t)n * a.HV + h) * KV : nullptr;
+            const size_t rk = c.transposed ? 1 : c.V, rv = c.transposed ? c.K : 1;
+#pragma unroll
+            for (int v = 0; v < VB; ++v) S[v] = p && mine && v0 + v < c.V ? p[kk * rk + (v0 + v) * rv] : 0.f;
+        };
+        auto store_state = [&](float* p) {
+            if (!mine) return;
+            p += (size_t)kk * c.V + v0;
+            const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+#pragma unroll
+            for (int v = 0; v < VB; v += 4) {   // V is a multiple of 8
+                if (v0 + v >= c.V) break;
+                if (vec) {
+                    *reinterpret_cast<float4*>(p + v) = make_float4(S[v], S[v + 1], S[v + 2], S[v + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[v + i] = S[v + i];
+                }
+            }
+        };
+        if (u == 0 && !LOCAL && c.s1) {   // final states of sequences without tokens
+            if (!a.ax.cu) {
+                if (a.ax.len == 0) {
+                    start_state(row);
+                    store_state(c.s1 + ((size_t)row * a.HV + h) * KV);
+                }
+            } else {
+                for (int n = 0; n < a.ax.N; ++n) {
+                    if (axis_cu(a.ax, n + 1) > axis_cu(a.ax, n)) continue;
+                    start_state(n);
+                    store_state(c.s1 + ((size_t)n * a.HV + h) * KV);
+                }
+            }
+        }
+        uint32_t ph = 0;
+        int seq = -1;
+        const uint32_t tk = tc::taddr(tb, q32, T_KV);
+        unsigned char* sb = mem + OFF_S + kk * 128;
+        for (Chunks k(a, row, t0, t1, c.back, LOCAL); k.more(); ph ^= 1) {
+            const int n = k.n();
+            if (LOCAL) {
+                if (seq < 0) {
+#pragma unroll
+                    for (int v = 0; v < VB; ++v) S[v] = 0.f;
+                }
+                seq = k.s.n;
+            } else {
+                if (seq < 0 || k.t == k.s.first) {
+                    start_state(k.s.n);
+                    for (int e = k.s.first < k.t ? k.s.first / a.unit_len : u; e < u; ++e) {   // it came through earlier windows
+                        const float f = lin_power(decay, (e + 1) * a.unit_len - max(k.s.first, e * a.unit_len));
+                        const float* p = c.local + ((size_t)(unit - u + e) * a.HV + h) * KV + (size_t)kk * c.V + v0;
+#pragma unroll
+                        for (int v = 0; v < VB; ++v)
+                            if (mine && v0 + v < c.V) S[v] = fmaf(S[v], f, p[v]);
+                    }
+                }
+                seq = k.s.n;
+#pragma unroll
+                for (int v = 0; v < VB; v += 8) {
+                    uint4 x;
+                    x.x = tc::pack_bf16(S[v], S[v + 1]);
+                    x.y = tc::pack_bf16(S[v + 2], S[v + 3]);
+                    x.z = tc::pack_bf16(S[v + 4], S[v + 5]);
+                    x.w = tc::pack_bf16(S[v + 6], S[v + 7]);
+                    *reinterpret_cast<uint4*>(sb + (((v >> 3) ^ (kk & 7)) << 4)) = x;
+                }
+                tc::fence_async_smem();
+            }
+            tc::fence_before_sync();
+            arrive_warp(&sm.s_full);
+            if (!wait(sm, &sm.kv_done, ph)) break;
+            tc::fence_after_sync();
+            const float2 an = n == C ? sm.an : make_float2(sm.pw[n], 0.f);
+#pragma unroll
+            for (int v = 0; v < VB; v += 16) {
+                float x[3][16];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) tc::tmem_ld16(tk + VB * i + v, x[i]);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float kv = x[0][i] + (x[1][i] + x[2][i]);
+                    S[v + i] = an.x == 1.f ? S[v + i] + kv : fmaf(S[v + i], an.x, fmaf(S[v + i], an.y, kv));
+                }
+            }
+            if (!LOCAL && k.t + n == k.s.end && c.s1) store_state(c.s1 + ((size_t)k.s.n * a.HV + h) * KV);
+            k.next(n);
+        }
+        if (LOCAL && seq >= 0) store_state(c.local + ((size_t)unit * a.HV + h) * KV);
+    } else if (role == 2) {
+        // ------------------------------------------------ V' in three parts, and outputs; this thread's token row
+        const int j = q32 + lane;
+        uint32_t ph = 0, stage = 0, fph = 0;
+        if (!LOCAL && blockIdx.x == 0 && blockIdx.y == 0 && a.err && a.ax.cu) {   // as axis_check, by this group
+            bool bad = false;
+            for (int n = j; n < a.ax.N; n += 128) bad |= a.ax.cu[n + 1] < a.ax.cu[n];
+            if (j == 0) bad |= a.ax.cu[0] != 0 || a.ax.cu[a.ax.N] != a.ax.len;
+            if (bad) atomicOr(a.err, 1);
+        }
+        const uint32_t t1a = tc::taddr(tb, q32, T_O1), t2a = tc::taddr(tb, q32, T_O2);
+        // The outputs of a chunk of n tokens from packed token z on.
+        auto output = [&](int n, int64_t z, uint32_t phase) {
+            const float gam = c.s * sm.pw[j < n ? (c.back ? n - 1 - j : j + 1) : 0];
+            if (!wait(sm, &sm.pv_done, phase)) return false;
+            tc::fence_after_sync();
+            float o[VB];
+#pragma unroll
+            for (int v = 0; v < VB; v += 16) {
+                float x[16], y[16];
+                tc::tmem_ld16(t1a + v, x);
+                tc::tmem_ld16(t2a + v, y);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int m = 0; m < 16; ++m) o[v + m] = fmaf(gam, x[m], y[m]);
+            }
+            tc::fence_before_sync();
+            arrive_warp(&sm.o_free);
+            if (j < n) {
+                const size_t to = ((size_t)(z + j) * a.HV + h) * c.V + v0;
+                if (c.o_f32) {
+                    float* p = static_cast<float*>(c.o) + to;
+#pragma unroll
+                    for (int v = 0; v < VB; v += 4)
+                        if (v0 + v < c.V) *reinterpret_cast<float4*>(p + v) = make_float4(o[v], o[v + 1], o[v + 2], o[v + 3]);
+                } else {
+                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(c.o) + to;
+#pragma unroll
+                    for (int v = 0; v < VB; v += 8) {
+                        uint4 x;
+                        x.x = tc::pack_bf16(o[v], o[v + 1]);
+                        x.y = tc::pack_bf16(o[v + 2], o[v + 3]);
+                        x.z = tc::pack_bf16(o[v + 4], o[v + 5]);
+                        x.w = tc::pack_bf16(o[v + 6], o[v + 7]);
+                        if (v0 + v < c.V) *reinterpret_cast<uint4*>(p + v) = x;
+                    }
+                }
+            }
+            return true;
+        };
+        int pn = 0;   // the previous chunk
+        int64_t pz = 0;
+        for (Chunks k(a, row, t0, t1, c.back, LOCAL); k.more();) {
+            const int n = k.n();
+            unsigned char* st = mem + stage * STAGE;
+            if (!wait(sm, &sm.full[stage], fph)) break;
+            if (pn && !wait(sm, &sm.kv_done, ph ^ 1)) break;
+            unsigned char* vr = st + OFF_V + j * 128;
+            unsigned char* to = mem + OFF_VP + j * 128;
+            if (j < n) {
+                const float e = c.w * sm.pw[c.back ? j + 1 : n - 1 - j];
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) {
+                    const uint32_t o = (ch ^ (j & 7)) << 4;
+                    const uint4 v = *reinterpret_cast<const uint4*>(vr + o);
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t out[3][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x = e * __uint_as_float(in[i] << 16), y = e * __uint_as_float(in[i] & 0xffff0000u);
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) {
+                            out[p][i] = tc::pack_bf16(x, y);
+                            x -= __uint_as_float(out[p][i] << 16);
+                            y -= __uint_as_float(out[p][i] & 0xffff0000u);
+                        }
+                    }
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        *reinterpret_cast<uint4*>(to + p * ATOM + o) = make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
+                }
+            } else {
+                const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) {
+                    *reinterpret_cast<uint4*>(vr + 16 * ch) = z;
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(to + p * ATOM + 16 * ch) = z;
+                    for (int p = 0; p < KA; ++p) *reinterpret_cast<uint4*>(st + OFF_K + p * ATOM + j * 128 + 16 * ch) = z;
+                }
+            }
+            tc::fence_async_smem();
+            arrive_warp(&sm.v_full);
+            if (!LOCAL && pn && !output(pn, pz, ph ^ 1)) {
+                pn = 0;
+                break;
+            }
+            pn = n;
+            pz = k.token(n);
+            ph ^= 1;
+            stage ^= 1;
+            fph ^= stage == 0;
+            k.next(n);
+        }
+        if (!LOCAL && pn) output(pn, pz, ph ^ 1);
+    } else if (warp == LOADER) {
+        // ---------------------------------------------------------------- loads
+        const CUtensorMap *mq = &g.map[g.mq[blockIdx.y]], *mk = &g.map[g.mk[blockIdx.y]], *mv = &g.map[g.mv[blockIdx.y]];
+        const int hq = h / c.gq, hk = h / c.gk, hv = h / c.gv;
+        uint32_t stage = 0, eph = 1;
+        int issued = 0;
+        for (Chunks k(a, row, t0, t1, c.back, LOCAL); k.more();) {
+            const int n = k.n(), z = (int)k.token(n);
+            if (!wait(sm, &sm.empty[stage], eph)) break;   // (the phase before the first counts as complete)
+            if (lane == 0) {
+                const uint32_t d = base + stage * STAGE;
+                tc::mbar_arrive_expect_tx(&sm.full[stage], ((LOCAL ? 1 : 2) * KA + 1) * ATOM);
+                for (int p = 0; p < KA; ++p) {
+                    tc::tma_load3(d + OFF_K + p * ATOM, mk, 64 * p, hk, z, &sm.full[stage]);
+                    if (!LOCAL) tc::tma_load3(d + p * ATOM, mq, 64 * p, hq, z, &sm.full[stage]);
+                }
+                tc::tma_load3(d + OFF_V, mv, v0, hv, z, &sm.full[stage]);
+            }
+            __syncwarp();
+            ++issued;
+            stage ^= 1;
+            eph ^= stage == 0;
+            k.next(n);
+        }
+        // no copy is in flight when the CTA ends, after a failure either
+        for (int i = max(0, issued - 2); i < issued; ++i) tc::mbar_wait(&sm.full[i & 1], (i >> 1) & 1);
+    } else if (warp == ISSUER) {
+        // ---------------------------------------------------------------- products
+        constexpr uint32_t I_SC = tc::idesc_bf16(C, C), I_O = tc::idesc_bf16_bmn(C, VB), I_KV = tc::idesc_bf16_abmn(C, 3 * VB);
+        uint32_t stage = 0, fph = 0, ph = 0;
+        bool first = true, ok = true;
+        const uint64_t dvp = tc::sdesc_mn(base + OFF_VP, ATOM, 0), dsb = tc::sdesc_mn(base + OFF_S, ATOM, 0);
+        for (Chunks k(a, row, t0, t1, c.back, LOCAL); k.more();) {
+            const int n = k.n();
+            const uint32_t st = base + stage * STAGE;
+            const uint64_t dq = tc::sdesc_k(st, C, 0), dk = tc::sdesc_k(st + OFF_K, C, 0);
+            ok = wait(sm, &sm.full[stage], fph);
+            if (!LOCAL) {
+                if (ok && !first) ok = wait(sm, &sm.sc_free, ph ^ 1);
+                if (!ok) break;
+                tc::fence_after_sync();
+                for (int s = 0; s < 4 * KA; ++s)
+                    tc::mma_bf16_w(tb + T_SC, tc::kstep_k(dq, C, s), tc::kstep_k(dk, C, s), I_SC, s > 0);
+                tc::mma_commit_w(&sm.sc_full);
+            }
+            ok = ok && wait(sm, &sm.s_full, ph);
+            if (!LOCAL && ok && !first) ok = wait(sm, &sm.o_free, ph ^ 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (!LOCAL) {
+                for (int s = 0; s < 4 * KA; ++s)
+                    tc::mma_bf16_w(tb + T_O1, tc::kstep_k(dq, C, s), tc::kstep_mn(dsb, s), I_O, s > 0);
+            }
+            ok = wait(sm, &sm.v_full, ph);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint64_t dkt = tc::sdesc_mn(st + OFF_K, ATOM, 0), dv = tc::sdesc_mn(st + OFF_V, ATOM, 0);
+            for (int s = 0; s < C / 16; ++s)
+                tc::mma_bf16_w(tb + T_KV, tc::kstep_mn(dkt, s), tc::kstep_mn(dvp, s), I_KV, s > 0);
+            tc::mma_commit_w(&sm.kv_done);
+            if (!LOCAL) {
+                ok = wait(sm, &sm.p_full, ph);
+                if (!ok) break;
+                tc::fence_after_sync();
+                for (int s = 0; s < C / 16; ++s)
+                    tc::mma_bf16_ts_w(tb + T_O2, tb + T_P + 8 * s, tc::kstep_mn(dv, s), I_O, s > 0);
+                tc::mma_commit_w(&sm.pv_done);
+            }
+            tc::mma_commit_w(&sm.empty[stage]);
+            first = false;
+            ph ^= 1;
+            stage ^= 1;
+            fph ^= stage == 0;
+            k.next(n);
+        }
+        // every product is done before the tensor memory goes back (after a failure, too)
+        tc::mma_commit_w(&sm.drain);
+        if (!tc::mbar_wait(&sm.drain, 0)) sm.dead = 1;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (threadIdx.x == 0 && sm.dead && a.err) atomicOr(a.err, 2);
+    if (warp == ISSUER) tc::tmem_dealloc(tb, 512);
+}
+
+template <bool LOCAL>
+cudaError_t run(const LinTc& g, cudaStream_t st) {
+    static SmemLimit limit;
+    const cudaError_t e = limit.set(reinterpret_cast<const void*>(&k_lin_tc<LOCAL>), SMEM);
+    if (e != cudaSuccess) return e;
+    int vmax = 1;
+    for (int i = 0; i < g.a.calls; ++i) vmax = g.a.c[i].V > vmax ? g.a.c[i].V : vmax;
+    const long long ctas = (long long)g.a.ax.rows * g.a.units_row * g.a.HV * ((vmax + VB - 1) / VB);
+    if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    return traced_launch(LOCAL ? "k_lin_tc_windows" : "k_lin_tc", st,
+                         [&] { k_lin_tc<LOCAL><<<dim3((unsigned)ctas, g.a.calls), NTHR, SMEM, st>>>(g); });
+}
+
+}  // namespace
+
+bool lin_tc_call(const LinCall& c) {
+    const auto on = [](const void* p, int64_t ld, int w) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && w % 8 == 0; };
+    return c.K <= C && on(c.q, c.ldq, c.K) && on(c.k, c.ldk, c.K) && on(c.v, c.ldv, c.V) && (reinterpret_cast<uintptr_t>(c.o) & 15) == 0;
+}
+
+// A row cut into n windows costs its CTAs' rounds over the SMs, each of a window's chunks (half as much again where the
+// windows' own states are formed first), some two chunks' time to start and a third of one for each earlier window's
+// state; the cheapest n of powers of two is taken.
+int lin_tc_window(int rows, int len, int ctas) {
+    const int chunks = (len + C - 1) / C;
+    if (chunks < 2) return C;
+    double least = 0;
+    int best = chunks;
+    for (int n = 1; n <= chunks && n <= 256; n *= 2) {
+        const int each = (chunks + n - 1) / n;
+        const long long all = (long long)rows * ctas * n, rounds = (all + sm_count() - 1) / sm_count();
+        const double cost = rounds * (each * (n > 1 ? 1.5 : 1.) + 2. + (n > 1 ? 0.17 * n + 2. : 0.));
+        if (n == 1 || cost < least) {
+            least = cost;
+            best = each;
+        }
+    }
+    return best * C;
+}
+
+cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st) {
+    LinTc g;
+    g.a = a;
+    const int64_t tokens = (int64_t)a.ax.rows * a.ax.len;
+    int maps = 0;
+    struct { const void* p; int64_t ld; int group, width; } seen[4];
+    const auto map = [&](const void* p, int64_t ld, int group, int width, int& to) {
+        for (to = 0; to < maps; ++to)   // the same tensor in another role
+            if (seen[to].p == p && seen[to].ld == ld && seen[to].group == group && seen[to].width == width) return true;
+        if (maps == 4) return false;
+        seen[maps] = {p, ld, group, width};
+        return tmap_tokens_bf16(&g.map[maps++], p, tokens, a.HV / group, width, ld, C);
+    };
+    for (int i = 0; i < a.calls; ++i) {
+        const LinCall& c = a.c[i];
+        if (!map(c.q, c.ldq, c.gq, c.K, g.mq[i]) || !map(c.k, c.ldk, c.gk, c.K, g.mk[i]) || !map(c.v, c.ldv, c.gv, c.V, g.mv[i]))
+            return cudaErrorInvalidValue;
+    }
+    if (a.units_row > 1) {
+        const cudaError_t e = run<true>(g, st);
+        if (e != cudaSuccess) return e;
+    }
+    return run<false>(g, st);
+}
+
+}  // namespace kda

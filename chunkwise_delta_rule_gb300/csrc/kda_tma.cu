@@ -24,6 +24,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
+// The driver's calls need a context on their thread, and a thread that has made no call of the runtime's yet (a
+// backward's, for one) has none: setting the device that is current binds it.
+bool bind_context() {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
 bool encode(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base, int Ttot, int H, int D,
             int box_x, CUtensorMapSwizzle sw) {
     auto fn = encode_fn();
@@ -40,6 +47,21 @@ bool encode(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base,
 
 bool tmap_rows_bf16(CUtensorMap* m, const void* base, int Ttot, int H, int D) {
     return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, Ttot, H, D, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool tmap_tokens_bf16(CUtensorMap* m, const void* base, int64_t tokens, int H, int D, int64_t ld, int rows) {
+    auto fn = encode_fn();
+    if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15)) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
+    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)rows};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    const auto encode = [&] {
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return encode() || (bind_context() && encode());
 }
 
 bool tmap_state_f32(CUtensorMap* m, const float* base, int NH, int K, int V) {

@@ -80,6 +80,7 @@ CASES += [dict(io="fp32", B=3, T=50, H=2, K=12, V=20, pad=p) for p in (4, 1)]
 CASES += [dict(io=io, B=2, T=200, H=5, K=64, V=64, state=True, decay=d) for io in ("bf16", "fp32") for d in (None, "strong", "up")]
 CASES += [dict(io=io, B=1, T=2100, H=1, K=64, V=64, state=True) for io in ("bf16", "fp32")]          # time windows
 CASES += [dict(io=io, B=1, H=1, HV=2, K=40, V=24, state=True, lengths=[3, 1500, 0, 2, 640, 129]) for io in ("bf16", "fp32")]
+CASES += [dict(io="bf16", B=1, T=T, H=1, HV=HV, K=K, V=V, state=True) for T, HV, K, V in ((4500, 1, 128, 128), (1000, 2, 120, 104), (513, 1, 72, 200))]
 CASES += [dict(io="bf16", B=2, T=200, H=2, K=64, V=64, scale=0.3), dict(io="fp32", B=4, T=0, H=2, K=8, V=8, state=True)]
 
 

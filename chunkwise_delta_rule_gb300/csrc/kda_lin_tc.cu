@@ -30,6 +30,7 @@ constexpr int T_SC = 0, T_P = 128, T_O1 = 192, T_O2 = 256, T_KV = 320;   // TMEM
 
 struct Shared {
     float pw[C + 1];            // a^m
+    alignas(16) float col[32];  // a block's column's power: to the block's end forwards, from its start backwards
     float2 an;                  // a^C in two parts
     uint64_t full[2], empty[2], sc_full, sc_free, p_full, pv_done, v_full, kv_done, s_full, o_free, drain;
     uint32_t tmem;
@@ -127,7 +128,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         tc::tmem_alloc(&sm.tmem, 512);
         tc::tmem_relinquish();
     }
+    const bool back = c.back != 0;
     for (int m = threadIdx.x; m <= C; m += NTHR) sm.pw[m] = lin_power(decay, m);
+    if (threadIdx.x < 32) sm.col[threadIdx.x] = lin_power(decay, back ? threadIdx.x : 31 - threadIdx.x);
     if (threadIdx.x == LOADER * 32) sm.an = lin_power2(decay, C);
     if (KA == 1)   // the second half of the key rows: nothing, in every chunk
         for (int i = threadIdx.x; i < 2 * ATOM / 16; i += NTHR)
@@ -142,13 +145,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         // ---------------------------------------------------------------- scores to P; this thread's row i
         const int i = q32 + lane, w = warp;
         const float sw = c.s * c.w;
-        float diag[32], rowf[4];
-#pragma unroll
-        for (int m = 0; m < 32; ++m) diag[m] = sw * sm.pw[abs(lane - m)];
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-            rowf[b] = sw * (c.back ? (b > w ? sm.pw[32 * b - i] : 0.f) : (b < w ? sm.pw[i - 32 * b - 31] : 0.f));
         const uint32_t tp = tc::taddr(tb, q32, T_P), ts = tc::taddr(tb, q32, T_SC);
+        const uint32_t tri = back ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);   // the diagonal block's columns that row i meets
         {
             uint32_t z[16];
 #pragma unroll
@@ -157,33 +155,46 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             tc::tmem_wait_st();
         }
         uint32_t ph = 0;
-        for (Chunks k(a, row, t0, t1, c.back, false); k.more(); ph ^= 1) {
+        for (Chunks k(a, row, t0, t1, back, false); k.more(); ph ^= 1) {
             const int n = k.n();
             if (!wait(sm, &sm.sc_full, ph)) break;
             tc::fence_after_sync();
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (c.back ? b < w : b > w) continue;
+            // (Loops as short as they get: a warp is alone on its scheduler with this code, and long straight runs of it
+            // wait for instructions.)
+#pragma unroll 1
+            for (int b = back ? w : 0; b <= (back ? 3 : w); ++b) {
                 float x[2][16];
                 tc::tmem_ld16(ts + 32 * b, x[0]);
                 tc::tmem_ld16(ts + 32 * b + 16, x[1]);
-                tc::tmem_wait_ld();
-                uint32_t p[16];
+                const int left = min(max(n - 32 * b, 0), 32);   // columns of tokens that the chunk has
+                uint32_t mask = left == 32 ? 0xffffffffu : (1u << left) - 1u, p[16];
+                if (b == w) {
+                    mask &= tri;
+                    float f[32];
 #pragma unroll
-                for (int m = 0; m < 32; m += 2) {
-                    float y[2];
+                    for (int m = 0; m < 32; ++m) f[m] = sw * sm.pw[abs(lane - m)];
+                    tc::tmem_wait_ld();
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const float v = x[(m + z) >> 4][(m + z) & 15];
-                        if (b == w) {
-                            y[z] = (c.back ? m + z >= lane : m + z <= lane) ? v * diag[m + z] : 0.f;
-                        } else {
-                            y[z] = v * (rowf[b] * sm.pw[c.back ? m + z : 31 - m - z]);
-                        }
-                        if (c.back && n < C && 32 * b + m + z >= n) y[z] = 0.f;
+                    for (int m = 0; m < 32; ++m) x[m >> 4][m & 15] = mask >> m & 1 ? x[m >> 4][m & 15] * f[m] : 0.f;
+                } else {
+                    const float rowf = sw * sm.pw[back ? 32 * b - i : i - 32 * b - 31];
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int m = 0; m < 32; m += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&sm.col[m]);
+                        float* y = &x[m >> 4][m & 15];
+                        y[0] *= rowf * f.x;
+                        y[1] *= rowf * f.y;
+                        y[2] *= rowf * f.z;
+                        y[3] *= rowf * f.w;
                     }
-                    p[m >> 1] = tc::pack_bf16(y[0], y[1]);
+                    if (back && left < 32) {
+#pragma unroll
+                        for (int m = 0; m < 32; ++m) x[m >> 4][m & 15] = mask >> m & 1 ? x[m >> 4][m & 15] : 0.f;
+                    }
                 }
+#pragma unroll
+                for (int m = 0; m < 16; ++m) p[m] = tc::pack_bf16(x[m >> 3][2 * m & 15], x[m >> 3][(2 * m & 15) + 1]);
                 tc::tmem_st16u(tp + 16 * b, p);
             }
             tc::tmem_wait_st();
@@ -198,22 +209,22 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
     } else if (role == 1) {
         // ---------------------------------------------------------------- the state; this thread's key row
         const int kk = q32 + lane;
-        const size_t KV = (size_t)c.K * c.V;
-        const bool mine = kk < c.K;
+        const size_t KV = (size_t)c.K * c.V, mine = (size_t)kk * c.V + v0;   // a state's elements, and this row's place in it
+        const int cols = kk < c.K ? min(VB, c.V - v0) : 0;                   // a multiple of 8
         float S[VB];
-        auto start_state = [&](int n) {
-            const float* p = c.s0 ? c.s0 + ((size_t)n * a.HV + h) * KV : nullptr;
-            const size_t rk = c.transposed ? 1 : c.V, rv = c.transposed ? c.K : 1;
-#pragma unroll
-            for (int v = 0; v < VB; ++v) S[v] = p && mine && v0 + v < c.V ? p[kk * rk + (v0 + v) * rv] : 0.f;
-        };
+        if (u == 0 && !LOCAL && c.s1) {   // final states of sequences without tokens
+            for (int n = a.ax.cu ? 0 : row; n < (a.ax.cu ? a.ax.N : row + 1); ++n) {
+                if (a.ax.cu ? axis_cu(a.ax, n + 1) > axis_cu(a.ax, n) : a.ax.len > 0) continue;
+                const size_t to = ((size_t)n * a.HV + h) * KV + mine;
+#pragma unroll 1
+                for (int v = 0; v < cols; ++v) c.s1[to + v] = c.s0 ? c.s0[to + v] : 0.f;   // (a call with s1 has natural states)
+            }
+        }
         auto store_state = [&](float* p) {
-            if (!mine) return;
-            p += (size_t)kk * c.V + v0;
             const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 #pragma unroll
-            for (int v = 0; v < VB; v += 4) {   // V is a multiple of 8
-                if (v0 + v >= c.V) break;
+            for (int v = 0; v < VB; v += 4) {
+                if (v >= cols) break;
                 if (vec) {
                     *reinterpret_cast<float4*>(p + v) = make_float4(S[v], S[v + 1], S[v + 2], S[v + 3]);
                 } else {
@@ -222,25 +233,11 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 }
             }
         };
-        if (u == 0 && !LOCAL && c.s1) {   // final states of sequences without tokens
-            if (!a.ax.cu) {
-                if (a.ax.len == 0) {
-                    start_state(row);
-                    store_state(c.s1 + ((size_t)row * a.HV + h) * KV);
-                }
-            } else {
-                for (int n = 0; n < a.ax.N; ++n) {
-                    if (axis_cu(a.ax, n + 1) > axis_cu(a.ax, n)) continue;
-                    start_state(n);
-                    store_state(c.s1 + ((size_t)n * a.HV + h) * KV);
-                }
-            }
-        }
         uint32_t ph = 0;
         int seq = -1;
         const uint32_t tk = tc::taddr(tb, q32, T_KV);
         unsigned char* sb = mem + OFF_S + kk * 128;
-        for (Chunks k(a, row, t0, t1, c.back, LOCAL); k.more(); ph ^= 1) {
+        for (Chunks k(a, row, t0, t1, back, LOCAL); k.more(); ph ^= 1) {
             const int n = k.n();
             if (LOCAL) {
                 if (seq < 0) {
@@ -250,13 +247,26 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 seq = k.s.n;
             } else {
                 if (seq < 0 || k.t == k.s.first) {
-                    start_state(k.s.n);
+                    const size_t rk = c.transposed ? 1 : c.V, rv = c.transposed ? c.K : 1;
+                    const float* p = c.s0 + ((size_t)k.s.n * a.HV + h) * KV + kk * rk + v0 * rv;
+                    const bool has = c.s0 != nullptr;
+#pragma unroll
+                    for (int v = 0; v < VB; ++v) {
+                        S[v] = has && v < cols ? *p : 0.f;
+                        p += rv;
+                    }
                     for (int e = k.s.first < k.t ? k.s.first / a.unit_len : u; e < u; ++e) {   // it came through earlier windows
                         const float f = lin_power(decay, (e + 1) * a.unit_len - max(k.s.first, e * a.unit_len));
-                        const float* p = c.local + ((size_t)(unit - u + e) * a.HV + h) * KV + (size_t)kk * c.V + v0;
+                        const float* y = c.local + ((size_t)(unit - u + e) * a.HV + h) * KV + mine;
 #pragma unroll
-                        for (int v = 0; v < VB; ++v)
-                            if (mine && v0 + v < c.V) S[v] = fmaf(S[v], f, p[v]);
+                        for (int v = 0; v < VB; v += 4) {
+                            if (v >= cols) break;
+                            const float4 x = *reinterpret_cast<const float4*>(y + v);
+                            S[v] = fmaf(S[v], f, x.x);
+                            S[v + 1] = fmaf(S[v + 1], f, x.y);
+                            S[v + 2] = fmaf(S[v + 2], f, x.z);
+                            S[v + 3] = fmaf(S[v + 3], f, x.w);
+                        }
                     }
                 }
                 seq = k.s.n;
@@ -277,21 +287,21 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             tc::fence_after_sync();
             const float2 an = n == C ? sm.an : make_float2(sm.pw[n], 0.f);
 #pragma unroll
-            for (int v = 0; v < VB; v += 16) {
-                float x[3][16];
+            for (int v = 0; v < VB; v += 8) {
+                float x[3][8];
 #pragma unroll
-                for (int i = 0; i < 3; ++i) tc::tmem_ld16(tk + VB * i + v, x[i]);
+                for (int i = 0; i < 3; ++i) tc::tmem_ld8(tk + VB * i + v, x[i]);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     const float kv = x[0][i] + (x[1][i] + x[2][i]);
-                    S[v + i] = an.x == 1.f ? S[v + i] + kv : fmaf(S[v + i], an.x, fmaf(S[v + i], an.y, kv));
+                    S[v + i] = fmaf(S[v + i], an.x, fmaf(S[v + i], an.y, kv));
                 }
             }
-            if (!LOCAL && k.t + n == k.s.end && c.s1) store_state(c.s1 + ((size_t)k.s.n * a.HV + h) * KV);
+            if (!LOCAL && k.t + n == k.s.end && c.s1) store_state(c.s1 + ((size_t)k.s.n * a.HV + h) * KV + mine);
             k.next(n);
         }
-        if (LOCAL && seq >= 0) store_state(c.local + ((size_t)unit * a.HV + h) * KV);
+        if (LOCAL && seq >= 0) store_state(c.local + ((size_t)unit * a.HV + h) * KV + mine);
     } else if (role == 2) {
         // ------------------------------------------------ V' in three parts, and outputs; this thread's token row
         const int j = q32 + lane;
@@ -305,46 +315,41 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         const uint32_t t1a = tc::taddr(tb, q32, T_O1), t2a = tc::taddr(tb, q32, T_O2);
         // The outputs of a chunk of n tokens from packed token z on.
         auto output = [&](int n, int64_t z, uint32_t phase) {
-            const float gam = c.s * sm.pw[j < n ? (c.back ? n - 1 - j : j + 1) : 0];
+            const float gam = c.s * sm.pw[j < n ? (back ? n - 1 - j : j + 1) : 0];
             if (!wait(sm, &sm.pv_done, phase)) return false;
             tc::fence_after_sync();
-            float o[VB];
-#pragma unroll
+            const bool there = j < n;
+            const size_t to = ((size_t)(z + (there ? j : 0)) * a.HV + h) * c.V + v0;
+#pragma unroll 1
             for (int v = 0; v < VB; v += 16) {
                 float x[16], y[16];
                 tc::tmem_ld16(t1a + v, x);
                 tc::tmem_ld16(t2a + v, y);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int m = 0; m < 16; ++m) o[v + m] = fmaf(gam, x[m], y[m]);
+                for (int m = 0; m < 16; ++m) x[m] = fmaf(gam, x[m], y[m]);
+                if (c.o_f32) {
+                    float* p = static_cast<float*>(c.o) + to + v;
+#pragma unroll
+                    for (int m = 0; m < 16; m += 4)
+                        if (there && v0 + v + m < c.V) *reinterpret_cast<float4*>(p + m) = make_float4(x[m], x[m + 1], x[m + 2], x[m + 3]);
+                } else {
+                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(c.o) + to + v;
+#pragma unroll
+                    for (int m = 0; m < 16; m += 8)
+                        if (there && v0 + v + m < c.V)
+                            *reinterpret_cast<uint4*>(p + m) =
+                                make_uint4(tc::pack_bf16(x[m], x[m + 1]), tc::pack_bf16(x[m + 2], x[m + 3]),
+                                           tc::pack_bf16(x[m + 4], x[m + 5]), tc::pack_bf16(x[m + 6], x[m + 7]));
+                }
             }
             tc::fence_before_sync();
             arrive_warp(&sm.o_free);
-            if (j < n) {
-                const size_t to = ((size_t)(z + j) * a.HV + h) * c.V + v0;
-                if (c.o_f32) {
-                    float* p = static_cast<float*>(c.o) + to;
-#pragma unroll
-                    for (int v = 0; v < VB; v += 4)
-                        if (v0 + v < c.V) *reinterpret_cast<float4*>(p + v) = make_float4(o[v], o[v + 1], o[v + 2], o[v + 3]);
-                } else {
-                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(c.o) + to;
-#pragma unroll
-                    for (int v = 0; v < VB; v += 8) {
-                        uint4 x;
-                        x.x = tc::pack_bf16(o[v], o[v + 1]);
-                        x.y = tc::pack_bf16(o[v + 2], o[v + 3]);
-                        x.z = tc::pack_bf16(o[v + 4], o[v + 5]);
-                        x.w = tc::pack_bf16(o[v + 6], o[v + 7]);
-                        if (v0 + v < c.V) *reinterpret_cast<uint4*>(p + v) = x;
-                    }
-                }
-            }
             return true;
         };
         int pn = 0;   // the previous chunk
         int64_t pz = 0;
-        for (Chunks k(a, row, t0, t1, c.back, LOCAL); k.more();) {
+        for (Chunks k(a, row, t0, t1, back, LOCAL); k.more();) {
             const int n = k.n();
             unsigned char* st = mem + stage * STAGE;
             if (!wait(sm, &sm.full[stage], fph)) break;
@@ -352,8 +357,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             unsigned char* vr = st + OFF_V + j * 128;
             unsigned char* to = mem + OFF_VP + j * 128;
             if (j < n) {
-                const float e = c.w * sm.pw[c.back ? j + 1 : n - 1 - j];
-#pragma unroll
+                const float e = c.w * sm.pw[back ? j + 1 : n - 1 - j];
+#pragma unroll 2
                 for (int ch = 0; ch < 8; ++ch) {
                     const uint32_t o = (ch ^ (j & 7)) << 4;
                     const uint4 v = *reinterpret_cast<const uint4*>(vr + o);
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 }
             } else {
                 const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
+#pragma unroll 1
                 for (int ch = 0; ch < 8; ++ch) {
                     *reinterpret_cast<uint4*>(vr + 16 * ch) = z;
 #pragma unroll
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         const int hq = h / c.gq, hk = h / c.gk, hv = h / c.gv;
         uint32_t stage = 0, eph = 1;
         int issued = 0;
-        for (Chunks k(a, row, t0, t1, c.back, LOCAL); k.more();) {
+        for (Chunks k(a, row, t0, t1, back, LOCAL); k.more();) {
             const int n = k.n(), z = (int)k.token(n);
             if (!wait(sm, &sm.empty[stage], eph)) break;   // (the phase before the first counts as complete)
             if (lane == 0) {
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         uint32_t stage = 0, fph = 0, ph = 0;
         bool first = true, ok = true;
         const uint64_t dvp = tc::sdesc_mn(base + OFF_VP, ATOM, 0), dsb = tc::sdesc_mn(base + OFF_S, ATOM, 0);
-        for (Chunks k(a, row, t0, t1, c.back, LOCAL); k.more();) {
+        for (Chunks k(a, row, t0, t1, back, LOCAL); k.more();) {
             const int n = k.n();
             const uint32_t st = base + stage * STAGE;
             const uint64_t dq = tc::sdesc_k(st, C, 0), dk = tc::sdesc_k(st + OFF_K, C, 0);

@@ -6,8 +6,8 @@
 //     P_ij = s w a^(j-i) (q_i k_j) for j >= i,   o_i = s a^(n-1-i) q_i S + sum_j P_ij v_j,   V'_j = w a^(j+1) v_j.
 // A CTA walks a head's 64 value columns through a time window; the serial chain from chunk to chunk is one multiply-add
 // per state element in registers, everything else runs ahead of it. Roles: one warp loads (TMA, two chunks deep), one
-// issues the four products Q K^T, Q S, K^T V' and P V, and three groups of four warps turn scores into P (TMEM to TMEM),
-// keep the state, and form V' and then write the previous chunk's outputs.
+// issues the four products Q K^T, Q S, K^T V' and P V, and three groups of four warps turn scores into P (TMEM to TMEM)
+// and then write the outputs, keep the state, and form V'.
 // Roundings: V' is three bf16 parts, 24 bits, so that the fp32 state is a sum of exact products (each chunk's is summed
 // by the tensor core from zero and added once); P and the copy of S that the queries meet are bf16; the output is
 // rounded once.
@@ -147,6 +147,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         const float sw = c.s * c.w;
         const uint32_t tp = tc::taddr(tb, q32, T_P), ts = tc::taddr(tb, q32, T_SC);
         const uint32_t tri = back ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);   // the diagonal block's columns that row i meets
+        if (blockIdx.x == 0 && blockIdx.y == 0 && a.err && a.ax.cu) {   // as axis_check, by these warps
+            bool bad = false;
+            for (int n = i; n < a.ax.N; n += 128) bad |= a.ax.cu[n + 1] < a.ax.cu[n];
+            if (i == 0) bad |= a.ax.cu[0] != 0 || a.ax.cu[a.ax.N] != a.ax.len;
+            if (bad) atomicOr(a.err, 1);
+        }
+        const uint32_t t1a = tc::taddr(tb, q32, T_O1), t2a = tc::taddr(tb, q32, T_O2);
         {
             uint32_t z[16];
 #pragma unroll
@@ -183,10 +190,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                     for (int m = 0; m < 32; m += 4) {
                         const float4 f = *reinterpret_cast<const float4*>(&sm.col[m]);
                         float* y = &x[m >> 4][m & 15];
-                        y[0] *= rowf * f.x;
-                        y[1] *= rowf * f.y;
-                        y[2] *= rowf * f.z;
-                        y[3] *= rowf * f.w;
+                        const float2 r = make_float2(rowf, rowf);
+                        const float2 lo = mul2(make_float2(y[0], y[1]), mul2(r, make_float2(f.x, f.y)));
+                        const float2 hi = mul2(make_float2(y[2], y[3]), mul2(r, make_float2(f.z, f.w)));
+                        y[0] = lo.x;
+                        y[1] = lo.y;
+                        y[2] = hi.x;
+                        y[3] = hi.y;
                     }
                     if (back && left < 32) {
 #pragma unroll
@@ -203,6 +213,43 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             if (lane == 0) {
                 tc::mbar_arrive(&sm.sc_free);
                 tc::mbar_arrive(&sm.p_full);
+            }
+            // the outputs
+            const bool there = i < n;
+            const float gam = c.s * sm.pw[there ? (back ? n - 1 - i : i + 1) : 0];
+            const size_t to = ((size_t)(k.token(n) + (there ? i : 0)) * a.HV + h) * c.V + v0;
+            if (!wait(sm, &sm.pv_done, ph)) break;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int v = 0; v < VB; v += 16) {
+                float x[16], y[16];
+                tc::tmem_ld16(t1a + v, x);
+                tc::tmem_ld16(t2a + v, y);
+                tc::tmem_wait_ld();
+                if (v == VB - 16) {
+                    tc::fence_before_sync();
+                    arrive_warp(&sm.o_free);
+                }
+#pragma unroll
+                for (int m = 0; m < 16; m += 2) {
+                    const float2 r = fma2(make_float2(gam, gam), make_float2(x[m], x[m + 1]), make_float2(y[m], y[m + 1]));
+                    x[m] = r.x;
+                    x[m + 1] = r.y;
+                }
+                if (c.o_f32) {
+                    float* p = static_cast<float*>(c.o) + to + v;
+#pragma unroll
+                    for (int m = 0; m < 16; m += 4)
+                        if (there && v0 + v + m < c.V) *reinterpret_cast<float4*>(p + m) = make_float4(x[m], x[m + 1], x[m + 2], x[m + 3]);
+                } else {
+                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(c.o) + to + v;
+#pragma unroll
+                    for (int m = 0; m < 16; m += 8)
+                        if (there && v0 + v + m < c.V)
+                            *reinterpret_cast<uint4*>(p + m) =
+                                make_uint4(tc::pack_bf16(x[m], x[m + 1]), tc::pack_bf16(x[m + 2], x[m + 3]),
+                                           tc::pack_bf16(x[m + 4], x[m + 5]), tc::pack_bf16(x[m + 6], x[m + 7]));
+                }
             }
             k.next(n);
         }
@@ -293,9 +340,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 for (int i = 0; i < 3; ++i) tc::tmem_ld8(tk + VB * i + v, x[i]);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float kv = x[0][i] + (x[1][i] + x[2][i]);
-                    S[v + i] = fmaf(S[v + i], an.x, fmaf(S[v + i], an.y, kv));
+                for (int i = 0; i < 8; i += 2) {
+                    float2 y = add2(make_float2(x[1][i], x[1][i + 1]), make_float2(x[2][i], x[2][i + 1]));
+                    y = add2(make_float2(x[0][i], x[0][i + 1]), y);
+                    const float2 z = make_float2(S[v + i], S[v + i + 1]);
+                    y = fma2(z, make_float2(an.x, an.x), fma2(z, make_float2(an.y, an.y), y));
+                    S[v + i] = y.x;
+                    S[v + i + 1] = y.y;
                 }
             }
             if (!LOCAL && k.t + n == k.s.end && c.s1) store_state(c.s1 + ((size_t)k.s.n * a.HV + h) * KV + mine);
@@ -306,54 +357,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         // ------------------------------------------------ V' in three parts, and outputs; this thread's token row
         const int j = q32 + lane;
         uint32_t ph = 0, stage = 0, fph = 0;
-        if (!LOCAL && blockIdx.x == 0 && blockIdx.y == 0 && a.err && a.ax.cu) {   // as axis_check, by this group
-            bool bad = false;
-            for (int n = j; n < a.ax.N; n += 128) bad |= a.ax.cu[n + 1] < a.ax.cu[n];
-            if (j == 0) bad |= a.ax.cu[0] != 0 || a.ax.cu[a.ax.N] != a.ax.len;
-            if (bad) atomicOr(a.err, 1);
-        }
-        const uint32_t t1a = tc::taddr(tb, q32, T_O1), t2a = tc::taddr(tb, q32, T_O2);
-        // The outputs of a chunk of n tokens from packed token z on.
-        auto output = [&](int n, int64_t z, uint32_t phase) {
-            const float gam = c.s * sm.pw[j < n ? (back ? n - 1 - j : j + 1) : 0];
-            if (!wait(sm, &sm.pv_done, phase)) return false;
-            tc::fence_after_sync();
-            const bool there = j < n;
-            const size_t to = ((size_t)(z + (there ? j : 0)) * a.HV + h) * c.V + v0;
-#pragma unroll 1
-            for (int v = 0; v < VB; v += 16) {
-                float x[16], y[16];
-                tc::tmem_ld16(t1a + v, x);
-                tc::tmem_ld16(t2a + v, y);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int m = 0; m < 16; ++m) x[m] = fmaf(gam, x[m], y[m]);
-                if (c.o_f32) {
-                    float* p = static_cast<float*>(c.o) + to + v;
-#pragma unroll
-                    for (int m = 0; m < 16; m += 4)
-                        if (there && v0 + v + m < c.V) *reinterpret_cast<float4*>(p + m) = make_float4(x[m], x[m + 1], x[m + 2], x[m + 3]);
-                } else {
-                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(c.o) + to + v;
-#pragma unroll
-                    for (int m = 0; m < 16; m += 8)
-                        if (there && v0 + v + m < c.V)
-                            *reinterpret_cast<uint4*>(p + m) =
-                                make_uint4(tc::pack_bf16(x[m], x[m + 1]), tc::pack_bf16(x[m + 2], x[m + 3]),
-                                           tc::pack_bf16(x[m + 4], x[m + 5]), tc::pack_bf16(x[m + 6], x[m + 7]));
-                }
-            }
-            tc::fence_before_sync();
-            arrive_warp(&sm.o_free);
-            return true;
-        };
-        int pn = 0;   // the previous chunk
-        int64_t pz = 0;
+        bool first = true;
         for (Chunks k(a, row, t0, t1, back, LOCAL); k.more();) {
             const int n = k.n();
             unsigned char* st = mem + stage * STAGE;
             if (!wait(sm, &sm.full[stage], fph)) break;
-            if (pn && !wait(sm, &sm.kv_done, ph ^ 1)) break;
+            if (!first && !wait(sm, &sm.kv_done, ph ^ 1)) break;
+            first = false;
             unsigned char* vr = st + OFF_V + j * 128;
             unsigned char* to = mem + OFF_VP + j * 128;
             if (j < n) {
@@ -366,12 +376,12 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                     uint32_t out[3][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float x = e * __uint_as_float(in[i] << 16), y = e * __uint_as_float(in[i] & 0xffff0000u);
+                        float2 x = mul2(make_float2(e, e), make_float2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)));
 #pragma unroll
-                        for (int p = 0; p < 3; ++p) {
-                            out[p][i] = tc::pack_bf16(x, y);
-                            x -= __uint_as_float(out[p][i] << 16);
-                            y -= __uint_as_float(out[p][i] & 0xffff0000u);
+                        for (int p = 0; p < 3; ++p) {   // the leading 8 bits of what is left, cut off: the third part is the rest
+                            const uint32_t lo = __float_as_uint(x.x), hi = __float_as_uint(x.y);
+                            out[p][i] = __byte_perm(lo, hi, 0x7632);
+                            x = add2(x, make_float2(-__uint_as_float(lo & 0xffff0000u), -__uint_as_float(hi & 0xffff0000u)));
                         }
                     }
 #pragma unroll
@@ -390,18 +400,11 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             }
             tc::fence_async_smem();
             arrive_warp(&sm.v_full);
-            if (!LOCAL && pn && !output(pn, pz, ph ^ 1)) {
-                pn = 0;
-                break;
-            }
-            pn = n;
-            pz = k.token(n);
             ph ^= 1;
             stage ^= 1;
             fph ^= stage == 0;
             k.next(n);
         }
-        if (!LOCAL && pn) output(pn, pz, ph ^ 1);
     } else if (warp == LOADER) {
         // ---------------------------------------------------------------- loads
         const CUtensorMap *mq = &g.map[g.mq[blockIdx.y]], *mk = &g.map[g.mk[blockIdx.y]], *mv = &g.map[g.mv[blockIdx.y]];

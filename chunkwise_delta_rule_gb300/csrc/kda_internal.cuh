@@ -40,6 +40,8 @@ bool tmap_rows_f32(CUtensorMap* m, const void* base, int Ttot, int H, int D, int
 // Token rows [tokens][H][D] of bf16, `ld` elements from token to token, in boxes of `rows` tokens x 64 columns of one
 // head, 128-byte swizzled; D and ld multiples of 8.
 bool tmap_tokens_bf16(CUtensorMap* m, const void* base, int64_t tokens, int H, int D, int64_t ld, int rows);
+// Contiguous fp32 rows [tokens][H][D] in boxes of `rows` tokens x 32 columns, 128-byte swizzled; D a multiple of 4.
+bool tmap_tokens_f32(CUtensorMap* m, const void* base, int64_t tokens, int H, int D, int rows);
 // fp32 states [NH][K][V] in boxes of 32 keys x 32 value columns, 128-byte swizzled (K, V multiples of
 // 32; false when the base is not 16-byte aligned).
 bool tmap_state_f32(CUtensorMap* m, const float* base, int NH, int K, int V);

@@ -9,7 +9,7 @@
 // issues the four products Q K^T, Q S, K^T V' and P V, and three groups of four warps turn scores into P (TMEM to TMEM)
 // and then write the outputs, keep the state, and form V'.
 // Roundings: V' is three bf16 parts, 24 bits, so that the fp32 state is a sum of exact products (each chunk's is summed
-// by the tensor core from zero and added once); P and the copy of S that the queries meet are bf16; the output is
+// by the tensor core from zero and added once), or two, 2^-17, in calls that return no state; P and the copy of S that the queries meet are bf16; the output is
 // rounded once.
 // Powers of a: |i - j| = (i - block end) + (block end - j) for columns left of the row's block of 32, so that a score
 // costs two products and no exponential; on the diagonal block a row's 32 powers stay in registers.
@@ -31,8 +31,7 @@ constexpr int T_SC = 0, T_P = 128, T_O1 = 192, T_O2 = 256, T_KV = 320;   // TMEM
 struct Shared {
     float pw[C + 1];            // a^m
     alignas(16) float col[32];  // a block's column's power: to the block's end forwards, from its start backwards
-    float2 an;                  // a^C in two parts
-    uint64_t full[2], empty[2], sc_full, sc_free, p_full, pv_done, v_full, kv_done, s_full, o_free, drain;
+    uint64_t full[2], k_free[2], v_free[2], o_ready[2], sc_full, sc_free, p_full, pv_done, v_full, kv_done, s_full, o_free, drain;
     uint32_t tmem;
     int dead;
 };
@@ -40,7 +39,7 @@ constexpr int SMEM = OFF_END + (int)sizeof(Shared) + 1024;
 static_assert(SMEM <= 232448, "shared memory above the per-block limit");
 
 struct LinTc {
-    CUtensorMap map[4];
+    CUtensorMap map[4], out[3];
     LinArgs a;
     int mq[3], mk[3], mv[3];    // each call's maps
 };
@@ -86,8 +85,8 @@ struct Chunks {
     }
 };
 
-// LOCAL: the end states of the windows' own tokens only.
-template <bool LOCAL>
+// LOCAL: the end states of the windows' own tokens only. NP: parts of V'.
+template <bool LOCAL, int NP>
 __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinTc g) {
     extern __shared__ unsigned char raw[];
     const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
@@ -107,31 +106,55 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
     const int KA = c.K > 64 ? 2 : 1;
     const float decay = a.decay ? a.decay[h] : 0.f;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&sm.full[i], 1);
-            tc::mbar_init(&sm.empty[i], 1);
+    const bool back = c.back != 0;
+
+    // The loader's copies of one chunk (lane 0); they arrive together. The first two chunks' start here.
+    const CUtensorMap *mq = &g.map[g.mq[blockIdx.y]], *mk = &g.map[g.mk[blockIdx.y]], *mv = &g.map[g.mv[blockIdx.y]];
+    const int hq = h / c.gq, hk = h / c.gk, hv = h / c.gv;
+    const auto load_q = [&](int st, int z) {
+        for (int p = 0; p < (LOCAL ? 0 : KA); ++p) tc::tma_load3(base + st * STAGE + p * ATOM, mq, 64 * p, hq, z, &sm.full[st]);
+    };
+    const auto load_k = [&](int st, int z) {
+        tc::mbar_arrive_expect_tx(&sm.full[st], ((LOCAL ? 1 : 2) * KA + 1) * ATOM);
+        for (int p = 0; p < KA; ++p) tc::tma_load3(base + st * STAGE + OFF_K + p * ATOM, mk, 64 * p, hk, z, &sm.full[st]);
+    };
+    const auto load_v = [&](int st, int z) { tc::tma_load3(base + st * STAGE + OFF_V, mv, v0, hv, z, &sm.full[st]); };
+    if (warp == LOADER) {
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i) {
+                tc::mbar_init(&sm.full[i], 1);
+                tc::mbar_init(&sm.k_free[i], 1);
+                tc::mbar_init(&sm.v_free[i], 1);
+                tc::mbar_init(&sm.o_ready[i], 4);
+            }
+            tc::mbar_init(&sm.sc_full, 1);
+            tc::mbar_init(&sm.pv_done, 1);
+            tc::mbar_init(&sm.kv_done, 1);
+            tc::mbar_init(&sm.drain, 1);
+            tc::mbar_init(&sm.sc_free, 4);
+            tc::mbar_init(&sm.p_full, 4);
+            tc::mbar_init(&sm.v_full, 4);
+            tc::mbar_init(&sm.s_full, 4);
+            tc::mbar_init(&sm.o_free, 4);
+            sm.dead = 0;
+            tc::fence_mbar_init();
+            Chunks k(a, row, t0, t1, back, LOCAL);
+            for (int i = 0; i < 2 && k.more(); ++i) {
+                const int n = k.n(), z = (int)k.token(n);
+                load_k(i, z);
+                load_q(i, z);
+                load_v(i, z);
+                k.next(n);
+            }
         }
-        tc::mbar_init(&sm.sc_full, 1);
-        tc::mbar_init(&sm.pv_done, 1);
-        tc::mbar_init(&sm.kv_done, 1);
-        tc::mbar_init(&sm.drain, 1);
-        tc::mbar_init(&sm.sc_free, 4);
-        tc::mbar_init(&sm.p_full, 4);
-        tc::mbar_init(&sm.v_full, 4);
-        tc::mbar_init(&sm.s_full, 4);
-        tc::mbar_init(&sm.o_free, 4);
-        sm.dead = 0;
-        tc::fence_mbar_init();
+        __syncwarp();
     }
     if (warp == ISSUER) {
         tc::tmem_alloc(&sm.tmem, 512);
         tc::tmem_relinquish();
     }
-    const bool back = c.back != 0;
     for (int m = threadIdx.x; m <= C; m += NTHR) sm.pw[m] = lin_power(decay, m);
     if (threadIdx.x < 32) sm.col[threadIdx.x] = lin_power(decay, back ? threadIdx.x : 31 - threadIdx.x);
-    if (threadIdx.x == LOADER * 32) sm.an = lin_power2(decay, C);
     if (KA == 1)   // the second half of the key rows: nothing, in every chunk
         for (int i = threadIdx.x; i < 2 * ATOM / 16; i += NTHR)
             *reinterpret_cast<uint4*>(mem + (i >= ATOM / 16) * STAGE + OFF_K + ATOM + i % (ATOM / 16) * 16) = make_uint4(0, 0, 0, 0);
@@ -161,8 +184,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             for (int b = 0; b < 4; ++b) tc::tmem_st16u(tp + 16 * b, z);
             tc::tmem_wait_st();
         }
-        uint32_t ph = 0;
-        for (Chunks k(a, row, t0, t1, back, false); k.more(); ph ^= 1) {
+        uint32_t ph = 0, stage = 0;
+        for (Chunks k(a, row, t0, t1, back, false); k.more(); ph ^= 1, stage ^= 1) {
             const int n = k.n();
             if (!wait(sm, &sm.sc_full, ph)) break;
             tc::fence_after_sync();
@@ -214,8 +237,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 tc::mbar_arrive(&sm.sc_free);
                 tc::mbar_arrive(&sm.p_full);
             }
-            // the outputs
-            const bool there = i < n;
+            // The outputs: a whole chunk's go through the tile of its queries, which every product has read, to one copy by
+            // the loader; others row by row, as the rows behind the chunk are another sequence's.
+            const bool there = i < n, whole = n == C;
+            unsigned char* tile = mem + stage * STAGE + i * 128;
             const float gam = c.s * sm.pw[there ? (back ? n - 1 - i : i + 1) : 0];
             const size_t to = ((size_t)(k.token(n) + (there ? i : 0)) * a.HV + h) * c.V + v0;
             if (!wait(sm, &sm.pv_done, ph)) break;
@@ -236,7 +261,20 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                     x[m] = r.x;
                     x[m + 1] = r.y;
                 }
-                if (c.o_f32) {
+                uint32_t bits[8];
+#pragma unroll
+                for (int m = 0; m < 8; ++m) bits[m] = tc::pack_bf16(x[2 * m], x[2 * m + 1]);
+                if (whole && !c.o_f32) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+                        *reinterpret_cast<uint4*>(tile + (((v / 8 + m) ^ (i & 7)) << 4)) =
+                            make_uint4(bits[4 * m], bits[4 * m + 1], bits[4 * m + 2], bits[4 * m + 3]);
+                } else if (whole) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        *reinterpret_cast<float4*>(tile + v / 32 * ATOM + (((v % 32 / 4 + m) ^ (i & 7)) << 4)) =
+                            make_float4(x[4 * m], x[4 * m + 1], x[4 * m + 2], x[4 * m + 3]);
+                } else if (c.o_f32) {
                     float* p = static_cast<float*>(c.o) + to + v;
 #pragma unroll
                     for (int m = 0; m < 16; m += 4)
@@ -244,13 +282,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 } else {
                     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(c.o) + to + v;
 #pragma unroll
-                    for (int m = 0; m < 16; m += 8)
-                        if (there && v0 + v + m < c.V)
-                            *reinterpret_cast<uint4*>(p + m) =
-                                make_uint4(tc::pack_bf16(x[m], x[m + 1]), tc::pack_bf16(x[m + 2], x[m + 3]),
-                                           tc::pack_bf16(x[m + 4], x[m + 5]), tc::pack_bf16(x[m + 6], x[m + 7]));
+                    for (int m = 0; m < 2; ++m)
+                        if (there && v0 + v + 8 * m < c.V)
+                            *reinterpret_cast<uint4*>(p + 8 * m) = make_uint4(bits[4 * m], bits[4 * m + 1], bits[4 * m + 2], bits[4 * m + 3]);
                 }
             }
+            if (whole) tc::fence_async_smem();
+            arrive_warp(&sm.o_ready[stage]);
             k.next(n);
         }
     } else if (role == 1) {
@@ -280,6 +318,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 }
             }
         };
+        float2 whole;   // a^C
+        if (lane == 0) whole = lin_power2(decay, C);
+        whole.x = __shfl_sync(0xffffffffu, whole.x, 0);
+        whole.y = __shfl_sync(0xffffffffu, whole.y, 0);
         uint32_t ph = 0;
         int seq = -1;
         const uint32_t tk = tc::taddr(tb, q32, T_KV);
@@ -332,16 +374,17 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             arrive_warp(&sm.s_full);
             if (!wait(sm, &sm.kv_done, ph)) break;
             tc::fence_after_sync();
-            const float2 an = n == C ? sm.an : make_float2(sm.pw[n], 0.f);
+            const float2 an = n == C ? whole : make_float2(sm.pw[n], 0.f);
 #pragma unroll
             for (int v = 0; v < VB; v += 8) {
-                float x[3][8];
+                float x[NP][8];
 #pragma unroll
-                for (int i = 0; i < 3; ++i) tc::tmem_ld8(tk + VB * i + v, x[i]);
+                for (int i = 0; i < NP; ++i) tc::tmem_ld8(tk + VB * i + v, x[i]);
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
-                    float2 y = add2(make_float2(x[1][i], x[1][i + 1]), make_float2(x[2][i], x[2][i + 1]));
+                    float2 y = make_float2(x[1][i], x[1][i + 1]);
+                    if (NP == 3) y = add2(y, make_float2(x[NP - 1][i], x[NP - 1][i + 1]));
                     y = add2(make_float2(x[0][i], x[0][i + 1]), y);
                     const float2 z = make_float2(S[v + i], S[v + i + 1]);
                     y = fma2(z, make_float2(an.x, an.x), fma2(z, make_float2(an.y, an.y), y));
@@ -373,19 +416,19 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                     const uint32_t o = (ch ^ (j & 7)) << 4;
                     const uint4 v = *reinterpret_cast<const uint4*>(vr + o);
                     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t out[3][4];
+                    uint32_t out[NP][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float2 x = mul2(make_float2(e, e), make_float2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)));
 #pragma unroll
-                        for (int p = 0; p < 3; ++p) {   // the leading 8 bits of what is left, cut off: the third part is the rest
+                        for (int p = 0; p < NP; ++p) {   // the leading 8 bits of what is left, cut off: the third part is the rest
                             const uint32_t lo = __float_as_uint(x.x), hi = __float_as_uint(x.y);
-                            out[p][i] = __byte_perm(lo, hi, 0x7632);
+                            out[p][i] = p == NP - 1 ? tc::pack_bf16(x.x, x.y) : __byte_perm(lo, hi, 0x7632);
                             x = add2(x, make_float2(-__uint_as_float(lo & 0xffff0000u), -__uint_as_float(hi & 0xffff0000u)));
                         }
                     }
 #pragma unroll
-                    for (int p = 0; p < 3; ++p)
+                    for (int p = 0; p < NP; ++p)
                         *reinterpret_cast<uint4*>(to + p * ATOM + o) = make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
                 }
             } else {
@@ -394,7 +437,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 for (int ch = 0; ch < 8; ++ch) {
                     *reinterpret_cast<uint4*>(vr + 16 * ch) = z;
 #pragma unroll
-                    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(to + p * ATOM + 16 * ch) = z;
+                    for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(to + p * ATOM + 16 * ch) = z;
                     for (int p = 0; p < KA; ++p) *reinterpret_cast<uint4*>(st + OFF_K + p * ATOM + j * 128 + 16 * ch) = z;
                 }
             }
@@ -406,34 +449,55 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             k.next(n);
         }
     } else if (warp == LOADER) {
-        // ---------------------------------------------------------------- loads
-        const CUtensorMap *mq = &g.map[g.mq[blockIdx.y]], *mk = &g.map[g.mk[blockIdx.y]], *mv = &g.map[g.mv[blockIdx.y]];
-        const int hq = h / c.gq, hk = h / c.gk, hv = h / c.gv;
-        uint32_t stage = 0, eph = 1;
-        int issued = 0;
-        for (Chunks k(a, row, t0, t1, back, LOCAL); k.more();) {
-            const int n = k.n(), z = (int)k.token(n);
-            if (!wait(sm, &sm.empty[stage], eph)) break;   // (the phase before the first counts as complete)
-            if (lane == 0) {
-                const uint32_t d = base + stage * STAGE;
-                tc::mbar_arrive_expect_tx(&sm.full[stage], ((LOCAL ? 1 : 2) * KA + 1) * ATOM);
-                for (int p = 0; p < KA; ++p) {
-                    tc::tma_load3(d + OFF_K + p * ATOM, mk, 64 * p, hk, z, &sm.full[stage]);
-                    if (!LOCAL) tc::tma_load3(d + p * ATOM, mq, 64 * p, hq, z, &sm.full[stage]);
-                }
-                tc::tma_load3(d + OFF_V, mv, v0, hv, z, &sm.full[stage]);
+        // ------------------------------------------------ loads, from the third chunk on, and whole chunks' outputs
+        int n1 = 0, n2 = 0, z1 = 0, z2 = 0, issued = 0;   // the last two chunks' tokens and first rows
+        const auto give = [&](int i, int n, int z) {      // the outputs of chunk i
+            if (LOCAL) return true;
+            if (!wait(sm, &sm.o_ready[i & 1], (i >> 1) & 1)) return false;
+            if (n == C && lane == 0) {
+                const uint32_t tile = base + (i & 1) * STAGE;
+                const CUtensorMap* mo = &g.out[blockIdx.y];
+                tc::tma_store3(mo, v0, h, z, tile);
+                if (c.o_f32 && v0 + 32 < c.V) tc::tma_store3(mo, v0 + 32, h, z, tile + ATOM);
+                tc::bulk_commit();
+                tc::bulk_wait_read();
             }
             __syncwarp();
-            ++issued;
-            stage ^= 1;
-            eph ^= stage == 0;
+            return true;
+        };
+        bool ok = true;
+        Chunks k(a, row, t0, t1, back, LOCAL);
+        for (; k.more(); ++issued) {
+            const int n = k.n(), z = (int)k.token(n), st = issued & 1;
+            if (issued > 1) {
+                const uint32_t ph = ((issued >> 1) - 1) & 1;
+                if (!LOCAL && lane < KA) tc::tma_prefetch3(mq, 64 * lane, hq, z);   // their place is free last
+                if (!(ok = wait(sm, &sm.k_free[st], ph))) break;
+                if (lane == 0) load_k(st, z);
+                ok = wait(sm, &sm.v_free[st], ph);
+                if (lane == 0) load_v(st, z);   // (the chunk's bytes are announced: all its copies are made)
+                ok = give(issued - 2, n2, z2) && ok;
+                if (lane == 0) load_q(st, z);
+                __syncwarp();
+            }
+            n2 = n1;
+            z2 = z1;
+            n1 = n;
+            z1 = z;
+            if (!ok) {
+                ++issued;
+                break;
+            }
             k.next(n);
         }
+        if (ok && issued > 1) ok = give(issued - 2, n2, z2);
+        if (ok && issued > 0) ok = give(issued - 1, n1, z1);
         // no copy is in flight when the CTA ends, after a failure either
+        if (lane == 0) tc::bulk_wait_all();
         for (int i = max(0, issued - 2); i < issued; ++i) tc::mbar_wait(&sm.full[i & 1], (i >> 1) & 1);
     } else if (warp == ISSUER) {
         // ---------------------------------------------------------------- products
-        constexpr uint32_t I_SC = tc::idesc_bf16(C, C), I_O = tc::idesc_bf16_bmn(C, VB), I_KV = tc::idesc_bf16_abmn(C, 3 * VB);
+        constexpr uint32_t I_SC = tc::idesc_bf16(C, C), I_O = tc::idesc_bf16_bmn(C, VB), I_KV = tc::idesc_bf16_abmn(C, NP * VB);
         uint32_t stage = 0, fph = 0, ph = 0;
         bool first = true, ok = true;
         const uint64_t dvp = tc::sdesc_mn(base + OFF_VP, ATOM, 0), dsb = tc::sdesc_mn(base + OFF_S, ATOM, 0);
@@ -465,6 +529,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             for (int s = 0; s < C / 16; ++s)
                 tc::mma_bf16_w(tb + T_KV, tc::kstep_mn(dkt, s), tc::kstep_mn(dvp, s), I_KV, s > 0);
             tc::mma_commit_w(&sm.kv_done);
+            tc::mma_commit_w(&sm.k_free[stage]);
             if (!LOCAL) {
                 ok = wait(sm, &sm.p_full, ph);
                 if (!ok) break;
@@ -473,7 +538,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                     tc::mma_bf16_ts_w(tb + T_O2, tb + T_P + 8 * s, tc::kstep_mn(dv, s), I_O, s > 0);
                 tc::mma_commit_w(&sm.pv_done);
             }
-            tc::mma_commit_w(&sm.empty[stage]);
+            tc::mma_commit_w(&sm.v_free[stage]);
             first = false;
             ph ^= 1;
             stage ^= 1;
@@ -491,17 +556,25 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
     if (warp == ISSUER) tc::tmem_dealloc(tb, 512);
 }
 
-template <bool LOCAL>
+template <bool LOCAL, int NP>
 cudaError_t run(const LinTc& g, cudaStream_t st) {
     static SmemLimit limit;
-    const cudaError_t e = limit.set(reinterpret_cast<const void*>(&k_lin_tc<LOCAL>), SMEM);
+    const cudaError_t e = limit.set(reinterpret_cast<const void*>(&k_lin_tc<LOCAL, NP>), SMEM);
     if (e != cudaSuccess) return e;
     int vmax = 1;
     for (int i = 0; i < g.a.calls; ++i) vmax = g.a.c[i].V > vmax ? g.a.c[i].V : vmax;
     const long long ctas = (long long)g.a.ax.rows * g.a.units_row * g.a.HV * ((vmax + VB - 1) / VB);
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return traced_launch(LOCAL ? "k_lin_tc_windows" : "k_lin_tc", st,
-                         [&] { k_lin_tc<LOCAL><<<dim3((unsigned)ctas, g.a.calls), NTHR, SMEM, st>>>(g); });
+                         [&] { k_lin_tc<LOCAL, NP><<<dim3((unsigned)ctas, g.a.calls), NTHR, SMEM, st>>>(g); });
+}
+template <int NP>
+cudaError_t run_both(const LinTc& g, cudaStream_t st) {
+    if (g.a.units_row > 1) {
+        const cudaError_t e = run<true, NP>(g, st);
+        if (e != cudaSuccess) return e;
+    }
+    return run<false, NP>(g, st);
 }
 
 }  // namespace
@@ -548,12 +621,12 @@ cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st) {
         const LinCall& c = a.c[i];
         if (!map(c.q, c.ldq, c.gq, c.K, g.mq[i]) || !map(c.k, c.ldk, c.gk, c.K, g.mk[i]) || !map(c.v, c.ldv, c.gv, c.V, g.mv[i]))
             return cudaErrorInvalidValue;
+        if (!(c.o_f32 ? tmap_tokens_f32(&g.out[i], c.o, tokens, a.HV, c.V, C) : tmap_tokens_bf16(&g.out[i], c.o, tokens, a.HV, c.V, (int64_t)a.HV * c.V, C)))
+            return cudaErrorInvalidValue;
     }
-    if (a.units_row > 1) {
-        const cudaError_t e = run<true>(g, st);
-        if (e != cudaSuccess) return e;
-    }
-    return run<false>(g, st);
+    bool states = false;   // they are fp32 results: all their bits are kept
+    for (int i = 0; i < a.calls; ++i) states = states || a.c[i].s1;
+    return states ? run_both<3>(g, st) : run_both<2>(g, st);
 }
 
 }  // namespace kda

@@ -43,6 +43,22 @@ bool encode(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Boxes of `rows` tokens x 128 bytes of one head's row, swizzled.
+bool encode_tokens(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base, int64_t tokens, int H, int D, int64_t ld,
+                   int rows) {
+    auto fn = encode_fn();
+    if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15)) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * esize, (cuuint64_t)ld * esize};
+    const cuuint32_t box[3] = {128u / esize, 1u, (cuuint32_t)rows};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    const auto encode = [&] {
+        return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return encode() || (bind_context() && encode());
+}
+
 }  // namespace
 
 bool tmap_rows_bf16(CUtensorMap* m, const void* base, int Ttot, int H, int D) {
@@ -50,18 +66,11 @@ bool tmap_rows_bf16(CUtensorMap* m, const void* base, int Ttot, int H, int D) {
 }
 
 bool tmap_tokens_bf16(CUtensorMap* m, const void* base, int64_t tokens, int H, int D, int64_t ld, int rows) {
-    auto fn = encode_fn();
-    if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15)) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
-    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)rows};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    const auto encode = [&] {
-        return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    };
-    return encode() || (bind_context() && encode());
+    return encode_tokens(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, tokens, H, D, ld, rows);
+}
+
+bool tmap_tokens_f32(CUtensorMap* m, const void* base, int64_t tokens, int H, int D, int rows) {
+    return encode_tokens(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, tokens, H, D, (int64_t)H * D, rows);
 }
 
 bool tmap_state_f32(CUtensorMap* m, const float* base, int NH, int K, int V) {

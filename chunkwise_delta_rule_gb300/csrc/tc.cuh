@@ -149,6 +149,13 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, 
         : "memory");
 }
 
+// Asks for that box to be brought into L2.
+__device__ __forceinline__ void tma_prefetch3(const CUtensorMap* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 // TMA store of one box of a 3-D tensor map at (x, y, z) from shared memory
 // (laid out as the map's swizzle expects), in this thread's bulk group. The
 // box is written whole: use it only where every row of the box is the caller's.

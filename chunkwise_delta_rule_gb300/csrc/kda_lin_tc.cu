@@ -510,8 +510,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 if (ok && !first) ok = wait(sm, &sm.sc_free, ph ^ 1);
                 if (!ok) break;
                 tc::fence_after_sync();
-                for (int s = 0; s < 4 * KA; ++s)
-                    tc::mma_bf16_w(tb + T_SC, tc::kstep_k(dq, C, s), tc::kstep_k(dk, C, s), I_SC, s > 0);
+                tc::mma4_bf16_w<false, false>(tb + T_SC, dq, dk, I_SC, 0);
+                if (KA > 1) tc::mma4_bf16_w<false, false>(tb + T_SC, tc::kstep_k(dq, C, 4), tc::kstep_k(dk, C, 4), I_SC, 1);
                 tc::mma_commit_w(&sm.sc_full);
             }
             ok = ok && wait(sm, &sm.s_full, ph);
@@ -519,23 +519,23 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             if (!ok) break;
             tc::fence_after_sync();
             if (!LOCAL) {
-                for (int s = 0; s < 4 * KA; ++s)
-                    tc::mma_bf16_w(tb + T_O1, tc::kstep_k(dq, C, s), tc::kstep_mn(dsb, s), I_O, s > 0);
+                tc::mma4_bf16_w<false, true>(tb + T_O1, dq, dsb, I_O, 0);
+                if (KA > 1) tc::mma4_bf16_w<false, true>(tb + T_O1, tc::kstep_k(dq, C, 4), tc::kstep_mn(dsb, 4), I_O, 1);
             }
             ok = wait(sm, &sm.v_full, ph);
             if (!ok) break;
             tc::fence_after_sync();
             const uint64_t dkt = tc::sdesc_mn(st + OFF_K, ATOM, 0), dv = tc::sdesc_mn(st + OFF_V, ATOM, 0);
-            for (int s = 0; s < C / 16; ++s)
-                tc::mma_bf16_w(tb + T_KV, tc::kstep_mn(dkt, s), tc::kstep_mn(dvp, s), I_KV, s > 0);
+            tc::mma4_bf16_w<true, true>(tb + T_KV, dkt, dvp, I_KV, 0);
+            tc::mma4_bf16_w<true, true>(tb + T_KV, tc::kstep_mn(dkt, 4), tc::kstep_mn(dvp, 4), I_KV, 1);
             tc::mma_commit_w(&sm.kv_done);
             tc::mma_commit_w(&sm.k_free[stage]);
             if (!LOCAL) {
                 ok = wait(sm, &sm.p_full, ph);
                 if (!ok) break;
                 tc::fence_after_sync();
-                for (int s = 0; s < C / 16; ++s)
-                    tc::mma_bf16_ts_w(tb + T_O2, tb + T_P + 8 * s, tc::kstep_mn(dv, s), I_O, s > 0);
+                tc::mma4_bf16_ts_w(tb + T_O2, tb + T_P, dv, I_O, 0);
+                tc::mma4_bf16_ts_w(tb + T_O2, tb + T_P + 32, tc::kstep_mn(dv, 4), I_O, 1);
                 tc::mma_commit_w(&sm.pv_done);
             }
             tc::mma_commit_w(&sm.v_free[stage]);

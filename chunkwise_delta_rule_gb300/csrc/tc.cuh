@@ -362,6 +362,34 @@ __device__ __forceinline__ void mma_tf32_ts_w(uint32_t d, uint32_t a, uint64_t b
         "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
+// Four k-steps (K = 64 bf16) of one product from its first step's descriptors (a TMEM address for A in TMEM), one choice
+// of a lane for all: a step issued by itself, with its own descriptors' arithmetic, costs some 110 cycles of the
+// issuing warp, more than most steps run. AMN, BMN: MN-major operands.
+template <bool AMN, bool BMN>
+__device__ __forceinline__ void mma4_bf16_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    constexpr int SA = AMN ? 128 : 2, SB = BMN ? 128 : 2;
+    asm volatile(
+        "{\n\t.reg .pred e, p, yes;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %8;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t"
+        "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %9;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t"
+        "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %10;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(SA), "n"(2 * SA), "n"(3 * SA), "n"(SB), "n"(2 * SB), "n"(3 * SB)
+        : "memory");
+}
+// A in TMEM, B MN-major.
+__device__ __forceinline__ void mma4_bf16_ts_w(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, yes;\n\t.reg .b32 x;\n\t.reg .b64 y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.s32 x, %1, 8;\n\tadd.s64 y, %2, 128;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, yes;\n\t"
+        "add.s32 x, %1, 16;\n\tadd.s64 y, %2, 256;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, yes;\n\t"
+        "add.s32 x, %1, 24;\n\tadd.s64 y, %2, 384;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, yes;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
 __device__ __forceinline__ void mma_commit_w(uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"

@@ -27,6 +27,8 @@ struct Mm8Args {
     void* y;
     int32_t* err;
 };
-cudaError_t launch_mm8(const Mm8Args& a, cudaStream_t st);
+// Bytes of workspace: copies of operands whose rows do not start every 16 bytes.
+size_t mm8_align_bytes(const Mm8Args& a);
+cudaError_t launch_mm8(Mm8Args a, void* ws, cudaStream_t st);
 
 }  // namespace kda

@@ -7,7 +7,7 @@ namespace {
 
 using namespace kda::api;
 
-constexpr int MAX_ROWS = 1 << 22, MAX_COLS = 1 << 20;   // a grid has at most 65535 tiles of 64 or 128 rows on its second axis
+constexpr int MAX_ROWS = 1 << 22, MAX_COLS = 1 << 20;   // a grid has at most 65535 tiles of 128 rows on its second and third axes
 
 kda_status quant8_args(const kda_quant8_problem* p, kda::Quant8Args& a) {
     if (!p) return fail(KDA_ERR_INVALID_ARG, "problem is NULL");
@@ -74,8 +74,7 @@ kda_status kda_quant8(const kda_quant8_problem* p, void* q, float* scale, void* 
 
 size_t kda_mm8_workspace_size(const kda_mm8_problem* p) {
     kda::Mm8Args a;
-    if (mm8_args(p, a) != KDA_OK) return 0;
-    return 0;
+    return mm8_args(p, a) == KDA_OK ? up(kda::mm8_align_bytes(a)) : 0;
 }
 
 kda_status kda_mm8(const kda_mm8_problem* p, void* y, void* ws, size_t ws_bytes, int32_t* err, kda_stream_t stream) {
@@ -87,7 +86,7 @@ kda_status kda_mm8(const kda_mm8_problem* p, void* y, void* ws, size_t ws_bytes,
     if ((st = check_ws(ws, ws_bytes, kda_mm8_workspace_size(p), "workspace")) != KDA_OK) return st;
     a.y = y;
     a.err = err;
-    return cuda_result(kda::launch_mm8(a, reinterpret_cast<cudaStream_t>(stream)), "8-bit product");
+    return cuda_result(kda::launch_mm8(a, ws, reinterpret_cast<cudaStream_t>(stream)), "8-bit product");
 }
 
 }  // extern "C"

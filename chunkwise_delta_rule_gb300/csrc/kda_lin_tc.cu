@@ -44,22 +44,7 @@ struct LinTc {
     int mq[3], mk[3], mv[3];    // each call's maps
 };
 
-// A whole warp waits for a phase; false once a wait of the CTA gave up (about 1 s).
-__device__ __forceinline__ bool wait(Shared& sm, uint64_t* bar, uint32_t parity) {
-    bool ok = tc::mbar_try_wait(bar, parity);
-    if (!ok) {
-        const uint64_t t0 = tc::global_ns();
-        for (uint32_t i = 1; !(ok = tc::mbar_try_wait(bar, parity)); ++i)
-            if ((i & 63u) == 0 && (*reinterpret_cast<volatile int*>(&sm.dead) || tc::global_ns() - t0 > 1000000000ull)) break;
-        if (!ok) *reinterpret_cast<volatile int*>(&sm.dead) = 1;
-    }
-    return __all_sync(0xffffffffu, ok);   // a warp goes one way
-}
-// One arrival per warp, after all its lanes.
-__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
-}
+__device__ __forceinline__ bool wait(Shared& sm, uint64_t* bar, uint32_t parity) { return tc::warp_wait(bar, parity, &sm.dead); }
 
 // The chunks of a window, the same for every role.
 struct Chunks {
@@ -253,7 +238,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 tc::tmem_wait_ld();
                 if (v == VB - 16) {
                     tc::fence_before_sync();
-                    arrive_warp(&sm.o_free);
+                    tc::warp_arrive(&sm.o_free);
                 }
 #pragma unroll
                 for (int m = 0; m < 16; m += 2) {
@@ -288,7 +273,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 }
             }
             if (whole) tc::fence_async_smem();
-            arrive_warp(&sm.o_ready[stage]);
+            tc::warp_arrive(&sm.o_ready[stage]);
             k.next(n);
         }
     } else if (role == 1) {
@@ -371,7 +356,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 tc::fence_async_smem();
             }
             tc::fence_before_sync();
-            arrive_warp(&sm.s_full);
+            tc::warp_arrive(&sm.s_full);
             if (!wait(sm, &sm.kv_done, ph)) break;
             tc::fence_after_sync();
             const float2 an = n == C ? whole : make_float2(sm.pw[n], 0.f);
@@ -442,7 +427,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 }
             }
             tc::fence_async_smem();
-            arrive_warp(&sm.v_full);
+            tc::warp_arrive(&sm.v_full);
             ph ^= 1;
             stage ^= 1;
             fph ^= stage == 0;

@@ -1,68 +1,294 @@
-// Matrix product of e4m3 values with a scale for each 128 columns (include/kda.h), on CUDA cores:
+// Matrix product of e4m3 values with a scale for each 128 columns (include/kda.h):
 //     y[m, n] = sum_g sa[m, g] sb[n, g] sum_{c in g} a[m, c] b[n, c].
-// A group's sum is formed in fp32, then scaled and added to the output's.
+// The scales vary along the contraction, so the tensor core sums one group at a time (four steps of K = 32 bytes, from
+// zero, in TMEM) and warps add it, scaled, to the output's sums in registers, while the next groups are summed.
+//
+// Few rows, k_mm8_rows: the tensor core's 128 rows are rows of b, its N are TN rows of a (16 to 128), so that the
+// weights go once through the SM whatever the number of tokens; the contraction is cut over a cluster of up to 8 CTAs,
+// whose sums meet in shared memory, in order.
 #include "kda_fp8.cuh"
+#include "tc.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int NT = 256, TM = 64, TK = 32;
+constexpr int G = FP8_GROUP;
 
-__device__ __forceinline__ float value(uint8_t x) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(x, __NV_E4M3)));
+struct Maps {
+    CUtensorMap a, b;
+};
+
+// ------------------------------------------------------------------ rows that no tensor map takes
+// Rows of K bytes, ld apart, to rows `pitch` apart (a multiple of 16; the bytes behind K are never read).
+__global__ void __launch_bounds__(256) k_mm8_align(const uint8_t* src, int64_t ld, uint8_t* dst, int64_t pitch, int K) {
+    const uint8_t* s = src + (int64_t)blockIdx.x * ld;
+    uint8_t* d = dst + (int64_t)blockIdx.x * pitch;
+    for (int c = threadIdx.x * 4; c < K; c += 1024) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w |= (c + i < K ? (uint32_t)s[c + i] : 0u) << (8 * i);
+        *reinterpret_cast<uint32_t*>(d + c) = w;
+    }
 }
 
-__global__ void __launch_bounds__(NT) k_mm8(Mm8Args a) {
-    __shared__ __align__(16) float as[TK][TM + 4], bs[TK][TM + 4];
-    const int m0 = blockIdx.x * TM, n0 = blockIdx.y * TM, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {}, part[4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += TK) {
-        __syncthreads();
-        for (int x = threadIdx.x; x < TM * TK; x += NT) {
-            const int r = x / TK, c = x - r * TK;
-            as[c][r] = m0 + r < a.M && k0 + c < a.K ? value(a.a[(int64_t)(m0 + r) * a.lda + k0 + c]) : 0.f;
-            bs[c][r] = n0 + r < a.N && k0 + c < a.K ? value(a.b[(int64_t)(n0 + r) * a.ldb + k0 + c]) : 0.f;
+// ------------------------------------------------------------------ few rows of a
+constexpr int SB = 8;   // groups of scales brought in at a time
+
+template <int TN>
+struct Rows {
+    static constexpr int BUF = TN <= 64 ? 8 : 4;                       // group sums in TMEM
+    static constexpr int COLS = BUF * TN < 32 ? 32 : BUF * TN;         // TMEM columns (a power of two)
+    static constexpr int STAGE = (G + TN) * 128;
+    static constexpr int STAGES = 8 * STAGE <= 200 * 1024 ? 8 : 6;
+    static constexpr int PITCH = G + 4;                                // floats of a token's sums in shared memory
+    struct Shared {
+        float sa[4][SB][TN];   // each warp's own
+        uint64_t full[STAGES], empty[STAGES], sum[BUF], free[BUF], drain;
+        uint32_t tmem;
+        int dead;
+    };
+    static constexpr int OFF = STAGES * STAGE;
+    static constexpr int SMEM = OFF + (int)sizeof(Shared) + 1024;
+    static_assert(TN * PITCH * 4 <= OFF, "the sums take the stages' place");
+    static_assert(SMEM <= 232448, "shared memory above the per-block limit");
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 peer_load(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+// Grid: (contraction pieces, tiles of 128 rows of b, tiles of TN rows of a); a cluster is one tile's pieces. Four warps
+// scale and add, one loads, one issues the products.
+template <int TN>
+__global__ void __launch_bounds__(192) k_mm8_rows(const __grid_constant__ Maps maps, Mm8Args p) {
+    using R = Rows<TN>;
+    extern __shared__ unsigned char raw[];
+    const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
+    unsigned char* mem = raw + (base - tc::smem_u32(raw));
+    typename R::Shared& sm = *reinterpret_cast<typename R::Shared*>(mem + R::OFF);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n0 = blockIdx.y * G, m0 = blockIdx.z * TN;
+    const int parts = gridDim.x, part = blockIdx.x;
+    const int g0 = (int)((int64_t)p.groups * part / parts), g1 = (int)((int64_t)p.groups * (part + 1) / parts);
+    if (warp == 4) {
+        if (lane == 0) {
+            for (int i = 0; i < R::STAGES; ++i) {
+                tc::mbar_init(&sm.full[i], 1);
+                tc::mbar_init(&sm.empty[i], 1);
+            }
+            for (int i = 0; i < R::BUF; ++i) {
+                tc::mbar_init(&sm.sum[i], 1);
+                tc::mbar_init(&sm.free[i], 4);
+            }
+            tc::mbar_init(&sm.drain, 1);
+            sm.dead = 0;
+            tc::fence_mbar_init();
         }
-        __syncthreads();
-#pragma unroll 8
-        for (int c = 0; c < TK; ++c) {
-            const float4 x = *reinterpret_cast<const float4*>(&as[c][ty * 4]), y = *reinterpret_cast<const float4*>(&bs[c][tx * 4]);
-            const float xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
+        __syncwarp();
+    }
+    const auto load = [&](int g) {   // lane 0 of the loader
+        const int st = (g - g0) % R::STAGES;
+        tc::mbar_arrive_expect_tx(&sm.full[st], R::STAGE);
+        tc::tma_load2(base + st * R::STAGE, &maps.b, g * G, n0, &sm.full[st]);
+        tc::tma_load2(base + st * R::STAGE + G * 128, &maps.a, g * G, m0, &sm.full[st]);
+    };
+    if (warp == 4 && lane == 0)
+        for (int g = g0; g < g1 && g < g0 + R::STAGES; ++g) load(g);
+    if (warp == 5) {
+        tc::tmem_alloc(&sm.tmem, R::COLS);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tb = sm.tmem;
+
+    float acc[TN];
+    if (warp < 4) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int t = 0; t < TN; ++t) acc[t] = 0.f;
+        const int n = n0 + warp * 32 + lane;
+        const float* sb = p.sb + (size_t)(p.b_rows ? min(n, p.N - 1) : blockIdx.y) * p.groups;
+        for (int g = g0; g < g1; ++g) {
+            const int i = g - g0, buf = i % R::BUF;
+            if (i % SB == 0) {
+                __syncwarp();
+                for (int t = lane; t < TN; t += 32) {
+                    const float* sa = p.sa + (size_t)min(m0 + t, p.M - 1) * p.groups + g;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) part[i][j] = fmaf(xa[i], ya[j], part[i][j]);
+                    for (int k = 0; k < SB; ++k) sm.sa[warp][k][t] = g + k < g1 ? sa[k] : 0.f;
+                }
+                __syncwarp();
+            }
+            const float s = sb[g];
+            if (!tc::warp_wait(&sm.sum[buf], (i / R::BUF) & 1, &sm.dead)) break;
+            tc::fence_after_sync();
+            const float* row = sm.sa[warp][i % SB];
+#pragma unroll
+            for (int c = 0; c < TN; c += 16) {
+                float x[16];
+                tc::tmem_ld16(tc::taddr(tb, warp * 32, buf * TN + c), x);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int t = 0; t < 16; t += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(row + c + t);
+                    const float2 lo = fma2(make_float2(x[t], x[t + 1]), mul2(make_float2(s, s), make_float2(f.x, f.y)),
+                                           make_float2(acc[c + t], acc[c + t + 1]));
+                    const float2 hi = fma2(make_float2(x[t + 2], x[t + 3]), mul2(make_float2(s, s), make_float2(f.z, f.w)),
+                                           make_float2(acc[c + t + 2], acc[c + t + 3]));
+                    acc[c + t] = lo.x;
+                    acc[c + t + 1] = lo.y;
+                    acc[c + t + 2] = hi.x;
+                    acc[c + t + 3] = hi.y;
+                }
+            }
+            tc::fence_before_sync();
+            tc::warp_arrive(&sm.free[buf]);
         }
-        const int g = k0 / FP8_GROUP;
-        if ((k0 + TK) % FP8_GROUP && k0 + TK < a.K) continue;
+    } else if (warp == 4) {
+        int issued = min(g1 - g0, R::STAGES);
+        for (; issued < g1 - g0; ++issued) {
+            if (!tc::warp_wait(&sm.empty[issued % R::STAGES], (issued / R::STAGES - 1) & 1, &sm.dead)) break;
+            if (lane == 0) load(g0 + issued);
+            __syncwarp();
+        }
+        // no copy is in flight when the sums take the stages' place, after a failure either
+        for (int i = max(0, issued - R::STAGES); i < issued; ++i) tc::mbar_wait(&sm.full[i % R::STAGES], (i / R::STAGES) & 1);
+    } else {
+        constexpr uint32_t I = tc::idesc_e4m3(G, TN);
+        for (int g = g0; g < g1; ++g) {
+            const int i = g - g0, buf = i % R::BUF, st = i % R::STAGES;
+            if (!tc::warp_wait(&sm.full[st], (i / R::STAGES) & 1, &sm.dead)) break;
+            if (i >= R::BUF && !tc::warp_wait(&sm.free[buf], (i / R::BUF - 1) & 1, &sm.dead)) break;
+            tc::fence_after_sync();
+            const uint32_t at = base + st * R::STAGE;
+            tc::mma4_e4m3_w(tb + buf * TN, tc::sdesc(at), tc::sdesc(at + G * 128), I);
+            tc::mma_commit_w(&sm.sum[buf]);
+            tc::mma_commit_w(&sm.empty[st]);
+        }
+        // every product is done before the tensor memory goes back (after a failure, too)
+        tc::mma_commit_w(&sm.drain);
+        if (!tc::mbar_wait(&sm.drain, 0)) sm.dead = 1;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 5) tc::tmem_dealloc(tb, R::COLS);
+    if (threadIdx.x == 0 && sm.dead && p.err) atomicOr(p.err, 2);
+
+    // this CTA's sums as [token][row of b]; the cluster's added up in order
+    float* sums = reinterpret_cast<float*>(mem);
+    if (warp < 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = m0 + ty * 4 + i;
-            const float sa = m < a.M ? a.sa[(size_t)m * a.groups + g] : 0.f;
+        for (int t = 0; t < TN; ++t) sums[t * R::PITCH + threadIdx.x] = acc[t];
+    }
+    cluster_sync();
+    if (warp < 4) {
+        const uint32_t rank = cluster_rank(), size = cluster_size();
+        const int nq = n0 + lane * 4;
+        const bool wide = p.N % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
+        for (int t = rank * 4 + warp; t < TN; t += 4 * size) {
+            const int m = m0 + t;
+            if (m >= p.M) break;
+            const uint32_t at = base + (t * R::PITCH + lane * 4) * 4;
+            float4 s = peer_load(at, 0);
+            for (uint32_t r = 1; r < size; ++r) {
+                const float4 x = peer_load(at, r);
+                s.x += x.x;
+                s.y += x.y;
+                s.z += x.z;
+                s.w += x.w;
+            }
+            const size_t to = (size_t)m * p.N + nq;
+            if (wide && nq < p.N) {
+                if (p.f32) *reinterpret_cast<float4*>(static_cast<float*>(p.y) + to) = s;
+                else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + to) = make_uint2(tc::pack_bf16(s.x, s.y), tc::pack_bf16(s.z, s.w));
+            } else {
+                const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + tx * 4 + j;
-                if (n < a.N) acc[i][j] = fmaf(part[i][j], sa * a.sb[(size_t)(a.b_rows ? n : n / FP8_GROUP) * a.groups + g], acc[i][j]);
-                part[i][j] = 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    if (nq + i >= p.N) break;
+                    if (p.f32) static_cast<float*>(p.y)[to + i] = v[i];
+                    else static_cast<__nv_bfloat16*>(p.y)[to + i] = __float2bfloat16_rn(v[i]);
+                }
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= a.M || n >= a.N) continue;
-            if (a.f32) static_cast<float*>(a.y)[(size_t)m * a.N + n] = acc[i][j];
-            else static_cast<__nv_bfloat16*>(a.y)[(size_t)m * a.N + n] = __float2bfloat16_rn(acc[i][j]);
-        }
+    cluster_sync();   // no CTA ends while its sums are read
 }
+
+template <int TN>
+cudaError_t run_rows(const Mm8Args& p, cudaStream_t st) {
+    using R = Rows<TN>;
+    Maps maps;
+    if (!tmap_rows_u8(&maps.a, p.a, p.M, p.K, p.lda, TN) || !tmap_rows_u8(&maps.b, p.b, p.N, p.K, p.ldb, G)) return cudaErrorInvalidValue;
+    static SmemLimit limit;
+    const cudaError_t e = limit.set(reinterpret_cast<const void*>(&k_mm8_rows<TN>), R::SMEM);
+    if (e != cudaSuccess) return e;
+    const int tn = (p.N + G - 1) / G, tm = (p.M + TN - 1) / TN;
+    int parts = 1;   // pieces of two groups at least, while they fit one round of the SMs
+    while (parts < 8 && 4 * parts <= p.groups && 2LL * parts * tn * tm <= sm_count()) parts *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(parts, tn, tm);
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = R::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = parts;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    cudaError_t launched = cudaSuccess;
+    const cudaError_t last = traced_launch("k_mm8_rows", st, [&] { launched = cudaLaunchKernelEx(&cfg, k_mm8_rows<TN>, maps, p); });
+    return launched != cudaSuccess ? launched : last;
+}
+
+bool on16(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 16 == 0; }
+size_t pitch_of(int K) { return ((size_t)K + 15) / 16 * 16; }
 
 }  // namespace
 
-cudaError_t launch_mm8(const Mm8Args& a, cudaStream_t st) {
-    const dim3 grid((a.M + TM - 1) / TM, (a.N + TM - 1) / TM);
-    return traced_launch("k_mm8", st, [&] { k_mm8<<<grid, NT, 0, st>>>(a); });
+size_t mm8_align_bytes(const Mm8Args& p) {
+    return (on16(p.a, p.lda) ? 0 : ((size_t)p.M * pitch_of(p.K) + 255) / 256 * 256) + (on16(p.b, p.ldb) ? 0 : (size_t)p.N * pitch_of(p.K));
+}
+
+cudaError_t launch_mm8(Mm8Args p, void* ws, cudaStream_t st) {
+    uint8_t* free = static_cast<uint8_t*>(ws);
+    const auto align = [&](const uint8_t*& x, int64_t& ld, int rows) {
+        if (on16(x, ld)) return cudaSuccess;
+        const int64_t pitch = (int64_t)pitch_of(p.K);
+        const uint8_t* src = x;
+        uint8_t* dst = free;
+        const cudaError_t e = traced_launch("k_mm8_align", st, [&] { k_mm8_align<<<rows, 256, 0, st>>>(src, ld, dst, pitch, p.K); });
+        x = dst;
+        ld = pitch;
+        free += ((size_t)rows * pitch + 255) / 256 * 256;
+        return e;
+    };
+    cudaError_t e = align(p.a, p.lda, p.M);
+    if (e != cudaSuccess || (e = align(p.b, p.ldb, p.N)) != cudaSuccess) return e;
+    if (p.M <= 16) return run_rows<16>(p, st);
+    if (p.M <= 32) return run_rows<32>(p, st);
+    if (p.M <= 64) return run_rows<64>(p, st);
+    return run_rows<128>(p, st);
 }
 
 }  // namespace kda

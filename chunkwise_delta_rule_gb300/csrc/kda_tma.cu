@@ -73,6 +73,21 @@ bool tmap_tokens_f32(CUtensorMap* m, const void* base, int64_t tokens, int H, in
     return encode_tokens(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, tokens, H, D, (int64_t)H * D, rows);
 }
 
+bool tmap_rows_u8(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int64_t ld, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15) || ld % 16) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1u, 1u};
+    const auto encode = [&] {
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return encode() || (bind_context() && encode());
+}
+
 bool tmap_state_f32(CUtensorMap* m, const float* base, int NH, int K, int V) {
     auto fn = encode_fn();
     if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15) || K % 32 != 0 || V % 32 != 0) return false;

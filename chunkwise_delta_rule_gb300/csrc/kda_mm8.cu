@@ -261,6 +261,247 @@ cudaError_t run_rows(const Mm8Args& p, cudaStream_t st) {
     return launched != cudaSuccess ? launched : last;
 }
 
+// ------------------------------------------------------------------ many rows of a
+// Two CTAs share a tile of 256 x 256: each loads its 128 rows of a and 128 of b, the tensor cores read the other's rows of b
+// over the pair, so that an SM's shared memory carries 64 KB per group in place of 96 (a tile of 128 x 256 by itself),
+// which is what bounds the products: 512 cycles of them per group. A CTA's sums are 128 rows x 256 columns, 128 columns
+// of one row to a thread of eight warps.
+constexpr int P_STAGES = 6, P_STAGE = 2 * G * 128, P_COLS = 256;
+constexpr int P_LOADER = 8, P_ISSUER = 9, P_SCALES = 10, P_THREADS = 11 * 32;
+struct PairShared {
+    float sb[2][SB][P_COLS];   // scales of b's rows
+    uint64_t full[P_STAGES], empty[P_STAGES], sum[2], free[2], s_full[2], s_free[2];
+    uint32_t tmem;
+    int dead;
+};
+constexpr int P_OFF = P_STAGES * P_STAGE, P_SMEM = P_OFF + (int)sizeof(PairShared) + 1024;
+static_assert(P_SMEM <= 232448, "shared memory above the per-block limit");
+
+// 32 bytes at once.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// BROWS: a scale per row of b, else per 128 rows. Clusters of two walk the tiles.
+template <bool BROWS>
+__global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant__ Maps maps, Mm8Args p, int tiles_m, int tiles) {
+    extern __shared__ unsigned char raw[];
+    const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
+    unsigned char* mem = raw + (base - tc::smem_u32(raw));
+    PairShared& sm = *reinterpret_cast<PairShared*>(mem + P_OFF);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < P_STAGES; ++i) {
+            tc::mbar_init(&sm.full[i], 1);
+            tc::mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sm.sum[i], 1);
+            tc::mbar_init(&sm.free[i], 16);
+            tc::mbar_init(&sm.s_full[i], 1);
+            tc::mbar_init(&sm.s_free[i], 8);
+        }
+        sm.dead = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == P_ISSUER) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers are set up
+    tc::fence_after_sync();
+    const uint32_t tb = sm.tmem;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (warp < 8) {
+        const int quad = warp & 3, half = warp >> 2;
+        const uint32_t ta = tc::taddr(tb, quad * 32, half * 128), lead = tc::peer_smem(tc::smem_u32(sm.free), 0);
+        const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 31) == 0 && p.N % 16 == 0;
+        uint32_t i = 0;   // groups so far
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += step) {
+            const int m = t % tiles_m * 256 + rank * 128 + quad * 32 + lane, n0 = t / tiles_m * 256 + half * 128;
+            const float* sa = p.sa + (size_t)min(m, p.M - 1) * p.groups;
+            const float* sb = p.sb + (size_t)(BROWS ? 0 : min(n0, p.N - 1) / G) * p.groups;
+            float acc[128];
+#pragma unroll
+            for (int c = 0; c < 128; ++c) acc[c] = 0.f;
+            float na = sa[0], nb = BROWS ? 1.f : sb[0];
+            for (int g = 0; g < p.groups; ++g, ++i) {
+                const uint32_t buf = i & 1;
+                const float s = na * nb;
+                if (g + 1 < p.groups) {
+                    na = sa[g + 1];
+                    if (!BROWS) nb = sb[g + 1];
+                }
+                const uint32_t round = (t - first) / step * ((p.groups + SB - 1) / SB) + g / SB;   // of scales
+                if (BROWS && g % SB == 0 && !(ok = tc::warp_wait(&sm.s_full[round & 1], round >> 1 & 1, &sm.dead))) break;
+                if (!(ok = tc::warp_wait(&sm.sum[buf], i >> 1 & 1, &sm.dead))) break;
+                tc::fence_after_sync();
+                const float* col = &sm.sb[round & 1][g % SB][half * 128];
+                const float2 s2 = make_float2(s, s);
+#pragma unroll
+                for (int c = 0; c < 128; c += 16) {
+                    float x[16];
+                    tc::tmem_ld16(ta + buf * P_COLS + c, x);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        float2 lo = s2, hi = s2;
+                        if (BROWS) {
+                            const float4 f = *reinterpret_cast<const float4*>(col + c + k);
+                            lo = mul2(s2, make_float2(f.x, f.y));
+                            hi = mul2(s2, make_float2(f.z, f.w));
+                        }
+                        lo = fma2(make_float2(x[k], x[k + 1]), lo, make_float2(acc[c + k], acc[c + k + 1]));
+                        hi = fma2(make_float2(x[k + 2], x[k + 3]), hi, make_float2(acc[c + k + 2], acc[c + k + 3]));
+                        acc[c + k] = lo.x;
+                        acc[c + k + 1] = lo.y;
+                        acc[c + k + 2] = hi.x;
+                        acc[c + k + 3] = hi.y;
+                    }
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::peer_arrive(lead + 8 * buf);
+                    if (BROWS && (g % SB == SB - 1 || g + 1 == p.groups)) tc::mbar_arrive(&sm.s_free[round & 1]);
+                }
+            }
+            if (!ok || m >= p.M) continue;
+            const size_t to = (size_t)m * p.N + n0;
+            if (p.f32) {
+                float* y = static_cast<float*>(p.y) + to;
+#pragma unroll
+                for (int c = 0; c < 128; c += 8) {
+                    if (wide) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(acc[c + k]);
+                        if (n0 + c < p.N) store32(y + c, v);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (n0 + c + k < p.N) y[c + k] = acc[c + k];
+                    }
+                }
+            } else {
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + to;
+#pragma unroll
+                for (int c = 0; c < 128; c += 16) {
+                    if (wide) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = tc::pack_bf16(acc[c + 2 * k], acc[c + 2 * k + 1]);
+                        if (n0 + c < p.N) store32(y + c, v);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (n0 + c + k < p.N) y[c + k] = __float2bfloat16_rn(acc[c + k]);
+                    }
+                }
+            }
+        }
+    } else if (warp == P_LOADER) {
+        uint32_t i = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += step) {
+            const int m0 = t % tiles_m * 256 + rank * 128, n0 = t / tiles_m * 256 + rank * 128;
+            for (int g = 0; g < p.groups; ++g, ++i) {
+                const uint32_t st = i % P_STAGES;
+                if (i >= P_STAGES && !(ok = tc::warp_wait(&sm.empty[st], (i / P_STAGES - 1) & 1, &sm.dead))) break;
+                if (lane == 0) {
+                    // the pair's products wait for both CTAs' rows on one barrier, that of rank 0
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&sm.full[st], 2 * P_STAGE);
+                    const uint32_t bar = tc::peer_smem(tc::smem_u32(&sm.full[st]), 0);
+                    tc::tma_load2_pair(base + st * P_STAGE, &maps.a, g * G, m0, bar);
+                    tc::tma_load2_pair(base + st * P_STAGE + G * 128, &maps.b, g * G, n0, bar);
+                }
+                __syncwarp();
+            }
+        }
+        // every copy has been read when the CTA ends (a failure's have had this wait's second to land)
+        for (uint32_t k = i > P_STAGES ? i - P_STAGES : 0; k < i; ++k) tc::mbar_wait(&sm.empty[k % P_STAGES], (k / P_STAGES) & 1);
+    } else if (warp == P_ISSUER && rank == 0) {
+        constexpr uint32_t I = tc::idesc_e4m3(256, 256);
+        uint32_t i = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += step)
+            for (int g = 0; g < p.groups; ++g, ++i) {
+                const uint32_t st = i % P_STAGES, buf = i & 1;
+                if (!(ok = tc::warp_wait(&sm.full[st], (i / P_STAGES) & 1, &sm.dead))) break;
+                if (i >= 2 && !(ok = tc::warp_wait(&sm.free[buf], ((i >> 1) - 1) & 1, &sm.dead))) break;
+                tc::fence_after_sync();
+                const uint32_t at = base + st * P_STAGE;
+                tc::mma4_e4m3_pair_w(tb + buf * P_COLS, tc::sdesc(at), tc::sdesc(at + G * 128), I);
+                tc::mma_commit_pair_w(&sm.sum[buf]);
+                tc::mma_commit_pair_w(&sm.empty[st]);
+            }
+    } else if (warp == P_SCALES && BROWS) {
+        uint32_t round = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += step) {
+            const int n0 = t / tiles_m * 256;
+            for (int g = 0; g < p.groups; g += SB, ++round) {
+                if (round >= 2 && !(ok = tc::warp_wait(&sm.s_free[round & 1], ((round >> 1) - 1) & 1, &sm.dead))) break;
+                for (int c = lane; c < P_COLS; c += 32) {
+                    const float* sb = p.sb + (size_t)min(n0 + c, p.N - 1) * p.groups + g;
+#pragma unroll
+                    for (int k = 0; k < SB; ++k) sm.sb[round & 1][k][c] = g + k < p.groups ? sb[k] : 0.f;
+                }
+                tc::warp_arrive(&sm.s_full[round & 1]);
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();   // neither CTA's memory goes back while the other uses it
+    tc::fence_after_sync();
+    if (threadIdx.x == 0 && sm.dead && p.err) atomicOr(p.err, 2);
+    if (warp == P_ISSUER) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tb) : "memory");
+}
+
+template <bool BROWS>
+cudaError_t run_pair(const Mm8Args& p, cudaStream_t st) {
+    Maps maps;
+    if (!tmap_rows_u8(&maps.a, p.a, p.M, p.K, p.lda, G) || !tmap_rows_u8(&maps.b, p.b, p.N, p.K, p.ldb, G)) return cudaErrorInvalidValue;
+    static SmemLimit limit;
+    const cudaError_t e = limit.set(reinterpret_cast<const void*>(&k_mm8_pair<BROWS>), P_SMEM);
+    if (e != cudaSuccess) return e;
+    const int tm = (p.M + 255) / 256, tn = (p.N + 255) / 256, tiles = tm * tn;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(P_THREADS);
+    cfg.dynamicSmemBytes = P_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    static std::atomic<int> fit[64];   // pairs that the device runs at once (not every SM has a partner)
+    int dev = 0, pairs = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+    if (dev < 64) pairs = fit[dev].load(std::memory_order_relaxed);
+    if (!pairs) {
+        if (cudaOccupancyMaxActiveClusters(&pairs, k_mm8_pair<BROWS>, &cfg) != cudaSuccess || pairs < 1) {
+            (void)cudaGetLastError();
+            pairs = sm_count() / 2;
+        }
+        if (dev < 64) fit[dev].store(pairs, std::memory_order_relaxed);
+    }
+    cfg.gridDim = dim3(2 * (tiles < pairs ? tiles : pairs));
+    cudaError_t launched = cudaSuccess;
+    const cudaError_t last = traced_launch("k_mm8_pair", st, [&] { launched = cudaLaunchKernelEx(&cfg, k_mm8_pair<BROWS>, maps, p, tm, tiles); });
+    return launched != cudaSuccess ? launched : last;
+}
+
 bool on16(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 16 == 0; }
 size_t pitch_of(int K) { return ((size_t)K + 15) / 16 * 16; }
 
@@ -285,6 +526,8 @@ cudaError_t launch_mm8(Mm8Args p, void* ws, cudaStream_t st) {
     };
     cudaError_t e = align(p.a, p.lda, p.M);
     if (e != cudaSuccess || (e = align(p.b, p.ldb, p.N)) != cudaSuccess) return e;
+    // (tiles of 256 x 256, two SMs each)
+    if ((long long)((p.M + 255) / 256) * ((p.N + 255) / 256) * 4 >= sm_count()) return p.b_rows ? run_pair<true>(p, st) : run_pair<false>(p, st);
     if (p.M <= 16) return run_rows<16>(p, st);
     if (p.M <= 32) return run_rows<32>(p, st);
     if (p.M <= 64) return run_rows<64>(p, st);

@@ -418,6 +418,44 @@ __device__ __forceinline__ void mma4_e4m3_w(uint32_t d, uint64_t a, uint64_t b, 
         ::"r"(d), "l"(a), "l"(b), "r"(idesc)
         : "memory");
 }
+// The same for a pair of CTAs (issued by the one of rank 0): each has half of A's rows and of B's in shared memory, at the
+// same offsets.
+__device__ __forceinline__ void mma4_e4m3_pair_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred e, no, yes;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 no, 0, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, no;\n\t"
+        "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, yes;\n\t"
+        "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, yes;\n\t"
+        "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, yes;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc)
+        : "memory");
+}
+// Completion of the pair's products arrives once on `bar` in each of the two CTAs.
+__device__ __forceinline__ void mma_commit_pair_w(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// Shared address `a` of this CTA in the cluster's CTA of the given rank.
+__device__ __forceinline__ uint32_t peer_smem(uint32_t a, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+// An arrival on a barrier of the cluster (address from peer_smem), and the wait that sees it.
+__device__ __forceinline__ void peer_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A 2-D box into this CTA's shared memory whose bytes are counted by a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load2_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
 // A in TMEM, B MN-major.
 __device__ __forceinline__ void mma4_bf16_ts_w(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(

@@ -136,7 +136,8 @@ def cuda(*t):
 
 MM = [(1, 1, 1), (1, 128, 128), (2, 16, 16), (3, 5, 7), (64, 128, 256), (1, 4096, 512), (7, 1000, 1111), (16, 256, 2048), (17, 129, 130),
       (64, 512, 4096), (65, 257, 384), (128, 128, 128), (129, 255, 640), (200, 384, 100), (300, 1000, 1040), (777, 130, 272),
-      (256, 512, 1024), (1030, 16, 4096), (128, 1, 128)]
+      (256, 512, 1024), (1030, 16, 4096), (128, 1, 128),
+      (2000, 1300, 300), (1537, 1793, 140), (4100, 770, 1100)]
 
 
 @pytest.mark.parametrize("M,N,K", MM)

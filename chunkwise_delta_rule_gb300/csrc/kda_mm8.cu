@@ -265,9 +265,10 @@ cudaError_t run_rows(const Mm8Args& p, cudaStream_t st) {
 // Two CTAs share a tile of 256 x 256: each loads its 128 rows of a and 128 of b, the tensor cores read the other's rows of b
 // over the pair, so that an SM's shared memory carries 64 KB per group in place of 96 (a tile of 128 x 256 by itself),
 // which is what bounds the products: 512 cycles of them per group. A CTA's sums are 128 rows x 256 columns, 128 columns
-// of one row to a thread of eight warps.
+// of one row to a thread of eight warps (sixteen warps of 64: 284 against 222 us at 16384 x 4096 x 4096).
 constexpr int P_STAGES = 6, P_STAGE = 2 * G * 128, P_COLS = 256;
-constexpr int P_LOADER = 8, P_ISSUER = 9, P_SCALES = 10, P_THREADS = 11 * 32;
+constexpr int P_W = 128;   // columns of a thread
+constexpr int P_ADDERS = 4 * P_COLS / P_W, P_LOADER = P_ADDERS, P_ISSUER = P_ADDERS + 1, P_SCALES = P_ADDERS + 2, P_THREADS = (P_ADDERS + 3) * 32;
 struct PairShared {
     float sb[2][SB][P_COLS];   // scales of b's rows
     uint64_t full[P_STAGES], empty[P_STAGES], sum[2], free[2], s_full[2], s_free[2];
@@ -300,9 +301,9 @@ __global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sm.sum[i], 1);
-            tc::mbar_init(&sm.free[i], 16);
+            tc::mbar_init(&sm.free[i], 2 * P_ADDERS);
             tc::mbar_init(&sm.s_full[i], 1);
-            tc::mbar_init(&sm.s_free[i], 8);
+            tc::mbar_init(&sm.s_free[i], P_ADDERS);
         }
         sm.dead = 0;
         tc::fence_mbar_init();
@@ -318,19 +319,19 @@ __global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant
     const uint32_t tb = sm.tmem;
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-    if (warp < 8) {
-        const int quad = warp & 3, half = warp >> 2;
-        const uint32_t ta = tc::taddr(tb, quad * 32, half * 128), lead = tc::peer_smem(tc::smem_u32(sm.free), 0);
+    if (warp < P_ADDERS) {
+        const int quad = warp & 3, part = warp >> 2;
+        const uint32_t ta = tc::taddr(tb, quad * 32, part * P_W), lead = tc::peer_smem(tc::smem_u32(sm.free), 0);
         const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 31) == 0 && p.N % 16 == 0;
         uint32_t i = 0;   // groups so far
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step) {
-            const int m = t % tiles_m * 256 + rank * 128 + quad * 32 + lane, n0 = t / tiles_m * 256 + half * 128;
+            const int m = t % tiles_m * 256 + rank * 128 + quad * 32 + lane, n0 = t / tiles_m * 256 + part * P_W;
             const float* sa = p.sa + (size_t)min(m, p.M - 1) * p.groups;
             const float* sb = p.sb + (size_t)(BROWS ? 0 : min(n0, p.N - 1) / G) * p.groups;
-            float acc[128];
+            float acc[P_W];
 #pragma unroll
-            for (int c = 0; c < 128; ++c) acc[c] = 0.f;
+            for (int c = 0; c < P_W; ++c) acc[c] = 0.f;
             float na = sa[0], nb = BROWS ? 1.f : sb[0];
             for (int g = 0; g < p.groups; ++g, ++i) {
                 const uint32_t buf = i & 1;
@@ -343,10 +344,10 @@ __global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant
                 if (BROWS && g % SB == 0 && !(ok = tc::warp_wait(&sm.s_full[round & 1], round >> 1 & 1, &sm.dead))) break;
                 if (!(ok = tc::warp_wait(&sm.sum[buf], i >> 1 & 1, &sm.dead))) break;
                 tc::fence_after_sync();
-                const float* col = &sm.sb[round & 1][g % SB][half * 128];
+                const float* col = &sm.sb[round & 1][g % SB][part * P_W];
                 const float2 s2 = make_float2(s, s);
 #pragma unroll
-                for (int c = 0; c < 128; c += 16) {
+                for (int c = 0; c < P_W; c += 16) {
                     float x[16];
                     tc::tmem_ld16(ta + buf * P_COLS + c, x);
                     tc::tmem_wait_ld();
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant
             if (p.f32) {
                 float* y = static_cast<float*>(p.y) + to;
 #pragma unroll
-                for (int c = 0; c < 128; c += 8) {
+                for (int c = 0; c < P_W; c += 8) {
                     if (wide) {
                         uint32_t v[8];
 #pragma unroll
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant
             } else {
                 __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + to;
 #pragma unroll
-                for (int c = 0; c < 128; c += 16) {
+                for (int c = 0; c < P_W; c += 16) {
                     if (wide) {
                         uint32_t v[8];
 #pragma unroll

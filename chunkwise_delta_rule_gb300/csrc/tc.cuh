@@ -445,9 +445,10 @@ __device__ __forceinline__ uint32_t peer_smem(uint32_t a, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
     return r;
 }
-// An arrival on a barrier of the cluster (address from peer_smem), and the wait that sees it.
+// An arrival on a barrier of the cluster (address from peer_smem). It orders no memory beyond the CTA's: what it hands
+// over is tensor memory that has been read (a release over the cluster is a fence that takes longer than a group's sums).
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // A 2-D box into this CTA's shared memory whose bytes are counted by a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load2_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {

@@ -44,6 +44,8 @@ bool tmap_tokens_bf16(CUtensorMap* m, const void* base, int64_t tokens, int H, i
 bool tmap_tokens_f32(CUtensorMap* m, const void* base, int64_t tokens, int H, int D, int rows);
 // Rows of bytes [rows][K], `ld` bytes apart (a multiple of 16), in boxes of `box` rows x 128 bytes, 128-byte swizzled.
 bool tmap_rows_u8(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int64_t ld, int box);
+// Contiguous rows [rows][D] of bf16 or fp32 (D a multiple of 8 or 4), in boxes of `box` rows x 128 bytes, swizzled.
+bool tmap_matrix(CUtensorMap* m, const void* base, int64_t rows, int D, int f32, int box);
 // fp32 states [NH][K][V] in boxes of 32 keys x 32 value columns, 128-byte swizzled (K, V multiples of
 // 32; false when the base is not 16-byte aligned).
 bool tmap_state_f32(CUtensorMap* m, const float* base, int NH, int K, int V);

@@ -15,7 +15,7 @@ namespace {
 constexpr int G = FP8_GROUP;
 
 struct Maps {
-    CUtensorMap a, b;
+    CUtensorMap a, b, y;
 };
 
 // ------------------------------------------------------------------ rows that no tensor map takes
@@ -265,29 +265,24 @@ cudaError_t run_rows(const Mm8Args& p, cudaStream_t st) {
 // Two CTAs share a tile of 256 x 256: each loads its 128 rows of a and 128 of b, the tensor cores read the other's rows of b
 // over the pair, so that an SM's shared memory carries 64 KB per group in place of 96 (a tile of 128 x 256 by itself),
 // which is what bounds the products: 512 cycles of them per group. A CTA's sums are 128 rows x 256 columns, 128 columns
-// of one row to a thread of eight warps (sixteen warps of 64: 284 against 222 us at 16384 x 4096 x 4096).
-constexpr int P_STAGES = 6, P_STAGE = 2 * G * 128, P_COLS = 256;
-constexpr int P_W = 128;   // columns of a thread
-constexpr int P_ADDERS = 4 * P_COLS / P_W, P_LOADER = P_ADDERS, P_ISSUER = P_ADDERS + 1, P_SCALES = P_ADDERS + 2, P_THREADS = (P_ADDERS + 3) * 32;
+// of one row to a thread of eight warps.
+constexpr int P_STAGES = 5, P_STAGE = 2 * G * 128, P_COLS = 256, P_W = 128, P_ADDERS = 8;   // columns of an adding thread, adding warps
+constexpr int P_LOADER = 8, P_ISSUER = 9, P_SCALES = 10, P_THREADS = 12 * 32;   // (the twelfth completes a warpgroup)
+constexpr int P_REGS_ADD = 208, P_REGS_REST = 88;   // 2 x 208 + 88 = 3 x 168, what a block of 384 threads starts with
+constexpr int P_OUT = 32 * 128;                     // bytes of outputs on their way, for each adding warp
 struct PairShared {
-    float sb[2][SB][P_COLS];   // scales of b's rows
+    float sa[2][SB][G + 4], sb[2][SB][P_COLS + 4];   // scales of SB groups: of this CTA's rows of a, of the tile's rows of b (or, one
+                                             // for 128 of them, in the first two places)
     uint64_t full[P_STAGES], empty[P_STAGES], sum[2], free[2], s_full[2], s_free[2];
     uint32_t tmem;
     int dead;
 };
-constexpr int P_OFF = P_STAGES * P_STAGE, P_SMEM = P_OFF + (int)sizeof(PairShared) + 1024;
+constexpr int P_OFF_OUT = P_STAGES * P_STAGE, P_OFF = P_OFF_OUT + P_ADDERS * P_OUT, P_SMEM = P_OFF + (int)sizeof(PairShared) + 1024;
 static_assert(P_SMEM <= 232448, "shared memory above the per-block limit");
-
-// 32 bytes at once.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
 
 // BROWS: a scale per row of b, else per 128 rows. Clusters of two walk the tiles.
 template <bool BROWS>
-__global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant__ Maps maps, Mm8Args p, int tiles_m, int tiles) {
+__global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant__ Maps maps, Mm8Args p, int tiles_m, int tiles, int tma_out) {
     extern __shared__ unsigned char raw[];
     const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
     unsigned char* mem = raw + (base - tc::smem_u32(raw));
@@ -320,36 +315,39 @@ __global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp < P_ADDERS) {
+        tc::regs_more<P_REGS_ADD>();
         const int quad = warp & 3, part = warp >> 2;
         const uint32_t ta = tc::taddr(tb, quad * 32, part * P_W), lead = tc::peer_smem(tc::smem_u32(sm.free), 0);
-        const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 31) == 0 && p.N % 16 == 0;
-        uint32_t i = 0;   // groups so far
+        uint32_t i = 0, round = 0;   // groups, and rounds of scales, so far
+        const uint32_t out = P_OFF_OUT + warp * P_OUT;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step) {
             const int m = t % tiles_m * 256 + rank * 128 + quad * 32 + lane, n0 = t / tiles_m * 256 + part * P_W;
-            const float* sa = p.sa + (size_t)min(m, p.M - 1) * p.groups;
-            const float* sb = p.sb + (size_t)(BROWS ? 0 : min(n0, p.N - 1) / G) * p.groups;
             float acc[P_W];
 #pragma unroll
             for (int c = 0; c < P_W; ++c) acc[c] = 0.f;
-            float na = sa[0], nb = BROWS ? 1.f : sb[0];
+            const float* sa = p.sa + (size_t)min(m, p.M - 1) * p.groups;
+            const float* sb = p.sb + (size_t)(BROWS ? 0 : min(n0, p.N - 1) / G) * p.groups;
+            const auto scale = [&](uint32_t from, int g) {   // of this row, and of b's rows where they share one
+                return BROWS ? sm.sa[from][g % SB][quad * 32 + lane] : sa[g] * sb[g];
+            };
+            float s = BROWS ? 0.f : scale(0, 0);   // the present group's: read while the group before it is added
             for (int g = 0; g < p.groups; ++g, ++i) {
-                const uint32_t buf = i & 1;
-                const float s = na * nb;
-                if (g + 1 < p.groups) {
-                    na = sa[g + 1];
-                    if (!BROWS) nb = sb[g + 1];
+                const uint32_t buf = i & 1, from = round & 1;
+                if (BROWS && g % SB == 0) {
+                    if (!(ok = tc::warp_wait(&sm.s_full[from], round >> 1 & 1, &sm.dead))) break;
+                    s = scale(from, g);
                 }
-                const uint32_t round = (t - first) / step * ((p.groups + SB - 1) / SB) + g / SB;   // of scales
-                if (BROWS && g % SB == 0 && !(ok = tc::warp_wait(&sm.s_full[round & 1], round >> 1 & 1, &sm.dead))) break;
+                const float* col = &sm.sb[from][g % SB][part * P_W];
+                const float2 s2 = make_float2(s, s);
+                if (!BROWS && g + 1 < p.groups) s = scale(0, g + 1);
                 if (!(ok = tc::warp_wait(&sm.sum[buf], i >> 1 & 1, &sm.dead))) break;
                 tc::fence_after_sync();
-                const float* col = &sm.sb[round & 1][g % SB][part * P_W];
-                const float2 s2 = make_float2(s, s);
+                // 16 columns are read while the 16 before them are added
 #pragma unroll
                 for (int c = 0; c < P_W; c += 16) {
-                    float x[16];
-                    tc::tmem_ld16(ta + buf * P_COLS + c, x);
+                    float y[16];
+                    tc::tmem_ld16(ta + buf * P_COLS + c, y);
                     tc::tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 16; k += 4) {
@@ -359,8 +357,8 @@ __global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant
                             lo = mul2(s2, make_float2(f.x, f.y));
                             hi = mul2(s2, make_float2(f.z, f.w));
                         }
-                        lo = fma2(make_float2(x[k], x[k + 1]), lo, make_float2(acc[c + k], acc[c + k + 1]));
-                        hi = fma2(make_float2(x[k + 2], x[k + 3]), hi, make_float2(acc[c + k + 2], acc[c + k + 3]));
+                        lo = fma2(make_float2(y[k], y[k + 1]), lo, make_float2(acc[c + k], acc[c + k + 1]));
+                        hi = fma2(make_float2(y[k + 2], y[k + 3]), hi, make_float2(acc[c + k + 2], acc[c + k + 3]));
                         acc[c + k] = lo.x;
                         acc[c + k + 1] = lo.y;
                         acc[c + k + 2] = hi.x;
@@ -369,46 +367,64 @@ __global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant
                 }
                 tc::fence_before_sync();
                 __syncwarp();
+                const bool last = g % SB == SB - 1 || g + 1 == p.groups;
                 if (lane == 0) {
                     tc::peer_arrive(lead + 8 * buf);
-                    if (BROWS && (g % SB == SB - 1 || g + 1 == p.groups)) tc::mbar_arrive(&sm.s_free[round & 1]);
+                    if (BROWS && last) tc::mbar_arrive(&sm.s_free[from]);
                 }
+                if (BROWS && !last) s = scale(from, g + 1);
+                round += last;
             }
-            if (!ok || m >= p.M) continue;
-            const size_t to = (size_t)m * p.N + n0;
-            if (p.f32) {
-                float* y = static_cast<float*>(p.y) + to;
+            if (!ok) break;
+            if (tma_out) {   // 128 bytes of the warp's 32 rows at a time
+                const auto piece = [&](int c, auto&& words) {
+                    if (lane == 0) tc::bulk_wait_read();
+                    __syncwarp();
 #pragma unroll
-                for (int c = 0; c < P_W; c += 8) {
-                    if (wide) {
-                        uint32_t v[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(acc[c + k]);
-                        if (n0 + c < p.N) store32(y + c, v);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (n0 + c + k < p.N) y[c + k] = acc[c + k];
+                    for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(mem + out + lane * 128 + ((k ^ (lane & 7)) << 4)) = words(k);
+                    tc::fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (n0 + c < p.N && m < p.M) tc::tma_store2(&maps.y, n0 + c, m, base + out);
+                        tc::bulk_commit();
                     }
+                };
+                if (p.f32) {
+#pragma unroll
+                    for (int c = 0; c < P_W; c += 32)
+                        piece(c, [&](int k) {
+                            const float* v = acc + c + 4 * k;
+                            return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+                        });
+                } else {
+#pragma unroll
+                    for (int c = 0; c < P_W; c += 64)
+                        piece(c, [&](int k) {
+                            const float* v = acc + c + 8 * k;
+                            return make_uint4(tc::pack_bf16(v[0], v[1]), tc::pack_bf16(v[2], v[3]), tc::pack_bf16(v[4], v[5]), tc::pack_bf16(v[6], v[7]));
+                        });
                 }
-            } else {
-                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + to;
+            } else if (m < p.M) {   // rows that no tensor map takes
+                const int left = p.N - n0;
+                if (p.f32) {
+                    float* y = static_cast<float*>(p.y) + (size_t)m * p.N + n0;
 #pragma unroll
-                for (int c = 0; c < P_W; c += 16) {
-                    if (wide) {
-                        uint32_t v[8];
+                    for (int c = 0; c < P_W; ++c)
+                        if (c < left) y[c] = acc[c];
+                } else {
+                    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + (size_t)m * p.N + n0;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = tc::pack_bf16(acc[c + 2 * k], acc[c + 2 * k + 1]);
-                        if (n0 + c < p.N) store32(y + c, v);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (n0 + c + k < p.N) y[c + k] = __float2bfloat16_rn(acc[c + k]);
-                    }
+                    for (int c = 0; c < P_W; ++c)
+                        if (c < left) y[c] = __float2bfloat16_rn(acc[c]);
                 }
             }
         }
-    } else if (warp == P_LOADER) {
+        if (lane == 0) tc::bulk_wait_all();
+        __syncwarp();
+    } else {
+        tc::regs_less<P_REGS_REST>();
+    }
+    if (warp == P_LOADER) {
         uint32_t i = 0;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step) {
@@ -447,14 +463,23 @@ __global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant
         uint32_t round = 0;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step) {
-            const int n0 = t / tiles_m * 256;
+            const int m0 = t % tiles_m * 256 + rank * 128, n0 = t / tiles_m * 256;
             for (int g = 0; g < p.groups; g += SB, ++round) {
                 if (round >= 2 && !(ok = tc::warp_wait(&sm.s_free[round & 1], ((round >> 1) - 1) & 1, &sm.dead))) break;
-                for (int c = lane; c < P_COLS; c += 32) {
-                    const float* sb = p.sb + (size_t)min(n0 + c, p.N - 1) * p.groups + g;
+                // 8 lanes read a row's SB neighbouring scales, 4 rows at a time, 64 rows in flight; rows of the copies are 4
+                // words off a bank's multiple, so that the lanes' words lie in banks of their own
+                static_assert(SB == 8, "a row's scales are 8 lanes'");
+                const int k = lane & 7, r4 = lane >> 3;
+                const auto copy = [&](const float* from, int row, int rows, float* to, int pitch) {
+                    float v[16];
 #pragma unroll
-                    for (int k = 0; k < SB; ++k) sm.sb[round & 1][k][c] = g + k < p.groups ? sb[k] : 0.f;
-                }
+                    for (int i = 0; i < 16; ++i)
+                        v[i] = g + k < p.groups ? from[(size_t)min(row + 4 * i + r4, rows - 1) * p.groups + g + k] : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) to[k * pitch + 4 * i + r4] = v[i];
+                };
+                for (int r = 0; r < G; r += 64) copy(p.sa, m0 + r, p.M, &sm.sa[round & 1][0][r], G + 4);
+                for (int r = 0; r < P_COLS; r += 64) copy(p.sb, n0 + r, p.N, &sm.sb[round & 1][0][r], P_COLS + 4);
                 tc::warp_arrive(&sm.s_full[round & 1]);
             }
         }
@@ -474,6 +499,7 @@ cudaError_t run_pair(const Mm8Args& p, cudaStream_t st) {
     static SmemLimit limit;
     const cudaError_t e = limit.set(reinterpret_cast<const void*>(&k_mm8_pair<BROWS>), P_SMEM);
     if (e != cudaSuccess) return e;
+    const int tma_out = tmap_matrix(&maps.y, p.y, p.M, p.N, p.f32, 32) ? 1 : 0;
     const int tm = (p.M + 255) / 256, tn = (p.N + 255) / 256, tiles = tm * tn;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2);
@@ -499,7 +525,7 @@ cudaError_t run_pair(const Mm8Args& p, cudaStream_t st) {
     }
     cfg.gridDim = dim3(2 * (tiles < pairs ? tiles : pairs));
     cudaError_t launched = cudaSuccess;
-    const cudaError_t last = traced_launch("k_mm8_pair", st, [&] { launched = cudaLaunchKernelEx(&cfg, k_mm8_pair<BROWS>, maps, p, tm, tiles); });
+    const cudaError_t last = traced_launch("k_mm8_pair", st, [&] { launched = cudaLaunchKernelEx(&cfg, k_mm8_pair<BROWS>, maps, p, tm, tiles, tma_out); });
     return launched != cudaSuccess ? launched : last;
 }
 

@@ -59,6 +59,21 @@ bool encode_tokens(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void
     return encode() || (bind_context() && encode());
 }
 
+// Rows of D elements, `pitch` bytes apart, in boxes of `box_rows` rows x 128 bytes, swizzled.
+bool encode_rows(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base, int64_t rows, int64_t D, int64_t pitch, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15) || pitch % 16) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {128u / esize, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1u, 1u};
+    const auto encode = [&] {
+        return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return encode() || (bind_context() && encode());
+}
+
 }  // namespace
 
 bool tmap_rows_bf16(CUtensorMap* m, const void* base, int Ttot, int H, int D) {
@@ -74,18 +89,12 @@ bool tmap_tokens_f32(CUtensorMap* m, const void* base, int64_t tokens, int H, in
 }
 
 bool tmap_rows_u8(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int64_t ld, int box_rows) {
-    auto fn = encode_fn();
-    if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15) || ld % 16) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld};
-    const cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1u, 1u};
-    const auto encode = [&] {
-        return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    };
-    return encode() || (bind_context() && encode());
+    return encode_rows(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, K, ld, box_rows);
+}
+
+bool tmap_matrix(CUtensorMap* m, const void* base, int64_t rows, int D, int f32, int box) {
+    return f32 ? encode_rows(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, rows, D, (int64_t)D * 4, box)
+               : encode_rows(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, D, (int64_t)D * 2, box);
 }
 
 bool tmap_state_f32(CUtensorMap* m, const float* base, int NH, int K, int V) {

@@ -22,7 +22,7 @@ __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162f
 
 // KR rows of the state per warp (K <= 8 KR), VEC neighbouring value columns per lane, TG tokens per group.
 template <typename TI, int KR, int VEC, int TG>
-__global__ void __launch_bounds__(NT) k_lin(LinArgs a, int local) {
+__global__ void __launch_bounds__(NT, KR * VEC >= 64 ? 1 : 2) k_lin(LinArgs a, int local) {
     constexpr int KM = NW * KR, SL = 32 * VEC;
     const LinCall& c = a.c[blockIdx.y];
     const int slices = (c.V + SL - 1) / SL;
@@ -34,7 +34,9 @@ __global__ void __launch_bounds__(NT) k_lin(LinArgs a, int local) {
     if (unit >= a.ax.rows * a.units_row) return;
     const int row = unit / a.units_row, u = unit - row * a.units_row;
 
-    __shared__ __align__(16) float sq[TG][KM], sk[TG][KM], sv[TG][SL], part[TG][NW][SL];
+    constexpr int LD = KM + 4;   // rows of q and k four words apart in the banks
+    constexpr int NK = TG * KM / NT, NV = TG * SL / NT > 0 ? TG * SL / NT : 1;   // a thread's values of a group
+    __shared__ __align__(16) float sq[TG][LD], sk[TG][LD], sv[TG][SL], part[TG][NW][SL];
     __shared__ float P[TG][TG];
     __shared__ float2 pw[TG + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k0 = warp * KR;
@@ -144,30 +146,56 @@ __global__ void __launch_bounds__(NT) k_lin(LinArgs a, int local) {
         }
         if (first && warp == NW - 1 && lane <= TG) pw[lane] = lin_power2(g, lane);
         first = false;
+        // the next group's values are on their way while a group is worked on
+        float nq[NK], nk[NK], nv[NV];
+        auto fetch = [&](int at) {
+            const int64_t base = (int64_t)row * a.ax.len;
+#pragma unroll
+            for (int x = 0; x < NK; ++x) {
+                const int i = (threadIdx.x + x * NT) / KM, d = (threadIdx.x + x * NT) % KM;
+                const bool on = at + i < end && d < c.K;
+                const int64_t tok = base + (c.back ? a.ax.len - 1 - (at + i) : at + i);
+                nk[x] = on ? as_float(static_cast<const TI*>(c.k)[tok * c.ldk + (int64_t)(h / c.gk) * c.K + d]) : 0.f;
+                nq[x] = on && !local ? as_float(static_cast<const TI*>(c.q)[tok * c.ldq + (int64_t)(h / c.gq) * c.K + d]) : 0.f;
+            }
+#pragma unroll
+            for (int x = 0; x < NV; ++x) {
+                const int i = (threadIdx.x + x * NT) / SL, d = (threadIdx.x + x * NT) % SL;
+                const int64_t tok = base + (c.back ? a.ax.len - 1 - (at + i) : at + i);
+                nv[x] = i < TG && at + i < end && v0 + d < c.V
+                            ? as_float(static_cast<const TI*>(c.v)[tok * c.ldv + (int64_t)(h / c.gv) * c.V + v0 + d]) : 0.f;
+            }
+        };
+        fetch(t);
         for (; t < end; t += TG) {
             const int n = min(TG, end - t);
             __syncthreads();   // the last group's readers are done
-            for (int x = threadIdx.x; x < n * KM; x += NT) {
-                const int i = x / KM, d = x - i * KM;
-                const size_t tok = (size_t)row * a.ax.len + (c.back ? a.ax.len - 1 - (t + i) : t + i);
-                sk[i][d] = d < c.K ? as_float(static_cast<const TI*>(c.k)[tok * c.ldk + (size_t)(h / c.gk) * c.K + d]) : 0.f;
-                if (!local) sq[i][d] = d < c.K ? as_float(static_cast<const TI*>(c.q)[tok * c.ldq + (size_t)(h / c.gq) * c.K + d]) : 0.f;
+#pragma unroll
+            for (int x = 0; x < NK; ++x) {
+                const int i = (threadIdx.x + x * NT) / KM, d = (threadIdx.x + x * NT) % KM;
+                sk[i][d] = nk[x];
+                if (!local) sq[i][d] = nq[x];
             }
-            for (int x = threadIdx.x; x < n * SL; x += NT) {
-                const int i = x / SL, d = x - i * SL;
-                const size_t tok = (size_t)row * a.ax.len + (c.back ? a.ax.len - 1 - (t + i) : t + i);
-                sv[i][d] = v0 + d < c.V ? as_float(static_cast<const TI*>(c.v)[tok * c.ldv + (size_t)(h / c.gv) * c.V + v0 + d]) : 0.f;
+#pragma unroll
+            for (int x = 0; x < NV; ++x) {
+                const int i = (threadIdx.x + x * NT) / SL, d = (threadIdx.x + x * NT) % SL;
+                if (i < TG) sv[i][d] = nv[x];
             }
             __syncthreads();
+            if (t + TG < end) fetch(t + TG);
             if (!local) {
-                for (int x = warp; x < n * n; x += NW) {
-                    const int i = x / n, j = x - i * n;
-                    if (j > i) continue;
+                {   // the group's scores, four threads to a pair of tokens
+                    const int pair = threadIdx.x >> 2, i = pair / TG, j = pair % TG, y0 = (threadIdx.x & 3) * 4;
                     float d = 0.f;
-                    for (int y = lane; y < c.K; y += 32) d = fmaf(sq[i][y], sk[j][y], d);
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(FULL, d, o);
-                    if (lane == 0) P[i][j] = d * pw[i - j].x * (c.s * c.w);
+                    if (pair < TG * TG && j <= i && i < n) {
+                        for (int y = y0; y < c.K; y += 16) {   // (the rows hold zeros behind K)
+                            const float4 x = *reinterpret_cast<const float4*>(&sq[i][y]), z = *reinterpret_cast<const float4*>(&sk[j][y]);
+                            d = fmaf(x.x, z.x, fmaf(x.y, z.y, fmaf(x.z, z.z, fmaf(x.w, z.w, d))));
+                        }
+                    }
+                    d += __shfl_xor_sync(FULL, d, 1);
+                    d += __shfl_xor_sync(FULL, d, 2);
+                    if ((threadIdx.x & 3) == 0 && pair < TG * TG && j <= i && i < n) P[i][j] = d * pw[i - j].x * (c.s * c.w);
                 }
 #pragma unroll
                 for (int i = 0; i < TG; ++i) {
@@ -237,6 +265,90 @@ __global__ void __launch_bounds__(NT) k_lin(LinArgs a, int local) {
     }
 }
 
+// One token of every sequence: S <- a S + k v^T, o = s q S, each state read and written once, 16 bytes at a time. A CTA
+// has a head's K rows of up to 128 columns, VL lanes to a row, NR rows to a thread, all of them requested before the
+// token's own values are waited for. Bound by HBM.
+template <typename TI, int VL, int NR>
+__global__ void __launch_bounds__(NT) k_lin_step(LinArgs a) {
+    constexpr int STEP = NT / VL, SL = VL * 4;   // rows side by side, columns
+    const LinCall& c = a.c[0];
+    const int slices = (c.V + SL - 1) / SL, slice = blockIdx.x % slices, h = blockIdx.x / slices % a.HV, n = blockIdx.x / slices / a.HV;
+    __shared__ __align__(16) float sq[STEP * NR], sk[STEP * NR], sv[SL], part[STEP][SL], dots[NW];
+    __shared__ float2 an;
+    const int r0 = threadIdx.x / VL, v = threadIdx.x % VL * 4, v0 = slice * SL;
+    const bool cols = v0 + v < c.V;
+    const size_t at = ((size_t)n * a.HV + h) * c.K * c.V + v0 + v;
+    float4 S[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int k = r0 + i * STEP;
+        S[i] = c.s0 && cols && k < c.K ? __ldcs(reinterpret_cast<const float4*>(c.s0 + at + (size_t)k * c.V)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float dot = 0.f;
+    for (int k = threadIdx.x; k < STEP * NR; k += NT) {
+        const bool on = k < c.K;
+        const float q = on ? as_float(static_cast<const TI*>(c.q)[n * c.ldq + (int64_t)(h / c.gq) * c.K + k]) : 0.f;
+        const float y = on ? as_float(static_cast<const TI*>(c.k)[n * c.ldk + (int64_t)(h / c.gk) * c.K + k]) : 0.f;
+        sq[k] = q;
+        sk[k] = y;
+        dot = fmaf(q, y, dot);
+    }
+    if (threadIdx.x < SL) sv[threadIdx.x] = v0 + threadIdx.x < c.V ? as_float(static_cast<const TI*>(c.v)[n * c.ldv + (int64_t)h * c.V + v0 + threadIdx.x]) : 0.f;
+    if (threadIdx.x == NT - 1) an = lin_power2(a.decay ? a.decay[h] : 0.f, 1);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(FULL, dot, o);
+    if ((threadIdx.x & 31) == 0) dots[threadIdx.x >> 5] = dot;
+    __syncthreads();
+    const float4 y = *reinterpret_cast<const float4*>(&sv[v]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int k = r0 + i * STEP;
+        const float q = sq[k], x = sk[k];
+        const auto one = [&](float& e, float& sum, float val) {
+            sum = fmaf(q, e, sum);
+            e = fmaf(e, an.x, fmaf(e, an.y, x * val));
+        };
+        one(S[i].x, o.x, y.x);
+        one(S[i].y, o.y, y.y);
+        one(S[i].z, o.z, y.z);
+        one(S[i].w, o.w, y.w);
+        if (c.s1 && cols && k < c.K) __stcs(reinterpret_cast<float4*>(c.s1 + at + (size_t)k * c.V), S[i]);
+    }
+    *reinterpret_cast<float4*>(&part[r0][v]) = o;
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d < SL && v0 + d < c.V) {
+        float sum = 0.f, qk = 0.f;
+#pragma unroll
+        for (int i = 0; i < STEP; ++i) sum += part[i][d];
+#pragma unroll
+        for (int i = 0; i < NW; ++i) qk += dots[i];
+        sum = c.s * fmaf(sum, an.x, qk * sv[d]);
+        static_cast<TI*>(c.o)[((size_t)n * a.HV + h) * c.V + v0 + d] = TI(sum);
+    }
+}
+
+// Whether a call is one token of every sequence in whole accesses.
+bool is_step(const LinArgs& a) {
+    const LinCall& c = a.c[0];
+    return a.calls == 1 && !a.ax.cu && a.ax.len == 1 && c.K <= 128 && c.V % 4 == 0 &&
+           ((reinterpret_cast<uintptr_t>(c.s0) | reinterpret_cast<uintptr_t>(c.s1)) & 15) == 0;
+}
+template <typename TI>
+cudaError_t run_step(const LinArgs& a, cudaStream_t st) {
+    const LinCall& c = a.c[0];
+    const int sl = c.V <= 32 ? 32 : c.V <= 64 ? 64 : 128;
+    const long long ctas = (long long)a.ax.rows * a.HV * ((c.V + sl - 1) / sl);
+    if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const unsigned g = (unsigned)ctas;
+    return traced_launch("k_lin_step", st, [&] {
+        if (sl == 32) c.K <= 64 ? k_lin_step<TI, 8, 2><<<g, NT, 0, st>>>(a) : k_lin_step<TI, 8, 4><<<g, NT, 0, st>>>(a);
+        else if (sl == 64) c.K <= 64 ? k_lin_step<TI, 16, 4><<<g, NT, 0, st>>>(a) : k_lin_step<TI, 16, 8><<<g, NT, 0, st>>>(a);
+        else c.K <= 64 ? k_lin_step<TI, 32, 8><<<g, NT, 0, st>>>(a) : k_lin_step<TI, 32, 16><<<g, NT, 0, st>>>(a);
+    });
+}
+
 template <typename TI, int KR, int VEC, int TG>
 cudaError_t run(const LinArgs& a, cudaStream_t st) {
     int vmax = 1;
@@ -253,6 +365,7 @@ cudaError_t run(const LinArgs& a, cudaStream_t st) {
 
 template <typename TI>
 cudaError_t pick(const LinArgs& a, cudaStream_t st) {
+    if (is_step(a)) return run_step<TI>(a, st);
     int kmax = 1, vmax = 1;
     for (int i = 0; i < a.calls; ++i) {
         kmax = a.c[i].K > kmax ? a.c[i].K : kmax;

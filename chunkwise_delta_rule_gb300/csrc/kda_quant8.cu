@@ -19,8 +19,8 @@ __device__ __forceinline__ float amax(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
     return r;
 }
-// What a group's values are multiplied by, in two factors: 448 / m may overflow, or m be above the range in which its
-// quotient is normal; such a group is brought to the middle of the range first.
+// What a group's values are multiplied by. 448 / m may overflow, or m be above the range in which its quotient is normal;
+// such a group (`by` is not 1) is brought to the middle of the range first.
 struct Factor {
     float by, inv;
 };
@@ -29,14 +29,63 @@ __device__ __forceinline__ Factor factor(float m) {
     const float v = m * by;
     return {by, v > 0.f ? FP8_MAX / v : v};   // 0 and NaN as they are
 }
-__device__ __forceinline__ uint32_t pack4(const float (&v)[4]) {
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3) |
-           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+// Four values of a group, rounded.
+__device__ __forceinline__ uint32_t round4(float2 a, float2 b, const Factor& f) {
+    if (f.by != 1.f) {
+        a = mul2(a, make_float2(f.by, f.by));
+        b = mul2(b, make_float2(f.by, f.by));
+    }
+    a = mul2(a, make_float2(f.inv, f.inv));
+    b = mul2(b, make_float2(f.inv, f.inv));
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) | (uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16;
 }
-
+// |x| of two bf16 values, and the larger ones of two pairs; a NaN stays.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7fff7fffu));
+    return r;
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// Maxima of |x| over the rows (all 8 values of each) and over the columns of a thread's 8 x 8 values.
+template <bool R, bool C>
+__device__ __forceinline__ void maxima(const Raw<__nv_bfloat16, 8> (&raw)[8], float (&rm)[8], float (&cm)[8]) {
+    uint32_t c[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[i]);
+        if (R) {
+            const uint32_t m = max_bf16x2(max_bf16x2(max_bf16x2(max_bf16x2(0u, w[0]), w[1]), w[2]), w[3]);
+            rm[i] = amax(low(m), high(m));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (C) c[j] = max_bf16x2(c[j], w[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (C) {
+            cm[2 * j] = low(c[j]);
+            cm[2 * j + 1] = high(c[j]);
+        }
+}
+template <bool R, bool C>
+__device__ __forceinline__ void maxima(const Raw<float, 8> (&raw)[8], float (&rm)[8], float (&cm)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cm[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        rm[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (R) rm[i] = amax(rm[i], raw[i].v[j]);
+            if (C) cm[j] = amax(cm[j], raw[i].v[j]);
+        }
+    }
+}
 // ROWS: q is wanted, COLS: qt.
 template <typename TI, bool BLOCKS, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(NT, 2) k_quant8(Quant8Args a, int vecx, int vecq, int vect) {
+__global__ void __launch_bounds__(NT, sizeof(TI) == 2 ? 3 : 2) k_quant8(Quant8Args a, int vecx, int vecq, int vect) {
     __shared__ __align__(16) uint2 turn[COLS ? TILE : 1][COLS ? TILE / PER : 1];
     __shared__ float cmax[COLS && !BLOCKS ? NT / 32 : 1][COLS && !BLOCKS ? TILE : 1];
     __shared__ float bmax[NT / 32];
@@ -58,19 +107,7 @@ __global__ void __launch_bounds__(NT, 2) k_quant8(Quant8Args a, int vecx, int ve
         }
     }
     float rm[PER], cm[PER];   // maxima of the rows and of the columns
-#pragma unroll
-    for (int j = 0; j < PER; ++j) cm[j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        float v[PER];
-        unpack<PER>(raw[i], v);
-        rm[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            if (BLOCKS || ROWS) rm[i] = amax(rm[i], v[j]);
-            if (COLS && !BLOCKS) cm[j] = amax(cm[j], v[j]);
-        }
-    }
+    maxima<BLOCKS || ROWS, COLS && !BLOCKS>(raw, rm, cm);
     if (BLOCKS) {
         float m = rm[0];
 #pragma unroll
@@ -121,12 +158,7 @@ __global__ void __launch_bounds__(NT, 2) k_quant8(Quant8Args a, int vecx, int ve
             unpack<PER>(raw[i], v);
             uint32_t w[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float x[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) x[z] = v[4 * j + z] * f.by * f.inv;
-                w[j] = pack4(x);
-            }
+            for (int j = 0; j < 2; ++j) w[j] = round4(make_float2(v[4 * j], v[4 * j + 1]), make_float2(v[4 * j + 2], v[4 * j + 3]), f);
             if (r0 + i >= a.rows) continue;
             uint8_t* q = a.q + (int64_t)(r0 + i) * a.ldq + c0;
             if (cols == PER && vecq) {
@@ -151,9 +183,9 @@ __global__ void __launch_bounds__(NT, 2) k_quant8(Quant8Args a, int vecx, int ve
                 for (int z = 0; z < 4; ++z) {
                     float v[PER];
                     unpack<PER>(raw[4 * i + z], v);
-                    x[z] = v[j] * f.by * f.inv;
+                    x[z] = v[j];
                 }
-                w[i] = pack4(x);
+                w[i] = round4(make_float2(x[0], x[1]), make_float2(x[2], x[3]), f);
             }
             turn[lx * PER + j][ty ^ lx] = make_uint2(w[0], w[1]);
         }

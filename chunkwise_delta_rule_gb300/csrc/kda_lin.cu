@@ -366,13 +366,16 @@ cudaError_t run(const LinArgs& a, cudaStream_t st) {
 template <typename TI>
 cudaError_t pick(const LinArgs& a, cudaStream_t st) {
     if (is_step(a)) return run_step<TI>(a, st);
-    int kmax = 1, vmax = 1;
+    int kmax = 1;
+    long long narrow = 0, wide = 0;   // columns that slices of 64 and of 128 walk
     for (int i = 0; i < a.calls; ++i) {
         kmax = a.c[i].K > kmax ? a.c[i].K : kmax;
-        vmax = a.c[i].V > vmax ? a.c[i].V : vmax;
+        narrow += (a.c[i].V + 63) / 64 * 64;
+        wide += (a.c[i].V + 127) / 128 * 128;
     }
-    if (kmax <= 64) return vmax <= 64 ? run<TI, 8, 2, 8>(a, st) : run<TI, 8, 4, 8>(a, st);
-    if (kmax <= 128) return vmax <= 64 ? run<TI, 16, 2, 8>(a, st) : run<TI, 16, 4, 8>(a, st);
+    if (kmax <= 64) return narrow < wide ? run<TI, 8, 2, 8>(a, st) : run<TI, 8, 4, 8>(a, st);
+    if (kmax <= 96) return narrow < wide ? run<TI, 12, 2, 8>(a, st) : run<TI, 12, 4, 8>(a, st);
+    if (kmax <= 128) return narrow < wide ? run<TI, 16, 2, 8>(a, st) : run<TI, 16, 4, 8>(a, st);
     return run<TI, 32, 2, 4>(a, st);
 }
 
@@ -389,10 +392,10 @@ __global__ void __launch_bounds__(256) k_lin_heads(const float* part, TI* out, i
 
 }  // namespace
 
-// Windows per row: as many as keep `ctas` per window below two CTAs on each SM, of 64 tokens at least.
+// Windows per row: as many as keep `ctas` per window below three CTAs on each SM, of 64 tokens at least.
 int lin_units(int rows, int len, int ctas) {
     const long long all = (long long)rows * ctas;
-    int n = (int)(2LL * sm_count() / (all > 0 ? all : 1));
+    int n = (int)(3LL * sm_count() / (all > 0 ? all : 1));
     if (n > len / 64) n = len / 64;
     return n > 1 ? n : 1;
 }

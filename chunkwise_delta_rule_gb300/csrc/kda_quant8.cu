@@ -87,7 +87,7 @@ __device__ __forceinline__ void maxima(const Raw<float, 8> (&raw)[8], float (&rm
 template <typename TI, bool BLOCKS, bool ROWS, bool COLS>
 __global__ void __launch_bounds__(NT, sizeof(TI) == 2 ? 3 : 2) k_quant8(Quant8Args a, int vecx, int vecq, int vect) {
     __shared__ __align__(16) uint2 turn[COLS ? TILE : 1][COLS ? TILE / PER : 1];
-    __shared__ float cmax[COLS && !BLOCKS ? NT / 32 : 1][COLS && !BLOCKS ? TILE : 1];
+    __shared__ __align__(16) float cmax[COLS && !BLOCKS ? NT / 32 : 1][COLS && !BLOCKS ? TILE : 1];   // then row 0: the columns' 448 / m
     __shared__ float bmax[NT / 32];
     const int lx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r0 = blockIdx.y * TILE + ty * PER, c0 = blockIdx.x * TILE + lx * PER;   // this thread's values
@@ -107,6 +107,8 @@ __global__ void __launch_bounds__(NT, sizeof(TI) == 2 ? 3 : 2) k_quant8(Quant8Ar
         }
     }
     float rm[PER], cm[PER];   // maxima of the rows and of the columns
+    Factor rf[PER], cf[PER];  // and their groups' factors
+    bool odd_rows = false;
     maxima<BLOCKS || ROWS, COLS && !BLOCKS>(raw, rm, cm);
     if (BLOCKS) {
         float m = rm[0];
@@ -118,19 +120,32 @@ __global__ void __launch_bounds__(NT, sizeof(TI) == 2 ? 3 : 2) k_quant8(Quant8Ar
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < NT / 32; ++w) m = amax(m, bmax[w]);
+        const Factor f = factor(m);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) rm[i] = cm[i] = m;
+        for (int i = 0; i < PER; ++i) rf[i] = cf[i] = f;
         if (threadIdx.x == 0) {
             if (ROWS) a.scale[(size_t)blockIdx.y * gd + blockIdx.x] = m / FP8_MAX;
             if (COLS) a.scale_t[(size_t)blockIdx.x * gr + blockIdx.y] = m / FP8_MAX;
         }
     } else {
         if (ROWS) {
+            // 8 maxima over 16 lanes: at each exchange a lane goes on with half of the rows, until it has one
+            float m4[4], m2[2];
+            const bool b3 = lx & 8, b2 = lx & 4, b1 = lx & 2;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
+            for (int i = 0; i < 4; ++i) m4[i] = amax(b3 ? rm[4 + i] : rm[i], __shfl_xor_sync(FULL, b3 ? rm[i] : rm[4 + i], 8));
 #pragma unroll
-                for (int o = 8; o; o >>= 1) rm[i] = amax(rm[i], __shfl_xor_sync(FULL, rm[i], o));
-                if (lx == 0 && r0 + i < a.rows) a.scale[(size_t)(r0 + i) * gd + blockIdx.x] = rm[i] / FP8_MAX;
+            for (int i = 0; i < 2; ++i) m2[i] = amax(b2 ? m4[2 + i] : m4[i], __shfl_xor_sync(FULL, b2 ? m4[i] : m4[2 + i], 4));
+            float m = amax(b1 ? m2[1] : m2[0], __shfl_xor_sync(FULL, b1 ? m2[0] : m2[1], 2));
+            m = amax(m, __shfl_xor_sync(FULL, m, 1));
+            const int i = lx >> 1;   // this lane's row
+            if (!(lx & 1) && r0 + i < a.rows) a.scale[(size_t)(r0 + i) * gd + blockIdx.x] = m / FP8_MAX;
+            const Factor f = factor(m);
+            odd_rows = __any_sync(FULL, f.by != 1.f);
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                rf[k].inv = __shfl_sync(FULL, f.inv, (lane & 16) | 2 * k);
+                rf[k].by = odd_rows ? __shfl_sync(FULL, f.by, (lane & 16) | 2 * k) : 1.f;
             }
         }
         if (COLS) {
@@ -140,20 +155,27 @@ __global__ void __launch_bounds__(NT, sizeof(TI) == 2 ? 3 : 2) k_quant8(Quant8Ar
                 if (lane < 16) cmax[warp][lx * PER + j] = cm[j];
             }
             __syncthreads();
+            int odd = 0;
+            if (threadIdx.x < TILE) {
+                float m = cmax[0][threadIdx.x];
 #pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                cm[j] = cmax[0][lx * PER + j];
-#pragma unroll
-                for (int w = 1; w < NT / 32; ++w) cm[j] = amax(cm[j], cmax[w][lx * PER + j]);
-                if (ty == 0 && j < cols) a.scale_t[(size_t)(c0 + j) * gr + blockIdx.y] = cm[j] / FP8_MAX;
+                for (int w = 1; w < NT / 32; ++w) m = amax(m, cmax[w][threadIdx.x]);
+                const int c = blockIdx.x * TILE + threadIdx.x;
+                if (c < a.D) a.scale_t[(size_t)c * gr + blockIdx.y] = m / FP8_MAX;
+                const Factor f = factor(m);
+                cmax[0][threadIdx.x] = f.inv;
+                cmax[1][threadIdx.x] = f.by;
+                odd = f.by != 1.f;
             }
+            odd = __syncthreads_or(odd);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) cf[j] = {odd ? cmax[1][lx * PER + j] : 1.f, cmax[0][lx * PER + j]};
         }
     }
     if (ROWS) {
-        Factor f = factor(rm[0]);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            if (!BLOCKS && i) f = factor(rm[i]);
+            const Factor f = rf[i];
             float v[PER];
             unpack<PER>(raw[i], v);
             uint32_t w[2];
@@ -171,10 +193,9 @@ __global__ void __launch_bounds__(NT, sizeof(TI) == 2 ? 3 : 2) k_quant8(Quant8Ar
         }
     }
     if (COLS) {
-        Factor f = factor(cm[0]);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            if (!BLOCKS && j) f = factor(cm[j]);
+            const Factor f = cf[j];
             uint32_t w[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {

@@ -22,7 +22,8 @@ namespace kda {
 namespace {
 
 constexpr int C = 128, VB = 64;                 // tokens of a chunk, value columns of a CTA
-constexpr int NTHR = 14 * 32, LOADER = 12, ISSUER = 13;   // warps of the last two roles
+constexpr int NTHR = 18 * 32, LOADER = 16, ISSUER = 17;   // warps of the last two roles
+constexpr int SV = 32;                          // columns of the state that a thread keeps
 constexpr int ATOM = C * 128;                   // bytes of 128 rows of 64 bf16
 constexpr int OFF_K = 2 * ATOM, OFF_V = 4 * ATOM, STAGE = 5 * ATOM;
 constexpr int OFF_VP = 2 * STAGE, OFF_S = OFF_VP + 3 * ATOM, OFF_END = OFF_S + ATOM;
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
     if (unit >= a.ax.rows * a.units_row) return;
     const int row = unit / a.units_row, u = unit - row * a.units_row;
     const int t0 = u * a.unit_len, t1 = min(a.ax.len, t0 + a.unit_len);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, role = warp >> 2, q32 = (warp & 3) * 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, role = warp < 4 ? 0 : warp < 12 ? 1 : warp < 16 ? 2 : 3, q32 = (warp & 3) * 32;
     const int KA = c.K > 64 ? 2 : 1;
     const float decay = a.decay ? a.decay[h] : 0.f;
 
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             tc::mbar_init(&sm.sc_free, 4);
             tc::mbar_init(&sm.p_full, 4);
             tc::mbar_init(&sm.v_full, 4);
-            tc::mbar_init(&sm.s_full, 4);
+            tc::mbar_init(&sm.s_full, 8);
             tc::mbar_init(&sm.o_free, 4);
             sm.dead = 0;
             tc::fence_mbar_init();
@@ -277,11 +278,11 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             k.next(n);
         }
     } else if (role == 1) {
-        // ---------------------------------------------------------------- the state; this thread's key row
-        const int kk = q32 + lane;
-        const size_t KV = (size_t)c.K * c.V, mine = (size_t)kk * c.V + v0;   // a state's elements, and this row's place in it
-        const int cols = kk < c.K ? min(VB, c.V - v0) : 0;                   // a multiple of 8
-        float S[VB];
+        // ---------------------------------------------------------------- the state; this thread's key row, 32 columns
+        const int kk = q32 + lane, s0 = v0 + (warp < 8 ? 0 : SV);
+        const size_t KV = (size_t)c.K * c.V, mine = (size_t)kk * c.V + s0;   // a state's elements, and this row's place in it
+        const int cols = kk < c.K ? min(SV, c.V - s0) : 0;                   // a multiple of 8, or less than 0
+        float S[SV];
         if (u == 0 && !LOCAL && c.s1) {   // final states of sequences without tokens
             for (int n = a.ax.cu ? 0 : row; n < (a.ax.cu ? a.ax.N : row + 1); ++n) {
                 if (a.ax.cu ? axis_cu(a.ax, n + 1) > axis_cu(a.ax, n) : a.ax.len > 0) continue;
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         auto store_state = [&](float* p) {
             const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 #pragma unroll
-            for (int v = 0; v < VB; v += 4) {
+            for (int v = 0; v < SV; v += 4) {
                 if (v >= cols) break;
                 if (vec) {
                     *reinterpret_cast<float4*>(p + v) = make_float4(S[v], S[v + 1], S[v + 2], S[v + 3]);
@@ -309,23 +310,23 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         whole.y = __shfl_sync(0xffffffffu, whole.y, 0);
         uint32_t ph = 0;
         int seq = -1;
-        const uint32_t tk = tc::taddr(tb, q32, T_KV);
+        const uint32_t tk = tc::taddr(tb, q32, T_KV + s0 - v0);
         unsigned char* sb = mem + OFF_S + kk * 128;
         for (Chunks k(a, row, t0, t1, back, LOCAL); k.more(); ph ^= 1) {
             const int n = k.n();
             if (LOCAL) {
                 if (seq < 0) {
 #pragma unroll
-                    for (int v = 0; v < VB; ++v) S[v] = 0.f;
+                    for (int v = 0; v < SV; ++v) S[v] = 0.f;
                 }
                 seq = k.s.n;
             } else {
                 if (seq < 0 || k.t == k.s.first) {
                     const size_t rk = c.transposed ? 1 : c.V, rv = c.transposed ? c.K : 1;
-                    const float* p = c.s0 + ((size_t)k.s.n * a.HV + h) * KV + kk * rk + v0 * rv;
+                    const float* p = c.s0 + ((size_t)k.s.n * a.HV + h) * KV + kk * rk + s0 * rv;
                     const bool has = c.s0 != nullptr;
 #pragma unroll
-                    for (int v = 0; v < VB; ++v) {
+                    for (int v = 0; v < SV; ++v) {
                         S[v] = has && v < cols ? *p : 0.f;
                         p += rv;
                     }
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                         const float f = lin_power(decay, (e + 1) * a.unit_len - max(k.s.first, e * a.unit_len));
                         const float* y = c.local + ((size_t)(unit - u + e) * a.HV + h) * KV + mine;
 #pragma unroll
-                        for (int v = 0; v < VB; v += 4) {
+                        for (int v = 0; v < SV; v += 4) {
                             if (v >= cols) break;
                             const float4 x = *reinterpret_cast<const float4*>(y + v);
                             S[v] = fmaf(S[v], f, x.x);
@@ -345,13 +346,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 }
                 seq = k.s.n;
 #pragma unroll
-                for (int v = 0; v < VB; v += 8) {
+                for (int v = 0; v < SV; v += 8) {
                     uint4 x;
                     x.x = tc::pack_bf16(S[v], S[v + 1]);
                     x.y = tc::pack_bf16(S[v + 2], S[v + 3]);
                     x.z = tc::pack_bf16(S[v + 4], S[v + 5]);
                     x.w = tc::pack_bf16(S[v + 6], S[v + 7]);
-                    *reinterpret_cast<uint4*>(sb + (((v >> 3) ^ (kk & 7)) << 4)) = x;
+                    *reinterpret_cast<uint4*>(sb + (((((s0 - v0 + v) >> 3)) ^ (kk & 7)) << 4)) = x;
                 }
                 tc::fence_async_smem();
             }
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             tc::fence_after_sync();
             const float2 an = n == C ? whole : make_float2(sm.pw[n], 0.f);
 #pragma unroll
-            for (int v = 0; v < VB; v += 8) {
+            for (int v = 0; v < SV; v += 8) {
                 float x[NP][8];
 #pragma unroll
                 for (int i = 0; i < NP; ++i) tc::tmem_ld8(tk + VB * i + v, x[i]);
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             unsigned char* to = mem + OFF_VP + j * 128;
             if (j < n) {
                 const float e = c.w * sm.pw[back ? j + 1 : n - 1 - j];
-#pragma unroll 2
+#pragma unroll 1
                 for (int ch = 0; ch < 8; ++ch) {
                     const uint32_t o = (ch ^ (j & 7)) << 4;
                     const uint4 v = *reinterpret_cast<const uint4*>(vr + o);

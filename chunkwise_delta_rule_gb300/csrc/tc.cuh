@@ -342,6 +342,11 @@ __device__ __forceinline__ void tmem_st16u(uint32_t a, const uint32_t (&v)[16]) 
         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st8u(uint32_t a, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t a, const float (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -429,6 +434,17 @@ __device__ __forceinline__ void mma4_bf16_w(uint32_t d, uint64_t a, uint64_t b, 
         "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %9;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t"
         "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %10;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t}"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(SA), "n"(2 * SA), "n"(3 * SA), "n"(SB), "n"(2 * SB), "n"(3 * SB)
+        : "memory");
+}
+// Two of them.
+template <bool AMN, bool BMN>
+__device__ __forceinline__ void mma2_bf16_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, yes;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(AMN ? 128 : 2), "n"(BMN ? 128 : 2)
         : "memory");
 }
 // The same with K-major operands of 8 bits (e4m3): K = 128 bytes, one 128-byte row of each.

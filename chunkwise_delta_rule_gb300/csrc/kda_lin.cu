@@ -131,18 +131,9 @@ __global__ void __launch_bounds__(NT, KR * VEC >= 64 ? 1 : 2) k_lin(LinArgs a, i
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) S[r][i] = 0.f;
         } else {
-            start_state(s.n);
-            if (s.first < t) {   // it came through earlier windows
-                for (int e = s.first / a.unit_len; e < u; ++e) {
-                    const float f = lin_power(g, (e + 1) * a.unit_len - max(s.first, e * a.unit_len));
-                    const float* p = c.local + ((size_t)(unit - u + e) * a.HV + h) * KV;
-#pragma unroll
-                    for (int r = 0; r < KR; ++r)
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i)
-                            if (k0 + r < c.K && vl + i < c.V) S[r][i] = fmaf(S[r][i], f, p[(size_t)(k0 + r) * c.V + vl + i]);
-                }
-            }
+            // (in the first window nothing has, whatever inconsistent offsets say)
+            if (first && u > 0 && s.first < t) load_state(c.local + ((size_t)(unit - 1) * a.HV + h) * KV, VEC > 1 && c.V % VEC == 0, c.V, 1);   // it came through earlier windows
+            else start_state(s.n);
         }
         if (first && warp == NW - 1 && lane <= TG) pw[lane] = lin_power2(g, lane);
         first = false;
@@ -357,8 +348,8 @@ cudaError_t run(const LinArgs& a, cudaStream_t st) {
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)ctas, a.calls);
     if (a.units_row > 1) {
-        const cudaError_t e = traced_launch("k_lin_windows", st, [&] { k_lin<TI, KR, VEC, TG><<<grid, NT, 0, st>>>(a, 1); });
-        if (e != cudaSuccess) return e;
+        cudaError_t e = traced_launch("k_lin_windows", st, [&] { k_lin<TI, KR, VEC, TG><<<grid, NT, 0, st>>>(a, 1); });
+        if (e != cudaSuccess || (e = launch_lin_join(a, st)) != cudaSuccess) return e;
     }
     return traced_launch("k_lin", st, [&] { k_lin<TI, KR, VEC, TG><<<grid, NT, 0, st>>>(a, 0); });
 }
@@ -377,6 +368,36 @@ cudaError_t pick(const LinArgs& a, cudaStream_t st) {
     if (kmax <= 96) return narrow < wide ? run<TI, 12, 2, 8>(a, st) : run<TI, 12, 4, 8>(a, st);
     if (kmax <= 128) return narrow < wide ? run<TI, 16, 2, 8>(a, st) : run<TI, 16, 4, 8>(a, st);
     return run<TI, 32, 2, 4>(a, st);
+}
+
+// One state element of a head through a row's windows, 8 windows' values on their way at a time: behind window e the state
+// is a^n (the state that entered, or that the sequence started from) + the window's own, n its tokens of the sequence.
+__global__ void __launch_bounds__(256) k_lin_join(LinArgs a) {
+    const LinCall& c = a.c[blockIdx.z];
+    const int row = blockIdx.y / a.HV, h = blockIdx.y % a.HV;
+    const int x = blockIdx.x * 256 + threadIdx.x, KV = c.K * c.V;
+    if (x >= KV) return;
+    const float g = a.decay ? a.decay[h] : 0.f;
+    const size_t step = (size_t)a.HV * KV;
+    float* p = c.local + ((size_t)row * a.units_row * a.HV + h) * KV + x;
+    const int from = c.transposed ? x % c.V * c.K + x / c.V : x;   // in s0
+    float S = 0.f;
+    constexpr int AHEAD = 8;
+    for (int e0 = 0; e0 < a.units_row - 1; e0 += AHEAD) {
+        float own[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) own[i] = e0 + i < a.units_row - 1 ? p[(size_t)(e0 + i) * step] : 0.f;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int e = e0 + i, t1 = (e + 1) * a.unit_len;
+            if (e >= a.units_row - 1) break;
+            const Seq s = lin_seq(a.ax, row, t1 - 1, c.back);
+            if (s.end <= t1) continue;   // nothing goes on
+            if (s.first >= e * a.unit_len) S = c.s0 ? c.s0[((size_t)s.n * a.HV + h) * KV + from] : 0.f;
+            S = fmaf(S, lin_power(g, t1 - max(s.first, e * a.unit_len)), own[i]);
+            p[(size_t)e * step] = S;
+        }
+    }
 }
 
 template <typename TI>
@@ -402,6 +423,13 @@ int lin_units(int rows, int len, int ctas) {
 
 cudaError_t launch_lin(const LinArgs& a, int bf16, cudaStream_t st) {
     return bf16 ? pick<__nv_bfloat16>(a, st) : pick<float>(a, st);
+}
+
+cudaError_t launch_lin_join(const LinArgs& a, cudaStream_t st) {
+    int most = 0;
+    for (int i = 0; i < a.calls; ++i) most = a.c[i].K * a.c[i].V > most ? a.c[i].K * a.c[i].V : most;
+    if ((long long)a.ax.rows * a.HV > 65535) return cudaErrorInvalidConfiguration;
+    return traced_launch("k_lin_join", st, [&] { k_lin_join<<<dim3((most + 255) / 256, a.ax.rows * a.HV, a.calls), 256, 0, st>>>(a); });
 }
 
 cudaError_t launch_lin_heads(const float* part, void* out, int64_t rows, int group, int width, int bf16, cudaStream_t st) {

@@ -22,7 +22,7 @@ struct LinCall {
     int transposed;            // s0 is [V][K]
     int back;
     float s, w;                // the formulas' s and w
-    float* local;              // [windows][HV][K][V]: end states of the windows' own tokens
+    float* local;              // [windows][HV][K][V]: end states of the windows' own tokens, then the states they hand on
 };
 
 struct LinArgs {
@@ -69,6 +69,8 @@ constexpr int LIN_TC_TOKENS = 32;
 int lin_tc_window(int rows, int len, int ctas);
 bool lin_tc_call(const LinCall& c);
 cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st);
+// Turns the windows' own end states into the states that the next windows' first sequences enter with.
+cudaError_t launch_lin_join(const LinArgs& a, cudaStream_t st);
 // out[t][h][:] = sum over the group's value heads of part[t][h * group + i][:], in order.
 cudaError_t launch_lin_heads(const float* part, void* out, int64_t rows, int group, int width, int bf16, cudaStream_t st);
 

@@ -71,8 +71,87 @@ struct Chunks {
     }
 };
 
-// LOCAL: the end states of the windows' own tokens only. NP: parts of V'.
-template <bool LOCAL, int NP>
+// Row j of V' from row j of V: e v in NP parts of 8 bits, the leading ones of what is left cut off, the last one rounded
+// (the third is the rest). A row behind the chunk's n tokens becomes zeros in V, V' and the keys' KA tiles.
+template <int NP>
+__device__ __forceinline__ void spread(unsigned char* v, unsigned char* vp, unsigned char* k, int KA, int j, int n, float e) {
+    v += j * 128;
+    vp += j * 128;
+    if (j < n) {
+#pragma unroll 1
+        for (int ch = 0; ch < 8; ++ch) {
+            const uint32_t o = (ch ^ (j & 7)) << 4;
+            const uint4 x4 = *reinterpret_cast<const uint4*>(v + o);
+            const uint32_t in[4] = {x4.x, x4.y, x4.z, x4.w};
+            uint32_t out[NP][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 x = mul2(make_float2(e, e), make_float2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)));
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    const uint32_t lo = __float_as_uint(x.x), hi = __float_as_uint(x.y);
+                    out[p][i] = p == NP - 1 ? tc::pack_bf16(x.x, x.y) : __byte_perm(lo, hi, 0x7632);
+                    x = add2(x, make_float2(-__uint_as_float(lo & 0xffff0000u), -__uint_as_float(hi & 0xffff0000u)));
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(vp + p * ATOM + o) = make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
+        }
+    } else {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int ch = 0; ch < 8; ++ch) {
+            *reinterpret_cast<uint4*>(v + 16 * ch) = z;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(vp + p * ATOM + 16 * ch) = z;
+            for (int p = 0; p < KA; ++p) *reinterpret_cast<uint4*>(k + p * ATOM + j * 128 + 16 * ch) = z;
+        }
+    }
+}
+// This thread's SV columns of the state behind a chunk: an S + the chunk's sums, NP parts of them in TMEM.
+template <int NP>
+__device__ __forceinline__ void advance(float (&S)[SV], uint32_t sums, float2 an) {
+#pragma unroll
+    for (int v = 0; v < SV; v += 8) {
+        float x[NP][8];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) tc::tmem_ld8(sums + VB * i + v, x[i]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            float2 y = make_float2(x[1][i], x[1][i + 1]);
+            if (NP == 3) y = add2(y, make_float2(x[NP - 1][i], x[NP - 1][i + 1]));
+            y = add2(make_float2(x[0][i], x[0][i + 1]), y);
+            const float2 z = make_float2(S[v + i], S[v + i + 1]);
+            y = fma2(z, make_float2(an.x, an.x), fma2(z, make_float2(an.y, an.y), y));
+            S[v + i] = y.x;
+            S[v + i + 1] = y.y;
+        }
+    }
+}
+// Stores the first `cols` (a multiple of 8, or none) of them.
+__device__ __forceinline__ void store_columns(float* p, const float (&S)[SV], int cols) {
+    const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+#pragma unroll
+    for (int v = 0; v < SV; v += 4) {
+        if (v >= cols) break;
+        if (vec) {
+            *reinterpret_cast<float4*>(p + v) = make_float4(S[v], S[v + 1], S[v + 2], S[v + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[v + i] = S[v + i];
+        }
+    }
+}
+// a^C in two parts, formed by one lane.
+__device__ __forceinline__ float2 whole_power(float decay, int lane) {
+    float2 x;
+    if (lane == 0) x = lin_power2(decay, C);
+    return make_float2(__shfl_sync(0xffffffffu, x.x, 0), __shfl_sync(0xffffffffu, x.y, 0));
+}
+
+// NP: parts of V'.
+template <int NP>
 __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinTc g) {
     extern __shared__ unsigned char raw[];
     const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
@@ -98,10 +177,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
     const CUtensorMap *mq = &g.map[g.mq[blockIdx.y]], *mk = &g.map[g.mk[blockIdx.y]], *mv = &g.map[g.mv[blockIdx.y]];
     const int hq = h / c.gq, hk = h / c.gk, hv = h / c.gv;
     const auto load_q = [&](int st, int z) {
-        for (int p = 0; p < (LOCAL ? 0 : KA); ++p) tc::tma_load3(base + st * STAGE + p * ATOM, mq, 64 * p, hq, z, &sm.full[st]);
+        for (int p = 0; p < KA; ++p) tc::tma_load3(base + st * STAGE + p * ATOM, mq, 64 * p, hq, z, &sm.full[st]);
     };
     const auto load_k = [&](int st, int z) {
-        tc::mbar_arrive_expect_tx(&sm.full[st], ((LOCAL ? 1 : 2) * KA + 1) * ATOM);
+        tc::mbar_arrive_expect_tx(&sm.full[st], (2 * KA + 1) * ATOM);
         for (int p = 0; p < KA; ++p) tc::tma_load3(base + st * STAGE + OFF_K + p * ATOM, mk, 64 * p, hk, z, &sm.full[st]);
     };
     const auto load_v = [&](int st, int z) { tc::tma_load3(base + st * STAGE + OFF_V, mv, v0, hv, z, &sm.full[st]); };
@@ -124,7 +203,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             tc::mbar_init(&sm.o_free, 4);
             sm.dead = 0;
             tc::fence_mbar_init();
-            Chunks k(a, row, t0, t1, back, LOCAL);
+            Chunks k(a, row, t0, t1, back, false);
             for (int i = 0; i < 2 && k.more(); ++i) {
                 const int n = k.n(), z = (int)k.token(n);
                 load_k(i, z);
@@ -150,7 +229,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
     tc::fence_after_sync();
     const uint32_t tb = sm.tmem;
 
-    if (role == 0 && !LOCAL) {
+    if (role == 0) {
         // ---------------------------------------------------------------- scores to P; this thread's row i
         const int i = q32 + lane, w = warp;
         const float sw = c.s * c.w;
@@ -283,7 +362,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         const size_t KV = (size_t)c.K * c.V, mine = (size_t)kk * c.V + s0;   // a state's elements, and this row's place in it
         const int cols = kk < c.K ? min(SV, c.V - s0) : 0;                   // a multiple of 8, or less than 0
         float S[SV];
-        if (u == 0 && !LOCAL && c.s1) {   // final states of sequences without tokens
+        if (u == 0 && c.s1) {   // final states of sequences without tokens
             for (int n = a.ax.cu ? 0 : row; n < (a.ax.cu ? a.ax.N : row + 1); ++n) {
                 if (a.ax.cu ? axis_cu(a.ax, n + 1) > axis_cu(a.ax, n) : a.ax.len > 0) continue;
                 const size_t to = ((size_t)n * a.HV + h) * KV + mine;
@@ -291,142 +370,55 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 for (int v = 0; v < cols; ++v) c.s1[to + v] = c.s0 ? c.s0[to + v] : 0.f;   // (a call with s1 has natural states)
             }
         }
-        auto store_state = [&](float* p) {
-            const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-#pragma unroll
-            for (int v = 0; v < SV; v += 4) {
-                if (v >= cols) break;
-                if (vec) {
-                    *reinterpret_cast<float4*>(p + v) = make_float4(S[v], S[v + 1], S[v + 2], S[v + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) p[v + i] = S[v + i];
-                }
-            }
-        };
-        float2 whole;   // a^C
-        if (lane == 0) whole = lin_power2(decay, C);
-        whole.x = __shfl_sync(0xffffffffu, whole.x, 0);
-        whole.y = __shfl_sync(0xffffffffu, whole.y, 0);
+        const float2 whole = whole_power(decay, lane);
         uint32_t ph = 0;
         int seq = -1;
         const uint32_t tk = tc::taddr(tb, q32, T_KV + s0 - v0);
         unsigned char* sb = mem + OFF_S + kk * 128;
-        for (Chunks k(a, row, t0, t1, back, LOCAL); k.more(); ph ^= 1) {
+        for (Chunks k(a, row, t0, t1, back, false); k.more(); ph ^= 1) {
             const int n = k.n();
-            if (LOCAL) {
-                if (seq < 0) {
+            if (seq < 0 || k.t == k.s.first) {   // a sequence that came through earlier windows goes on from the state joined there
+                const bool joined = seq < 0 && u > 0 && k.s.first < k.t;   // (in the first window none, whatever inconsistent offsets say)
+                const size_t rk = c.transposed && !joined ? 1 : c.V, rv = c.transposed && !joined ? c.K : 1;
+                const float* p = (joined ? c.local + ((size_t)(unit - 1) * a.HV + h) * KV : c.s0 + ((size_t)k.s.n * a.HV + h) * KV) + kk * rk + s0 * rv;
+                const bool has = joined || c.s0;
 #pragma unroll
-                    for (int v = 0; v < SV; ++v) S[v] = 0.f;
+                for (int v = 0; v < SV; ++v) {
+                    S[v] = has && v < cols ? *p : 0.f;
+                    p += rv;
                 }
-                seq = k.s.n;
-            } else {
-                if (seq < 0 || k.t == k.s.first) {
-                    const size_t rk = c.transposed ? 1 : c.V, rv = c.transposed ? c.K : 1;
-                    const float* p = c.s0 + ((size_t)k.s.n * a.HV + h) * KV + kk * rk + s0 * rv;
-                    const bool has = c.s0 != nullptr;
-#pragma unroll
-                    for (int v = 0; v < SV; ++v) {
-                        S[v] = has && v < cols ? *p : 0.f;
-                        p += rv;
-                    }
-                    for (int e = k.s.first < k.t ? k.s.first / a.unit_len : u; e < u; ++e) {   // it came through earlier windows
-                        const float f = lin_power(decay, (e + 1) * a.unit_len - max(k.s.first, e * a.unit_len));
-                        const float* y = c.local + ((size_t)(unit - u + e) * a.HV + h) * KV + mine;
-#pragma unroll
-                        for (int v = 0; v < SV; v += 4) {
-                            if (v >= cols) break;
-                            const float4 x = *reinterpret_cast<const float4*>(y + v);
-                            S[v] = fmaf(S[v], f, x.x);
-                            S[v + 1] = fmaf(S[v + 1], f, x.y);
-                            S[v + 2] = fmaf(S[v + 2], f, x.z);
-                            S[v + 3] = fmaf(S[v + 3], f, x.w);
-                        }
-                    }
-                }
-                seq = k.s.n;
-#pragma unroll
-                for (int v = 0; v < SV; v += 8) {
-                    uint4 x;
-                    x.x = tc::pack_bf16(S[v], S[v + 1]);
-                    x.y = tc::pack_bf16(S[v + 2], S[v + 3]);
-                    x.z = tc::pack_bf16(S[v + 4], S[v + 5]);
-                    x.w = tc::pack_bf16(S[v + 6], S[v + 7]);
-                    *reinterpret_cast<uint4*>(sb + (((((s0 - v0 + v) >> 3)) ^ (kk & 7)) << 4)) = x;
-                }
-                tc::fence_async_smem();
             }
+            seq = k.s.n;
+#pragma unroll
+            for (int v = 0; v < SV; v += 8) {
+                uint4 x;
+                x.x = tc::pack_bf16(S[v], S[v + 1]);
+                x.y = tc::pack_bf16(S[v + 2], S[v + 3]);
+                x.z = tc::pack_bf16(S[v + 4], S[v + 5]);
+                x.w = tc::pack_bf16(S[v + 6], S[v + 7]);
+                *reinterpret_cast<uint4*>(sb + (((((s0 - v0 + v) >> 3)) ^ (kk & 7)) << 4)) = x;
+            }
+            tc::fence_async_smem();
             tc::fence_before_sync();
             tc::warp_arrive(&sm.s_full);
             if (!wait(sm, &sm.kv_done, ph)) break;
             tc::fence_after_sync();
-            const float2 an = n == C ? whole : make_float2(sm.pw[n], 0.f);
-#pragma unroll
-            for (int v = 0; v < SV; v += 8) {
-                float x[NP][8];
-#pragma unroll
-                for (int i = 0; i < NP; ++i) tc::tmem_ld8(tk + VB * i + v, x[i]);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    float2 y = make_float2(x[1][i], x[1][i + 1]);
-                    if (NP == 3) y = add2(y, make_float2(x[NP - 1][i], x[NP - 1][i + 1]));
-                    y = add2(make_float2(x[0][i], x[0][i + 1]), y);
-                    const float2 z = make_float2(S[v + i], S[v + i + 1]);
-                    y = fma2(z, make_float2(an.x, an.x), fma2(z, make_float2(an.y, an.y), y));
-                    S[v + i] = y.x;
-                    S[v + i + 1] = y.y;
-                }
-            }
-            if (!LOCAL && k.t + n == k.s.end && c.s1) store_state(c.s1 + ((size_t)k.s.n * a.HV + h) * KV + mine);
+            advance<NP>(S, tk, n == C ? whole : make_float2(sm.pw[n], 0.f));
+            if (k.t + n == k.s.end && c.s1) store_columns(c.s1 + ((size_t)k.s.n * a.HV + h) * KV + mine, S, cols);
             k.next(n);
         }
-        if (LOCAL && seq >= 0) store_state(c.local + ((size_t)unit * a.HV + h) * KV + mine);
     } else if (role == 2) {
         // ------------------------------------------------ V' in three parts, and outputs; this thread's token row
         const int j = q32 + lane;
         uint32_t ph = 0, stage = 0, fph = 0;
         bool first = true;
-        for (Chunks k(a, row, t0, t1, back, LOCAL); k.more();) {
+        for (Chunks k(a, row, t0, t1, back, false); k.more();) {
             const int n = k.n();
             unsigned char* st = mem + stage * STAGE;
             if (!wait(sm, &sm.full[stage], fph)) break;
             if (!first && !wait(sm, &sm.kv_done, ph ^ 1)) break;
             first = false;
-            unsigned char* vr = st + OFF_V + j * 128;
-            unsigned char* to = mem + OFF_VP + j * 128;
-            if (j < n) {
-                const float e = c.w * sm.pw[back ? j + 1 : n - 1 - j];
-#pragma unroll 1
-                for (int ch = 0; ch < 8; ++ch) {
-                    const uint32_t o = (ch ^ (j & 7)) << 4;
-                    const uint4 v = *reinterpret_cast<const uint4*>(vr + o);
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t out[NP][4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float2 x = mul2(make_float2(e, e), make_float2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)));
-#pragma unroll
-                        for (int p = 0; p < NP; ++p) {   // the leading 8 bits of what is left, cut off: the third part is the rest
-                            const uint32_t lo = __float_as_uint(x.x), hi = __float_as_uint(x.y);
-                            out[p][i] = p == NP - 1 ? tc::pack_bf16(x.x, x.y) : __byte_perm(lo, hi, 0x7632);
-                            x = add2(x, make_float2(-__uint_as_float(lo & 0xffff0000u), -__uint_as_float(hi & 0xffff0000u)));
-                        }
-                    }
-#pragma unroll
-                    for (int p = 0; p < NP; ++p)
-                        *reinterpret_cast<uint4*>(to + p * ATOM + o) = make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
-                }
-            } else {
-                const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-                for (int ch = 0; ch < 8; ++ch) {
-                    *reinterpret_cast<uint4*>(vr + 16 * ch) = z;
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(to + p * ATOM + 16 * ch) = z;
-                    for (int p = 0; p < KA; ++p) *reinterpret_cast<uint4*>(st + OFF_K + p * ATOM + j * 128 + 16 * ch) = z;
-                }
-            }
+            spread<NP>(st + OFF_V, mem + OFF_VP, st + OFF_K, KA, j, n, c.w * sm.pw[j < n ? (back ? j + 1 : n - 1 - j) : 0]);
             tc::fence_async_smem();
             tc::warp_arrive(&sm.v_full);
             ph ^= 1;
@@ -438,7 +430,6 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         // ------------------------------------------------ loads, from the third chunk on, and whole chunks' outputs
         int n1 = 0, n2 = 0, z1 = 0, z2 = 0, issued = 0;   // the last two chunks' tokens and first rows
         const auto give = [&](int i, int n, int z) {      // the outputs of chunk i
-            if (LOCAL) return true;
             if (!wait(sm, &sm.o_ready[i & 1], (i >> 1) & 1)) return false;
             if (n == C && lane == 0) {
                 const uint32_t tile = base + (i & 1) * STAGE;
@@ -452,12 +443,12 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             return true;
         };
         bool ok = true;
-        Chunks k(a, row, t0, t1, back, LOCAL);
+        Chunks k(a, row, t0, t1, back, false);
         for (; k.more(); ++issued) {
             const int n = k.n(), z = (int)k.token(n), st = issued & 1;
             if (issued > 1) {
                 const uint32_t ph = ((issued >> 1) - 1) & 1;
-                if (!LOCAL && lane < KA) tc::tma_prefetch3(mq, 64 * lane, hq, z);   // their place is free last
+                if (lane < KA) tc::tma_prefetch3(mq, 64 * lane, hq, z);   // their place is free last
                 if (!(ok = wait(sm, &sm.k_free[st], ph))) break;
                 if (lane == 0) load_k(st, z);
                 ok = wait(sm, &sm.v_free[st], ph);
@@ -487,27 +478,23 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         uint32_t stage = 0, fph = 0, ph = 0;
         bool first = true, ok = true;
         const uint64_t dvp = tc::sdesc_mn(base + OFF_VP, ATOM, 0), dsb = tc::sdesc_mn(base + OFF_S, ATOM, 0);
-        for (Chunks k(a, row, t0, t1, back, LOCAL); k.more();) {
+        for (Chunks k(a, row, t0, t1, back, false); k.more();) {
             const int n = k.n();
             const uint32_t st = base + stage * STAGE;
             const uint64_t dq = tc::sdesc_k(st, C, 0), dk = tc::sdesc_k(st + OFF_K, C, 0);
             ok = wait(sm, &sm.full[stage], fph);
-            if (!LOCAL) {
-                if (ok && !first) ok = wait(sm, &sm.sc_free, ph ^ 1);
-                if (!ok) break;
-                tc::fence_after_sync();
-                tc::mma4_bf16_w<false, false>(tb + T_SC, dq, dk, I_SC, 0);
-                if (KA > 1) tc::mma4_bf16_w<false, false>(tb + T_SC, tc::kstep_k(dq, C, 4), tc::kstep_k(dk, C, 4), I_SC, 1);
-                tc::mma_commit_w(&sm.sc_full);
-            }
-            ok = ok && wait(sm, &sm.s_full, ph);
-            if (!LOCAL && ok && !first) ok = wait(sm, &sm.o_free, ph ^ 1);
+            if (ok && !first) ok = wait(sm, &sm.sc_free, ph ^ 1);
             if (!ok) break;
             tc::fence_after_sync();
-            if (!LOCAL) {
-                tc::mma4_bf16_w<false, true>(tb + T_O1, dq, dsb, I_O, 0);
-                if (KA > 1) tc::mma4_bf16_w<false, true>(tb + T_O1, tc::kstep_k(dq, C, 4), tc::kstep_mn(dsb, 4), I_O, 1);
-            }
+            tc::mma4_bf16_w<false, false>(tb + T_SC, dq, dk, I_SC, 0);
+            if (KA > 1) tc::mma4_bf16_w<false, false>(tb + T_SC, tc::kstep_k(dq, C, 4), tc::kstep_k(dk, C, 4), I_SC, 1);
+            tc::mma_commit_w(&sm.sc_full);
+            ok = wait(sm, &sm.s_full, ph);
+            if (ok && !first) ok = wait(sm, &sm.o_free, ph ^ 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            tc::mma4_bf16_w<false, true>(tb + T_O1, dq, dsb, I_O, 0);
+            if (KA > 1) tc::mma4_bf16_w<false, true>(tb + T_O1, tc::kstep_k(dq, C, 4), tc::kstep_mn(dsb, 4), I_O, 1);
             ok = wait(sm, &sm.v_full, ph);
             if (!ok) break;
             tc::fence_after_sync();
@@ -516,14 +503,12 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             tc::mma4_bf16_w<true, true>(tb + T_KV, tc::kstep_mn(dkt, 4), tc::kstep_mn(dvp, 4), I_KV, 1);
             tc::mma_commit_w(&sm.kv_done);
             tc::mma_commit_w(&sm.k_free[stage]);
-            if (!LOCAL) {
-                ok = wait(sm, &sm.p_full, ph);
-                if (!ok) break;
-                tc::fence_after_sync();
-                tc::mma4_bf16_ts_w(tb + T_O2, tb + T_P, dv, I_O, 0);
-                tc::mma4_bf16_ts_w(tb + T_O2, tb + T_P + 32, tc::kstep_mn(dv, 4), I_O, 1);
-                tc::mma_commit_w(&sm.pv_done);
-            }
+            ok = wait(sm, &sm.p_full, ph);
+            if (!ok) break;
+            tc::fence_after_sync();
+            tc::mma4_bf16_ts_w(tb + T_O2, tb + T_P, dv, I_O, 0);
+            tc::mma4_bf16_ts_w(tb + T_O2, tb + T_P + 32, tc::kstep_mn(dv, 4), I_O, 1);
+            tc::mma_commit_w(&sm.pv_done);
             tc::mma_commit_w(&sm.v_free[stage]);
             first = false;
             ph ^= 1;
@@ -542,25 +527,176 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
     if (warp == ISSUER) tc::tmem_dealloc(tb, 512);
 }
 
-template <bool LOCAL, int NP>
+// ------------------------------------------------------------------ the windows' own states
+// End states of the windows' own tokens, from zero: only the state's half of a chunk's work, two chunks at once (the
+// scores' warps form every other V', which has two places, as the sums have).
+constexpr int W_V = 2 * ATOM, W_STAGE = 3 * ATOM, W_VP = 2 * W_STAGE, W_END = W_VP + 6 * ATOM;
+struct WindowShared {
+    float pw[C + 1];
+    uint64_t full[2], v_full[2], kv_done[2], kv_free[2], drain;
+    uint32_t tmem;
+    int dead;
+};
+constexpr int W_SMEM = W_END + (int)sizeof(WindowShared) + 1024;
+static_assert(W_SMEM <= 232448, "shared memory above the per-block limit");
+
+template <int NP>
+__global__ void __launch_bounds__(NTHR, 1) k_lin_tc_windows(const __grid_constant__ LinTc g) {
+    extern __shared__ unsigned char raw[];
+    const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
+    unsigned char* mem = raw + (base - tc::smem_u32(raw));
+    WindowShared& sm = *reinterpret_cast<WindowShared*>(mem + W_END);
+    const LinArgs& a = g.a;
+    const LinCall& c = a.c[blockIdx.y];
+    const int blocks = (c.V + VB - 1) / VB;
+    int at = blockIdx.x;
+    const int v0 = at % blocks * VB;
+    at /= blocks;
+    const int h = at % a.HV, unit = at / a.HV;
+    if (unit >= a.ax.rows * a.units_row) return;
+    const int row = unit / a.units_row, u = unit - row * a.units_row;
+    if (u == a.units_row - 1) return;   // nothing comes behind a row's last window
+    const int t0 = u * a.unit_len, t1 = min(a.ax.len, t0 + a.unit_len);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q32 = (warp & 3) * 32, KA = c.K > 64 ? 2 : 1;
+    const float decay = a.decay ? a.decay[h] : 0.f;
+    const bool back = c.back != 0;
+    {
+        const Chunks k(a, row, t0, t1, back, true);
+        if (!k.more()) return;   // its last sequence ends with it
+    }
+    const CUtensorMap *mk = &g.map[g.mk[blockIdx.y]], *mv = &g.map[g.mv[blockIdx.y]];
+    const int hk = h / c.gk, hv = h / c.gv;
+    const auto load = [&](int st, int z) {
+        tc::mbar_arrive_expect_tx(&sm.full[st], (KA + 1) * ATOM);
+        for (int p = 0; p < KA; ++p) tc::tma_load3(base + st * W_STAGE + p * ATOM, mk, 64 * p, hk, z, &sm.full[st]);
+        tc::tma_load3(base + st * W_STAGE + W_V, mv, v0, hv, z, &sm.full[st]);
+    };
+    if (warp == LOADER) {
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i) {
+                tc::mbar_init(&sm.full[i], 1);
+                tc::mbar_init(&sm.v_full[i], 4);
+                tc::mbar_init(&sm.kv_done[i], 1);
+                tc::mbar_init(&sm.kv_free[i], 8);
+            }
+            tc::mbar_init(&sm.drain, 1);
+            sm.dead = 0;
+            tc::fence_mbar_init();
+            Chunks k(a, row, t0, t1, back, true);
+            for (int i = 0; i < 2 && k.more(); ++i) {
+                const int n = k.n();
+                load(i, (int)k.token(n));
+                k.next(n);
+            }
+        }
+        __syncwarp();
+    }
+    if (warp == ISSUER) {
+        tc::tmem_alloc(&sm.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    for (int m = threadIdx.x; m <= C; m += NTHR) sm.pw[m] = lin_power(decay, m);
+    if (KA == 1)   // the second half of the key rows: nothing, in every chunk
+        for (int i = threadIdx.x; i < 2 * ATOM / 16; i += NTHR)
+            *reinterpret_cast<uint4*>(mem + (i >= ATOM / 16) * W_STAGE + ATOM + i % (ATOM / 16) * 16) = make_uint4(0, 0, 0, 0);
+    tc::fence_async_smem();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tb = sm.tmem;
+
+    if (warp < 4 || (warp >= 12 && warp < 16)) {
+        // ------------------------------------------------ V' of every other chunk; this thread's token row
+        const int j = q32 + lane, mine = warp < 4 ? 0 : 1;
+        int i = 0;
+        for (Chunks k(a, row, t0, t1, back, true); k.more(); ++i) {
+            const int n = k.n();
+            if ((i & 1) == mine) {
+                const uint32_t ph = i >> 1 & 1;
+                if (!tc::warp_wait(&sm.full[mine], ph, &sm.dead)) break;
+                if (i > 1 && !tc::warp_wait(&sm.kv_done[mine], ph ^ 1, &sm.dead)) break;
+                unsigned char* st = mem + mine * W_STAGE;
+                spread<NP>(st + W_V, mem + W_VP + mine * 3 * ATOM, st, KA, j, n, c.w * sm.pw[j < n ? (back ? j + 1 : n - 1 - j) : 0]);
+                tc::fence_async_smem();
+                tc::warp_arrive(&sm.v_full[mine]);
+            }
+            k.next(n);
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------ the state; this thread's key row, 32 columns
+        const int kk = q32 + lane, s0 = v0 + (warp < 8 ? 0 : SV), cols = kk < c.K ? min(SV, c.V - s0) : 0;
+        float S[SV];
+#pragma unroll
+        for (int v = 0; v < SV; ++v) S[v] = 0.f;
+        const float2 whole = whole_power(decay, lane);
+        int i = 0;
+        for (Chunks k(a, row, t0, t1, back, true); k.more(); ++i) {
+            const int n = k.n();
+            if (!tc::warp_wait(&sm.kv_done[i & 1], i >> 1 & 1, &sm.dead)) break;
+            tc::fence_after_sync();
+            advance<NP>(S, tc::taddr(tb, q32, (i & 1) * 256 + s0 - v0), n == C ? whole : make_float2(sm.pw[n], 0.f));
+            tc::fence_before_sync();
+            tc::warp_arrive(&sm.kv_free[i & 1]);
+            k.next(n);
+        }
+        store_columns(c.local + (((size_t)unit * a.HV + h) * c.K + kk) * c.V + s0, S, cols);
+    } else if (warp == LOADER) {
+        int issued = 0;
+        for (Chunks k(a, row, t0, t1, back, true); k.more(); ++issued) {
+            const int n = k.n();
+            if (issued > 1) {
+                if (!tc::warp_wait(&sm.kv_done[issued & 1], ((issued >> 1) - 1) & 1, &sm.dead)) break;
+                if (lane == 0) load(issued & 1, (int)k.token(n));
+                __syncwarp();
+            }
+            k.next(n);
+        }
+        // no copy is in flight when the CTA ends, after a failure either
+        for (int i = max(0, issued - 2); i < issued; ++i) tc::mbar_wait(&sm.full[i & 1], (i >> 1) & 1);
+    } else {
+        constexpr uint32_t I_KV = tc::idesc_bf16_abmn(C, NP * VB);
+        int i = 0;
+        for (Chunks k(a, row, t0, t1, back, true); k.more(); ++i) {
+            const int n = k.n(), b = i & 1;
+            const uint32_t ph = i >> 1 & 1;
+            if (!tc::warp_wait(&sm.full[b], ph, &sm.dead) || !tc::warp_wait(&sm.v_full[b], ph, &sm.dead)) break;
+            if (i > 1 && !tc::warp_wait(&sm.kv_free[b], ph ^ 1, &sm.dead)) break;
+            tc::fence_after_sync();
+            const uint64_t dk = tc::sdesc_mn(base + b * W_STAGE, ATOM, 0), dv = tc::sdesc_mn(base + W_VP + b * 3 * ATOM, ATOM, 0);
+            tc::mma4_bf16_w<true, true>(tb + b * 256, dk, dv, I_KV, 0);
+            tc::mma4_bf16_w<true, true>(tb + b * 256, tc::kstep_mn(dk, 4), tc::kstep_mn(dv, 4), I_KV, 1);
+            tc::mma_commit_w(&sm.kv_done[b]);
+            k.next(n);
+        }
+        // every product is done before the tensor memory goes back (after a failure, too)
+        tc::mma_commit_w(&sm.drain);
+        if (!tc::mbar_wait(&sm.drain, 0)) sm.dead = 1;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (threadIdx.x == 0 && sm.dead && a.err) atomicOr(a.err, 2);
+    if (warp == ISSUER) tc::tmem_dealloc(tb, 512);
+}
+
+template <int NP>
 cudaError_t run(const LinTc& g, cudaStream_t st) {
-    static SmemLimit limit;
-    const cudaError_t e = limit.set(reinterpret_cast<const void*>(&k_lin_tc<LOCAL, NP>), SMEM);
-    if (e != cudaSuccess) return e;
     int vmax = 1;
     for (int i = 0; i < g.a.calls; ++i) vmax = g.a.c[i].V > vmax ? g.a.c[i].V : vmax;
     const long long ctas = (long long)g.a.ax.rows * g.a.units_row * g.a.HV * ((vmax + VB - 1) / VB);
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    return traced_launch(LOCAL ? "k_lin_tc_windows" : "k_lin_tc", st,
-                         [&] { k_lin_tc<LOCAL, NP><<<dim3((unsigned)ctas, g.a.calls), NTHR, SMEM, st>>>(g); });
-}
-template <int NP>
-cudaError_t run_both(const LinTc& g, cudaStream_t st) {
+    const dim3 grid((unsigned)ctas, g.a.calls);
     if (g.a.units_row > 1) {
-        const cudaError_t e = run<true, NP>(g, st);
+        static SmemLimit limit;
+        cudaError_t e = limit.set(reinterpret_cast<const void*>(&k_lin_tc_windows<NP>), W_SMEM);
         if (e != cudaSuccess) return e;
+        e = traced_launch("k_lin_tc_windows", st, [&] { k_lin_tc_windows<NP><<<grid, NTHR, W_SMEM, st>>>(g); });
+        if (e != cudaSuccess || (e = launch_lin_join(g.a, st)) != cudaSuccess) return e;
     }
-    return run<false, NP>(g, st);
+    static SmemLimit limit;
+    const cudaError_t e = limit.set(reinterpret_cast<const void*>(&k_lin_tc<NP>), SMEM);
+    if (e != cudaSuccess) return e;
+    return traced_launch("k_lin_tc", st, [&] { k_lin_tc<NP><<<grid, NTHR, SMEM, st>>>(g); });
 }
 
 }  // namespace
@@ -612,7 +748,7 @@ cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st) {
     }
     bool states = false;   // they are fp32 results: all their bits are kept
     for (int i = 0; i < a.calls; ++i) states = states || a.c[i].s1;
-    return states ? run_both<3>(g, st) : run_both<2>(g, st);
+    return states ? run<3>(g, st) : run<2>(g, st);
 }
 
 }  // namespace kda

@@ -163,11 +163,12 @@ def test_a_sequence_does_not_reach_its_neighbours(io, bad):
 
 
 @pytest.mark.parametrize("cu", [[0, 50, 30, 100], [5, 50, 60, 100], [0, 50, 60, 99], [0, 200, -7, 100], [100, 100, 100, 100]])
-def test_inconsistent_offsets_are_reported(cu):
+@pytest.mark.parametrize("times", [1, 25])     # in one window, and in several
+def test_inconsistent_offsets_are_reported(cu, times):
     import chunkwise_delta_rule_gb300 as kda
     for io in ("bf16", "fp32"):
-        k, g, _, _ = lin_case(dict(io=io, B=1, H=2, K=64, V=64, state=True, lengths=[30, 40, 30]), 26)
-        p = problem(k, g, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        k, g, _, _ = lin_case(dict(io=io, B=1, H=2, K=64, V=64, state=True, lengths=[30 * times, 40 * times, 30 * times]), 26)
+        p = problem(k, g, torch.tensor(cu, dtype=torch.int32, device="cuda") * times)
         err = torch.zeros(2, dtype=torch.int32, device="cuda")
         kda.kda_lin_fwd(p, err=err[:1])
         kda.kda_lin_bwd(p, g["do"], g["dht"], err=err[1:])

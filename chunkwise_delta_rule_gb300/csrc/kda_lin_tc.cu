@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
 constexpr int W_V = 2 * ATOM, W_STAGE = 3 * ATOM, W_VP = 2 * W_STAGE, W_END = W_VP + 6 * ATOM;
 struct WindowShared {
     float pw[C + 1];
-    uint64_t full[2], v_full[2], kv_done[2], kv_free[2], drain;
+    uint64_t k_in[2], v_in[2], v_full[2], kv_done[2], kv_free[2], drain;
     uint32_t tmem;
     int dead;
 };
@@ -566,15 +566,19 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc_windows(const __grid_constan
     }
     const CUtensorMap *mk = &g.map[g.mk[blockIdx.y]], *mv = &g.map[g.mv[blockIdx.y]];
     const int hk = h / c.gk, hv = h / c.gv;
-    const auto load = [&](int st, int z) {
-        tc::mbar_arrive_expect_tx(&sm.full[st], (KA + 1) * ATOM);
-        for (int p = 0; p < KA; ++p) tc::tma_load3(base + st * W_STAGE + p * ATOM, mk, 64 * p, hk, z, &sm.full[st]);
-        tc::tma_load3(base + st * W_STAGE + W_V, mv, v0, hv, z, &sm.full[st]);
+    const auto load_k = [&](int st, int z) {
+        tc::mbar_arrive_expect_tx(&sm.k_in[st], KA * ATOM);
+        for (int p = 0; p < KA; ++p) tc::tma_load3(base + st * W_STAGE + p * ATOM, mk, 64 * p, hk, z, &sm.k_in[st]);
+    };
+    const auto load_v = [&](int st, int z) {
+        tc::mbar_arrive_expect_tx(&sm.v_in[st], ATOM);
+        tc::tma_load3(base + st * W_STAGE + W_V, mv, v0, hv, z, &sm.v_in[st]);
     };
     if (warp == LOADER) {
         if (lane == 0) {
             for (int i = 0; i < 2; ++i) {
-                tc::mbar_init(&sm.full[i], 1);
+                tc::mbar_init(&sm.k_in[i], 1);
+                tc::mbar_init(&sm.v_in[i], 1);
                 tc::mbar_init(&sm.v_full[i], 4);
                 tc::mbar_init(&sm.kv_done[i], 1);
                 tc::mbar_init(&sm.kv_free[i], 8);
@@ -585,7 +589,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc_windows(const __grid_constan
             Chunks k(a, row, t0, t1, back, true);
             for (int i = 0; i < 2 && k.more(); ++i) {
                 const int n = k.n();
-                load(i, (int)k.token(n));
+                load_v(i, (int)k.token(n));
+                load_k(i, (int)k.token(n));
                 k.next(n);
             }
         }
@@ -613,7 +618,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc_windows(const __grid_constan
             const int n = k.n();
             if ((i & 1) == mine) {
                 const uint32_t ph = i >> 1 & 1;
-                if (!tc::warp_wait(&sm.full[mine], ph, &sm.dead)) break;
+                if (!tc::warp_wait(&sm.v_in[mine], ph, &sm.dead)) break;
+                if (n < C && !tc::warp_wait(&sm.k_in[mine], ph, &sm.dead)) break;   // its rows behind the chunk are cleared
                 if (i > 1 && !tc::warp_wait(&sm.kv_done[mine], ph ^ 1, &sm.dead)) break;
                 unsigned char* st = mem + mine * W_STAGE;
                 spread<NP>(st + W_V, mem + W_VP + mine * 3 * ATOM, st, KA, j, n, c.w * sm.pw[j < n ? (back ? j + 1 : n - 1 - j) : 0]);
@@ -642,24 +648,35 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc_windows(const __grid_constan
         store_columns(c.local + (((size_t)unit * a.HV + h) * c.K + kk) * c.V + s0, S, cols);
     } else if (warp == LOADER) {
         int issued = 0;
+        bool ok = true;
         for (Chunks k(a, row, t0, t1, back, true); k.more(); ++issued) {
             const int n = k.n();
             if (issued > 1) {
-                if (!tc::warp_wait(&sm.kv_done[issued & 1], ((issued >> 1) - 1) & 1, &sm.dead)) break;
-                if (lane == 0) load(issued & 1, (int)k.token(n));
+                const uint32_t ph = ((issued >> 1) - 1) & 1;
+                if (!tc::warp_wait(&sm.v_full[issued & 1], ph, &sm.dead)) break;   // V has been read
+                if (lane == 0) load_v(issued & 1, (int)k.token(n));
+                ok = tc::warp_wait(&sm.kv_done[issued & 1], ph, &sm.dead);
+                if (lane == 0) load_k(issued & 1, (int)k.token(n));
                 __syncwarp();
+                if (!ok) {
+                    ++issued;
+                    break;
+                }
             }
             k.next(n);
         }
         // no copy is in flight when the CTA ends, after a failure either
-        for (int i = max(0, issued - 2); i < issued; ++i) tc::mbar_wait(&sm.full[i & 1], (i >> 1) & 1);
+        for (int i = max(0, issued - 2); i < issued; ++i) {
+            tc::mbar_wait(&sm.v_in[i & 1], (i >> 1) & 1);
+            tc::mbar_wait(&sm.k_in[i & 1], (i >> 1) & 1);
+        }
     } else {
         constexpr uint32_t I_KV = tc::idesc_bf16_abmn(C, NP * VB);
         int i = 0;
         for (Chunks k(a, row, t0, t1, back, true); k.more(); ++i) {
             const int n = k.n(), b = i & 1;
             const uint32_t ph = i >> 1 & 1;
-            if (!tc::warp_wait(&sm.full[b], ph, &sm.dead) || !tc::warp_wait(&sm.v_full[b], ph, &sm.dead)) break;
+            if (!tc::warp_wait(&sm.k_in[b], ph, &sm.dead) || !tc::warp_wait(&sm.v_full[b], ph, &sm.dead)) break;
             if (i > 1 && !tc::warp_wait(&sm.kv_free[b], ph ^ 1, &sm.dead)) break;
             tc::fence_after_sync();
             const uint64_t dk = tc::sdesc_mn(base + b * W_STAGE, ATOM, 0), dv = tc::sdesc_mn(base + W_VP + b * 3 * ATOM, ATOM, 0);
@@ -706,18 +723,19 @@ bool lin_tc_call(const LinCall& c) {
     return c.K <= C && on(c.q, c.ldq, c.K) && on(c.k, c.ldk, c.K) && on(c.v, c.ldv, c.V) && (reinterpret_cast<uintptr_t>(c.o) & 15) == 0;
 }
 
-// A row cut into n windows costs its CTAs' rounds over the SMs, each of a window's chunks (half as much again where the
-// windows' own states are formed first), some two chunks' time to start and a third of one for each earlier window's
-// state; the cheapest n of powers of two is taken.
+// The cheapest number of windows n of a row, in chunks' times (2 us): every round of CTAs over the SMs takes a window's
+// chunks, 0.6 of a chunk's time more for each where the windows' own states are formed first, and 3 to start; windows cost
+// two launches more, and a little each where they are joined. (Measured, us: 32768 tokens, 16 heads of 128, 32 CTAs a
+// window: one 524, two 407, four 223, eight 246; 8192 tokens, 2 x 24 CTAs backwards: one 134, two 144, three 96, four 118;
+// 2 x 4096 tokens, 64 CTAs: one 74, two 79.)
 int lin_tc_window(int rows, int len, int ctas) {
     const int chunks = (len + C - 1) / C;
-    if (chunks < 2) return C;
     double least = 0;
-    int best = chunks;
-    for (int n = 1; n <= chunks && n <= 256; n *= 2) {
+    int best = chunks > 0 ? chunks : 1;
+    for (int n = 1; n <= chunks && n <= 256; ++n) {
         const int each = (chunks + n - 1) / n;
         const long long all = (long long)rows * ctas * n, rounds = (all + sm_count() - 1) / sm_count();
-        const double cost = rounds * (each * (n > 1 ? 1.5 : 1.) + 2. + (n > 1 ? 0.17 * n + 2. : 0.));
+        const double cost = rounds * (each * (n > 1 ? 1.6 : 1.) + 3.) + (n > 1 ? 10. + 0.06 * n : 0.);
         if (n == 1 || cost < least) {
             least = cost;
             best = each;

@@ -36,13 +36,13 @@ constexpr int SB = 8;   // groups of scales brought in at a time
 
 template <int TN>
 struct Rows {
-    static constexpr int BUF = TN <= 64 ? 8 : 4;                       // group sums in TMEM
+    static constexpr int BUF = TN <= 64 ? 4 : 2;                       // group sums in TMEM
     static constexpr int COLS = BUF * TN < 32 ? 32 : BUF * TN;         // TMEM columns (a power of two)
     static constexpr int STAGE = (G + TN) * 128;
-    static constexpr int STAGES = 8 * STAGE <= 200 * 1024 ? 8 : 6;
+    static constexpr int STAGES = 100 * 1024 / STAGE;                  // two CTAs on an SM
     static constexpr int PITCH = G + 4;                                // floats of a token's sums in shared memory
     struct Shared {
-        float sa[4][SB][TN];   // each warp's own
+        float sa[4][4][TN];   // of four groups, each warp's own
         uint64_t full[STAGES], empty[STAGES], sum[BUF], free[BUF], drain;
         uint32_t tmem;
         int dead;
@@ -77,7 +77,7 @@ __device__ __forceinline__ float4 peer_load(uint32_t addr, uint32_t rank) {
 // Grid: (contraction pieces, tiles of 128 rows of b, tiles of TN rows of a); a cluster is one tile's pieces. Four warps
 // scale and add, one loads, one issues the products.
 template <int TN>
-__global__ void __launch_bounds__(192) k_mm8_rows(const __grid_constant__ Maps maps, Mm8Args p) {
+__global__ void __launch_bounds__(192, 2) k_mm8_rows(const __grid_constant__ Maps maps, Mm8Args p) {
     using R = Rows<TN>;
     extern __shared__ unsigned char raw[];
     const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
@@ -128,19 +128,19 @@ __global__ void __launch_bounds__(192) k_mm8_rows(const __grid_constant__ Maps m
         const float* sb = p.sb + (size_t)(p.b_rows ? min(n, p.N - 1) : blockIdx.y) * p.groups;
         for (int g = g0; g < g1; ++g) {
             const int i = g - g0, buf = i % R::BUF;
-            if (i % SB == 0) {
+            if (i % 4 == 0) {
                 __syncwarp();
                 for (int t = lane; t < TN; t += 32) {
                     const float* sa = p.sa + (size_t)min(m0 + t, p.M - 1) * p.groups + g;
 #pragma unroll
-                    for (int k = 0; k < SB; ++k) sm.sa[warp][k][t] = g + k < g1 ? sa[k] : 0.f;
+                    for (int k = 0; k < 4; ++k) sm.sa[warp][k][t] = g + k < g1 ? sa[k] : 0.f;
                 }
                 __syncwarp();
             }
             const float s = sb[g];
             if (!tc::warp_wait(&sm.sum[buf], (i / R::BUF) & 1, &sm.dead)) break;
             tc::fence_after_sync();
-            const float* row = sm.sa[warp][i % SB];
+            const float* row = sm.sa[warp][i % 4];
 #pragma unroll
             for (int c = 0; c < TN; c += 16) {
                 float x[16];
@@ -208,14 +208,19 @@ __global__ void __launch_bounds__(192) k_mm8_rows(const __grid_constant__ Maps m
             const int m = m0 + t;
             if (m >= p.M) break;
             const uint32_t at = base + (t * R::PITCH + lane * 4) * 4;
-            float4 s = peer_load(at, 0);
-            for (uint32_t r = 1; r < size; ++r) {
-                const float4 x = peer_load(at, r);
-                s.x += x.x;
-                s.y += x.y;
-                s.z += x.z;
-                s.w += x.w;
-            }
+            float4 x[8];   // all of them on their way at once
+#pragma unroll
+            for (uint32_t r = 0; r < 8; ++r)
+                if (r < size) x[r] = peer_load(at, r);
+            float4 s = x[0];
+#pragma unroll
+            for (uint32_t r = 1; r < 8; ++r)
+                if (r < size) {
+                    s.x += x[r].x;
+                    s.y += x[r].y;
+                    s.z += x[r].z;
+                    s.w += x[r].w;
+                }
             const size_t to = (size_t)m * p.N + nq;
             if (wide && nq < p.N) {
                 if (p.f32) *reinterpret_cast<float4*>(static_cast<float*>(p.y) + to) = s;
@@ -243,8 +248,8 @@ cudaError_t run_rows(const Mm8Args& p, cudaStream_t st) {
     const cudaError_t e = limit.set(reinterpret_cast<const void*>(&k_mm8_rows<TN>), R::SMEM);
     if (e != cudaSuccess) return e;
     const int tn = (p.N + G - 1) / G, tm = (p.M + TN - 1) / TN;
-    int parts = 1;   // pieces of two groups at least, while they fit one round of the SMs
-    while (parts < 8 && 4 * parts <= p.groups && 2LL * parts * tn * tm <= sm_count()) parts *= 2;
+    int parts = 1;   // pieces of two groups at least, while they fit one round of the SMs, two on each
+    while (parts < 8 && 4 * parts <= p.groups && (long long)parts * tn * tm <= sm_count()) parts *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(parts, tn, tm);
     cfg.blockDim = dim3(192);
@@ -553,8 +558,9 @@ cudaError_t launch_mm8(Mm8Args p, void* ws, cudaStream_t st) {
     };
     cudaError_t e = align(p.a, p.lda, p.M);
     if (e != cudaSuccess || (e = align(p.b, p.ldb, p.N)) != cudaSuccess) return e;
-    // (tiles of 256 x 256, two SMs each)
-    if ((long long)((p.M + 255) / 256) * ((p.N + 255) / 256) * 4 >= sm_count()) return p.b_rows ? run_pair<true>(p, st) : run_pair<false>(p, st);
+    // From 17 tiles of 256 x 256 on, for two SMs each (us, K 4096: 512 x 4096, 32 tiles, 18.0 against 29.9 in tiles of 128 rows
+    // of b; 256 x 4096, 16 tiles, takes 18.3 in those).
+    if ((long long)((p.M + 255) / 256) * ((p.N + 255) / 256) * 9 >= sm_count()) return p.b_rows ? run_pair<true>(p, st) : run_pair<false>(p, st);
     if (p.M <= 16) return run_rows<16>(p, st);
     if (p.M <= 32) return run_rows<32>(p, st);
     if (p.M <= 64) return run_rows<64>(p, st);

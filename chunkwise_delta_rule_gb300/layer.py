@@ -386,6 +386,7 @@ class Linear8Function(torch.autograd.Function):
         y = kda_mm8(make_mm8_problem(a.q, a.scale, w.q, w.scale, out=out), err=err)
         ctx.save_for_backward(a.qt, a.scale_t, w.qt, w.scale_t)
         ctx.meta = (out, weight.dtype, err)
+        ctx.shape = weight.shape
         return y
 
     @staticmethod
@@ -394,6 +395,9 @@ class Linear8Function(torch.autograd.Function):
         xt, xt_scale, wt, wt_scale = ctx.saved_tensors
         out, wtype, err = ctx.meta
         need_x, need_w = ctx.needs_input_grad[:2]
+        if dy.numel() == 0:   # no tokens: nothing to sum over
+            dx = dy.new_zeros(dy.shape[:-1] + ctx.shape[1:]) if need_x else None
+            return dx, dy.new_zeros(ctx.shape, dtype=wtype) if need_w else None, None
         d = kda_quant8(make_quant8_problem(dy.contiguous(), rows=need_x, transposed=need_w))
         dx = kda_mm8(make_mm8_problem(d.q, d.scale, wt, wt_scale, out=out), err=err) if need_x else None
         dw = None

@@ -412,10 +412,12 @@ size_t kda_lin_workspace_size(const kda_lin_problem *p, int for_backward);
 
 /* Writes o [B*T, HV, V] and, if not NULL, the final states ht [N, HV, K, V]
  * fp32, which may be the same buffer as h0 (decoding in place). bf16 rows that
- * are whole 16-byte accesses (K and V multiples of 8, K <= 128, leading
- * dimensions too) run on the tensor cores unless the sequences are short; there
- * the states are fp32 sums of exact products and one copy of them in bf16 is
- * what a chunk's queries meet. Bit 1 of *err is set where a bounded wait inside
+ * are whole 16-byte accesses (K and V multiples of 8, K <= 128, backwards V <=
+ * 128, leading dimensions too) run on the tensor cores unless the sequences are
+ * short; there the states are fp32 sums of exact products, and a copy of them in
+ * bf16 is what a chunk's queries meet. A NaN or an infinity in a token can reach
+ * the outputs of other tokens of its sequence within 128, earlier ones too;
+ * other sequences are not touched. Bit 1 of *err is set where a bounded wait inside
  * the kernel gave up; the results are then unspecified. */
 kda_status kda_lin_fwd(const kda_lin_problem *p, void *o, float *ht, void *ws, size_t ws_bytes, int32_t *err,
                        kda_stream_t stream);
@@ -461,7 +463,8 @@ typedef struct {
 } kda_mm8_problem;
 
 /* Bytes of workspace kda_mm8 needs (256-byte aligned; 0 where none is needed or
- * the problem is invalid). */
+ * the problem is invalid): copies of a and b where their rows do not start every
+ * 16 bytes, which is read off the pointers and leading dimensions. */
 size_t kda_mm8_workspace_size(const kda_mm8_problem *p);
 
 /* Writes y [M, N]. Bit 1 of *err (NULL or a device int32 word) is set where a

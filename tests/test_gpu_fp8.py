@@ -269,6 +269,15 @@ def test_linear8_gradients(io, wio):
         assert torch.equal(kda.linear8(x.cuda(), w.cuda()), y.flatten(0, 1))
 
 
+def test_linear8_without_tokens():
+    import chunkwise_delta_rule_gb300 as kda
+    x = torch.zeros(2, 0, 64, device="cuda", requires_grad=True)
+    w = torch.ones(32, 64, device="cuda", requires_grad=True)
+    y = kda.linear8(x, w)
+    y.sum().backward()
+    assert y.shape == (2, 0, 32) and x.grad.shape == x.shape and w.grad.shape == w.shape and not w.grad.any()
+
+
 def test_graph_and_streams():
     """A captured product replays on new values; products on two streams at once keep theirs."""
     import chunkwise_delta_rule_gb300 as kda

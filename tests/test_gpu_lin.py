@@ -99,6 +99,21 @@ def test_matches_oracle(kw):
         check_close(n, np64(t).reshape(ref[n].shape), ref[n], tol(t))
 
 
+@pytest.mark.parametrize("kw", [dict(io="bf16", B=2, T=300, H=2, K=64, V=64), dict(io="bf16", B=1, T=2100, H=1, HV=2, K=128, V=128),
+                                dict(io="bf16", B=1, H=2, K=64, V=72, lengths=LENGTHS), dict(io="fp32", B=1, T=900, H=1, K=40, V=24)], ids=str)
+def test_without_states(kw):
+    """Calls that return no state: outputs and gradients as with one."""
+    import chunkwise_delta_rule_gb300 as kda
+    k, g, cu, c = lin_case(dict(kw, state=True), 37)
+    p = problem(k, g, cu)
+    ref = lin_ref(k, c)
+    o, ht = kda.kda_lin_fwd(p, output_final_state=False)
+    r = kda.kda_lin_bwd(p, g["do"], g["dht"], need_dh0=False)
+    assert ht is None and r.dh0 is None
+    for n, t in dict(o=o, dq=r.dq, dk=r.dk, dv=r.dv).items():
+        check_close(n, np64(t).reshape(ref[n].shape), ref[n], tol(t))
+
+
 @pytest.mark.parametrize("kw", [CASES[0], CASES[8], CASES[-4], CASES[-3], CASES[44]], ids=str)
 def test_state_in_place(kw):
     """Every window and sequence reads the initial states, whatever the call has written."""

@@ -19,15 +19,29 @@ struct Maps {
 };
 
 // ------------------------------------------------------------------ rows that no tensor map takes
-// Rows of K bytes, ld apart, to rows `pitch` apart (a multiple of 16; the bytes behind K are never read).
+// Rows of K bytes, ld apart, to rows `pitch` apart (a multiple of 16; the bytes behind K are never read), 16 bytes to a
+// thread: five whole words around them, shifted; byte by byte where those would reach behind the row.
 __global__ void __launch_bounds__(256) k_mm8_align(const uint8_t* src, int64_t ld, uint8_t* dst, int64_t pitch, int K) {
     const uint8_t* s = src + (int64_t)blockIdx.x * ld;
     uint8_t* d = dst + (int64_t)blockIdx.x * pitch;
-    for (int c = threadIdx.x * 4; c < K; c += 1024) {
-        uint32_t w = 0;
+    const uint32_t off = reinterpret_cast<uintptr_t>(s) & 3;
+    for (int c = threadIdx.x * 16; c < K; c += 256 * 16) {
+        uint32_t w[5];
+        if (c + 20 <= K) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(s + c - off);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w |= (c + i < K ? (uint32_t)s[c + i] : 0u) << (8 * i);
-        *reinterpret_cast<uint32_t*>(d + c) = w;
+            for (int i = 0; i < 5; ++i) w[i] = q[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], off * 8);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[i] |= (c + 4 * i + k < K ? (uint32_t)s[c + 4 * i + k] : 0u) << (8 * k);
+            }
+        }
+        *reinterpret_cast<uint4*>(d + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 

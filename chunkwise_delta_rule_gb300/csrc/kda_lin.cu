@@ -370,7 +370,7 @@ cudaError_t pick(const LinArgs& a, cudaStream_t st) {
     return run<TI, 32, 2, 4>(a, st);
 }
 
-// One state element of a head through a row's windows, 8 windows' values on their way at a time: behind window e the state
+// One state element of a head through a row's windows, the next 8 windows' values on their way: behind window e the state
 // is a^n (the state that entered, or that the sequence started from) + the window's own, n its tokens of the sequence.
 __global__ void __launch_bounds__(256) k_lin_join(LinArgs a) {
     const LinCall& c = a.c[blockIdx.z];
@@ -382,20 +382,38 @@ __global__ void __launch_bounds__(256) k_lin_join(LinArgs a) {
     float* p = c.local + ((size_t)row * a.units_row * a.HV + h) * KV + x;
     const int from = c.transposed ? x % c.V * c.K + x / c.V : x;   // in s0
     float S = 0.f;
+    const int last = a.units_row - 1;
     constexpr int AHEAD = 8;
-    for (int e0 = 0; e0 < a.units_row - 1; e0 += AHEAD) {
-        float own[AHEAD];
+    float own[AHEAD], next[AHEAD];
+    const auto fetch = [&](int e0) {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) own[i] = e0 + i < a.units_row - 1 ? p[(size_t)(e0 + i) * step] : 0.f;
+        for (int i = 0; i < AHEAD; ++i) next[i] = e0 + i < last ? p[(size_t)(e0 + i) * step] : 0.f;
+    };
+    fetch(0);
+    for (int e0 = 0; e0 < last; e0 += AHEAD) {
+        // what of the chain does not need the state: powers (negative where nothing goes on), and states that sequences start from
+        float f[AHEAD], start[AHEAD];
+        bool fresh[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
+            own[i] = next[i];
             const int e = e0 + i, t1 = (e + 1) * a.unit_len;
-            if (e >= a.units_row - 1) break;
+            f[i] = -1.f;
+            fresh[i] = false;
+            start[i] = 0.f;
+            if (e >= last) continue;
             const Seq s = lin_seq(a.ax, row, t1 - 1, c.back);
             if (s.end <= t1) continue;   // nothing goes on
-            if (s.first >= e * a.unit_len) S = c.s0 ? c.s0[((size_t)s.n * a.HV + h) * KV + from] : 0.f;
-            S = fmaf(S, lin_power(g, t1 - max(s.first, e * a.unit_len)), own[i]);
-            p[(size_t)e * step] = S;
+            fresh[i] = s.first >= e * a.unit_len;
+            if (fresh[i] && c.s0) start[i] = c.s0[((size_t)s.n * a.HV + h) * KV + from];
+            f[i] = lin_power(g, t1 - max(s.first, e * a.unit_len));
+        }
+        fetch(e0 + AHEAD);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (f[i] < 0.f) continue;
+            S = fmaf(fresh[i] ? start[i] : S, f[i], own[i]);
+            p[(size_t)(e0 + i) * step] = S;
         }
     }
 }

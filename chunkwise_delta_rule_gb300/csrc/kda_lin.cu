@@ -4,7 +4,11 @@
 //     o_i = s (a^(i+1) q_i S + sum_{j<=i} a^(i-j) w (q_i k_j) v_j),   S <- a^n S + sum_j w a^(n-1-j) k_j v_j^T
 // (backwards: a^i, and a^(n-j)). The state is rounded once per group instead of once per token, and a token costs two
 // multiply-adds per state element instead of four.
-// Sums are fp32; the outputs are rounded once.
+// Sums are fp32; the outputs are rounded once. Bound by the instructions around its multiply-adds: groups of 8 tokens pass
+// four barriers, two CTAs to an SM (fp32, 3 x 777 tokens, 10 heads of 40 x 72, forward and backward: 484 us; 1002 before
+// the groups' values were fetched ahead and the slices went by the widths).
+// One token per sequence has a kernel of its own, k_lin_step: 64 sequences of 32 heads of 128 x 128 take 43.6 us, 6.2 TB/s
+// (92% of the copy rate; 115 us through the group kernel).
 #include "kda_lin.cuh"
 
 namespace kda {

@@ -4,7 +4,10 @@
 // neighbouring rows, so that a row's maximum is an exchange of 16 lanes, a column's one of a thread's own rows, a
 // lane and eight warps, a row of q leaves in 8-byte pieces, and a column's 8 values are one 8-byte piece of qt. Those
 // pieces turn in shared memory, piece p of column c at place p ^ (c / 8), which spreads both sides over all banks.
-// Bound by HBM.
+// 16384 x 4096 bf16 with both copies 61 us, 4.4 TB/s (66% of the copy rate); 4096 x 4096 fp32 in blocks 22.6 us. Bound by
+// instructions (2.5 of 4 a cycle) rather than by HBM: two roundings of each value and the exchanges around them. Its
+// factors are formed once per group, by one lane or thread, and handed round (each thread forming its own: 88 us); bf16
+// maxima go two at a time (99 us before).
 #include "kda_fp8.cuh"
 
 namespace kda {

@@ -6,21 +6,22 @@
 //     P_ij = s w a^(j-i) (q_i k_j) for j >= i,   o_i = s a^(n-1-i) q_i S + sum_j P_ij v_j,   V'_j = w a^(j+1) v_j.
 // A CTA walks a head's 64 value columns through a time window; the serial chain from chunk to chunk is one multiply-add
 // per state element in registers, everything else runs ahead of it. Roles: one warp loads (TMA, two chunks deep), one
-// issues the four products Q K^T, Q S, K^T V' and P V, and three groups of four warps turn scores into P (TMEM to TMEM)
-// and then write the outputs, keep the state, and form V'.
+// issues the four products Q K^T, Q S, K^T V' and P V, four turn scores into P (TMEM to TMEM) and then write the outputs,
+// eight keep the state and four form V'.
 // Roundings: V' is three bf16 parts, 24 bits, so that the fp32 state is a sum of exact products (each chunk's is summed
-// by the tensor core from zero and added once), or two, 2^-17, in calls that return no state; P and the copy of S that the queries meet are bf16; the output is
-// rounded once.
+// by the tensor core from zero and added once), or two, 2^-17, in calls that return no state; P and the copy of S that the
+// queries meet are bf16; the output is rounded once.
 // Powers of a: |i - j| = (i - block end) + (block end - j) for columns left of the row's block of 32, so that a score
 // costs two products and no exponential; on the diagonal block a row's 32 powers stay in registers.
-// Measured (bf16, K = V = 128): 2 x 8192 tokens of 32 heads 141 us, 3.8 TB/s of 537 MB (57% of the copy rate); their
-// backward, three such calls in one launch, 222 us for 4 x 4096 tokens of 16 heads. What bounds it: a chunk takes some
-// 4000 cycles of its CTA, where HBM would take 2350; the tensor cores are busy in 37% of them, and shared memory, which
-// carries loads, operands and V' (3200 accesses of 128 bytes a chunk), in most. Kept out after measuring (us, the forward
-// above): K^T V' before Q S with the sums handed back early 202, outputs by the state's warps 160, with P V behind the next
-// Q K^T 161, P two blocks ahead or in units of 16 columns 190 and 152, V' unrolled by four 159 (by two 141.5, one 139.5).
-// The state lies over eight warps rather than four for their code: what runs once a chunk has to come from memory each
-// time (time windows of 32768 tokens of 4 heads of 64: 115 against 83 us).
+// Measured (bf16, K = V = 128): 2 x 8192 tokens of 32 heads 141 us, 3.8 TB/s of 537 MB (57% of the copy rate); 4 x 4096 tokens
+// of 16 heads 76 us and their backward, three such calls in one launch, 222. What bounds it: a chunk takes some 4000
+// cycles of its CTA, where HBM would take 2300 and the tensor cores are busy in 37%; the hand-overs Q K^T, P, P V one behind
+// the other, and the roles' instructions, which run once a chunk and have to be fetched anew each time (V' unrolled by
+// four 159 us, by two 141.5, not at all 139.5; two parts of V' in place of three 141.3). Kept out after measuring (the 2 x
+// 8192 tokens above, against 140 to 141 us in the same call): outputs by the state's warps 160, the same with P V behind the
+// next Q K^T 161; P in units of 16 columns, 152 against 150; K^T V' before Q S in quarters of V', 5700 cycles a chunk.
+// The state lies over eight warps rather than four for the same reason (32768 tokens of 4 heads of 64 in time windows: 83
+// us against 115).
 // Rows of the tiles behind a sequence's end belong to its neighbour: K, V and V' are zeroed there, so that whatever they
 // hold adds nothing; P is chosen, not multiplied, where masked.
 #include "kda_lin.cuh"
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             k.next(n);
         }
     } else if (role == 2) {
-        // ------------------------------------------------ V' in three parts, and outputs; this thread's token row
+        // ------------------------------------------------ V' in its parts; this thread's token row
         const int j = q32 + lane;
         uint32_t ph = 0, stage = 0, fph = 0;
         bool first = true;
@@ -537,9 +538,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
 
 // ------------------------------------------------------------------ the windows' own states
 // End states of the windows' own tokens, from zero: only the state's half of a chunk's work, two chunks at once (the
-// scores' warps form every other V', which has two places, as the sums have). Some 2400 cycles a chunk, of V' and of the
-// products behind it (32768 tokens of 16 heads of 128 in four windows: 223 us in all; 243 with K and V loaded together,
-// 248 with the main kernel's loop).
+// scores' warps form every other V', which has two places, as the sums have). Bound by V' and the products behind it
+// (32768 tokens of 16 heads of 128 in four windows: 223 us in all; 243 with K and V loaded together, 247 with the main
+// kernel's loop).
 constexpr int W_V = 2 * ATOM, W_STAGE = 3 * ATOM, W_VP = 2 * W_STAGE, W_END = W_VP + 6 * ATOM;
 struct WindowShared {
     float pw[C + 1];

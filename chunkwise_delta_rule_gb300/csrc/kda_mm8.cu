@@ -7,11 +7,11 @@
 // weights go once through the SM whatever the number of tokens; the contraction is cut over a cluster of up to 8 CTAs,
 // whose sums meet in shared memory, in order. 64 x 4096 x 4096: 9.8 us on the device (floor 2.5: 17 MB), 1 x 4096 x 4096: 5.6;
 // the launch, one load's latency, the groups' additions one after the other and the meeting take most of it.
-// Many rows, k_mm8_pair: 16384 x 4096 x 4096 in 225 to 240 us, 2.3 to 2.45 PFLOP/s, with a scale per row of b (4096 x 4096 x 16384,
-// fp32) 360. The tensor cores are busy in 57% of the cycles: a warp reads its 128 columns of a group's sums 16 at a time,
-// some 65 cycles each with the additions, and two sets of sums are all that fits TMEM, so that 700 to 900 cycles a group
-// stand against 512 of products. Kept out after measuring: the next 16 columns read ahead 287 us (the compiler's waits
-// then cover them too), 32 at a time 275 (spills), sixteen warps of 64 columns 240.
+// Many rows, k_mm8_pair: 16384 x 4096 x 4096 in 225 to 242 us, 2.3 to 2.45 PFLOP/s; with a scale per row of b (4096 x 4096 x
+// 16384, fp32) 360. A group takes some 1000 cycles, of them 57% on the tensor cores: two sets of sums are all that fits
+// TMEM, and a set is free again only when its warps have read all of it, 16 columns and one wait at a time. Kept out after
+// measuring (us, against 225 to 240): the next 16 columns read ahead 287, 32 at a time 275 (both spill); sixteen warps of 64
+// columns took as long as eight of 128.
 #include "kda_fp8.cuh"
 #include "tc.cuh"
 

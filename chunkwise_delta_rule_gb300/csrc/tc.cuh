@@ -314,17 +314,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t a, float (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-// 32 lanes x 32 bits, 32 consecutive columns per thread.
-__device__ __forceinline__ void tmem_ld32(uint32_t a, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(a));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
 // 32 lanes x 32 bits, 8 consecutive columns per thread.
 __device__ __forceinline__ void tmem_ld8(uint32_t a, float (&v)[8]) {
     uint32_t r[8];
@@ -341,11 +330,6 @@ __device__ __forceinline__ void tmem_st16u(uint32_t a, const uint32_t (&v)[16]) 
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
-}
-__device__ __forceinline__ void tmem_st8u(uint32_t a, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t a, const float (&v)[16]) {
     asm volatile(
@@ -434,17 +418,6 @@ __device__ __forceinline__ void mma4_bf16_w(uint32_t d, uint64_t a, uint64_t b, 
         "add.s64 x, %1, %6;\n\tadd.s64 y, %2, %9;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t"
         "add.s64 x, %1, %7;\n\tadd.s64 y, %2, %10;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t}"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(SA), "n"(2 * SA), "n"(3 * SA), "n"(SB), "n"(2 * SB), "n"(3 * SB)
-        : "memory");
-}
-// Two of them.
-template <bool AMN, bool BMN>
-__device__ __forceinline__ void mma2_bf16_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred e, p, yes;\n\t.reg .b64 x, y;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-        "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(AMN ? 128 : 2), "n"(BMN ? 128 : 2)
         : "memory");
 }
 // The same with K-major operands of 8 bits (e4m3): K = 128 bytes, one 128-byte row of each.

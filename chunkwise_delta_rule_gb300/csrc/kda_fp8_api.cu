@@ -32,8 +32,8 @@ kda_status mm8_args(const kda_mm8_problem* p, kda::Mm8Args& a) {
     if (!p) return fail(KDA_ERR_INVALID_ARG, "problem is NULL");
     a = kda::Mm8Args{};
     if (p->M < 0 || p->N < 1 || p->K < 1) return fail(KDA_ERR_INVALID_ARG, "M must be >= 0, N and K >= 1");
-    if (p->M > MAX_ROWS || p->N > MAX_COLS || p->K > MAX_COLS)
-        return fail(KDA_ERR_UNSUPPORTED, "more than 2^22 rows of a, or 2^20 rows of b or columns");
+    if (p->M > MAX_ROWS || p->N > MAX_COLS || p->K > MAX_ROWS)   // (the columns of a transposed copy are its rows)
+        return fail(KDA_ERR_UNSUPPORTED, "more than 2^22 rows of a or columns, or 2^20 rows of b");
     if (p->out != KDA_BF16 && p->out != KDA_FP32) return fail(KDA_ERR_INVALID_ARG, "unknown output dtype");
     if (p->b_rows != 0 && p->b_rows != 1) return fail(KDA_ERR_INVALID_ARG, "b_rows must be 0 or 1");
     if ((p->lda && p->lda < p->K) || (p->ldb && p->ldb < p->K))

@@ -288,8 +288,8 @@ cudaError_t run_rows(const Mm8Args& p, cudaStream_t st) {
 
 // ------------------------------------------------------------------ many rows of a
 // Two CTAs share a tile of 256 x 256: each loads its 128 rows of a and 128 of b, the tensor cores read the other's rows of b
-// over the pair, so that an SM's shared memory carries 64 KB per group in place of 96 (a tile of 128 x 256 by itself),
-// which is what bounds the products: 512 cycles of them per group. A CTA's sums are 128 rows x 256 columns, 128 columns
+// over the pair, so that an SM's shared memory carries 64 KB per group in place of 96 (a tile of 128 x 256 by itself), for 512
+// cycles of products. A CTA's sums are 128 rows x 256 columns, 128 columns
 // of one row to a thread of eight warps.
 constexpr int P_STAGES = 5, P_STAGE = 2 * G * 128, P_COLS = 256, P_W = 128, P_ADDERS = 8;   // columns of an adding thread, adding warps
 constexpr int P_LOADER = 8, P_ISSUER = 9, P_SCALES = 10, P_THREADS = 12 * 32;   // (the twelfth completes a warpgroup)
@@ -368,7 +368,6 @@ __global__ void __launch_bounds__(P_THREADS, 1) k_mm8_pair(const __grid_constant
                 if (!BROWS && g + 1 < p.groups) s = scale(0, g + 1);
                 if (!(ok = tc::warp_wait(&sm.sum[buf], i >> 1 & 1, &sm.dead))) break;
                 tc::fence_after_sync();
-                // 16 columns are read while the 16 before them are added
 #pragma unroll
                 for (int c = 0; c < P_W; c += 16) {
                     float y[16];

@@ -453,7 +453,7 @@ kda_status kda_quant8(const kda_quant8_problem *p, void *q, float *scale, void *
  *     y[m, n] = sum_g scale_a[m, g] scale_b[n, g] sum_{c in group g} a[m, c] b[n, c],
  * group sums and their scaled sum in fp32, one rounding to y's type. */
 typedef struct {
-    int M, N, K;                /* up to 2^22, 2^20, 2^20 */
+    int M, N, K;                /* up to 2^22, 2^20, 2^22 */
     int out;                    /* kda_dtype of y */
     int b_rows;                 /* 0: scale_b per 128 rows of b; 1: per row */
     int64_t lda, ldb;           /* bytes between rows (0: K) */

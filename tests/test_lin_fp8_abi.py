@@ -83,7 +83,7 @@ def test_quant8_outputs_come_in_pairs():
 
 
 @pytest.mark.parametrize("kw,status", [(dict(M=-1), 1), (dict(N=0), 1), (dict(K=0), 1), (dict(M=(1 << 22) + 1), 2),
-                                       (dict(N=(1 << 20) + 1), 2), (dict(K=(1 << 20) + 1), 2), (dict(out=2), 1),
+                                       (dict(N=(1 << 20) + 1), 2), (dict(K=(1 << 22) + 1), 2), (dict(out=2), 1),
                                        (dict(b_rows=2), 1), (dict(lda=63), 1), (dict(ldb=63), 1), (dict(a=None), 1),
                                        (dict(b=None), 1), (dict(scale_a=None), 1), (dict(scale_b=None), 1)])
 def test_mm8_refusals(kw, status):

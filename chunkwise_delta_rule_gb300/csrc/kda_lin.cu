@@ -5,8 +5,9 @@
 // (backwards: a^i, and a^(n-j)). The state is rounded once per group instead of once per token, and a token costs two
 // multiply-adds per state element instead of four.
 // Sums are fp32; the outputs are rounded once. Bound by the instructions around its multiply-adds: groups of 8 tokens pass
-// four barriers, two CTAs to an SM (fp32, 3 x 777 tokens, 10 heads of 40 x 72, forward and backward: 484 us; 1002 before
-// the groups' values were fetched ahead and the slices went by the widths).
+// three barriers, two CTAs to an SM (fp32, 3 x 777 tokens, 10 heads of 40 x 72, forward and backward: 433 us; 1002 before the
+// groups' values were fetched ahead and the slices went by the widths, 484 before multiply-adds took pairs of rows and the
+// windows filled whole rounds of the SMs).
 // One token per sequence has a kernel of its own, k_lin_step: 64 sequences of 32 heads of 128 x 128 take 43.6 us, 6.2 TB/s
 // (92% of the copy rate; 115 us through the group kernel).
 #include "kda_lin.cuh"
@@ -41,7 +42,7 @@ __global__ void __launch_bounds__(NT, KR * VEC >= 64 ? 1 : 2) k_lin(LinArgs a, i
     constexpr int LD = KM + 4;   // rows of q and k four words apart in the banks
     constexpr int NK = TG * KM / NT, NV = TG * SL / NT > 0 ? TG * SL / NT : 1;   // a thread's values of a group
     __shared__ __align__(16) float sq[TG][LD], sk[TG][LD], sv[TG][SL], part[TG][NW][SL];
-    __shared__ float P[TG][TG];
+    __shared__ __align__(16) float P[TG][TG];
     __shared__ float2 pw[TG + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k0 = warp * KR;
     const int v0 = slice * SL, vl = v0 + lane * VEC;       // this lane's columns
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(NT, KR * VEC >= 64 ? 1 : 2) k_lin(LinArgs a, i
     const size_t KV = (size_t)c.K * c.V;
     if (blockIdx.x == 0 && blockIdx.y == 0 && !local) axis_check(a.ax, a.err);
 
-    float S[KR][VEC];
+    float2 S[KR / 2][VEC];   // two neighbouring rows each: a multiply-add takes a pair
     // One access per row where the columns lie side by side and start on the access's size.
     const bool vec = VEC > 1 && c.V % VEC == 0 && !c.transposed &&
                      ((reinterpret_cast<uintptr_t>(c.s0) | reinterpret_cast<uintptr_t>(c.s1)) & (4 * VEC - 1)) == 0;
@@ -58,20 +59,23 @@ __global__ void __launch_bounds__(NT, KR * VEC >= 64 ? 1 : 2) k_lin(LinArgs a, i
     auto load_state = [&](const float* p, bool wide, size_t dk, size_t dv) {
 #pragma unroll
         for (int r = 0; r < KR; ++r) {
+            float z[VEC];
             if (k0 + r < c.K && vl < c.V) {
                 const float* x = p + (k0 + r) * dk + vl * dv;
                 if (VEC > 1 && wide) {
                     const Raw<float, VEC> y = load_raw<float, VEC>(x);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) S[r][i] = y.v[i];
+                    for (int i = 0; i < VEC; ++i) z[i] = y.v[i];
                 } else {
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) S[r][i] = vl + i < c.V ? x[i * dv] : 0.f;
+                    for (int i = 0; i < VEC; ++i) z[i] = vl + i < c.V ? x[i * dv] : 0.f;
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) S[r][i] = 0.f;
+                for (int i = 0; i < VEC; ++i) z[i] = 0.f;
             }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) (r & 1 ? S[r / 2][i].y : S[r / 2][i].x) = z[i];
         }
     };
     auto store_state = [&](float* p, bool wide) {
@@ -79,12 +83,15 @@ __global__ void __launch_bounds__(NT, KR * VEC >= 64 ? 1 : 2) k_lin(LinArgs a, i
         for (int r = 0; r < KR; ++r) {
             if (k0 + r >= c.K || vl >= c.V) continue;
             float* x = p + (size_t)(k0 + r) * c.V + vl;
+            float z[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) z[i] = r & 1 ? S[r / 2][i].y : S[r / 2][i].x;
             if (VEC > 1 && wide) {
-                store_values<VEC>(x, S[r]);
+                store_values<VEC>(x, z);
             } else {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
-                    if (vl + i < c.V) x[i] = S[r][i];
+                    if (vl + i < c.V) x[i] = z[i];
             }
         }
     };
@@ -94,9 +101,9 @@ __global__ void __launch_bounds__(NT, KR * VEC >= 64 ? 1 : 2) k_lin(LinArgs a, i
             load_state(c.s0 + ((size_t)n * a.HV + h) * KV, vec, rk, rv);
         } else {
 #pragma unroll
-            for (int r = 0; r < KR; ++r)
+            for (int r = 0; r < KR / 2; ++r)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) S[r][i] = 0.f;
+                for (int i = 0; i < VEC; ++i) S[r][i] = make_float2(0.f, 0.f);
         }
     };
 
@@ -131,9 +138,9 @@ __global__ void __launch_bounds__(NT, KR * VEC >= 64 ? 1 : 2) k_lin(LinArgs a, i
         const int end = min(s.end, t1);
         if (local) {
 #pragma unroll
-            for (int r = 0; r < KR; ++r)
+            for (int r = 0; r < KR / 2; ++r)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) S[r][i] = 0.f;
+                for (int i = 0; i < VEC; ++i) S[r][i] = make_float2(0.f, 0.f);
         } else {
             // (in the first window nothing has, whatever inconsistent offsets say)
             if (first && u > 0 && s.first < t) load_state(c.local + ((size_t)(unit - 1) * a.HV + h) * KV, VEC > 1 && c.V % VEC == 0, c.V, 1);   // it came through earlier windows
@@ -195,55 +202,72 @@ __global__ void __launch_bounds__(NT, KR * VEC >= 64 ? 1 : 2) k_lin(LinArgs a, i
 #pragma unroll
                 for (int i = 0; i < TG; ++i) {
                     if (i >= n) break;
-                    float o[VEC];
+                    float2 o[VEC];
 #pragma unroll
-                    for (int y = 0; y < VEC; ++y) o[y] = 0.f;
+                    for (int y = 0; y < VEC; ++y) o[y] = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int r = 0; r < KR; r += 4) {
                         const float4 qv = *reinterpret_cast<const float4*>(&sq[i][k0 + r]);
-                        const float qa[4] = {qv.x, qv.y, qv.z, qv.w};
 #pragma unroll
-                        for (int z = 0; z < 4; ++z)
+                        for (int y = 0; y < VEC; ++y) o[y] = fma2(make_float2(qv.x, qv.y), S[r / 2][y], o[y]);
 #pragma unroll
-                            for (int y = 0; y < VEC; ++y) o[y] = fmaf(qa[z], S[r + z][y], o[y]);
+                        for (int y = 0; y < VEC; ++y) o[y] = fma2(make_float2(qv.z, qv.w), S[r / 2 + 1][y], o[y]);
                     }
 #pragma unroll
-                    for (int y = 0; y < VEC; ++y) part[i][warp][lane * VEC + y] = o[y];
+                    for (int y = 0; y < VEC; ++y) part[i][warp][lane * VEC + y] = o[y].x + o[y].y;
                 }
             }
             // the state behind the group
             const float2 an = pw[n];
+            if (an.x != 1.f) {
 #pragma unroll
-            for (int r = 0; r < KR; ++r)
+                for (int r = 0; r < KR / 2; ++r)
 #pragma unroll
-                for (int y = 0; y < VEC; ++y) S[r][y] = an.x == 1.f ? S[r][y] : fmaf(S[r][y], an.x, S[r][y] * an.y);
+                    for (int y = 0; y < VEC; ++y)
+                        S[r][y] = fma2(S[r][y], make_float2(an.x, an.x), mul2(S[r][y], make_float2(an.y, an.y)));
+            }
 #pragma unroll
             for (int j = 0; j < TG; ++j) {
                 if (j >= n) break;
                 const float e = c.w * pw[c.back ? n - j : n - 1 - j].x;
-                float vj[VEC];
+                float2 vj[VEC];
 #pragma unroll
-                for (int y = 0; y < VEC; ++y) vj[y] = e * sv[j][lane * VEC + y];
+                for (int y = 0; y < VEC; ++y) {
+                    const float x = e * sv[j][lane * VEC + y];
+                    vj[y] = make_float2(x, x);
+                }
 #pragma unroll
                 for (int r = 0; r < KR; r += 4) {
                     const float4 kv = *reinterpret_cast<const float4*>(&sk[j][k0 + r]);
-                    const float ka[4] = {kv.x, kv.y, kv.z, kv.w};
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
+                    for (int y = 0; y < VEC; ++y) S[r / 2][y] = fma2(make_float2(kv.x, kv.y), vj[y], S[r / 2][y]);
 #pragma unroll
-                        for (int y = 0; y < VEC; ++y) S[r + z][y] = fmaf(ka[z], vj[y], S[r + z][y]);
+                    for (int y = 0; y < VEC; ++y) S[r / 2 + 1][y] = fma2(make_float2(kv.z, kv.w), vj[y], S[r / 2 + 1][y]);
                 }
             }
             if (local) continue;
             __syncthreads();
-            for (int x = threadIdx.x; x < n * SL; x += NT) {
-                const int i = x / SL, d = x - i * SL;
-                if (v0 + d >= c.V) continue;
+            const int d = threadIdx.x % SL;   // this thread's column, of every NT / SL-th token
+            if (v0 + d >= c.V) continue;
+            float vd[TG];
+#pragma unroll
+            for (int j = 0; j < TG; ++j) vd[j] = sv[j][d];
+#pragma unroll
+            for (int x = 0; x < TG * SL / NT; ++x) {
+                const int i = x * (NT / SL) + threadIdx.x / SL;
+                if (i >= n) break;
                 float o = 0.f;
 #pragma unroll
                 for (int y = 0; y < NW; ++y) o += part[i][y][d];
                 o *= c.s * pw[c.back ? i : i + 1].x;
-                for (int j = 0; j <= i; ++j) o = fmaf(P[i][j], sv[j][d], o);
+#pragma unroll
+                for (int j = 0; j < TG; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(&P[i][j]);
+                    if (j <= i) o = fmaf(f.x, vd[j], o);
+                    if (j + 1 <= i) o = fmaf(f.y, vd[j + 1], o);
+                    if (j + 2 <= i) o = fmaf(f.z, vd[j + 2], o);
+                    if (j + 3 <= i) o = fmaf(f.w, vd[j + 3], o);
+                }
                 const size_t tok = (size_t)row * a.ax.len + (c.back ? a.ax.len - 1 - (t + i) : t + i);
                 const size_t to = (tok * a.HV + h) * c.V + v0 + d;
                 if (c.o_f32) static_cast<float*>(c.o)[to] = o;
@@ -361,16 +385,15 @@ cudaError_t run(const LinArgs& a, cudaStream_t st) {
 template <typename TI>
 cudaError_t pick(const LinArgs& a, cudaStream_t st) {
     if (is_step(a)) return run_step<TI>(a, st);
-    int kmax = 1;
-    long long narrow = 0, wide = 0;   // columns that slices of 64 and of 128 walk
+    int kmax = 1, widths[3];
     for (int i = 0; i < a.calls; ++i) {
         kmax = a.c[i].K > kmax ? a.c[i].K : kmax;
-        narrow += (a.c[i].V + 63) / 64 * 64;
-        wide += (a.c[i].V + 127) / 128 * 128;
+        widths[i] = a.c[i].V;
     }
-    if (kmax <= 64) return narrow < wide ? run<TI, 8, 2, 8>(a, st) : run<TI, 8, 4, 8>(a, st);
-    if (kmax <= 96) return narrow < wide ? run<TI, 12, 2, 8>(a, st) : run<TI, 12, 4, 8>(a, st);
-    if (kmax <= 128) return narrow < wide ? run<TI, 16, 2, 8>(a, st) : run<TI, 16, 4, 8>(a, st);
+    const bool narrow = lin_slice(kmax, widths, a.calls) == 64;
+    if (kmax <= 64) return narrow ? run<TI, 8, 2, 8>(a, st) : run<TI, 8, 4, 8>(a, st);
+    if (kmax <= 96) return narrow ? run<TI, 12, 2, 8>(a, st) : run<TI, 12, 4, 8>(a, st);
+    if (kmax <= 128) return narrow ? run<TI, 16, 2, 8>(a, st) : run<TI, 16, 4, 8>(a, st);
     return run<TI, 32, 2, 4>(a, st);
 }
 
@@ -435,12 +458,38 @@ __global__ void __launch_bounds__(256) k_lin_heads(const float* part, TI* out, i
 
 }  // namespace
 
-// Windows per row: as many as keep `ctas` per window below three CTAs on each SM, of 64 tokens at least.
-int lin_units(int rows, int len, int ctas) {
-    const long long all = (long long)rows * ctas;
-    int n = (int)(3LL * sm_count() / (all > 0 ? all : 1));
-    if (n > len / 64) n = len / 64;
-    return n > 1 ? n : 1;
+// Value columns of a CTA: 128, or 64 where slices of those walk fewer columns in all, or keys are wide.
+int lin_slice(int kmax, const int* widths, int calls) {
+    long long narrow = 0, wide = 0;
+    for (int i = 0; i < calls; ++i) {
+        narrow += (widths[i] + 63) / 64 * 64;
+        wide += (widths[i] + 127) / 128 * 128;
+    }
+    return kmax > 128 || narrow < wide ? 64 : 128;
+}
+
+// The cheapest number of windows n of a row, in groups' times (some 5.7 us where two CTAs share an SM, or one of the widest
+// has it): the CTAs over the SMs, a quarter of a round more for the uneven end of several; 0.65 more for each group where
+// the windows' own states are formed first, 3 for a window's states, and windows cost two launches and a join. (Measured, us:
+// fp32, 3 x 777 tokens, 10 heads of 40 x 72, forward in 1, 5, 10, 12 windows 366, 135, 112, 132, backward 452, 321, 335, 329; 300
+// tokens, 4 heads of 64, forward in 1, 4, 10, 24: 105, 57, 35, 29; 2 x 4096 tokens, 16 heads of 128, backward in 1, 4, 24: 2928,
+// 3081, 3186; bf16, 4 x 1000 tokens, 8 heads of 200, forward in 1, 2: 1253, 1674.)
+int lin_window(int rows, int len, int ctas, int kmax, int slice) {
+    const int groups = (len + 7) / 8;
+    const double sms = sm_count(), fit = sms * (kmax > 128 || (kmax > 96 && slice == 128) ? 1 : 2);   // CTAs at once
+    double least = 0;
+    int best = groups > 0 ? groups : 1;
+    for (int n = 1; n <= 256 && n <= groups; ++n) {
+        const int each = (groups + n - 1) / n;
+        const double all = (double)rows * ctas * n;
+        const double rounds = all > fit ? all / fit + 0.25 : all > sms || fit == sms ? 1. : 0.95;
+        const double cost = rounds * (each * (n > 1 ? 1.65 : 1.) + 3.) + (n > 1 ? 4. + 0.1 * n : 0.);
+        if (n == 1 || cost < least) {
+            least = cost;
+            best = each;
+        }
+    }
+    return best * 8;
 }
 
 cudaError_t launch_lin(const LinArgs& a, int bf16, cudaStream_t st) {

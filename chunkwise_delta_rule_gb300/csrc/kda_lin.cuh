@@ -60,8 +60,10 @@ __device__ __forceinline__ float2 lin_power2(float g, int m) {
 
 constexpr int LIN_MAX_W = 256;    // widest key or value
 
-// Time windows of the kernel on CUDA cores.
-int lin_units(int rows, int len, int ctas);
+// The kernel on CUDA cores: value columns of a CTA for calls of these widths; the tokens of its time windows where a window
+// is `ctas` CTAs.
+int lin_slice(int kmax, const int* widths, int calls);
+int lin_window(int rows, int len, int ctas, int kmax, int slice);
 cudaError_t launch_lin(const LinArgs& a, int bf16, cudaStream_t st);
 // The tensor cores' kernel: from this many tokens per sequence on; the tokens of its time windows where a window is
 // `ctas` CTAs; whether a bf16 call's widths and rows fit it.

@@ -47,14 +47,16 @@ bool tc_sizes(const Lin& l, bool backward) {
     return (int64_t)l.a.ax.rows * l.a.ax.len >= (int64_t)(backward ? kda::LIN_TC_TOKENS_BACK : kda::LIN_TC_TOKENS) * l.a.ax.N;
 }
 void set_windows(Lin& l, bool backward, bool tc) {
-    const int heads = l.a.HV * (backward ? 3 : 1);
     int len;
     if (tc) {
         const int blocks = (l.V + 63) / 64, kblocks = (l.K + 63) / 64;
         len = kda::lin_tc_window(l.a.ax.rows, l.a.ax.len, backward ? l.a.HV * (blocks + 2 * kblocks) : l.a.HV * blocks);
     } else {
-        const int units = kda::lin_units(l.a.ax.rows, l.a.ax.len, heads * ((l.V + 127) / 128));
-        len = ((l.a.ax.len + units - 1) / units + 63) / 64 * 64;
+        const int widths[3] = {l.V, l.K, l.K}, calls = backward ? 3 : 1;
+        const int kmax = backward && l.V > l.K ? l.V : l.K, slice = kda::lin_slice(kmax, widths, calls);
+        int ctas = 0;
+        for (int i = 0; i < calls; ++i) ctas += l.a.HV * ((widths[i] + slice - 1) / slice);
+        len = kda::lin_window(l.a.ax.rows, l.a.ax.len, ctas, kmax, slice);
     }
     l.a.unit_len = len > 0 ? len : 64;
     l.a.units_row = l.a.ax.len > 0 ? (l.a.ax.len + l.a.unit_len - 1) / l.a.unit_len : 1;

@@ -67,8 +67,8 @@ int lin_window(int rows, int len, int ctas, int kmax, int slice);
 cudaError_t launch_lin(const LinArgs& a, int bf16, cudaStream_t st);
 // The tensor cores' kernel: from this many tokens per sequence on; the tokens of its time windows where a window is
 // `ctas` CTAs; whether a bf16 call's widths and rows fit it.
-// (64 sequences of 32 heads of 128, us, tensor cores against the kernel on CUDA cores: forward 8 tokens 371 against 223, 16
-// 369 against 364, 32 365 against 645; backward 8 tokens 816 against 739, 16 807 against 1107.)
+// (64 sequences of 32 heads of 128, us, tensor cores against the kernel on CUDA cores: forward 8 tokens 371 against 230, 16
+// 381 against 377, 32 368 against 670; backward 8 tokens 816 against 762, 16 830 against 1148.)
 constexpr int LIN_TC_TOKENS = 16, LIN_TC_TOKENS_BACK = 10;
 int lin_tc_window(int rows, int len, int ctas);
 bool lin_tc_call(const LinCall& c);

@@ -1,6 +1,6 @@
 """The operators together, as a layer has them: norm with 8-bit rows, projections in
-8 bits, linear attention over packed prompts, then token by token; and a training
-step through the same parts."""
+8 bits, linear attention over packed prompts, then token by token; and training
+steps through the same parts, one of them captured."""
 
 import numpy as np
 import pytest
@@ -91,3 +91,36 @@ def test_a_training_step():
     d = kda.kda_quant8(kda.make_quant8_problem(dy[0]))
     hd = np64(d.q.float()) * np.repeat(np64(d.scale), 128, 1)[:, :D]
     check_close("do", np64(o.grad)[0].reshape(253, -1), hd @ held, 4e-3)
+
+
+def test_a_captured_training_step():
+    """Forward and backward of the projections and the attention in one graph: replays on new values give what the eager
+    step gives, bit for bit (no sum goes by the order of arrival)."""
+    import chunkwise_delta_rule_gb300 as kda
+    inp, outp = (t.requires_grad_() for t in weights(65))
+    decay = -torch.exp2(-torch.arange(1.0, HV + 1, device="cuda"))
+    g = gen_of(66)
+    x, dy = (torch.randn(2, 300, D, generator=g).bfloat16().cuda() for _ in range(2))
+    x.requires_grad_()
+
+    def step():
+        o, _ = kda.linear_attention(*heads(kda.linear8(x, inp)), decay)
+        return torch.autograd.grad(kda.linear8(o.flatten(2), outp), (x, inp, outp), dy)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(2):
+        with torch.no_grad():
+            x.copy_(torch.randn(x.shape, generator=g))
+            dy.copy_(torch.randn(dy.shape, generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        assert all(torch.equal(a, b) and a.any() for a, b in zip(kept, step()))

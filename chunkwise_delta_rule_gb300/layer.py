@@ -379,10 +379,10 @@ class Linear8Function(torch.autograd.Function):
     """Autograd wrapper: the three products run in 8 bits."""
 
     @staticmethod
-    def forward(ctx, x, weight, err):
+    def forward(ctx, x, weight, err, recorded):
         out = "bf16" if x.dtype == torch.bfloat16 else "fp32"
-        a = kda_quant8(make_quant8_problem(x, transposed=ctx.needs_input_grad[1]))
-        w = kda_quant8(make_quant8_problem(weight, blocks=True, transposed=ctx.needs_input_grad[0]))
+        a = kda_quant8(make_quant8_problem(x, transposed=recorded and ctx.needs_input_grad[1]))
+        w = kda_quant8(make_quant8_problem(weight, blocks=True, transposed=recorded and ctx.needs_input_grad[0]))
         y = kda_mm8(make_mm8_problem(a.q, a.scale, w.q, w.scale, out=out), err=err)
         ctx.save_for_backward(a.qt, a.scale_t, w.qt, w.scale_t)
         ctx.meta = (out, weight.dtype, err)
@@ -397,14 +397,14 @@ class Linear8Function(torch.autograd.Function):
         need_x, need_w = ctx.needs_input_grad[:2]
         if dy.numel() == 0:   # no tokens: nothing to sum over
             dx = dy.new_zeros(dy.shape[:-1] + ctx.shape[1:]) if need_x else None
-            return dx, dy.new_zeros(ctx.shape, dtype=wtype) if need_w else None, None
+            return dx, dy.new_zeros(ctx.shape, dtype=wtype) if need_w else None, None, None
         d = kda_quant8(make_quant8_problem(dy.contiguous(), rows=need_x, transposed=need_w))
         dx = kda_mm8(make_mm8_problem(d.q, d.scale, wt, wt_scale, out=out), err=err) if need_x else None
         dw = None
         if need_w:
             wout = "bf16" if wtype == torch.bfloat16 else "fp32"
             dw = kda_mm8(make_mm8_problem(d.qt, d.scale_t, xt, xt_scale, out=wout), err=err)
-        return dx, dw, None
+        return dx, dw, None, None
 
 
 def linear8(x, weight, *, err: Optional[torch.Tensor] = None):
@@ -413,5 +413,7 @@ def linear8(x, weight, *, err: Optional[torch.Tensor] = None):
     by blocks of 128 x 128; the backward rounds the output's gradient by rows for
     x's gradient and by groups of 128 tokens, as x, for the weight's. The roundings
     pass their gradients through. y and dx come in x's type, the weight's gradient
-    in its own. ``err`` as in ``kda_mm8``."""
-    return Linear8Function.apply(x, weight, err)
+    in its own. ``err`` as in ``kda_mm8``. The weight is rounded in every call:
+    serving rounds it once with ``kda_quant8`` and calls ``kda_mm8``."""
+    # (needs_input_grad says what the tensors ask for, not whether the call is recorded)
+    return Linear8Function.apply(x, weight, err, torch.is_grad_enabled())

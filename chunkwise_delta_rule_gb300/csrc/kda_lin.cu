@@ -398,49 +398,56 @@ cudaError_t pick(const LinArgs& a, cudaStream_t st) {
 }
 
 // One state element of a head through a row's windows, the next 8 windows' values on their way: behind window e the state
-// is a^n (the state that entered, or that the sequence started from) + the window's own, n its tokens of the sequence.
+// is a^n (the state that entered, or that the sequence started from) + the window's own, n its tokens of the sequence. The
+// powers are in two parts (a state meets one per window) and formed once per CTA, a thread for each window.
 __global__ void __launch_bounds__(256) k_lin_join(LinArgs a) {
     const LinCall& c = a.c[blockIdx.z];
     const int row = blockIdx.y / a.HV, h = blockIdx.y % a.HV;
     const int x = blockIdx.x * 256 + threadIdx.x, KV = c.K * c.V;
-    if (x >= KV) return;
-    const float g = a.decay ? a.decay[h] : 0.f;
     const size_t step = (size_t)a.HV * KV;
     float* p = c.local + ((size_t)row * a.units_row * a.HV + h) * KV + x;
-    const int from = c.transposed ? x % c.V * c.K + x / c.V : x;   // in s0
-    float S = 0.f;
     const int last = a.units_row - 1;
-    constexpr int AHEAD = 8;
+    constexpr int AHEAD = 8, GOES_ON = -1, ENDS = -2;
     float own[AHEAD], next[AHEAD];
     const auto fetch = [&](int e0) {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) next[i] = e0 + i < last ? p[(size_t)(e0 + i) * step] : 0.f;
+        for (int i = 0; i < AHEAD; ++i) next[i] = e0 + i < last && x < KV ? p[(size_t)(e0 + i) * step] : 0.f;
     };
     fetch(0);
+    __shared__ float2 powers[2], power[LIN_MAX_WINDOWS];   // of a token and of a whole window; of each window's tokens
+    __shared__ int enters[LIN_MAX_WINDOWS];                // the sequence whose initial state enters, or one of the two above
+    const int mine = threadIdx.x;
+    int n = 0;
+    if (mine < last) {
+        const int t0 = mine * a.unit_len, t1 = t0 + a.unit_len;
+        const Seq s = lin_seq(a.ax, row, t1 - 1, c.back);
+        if (s.end > t1) n = t1 - max(s.first, t0);
+        enters[mine] = s.end <= t1 ? ENDS : s.first >= t0 ? s.n : GOES_ON;
+    }
+    if (mine == 0 || mine == 32) powers[mine >> 5] = lin_power2(a.decay ? a.decay[h] : 0.f, mine ? a.unit_len : 1);
+    __syncthreads();
+    if (n > 0) power[mine] = n == a.unit_len ? powers[1] : lin_raise(powers[0], n);
+    __syncthreads();
+    if (x >= KV) return;
+    const int from = c.transposed ? x % c.V * c.K + x / c.V : x;   // in s0
+    float S = 0.f;
     for (int e0 = 0; e0 < last; e0 += AHEAD) {
-        // what of the chain does not need the state: powers (negative where nothing goes on), and states that sequences start from
-        float f[AHEAD], start[AHEAD];
-        bool fresh[AHEAD];
+        float start[AHEAD];   // does not need the state
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             own[i] = next[i];
-            const int e = e0 + i, t1 = (e + 1) * a.unit_len;
-            f[i] = -1.f;
-            fresh[i] = false;
-            start[i] = 0.f;
-            if (e >= last) continue;
-            const Seq s = lin_seq(a.ax, row, t1 - 1, c.back);
-            if (s.end <= t1) continue;   // nothing goes on
-            fresh[i] = s.first >= e * a.unit_len;
-            if (fresh[i] && c.s0) start[i] = c.s0[((size_t)s.n * a.HV + h) * KV + from];
-            f[i] = lin_power(g, t1 - max(s.first, e * a.unit_len));
+            const int seq = e0 + i < last ? enters[e0 + i] : ENDS;
+            start[i] = seq >= 0 && c.s0 ? c.s0[((size_t)seq * a.HV + h) * KV + from] : 0.f;
         }
         fetch(e0 + AHEAD);
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            if (f[i] < 0.f) continue;
-            S = fmaf(fresh[i] ? start[i] : S, f[i], own[i]);
-            p[(size_t)(e0 + i) * step] = S;
+            const int e = e0 + i;
+            if (e >= last || enters[e] == ENDS) continue;
+            if (enters[e] >= 0) S = start[i];
+            const float2 f = power[e];
+            S = fmaf(S, f.x, fmaf(S, f.y, own[i]));
+            p[(size_t)e * step] = S;
         }
     }
 }
@@ -479,7 +486,7 @@ int lin_window(int rows, int len, int ctas, int kmax, int slice) {
     const double sms = sm_count(), fit = sms * (kmax > 128 || (kmax > 96 && slice == 128) ? 1 : 2);   // CTAs at once
     double least = 0;
     int best = groups > 0 ? groups : 1;
-    for (int n = 1; n <= 256 && n <= groups; ++n) {
+    for (int n = 1; n <= LIN_MAX_WINDOWS && n <= groups; ++n) {
         const int each = (groups + n - 1) / n;
         const double all = (double)rows * ctas * n;
         const double rounds = all > fit ? all / fit + 0.25 : all > sms || fit == sms ? 1. : 0.95;

@@ -57,8 +57,26 @@ __device__ __forceinline__ float2 lin_power2(float g, int m) {
     const float hi = (float)e;
     return make_float2(hi, isfinite(hi) ? (float)(e - hi) : 0.f);
 }
+// The same from `one`, a^1 in two parts, for m >= 1 and without 64 bits, which a whole warp has no room for: squares and
+// products of two-part values, each off by some 2^-46, so that a^m is off by m 2^-47 (2^-40 for a chunk of 128 tokens).
+__device__ __forceinline__ float2 lin_mul2(float2 a, float2 b) {
+    const float hi = __fmul_rn(a.x, b.x);
+    if (!isfinite(hi)) return make_float2(hi, 0.f);
+    const float lo = __fadd_rn(fmaf(a.x, b.x, -hi), fmaf(a.x, b.y, a.y * b.x)), sum = __fadd_rn(hi, lo);
+    return make_float2(sum, __fadd_rn(lo, -__fadd_rn(sum, -hi)));
+}
+__device__ __forceinline__ float2 lin_raise(float2 one, int m) {
+    float2 r = one;
+#pragma unroll 1
+    for (int b = 30 - __clz(m); b >= 0; --b) {
+        r = lin_mul2(r, r);
+        if (m >> b & 1) r = lin_mul2(r, one);
+    }
+    return r;
+}
 
 constexpr int LIN_MAX_W = 256;    // widest key or value
+constexpr int LIN_MAX_WINDOWS = 256;   // time windows of a row
 
 // The kernel on CUDA cores: value columns of a CTA for calls of these widths; the tokens of its time windows where a window
 // is `ctas` CTAs.

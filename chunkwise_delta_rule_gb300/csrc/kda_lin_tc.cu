@@ -40,7 +40,7 @@ constexpr int T_SC = 0, T_P = 128, T_O1 = 192, T_O2 = 256, T_KV = 320;   // TMEM
 
 struct Shared {
     float pw[C + 1];            // a^m
-    float2 whole;               // a^C in two parts
+    float2 one;                 // a in two parts
     alignas(16) float col[32];  // a block's column's power: to the block's end forwards, from its start backwards
     uint64_t full[2], k_free[2], v_free[2], o_ready[2], sc_full, sc_free, p_full, pv_done, v_full, kv_done, s_full, o_free, drain;
     uint32_t tmem;
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
     }
     // (A 64-bit exponential: by one thread, beside the set-up. 64 sequences of 128 tokens, 32 heads of 128, forward and backward:
     // 328 and 660 us; 348 and 746 with one in each of the state's warps, behind it.)
-    if (threadIdx.x == 13 * 32) sm.whole = lin_power2(decay, C);
+    if (threadIdx.x == 13 * 32) sm.one = lin_power2(decay, 1);
     for (int m = threadIdx.x; m <= C; m += NTHR) sm.pw[m] = lin_power(decay, m);
     if (threadIdx.x < 32) sm.col[threadIdx.x] = lin_power(decay, back ? threadIdx.x : 31 - threadIdx.x);
     if (KA == 1)   // the second half of the key rows: nothing, in every chunk
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 for (int v = 0; v < cols; ++v) c.s1[to + v] = c.s0 ? c.s0[to + v] : 0.f;   // (a call with s1 has natural states)
             }
         }
-        const float2 whole = sm.whole;
+        const float2 one = sm.one, whole = lin_raise(one, C);
         uint32_t ph = 0;
         int seq = -1;
         const uint32_t tk = tc::taddr(tb, q32, T_KV + s0 - v0);
@@ -407,9 +407,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
             tc::fence_async_smem();
             tc::fence_before_sync();
             tc::warp_arrive(&sm.s_full);
+            const float2 an = n == C ? whole : lin_raise(one, n);   // a partial chunk meets the state as often as a whole one
             if (!wait(sm, &sm.kv_done, ph)) break;
             tc::fence_after_sync();
-            advance<NP>(S, tk, n == C ? whole : make_float2(sm.pw[n], 0.f));
+            advance<NP>(S, tk, an);
             if (k.t + n == k.s.end && c.s1) store_columns(c.s1 + ((size_t)k.s.n * a.HV + h) * KV + mine, S, cols);
             k.next(n);
         }
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
 constexpr int W_V = 2 * ATOM, W_STAGE = 3 * ATOM, W_VP = 2 * W_STAGE, W_END = W_VP + 6 * ATOM;
 struct WindowShared {
     float pw[C + 1];
-    float2 whole;
+    float2 one;
     uint64_t k_in[2], v_in[2], v_full[2], kv_done[2], kv_free[2], drain;
     uint32_t tmem;
     int dead;
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc_windows(const __grid_constan
         tc::tmem_alloc(&sm.tmem, 512);
         tc::tmem_relinquish();
     }
-    if (threadIdx.x == 13 * 32) sm.whole = lin_power2(decay, C);
+    if (threadIdx.x == 13 * 32) sm.one = lin_power2(decay, 1);
     for (int m = threadIdx.x; m <= C; m += NTHR) sm.pw[m] = lin_power(decay, m);
     if (KA == 1)   // the second half of the key rows: nothing, in every chunk
         for (int i = threadIdx.x; i < 2 * ATOM / 16; i += NTHR)
@@ -644,13 +645,14 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc_windows(const __grid_constan
         float S[SV];
 #pragma unroll
         for (int v = 0; v < SV; ++v) S[v] = 0.f;
-        const float2 whole = sm.whole;
+        const float2 one = sm.one, whole = lin_raise(one, C);
         int i = 0;
         for (Chunks k(a, row, t0, t1, back, true); k.more(); ++i) {
             const int n = k.n();
+            const float2 an = n == C ? whole : lin_raise(one, n);
             if (!tc::warp_wait(&sm.kv_done[i & 1], i >> 1 & 1, &sm.dead)) break;
             tc::fence_after_sync();
-            advance<NP>(S, tc::taddr(tb, q32, (i & 1) * 256 + s0 - v0), n == C ? whole : make_float2(sm.pw[n], 0.f));
+            advance<NP>(S, tc::taddr(tb, q32, (i & 1) * 256 + s0 - v0), an);
             tc::fence_before_sync();
             tc::warp_arrive(&sm.kv_free[i & 1]);
             k.next(n);
@@ -742,7 +744,7 @@ int lin_tc_window(int rows, int len, int ctas) {
     const int chunks = (len + C - 1) / C;
     double least = 0;
     int best = chunks > 0 ? chunks : 1;
-    for (int n = 1; n <= chunks && n <= 256; ++n) {
+    for (int n = 1; n <= chunks && n <= LIN_MAX_WINDOWS; ++n) {
         const int each = (chunks + n - 1) / n;
         const long long all = (long long)rows * ctas * n, rounds = (all + sm_count() - 1) / sm_count();
         const double cost = rounds * (each * (n > 1 ? 1.6 : 1.) + 3.) + (n > 1 ? 10. + 0.06 * n : 0.);

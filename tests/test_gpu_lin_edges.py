@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from tests.helpers import check_close, np64
-from tests.test_gpu_layer import DT, gen_of
+from tests.test_gpu_layer import DT
 from tests.test_gpu_lin import lin_case, lin_ref, problem, tol
 
 pytestmark = pytest.mark.gpu
@@ -208,3 +208,49 @@ def test_single_tokens_packed_beside_a_prompt(io, lengths):
     assert ("k_lin_tc" in names) == (io == "bf16" and len(lengths) < 60)
     check_close("o", np64(o)[0], ref["o"], tol(o))
     check_close("ht", np64(h), ref["ht"], 1e-5)
+
+
+def step_bound(steps):
+    """A state that only decays is rounded once a step, by at most 2^-24 of it with a sign of its own: eight standard
+    deviations of a sum of `steps` of them, and 4 for the powers and their products themselves."""
+    return 2.0 ** -24 * (8 * (steps / 3) ** 0.5 + 4)
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [33, 100, 127])
+def test_a_decay_does_not_drift_over_calls(io, T):
+    """A state carried through 400 calls of T tokens, each a partial chunk on the tensor cores."""
+    import chunkwise_delta_rule_gb300 as kda
+    calls = 400
+    d = -torch.exp2(-torch.arange(9, 17.0, device="cuda"))
+    z = torch.zeros(1, T, 8, 64, dtype=DT[io], device="cuda")
+    h = torch.ones(1, 8, 64, 64, device="cuda")
+    p = kda.make_lin_problem(z, z, z, d, initial_state=h)
+    names = launched(lambda: kda.kda_lin_fwd(p, ht=h))[1]
+    assert ("k_lin_tc" in names) == (io == "bf16")
+    for _ in range(calls - 1):
+        kda.kda_lin_fwd(p, ht=h)
+    want = np.exp(np64(d) * T * calls).reshape(1, 8, 1, 1)
+    keep = want[0, :, 0, 0] > 1e-30
+    assert keep.sum() >= 7
+    off = np.max(np.abs(np64(h) / want - 1)[:, keep])
+    assert off <= step_bound(calls * (1 if io == "bf16" else -(-T // 8))), off * 2 ** 24
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_a_decay_does_not_drift_over_windows(io):
+    """A state carried through the windows of one long row; backwards in time the same of a final state's gradient."""
+    import chunkwise_delta_rule_gb300 as kda
+    T = 32768
+    z = torch.zeros(1, T, 1, 64, dtype=DT[io], device="cuda")
+    ones = torch.ones(1, 1, 64, 64, device="cuda")
+    for e in range(9, 17):
+        d = torch.full((1,), -2.0 ** -e, device="cuda")
+        p = kda.make_lin_problem(z, z, z, d, initial_state=ones)
+        (_, ht), names = launched(lambda: kda.kda_lin_fwd(p))
+        assert names == (TC if io == "bf16" else CORES)
+        dh0 = kda.kda_lin_bwd(p, z, ones).dh0
+        want = np.exp(-2.0 ** -e * T)
+        for n, t in (("ht", ht), ("dh0", dh0)):
+            off = np.max(np.abs(np64(t) / want - 1))
+            assert off <= step_bound(96 if io == "bf16" else 288), (n, e, off * 2 ** 24)

@@ -9,7 +9,7 @@
 // issues the four products Q K^T, Q S, K^T V' and P V, four turn scores into P (TMEM to TMEM) and then write the outputs,
 // eight keep the state and four form V'.
 // Roundings: V' is three bf16 parts, 24 bits, so that the fp32 state is a sum of exact products (each chunk's is summed
-// by the tensor core from zero and added once), or two, 2^-17, in calls that return no state; P and the copy of S that the
+// by the tensor core from zero and added once), or two, 2^-16, in calls that return no state; P and the copy of S that the
 // queries meet are bf16; the output is rounded once.
 // Powers of a: |i - j| = (i - block end) + (block end - j) for columns left of the row's block of 32, so that a score
 // costs two products and no exponential; on the diagonal block a row's 32 powers stay in registers.

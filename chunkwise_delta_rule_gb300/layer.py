@@ -174,7 +174,9 @@ def make_lin_problem(q, k, v, decay: Optional[torch.Tensor] = None, *, scale: Op
     in one type (bf16 or fp32; HV a multiple of H, value head j reading key head
     j // (HV // H); widths up to 256), ``decay`` [HV] fp32, the natural logarithm
     of each head's factor per token, or None for no decay, ``scale`` of the
-    queries (K ** -0.5 by default), ``initial_state`` [N, HV, K, V] fp32 or None."""
+    queries (K ** -0.5 by default), ``initial_state`` [N, HV, K, V] fp32 or None.
+    ``include/kda.h`` says which of a call's values are rounded to bf16 on the
+    tensor cores, and what a NaN in a token reaches."""
     return _binding.LinProblem(q, k, v, decay, scale, initial_state, cu_seqlens)
 
 

@@ -390,7 +390,9 @@ kda_status kda_norm_bwd(const kda_norm_problem *p, const void *dy, const void *d
  *     S_t = a S_{t-1} + k_t v_t^T,   o_t = S_t^T (scale q_t)
  * HV = G * H value heads (0: H) share H heads of queries and keys, value head j
  * reading head j / G; S_0 = h0 or zero. Any real decay is taken (-infinity: a
- * state that holds its own token alone); a positive one grows the state. */
+ * state that holds its own token alone); a positive one grows the state, and its
+ * power over a call's tokens has to stay within fp32 (beyond, a NaN can stand
+ * where growth met a zero). */
 typedef struct {
     int B, T, H, K, V;          /* batch, tokens per sequence (total when packed), heads, key and value width (1..256) */
     int N;                      /* packed sequences (used only when cu_seqlens != NULL; then B == 1) */
@@ -414,11 +416,16 @@ size_t kda_lin_workspace_size(const kda_lin_problem *p, int for_backward);
  * fp32, which may be the same buffer as h0 (decoding in place). bf16 rows that
  * are whole 16-byte accesses (K and V multiples of 8, K <= 128, backwards V <=
  * 128, leading dimensions too) run on the tensor cores unless the sequences are
- * short; there the states are fp32 sums of exact products, and a copy of them in
- * bf16 is what a chunk's queries meet. A NaN or an infinity in a token can reach
- * the outputs of other tokens of its sequence within 128, earlier ones too;
- * other sequences are not touched. Bit 1 of *err is set where a bounded wait inside
- * the kernel gave up; the results are then unspecified. */
+ * short, in chunks of up to 128 tokens. There the scores of a chunk, and the copy
+ * of the state that its queries meet, are rounded to bf16, 2^-8 of each term of an
+ * output beside the output's own rounding; the state itself is an fp32 sum of exact
+ * products where the call returns states, and of products of v to 2^-16 where it
+ * returns none and only outputs come of it. On the CUDA cores everything is fp32.
+ * A NaN or an infinity in a token's k or v reaches its own output, all later ones of
+ * its sequence and the final state; on the tensor cores it can reach earlier ones of
+ * its chunk, too. One in q reaches its token's output. Other sequences are not
+ * touched. Bit 1 of *err is set where a bounded wait inside the kernel gave up; the
+ * results are then unspecified. */
 kda_status kda_lin_fwd(const kda_lin_problem *p, void *o, float *ht, void *ws, size_t ws_bytes, int32_t *err,
                        kda_stream_t stream);
 
@@ -426,14 +433,19 @@ kda_status kda_lin_fwd(const kda_lin_problem *p, void *o, float *ht, void *ws, s
  * or NULL; writes dq, dk [B*T, H, K], dv [B*T, HV, V] and, if not NULL, dh0
  * [N, HV, K, V] fp32 (a buffer of its own). The decay has no gradient. The sums
  * over a key head's value heads are formed in order: repeated calls agree
- * bitwise. */
+ * bitwise. Roundings as in the forward, those of states by whether dh0 is asked
+ * for. What is not finite goes backwards in time here: in q or dout it reaches dk
+ * and dv of its token and all earlier ones, and dh0 (of later ones at most its
+ * chunk's, chunks counted from the end); in k or v it reaches dq as it does o. */
 kda_status kda_lin_bwd(const kda_lin_problem *p, const void *dout, const float *dht, void *dq, void *dk, void *dv,
                        float *dh0, void *ws, size_t ws_bytes, int32_t *err, kda_stream_t stream);
 
 /* Rounding to e4m3 with a scale for each group of 128 columns (or block of 128 x
  * 128): scale = max |x| / 448 over the group, x ~ scale * e4m3, as kda_norm_fwd
- * writes its 8-bit rows; a group of zeros has scale 0, and one that holds a NaN
- * or an infinity has a NaN or infinite scale. */
+ * writes its 8-bit rows: x times the fp32 quotient 448 / max |x|, to nearest even,
+ * so that a value as near to the middle of two as those two roundings may go to
+ * either. A group of zeros has scale 0, and one that holds a NaN or an infinity has
+ * a NaN or infinite scale. */
 typedef struct {
     int rows, D;                /* rows up to 2^22, D up to 2^20 */
     kda_dtype io;               /* type of x */
@@ -451,7 +463,9 @@ kda_status kda_quant8(const kda_quant8_problem *p, void *q, float *scale, void *
 
 /* Matrix product of e4m3 values with a scale for each 128 columns,
  *     y[m, n] = sum_g scale_a[m, g] scale_b[n, g] sum_{c in group g} a[m, c] b[n, c],
- * group sums and their scaled sum in fp32, one rounding to y's type. */
+ * group sums and their scaled sum in fp32, one rounding to y's type. The two
+ * scales are multiplied first: their product has to be a normal fp32 number (a
+ * smaller one loses bits, and an infinite one turns a group sum of zero into NaN). */
 typedef struct {
     int M, N, K;                /* up to 2^22, 2^20, 2^22 */
     int out;                    /* kda_dtype of y */

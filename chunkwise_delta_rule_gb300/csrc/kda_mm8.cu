@@ -3,9 +3,9 @@
 // The scales vary along the contraction, so the tensor core sums one group at a time (four steps of K = 32 bytes, from
 // zero, in TMEM) and warps add it, scaled, to the output's sums in registers, while the next groups are summed.
 //
-// Few rows, k_mm8_rows: the tensor core's 128 rows are rows of b, its N are TN rows of a (16 to 128), so that the
-// weights go once through the SM whatever the number of tokens; the contraction is cut over a cluster of up to 8 CTAs,
-// whose sums meet in shared memory, in order. 64 x 4096 x 4096: 9.8 us on the device (floor 2.5: 17 MB), 1 x 4096 x 4096: 5.6;
+// Few rows (up to 64, or few tiles), k_mm8_rows: the tensor core's 128 rows are rows of b, its N are TN rows of a (16 to
+// 128), so that the weights go once through the SM whatever the number of tokens; the contraction is cut over a cluster of
+// up to 8 CTAs, whose sums meet in shared memory, in order. 64 x 4096 x 4096: 9.8 us on the device (floor 2.5: 17 MB), 1 x 4096 x 4096: 5.6;
 // the launch, one load's latency, the groups' additions one after the other and the meeting take most of it.
 // Many rows, k_mm8_pair: 16384 x 4096 x 4096 in 225 to 242 us, 2.3 to 2.45 PFLOP/s; with a scale per row of b (4096 x 4096 x
 // 16384, fp32) 360. A group takes some 1000 cycles, of them 57% on the tensor cores: two sets of sums are all that fits
@@ -577,9 +577,14 @@ cudaError_t launch_mm8(Mm8Args p, void* ws, cudaStream_t st) {
     };
     cudaError_t e = align(p.a, p.lda, p.M);
     if (e != cudaSuccess || (e = align(p.b, p.ldb, p.N)) != cudaSuccess) return e;
-    // From 17 tiles of 256 x 256 on, for two SMs each (us, K 4096: 512 x 4096, 32 tiles, 18.0 against 29.9 in tiles of 128 rows
-    // of b; 256 x 4096, 16 tiles, takes 18.3 in those).
-    if ((long long)((p.M + 255) / 256) * ((p.N + 255) / 256) * 9 >= sm_count()) return p.b_rows ? run_pair<true>(p, st) : run_pair<false>(p, st);
+    // Tiles of 256 x 256 for pairs of SMs from 17 of them on, if a has more than 64 rows: fewer leave most of a tile empty, at
+    // the time of a whole one. (us, tiles of 128 rows of b against pairs, b from HBM. K 4096, blocks, bf16: M 1, N 2048 6.1
+    // against 17.0, N 8192 9.3, 18.2, N 131072 84, 161; M 64, N 4096 10.6, 17.6, N 8192 13.1, 17.9, N 16384 19.5, 18.9, N
+    // 131072 118, 105; M 128, N 4096 14.7, 18.5, N 8192 19.2, 18.8, N 16384 30.8, 20.0; M 256, N 4096 18.9, 18.6, N 8192 30.4,
+    // 18.9; M 512, N 2048 18.6, 18.4, N 4096 30.0, 18.7. K 1024: M 64, N 8192 7.9, 8.7, N 131072 46, 36; M 256, N 4096 10.5,
+    // 8.8. K 16384: M 64, N 8192 31, 55; M 256, N 4096 50, 58; M 1280, N 1280, rows, fp32 99, 93. Rows, fp32, K 4096: M 64, N
+    // 32768 37, 54; M 128, N 8192 20.5, 30.7, N 16384 33.1, 31.8; M 256, N 4096 19.8, 31.1, N 8192 32.1, 31.2.)
+    if (p.M > 64 && (long long)((p.M + 255) / 256) * ((p.N + 255) / 256) * 9 >= sm_count()) return p.b_rows ? run_pair<true>(p, st) : run_pair<false>(p, st);
     if (p.M <= 16) return run_rows<16>(p, st);
     if (p.M <= 32) return run_rows<32>(p, st);
     if (p.M <= 64) return run_rows<64>(p, st);

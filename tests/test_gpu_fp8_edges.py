@@ -31,6 +31,18 @@ def test_several_tiles_to_a_pair(M, N, K, b):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("M,N,K,kernel", [(1, 5000, 1040, "rows"), (16, 20001, 272, "rows"), (64, 8200, 400, "rows"), (65, 4500, 272, "pair"),
+                                          (256, 4096, 144, "rows"), (512, 4096, 144, "pair")])
+@pytest.mark.parametrize("b", ["blocks", "rows"])
+def test_few_rows_of_a_and_many_of_b(M, N, K, kernel, b):
+    """Both sides of the rule that chooses the kernel: up to 64 rows never go through tiles of 256."""
+    import chunkwise_delta_rule_gb300 as kda
+    c = mm_case(M, N, K, b, 96)
+    y, names = launched(lambda: kda.kda_mm8(kda.make_mm8_problem(*cuda(*c), out="fp32")))
+    assert names == {"k_mm8_" + kernel}
+    check_close("y", np64(y), mm_ref(*c), 1e-5)
+
+
 @pytest.mark.parametrize("M,N,K", [(40, 64, 256), (2000, 1300, 300)])
 @pytest.mark.parametrize("out", ["bf16", "fp32"])
 def test_an_output_off_16_bytes(M, N, K, out):

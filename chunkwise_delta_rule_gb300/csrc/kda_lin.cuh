@@ -83,11 +83,18 @@ constexpr int LIN_MAX_WINDOWS = 256;   // time windows of a row
 int lin_slice(int kmax, const int* widths, int calls);
 int lin_window(int rows, int len, int ctas, int kmax, int slice);
 cudaError_t launch_lin(const LinArgs& a, int bf16, cudaStream_t st);
-// The tensor cores' kernel: from this many tokens per sequence on; the tokens of its time windows where a window is
+// The tensor cores' kernel: from this many tokens per sequence on (in the mean); the tokens of its time windows where a window is
 // `ctas` CTAs; whether a bf16 call's widths and rows fit it.
 // (64 sequences of 32 heads of 128, us, tensor cores against the kernel on CUDA cores: forward 8 tokens 371 against 230, 16
 // 381 against 377, 32 368 against 670; backward 8 tokens 816 against 762, 16 830 against 1148.)
 constexpr int LIN_TC_TOKENS = 16, LIN_TC_TOKENS_BACK = 10;
+// Packed sequences lie one behind the other in a window, and each of them costs its CTA 7 to 12 us there however short it is: a
+// higher mean. (us, tensor cores against CUDA cores, states carried. 16 heads of 128, forward: 64 sequences of 16 tokens 709
+// against 222, of 32 692, 383, of 64 189, 703; 64 single tokens beside 1000 tokens, mean 16, 751, 626, beside 4000, mean 63,
+// 777, 1281; backward: 64 of 16 694, 635, of 32 683, 1054; 64 beside 1000 736, 1457. 4 heads of 64, forward: 16 of 32 115,
+// 30, of 64 110, 46, of 128 20, 54; 64 beside 4000 495, 230; backward: 16 of 32 114, 46, 64 of 32 74, 90, 64 of 64 59, 142;
+// 64 beside 1000 491, 238.)
+constexpr int LIN_TC_PACKED = 48, LIN_TC_PACKED_BACK = 24;
 int lin_tc_window(int rows, int len, int ctas);
 bool lin_tc_call(const LinCall& c);
 cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st);

@@ -44,7 +44,9 @@ size_t state_bytes(const Lin& l, size_t n) { return up(sizeof(float) * n * l.a.H
 // Whether sizes alone let a call run on the tensor cores (its rows' alignment has to, too).
 bool tc_sizes(const Lin& l, bool backward) {
     if (!l.bf16 || l.K % 8 || l.V % 8 || l.K > 128 || (backward && l.V > 128)) return false;
-    return (int64_t)l.a.ax.rows * l.a.ax.len >= (int64_t)(backward ? kda::LIN_TC_TOKENS_BACK : kda::LIN_TC_TOKENS) * l.a.ax.N;
+    const int least = l.a.ax.cu ? (backward ? kda::LIN_TC_PACKED_BACK : kda::LIN_TC_PACKED)
+                                : (backward ? kda::LIN_TC_TOKENS_BACK : kda::LIN_TC_TOKENS);
+    return (int64_t)l.a.ax.rows * l.a.ax.len >= (int64_t)least * l.a.ax.N;
 }
 void set_windows(Lin& l, bool backward, bool tc) {
     int len;

@@ -197,17 +197,22 @@ def test_single_tokens_of_other_widths(io, K, V):
 
 
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
-@pytest.mark.parametrize("lengths", [[1] * 40 + [900] + [1] * 7, [1] * 100 + [900, 0, 1]], ids=["few", "many"])
-def test_single_tokens_packed_beside_a_prompt(io, lengths):
-    """A serving step's mix; its mean length decides between the tensor cores and the CUDA cores."""
+@pytest.mark.parametrize("lengths,forward,backward", [([1] * 10 + [900] + [1] * 7, True, True), ([1] * 20 + [900, 0, 1], False, True),
+                                                      ([1] * 100 + [900, 0, 1], False, False), ([48] * 5, True, True), ([47] * 5, False, True),
+                                                      ([24] * 5, False, True), ([23] * 5, False, False), ([1] * 70, False, False)])
+def test_single_tokens_packed_beside_a_prompt(io, lengths, forward, backward):
+    """Mixes of a serving step, and both sides of the mean lengths from which packed calls take the tensor cores."""
     import chunkwise_delta_rule_gb300 as kda
     k, g, cu, c = lin_case(dict(io=io, B=1, H=2, HV=2, K=64, V=64, state=True, lengths=lengths), 85)
     ref = lin_ref(k, c)
+    p = problem(k, g, cu)
+    r, names = launched(lambda: kda.kda_lin_bwd(p, g["do"], g["dht"]))
+    assert ("k_lin_tc" in names) == (io == "bf16" and backward)
     h = g["h0"].clone()
     (o, _), names = launched(lambda: kda.kda_lin_fwd(problem(k, dict(g, h0=h), cu), ht=h))
-    assert ("k_lin_tc" in names) == (io == "bf16" and len(lengths) < 60)
-    check_close("o", np64(o)[0], ref["o"], tol(o))
-    check_close("ht", np64(h), ref["ht"], 1e-5)
+    assert ("k_lin_tc" in names) == (io == "bf16" and forward)
+    for n, t in dict(o=o, ht=h, dq=r.dq, dk=r.dk, dv=r.dv, dh0=r.dh0).items():
+        check_close(n, np64(t).reshape(ref[n].shape), ref[n], tol(t))
 
 
 def step_bound(steps):

@@ -88,12 +88,15 @@ cudaError_t launch_lin(const LinArgs& a, int bf16, cudaStream_t st);
 // (64 sequences of 32 heads of 128, us, tensor cores against the kernel on CUDA cores: forward 8 tokens 371 against 230, 16
 // 381 against 377, 32 368 against 670; backward 8 tokens 816 against 762, 16 830 against 1148.)
 constexpr int LIN_TC_TOKENS = 16, LIN_TC_TOKENS_BACK = 10;
-// Packed sequences lie one behind the other in a window, and each of them costs its CTA 7 to 12 us there however short it is: a
-// higher mean. (us, tensor cores against CUDA cores, states carried. 16 heads of 128, forward: 64 sequences of 16 tokens 709
-// against 222, of 32 692, 383, of 64 189, 703; 64 single tokens beside 1000 tokens, mean 16, 751, 626, beside 4000, mean 63,
-// 777, 1281; backward: 64 of 16 694, 635, of 32 683, 1054; 64 beside 1000 736, 1457. 4 heads of 64, forward: 16 of 32 115,
-// 30, of 64 110, 46, of 128 20, 54; 64 beside 4000 495, 230; backward: 16 of 32 114, 46, 64 of 32 74, 90, 64 of 64 59, 142;
-// 64 beside 1000 491, 238.)
+// Packed sequences lie one behind the other in a window, and each of them costs its CTA 7 to 12 us there however short it is,
+// while the CUDA cores' windows spread a call of few heads over the SMs: such calls, of less than a third of the SMs' CTAs a
+// window, need a higher mean. (us, tensor cores against CUDA cores, states carried; n x t: n sequences of t tokens, n + t: n
+// single tokens beside one of t. Forward, 4 heads of 64: 16 x 32 115, 30, 16 x 64 110, 46, 16 x 128 20, 54, 64 + 4000 495,
+// 230; 8 heads of 128: 12 x 24 128, 50, 12 x 64 121, 96, 64 x 24 670, 152, 64 x 48 100, 272, 64 + 1200 724, 440; 16 heads of
+// 128: 64 x 32 692, 383, 64 x 64 189, 703, 64 + 4000 777, 1281; 32 heads of 128: 12 x 16 130, 74, 64 x 32 698, 771, 64 + 1200
+// 756, 1022; 64 heads of 128: 12 x 16 132, 178, 64 + 1200 759, 1335. Backward, 4 heads of 64: 16 x 32 114, 46, 64 x 64 59,
+// 142, 64 + 1000 491, 238; 8 heads of 128: 64 x 16 684, 301, 64 x 48 257, 710, 64 + 1200 734, 1084; 16 heads of 128: 64 x 16
+// 694, 635, 64 + 1000 736, 1457.)
 constexpr int LIN_TC_PACKED = 48, LIN_TC_PACKED_BACK = 24;
 int lin_tc_window(int rows, int len, int ctas);
 bool lin_tc_call(const LinCall& c);

@@ -41,18 +41,22 @@ kda_status lin_args(const kda_lin_problem* p, Lin& l) {
 }
 
 size_t state_bytes(const Lin& l, size_t n) { return up(sizeof(float) * n * l.a.HV * l.K * l.V); }
+// CTAs of a time window on the tensor cores.
+int tc_ctas(const Lin& l, bool backward) {
+    const int blocks = (l.V + 63) / 64, kblocks = (l.K + 63) / 64;
+    return l.a.HV * (backward ? blocks + 2 * kblocks : blocks);
+}
 // Whether sizes alone let a call run on the tensor cores (its rows' alignment has to, too).
 bool tc_sizes(const Lin& l, bool backward) {
     if (!l.bf16 || l.K % 8 || l.V % 8 || l.K > 128 || (backward && l.V > 128)) return false;
-    const int least = l.a.ax.cu ? (backward ? kda::LIN_TC_PACKED_BACK : kda::LIN_TC_PACKED)
-                                : (backward ? kda::LIN_TC_TOKENS_BACK : kda::LIN_TC_TOKENS);
+    const bool spread = l.a.ax.cu && 3ll * tc_ctas(l, backward) < kda::sm_count();
+    const int least = spread ? (backward ? kda::LIN_TC_PACKED_BACK : kda::LIN_TC_PACKED) : (backward ? kda::LIN_TC_TOKENS_BACK : kda::LIN_TC_TOKENS);
     return (int64_t)l.a.ax.rows * l.a.ax.len >= (int64_t)least * l.a.ax.N;
 }
 void set_windows(Lin& l, bool backward, bool tc) {
     int len;
     if (tc) {
-        const int blocks = (l.V + 63) / 64, kblocks = (l.K + 63) / 64;
-        len = kda::lin_tc_window(l.a.ax.rows, l.a.ax.len, backward ? l.a.HV * (blocks + 2 * kblocks) : l.a.HV * blocks);
+        len = kda::lin_tc_window(l.a.ax.rows, l.a.ax.len, tc_ctas(l, backward));
     } else {
         const int widths[3] = {l.V, l.K, l.K}, calls = backward ? 3 : 1;
         const int kmax = backward && l.V > l.K ? l.V : l.K, slice = kda::lin_slice(kmax, widths, calls);

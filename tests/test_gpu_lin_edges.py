@@ -197,13 +197,15 @@ def test_single_tokens_of_other_widths(io, K, V):
 
 
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
-@pytest.mark.parametrize("lengths,forward,backward", [([1] * 10 + [900] + [1] * 7, True, True), ([1] * 20 + [900, 0, 1], False, True),
-                                                      ([1] * 100 + [900, 0, 1], False, False), ([48] * 5, True, True), ([47] * 5, False, True),
-                                                      ([24] * 5, False, True), ([23] * 5, False, False), ([1] * 70, False, False)])
-def test_single_tokens_packed_beside_a_prompt(io, lengths, forward, backward):
-    """Mixes of a serving step, and both sides of the mean lengths from which packed calls take the tensor cores."""
+@pytest.mark.parametrize("H,lengths,forward,backward", [
+    (2, [1] * 10 + [900] + [1] * 7, True, True), (2, [1] * 20 + [900, 0, 1], False, True), (2, [1] * 100 + [900, 0, 1], False, False),
+    (2, [48] * 5, True, True), (2, [47] * 5, False, True), (2, [24] * 5, False, True), (2, [23] * 5, False, False), (2, [1] * 70, False, False),
+    (64, [1, 30, 0, 33], True, True), (64, [15] * 3, False, True), (64, [9] * 3, False, False)])
+def test_packed_mixes(io, H, lengths, forward, backward):
+    """Mixes of a serving step, and both sides of the mean lengths from which packed calls of few and of many heads take the
+    tensor cores."""
     import chunkwise_delta_rule_gb300 as kda
-    k, g, cu, c = lin_case(dict(io=io, B=1, H=2, HV=2, K=64, V=64, state=True, lengths=lengths), 85)
+    k, g, cu, c = lin_case(dict(io=io, B=1, H=H, HV=H, K=64, V=64, state=True, lengths=lengths), 85)
     ref = lin_ref(k, c)
     p = problem(k, g, cu)
     r, names = launched(lambda: kda.kda_lin_bwd(p, g["do"], g["dht"]))

@@ -40,7 +40,7 @@ constexpr int T_SC = 0, T_P = 128, T_O1 = 192, T_O2 = 256, T_KV = 320;   // TMEM
 
 struct Shared {
     float pw[C + 1];            // a^m
-    float2 one;                 // a in two parts
+    float2 one, whole;          // a and a^C in two parts
     alignas(16) float col[32];  // a block's column's power: to the block's end forwards, from its start backwards
     uint64_t full[2], k_free[2], v_free[2], o_ready[2], sc_full, sc_free, p_full, pv_done, v_full, kv_done, s_full, o_free, drain;
     uint32_t tmem;
@@ -221,9 +221,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
         tc::tmem_alloc(&sm.tmem, 512);
         tc::tmem_relinquish();
     }
-    // (A 64-bit exponential: by one thread, beside the set-up. 64 sequences of 128 tokens, 32 heads of 128, forward and backward:
+    // (64-bit exponentials: by one thread each, beside the set-up. 64 sequences of 128 tokens, 32 heads of 128, forward and backward:
     // 328 and 660 us; 348 and 746 with one in each of the state's warps, behind it.)
-    if (threadIdx.x == 13 * 32) sm.one = lin_power2(decay, 1);
+    if (threadIdx.x == 13 * 32) sm.whole = lin_power2(decay, C);
+    if (threadIdx.x == 14 * 32) sm.one = lin_power2(decay, 1);
     for (int m = threadIdx.x; m <= C; m += NTHR) sm.pw[m] = lin_power(decay, m);
     if (threadIdx.x < 32) sm.col[threadIdx.x] = lin_power(decay, back ? threadIdx.x : 31 - threadIdx.x);
     if (KA == 1)   // the second half of the key rows: nothing, in every chunk
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
                 for (int v = 0; v < cols; ++v) c.s1[to + v] = c.s0 ? c.s0[to + v] : 0.f;   // (a call with s1 has natural states)
             }
         }
-        const float2 one = sm.one, whole = lin_raise(one, C);
+        const float2 one = sm.one, whole = sm.whole;
         uint32_t ph = 0;
         int seq = -1;
         const uint32_t tk = tc::taddr(tb, q32, T_KV + s0 - v0);
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc(const __grid_constant__ LinT
 constexpr int W_V = 2 * ATOM, W_STAGE = 3 * ATOM, W_VP = 2 * W_STAGE, W_END = W_VP + 6 * ATOM;
 struct WindowShared {
     float pw[C + 1];
-    float2 one;
+    float2 one, whole;
     uint64_t k_in[2], v_in[2], v_full[2], kv_done[2], kv_free[2], drain;
     uint32_t tmem;
     int dead;
@@ -610,7 +611,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc_windows(const __grid_constan
         tc::tmem_alloc(&sm.tmem, 512);
         tc::tmem_relinquish();
     }
-    if (threadIdx.x == 13 * 32) sm.one = lin_power2(decay, 1);
+    if (threadIdx.x == 13 * 32) sm.whole = lin_power2(decay, C);
+    if (threadIdx.x == 14 * 32) sm.one = lin_power2(decay, 1);
     for (int m = threadIdx.x; m <= C; m += NTHR) sm.pw[m] = lin_power(decay, m);
     if (KA == 1)   // the second half of the key rows: nothing, in every chunk
         for (int i = threadIdx.x; i < 2 * ATOM / 16; i += NTHR)
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_lin_tc_windows(const __grid_constan
         float S[SV];
 #pragma unroll
         for (int v = 0; v < SV; ++v) S[v] = 0.f;
-        const float2 one = sm.one, whole = lin_raise(one, C);
+        const float2 one = sm.one, whole = sm.whole;
         int i = 0;
         for (Chunks k(a, row, t0, t1, back, true); k.more(); ++i) {
             const int n = k.n();

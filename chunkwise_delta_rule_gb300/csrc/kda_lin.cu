@@ -5,7 +5,7 @@
 // (backwards: a^i, and a^(n-j)). The state is rounded once per group instead of once per token, and a token costs two
 // multiply-adds per state element instead of four.
 // Sums are fp32; the outputs are rounded once. Bound by the instructions around its multiply-adds: groups of 8 tokens pass
-// three barriers, two CTAs to an SM (fp32, 3 x 777 tokens, 10 heads of 40 x 72, forward and backward: 433 us; 1002 before the
+// three barriers, two CTAs to an SM (fp32, 3 x 777 tokens, 10 heads of 40 x 72, forward and backward: 438 us; 1002 before the
 // groups' values were fetched ahead and the slices went by the widths, 484 before multiply-adds took pairs of rows and the
 // windows filled whole rounds of the SMs).
 // One token per sequence has a kernel of its own, k_lin_step: 64 sequences of 32 heads of 128 x 128 take 43.6 us, 6.2 TB/s

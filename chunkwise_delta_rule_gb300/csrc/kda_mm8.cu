@@ -5,13 +5,14 @@
 //
 // Few rows (up to 64, or few tiles), k_mm8_rows: the tensor core's 128 rows are rows of b, its N are TN rows of a (16 to
 // 128), so that the weights go once through the SM whatever the number of tokens; the contraction is cut over a cluster of
-// up to 8 CTAs, whose sums meet in shared memory, in order. 64 x 4096 x 4096: 9.8 us on the device (floor 2.5: 17 MB), 1 x 4096 x 4096: 5.6;
-// the launch, one load's latency, the groups' additions one after the other and the meeting take most of it.
-// Many rows, k_mm8_pair: 16384 x 4096 x 4096 in 225 to 242 us, 2.3 to 2.45 PFLOP/s; with a scale per row of b (4096 x 4096 x
-// 16384, fp32) 360. A group takes some 1000 cycles, of them 57% on the tensor cores: two sets of sums are all that fits
+// up to 8 CTAs, whose sums meet in shared memory, in order. 64 x 4096 x 4096: 9.8 us on the device (floor 2.5: 17 MB), 1 x
+// 4096 x 4096: 5.6; the launch, one load's latency and the meeting take most of the latter, the additions of 64 columns per
+// group the rest.
+// Many rows, k_mm8_pair: 16384 x 4096 x 4096 in 218 to 242 us, 2.3 to 2.5 PFLOP/s; with a scale per row of b (4096 x 4096 x
+// 16384, fp32) 358. A group takes some 1000 cycles, of them 57% on the tensor cores: two sets of sums are all that fits
 // TMEM, and a set is free again only when its warps have read all of it, 16 columns and one wait at a time. Kept out after
 // measuring (us, against 225 to 240): the next 16 columns read ahead 287, 32 at a time 275 (both spill); sixteen warps of 64
-// columns took as long as eight of 128.
+// columns 284 against 222 (before the outputs went by TMA).
 #include "kda_fp8.cuh"
 #include "tc.cuh"
 

@@ -176,7 +176,8 @@ def make_lin_problem(q, k, v, decay: Optional[torch.Tensor] = None, *, scale: Op
     of each head's factor per token, or None for no decay, ``scale`` of the
     queries (K ** -0.5 by default), ``initial_state`` [N, HV, K, V] fp32 or None.
     ``include/kda.h`` says which of a call's values are rounded to bf16 on the
-    tensor cores, and what a NaN in a token reaches."""
+    tensor cores, and what a NaN in a token reaches. Single tokens of decoding are
+    a call of their own, [N, 1, ...]; packed beside prompts they take longer."""
     return _binding.LinProblem(q, k, v, decay, scale, initial_state, cu_seqlens)
 
 

@@ -436,7 +436,8 @@ kda_status kda_lin_fwd(const kda_lin_problem *p, void *o, float *ht, void *ws, s
  * bitwise. Roundings as in the forward, those of states by whether dh0 is asked
  * for. What is not finite goes backwards in time here: in q or dout it reaches dk
  * and dv of its token and all earlier ones, and dh0 (of later ones at most its
- * chunk's, chunks counted from the end); in k or v it reaches dq as it does o. */
+ * chunk's, chunks counted from the end); in k or v it reaches dq as it does o.
+ * Beside that it stays with its token's own gradients. */
 kda_status kda_lin_bwd(const kda_lin_problem *p, const void *dout, const float *dht, void *dq, void *dk, void *dv,
                        float *dh0, void *ws, size_t ws_bytes, int32_t *err, kda_stream_t stream);
 

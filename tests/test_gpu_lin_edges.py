@@ -67,6 +67,22 @@ def test_windows_against_the_oracle_and_in_place(kw, kernels):
         assert all(torch.equal(a, b) for a, b in zip(r, again))
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("decay", [None, "strong", "up"])
+@pytest.mark.parametrize("lengths", [None, [1, 800, 0, 129, 1170]], ids=["one", "packed"])
+def test_windows_of_other_decays(io, decay, lengths):
+    """No decay, decays down to -infinity and growing states through joined windows, whole and partial."""
+    import chunkwise_delta_rule_gb300 as kda
+    k, g, cu, c = lin_case(dict(io=io, B=1, T=0 if lengths else 2100, H=5, K=64, V=64, state=True, decay=decay, lengths=lengths), 70)
+    p = problem(k, g, cu)
+    (o, ht), names = launched(lambda: kda.kda_lin_fwd(p))
+    assert names == (TC if io == "bf16" else CORES)
+    r = kda.kda_lin_bwd(p, g["do"], g["dht"])
+    ref = lin_ref(k, c)
+    for n, t in dict(o=o, ht=ht, dq=r.dq, dk=r.dk, dv=r.dv, dh0=r.dh0).items():
+        check_close(n, np64(t).reshape(ref[n].shape), ref[n], tol(t))
+
+
 def test_windows_on_streams_and_in_graphs():
     """Windows' states lie in workspaces: calls on several streams at once, and replays of two graphs, keep their own."""
     import chunkwise_delta_rule_gb300 as kda
